@@ -13,6 +13,12 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix):
 * :func:`chunk_fwd` -- the chunked KDA forward (``kda_chunk_fwd[_ex]``).
 * :func:`chunk_bwd` -- its gradient (``kda_chunk_bwd``).
 * :func:`short_conv_silu` -- the causal conv + SiLU (+ L2) prologue.
+* :func:`step` -- one token per sequence through the delta rule
+  (``kda_step``), on cached states.
+* :func:`ssm_fwd`, :func:`ssm_step` -- the selective state space operator
+  with its short convolution, on prompts and on single tokens.
+* :func:`block_norm`, :func:`block_norm_bwd` -- the norms before and after a
+  block fused with its gate and residual scale, and their gradients.
 * :func:`workspace_size`, :func:`read_device_status`,
   :func:`clear_device_status`, :func:`status_string`, :func:`version`.
 * :func:`lib` -- the raw ctypes library with typed signatures.
@@ -42,6 +48,18 @@ class KdaError(RuntimeError):
         self.status = status
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)} "
                          f"({status_string(status)})")
+
+
+class kda_ssm_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "P", "N", "G", "dtype")] + \
+        [(n, ctypes.c_longlong) for n in ("xbc_stride_b", "xbc_stride_t", "z_stride_b",
+                                          "z_stride_t", "dt_stride_b", "dt_stride_t")]
+
+
+class kda_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("gate_act", ctypes.c_int), ("gate_rows", ctypes.c_longlong),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class kda_shape(ctypes.Structure):
@@ -127,6 +145,24 @@ def lib():
         L.kda_chunk_fwd_noalloc.restype = i
         L.kda_chunk_fwd_noalloc_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         L.kda_chunk_fwd_noalloc_status.restype = i
+        ssp, ndp, ll = ctypes.POINTER(kda_ssm_shape), ctypes.POINTER(kda_norm_desc), ctypes.c_longlong
+        L.kda_ssm_fwd_workspace_size.argtypes = [ssp, i]
+        L.kda_ssm_fwd_workspace_size.restype = u64
+        L.kda_ssm_fwd.argtypes = [ssp] + [vp] * 15 + [u64, i, vp]
+        L.kda_ssm_fwd.restype = i
+        L.kda_step_workspace_size.argtypes = [i, i]
+        L.kda_step_workspace_size.restype = u64
+        L.kda_ssm_step.argtypes = [ssp] + [vp] * 9 + [i] + [vp] * 4 + [u64, vp]
+        L.kda_ssm_step.restype = i
+        L.kda_step.argtypes = [sp, vp, vp, vp, ll, ll, ll, vp, vp, f, vp, vp, i, vp, i, vp, vp, vp,
+                               u64, vp]
+        L.kda_step.restype = i
+        L.kda_block_norm_fwd.argtypes = [ndp] + [vp] * 9
+        L.kda_block_norm_fwd.restype = i
+        L.kda_block_norm_bwd_workspace_size.argtypes = [ndp, i]
+        L.kda_block_norm_bwd_workspace_size.restype = u64
+        L.kda_block_norm_bwd.argtypes = [ndp] + [vp] * 14 + [u64, vp]
+        L.kda_block_norm_bwd.restype = i
         L.kda_selftest_wait_timeout.argtypes = [vp, ctypes.c_longlong, vp]
         L.kda_selftest_wait_timeout.restype = i
         _lib = L
@@ -562,3 +598,307 @@ def clear_device_status(workspace, stream=None) -> None:
     st = lib().kda_clear_device_status(_ptr(workspace), _stream_ptr(stream, workspace.device))
     if st != KDA_OK:
         raise KdaError(st, "kda_clear_device_status")
+
+
+# ---------------------------------------------------------------------------
+# one token per sequence, the state space operator, the norms around a block
+
+
+def _data(t, name, shape, dtype, device, contiguous=True):
+    """Address of an optional tensor, checked."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _inner(t, name, dims):
+    """The last ``dims`` dimensions of ``t`` must be contiguous; the outer
+    ones may have any stride."""
+    n = 1
+    for size, stride in zip(reversed(t.shape[-dims:]), reversed(t.stride()[-dims:])):
+        if size != 1 and stride != n:
+            raise ValueError(f"the last {dims} dimension(s) of {name} must be contiguous")
+        n *= size
+
+
+def _cuda(t, where):
+    if not t.is_cuda:
+        raise ValueError(f"{where} needs CUDA tensors")
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{where}: dtype must be float32 or bfloat16, got {t.dtype}")
+    return t.device, t.dtype
+
+
+def _scratch(workspace, need, device, where, zero):
+    if workspace is None:
+        if need == 0:
+            raise KdaError(2, where)
+        make = torch.zeros if zero else torch.empty
+        workspace = make(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _raw_stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def step_workspace_size(B, H) -> int:
+    """Workspace bytes of :func:`step` and :func:`ssm_step`."""
+    return int(lib().kda_step_workspace_size(int(B), int(H)))
+
+
+def alloc_step_workspace(B, H, device=None) -> torch.Tensor:
+    """Zero-filled workspace of :func:`step` and :func:`ssm_step` (one for
+    each stream that makes such calls)."""
+    n = step_workspace_size(B, H)
+    if n == 0:
+        raise KdaError(1, "kda_step_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_state=None,
+         l2norm_qk=False, out=None, workspace=None, stream=None):
+    """One token per sequence through the delta rule, on cached states.
+
+    q, k: [B,H,K]; v: [B,H,V] (bf16 or fp32; any stride between the rows);
+    g: [B,H,K] fp32 log-decay; beta: [B,H] fp32; state: [n_slots,H,K,V] fp32,
+    moved on in place.  ``slots`` [B] int32 gives each sequence's place in
+    the cache (None: its row; a place outside the cache marks an idle
+    sequence, whose output is 0).  With ``conv_w`` (as short_conv_silu) and
+    ``conv_state`` [n_slots,3,H*(2K+V)] (moved on in place) q, k, v are the
+    inputs of the convolution.  Returns o [B,H,V]."""
+    dev, dt = _cuda(q, "step")
+    B, H, K = q.shape
+    V = v.shape[-1]
+    n_slots = state.shape[0]
+    for t, name, width in ((q, "q", K), (k, "k", K), (v, "v", V)):
+        _data(t, name, (B, H, width), dt, dev, False)
+        _inner(t, name, 2)
+    f32 = torch.float32
+    if conv_w is not None and conv_w.numel() == 4 * H * (2 * K + V):
+        conv_w = conv_w.view(-1, 4)
+    o = torch.empty((B, H, V), dtype=dt, device=dev) if out is None else out
+    ws, n = _scratch(workspace, step_workspace_size(B, H) if workspace is None else 0, dev,
+                     "kda_step_workspace_size", True)
+    st = lib().kda_step(
+        kda_shape(B, 1, H, K, V, DTYPES[dt]), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        q.stride(0), k.stride(0), v.stride(0), _data(g, "g", (B, H, K), f32, dev),
+        _data(beta, "beta", (B, H), f32, dev), K ** -0.5 if scale is None else float(scale),
+        _data(conv_w, "conv_w", (H * (2 * K + V), 4), f32, dev),
+        _data(conv_state, "conv_state", (n_slots, 3, H * (2 * K + V)), dt, dev), int(l2norm_qk),
+        _data(slots, "slots", (B,), torch.int32, dev), n_slots,
+        _data(state, "state", (n_slots, H, K, V), f32, dev), _data(o, "out", (B, H, V), dt, dev),
+        ws.data_ptr(), n, _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_step")
+    return o
+
+
+def _ssm_dims(xbc, dt, A, head_dim, state_dim):
+    H, P, N = A.numel(), int(head_dim), int(state_dim)
+    C = xbc.shape[-1]
+    groups, rest = divmod(C - H * P, 2 * N)
+    if rest or groups < 1:
+        raise ValueError(f"xbc has {C} channels, expected {H}*{P} + 2*G*{N}")
+    return H, P, N, groups, C
+
+
+def ssm_workspace_size(B, T, H, P, N, G, dtype=torch.bfloat16, impl="auto") -> int:
+    """Workspace bytes of :func:`ssm_fwd` (0 when the shape is not served)."""
+    s = kda_ssm_shape(int(B), int(T), int(H), int(P), int(N), int(G), DTYPES[dtype])
+    return int(lib().kda_ssm_fwd_workspace_size(s, IMPLS[impl]))
+
+
+def alloc_ssm_workspace(B, T, H, P, N, G, dtype=torch.bfloat16, impl="auto",
+                        device=None) -> torch.Tensor:
+    """Zero-filled workspace of :func:`ssm_fwd`."""
+    n = ssm_workspace_size(B, T, H, P, N, G, dtype, impl)
+    if n == 0:
+        raise KdaError(2, "kda_ssm_fwd_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=None, D=None,
+            z=None, initial_state=None, conv_state=None, segment_ids=None,
+            output_final_state=False, out=None, workspace=None, impl="auto", stream=None):
+    """The selective state space operator on prompts (see include/kda.h).
+
+    xbc: [B,T,H*P+2*G*N], z: [B,T,H*P] or None, dt: [B,T,H], all of one dtype
+    (bf16 or fp32) and possibly slices of one projection (last dimension
+    contiguous); conv_w: [channels,4], conv_bias: [channels], A, D, dt_bias:
+    [H], all fp32; initial_state: [B,H,N,P] fp32; conv_state: [B,3,channels].
+    Returns ``(y [B,T,H,P], final_state, conv_state_out)``, the last two None
+    unless ``output_final_state``."""
+    dev, ty = _cuda(xbc, "ssm_fwd")
+    B, T, _ = xbc.shape
+    H, P, N, G, C = _ssm_dims(xbc, dt, A, head_dim, state_dim)
+    f32 = torch.float32
+    for t, name, width in ((xbc, "xbc", C), (dt, "dt", H), (z, "z", H * P)):
+        if t is not None:
+            _data(t, name, (B, T, width), ty, dev, False)
+            _inner(t, name, 1)
+    y = torch.empty((B, T, H, P), dtype=ty, device=dev) if out is None else out
+    fs = conv = None
+    if output_final_state:
+        fs = torch.empty((B, H, N, P), dtype=f32, device=dev)
+        conv = torch.empty((B, 3, C), dtype=ty, device=dev)
+    zs = z.stride() if z is not None else (0, 0)
+    xs, ds = xbc.stride(), dt.stride()
+    s = kda_ssm_shape(B, T, H, P, N, G, DTYPES[ty], xs[0], xs[1], zs[0], zs[1], ds[0], ds[1])
+    ws, n = _scratch(workspace, lib().kda_ssm_fwd_workspace_size(s, IMPLS[impl])
+                     if workspace is None else 0, dev, "kda_ssm_fwd_workspace_size", True)
+    st = lib().kda_ssm_fwd(
+        s, xbc.data_ptr(), dt.data_ptr(), None if z is None else z.data_ptr(),
+        _data(conv_w, "conv_w", (C, 4), f32, dev), _data(conv_bias, "conv_bias", (C,), f32, dev),
+        _data(A, "A", (H,), f32, dev), _data(D, "D", (H,), f32, dev),
+        _data(dt_bias, "dt_bias", (H,), f32, dev),
+        _data(initial_state, "initial_state", (B, H, N, P), f32, dev),
+        _data(conv_state, "conv_state", (B, 3, C), ty, dev),
+        _data(segment_ids, "segment_ids", (B, T), torch.int32, dev),
+        _data(y, "out", (B, T, H, P), ty, dev), None if fs is None else fs.data_ptr(),
+        None if conv is None else conv.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_ssm_fwd")
+    return y, fs, conv
+
+
+def ssm_step(xbc, dt, conv_w, A, state, conv_state, *, head_dim, state_dim, conv_bias=None,
+             dt_bias=None, D=None, z=None, slots=None, out=None, workspace=None, stream=None):
+    """One token per sequence through the state space operator, on cached
+    states: xbc [B,H*P+2*G*N], z [B,H*P] or None, dt [B,H] (any stride between
+    the rows); state [n_slots,H,N,P] fp32 and conv_state [n_slots,3,channels]
+    are moved on in place; ``slots`` as :func:`step`.  Returns y [B,H,P]."""
+    dev, ty = _cuda(xbc, "ssm_step")
+    B = xbc.shape[0]
+    H, P, N, G, C = _ssm_dims(xbc, dt, A, head_dim, state_dim)
+    f32, n_slots = torch.float32, state.shape[0]
+    for t, name, width in ((xbc, "xbc", C), (dt, "dt", H), (z, "z", H * P)):
+        if t is not None:
+            _data(t, name, (B, width), ty, dev, False)
+            _inner(t, name, 1)
+    y = torch.empty((B, H, P), dtype=ty, device=dev) if out is None else out
+    ws, n = _scratch(workspace, step_workspace_size(B, H) if workspace is None else 0, dev,
+                     "kda_step_workspace_size", True)
+    s = kda_ssm_shape(B, 1, H, P, N, G, DTYPES[ty], xbc.stride(0), 0,
+                      0 if z is None else z.stride(0), 0, dt.stride(0), 0)
+    st = lib().kda_ssm_step(
+        s, xbc.data_ptr(), dt.data_ptr(), None if z is None else z.data_ptr(),
+        _data(conv_w, "conv_w", (C, 4), f32, dev), _data(conv_bias, "conv_bias", (C,), f32, dev),
+        _data(A, "A", (H,), f32, dev), _data(D, "D", (H,), f32, dev),
+        _data(dt_bias, "dt_bias", (H,), f32, dev), _data(slots, "slots", (B,), torch.int32, dev),
+        n_slots, _data(conv_state, "conv_state", (n_slots, 3, C), ty, dev),
+        _data(state, "state", (n_slots, H, N, P), f32, dev), _data(y, "out", (B, H, P), ty, dev),
+        ws.data_ptr(), n, _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_ssm_step")
+    return y
+
+
+GATE_ACTS = {"none": 0, "sigmoid": 1, "silu": 2, "tanh": 3}
+
+
+def _norm_desc(y, gate, gate_act, scale, eps):
+    D = y.shape[-1]
+    if D == 0 or y.numel() == 0:
+        raise ValueError("y must not be empty")
+    rows = y.numel() // D
+    grows = gate.numel() // D if gate is not None else 0
+    if gate is not None and (gate.shape[-1] != D or grows == 0 or rows % grows):
+        raise ValueError(f"gate {tuple(gate.shape)} does not divide the rows of {tuple(y.shape)}")
+    if gate_act not in GATE_ACTS:
+        raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}, got {gate_act!r}")
+    return kda_norm_desc(rows, D, DTYPES[y.dtype], GATE_ACTS[gate_act], grows, float(scale),
+                         float(eps)), rows, D
+
+
+def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale=1.0, w_pre=None,
+               eps=1e-6, save_stats=False, out=None, stream=None):
+    """The norm after a block, its gate and residual scale, and the norm
+    before the next block: ``out = residual + scale * act(gate) * rms(y) *
+    w_post``, ``x = rms(out) * w_pre``.
+
+    y, residual: [..., D] (bf16 or fp32, contiguous); gate: [..., D] with as
+    many rows as y, or fewer that divide them (each then serves as many
+    consecutive rows); w_post, w_pre: [D] fp32.  residual, gate and w_pre may be
+    None.  ``out`` may be the residual itself.  Returns ``(out, x or None)``, and
+    the statistics block_norm_bwd reads when ``save_stats``."""
+    dev, ty = _cuda(y, "block_norm")
+    d, rows, D = _norm_desc(y, gate, gate_act, scale, eps)
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty(y.shape, dtype=ty, device=dev)
+    x = torch.empty(y.shape, dtype=ty, device=dev) if w_pre is not None else None
+    stats = torch.empty((2, rows), dtype=f32, device=dev) if save_stats else None
+    st = lib().kda_block_norm_fwd(
+        d, _data(y, "y", y.shape, ty, dev), _data(w_post, "w_post", (D,), f32, dev),
+        _data(residual, "residual", y.shape, ty, dev),
+        None if gate is None else _data(gate, "gate", gate.shape, ty, dev),
+        _data(w_pre, "w_pre", (D,), f32, dev), _data(out, "out", y.shape, ty, dev),
+        None if x is None else x.data_ptr(), None if stats is None else stats.data_ptr(),
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_block_norm_fwd")
+    return (out, x, stats) if save_stats else (out, x)
+
+
+def block_norm_workspace_size(rows, D, gate_rows=0) -> int:
+    """Workspace bytes of :func:`block_norm_bwd` for either type (gate_rows
+    0: no gate)."""
+    d = kda_norm_desc(int(rows), int(D), 0, 1, int(gate_rows), 1.0, 0.0)
+    return int(lib().kda_block_norm_bwd_workspace_size(d, int(gate_rows > 0)))
+
+
+def alloc_block_norm_workspace(rows, D, gate_rows=0, device=None) -> torch.Tensor:
+    """Workspace of :func:`block_norm_bwd` (needs no initialisation)."""
+    n = block_norm_workspace_size(rows, D, gate_rows)
+    if n == 0:
+        raise KdaError(2, "kda_block_norm_bwd_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=None,
+                   gate_act="sigmoid", scale=1.0, w_pre=None, eps=1e-6, workspace=None,
+                   stream=None):
+    """Gradients of block_norm from its inputs and statistics, given the
+    gradients of ``out`` and ``x`` (one of them may be None): ``(dy, d_residual,
+    d_gate, dw_post, dw_pre)``, None in the place of an input that was None."""
+    dev, ty = _cuda(y, "block_norm_bwd")
+    d, rows, D = _norm_desc(y, gate, gate_act, scale, eps)
+    f32 = torch.float32
+
+    def like(t):
+        return None if t is None else torch.empty(t.shape, dtype=ty, device=dev)
+
+    dy, dres, dgate = like(y), like(residual), like(gate)
+    dw_post = torch.empty(D, dtype=f32, device=dev)
+    dw_pre = None if w_pre is None else torch.empty(D, dtype=f32, device=dev)
+    need = 0
+    if workspace is None:
+        need = lib().kda_block_norm_bwd_workspace_size(d, int(gate is not None))
+    ws, n = _scratch(workspace, need, dev, "kda_block_norm_bwd_workspace_size", False)
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    st = lib().kda_block_norm_bwd(
+        d, _data(y, "y", y.shape, ty, dev), _data(w_post, "w_post", (D,), f32, dev),
+        _data(residual, "residual", y.shape, ty, dev),
+        None if gate is None else _data(gate, "gate", gate.shape, ty, dev),
+        _data(w_pre, "w_pre", (D,), f32, dev), _data(stats, "stats", (2, rows), f32, dev),
+        _data(d_out, "d_out", y.shape, ty, dev), _data(d_x, "d_x", y.shape, ty, dev),
+        ptr(dy), ptr(dres), ptr(dgate), ptr(dw_post), ptr(dw_pre), ws.data_ptr(), n,
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_block_norm_bwd")
+    return dy, dres, dgate, dw_post, dw_pre

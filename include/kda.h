@@ -496,6 +496,155 @@ KDA_API kda_status kda_chunk_bwd_from_saved(const kda_shape *s, const void *q, c
 KDA_API kda_status kda_selftest_wait_timeout(void *workspace, long long limit_cycles,
                                              kda_stream_t stream);
 
+/*
+ * The selective state space operator with its short causal convolution, on
+ * prompts (kda_ssm_fwd) and on single tokens (kda_ssm_step).  Per row and
+ * head, with the heads of group h / (H / G) sharing B and C:
+ *     u = SiLU(sum_{i=0}^{3} w[c][3-i] xbc_{t-i}[c] + bias[c])  = (x | B | C)
+ *     d = softplus(dt + dt_bias[h])
+ *     S = e^{d A[h]} S + d B (outer) x          S: [N][P], float32
+ *     y = (C^T S + D[h] x) SiLU(z)
+ * The channels of xbc are H heads of P (x), then G groups of N (B), then G
+ * groups of N (C).
+ *   xbc           device [B,T,H*P+2*G*N] of s->dtype: channels contiguous, rows
+ *                 and tokens at the shape's strides, so it may be a slice of
+ *                 a projection's output; likewise z [B,T,H*P] (NULL: no gate)
+ *                 and dt [B,T,H].
+ *   w, bias       device float32 [channels][4], [channels] (bias NULL: zeros).
+ *   A, D, dt_bias device float32 [H]; D, dt_bias NULL: zeros.  Contract: A <= 0.
+ *   state         float32 [..][H][N][P], the layout of the KDA states
+ *                 ([key][value]); conv state [..][3][channels] of s->dtype: the
+ *                 last three inputs of xbc, oldest first.
+ * N and P are 32, 64 or 128, G divides H (KDA_ERR_UNSUPPORTED, _INVALID_ARG).
+ */
+typedef struct kda_ssm_shape {
+  int B, T, H, P, N, G;
+  kda_dtype dtype;
+  /* element strides between rows and between tokens */
+  long long xbc_stride_b, xbc_stride_t, z_stride_b, z_stride_t, dt_stride_b, dt_stride_t;
+} kda_ssm_shape;
+/*
+ * Prompts.  segment_ids as kda_chunk_fwd: tokens of id 0 are padding (y = 0,
+ * the states are held), a run that is not its row's first starts from zero
+ * states.  initial_state [B,H,N,P] and conv_state [B,3,channels] (NULL:
+ * zeros) seed the row's first run.  Outputs: y [B,T,H,P]; final_state and
+ * conv_out (NULL: not wanted) after the row's last token that is not
+ * padding, for kda_ssm_step to go on from; a row without one passes its
+ * states on.  conv_out must not be conv_state's buffer.
+ *   impl          KDA_IMPL_AUTO, KDA_IMPL_SIMT (fp32 CUDA cores, every shape).
+ *   workspace     device, kda_ssm_fwd_workspace_size bytes, 256-byte aligned,
+ *                 zero-filled before its first use.
+ * xbc, z and the states are 16-byte aligned and the strides of xbc and z
+ * multiples of 16 bytes (KDA_ERR_ALIGNMENT).  Asynchronous on `stream`.
+ */
+KDA_API size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape *s, kda_impl impl);
+KDA_API kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt,
+                               const void *z, const float *w, const float *bias, const float *A,
+                               const float *D, const float *dt_bias, const float *initial_state,
+                               const void *conv_state, const int32_t *segment_ids, void *y,
+                               float *final_state, void *conv_out, void *workspace,
+                               size_t workspace_bytes, kda_impl impl, kda_stream_t stream);
+/*
+ * One token per sequence (s->T = 1; s's token strides are not read) on
+ * cached states, which are moved on in place: state [n_slots,H,N,P] and
+ * conv_state [n_slots,3,channels].  Sequence b uses place slots[b] (device
+ * int32 [B]; NULL: place b); a place outside [0, n_slots) marks an idle
+ * sequence, whose y is 0 and which touches no state.  The places of one call
+ * must differ.  y [B,H,P].
+ *   workspace     device, kda_step_workspace_size(B, H) bytes, 256-byte
+ *                 aligned, zero-filled before its first use; the call leaves
+ *                 it reusable.  Calls on different streams need their own.
+ * w and state are 16-byte aligned; xbc, z and dt need no alignment.
+ */
+KDA_API size_t kda_step_workspace_size(int B, int H);
+KDA_API kda_status kda_ssm_step(const kda_ssm_shape *s, const void *xbc, const void *dt,
+                                const void *z, const float *w, const float *bias, const float *A,
+                                const float *D, const float *dt_bias, const int32_t *slots,
+                                int n_slots, void *conv_state, float *state, void *y,
+                                void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * One token per sequence through the delta rule (s->T = 1) on cached states,
+ * which are moved on in place: the recurrence of kda_chunk_fwd, for the
+ * tokens that follow its prompt.
+ *   q, k, v       device [B,H,K|V] of s->qkv_dtype, heads contiguous, rows at the
+ *                 given element strides (slices of one projection will do).
+ *   g, beta       device float32 [B,H,K], [B,H], as kda_chunk_fwd.
+ *   conv_w, conv_state  both NULL, or the prologue of kda_short_conv_silu at
+ *                 this token: its weights ([H*(2K+V)][4]) and the cached inputs
+ *                 [n_slots,3,H*(2K+V)] (channels q | k | v, oldest first) of
+ *                 s->qkv_dtype, moved on in place.
+ *   l2norm_qk     != 0: q and k are scaled by (sum x^2 + 1e-6)^-1/2.
+ *   state         device float32 [n_slots,H,K,V], 16-byte aligned.
+ *   slots, n_slots, workspace  as kda_ssm_step.
+ *   o             device [B,H,V] of s->qkv_dtype.
+ * Everything between the inputs and o is fp32 (kda_short_conv_silu rounds
+ * q, k, v to s->qkv_dtype between its two kernels; this call does not).
+ */
+KDA_API kda_status kda_step(const kda_shape *s, const void *q, const void *k, const void *v,
+                            long long q_stride, long long k_stride, long long v_stride,
+                            const float *g, const float *beta, float scale, const float *conv_w,
+                            void *conv_state, int l2norm_qk, const int32_t *slots, int n_slots,
+                            float *state, void *o, void *workspace, size_t workspace_bytes,
+                            kda_stream_t stream);
+
+/*
+ * The norms before and after a block, fused with the block's gate and
+ * residual scale (the KDA layer's output gate norm is the case without
+ * residual and w_pre, one row per token and head).  Per row of `dim` values:
+ *     u   = y * (mean(y^2) + eps)^-1/2 * w_post
+ *     out = residual + scale * act(gate) * u
+ *     x   = out * (mean(out^2) + eps)^-1/2 * w_pre
+ * in fp32, rounded once at out and x (x is made from the unrounded out).
+ *   y, residual, out, x   device [rows, dim] of d->dtype, contiguous; residual
+ *                 NULL: no residual (zeros); out may be the residual's buffer.
+ *   gate          device [gate_rows, dim] of d->dtype or NULL (act(gate) = 1);
+ *                 gate row g serves rows [g, g + 1) * rows / gate_rows.
+ *   w_post, w_pre device float32 [dim]; w_pre and x both NULL: no second norm.
+ *   stats         device float32 [2, rows] or NULL: the two inverse root mean
+ *                 squares, which the backward reads (the second is 0 without w_pre).
+ * dim is 1 to 16384 and rows below 2^31 (KDA_ERR_UNSUPPORTED above); gate_rows
+ * divides rows.  Pointers that are not 16-byte aligned and dims that do not
+ * fill 16-byte accesses are served, at lower speed.  Asynchronous on `stream`.
+ */
+typedef enum kda_gate_act {
+  KDA_GATE_NONE = 0,
+  KDA_GATE_SIGMOID = 1,
+  KDA_GATE_SILU = 2,
+  KDA_GATE_TANH = 3
+} kda_gate_act;
+typedef struct kda_norm_desc {
+  long long rows;
+  int dim;
+  kda_dtype dtype;
+  kda_gate_act gate_act;
+  long long gate_rows;  /* read only when a gate is given */
+  float scale, eps;
+} kda_norm_desc;
+KDA_API kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y, const float *w_post,
+                                      const void *residual, const void *gate, const float *w_pre,
+                                      void *out, void *x, float *stats, kda_stream_t stream);
+/*
+ * Its gradients, from the inputs and the forward's stats.
+ *   d_out, d_x    device [rows, dim] of d->dtype; one of them may be NULL
+ *                 (zeros); d_x needs w_pre.
+ *   dy            device [rows, dim] of d->dtype.
+ *   d_residual, d_gate  of d->dtype, or NULL (not wanted); d_gate [gate_rows,
+ *                 dim] is the sum over the rows a gate row serves.
+ *   dw_post, dw_pre     device float32 [dim]; dw_pre exactly when w_pre is given.
+ *   workspace     device, kda_block_norm_bwd_workspace_size bytes, 16-byte
+ *                 aligned; needs no initialisation.
+ * Sums over rows are fp32, in an order that depends on the sizes alone, so
+ * repeated calls agree bit for bit.  Outputs must not alias inputs.
+ */
+KDA_API size_t kda_block_norm_bwd_workspace_size(const kda_norm_desc *d, int has_gate);
+KDA_API kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float *w_post,
+                                      const void *residual, const void *gate, const float *w_pre,
+                                      const float *stats, const void *d_out, const void *d_x,
+                                      void *dy, void *d_residual, void *d_gate, float *dw_post,
+                                      float *dw_pre, void *workspace, size_t workspace_bytes,
+                                      kda_stream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 KDA_API const char *kda_status_string(kda_status status);
 
