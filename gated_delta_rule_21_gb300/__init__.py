@@ -637,12 +637,14 @@ def _cuda(t, where):
     return t.device, t.dtype
 
 
-def _scratch(workspace, need, device, where, zero):
+def _scratch(workspace, need, device, where, zeros):
+    """The workspace, or a new one whose first ``zeros`` bytes are zero."""
     if workspace is None:
         if need == 0:
             raise KdaError(2, where)
-        make = torch.zeros if zero else torch.empty
-        workspace = make(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if zeros:
+            workspace[:zeros].zero_()
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()
@@ -689,7 +691,7 @@ def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_stat
         conv_w = conv_w.view(-1, 4)
     o = torch.empty((B, H, V), dtype=dt, device=dev) if out is None else out
     ws, n = _scratch(workspace, step_workspace_size(B, H) if workspace is None else 0, dev,
-                     "kda_step_workspace_size", True)
+                     "kda_step_workspace_size", 1 << 40)
     st = lib().kda_step(
         kda_shape(B, 1, H, K, V, DTYPES[dt]), q.data_ptr(), k.data_ptr(), v.data_ptr(),
         q.stride(0), k.stride(0), v.stride(0), _data(g, "g", (B, H, K), f32, dev),
@@ -721,11 +723,9 @@ def ssm_workspace_size(B, T, H, P, N, G, dtype=torch.bfloat16, impl="auto") -> i
 
 def alloc_ssm_workspace(B, T, H, P, N, G, dtype=torch.bfloat16, impl="auto",
                         device=None) -> torch.Tensor:
-    """Zero-filled workspace of :func:`ssm_fwd`."""
-    n = ssm_workspace_size(B, T, H, P, N, G, dtype, impl)
-    if n == 0:
-        raise KdaError(2, "kda_ssm_fwd_workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    """Workspace of :func:`ssm_fwd`, its header zero-filled."""
+    return _scratch(None, ssm_workspace_size(B, T, H, P, N, G, dtype, impl), device or "cuda",
+                    "kda_ssm_fwd_workspace_size", 256)[0]
 
 
 def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=None, D=None,
@@ -756,7 +756,7 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     xs, ds = xbc.stride(), dt.stride()
     s = kda_ssm_shape(B, T, H, P, N, G, DTYPES[ty], xs[0], xs[1], zs[0], zs[1], ds[0], ds[1])
     ws, n = _scratch(workspace, lib().kda_ssm_fwd_workspace_size(s, IMPLS[impl])
-                     if workspace is None else 0, dev, "kda_ssm_fwd_workspace_size", True)
+                     if workspace is None else 0, dev, "kda_ssm_fwd_workspace_size", 256)
     st = lib().kda_ssm_fwd(
         s, xbc.data_ptr(), dt.data_ptr(), None if z is None else z.data_ptr(),
         _data(conv_w, "conv_w", (C, 4), f32, dev), _data(conv_bias, "conv_bias", (C,), f32, dev),
@@ -789,7 +789,7 @@ def ssm_step(xbc, dt, conv_w, A, state, conv_state, *, head_dim, state_dim, conv
             _inner(t, name, 1)
     y = torch.empty((B, H, P), dtype=ty, device=dev) if out is None else out
     ws, n = _scratch(workspace, step_workspace_size(B, H) if workspace is None else 0, dev,
-                     "kda_step_workspace_size", True)
+                     "kda_step_workspace_size", 1 << 40)
     s = kda_ssm_shape(B, 1, H, P, N, G, DTYPES[ty], xbc.stride(0), 0,
                       0 if z is None else z.stride(0), 0, dt.stride(0), 0)
     st = lib().kda_ssm_step(
@@ -886,7 +886,7 @@ def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=Non
     need = 0
     if workspace is None:
         need = lib().kda_block_norm_bwd_workspace_size(d, int(gate is not None))
-    ws, n = _scratch(workspace, need, dev, "kda_block_norm_bwd_workspace_size", False)
+    ws, n = _scratch(workspace, need, dev, "kda_block_norm_bwd_workspace_size", 0)
 
     def ptr(t):
         return None if t is None else t.data_ptr()

@@ -197,8 +197,12 @@ extern "C" {
 
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape *s, kda_impl impl) {
   if (check_ssm_shape(s) != KDA_OK) return 0;
-  if (impl != KDA_IMPL_AUTO && impl != KDA_IMPL_SIMT) return 0;
-  return rows_bytes(s->B);
+  const bool bf16 = s->dtype == KDA_DTYPE_BF16;
+  if (impl == KDA_IMPL_SIMT || (impl == KDA_IMPL_AUTO && !bf16)) return rows_bytes(s->B);
+  if ((impl != KDA_IMPL_AUTO && impl != KDA_IMPL_TC) || !bf16) return 0;
+  SsmParams p = {};
+  p.B = s->B; p.T = s->T; p.H = s->H; p.P = s->P; p.N = s->N; p.G = s->G;
+  return rows_bytes(s->B) + ssm_tc_bytes(p);
 }
 
 kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt, const void *z,
@@ -242,7 +246,10 @@ kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt, 
   if (bf16) ssm_rows_kernel<__nv_bfloat16><<<s->B, 512, 0, cs>>>(p);
   else ssm_rows_kernel<float><<<s->B, 512, 0, cs>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess)
+  if (e != cudaSuccess) return KDA_ERR_CUDA;
+  if (bf16 && impl != KDA_IMPL_SIMT)
+    e = launch_ssm_tc(p, &reinterpret_cast<WsHeader *>(workspace)->status, cs);
+  else
     e = bf16 ? launch_simt_t<__nv_bfloat16>(p, cs) : launch_simt_t<float>(p, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -1,0 +1,908 @@
+// kda_ssm_tc.cu -- the selective state space operator on prompts, on the
+// tensor cores (tcgen05): bf16 activations, every N, P in {32, 64, 128}.
+//
+// In blocks of 128 tokens, with c_r the sum of d A over a block's tokens up to
+// r and S the state that enters the block,
+//     y_r  = e^{c_r} C_r^T S + sum_{j <= r} (C_r . B_j) e^{c_r - c_j} d_j x_j
+//     S'   = e^{c_127} S + sum_j e^{c_127 - c_j} d_j B_j (outer) x_j
+// so a block is three products of 128 rows and the state is carried from
+// block to block.  Three launches:
+//   1. ssm_prep_kernel: the convolution of B and C into operand tiles, and per
+//      token and head the factors above (all blocks in parallel).
+//   2. ssm_state_kernel: one CTA per (row, head, column tile) walks the blocks:
+//      the convolution of x, S' and, for each block, the S that enters it.
+//   3. ssm_out_kernel: y of every (block, head), all in parallel.
+//
+// Rounding.  The final state is carried to tokens and on, so S' is formed to
+// fp32 grade: B and the scaled x are each split into two bf16 parts, three
+// of the four products are kept (the dropped one is below 2^-16 of a term)
+// and S is updated in fp32 registers, never in the accumulator.  y is rounded
+// to bf16 at the end, and its products' operands (C, B, x, S and the 128 x 128
+// matrix of factors) are bf16 too; their errors are of y's own rounding's
+// size and average out over the sums.
+#include "kda_ssm.cuh"
+#include "kda_tc_common.cuh"
+#include "kda_f32x2.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+using bf16 = __nv_bfloat16;
+
+constexpr int kQ = 128;            // tokens per block
+constexpr int kConv = 256;         // threads that run the convolution
+
+// What the kernels hand to one another, in the workspace.
+struct TcBufs {
+  int nb;                          // blocks per row
+  unsigned char *bhi, *blo, *ct;   // [B][nb][G] tiles (token, state), op_off(t, n, N)
+  unsigned char *xt;               // [B][nb][H] tiles of x, mn_off(p, t, 128)
+  unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
+  float *ein, *wst, *cum, *cumj;   // [B][H][nb * 128], see prep_factors
+  float *dec;                      // [B][H][nb]: e^{c_127}, or -1: the block resets the state
+  int *run;                        // [B][nb * 128]: resets so far in the block, -1: padding
+  unsigned char *tok;              // [B][nb * 128]: place | first << 2 | live << 3
+  int *flags;                      // [B][nb]: kPlain, kResets
+  uint32_t *status;
+};
+constexpr int kPlain = 1;          // every token has its whole window in the staged rows
+constexpr int kResets = 2;
+
+size_t layout_bufs(const SsmParams &p, unsigned char *base, TcBufs *t) {
+  const int nb = (p.T + kQ - 1) / kQ;
+  const size_t bt = (size_t)p.B * nb, toks = bt * kQ;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    unsigned char *q = base + off;
+    off += align_up(n, 256);
+    return q;
+  };
+  t->nb = nb;
+  t->bhi = take(bt * p.G * kQ * p.N * 2);
+  t->blo = take(bt * p.G * kQ * p.N * 2);
+  t->ct = take(bt * p.G * kQ * p.N * 2);
+  t->xt = take(bt * p.H * kQ * p.P * 2);
+  t->st = take(bt * p.H * p.N * p.P * 2);
+  t->ein = (float *)take(toks * p.H * 4);
+  t->wst = (float *)take(toks * p.H * 4);
+  t->cum = (float *)take(toks * p.H * 4);
+  t->cumj = (float *)take(toks * p.H * 4);
+  t->dec = (float *)take(bt * p.H * 4);
+  t->run = (int *)take(toks * 4);
+  t->tok = take(toks);
+  t->flags = (int *)take(bt * 4);
+  return off;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// The convolution of a tile of TP channels x 128 tokens by 256 threads.  The
+// tile's rows and the 3 before it are staged by cp.async; a warp owns 8
+// channels and a lane a strip of consecutive tokens, an odd number of them,
+// so that the 16-byte reads of the staged rows and the 16-byte writes of the
+// operand tiles touch all banks.
+template <int TP>
+struct Conv {
+  static constexpr int kPieces = TP / 8;                   // 8-channel pieces per row
+  static constexpr int kParts = kConv / 32 / kPieces;      // warps per piece
+  static constexpr int kSpan = kQ / kParts;                // tokens per warp
+  static constexpr int kStrip = (kSpan + 31) / 32 % 2 ? (kSpan + 31) / 32 : (kSpan + 31) / 32 + 1;
+  static constexpr int kRows = kQ + kSsmTaps - 1;
+  static constexpr uint32_t kBytes = TP == 64 ? kRows * 128u : kRows * 80u;
+
+  // 64 channels: rows of 128 bytes whose pieces are permuted by the row;
+  // 32 channels: rows of 80 bytes.
+  static __device__ __forceinline__ uint32_t off(int row, int piece) {
+    return TP == 64 ? (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4))
+                    : (uint32_t)(row * 80 + piece * 16);
+  }
+
+  float wt[8][kSsmTaps], bias[8];
+
+  __device__ __forceinline__ void weights(const SsmParams &p, int channel) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float4 w = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)(channel + c));
+      wt[c][0] = w.x; wt[c][1] = w.y; wt[c][2] = w.z; wt[c][3] = w.w;
+      bias[c] = p.bias ? p.bias[channel + c] : 0.f;
+    }
+  }
+
+  // x: the row's token 0 at the tile's channel; past: the cached inputs that
+  // precede it (or null), for a row whose first run starts at token 0.
+  static __device__ __forceinline__ void stage(uint32_t dst, const bf16 *x, long long st,
+                                               const bf16 *past, int channels, int t0, int T,
+                                               int tid) {
+    for (int i = tid; i < kRows * kPieces; i += kConv) {
+      const int row = i / kPieces, piece = i % kPieces, t = t0 - (kSsmTaps - 1) + row;
+      const bf16 *src = x;
+      bool ok = t >= 0 && t < T;
+      if (ok) {
+        src = x + (long long)t * st + piece * 8;
+      } else if (t < 0 && past) {
+        src = past + (size_t)(kSsmTaps - 1 + t) * channels + piece * 8;
+        ok = true;
+      }
+      cp_async16(dst + off(row, piece), src, ok);
+    }
+    cp_async_commit();
+  }
+
+  // f(j, u): token j of the block, u = SiLU(conv) of the warp's 8 channels.
+  // tok (null: a plain block): the tokens' windows; past: the cached inputs
+  // of the row at the tile's channel, or null.
+  template <typename F>
+  __device__ __forceinline__ void run(const unsigned char *rows, int tid, const unsigned char *tok,
+                                      const bf16 *past, int channels, F f) const {
+    const int warp = tid >> 5, lane = tid & 31, piece = warp % kPieces;
+    const int begin = warp / kPieces * kSpan + lane * kStrip;
+    const int end = min(begin + kStrip, (warp / kPieces + 1) * kSpan);
+    float win[kSsmTaps - 1][8];
+#pragma unroll
+    for (int i = 0; i < kSsmTaps - 1; ++i) {
+      const int r = min(begin + i, kRows - 1);
+      ld_bf16x8(rows + off(r, piece), win[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kStrip; ++i) {
+      const int j = begin + i;
+      if (j < end) {
+        float x[8], u[8];
+        ld_bf16x8(rows + off(j + kSsmTaps - 1, piece), x);
+        if (!tok) {
+          taps(win[0], win[1], win[2], x, u);
+        } else {
+          const int k = tok[j], place = k & 3;
+          float a[kSsmTaps - 1][8];
+#pragma unroll
+          for (int age = 1; age < kSsmTaps; ++age) {
+            float(&w)[8] = a[kSsmTaps - 1 - age];
+            if (age <= place) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) w[c] = win[kSsmTaps - 1 - age][c];
+            } else if ((k & 4) && past) {
+              ld_bf16x8(reinterpret_cast<const unsigned char *>(
+                            past + (size_t)(kSsmTaps - 1 + place - age) * channels + piece * 8),
+                        w);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) w[c] = 0.f;
+            }
+          }
+          taps(a[0], a[1], a[2], x, u);
+          if (!(k & 8))
+#pragma unroll
+            for (int c = 0; c < 8; ++c) u[c] = 0.f;
+        }
+        f(j, u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          win[0][c] = win[1][c];
+          win[1][c] = win[2][c];
+          win[2][c] = x[c];
+        }
+      }
+    }
+  }
+
+ private:
+  __device__ __forceinline__ void taps(const float (&a)[8], const float (&b)[8],
+                                       const float (&c)[8], const float (&x)[8],
+                                       float (&u)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      u64 v = fma2(pk2(wt[i][3], wt[i + 1][3]), pk2(x[i], x[i + 1]), pk2(bias[i], bias[i + 1]));
+      v = fma2(pk2(wt[i][2], wt[i + 1][2]), pk2(c[i], c[i + 1]), v);
+      v = fma2(pk2(wt[i][1], wt[i + 1][1]), pk2(b[i], b[i + 1]), v);
+      v = fma2(pk2(wt[i][0], wt[i + 1][0]), pk2(a[i], a[i + 1]), v);
+      float e0, e1, d0, d1;
+      upk2(mul2(v, pk2(-kLog2e, -kLog2e)), e0, e1);
+      upk2(add2(pk2(1.f, 1.f), pk2(ex2(e0), ex2(e1))), d0, d1);
+      upk2(mul2(v, pk2(rcp(d0), rcp(d1))), u[i], u[i + 1]);
+    }
+  }
+  static __device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+  }
+};
+
+// 8 values as bf16, and what that leaves, again as bf16.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    l[i] = pack_bf16(v[2 * i] - __uint_as_float(h[i] << 16),
+                     v[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                    pack_bf16(v[6], v[7]));
+}
+
+__device__ __forceinline__ SsmRow row_of(const SsmParams &p, int b) {
+  if (p.segment_ids) return p.rows[b];
+  SsmRow r = {0, p.T, p.T - 1, 0};
+  return r;
+}
+__device__ __forceinline__ const bf16 *past_of(const SsmParams &p, int b) {
+  return p.conv_state ? static_cast<const bf16 *>(p.conv_state) +
+                            (size_t)b * (kSsmTaps - 1) * p.channels
+                      : nullptr;
+}
+
+// ---------------------------------------------------------------------------
+// 1. prep
+
+// Per token and head of a block, a = d A log2(e):
+//   cum  = sum of a up to the token            cumj = cum - log2 d
+//   ein  = 2^cum where the entering state reaches the token, else 0
+//   wst  = d 2^(sum of a after the token) where the token reaches the state
+//          that leaves the block, else 0 (summed from the end: exact where
+//          it matters)
+// A warp takes a head, a lane 4 tokens.
+__device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t, int b, int blk,
+                                             unsigned char *smem) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blk * kQ;
+  const int32_t *ids = p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr;
+  int *srun = reinterpret_cast<int *>(smem);                   // [128]
+  int *scount = srun + kQ;                                     // resets per warp
+  float *sdt = reinterpret_cast<float *>(scount + 8);          // [128][33]
+  const SsmRow row = row_of(p, b);
+  int n = 0, plain = 1;
+  SsmToken k = {};
+  if (tid < kQ) {
+    k = ssm_token(ids, t0 + tid, p.T, row);
+    const unsigned m = __ballot_sync(0xffffffffu, k.reset);
+    n = __popc(m & (0xffffffffu >> (31 - lane)));
+    if (lane == 0) scount[warp] = __popc(m);
+    // the rows before token 0 are staged from the cache
+    plain = t0 + tid >= p.T ||
+            (k.live && (k.place == kSsmTaps - 1 || (row.first == 0 && t0 + tid == k.place)));
+  }
+  plain = __syncthreads_and(plain);
+  if (tid < kQ) {
+    for (int w = 0; w < warp; ++w) n += scount[w];
+    srun[tid] = n;
+    const size_t at = (size_t)b * t.nb * kQ + t0 + tid;
+    t.run[at] = k.live ? n : -1;
+    t.tok[at] = (unsigned char)(k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0));
+  }
+  if (tid == 0) {
+    const int resets = scount[0] + scount[1] + scount[2] + scount[3];
+    t.flags[(size_t)b * t.nb + blk] = (plain ? kPlain : 0) | (resets ? kResets : 0);
+  }
+  const bf16 *dt = static_cast<const bf16 *>(p.dt) + (size_t)b * p.dt_sb;
+  for (int h0 = 0; h0 < p.H; h0 += 32) {
+    const int nh = min(32, p.H - h0);
+    __syncthreads();
+    for (int i = tid; i < kQ * 32; i += blockDim.x) {
+      const int tt = i >> 5, hh = i & 31;
+      float d = 0.f;
+      if (hh < nh && t0 + tt < p.T && ssm_id(ids, t0 + tt, p.T) != 0)
+        d = ssm_softplus(to_f32(dt[(long long)(t0 + tt) * p.dt_st + h0 + hh]) +
+                         (p.dt_bias ? p.dt_bias[h0 + hh] : 0.f));
+      sdt[tt * 33 + hh] = d;
+    }
+    __syncthreads();
+    for (int hh = warp; hh < nh; hh += kConv / 32) {
+      const float a2 = p.A[h0 + hh] * kLog2e;
+      float d[4], a[4], pre[4], suf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = sdt[(lane * 4 + i) * 33 + hh];
+        a[i] = d[i] > 0.f ? d[i] * a2 : 0.f;
+      }
+      pre[0] = a[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + a[i];
+      suf[3] = 0.f;
+#pragma unroll
+      for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + a[i + 1];
+      const float sum = pre[3];
+      float before = sum, after = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, before, o);
+        const float v = __shfl_down_sync(0xffffffffu, after, o);
+        if (lane >= o) before += u;
+        if (lane + o < 32) after += v;
+      }
+      const float total = __shfl_sync(0xffffffffu, before, 31);
+      before = __shfl_up_sync(0xffffffffu, before, 1);
+      after = __shfl_down_sync(0xffffffffu, after, 1);
+      if (lane == 0) before = 0.f;
+      if (lane == 31) after = 0.f;
+      const int last = srun[kQ - 1];
+      float4 ein, wst, cum, cumj;
+      float *fe = &ein.x, *fw = &wst.x, *fc = &cum.x, *fj = &cumj.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int run = srun[lane * 4 + i];
+        fc[i] = before + pre[i];
+        fj[i] = fc[i] - log2f(d[i]);     // d = 0: +inf, a factor of 0
+        fe[i] = run == 0 ? exp2f(fc[i]) : 0.f;
+        fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : 0.f;
+      }
+      const size_t at = (((size_t)b * p.H + h0 + hh) * t.nb + blk) * kQ + lane * 4;
+      *reinterpret_cast<float4 *>(t.ein + at) = ein;
+      *reinterpret_cast<float4 *>(t.wst + at) = wst;
+      *reinterpret_cast<float4 *>(t.cum + at) = cum;
+      *reinterpret_cast<float4 *>(t.cumj + at) = cumj;
+      if (lane == 0)
+        t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] = last == 0 ? exp2f(total) : -1.f;
+    }
+  }
+}
+
+// The convolution of TP channels of B or C into its operand tiles.
+template <int TP>
+__device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, int b, int blk,
+                                          int g, int part, unsigned char *smem) {
+  const int tid = threadIdx.x, t0 = blk * kQ;
+  const bool is_c = part >= p.N / TP;
+  const int n0 = (is_c ? part - p.N / TP : part) * TP;
+  const int ch = p.H * p.P + (is_c ? p.G * p.N : 0) + g * p.N + n0;
+  const SsmRow row = row_of(p, b);
+  const bf16 *past = past_of(p, b);
+  const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
+  Conv<TP>::stage(smem_u32(smem), x, p.xbc_st, past && row.first == 0 ? past + ch : nullptr,
+                  p.channels, t0, p.T, tid);
+  Conv<TP> cv;
+  const int piece = (tid >> 5) % Conv<TP>::kPieces;
+  cv.weights(p, ch + piece * 8);
+  // whether any token's window leaves the staged rows
+  unsigned char *stok = smem + Conv<TP>::kBytes;
+  int plain = 1;
+  if (tid < kQ) {
+    const SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr,
+                                 t0 + tid, p.T, row);
+    stok[tid] = (unsigned char)(k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0));
+    plain = t0 + tid >= p.T ||
+            (k.live && (k.place == kSsmTaps - 1 || (row.first == 0 && t0 + tid == k.place)));
+  }
+  cp_async_wait_all();
+  plain = __syncthreads_and(plain);
+  const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2;
+  const uint32_t at = (uint32_t)((n0 / 8 + piece) * 128);
+  cv.run(smem, tid, plain ? nullptr : stok, past ? past + ch : nullptr, p.channels,
+         [&](int j, float(&u)[8]) {
+           const size_t o = tile + at + (j & 7) * 16 + (size_t)(j >> 3) * p.N * 16;
+           if (is_c) {
+             *reinterpret_cast<uint4 *>(t.ct + o) = pack8(u);
+           } else {
+             uint4 hi, lo;
+             split8(u, hi, lo);
+             *reinterpret_cast<uint4 *>(t.bhi + o) = hi;
+             *reinterpret_cast<uint4 *>(t.blo + o) = lo;
+           }
+         });
+}
+
+// CTAs [0, B nb) make the factors, the others one tile of B or C each.
+template <int TP>
+__global__ void __launch_bounds__(kConv) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  int u = blockIdx.x;
+  if (u < p.B * t.nb) {
+    prep_factors(p, t, u / t.nb, u % t.nb, smem);
+    return;
+  }
+  u -= p.B * t.nb;
+  const int parts = 2 * p.N / TP;
+  const int part = u % parts;
+  u /= parts;
+  const int g = u % p.G;
+  u /= p.G;
+  prep_conv<TP>(p, t, u / t.nb, u % t.nb, g, part, smem);
+}
+
+// ---------------------------------------------------------------------------
+// 2. states
+
+// Barrier of the 256 convolving threads; whether any of them says so.
+__device__ __forceinline__ bool any_of_conv(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kConv)
+      : "memory");
+  return r != 0;
+}
+
+// Shared memory of ssm_state_kernel.
+template <int TP>
+struct StateSmem {
+  static constexpr uint32_t kX = 0;                                 // 2 x [hi | lo] tiles
+  static constexpr uint32_t kXBytes = kQ * TP * 2 * 2;
+  static constexpr uint32_t kB = kX + 2 * kXBytes;                  // 2 x (hi, lo) tiles
+  static constexpr uint32_t kBBytes = 2 * kQ * 128 * 2;
+  static constexpr uint32_t kRows = kB + 2 * kBBytes;               // 2 staged tiles of x
+  static constexpr uint32_t kW = kRows + 2 * Conv<TP>::kBytes;      // 2 x wst
+  static constexpr uint32_t kBar = kW + 2 * kQ * 4;
+  static constexpr uint32_t kBytes = kBar + 64;
+};
+
+// 256 threads run the convolution, keep S and write it; a ninth warp copies
+// the tiles of B and issues the products.  Per block i the threads
+//   convolve x into the operand buffer i % 2 while the products of block
+//   i - 1 run, then wait for those, write the S that entered block i - 1 and
+//   update it.
+// A thread holds TP / 2 columns of one state row (its TMEM lane).
+template <int TP>
+__global__ void __launch_bounds__(kConv + 32, 1)
+    ssm_state_kernel(const SsmParams p, const TcBufs t) {
+  using L = StateSmem<TP>;
+  constexpr int kCols = TP / 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint32_t s_tmem;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t bar_x = sb + L::kBar, bar_b = bar_x + 16, bar_d = bar_x + 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = p.P / TP, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int h = bh % p.H, b = bh / p.H, g = h / (p.H / p.G), c0 = tile * TP;
+  const int nb = t.nb, N = p.N;
+  if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 4 * TP);
+  if (tid == 0) {
+    mbar_init(bar_x, kConv);
+    mbar_init(bar_x + 8, kConv);
+    mbar_init(bar_b, 1);
+    mbar_init(bar_b + 8, 1);
+    mbar_init(bar_d, 1);
+    mbar_init(bar_d + 8, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
+
+  if (warp == kConv / 32) {
+    if (lane == 0) {
+      const uint32_t tb = (uint32_t)(kQ * N * 2);
+      auto load = [&](int i) {
+        const size_t o = (((size_t)b * nb + i) * p.G + g) * tb;
+        const uint32_t bar = bar_b + 8u * (i & 1), dst = sb + L::kB + (i & 1) * L::kBBytes;
+        mbar_expect_tx(bar, 2 * tb);
+        bulk_load(dst, t.bhi + o, tb, bar);
+        bulk_load(dst + tb, t.blo + o, tb, bar);
+      };
+      int loaded = 0, landed = 0, issued = 0, done = 0;
+      bool ok = true;
+      for (; loaded < 2 && loaded < nb; ++loaded) load(loaded);
+      for (int i = 0; i < nb && ok; ++i) {
+        ok = mbar_wait(bar_b + 8u * (i & 1), (i >> 1) & 1);
+        if (!ok) break;
+        ++landed;
+        ok = mbar_wait(bar_x + 8u * (i & 1), (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (i & 1) * 2 * TP;
+        const uint32_t bt = sb + L::kB + (i & 1) * L::kBBytes;
+        const Opnd x = {sb + L::kX + (i & 1) * L::kXBytes, 128, kQ * 16};
+        const Opnd bh_ = {bt, (uint32_t)N * 16, 128}, bl_ = {bt + tb, (uint32_t)N * 16, 128};
+        mma_k(d, bh_, 1, x, 1, kQ / 16, 2 * TP, false);
+        mma_k(d, bl_, 1, x, 1, kQ / 16, TP, true);
+        mma_commit(bar_d + 8u * (i & 1));
+        ++issued;
+        if (i > 0 && loaded < nb) {      // block i - 1's tiles are free once it is done
+          ok = mbar_wait(bar_d + 8u * ((i - 1) & 1), ((i - 1) >> 1) & 1);
+          if (!ok) break;
+          ++done;
+          load(loaded++);
+        }
+      }
+      if (!ok) set_status(t.status, KDA_DEVICE_TIMEOUT);
+      // nothing of this warp's is in flight when it leaves
+      for (int i = landed; i < loaded; ++i) mbar_wait(bar_b + 8u * (i & 1), (i >> 1) & 1);
+      for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i)
+        mbar_wait(bar_d + 8u * (i & 1), (i >> 1) & 1);
+    }
+    __syncwarp();
+  } else {
+    const SsmRow row = row_of(p, b);
+    const bf16 *past = past_of(p, b);
+    const int ch = h * p.P + c0;
+    const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
+    const bf16 *before = past && row.first == 0 ? past + ch : nullptr;
+    const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
+    const float *dec = t.dec + ((size_t)b * p.H + h) * nb;
+    Conv<TP> cv;
+    const int piece = warp % Conv<TP>::kPieces;
+    cv.weights(p, ch + piece * 8);
+    const int n = 32 * (warp & 3) + lane, col0 = (warp >> 2) * kCols;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col0;
+    const size_t state = (((size_t)b * p.H + h) * N + n) * p.P + c0 + col0;
+    float s[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) s[i] = 0.f;
+    if (p.initial_state && n < N) {
+#pragma unroll
+      for (int i = 0; i < kCols; i += 4)
+        *reinterpret_cast<float4 *>(s + i) =
+            *reinterpret_cast<const float4 *>(p.initial_state + state + i);
+    }
+    auto stage = [&](int i) {
+      if (i < nb) {
+        if (tid < kQ / 4)
+          cp_async16(sb + L::kW + (i & 1) * kQ * 4 + tid * 16, wst + (size_t)i * kQ + tid * 4, true);
+        Conv<TP>::stage(sb + L::kRows + (i & 1) * Conv<TP>::kBytes, x, p.xbc_st, before,
+                        p.channels, i * kQ, p.T, tid);
+      }
+    };
+    bool bad = false;
+    // the state after block i, once its products are done
+    auto finish = [&](int i) {
+      if (n < N) {
+        unsigned char *st = t.st + ((((size_t)b * nb + i) * p.H + h) * N) * p.P * 2 +
+                            (size_t)((c0 + col0) / 8) * N * 16 + (n >> 3) * 128 + (n & 7) * 16;
+#pragma unroll
+        for (int k = 0; k < kCols; k += 8) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = s[k + e];
+          *reinterpret_cast<uint4 *>(st + (size_t)(k / 8) * N * 16) = pack8(v);
+        }
+      }
+      const float a = dec[i];
+      if (!mbar_wait(bar_d + 8u * (i & 1), (i >> 1) & 1)) {
+        bad = true;
+        set_status(t.status, KDA_DEVICE_TIMEOUT);
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < kCols; k += 16) {
+        float hi[16], lo[16];
+        tmem_ld16x2(tl + (i & 1) * 2 * TP + k, tl + (i & 1) * 2 * TP + TP + k, hi, lo);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float d = hi[e] + lo[e];
+          s[k + e] = a < 0.f ? d : fmaf(a, s[k + e], d);
+        }
+      }
+      tc_fence_before();
+    };
+    stage(0);
+    int i = 0;
+    for (; i < nb; ++i) {
+      cp_async_wait_all();
+      if (any_of_conv(bad)) break;   // a wait ran out somewhere: all leave
+      stage(i + 1);
+      const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
+      unsigned char *xo = smem + L::kX + (i & 1) * L::kXBytes + piece * 2048;
+      unsigned char *xt = t.xt + (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
+                          (size_t)(c0 / 8 + piece) * 2048;
+      const bool plain = (t.flags[(size_t)b * nb + i] & kPlain) != 0;
+      cv.run(smem + L::kRows + (i & 1) * Conv<TP>::kBytes, tid,
+             plain ? nullptr : t.tok + ((size_t)b * nb + i) * kQ, past ? past + ch : nullptr,
+             p.channels, [&](int j, float(&u)[8]) {
+               const int o = (j >> 3) * 128 + (j & 7) * 16;
+               *reinterpret_cast<uint4 *>(xt + o) = pack8(u);
+               const float f = w[j];
+               // a token that does not reach the state adds nothing, whatever it holds
+#pragma unroll
+               for (int e = 0; e < 8; ++e) u[e] = f != 0.f ? u[e] * f : 0.f;
+               uint4 hi, lo;
+               split8(u, hi, lo);
+               *reinterpret_cast<uint4 *>(xo + o) = hi;
+               *reinterpret_cast<uint4 *>(xo + TP / 8 * 2048 + o) = lo;
+             });
+      fence_proxy_async();
+      tc_fence_before();
+      mbar_arrive(bar_x + 8u * (i & 1));
+      if (i > 0) finish(i - 1);
+    }
+    cp_async_wait_all();
+    if (i == nb) finish(nb - 1);
+    if (p.final_state && n < N) {
+#pragma unroll
+      for (int k = 0; k < kCols; k += 4)
+        *reinterpret_cast<float4 *>(p.final_state + state + k) =
+            make_float4(s[k], s[k + 1], s[k + 2], s[k + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 4 * TP);
+}
+
+// ---------------------------------------------------------------------------
+// 3. outputs
+
+// Shared memory of ssm_out_kernel: C; B, then the matrix of factors; x; the
+// entering state, then z and y.
+template <int PT>
+struct OutSmem {
+  static constexpr uint32_t kC = 0;
+  static constexpr uint32_t kF = kC + kQ * 128 * 2;
+  static constexpr uint32_t kX = kF + kQ * kQ * 2;
+  static constexpr uint32_t kS = kX + kQ * PT * 2;
+  static constexpr uint32_t kV = kS + kQ * PT * 2;     // ein, cum, cumj, run: 128 each
+  static constexpr uint32_t kBar = kV + 4 * kQ * 4;
+  static constexpr uint32_t kBytes = kBar + 32;
+};
+
+// One CTA per (row, block, group, `heads` of its heads); TMEM holds C B^T of
+// the block, shared by the heads, and the two parts of y of PT columns.  Two
+// CTAs fit an SM and fill each other's waits.
+template <int PT>
+__global__ void __launch_bounds__(256, 2)
+    ssm_out_kernel(const SsmParams p, const TcBufs t, int heads) {
+  using L = OutSmem<PT>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint32_t s_tmem;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t bar_cb = sb + L::kBar, bar_xs = bar_cb + 8, bar_m = bar_cb + 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quad = warp & 3, half = warp >> 2, r = 32 * quad + lane;
+  const int nb = t.nb, N = p.N, hg = p.H / p.G, per = (hg + heads - 1) / heads;
+  int u = blockIdx.x;
+  const int part = u % per;
+  u /= per;
+  const int g = u % p.G;
+  u /= p.G;
+  const int blk = u % nb, b = u / nb, t0 = blk * kQ;
+  const int h_lo = g * hg + part * heads, h_hi = min(h_lo + heads, (g + 1) * hg);
+  const int subs = p.P / PT;
+  const int n_items = (h_hi - h_lo) * subs;
+  if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 128 + 2 * PT > 256 ? 512 : 256);
+  if (tid == 0) {
+    mbar_init(bar_cb, 1);
+    mbar_init(bar_xs, 1);
+    mbar_init(bar_m, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
+  const uint32_t t_cb = tmem, t_yi = tmem + 128, t_yx = tmem + 128 + PT;
+  const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+  uint32_t n_m = 0;       // commits waited for
+  bool bad = false;
+  auto give_up = [&]() {
+    bad = true;
+    set_status(t.status, KDA_DEVICE_TIMEOUT);
+  };
+  auto wait_mma = [&]() {
+    if (!mbar_wait(bar_m, n_m & 1)) give_up();
+    ++n_m;
+    tc_fence_after();
+  };
+  const uint32_t tile = (uint32_t)(kQ * N * 2);
+  const uint32_t xs_bytes = (uint32_t)(kQ * PT * 2 + N * PT * 2);
+  auto load_item = [&](int k) {      // thread 0: x and S of item k
+    const int h = h_lo + k / subs, c = k % subs * PT;
+    const size_t at = ((size_t)b * nb + blk) * p.H + h;
+    mbar_expect_tx(bar_xs, xs_bytes);
+    bulk_load(sb + L::kX, t.xt + at * kQ * p.P * 2 + (size_t)c * kQ * 2, kQ * PT * 2, bar_xs);
+    bulk_load(sb + L::kS, t.st + at * N * p.P * 2 + (size_t)c * N * 2, N * PT * 2, bar_xs);
+  };
+  if (tid == 0) {
+    const size_t o = (((size_t)b * nb + blk) * p.G + g) * tile;
+    mbar_expect_tx(bar_cb, 2 * tile);
+    bulk_load(sb + L::kC, t.ct + o, tile, bar_cb);
+    bulk_load(sb + L::kF, t.bhi + o, tile, bar_cb);
+    load_item(0);
+  }
+  const int flags = t.flags[(size_t)b * nb + blk];
+  const int run = t.run[((size_t)b * nb + blk) * kQ + r];
+  int *srun = reinterpret_cast<int *>(smem + L::kV + 3 * kQ * 4);
+  if (half == 0) srun[r] = run;
+  const Opnd opC = {sb + L::kC, 128, (uint32_t)N * 16};
+  if (!mbar_wait(bar_cb, 0)) give_up();
+  if (tid == 0 && !bad) {
+    const Opnd opB = {sb + L::kF, 128, (uint32_t)N * 16};
+    mma_k(t_cb, opC, 0, opB, 0, N / 16, 128, false);
+    mma_commit(bar_m);
+  }
+  wait_mma();
+  __syncthreads();
+  // entries above the diagonal's 32-row steps are never written again
+  for (int i = tid; i < kQ * kQ * 2 / 16; i += 256)
+    *reinterpret_cast<uint4 *>(smem + L::kF + i * 16) = make_uint4(0, 0, 0, 0);
+
+  float *sein = reinterpret_cast<float *>(smem + L::kV);
+  float *scum = sein + kQ, *scumj = scum + kQ;
+  int k = 0;
+  for (; k < n_items; ++k) {
+    const int h = h_lo + k / subs, c = k % subs * PT;
+    if (__syncthreads_or(bad)) break;      // the last item's arrays are read
+    const size_t at = (((size_t)b * p.H + h) * nb + blk) * kQ;
+    if (tid < kQ) {
+      sein[tid] = t.ein[at + tid];
+      scum[tid] = t.cum[at + tid];
+    } else {
+      scumj[tid - kQ] = t.cumj[at + tid - kQ];
+    }
+    if (!mbar_wait(bar_xs, k & 1)) give_up();
+    if (__syncthreads_or(bad)) break;
+    if (tid == 0) {
+      const Opnd opS = {sb + L::kS, 128, (uint32_t)N * 16};
+      mma_k(t_yi, opC, 0, opS, 1, N / 16, PT, false);
+      mma_commit(bar_m);
+    }
+    if (c == 0) {
+      // factors of the head: rows r, 16 columns at a time, up to the diagonal
+      const float cr = scum[r];
+#pragma unroll 1
+      for (int q = half; q < 2 * quad + 2; q += 2) {
+        float v[16];
+        tmem_ld16(t_cb + lanes + 16 * q, v);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 cj = *reinterpret_cast<const float4 *>(scumj + 16 * q + e);
+          const float w[4] = {cj.x, cj.y, cj.z, cj.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 16 * q + e + i;
+            bool on = j <= r;
+            if (flags & kResets) on = on && srun[j] == run;
+            const float f = ex2(cr - w[i]);
+            v[e + i] = on ? v[e + i] * f : 0.f;
+          }
+        }
+        unsigned char *f = smem + L::kF + (r & 7) * 16 + (r >> 3) * 2048 + 2 * q * 128;
+        float a[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = v[e];
+        *reinterpret_cast<uint4 *>(f) = pack8(a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = v[8 + e];
+        *reinterpret_cast<uint4 *>(f + 128) = pack8(a);
+      }
+      fence_proxy_async();
+    }
+    wait_mma();                    // C S is done: its tile makes room for z
+    tc_fence_before();
+    if (__syncthreads_or(bad)) break;
+    if (tid == 0) {
+      const Opnd opF = {sb + L::kF, 128, kQ * 16}, opX = {sb + L::kX, 128, kQ * 16};
+      mma_k(t_yx, opF, 0, opX, 1, kQ / 16, PT, false);
+      mma_commit(bar_m);
+    }
+    const int ch = h * p.P + c;
+    auto piece = [&](int row, int q) {   // 16-byte piece of the [128][PT] tile of z and y
+      return (uint32_t)(L::kS + row * PT * 2 + ((q ^ (PT == 64 ? row & 7 : row >> 1 & 3)) << 4));
+    };
+    if (p.z) {
+      const bf16 *z = static_cast<const bf16 *>(p.z) + (size_t)b * p.z_sb + ch;
+      for (int i = tid; i < kQ * PT / 8; i += 256) {
+        const int row = i / (PT / 8), q = i % (PT / 8);
+        const bool ok = t0 + row < p.T;
+        cp_async16(sb + piece(row, q), z + (ok ? (long long)(t0 + row) * p.z_st : 0) + q * 8, ok);
+      }
+      cp_async_commit();
+    }
+    wait_mma();
+    cp_async_wait_all();
+    __syncthreads();
+    // y of row r, columns [half PT / 2, (half + 1) PT / 2)
+    const float ein = sein[r], D = p.D ? p.D[h] : 0.f;
+#pragma unroll
+    for (int e0 = 0; e0 < PT / 2; e0 += 16) {
+      const int col = half * (PT / 2) + e0;
+      float yi[16], yx[16];
+      tmem_ld16x2(t_yi + lanes + col, t_yx + lanes + col, yi, yx);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float x[8], z[8], v[8];
+        ld_bf16x8(smem + L::kX + (col / 8 + q) * 2048 + (r >> 3) * 128 + (r & 7) * 16, x);
+        unsigned char *zp = smem + piece(r, col / 8 + q);
+        if (p.z) ld_bf16x8(zp, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float y = fmaf(ein, yi[8 * q + e], yx[8 * q + e]) + D * x[e];
+          if (p.z) y *= z[e] * __fdividef(1.f, 1.f + ex2(-kLog2e * z[e]));
+          v[e] = run < 0 ? 0.f : y;
+        }
+        *reinterpret_cast<uint4 *>(zp) = pack8(v);
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    bf16 *y = static_cast<bf16 *>(p.y) + ((size_t)b * p.T + t0) * p.H * p.P + ch;
+    for (int i = tid; i < kQ * PT / 8; i += 256) {
+      const int row = i / (PT / 8), q = i % (PT / 8);
+      if (t0 + row < p.T)
+        *reinterpret_cast<uint4 *>(y + (size_t)row * p.H * p.P + q * 8) =
+            *reinterpret_cast<const uint4 *>(smem + piece(row, q));
+    }
+    fence_proxy_async();
+    __syncthreads();
+    if (tid == 0 && k + 1 < n_items) load_item(k + 1);
+  }
+  // After a wait that ran out: nothing is in flight when the CTA leaves.
+  if (k < n_items) {
+    mbar_wait(bar_cb, 0);
+    mbar_wait(bar_xs, k & 1);
+    mbar_wait(bar_m, (n_m - 1) & 1);
+    cp_async_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 128 + 2 * PT > 256 ? 512 : 256);
+}
+
+template <int TP>
+cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+  size_t smem = Conv<TP>::kBytes + kQ;
+  const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
+  if (f > smem) smem = f;
+  const unsigned grid = (unsigned)(p.B * t.nb * (1 + p.G * (2 * p.N / TP)));
+  ssm_prep_kernel<TP><<<grid, kConv, smem, cs>>>(p, t);
+  return cudaGetLastError();
+}
+
+template <int TP>
+cudaError_t launch_state(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(ssm_state_kernel<TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)StateSmem<TP>::kBytes);
+  if (e != cudaSuccess) return e;
+  ssm_state_kernel<TP><<<(unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, StateSmem<TP>::kBytes,
+                         cs>>>(p, t);
+  return cudaGetLastError();
+}
+
+template <int PT>
+cudaError_t launch_out(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(ssm_out_kernel<PT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)OutSmem<PT>::kBytes);
+  if (e != cudaSuccess) return e;
+  // heads per CTA: up to 4, as long as the CTAs fill the GPU twice over
+  const int hg = p.H / p.G;
+  int heads = 4;
+  auto ctas = [&](int n) { return (long long)p.B * t.nb * p.G * ((hg + n - 1) / n); };
+  while (heads > 1 && ctas(heads) < 4ll * num_sms()) heads /= 2;
+  ssm_out_kernel<PT><<<(unsigned)ctas(heads), 256, OutSmem<PT>::kBytes, cs>>>(p, t, heads);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t ssm_tc_bytes(const SsmParams &p) {
+  TcBufs t;
+  return layout_bufs(p, nullptr, &t);
+}
+
+cudaError_t launch_ssm_tc(const SsmParams &p, uint32_t *status, cudaStream_t cs) {
+  TcBufs t;
+  layout_bufs(p, p.ws, &t);
+  t.status = status;
+  cudaError_t e = p.N == 32 ? launch_prep<32>(p, t, cs) : launch_prep<64>(p, t, cs);
+  if (e != cudaSuccess) return e;
+  // 64-column tiles halve the traffic of B's tiles; 32 where they would
+  // leave SMs without a CTA
+  const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
+  e = narrow ? launch_state<32>(p, t, cs) : launch_state<64>(p, t, cs);
+  if (e != cudaSuccess) return e;
+  return p.P == 32 ? launch_out<32>(p, t, cs) : launch_out<64>(p, t, cs);
+}
+
+}  // namespace kda

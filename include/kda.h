@@ -531,9 +531,13 @@ typedef struct kda_ssm_shape {
  * conv_out (NULL: not wanted) after the row's last token that is not
  * padding, for kda_ssm_step to go on from; a row without one passes its
  * states on.  conv_out must not be conv_state's buffer.
- *   impl          KDA_IMPL_AUTO, KDA_IMPL_SIMT (fp32 CUDA cores, every shape).
+ *   impl          KDA_IMPL_SIMT: fp32 CUDA cores, every shape; KDA_IMPL_TC: the
+ *                 tensor cores, bf16; KDA_IMPL_AUTO: TC for bf16, else SIMT.
  *   workspace     device, kda_ssm_fwd_workspace_size bytes, 256-byte aligned,
- *                 zero-filled before its first use.
+ *                 its first 256 bytes zero-filled before its first use (the
+ *                 device status word, see kda_read_device_status).
+ * TC computes a row in blocks of 128 tokens: a value that is not finite
+ * spreads to other runs that share a block with it (never from padding).
  * xbc, z and the states are 16-byte aligned and the strides of xbc and z
  * multiples of 16 bytes (KDA_ERR_ALIGNMENT).  Asynchronous on `stream`.
  */
