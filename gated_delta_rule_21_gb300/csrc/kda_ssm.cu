@@ -22,51 +22,36 @@ __device__ __forceinline__ int block_min(int v, int *red) {
   return v;
 }
 
-// One CTA per row: its first run, its last token, and the inputs that the
-// convolution's cache holds after it.
-template <typename T>
-__global__ void __launch_bounds__(512) ssm_rows_kernel(const SsmParams p) {
-  __shared__ int red[16];
+// One CTA per row: its first run and its last token.
+__global__ void __launch_bounds__(1024) ssm_rows_kernel(const SsmParams p) {
+  __shared__ int red[32];
   const int b = blockIdx.x;
-  const int32_t *ids = p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr;
+  const int32_t *ids = p.segment_ids + (size_t)b * p.T;
   SsmRow row = {0, p.T, p.T - 1, 0};
-  if (ids) {
-    int f = p.T, l = p.T;   // l: T - 1 - last
-    for (int t = threadIdx.x; t < p.T; t += blockDim.x)
-      if (ids[t] != 0) {
-        f = min(f, t);
-        l = min(l, p.T - 1 - t);
-      }
-    row.first = block_min(f, red);
-    row.last = p.T - 1 - block_min(l, red);
-    int e = p.T;
-    if (row.first < p.T) {
-      const int id = ids[row.first];
-      for (int t = threadIdx.x; t < p.T; t += blockDim.x)
-        if (t > row.first && ids[t] != id) {
-          e = t;
-          break;
-        }
+  int f = p.T, l = p.T;   // l: T - 1 - last
+#pragma unroll 8
+  for (int t = threadIdx.x; t < p.T; t += 1024)
+    if (ids[t] != 0) {
+      f = min(f, t);
+      l = min(l, p.T - 1 - t);
     }
-    row.first_end = block_min(e, red);
+  row.first = block_min(f, red);
+  row.last = p.T - 1 - block_min(l, red);
+  int e = p.T;
+  if (row.first < p.T) {
+    const int id = ids[row.first];
+#pragma unroll 8
+    for (int t = threadIdx.x; t < p.T; t += 1024)
+      if (t > row.first && ids[t] != id) e = min(e, t);
   }
+  row.first_end = block_min(e, red);
   if (threadIdx.x == 0) p.rows[b] = row;
-  if (!p.conv_out) return;
-  const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb;
-  const T *past = p.conv_state
-                      ? static_cast<const T *>(p.conv_state) +
-                            (size_t)b * (kSsmTaps - 1) * p.channels
-                      : nullptr;
-  T *out = static_cast<T *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels;
-  SsmToken k = ssm_token(ids, row.last, p.T, row);
-  if (row.last < 0) k.live = false;
-  for (int i = threadIdx.x; i < (kSsmTaps - 1) * p.channels; i += blockDim.x) {
-    const int age = kSsmTaps - 2 - i / p.channels, c = i % p.channels;
-    float v;
-    if (k.live) v = ssm_tap(x, p.xbc_st, past, p.channels, c, row.last, age, k);
-    else v = past ? to_f32(past[i]) : 0.f;    // a row without a token keeps its cache
-    out[i] = from_f32<T>(v);
-  }
+}
+
+__device__ __forceinline__ SsmRow simt_row(const SsmParams &p, int b) {
+  if (p.segment_ids) return p.rows[b];
+  SsmRow r = {0, p.T, p.T - 1, 0};
+  return r;
 }
 
 constexpr int kThreads = 256, kCols = 32, kTok = 32, kWarps = kThreads / 32;
@@ -86,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p) {
   const int tiles = p.P / kCols, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % p.H, b = bh / p.H, c0 = tile * kCols, g = h / (p.H / p.G);
   const int32_t *ids = p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr;
-  const SsmRow row = p.rows[b];
+  const SsmRow row = simt_row(p, b);
   const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb;
   const T *past = p.conv_state
                       ? static_cast<const T *>(p.conv_state) +
@@ -161,6 +146,16 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p) {
       static_cast<T *>(p.y)[(((size_t)b * p.T + t0 + t) * p.H + h) * p.P + c0 + c] =
           from_f32<T>(v);
     }
+  }
+  if (p.conv_out) {      // head h moves its share of the channels
+    const SsmToken k = ssm_token(ids, row.last, p.T, row);
+    T *out = static_cast<T *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels;
+    const int ctas = p.H * tiles, me = h * tiles + tile;
+    for (int c = me * kThreads + tid; c < p.channels; c += ctas * kThreads)
+#pragma unroll
+      for (int i = 0; i < kSsmTaps - 1; ++i)
+        out[(size_t)i * p.channels + c] =
+            ssm_cached(x, p.xbc_st, past, p.channels, c, i, row.last, k);
   }
   if (p.final_state) {
 #pragma unroll
@@ -243,10 +238,12 @@ kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt, 
   p.ws = static_cast<unsigned char *>(workspace) + rows_bytes(s->B);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = s->dtype == KDA_DTYPE_BF16;
-  if (bf16) ssm_rows_kernel<__nv_bfloat16><<<s->B, 512, 0, cs>>>(p);
-  else ssm_rows_kernel<float><<<s->B, 512, 0, cs>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return KDA_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (segment_ids) {
+    ssm_rows_kernel<<<s->B, 1024, 0, cs>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return KDA_ERR_CUDA;
+  }
   if (bf16 && impl != KDA_IMPL_SIMT)
     e = launch_ssm_tc(p, &reinterpret_cast<WsHeader *>(workspace)->status, cs);
   else

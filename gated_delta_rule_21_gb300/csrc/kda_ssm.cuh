@@ -67,6 +67,16 @@ __device__ __forceinline__ float ssm_tap(const T *x, long long st, const T *past
   return 0.f;
 }
 
+// Entry i (oldest first) of the convolution's cache after a row that ends with
+// token `last`, k its place; a row without a token keeps the cache it had.
+template <typename T>
+__device__ __forceinline__ T ssm_cached(const T *x, long long st, const T *past, int channels,
+                                        int c, int i, int last, const SsmToken &k) {
+  float v = past ? to_f32(past[(size_t)i * channels + c]) : 0.f;
+  if (k.live) v = ssm_tap(x, st, past, channels, c, last, kSsmTaps - 2 - i, k);
+  return from_f32<T>(v);
+}
+
 __device__ __forceinline__ float ssm_softplus(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }

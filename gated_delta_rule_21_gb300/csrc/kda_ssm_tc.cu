@@ -140,60 +140,58 @@ struct Conv {
     cp_async_commit();
   }
 
-  // f(j, u): token j of the block, u = SiLU(conv) of the warp's 8 channels.
-  // tok (null: a plain block): the tokens' windows; past: the cached inputs
-  // of the row at the tile's channel, or null.
+  // f(j, ok, u): u = SiLU(conv) of the warp's 8 channels at token j of the
+  // block.  Lanes past their warp's tokens repeat the last one with ok false:
+  // without branches around them the tokens of a strip overlap.
   template <typename F>
-  __device__ __forceinline__ void run(const unsigned char *rows, int tid, const unsigned char *tok,
-                                      const bf16 *past, int channels, F f) const {
+  __device__ __forceinline__ void run(const unsigned char *rows, int tid, F f) const {
     const int warp = tid >> 5, lane = tid & 31, piece = warp % kPieces;
-    const int begin = warp / kPieces * kSpan + lane * kStrip;
-    const int end = min(begin + kStrip, (warp / kPieces + 1) * kSpan);
-    float win[kSsmTaps - 1][8];
+    const int part = warp / kPieces, begin = part * kSpan + lane * kStrip;
+    const int end = (part + 1) * kSpan;
+    float x[kStrip + kSsmTaps - 1][8];
 #pragma unroll
-    for (int i = 0; i < kSsmTaps - 1; ++i) {
-      const int r = min(begin + i, kRows - 1);
-      ld_bf16x8(rows + off(r, piece), win[i]);
-    }
+    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i)
+      ld_bf16x8(rows + off(min(begin + i, kRows - 1), piece), x[i]);
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
-      const int j = begin + i;
-      if (j < end) {
-        float x[8], u[8];
-        ld_bf16x8(rows + off(j + kSsmTaps - 1, piece), x);
-        if (!tok) {
-          taps(win[0], win[1], win[2], x, u);
+      float u[8];
+      taps(x[i], x[i + 1], x[i + 2], x[i + 3], u);
+      f(min(begin + i, end - 1), begin + i < end, u);
+    }
+  }
+
+  // The same where windows are cut by runs: tok holds the tokens' windows,
+  // past the cached inputs of the row at the tile's channel (or null).
+  template <typename F>
+  __device__ __forceinline__ void run_cut(const unsigned char *rows, int tid,
+                                          const unsigned char *tok, const bf16 *past,
+                                          int channels, F f) const {
+    const int warp = tid >> 5, lane = tid & 31, piece = warp % kPieces;
+    const int part = warp / kPieces, begin = part * kSpan + lane * kStrip;
+    const int end = min(begin + kStrip, (part + 1) * kSpan);
+#pragma unroll 1
+    for (int j = begin; j < end; ++j) {
+      float a[kSsmTaps][8], u[8];
+      const int k = tok[j], place = k & 3;
+#pragma unroll
+      for (int age = 0; age < kSsmTaps; ++age) {
+        float(&w)[8] = a[kSsmTaps - 1 - age];
+        if (age <= place) {
+          ld_bf16x8(rows + off(j + kSsmTaps - 1 - age, piece), w);
+        } else if ((k & 4) && past) {
+          ld_bf16x8(reinterpret_cast<const unsigned char *>(
+                        past + (size_t)(kSsmTaps - 1 + place - age) * channels + piece * 8),
+                    w);
         } else {
-          const int k = tok[j], place = k & 3;
-          float a[kSsmTaps - 1][8];
 #pragma unroll
-          for (int age = 1; age < kSsmTaps; ++age) {
-            float(&w)[8] = a[kSsmTaps - 1 - age];
-            if (age <= place) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) w[c] = win[kSsmTaps - 1 - age][c];
-            } else if ((k & 4) && past) {
-              ld_bf16x8(reinterpret_cast<const unsigned char *>(
-                            past + (size_t)(kSsmTaps - 1 + place - age) * channels + piece * 8),
-                        w);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) w[c] = 0.f;
-            }
-          }
-          taps(a[0], a[1], a[2], x, u);
-          if (!(k & 8))
-#pragma unroll
-            for (int c = 0; c < 8; ++c) u[c] = 0.f;
-        }
-        f(j, u);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          win[0][c] = win[1][c];
-          win[1][c] = win[2][c];
-          win[2][c] = x[c];
+          for (int c = 0; c < 8; ++c) w[c] = 0.f;
         }
       }
+      taps(a[0], a[1], a[2], a[3], u);
+      if (!(k & 8))
+#pragma unroll
+        for (int c = 0; c < 8; ++c) u[c] = 0.f;
+      f(j, true, u);
     }
   }
 
@@ -383,21 +381,34 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   plain = __syncthreads_and(plain);
   const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2;
   const uint32_t at = (uint32_t)((n0 / 8 + piece) * 128);
-  cv.run(smem, tid, plain ? nullptr : stok, past ? past + ch : nullptr, p.channels,
-         [&](int j, float(&u)[8]) {
-           const size_t o = tile + at + (j & 7) * 16 + (size_t)(j >> 3) * p.N * 16;
-           if (is_c) {
-             *reinterpret_cast<uint4 *>(t.ct + o) = pack8(u);
-           } else {
-             uint4 hi, lo;
-             split8(u, hi, lo);
-             *reinterpret_cast<uint4 *>(t.bhi + o) = hi;
-             *reinterpret_cast<uint4 *>(t.blo + o) = lo;
-           }
-         });
+  unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile + at, *lo_tile = t.blo + tile + at;
+  auto put = [&](int j, bool ok, float(&u)[8]) {
+    const size_t o = (size_t)((j & 7) * 16) + (size_t)(j >> 3) * p.N * 16;
+    uint4 hi, lo;
+    split8(u, hi, lo);
+    if (ok) *reinterpret_cast<uint4 *>(hi_tile + o) = hi;
+    if (ok && !is_c) *reinterpret_cast<uint4 *>(lo_tile + o) = lo;
+  };
+  if (plain) cv.run(smem, tid, put);
+  else cv.run_cut(smem, tid, stok, past ? past + ch : nullptr, p.channels, put);
 }
 
-// CTAs [0, B nb) make the factors, the others one tile of B or C each.
+// The inputs that the convolution's cache holds after the row.
+__device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) {
+  const SsmRow row = row_of(p, b);
+  const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb, *past = past_of(p, b);
+  SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr, row.last, p.T,
+                         row);
+  const int c = part * kConv + threadIdx.x;
+  if (c >= p.channels) return;
+  bf16 *out = static_cast<bf16 *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels + c;
+#pragma unroll
+  for (int i = 0; i < kSsmTaps - 1; ++i)
+    out[(size_t)i * p.channels] = ssm_cached(x, p.xbc_st, past, p.channels, c, i, row.last, k);
+}
+
+// CTAs [0, B nb) make the factors, the next ones a tile of B or C each, the
+// last ones the convolution's cache.
 template <int TP>
 __global__ void __launch_bounds__(kConv) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -412,7 +423,14 @@ __global__ void __launch_bounds__(kConv) ssm_prep_kernel(const SsmParams p, cons
   u /= parts;
   const int g = u % p.G;
   u /= p.G;
-  prep_conv<TP>(p, t, u / t.nb, u % t.nb, g, part, smem);
+  if (u < p.B * t.nb) {
+    prep_conv<TP>(p, t, u / t.nb, u % t.nb, g, part, smem);
+    return;
+  }
+  // (the ids of these CTAs run on in the same order)
+  u = blockIdx.x - p.B * t.nb * (1 + p.G * parts);
+  const int caches = (p.channels + kConv - 1) / kConv;
+  prep_cache(p, u / caches, u % caches);
 }
 
 // ---------------------------------------------------------------------------
@@ -554,7 +572,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     };
     bool bad = false;
     // the state after block i, once its products are done
-    auto finish = [&](int i) {
+    auto finish = [&](int i, float a) {
       if (n < N) {
         unsigned char *st = t.st + ((((size_t)b * nb + i) * p.H + h) * N) * p.P * 2 +
                             (size_t)((c0 + col0) / 8) * N * 16 + (n >> 3) * 128 + (n & 7) * 16;
@@ -566,7 +584,6 @@ __global__ void __launch_bounds__(kConv + 32, 1)
           *reinterpret_cast<uint4 *>(st + (size_t)(k / 8) * N * 16) = pack8(v);
         }
       }
-      const float a = dec[i];
       if (!mbar_wait(bar_d + 8u * (i & 1), (i >> 1) & 1)) {
         bad = true;
         set_status(t.status, KDA_DEVICE_TIMEOUT);
@@ -585,37 +602,48 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       tc_fence_before();
     };
     stage(0);
+    // the next block's flags and this and the last block's decay, loaded early
+    int flags = t.flags[(size_t)b * nb], flags_next;
+    float a_prev = 0.f, a_now = dec[0];
     int i = 0;
-    for (; i < nb; ++i) {
+    for (; i < nb; ++i, flags = flags_next) {
       cp_async_wait_all();
       if (any_of_conv(bad)) break;   // a wait ran out somewhere: all leave
       stage(i + 1);
+      flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
+      const float a_next = i + 1 < nb ? dec[i + 1] : 0.f;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
       unsigned char *xo = smem + L::kX + (i & 1) * L::kXBytes + piece * 2048;
       unsigned char *xt = t.xt + (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
                           (size_t)(c0 / 8 + piece) * 2048;
-      const bool plain = (t.flags[(size_t)b * nb + i] & kPlain) != 0;
-      cv.run(smem + L::kRows + (i & 1) * Conv<TP>::kBytes, tid,
-             plain ? nullptr : t.tok + ((size_t)b * nb + i) * kQ, past ? past + ch : nullptr,
-             p.channels, [&](int j, float(&u)[8]) {
-               const int o = (j >> 3) * 128 + (j & 7) * 16;
-               *reinterpret_cast<uint4 *>(xt + o) = pack8(u);
-               const float f = w[j];
-               // a token that does not reach the state adds nothing, whatever it holds
+      auto put = [&](int j, bool ok, float(&u)[8]) {
+        const int o = (j >> 3) * 128 + (j & 7) * 16;
+        const uint4 v = pack8(u);
+        const float f = w[j];
+        // a token that does not reach the state adds nothing, whatever it holds
 #pragma unroll
-               for (int e = 0; e < 8; ++e) u[e] = f != 0.f ? u[e] * f : 0.f;
-               uint4 hi, lo;
-               split8(u, hi, lo);
-               *reinterpret_cast<uint4 *>(xo + o) = hi;
-               *reinterpret_cast<uint4 *>(xo + TP / 8 * 2048 + o) = lo;
-             });
+        for (int e = 0; e < 8; ++e) u[e] = f != 0.f ? u[e] * f : 0.f;
+        uint4 hi, lo;
+        split8(u, hi, lo);
+        if (ok) {
+          *reinterpret_cast<uint4 *>(xt + o) = v;
+          *reinterpret_cast<uint4 *>(xo + o) = hi;
+          *reinterpret_cast<uint4 *>(xo + TP / 8 * 2048 + o) = lo;
+        }
+      };
+      const unsigned char *rows = smem + L::kRows + (i & 1) * Conv<TP>::kBytes;
+      if (flags & kPlain) cv.run(rows, tid, put);
+      else cv.run_cut(rows, tid, t.tok + ((size_t)b * nb + i) * kQ, past ? past + ch : nullptr,
+                      p.channels, put);
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
-      if (i > 0) finish(i - 1);
+      if (i > 0) finish(i - 1, a_prev);
+      a_prev = a_now;
+      a_now = a_next;
     }
     cp_async_wait_all();
-    if (i == nb) finish(nb - 1);
+    if (i == nb) finish(nb - 1, a_prev);
     if (p.final_state && n < N) {
 #pragma unroll
       for (int k = 0; k < kCols; k += 4)
@@ -853,7 +881,8 @@ cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
   size_t smem = Conv<TP>::kBytes + kQ;
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
-  const unsigned grid = (unsigned)(p.B * t.nb * (1 + p.G * (2 * p.N / TP)));
+  const int caches = p.conv_out ? (p.channels + kConv - 1) / kConv : 0;
+  const unsigned grid = (unsigned)(p.B * (t.nb * (1 + p.G * (2 * p.N / TP)) + caches));
   ssm_prep_kernel<TP><<<grid, kConv, smem, cs>>>(p, t);
   return cudaGetLastError();
 }
