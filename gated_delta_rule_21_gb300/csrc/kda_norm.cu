@@ -23,7 +23,10 @@
 // two up to a warp, else whole warps), each owning VEC-wide pieces of 16
 // bytes tpr apart; a CTA holds rg = 256 / tpr rows when a row needs fewer
 // than 256 threads.  Rows whose length or pointers do not allow 16-byte
-// accesses take the same code with VEC = 1.
+// accesses take the same code with VEC = 2 (bf16 rows of even length) or 1.
+#include <type_traits>
+
+#include "kda_f32x2.cuh"
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -31,14 +34,14 @@ namespace {
 
 constexpr int kMaxDim = 16384;
 constexpr int kBlock = 256;        // threads when a row needs at most these
-constexpr int kStages = 2;         // rows staged per thread in the backward
+constexpr int kStages = 3;         // rows staged per thread in the backward
 constexpr size_t kStageMax = 200 * 1024;   // longer rows are read directly
 
 enum { kGateNone = 0, kGateEach = 1, kGateGroup = 2 };
 
 // How a row is laid over threads.
 struct Layout {
-  int vec;      // elements per access (16 bytes, or 1)
+  int vec;      // elements per access: 16 bytes, 2 (bf16, even rows) or 1
   int items;    // accesses per thread and row
   int tpr;      // threads per row
   int rg;       // rows per CTA
@@ -46,11 +49,12 @@ struct Layout {
 
 Layout layout_for(int D, int elt, bool vector_ok) {
   Layout l;
-  l.vec = vector_ok && D % (16 / elt) == 0 ? 16 / elt : 1;
+  l.vec = !vector_ok ? 1 : D % (16 / elt) == 0 ? 16 / elt : elt == 2 && D % 2 == 0 ? 2 : 1;
   const int n = D / l.vec;
-  const int most = l.vec > 1 ? 512 : 1024;     // threads of one row
-  l.items = l.vec > 1 ? 1 : 4;
-  while (l.items * most < n) l.items *= l.vec > 1 ? 2 : 4;
+  const int most = l.vec > 2 ? 512 : 1024;     // threads of one row
+  // the kernels' numbers of accesses: 1, 2, 4, 8; 2, 8; 4, 16
+  l.items = l.vec > 2 ? 1 : l.vec == 2 ? 2 : 4;
+  while (l.items * most < n) l.items *= l.vec > 2 ? 2 : 4;
   int t = (n + l.items - 1) / l.items;
   if (t > 32) {
     t = (t + 31) / 32 * 32;
@@ -64,59 +68,86 @@ Layout layout_for(int D, int elt, bool vector_ok) {
   return l;
 }
 
-// VEC elements as fp32.
+// One or two fp32 values: pairs use the packed f32x2 instructions, which
+// halve the arithmetic a row costs.
+struct P1 { float v; };
+struct P2 { u64 v; };
+__device__ __forceinline__ P1 mul(P1 a, P1 b) { return {a.v * b.v}; }
+__device__ __forceinline__ P1 add(P1 a, P1 b) { return {a.v + b.v}; }
+__device__ __forceinline__ P1 fma(P1 a, P1 b, P1 c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ float total(P1 a) { return a.v; }
+__device__ __forceinline__ P2 mul(P2 a, P2 b) { return {mul2(a.v, b.v)}; }
+__device__ __forceinline__ P2 add(P2 a, P2 b) { return {add2(a.v, b.v)}; }
+__device__ __forceinline__ P2 fma(P2 a, P2 b, P2 c) { return {fma2(a.v, b.v, c.v)}; }
+__device__ __forceinline__ float total(P2 a) {
+  float x, y;
+  upk2(a.v, x, y);
+  return x + y;
+}
+template <typename P> __device__ __forceinline__ P both(float a);
+template <> __device__ __forceinline__ P1 both<P1>(float a) { return {a}; }
+template <> __device__ __forceinline__ P2 both<P2>(float a) { return {pk2(a, a)}; }
+
+// VEC elements in memory (Raw) and in registers (E values of type P).
 template <typename T, int VEC>
-struct Piece;
-template <>
-struct Piece<__nv_bfloat16, 8> {
-  using Raw = uint4;
-  static __device__ __forceinline__ void get(const Raw &a, float (&f)[8]) {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Piece {
+  static_assert(VEC * sizeof(T) == 16 || (VEC == 2 && sizeof(T) == 2), "accesses");
+  using Raw = typename std::conditional<VEC * sizeof(T) == 16, uint4, uint32_t>::type;
+  using P = P2;
+  static constexpr int E = VEC / 2;
+  static __device__ __forceinline__ void get(const Raw &a, P2 (&f)[E]) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&a);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < E; ++i)
+      f[i].v = sizeof(T) == 4
+                   ? pk2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]))
+                   : pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ Raw put(const P2 (&f)[E]) {
+    Raw a;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&a);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      float x, y;
+      upk2(f[i].v, x, y);
+      if (sizeof(T) == 4) {
+        w[2 * i] = __float_as_uint(x);
+        w[2 * i + 1] = __float_as_uint(y);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+    return a;
+  }
+  static __device__ __forceinline__ void weight(const float *w, P2 (&f)[E]) {
+    if constexpr (VEC == 2) {
+      const float2 a = *reinterpret_cast<const float2 *>(w);
+      f[0].v = pk2(a.x, a.y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const float4 a = *reinterpret_cast<const float4 *>(w + 2 * i);
+        f[i].v = pk2(a.x, a.y);
+        f[i + 1].v = pk2(a.z, a.w);
+      }
     }
   }
-  static __device__ __forceinline__ Raw put(const float (&f)[8]) {
-    uint32_t w[4];
+  static __device__ __forceinline__ void store(float *w, const P2 (&f)[E]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Piece<float, 4> {
-  using Raw = float4;
-  static __device__ __forceinline__ void get(const Raw &a, float (&f)[4]) {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  }
-  static __device__ __forceinline__ Raw put(const float (&f)[4]) {
-    return make_float4(f[0], f[1], f[2], f[3]);
+    for (int i = 0; i < E; ++i) upk2(f[i].v, w[2 * i], w[2 * i + 1]);
   }
 };
 template <typename T>
 struct Piece<T, 1> {
   using Raw = T;
-  static __device__ __forceinline__ void get(const Raw &a, float (&f)[1]) { f[0] = to_f32(a); }
-  static __device__ __forceinline__ Raw put(const float (&f)[1]) { return from_f32<T>(f[0]); }
+  using P = P1;
+  static constexpr int E = 1;
+  static __device__ __forceinline__ void get(const Raw &a, P1 (&f)[1]) { f[0].v = to_f32(a); }
+  static __device__ __forceinline__ Raw put(const P1 (&f)[1]) { return from_f32<T>(f[0].v); }
+  static __device__ __forceinline__ void weight(const float *w, P1 (&f)[1]) { f[0].v = *w; }
+  static __device__ __forceinline__ void store(float *w, const P1 (&f)[1]) { *w = f[0].v; }
 };
-
-template <int VEC>
-__device__ __forceinline__ void load_w(const float *w, float (&f)[VEC]) {
-  if constexpr (VEC == 1) {
-    f[0] = *w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(w + i);
-      f[i] = a.x; f[i + 1] = a.y; f[i + 2] = a.z; f[i + 3] = a.w;
-    }
-  }
-}
 
 // act(a), and its derivative when DER.  The sigmoid takes the approximate
 // exp2 and reciprocal (a few fp32 ulp); tanh needs tanhf, whose relative
@@ -141,6 +172,19 @@ __device__ __forceinline__ void gate_value(float a, int act, float &v, float &d)
     v = a * s;
     if (DER) d = s * (1.f + a * (1.f - s));
   }
+}
+template <bool DER>
+__device__ __forceinline__ void gate_value(P1 a, int act, P1 &v, P1 &d) {
+  gate_value<DER>(a.v, act, v.v, d.v);
+}
+template <bool DER>
+__device__ __forceinline__ void gate_value(P2 a, int act, P2 &v, P2 &d) {
+  float x, y, vx, vy, dx = 0.f, dy = 0.f;
+  upk2(a.v, x, y);
+  gate_value<DER>(x, act, vx, dx);
+  gate_value<DER>(y, act, vy, dy);
+  v.v = pk2(vx, vy);
+  if (DER) d.v = pk2(dx, dy);
 }
 
 // Sums of N values over the tpr threads of a row, in every thread of the
@@ -178,85 +222,143 @@ struct NormParams {
   const float *w_post, *w_pre;
   void *out, *x;
   float *stats;                 // [2][R]: s1, s2
+  int n_in;        // input arrays staged per row
+  int stages;      // kStages, or 0: inputs are read where they are used
 };
 
-// One row per row group at a time, rows gridDim.x * rg apart.  The weights
-// stay in registers; every input element is read once and kept as `out`.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's own pieces of the rows to come, copied to shared memory
+// kStages - 1 rows ahead.  With stages = 0 (rows too long, or accesses of
+// less than 16 bytes) pieces are read where they are used.
 template <typename T, int VEC, int ITEMS>
-__global__ void __launch_bounds__(VEC > 1 ? 512 : 1024) norm_fwd_kernel(const NormParams p) {
-  using P = Piece<T, VEC>;
-  using Raw = typename P::Raw;
+struct Stage {
+  using Raw = typename Piece<T, VEC>::Raw;
+  static constexpr bool kAsync = sizeof(Raw) == 16;
+  Raw *base;
+  int n_in, nthr, stages, D, lane, tpr;
+
+  template <typename... A>
+  __device__ __forceinline__ void fetch(int st, bool live, size_t row, const A *...arrays) const {
+    if constexpr (kAsync) {
+      if (stages && live) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int c = (lane + i * tpr) * VEC;
+          if (c < D) {
+            Raw *d = base + (size_t)(st * ITEMS + i) * n_in * nthr;
+            ((arrays ? (cp_async16(d, static_cast<const T *>(arrays) + row + c), d += nthr) : d), ...);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  // piece `i` of input number `k` (which is `array`)
+  __device__ __forceinline__ Raw get(int st, int i, int k, const void *array, size_t row) const {
+    if (kAsync && stages) return base[((size_t)(st * ITEMS + i) * n_in + k) * nthr];
+    return *reinterpret_cast<const Raw *>(static_cast<const T *>(array) + row +
+                                          (lane + i * tpr) * VEC);
+  }
+};
+
+// A CTA walks rows gridDim.x * rg apart, one row per row group at a time.
+template <typename T, int VEC, int ITEMS>
+__global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_fwd_kernel(const NormParams p) {
+  using Pc = Piece<T, VEC>;
+  using P = typename Pc::P;
+  using Raw = typename Pc::Raw;
+  constexpr int E = Pc::E;
+  extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float red[2][1][32];
   const int tid = threadIdx.x, tpr = p.tpr, rg = p.rg;
   const int group = tid / tpr, lane = tid - group * tpr;
-  int slot = 0;
-  for (long long r0 = (long long)blockIdx.x * rg; r0 < p.R; r0 += (long long)gridDim.x * rg) {
+  const Stage<T, VEC, ITEMS> in = {reinterpret_cast<Raw *>(smem) + tid, p.n_in, (int)blockDim.x,
+                                   p.stages, p.D, lane, tpr};
+  const int k_res = 1, k_gate = 1 + (p.res != nullptr);
+  int slot = 0, st = 0;
+  const long long step = (long long)gridDim.x * rg;
+  auto gate_at = [&](long long row) {
+    return p.gate ? (const T *)p.gate + ((ptrdiff_t)((unsigned)row / p.rows_per_gate) - row) * p.D
+                  : (const T *)nullptr;    // as if it had a row for each
+  };
+  auto fetch = [&](long long row, int s) {
+    in.fetch(s, row < p.R, (size_t)row * p.D, (const T *)p.y, (const T *)p.res, gate_at(row));
+  };
+  const long long first = (long long)blockIdx.x * rg;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(first + group + s * step, s);
+  for (long long r0 = first; r0 < p.R; r0 += step) {
     const long long row = r0 + group;
     const bool live = row < p.R;
-    const size_t base = (size_t)row * p.D;
-    const size_t gbase = p.gate && live ? (size_t)((unsigned)row / p.rows_per_gate) * p.D : 0;
-    Raw ry[ITEMS], rr[ITEMS], rgt[ITEMS];
+    const size_t at = (size_t)row * p.D;
+    const T *gate = gate_at(row);
+    fetch(row + (kStages - 1) * step, st == 0 ? kStages - 1 : st - 1);
+    if (in.kAsync) cp_async_wait<kStages - 1>();
+    P v[ITEMS][E], acc = both<P>(0.f);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int c = (lane + i * tpr) * VEC;
-      if (live && c < p.D) {
-        ry[i] = *reinterpret_cast<const Raw *>((const T *)p.y + base + c);
-        if (p.gate) rgt[i] = *reinterpret_cast<const Raw *>((const T *)p.gate + gbase + c);
-        if (p.res) rr[i] = *reinterpret_cast<const Raw *>((const T *)p.res + base + c);
-      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = both<P>(0.f);
+      if (live && (lane + i * tpr) * VEC < p.D) Pc::get(in.get(st, i, 0, p.y, at), v[i]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc = fma(v[i][e], v[i][e], acc);
     }
-    float v[ITEMS][VEC], ss[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const bool ok = live && (lane + i * tpr) * VEC < p.D;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-      if (ok) P::get(ry[i], v[i]);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) ss[0] += v[i][e] * v[i][e];
-    }
+    float ss[1] = {total(acc)};
     row_sum(ss, tpr, red, slot);
-    const float s1 = rsqrtf(ss[0] * p.inv_d + p.eps), k = s1 * p.scale;
-    ss[0] = 0.f;
+    const float s1 = rsqrtf(ss[0] * p.inv_d + p.eps);
+    const P k = both<P>(s1 * p.scale);
+    acc = both<P>(0.f);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = (lane + i * tpr) * VEC;
       if (live && c < p.D) {
-        float w[VEC], a[VEC], d;
-        load_w<VEC>(p.w_post + c, w);
+        P w[E], a[E];
+        Pc::weight(p.w_post + c, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] *= k * w[e];
-        if (p.gate) {
-          P::get(rgt[i], a);
+        for (int e = 0; e < E; ++e) v[i][e] = mul(mul(v[i][e], k), w[e]);
+        if (gate) {
+          Pc::get(in.get(st, i, k_gate, gate, at), a);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
+          for (int e = 0; e < E; ++e) {
+            P d;
             gate_value<false>(a[e], p.act, a[e], d);
-            v[i][e] *= a[e];
+            v[i][e] = mul(v[i][e], a[e]);
           }
         }
         if (p.res) {
-          P::get(rr[i], a);
+          Pc::get(in.get(st, i, k_res, p.res, at), a);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[i][e] += a[e];
+          for (int e = 0; e < E; ++e) v[i][e] = add(v[i][e], a[e]);
         }
-        *reinterpret_cast<Raw *>((T *)p.out + base + c) = P::put(v[i]);
+        *reinterpret_cast<Raw *>((T *)p.out + at + c) = Pc::put(v[i]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss[0] += v[i][e] * v[i][e];
+        for (int e = 0; e < E; ++e) acc = fma(v[i][e], v[i][e], acc);
       }
     }
     float s2 = 0.f;
     if (p.w_pre) {
+      ss[0] = total(acc);
       row_sum(ss, tpr, red, slot);
       s2 = rsqrtf(ss[0] * p.inv_d + p.eps);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         const int c = (lane + i * tpr) * VEC;
         if (live && c < p.D) {
-          float w[VEC];
-          load_w<VEC>(p.w_pre + c, w);
+          P w[E];
+          Pc::weight(p.w_pre + c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[i][e] *= s2 * w[e];
-          *reinterpret_cast<Raw *>((T *)p.x + base + c) = P::put(v[i]);
+          for (int e = 0; e < E; ++e) v[i][e] = mul(mul(v[i][e], both<P>(s2)), w[e]);
+          *reinterpret_cast<Raw *>((T *)p.x + at + c) = Pc::put(v[i]);
         }
       }
     }
@@ -264,7 +366,9 @@ __global__ void __launch_bounds__(VEC > 1 ? 512 : 1024) norm_fwd_kernel(const No
       p.stats[row] = s1;
       p.stats[p.R + row] = s2;
     }
+    st = st + 1 == kStages ? 0 : st + 1;
   }
+  if (in.kAsync) cp_async_wait<0>();
 }
 
 struct NormBwdParams {
@@ -274,60 +378,82 @@ struct NormBwdParams {
   float *part_post, *part_pre, *part_gate;   // [units][D]
   long long gate_rows;
   int splits;      // units per gate row (group gates), 0: whole gate rows per unit
-  int n_in;        // input arrays staged per row
-  int stages;      // kStages, or 0: inputs are read directly
 };
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src)
-               : "memory");
-}
-
-// Sums `acc` over the CTA's row groups and hands the totals of the first
-// group's columns to `put(column, values)`.  Uniform over the CTA.
-template <int VEC, int ITEMS, typename F>
-__device__ __forceinline__ void flush(float (&acc)[ITEMS][VEC], int tpr, int rg, int group,
-                                      int lane, int D, float *buf, F put) {
+// Sums `acc` over the CTA's row groups and hands the totals to the first
+// group's threads: put(column, values).  Uniform over the CTA.
+template <typename Pc, int ITEMS, int VEC, typename F>
+__device__ __forceinline__ void flush(typename Pc::P (&acc)[ITEMS][Pc::E], int tpr, int rg,
+                                      int group, int lane, int D, typename Pc::P *buf, F put) {
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int c = (lane + i * tpr) * VEC;
     if (rg > 1) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) buf[threadIdx.x * VEC + e] = acc[i][e];
+      for (int e = 0; e < Pc::E; ++e) buf[threadIdx.x * Pc::E + e] = acc[i][e];
       __syncthreads();
       if (group == 0)
         for (int g = 1; g < rg; ++g)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) acc[i][e] += buf[(g * tpr + lane) * VEC + e];
+          for (int e = 0; e < Pc::E; ++e)
+            acc[i][e] = add(acc[i][e], buf[(g * tpr + lane) * Pc::E + e]);
     }
-    if (group == 0 && c < D) put(c, acc[i]);
+    if (group == 0 && c < D) put(i, c, acc[i]);
   }
 }
 
-// A unit (CTA) owns a contiguous range of rows, keeps its sums of dw_post,
-// dw_pre and (group gates) d_gate in registers and writes them once; the
-// units' sums are added in a fixed order by norm_sum_kernel, so no result
-// depends on timing.  A thread copies its own pieces of the next row to
-// shared memory (cp.async) while it works on this one.
+// A unit (CTA) owns a contiguous range of rows, keeps its column sums in
+// registers and writes them once; the units' sums are added in a fixed order
+// by norm_sum_kernel, so no result depends on timing.
+//
+// With m = out, v = d_out + s2 d_x w_pre and q = aw n1 (aw = scale act(gate)
+// w_post), a row needs sum(d_x w_pre m), sum(q v) and sum(q m); then
+//   r = v - k m,  dy = s1 (aw r - c1 n1),
+// and the column sums of r n1 give dw_post and (gate rows shared by rows,
+// where act(gate) is a factor of the column) d_gate at once.  One piece per
+// thread keeps these values for the second pass over the row, more pieces
+// make them again from the staged inputs.
 template <typename T, int VEC, int ITEMS, int GATE>
-__global__ void __launch_bounds__(VEC > 1 ? 512 : 1024) norm_bwd_kernel(const NormBwdParams q) {
-  using P = Piece<T, VEC>;
-  using Raw = typename P::Raw;
-  constexpr bool kAsync = VEC > 1;
+__global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_bwd_kernel(const NormBwdParams q) {
+  using Pc = Piece<T, VEC>;
+  using P = typename Pc::P;
+  using Raw = typename Pc::Raw;
+  constexpr int E = Pc::E;
+  constexpr bool kKeep = ITEMS == 1;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float red[2][3][32];
   const NormParams &p = q.f;
   const int tid = threadIdx.x, tpr = p.tpr, rg = p.rg, nthr = blockDim.x;
   const int group = tid / tpr, lane = tid - group * tpr;
-  float *buf = reinterpret_cast<float *>(smem);
-  Raw *stage = reinterpret_cast<Raw *>(smem + (rg > 1 ? sizeof(float) * nthr * VEC : 0));
+  P *buf = reinterpret_cast<P *>(smem);
+  const Stage<T, VEC, ITEMS> in = {
+      reinterpret_cast<Raw *>(smem + (rg > 1 ? sizeof(float) * nthr * VEC : 0)) + tid,
+      p.n_in, nthr, p.stages, p.D, lane, tpr};
+  const int k_out = 1, k_x = k_out + (q.d_out != nullptr), k_res = k_x + (q.d_x != nullptr),
+            k_gate = k_res + (p.res != nullptr);
   int slot = 0;
 
-  float dw1[ITEMS][VEC] = {}, dw2[ITEMS][VEC] = {};
-  constexpr int GI = GATE == kGateGroup ? ITEMS : 1;
+  P dw1[ITEMS][E], dw2[ITEMS][E], w1k[1][E], w2k[1][E];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw1[i][e] = dw2[i][e] = both<P>(0.f);
+  const P scale = both<P>(p.scale);
+  // scale * w_post and w_pre of a piece
+  auto weights = [&](int i, P(&w1)[E], P(&w2)[E]) {
+    const int c = (lane + i * tpr) * VEC;
+#pragma unroll
+    for (int e = 0; e < E; ++e) w1[e] = w2[e] = both<P>(0.f);
+    if (c < p.D) {
+      Pc::weight(p.w_post + c, w1);
+      if (p.w_pre) Pc::weight(p.w_pre + c, w2);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) w1[e] = mul(w1[e], scale);
+  };
+  if (kKeep) weights(0, w1k[0], w2k[0]);
+
   // the gate rows [g_lo, g_hi) of this unit, or its part of one gate row
   long long g_lo = 0, g_hi = 1;
   if (GATE == kGateGroup) {
@@ -350,150 +476,161 @@ __global__ void __launch_bounds__(VEC > 1 ? 512 : 1024) norm_bwd_kernel(const No
       lo = (long long)blockIdx.x * p.R / gridDim.x;
       hi = (long long)(blockIdx.x + 1) * p.R / gridDim.x;
     }
-    float ga[GI][VEC], gd[GI][VEC], dg[GI][VEC];
+    // group gates: act(gate) of the unit's pieces, and the sums of r n1
+    constexpr int GI = GATE == kGateGroup ? ITEMS : 1;
+    P ga[GI][E], es[GI][E];
     if (GATE == kGateGroup) {
 #pragma unroll
       for (int i = 0; i < GI; ++i) {
         const int c = (lane + i * tpr) * VEC;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dg[i][e] = ga[i][e] = gd[i][e] = 0.f;
+        for (int e = 0; e < E; ++e) es[i][e] = ga[i][e] = both<P>(0.f);
         if (c < p.D) {
-          float a[VEC];
-          P::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), a);
+          P a[E], d;
+          Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), a);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) gate_value<true>(a[e], p.act, ga[i][e], gd[i][e]);
+          for (int e = 0; e < E; ++e) gate_value<false>(a[e], p.act, ga[i][e], d);
         }
       }
     }
-    auto fetch = [&](long long row, int st) {
-      if constexpr (kAsync) {
-        if (q.stages && row < hi) {
-          const size_t base = (size_t)row * p.D;
-#pragma unroll
-          for (int i = 0; i < ITEMS; ++i) {
-            const int c = (lane + i * tpr) * VEC;
-            if (c < p.D) {
-              Raw *d = stage + (size_t)(st * ITEMS + i) * q.n_in * nthr + tid;
-              cp_async16(d, (const T *)p.y + base + c); d += nthr;
-              if (q.d_out) { cp_async16(d, (const T *)q.d_out + base + c); d += nthr; }
-              if (q.d_x) { cp_async16(d, (const T *)q.d_x + base + c); d += nthr; }
-              if (p.res) { cp_async16(d, (const T *)p.res + base + c); d += nthr; }
-              if (GATE == kGateEach) cp_async16(d, (const T *)p.gate + base + c);
-            }
-          }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
+    auto fetch = [&](long long row, int s) {
+      in.fetch(s, row < hi, (size_t)row * p.D, (const T *)p.y, (const T *)q.d_out,
+               (const T *)q.d_x, (const T *)p.res,
+               GATE == kGateEach ? (const T *)p.gate : (const T *)nullptr);
     };
     int st = 0;
-    fetch(lo + group, 0);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(lo + group + s * rg, s);
     for (long long r0 = lo; r0 < hi; r0 += rg) {
       const long long row = r0 + group;
       const bool live = row < hi;
-      fetch(row + rg, st ^ 1);
+      const size_t at = (size_t)row * p.D;
       float s1 = 0.f, s2 = 0.f;
       if (live) {
         s1 = p.stats[row];
         s2 = p.stats[p.R + row];
       }
-      if constexpr (kAsync) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      const size_t base = (size_t)row * p.D;
-      // n1, n2, the incoming gradients, act(gate) and its derivative
-      float n1[ITEMS][VEC], n2[ITEMS][VEC], go[ITEMS][VEC], gx[ITEMS][VEC], a[ITEMS][VEC],
-          da[ITEMS][VEC], sum[3] = {0.f, 0.f, 0.f};
+      fetch(row + (kStages - 1) * rg, st == 0 ? kStages - 1 : st - 1);
+      if (in.kAsync) cp_async_wait<kStages - 1>();
+      // n1, m, v, d_x, act(gate) and its derivative of a piece
+      auto front = [&](int i, const P(&w1)[E], const P(&w2)[E], P(&n1)[E], P(&m)[E], P(&v)[E],
+                       P(&gx)[E], P(&a)[E], P(&da)[E], P(&qv)[E]) {
+        Pc::get(in.get(st, i, 0, p.y, at), n1);
+        if (q.d_out) Pc::get(in.get(st, i, k_out, q.d_out, at), v);
+        else
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = both<P>(0.f);
+        if (q.d_x) Pc::get(in.get(st, i, k_x, q.d_x, at), gx);
+        else
+#pragma unroll
+          for (int e = 0; e < E; ++e) gx[e] = both<P>(0.f);
+        if (p.res) Pc::get(in.get(st, i, k_res, p.res, at), m);
+        else
+#pragma unroll
+          for (int e = 0; e < E; ++e) m[e] = both<P>(0.f);
+        if (GATE == kGateEach) {
+          Pc::get(in.get(st, i, k_gate, p.gate, at), a);
+#pragma unroll
+          for (int e = 0; e < E; ++e) gate_value<true>(a[e], p.act, a[e], da[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          n1[e] = mul(n1[e], both<P>(s1));
+          qv[e] = mul(w1[e], n1[e]);
+          if (GATE == kGateEach) qv[e] = mul(qv[e], a[e]);
+          if (GATE == kGateGroup) qv[e] = mul(qv[e], ga[i < GI ? i : 0][e]);
+          m[e] = add(m[e], qv[e]);
+          v[e] = fma(mul(gx[e], w2[e]), both<P>(s2), v[e]);
+        }
+      };
+      P n1[1][E], m[1][E], v[1][E], gx[1][E], a[1][E], da[1][E];
+      P acc0 = both<P>(0.f), acc1 = acc0, acc2 = acc0;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
-        const int c = (lane + i * tpr) * VEC;
-        const bool ok = live && c < p.D;
+        if (live && (lane + i * tpr) * VEC < p.D) {
+          P w1[E], w2[E], qv[E];
+          if (!kKeep) weights(i, w1, w2);
+          front(i, kKeep ? w1k[0] : w1, kKeep ? w2k[0] : w2, n1[0], m[0], v[0], gx[0], a[0], da[0],
+                qv);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          n1[i][e] = n2[i][e] = go[i][e] = gx[i][e] = a[i][e] = da[i][e] = 0.f;
-        if (ok) {
-          float w1[VEC], w2[VEC], t[VEC];
-          const Raw *sp = stage + (size_t)(st * ITEMS + i) * q.n_in * nthr + tid;
-          auto next = [&](const void *src) {
-            if (kAsync && q.stages) {
-              const Raw v = *sp;
-              sp += nthr;
-              return v;
-            }
-            return *reinterpret_cast<const Raw *>((const T *)src + base + c);
-          };
-          P::get(next(p.y), n1[i]);
-          if (q.d_out) P::get(next(q.d_out), go[i]);
-          if (q.d_x) P::get(next(q.d_x), gx[i]);
-          if (p.res) P::get(next(p.res), n2[i]);
-          if (GATE == kGateEach) {
-            P::get(next(p.gate), t);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) gate_value<true>(t[e], p.act, a[i][e], da[i][e]);
-          }
-          load_w<VEC>(p.w_post + c, w1);
-          if (p.w_pre) load_w<VEC>(p.w_pre + c, w2);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            if (GATE == kGateNone) a[i][e] = 1.f;
-            if (GATE == kGateGroup) a[i][e] = ga[i < GI ? i : 0][e];
-            n1[i][e] *= s1;
-            const float qv = p.scale * a[i][e] * w1[e] * n1[i][e];
-            n2[i][e] = (n2[i][e] + qv) * s2;
-            const float gw = p.w_pre ? gx[i][e] * w2[e] : 0.f;
-            sum[0] += gw * n2[i][e];
-            sum[1] += qv * (go[i][e] + s2 * gw);
-            sum[2] += qv * n2[i][e];
+          for (int e = 0; e < E; ++e) {
+            acc0 = fma(mul(gx[0][e], kKeep ? w2k[0][e] : w2[e]), m[0][e], acc0);
+            acc1 = fma(qv[e], v[0][e], acc1);
+            acc2 = fma(qv[e], m[0][e], acc2);
           }
         }
       }
+      float sum[3] = {total(acc0), total(acc1), total(acc2)};
       row_sum(sum, tpr, red, slot);
-      const float c2 = sum[0] * p.inv_d;
-      const float c1 = (sum[1] - s2 * c2 * sum[2]) * p.inv_d;
+      const float k = s2 * s2 * s2 * sum[0] * p.inv_d;   // s2 c2, times s2: r = v - k m
+      const float c1 = (sum[1] - k * sum[2]) * p.inv_d;
+      const P nk = both<P>(-k), nc = both<P>(-c1 * s1), ps1 = both<P>(s1), ps2 = both<P>(s2);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         const int c = (lane + i * tpr) * VEC;
         if (live && c < p.D) {
-          float w1[VEC], w2[VEC], oy[VEC], og[VEC];
-          load_w<VEC>(p.w_post + c, w1);
-          if (p.w_pre) load_w<VEC>(p.w_pre + c, w2);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float r = go[i][e];
-            if (p.w_pre) r += s2 * (gx[i][e] * w2[e] - n2[i][e] * c2);
-            dw2[i][e] += gx[i][e] * n2[i][e];
-            const float sr = p.scale * r, ar = a[i][e] * sr;
-            dw1[i][e] += ar * n1[i][e];
-            const float ug = sr * n1[i][e] * w1[e];
-            if (GATE == kGateEach) og[e] = ug * da[i][e];
-            if (GATE == kGateGroup) dg[i < GI ? i : 0][e] += ug * gd[i < GI ? i : 0][e];
-            oy[e] = s1 * (ar * w1[e] - n1[i][e] * c1);
-            go[i][e] = r;
+          P w1[E], w2[E], oy[E], og[E], qv[E];
+          if (!kKeep) {
+            weights(i, w1, w2);
+            front(i, w1, w2, n1[0], m[0], v[0], gx[0], a[0], da[0], qv);
           }
-          *reinterpret_cast<Raw *>((T *)q.dy + base + c) = P::put(oy);
-          if (q.d_res) *reinterpret_cast<Raw *>((T *)q.d_res + base + c) = P::put(go[i]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const P w = kKeep ? w1k[0][e] : w1[e];
+            dw2[i][e] = fma(mul(gx[0][e], ps2), m[0][e], dw2[i][e]);
+            v[0][e] = fma(m[0][e], nk, v[0][e]);            // r
+            P aw = w;
+            if (GATE == kGateEach) {
+              const P x = mul(v[0][e], n1[0][e]);
+              dw1[i][e] = fma(a[0][e], x, dw1[i][e]);
+              og[e] = mul(mul(w, da[0][e]), x);
+              aw = mul(w, a[0][e]);
+            } else if (GATE == kGateGroup) {
+              es[i < GI ? i : 0][e] = fma(v[0][e], n1[0][e], es[i < GI ? i : 0][e]);
+              aw = mul(w, ga[i < GI ? i : 0][e]);
+            } else {
+              dw1[i][e] = fma(v[0][e], n1[0][e], dw1[i][e]);
+            }
+            oy[e] = fma(mul(aw, v[0][e]), ps1, mul(n1[0][e], nc));
+          }
+          *reinterpret_cast<Raw *>((T *)q.dy + at + c) = Pc::put(oy);
+          if (q.d_res) *reinterpret_cast<Raw *>((T *)q.d_res + at + c) = Pc::put(v[0]);
           if (GATE == kGateEach && q.d_gate)
-            *reinterpret_cast<Raw *>((T *)q.d_gate + base + c) = P::put(og);
+            *reinterpret_cast<Raw *>((T *)q.d_gate + at + c) = Pc::put(og);
         }
       }
-      st ^= 1;
+      st = st + 1 == kStages ? 0 : st + 1;
     }
-    if constexpr (kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (GATE == kGateGroup && q.d_gate)
-      flush<VEC, GI>(dg, tpr, rg, group, lane, p.D, buf, [&](int c, float (&v)[VEC]) {
-        if (q.splits) {
+    if (in.kAsync) cp_async_wait<0>();
+    if constexpr (GATE == kGateGroup) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) q.part_gate[(size_t)blockIdx.x * p.D + c + e] = v[e];
-        } else {
-          *reinterpret_cast<Raw *>((T *)q.d_gate + (size_t)g * p.D + c) = P::put(v);
-        }
-      });
+      for (int i = 0; i < GI; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw1[i][e] = fma(ga[i][e], es[i][e], dw1[i][e]);
+      if (q.d_gate)
+        flush<Pc, GI, VEC>(es, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
+          P w1[E], w2[E], a[E];
+          weights(i, w1, w2);
+          Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), a);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            P value, d;
+            gate_value<true>(a[e], p.act, value, d);
+            a[e] = mul(mul(w1[e], d), s[e]);
+          }
+          if (q.splits) Pc::store(q.part_gate + (size_t)blockIdx.x * p.D + c, a);
+          else *reinterpret_cast<Raw *>((T *)q.d_gate + (size_t)g * p.D + c) = Pc::put(a);
+        });
+    }
   }
-  flush<VEC, ITEMS>(dw1, tpr, rg, group, lane, p.D, buf, [&](int c, float (&v)[VEC]) {
+  flush<Pc, ITEMS, VEC>(dw1, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) q.part_post[(size_t)blockIdx.x * p.D + c + e] = v[e];
+    for (int e = 0; e < E; ++e) s[e] = mul(s[e], scale);
+    Pc::store(q.part_post + (size_t)blockIdx.x * p.D + c, s);
   });
   if (p.w_pre)
-    flush<VEC, ITEMS>(dw2, tpr, rg, group, lane, p.D, buf, [&](int c, float (&v)[VEC]) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) q.part_pre[(size_t)blockIdx.x * p.D + c + e] = v[e];
+    flush<Pc, ITEMS, VEC>(dw2, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
+      Pc::store(q.part_pre + (size_t)blockIdx.x * p.D + c, s);
     });
 }
 
@@ -513,7 +650,7 @@ __global__ void __launch_bounds__(1024)
   const int n = what < 2 ? units : splits;
   float v = 0.f;
   if (c < D)
-#pragma unroll 4
+#pragma unroll 8
     for (int u = y; u < n; u += 32) v += src[(size_t)u * D + c];
   s[y][x] = v;
   __syncthreads();
@@ -549,10 +686,10 @@ NormParams params_of(const kda_norm_desc *d, const Layout &l, const void *y, con
   return p;
 }
 
-// Units (CTAs) of the backward: two for each of the 152 SMs, four where a
-// CTA holds several rows, and no more than there are row groups.
+// Units (CTAs) of the backward: as many as are resident on 152 SMs at up to
+// 128 registers per thread, and no more than there are row groups.
 int units_for(const kda_norm_desc *d, const Layout &l) {
-  const long long most = 152ll * (l.rg > 1 ? 4 : 2);
+  const long long most = 152ll * (l.tpr * l.rg > 256 ? 1 : 2);
   const long long n = (d->rows + l.rg - 1) / l.rg;
   return (int)(n < most ? n : most);
 }
@@ -566,15 +703,35 @@ int splits_for(const kda_norm_desc *d, const Layout &l, int units) {
   return (int)(s < 1 ? 1 : s);
 }
 
+// Dynamic shared memory of the staged rows (and p.stages).
 template <typename T, int VEC, int ITEMS>
-cudaError_t launch_fwd_t(const NormParams &p, cudaStream_t stream) {
+size_t stage_bytes(NormParams &p, int threads) {
+  if (VEC * sizeof(T) != 16) return 0;
+  const size_t n = (size_t)kStages * ITEMS * p.n_in * threads * 16;
+  if (n > kStageMax) return 0;
+  p.stages = kStages;
+  return n;
+}
+template <typename K>
+cudaError_t allow_smem(K kern, size_t smem) {
+  // with the static arrays, above the default 48 KB
+  return smem > 32 * 1024
+             ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+             : cudaSuccess;
+}
+
+template <typename T, int VEC, int ITEMS>
+cudaError_t launch_fwd_t(NormParams p, cudaStream_t stream) {
   auto kern = norm_fwd_kernel<T, VEC, ITEMS>;
   const int threads = p.tpr * p.rg;
+  const size_t smem = stage_bytes<T, VEC, ITEMS>(p, threads);
+  cudaError_t e = allow_smem(kern, smem);
   int per_sm = 1;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
   if (e != cudaSuccess) return e;
   const long long n = (p.R + p.rg - 1) / p.rg, most = (long long)num_sms() * per_sm;
-  kern<<<(unsigned)(n < most ? n : most), threads, 0, stream>>>(p);
+  kern<<<(unsigned)(n < most ? n : most), threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -582,17 +739,10 @@ template <typename T, int VEC, int ITEMS, int GATE>
 cudaError_t launch_bwd_t(NormBwdParams q, int units, cudaStream_t stream) {
   auto kern = norm_bwd_kernel<T, VEC, ITEMS, GATE>;
   const int threads = q.f.tpr * q.f.rg;
-  size_t smem = q.f.rg > 1 ? sizeof(float) * threads * VEC : 0;
-  const size_t staged = VEC > 1 ? (size_t)kStages * ITEMS * q.n_in * threads * 16 : 0;
-  if (staged && staged <= kStageMax) {
-    q.stages = kStages;
-    smem += staged;
-  }
-  if (smem > 32 * 1024) {   // with the static arrays, above the default 48 KB
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = (q.f.rg > 1 ? sizeof(float) * threads * VEC : 0) +
+                      stage_bytes<T, VEC, ITEMS>(q.f, threads);
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
   kern<<<units, threads, smem, stream>>>(q);
   return cudaGetLastError();
 }
@@ -625,17 +775,20 @@ kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y, const float
   const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec);
   NormParams p = params_of(d, l, y, w_post, residual, gate, w_pre);
   p.out = out; p.x = x; p.stats = stats;
+  p.n_in = 1 + (residual != nullptr) + (gate != nullptr);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
   using B = __nv_bfloat16;
-  if (l.vec > 1 && bf16)
+  if (l.vec > 2 && bf16)
     e = l.items == 1 ? launch_fwd_t<B, 8, 1>(p, cs) : l.items == 2 ? launch_fwd_t<B, 8, 2>(p, cs)
                                                                    : launch_fwd_t<B, 8, 4>(p, cs);
-  else if (l.vec > 1)
+  else if (l.vec > 2)
     e = l.items == 1   ? launch_fwd_t<float, 4, 1>(p, cs)
         : l.items == 2 ? launch_fwd_t<float, 4, 2>(p, cs)
         : l.items == 4 ? launch_fwd_t<float, 4, 4>(p, cs)
                        : launch_fwd_t<float, 4, 8>(p, cs);
+  else if (l.vec == 2)
+    e = l.items == 2 ? launch_fwd_t<B, 2, 2>(p, cs) : launch_fwd_t<B, 2, 8>(p, cs);
   else if (bf16)
     e = l.items == 4 ? launch_fwd_t<B, 1, 4>(p, cs) : launch_fwd_t<B, 1, 16>(p, cs);
   else
@@ -685,7 +838,7 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
   q.d_out = d_out; q.d_x = d_x; q.dy = dy; q.d_res = d_residual; q.d_gate = d_gate;
   q.gate_rows = gate ? d->gate_rows : 0;
   const int mode = !gate ? kGateNone : d->gate_rows == d->rows ? kGateEach : kGateGroup;
-  q.n_in = 1 + (d_out != nullptr) + (d_x != nullptr) + (residual != nullptr) + (mode == kGateEach);
+  q.f.n_in = 1 + (d_out != nullptr) + (d_x != nullptr) + (residual != nullptr) + (mode == kGateEach);
   int units = units_for(d, l);
   if (mode == kGateGroup) {
     q.splits = splits_for(d, l, units);
@@ -698,15 +851,18 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
   using B = __nv_bfloat16;
-  if (l.vec > 1 && bf16)
+  if (l.vec > 2 && bf16)
     e = l.items == 1   ? launch_bwd_g<B, 8, 1>(q, mode, units, cs)
         : l.items == 2 ? launch_bwd_g<B, 8, 2>(q, mode, units, cs)
                        : launch_bwd_g<B, 8, 4>(q, mode, units, cs);
-  else if (l.vec > 1)
+  else if (l.vec > 2)
     e = l.items == 1   ? launch_bwd_g<float, 4, 1>(q, mode, units, cs)
         : l.items == 2 ? launch_bwd_g<float, 4, 2>(q, mode, units, cs)
         : l.items == 4 ? launch_bwd_g<float, 4, 4>(q, mode, units, cs)
                        : launch_bwd_g<float, 4, 8>(q, mode, units, cs);
+  else if (l.vec == 2)
+    e = l.items == 2 ? launch_bwd_g<B, 2, 2>(q, mode, units, cs)
+                     : launch_bwd_g<B, 2, 8>(q, mode, units, cs);
   else if (bf16)
     e = l.items == 4 ? launch_bwd_g<B, 1, 4>(q, mode, units, cs)
                      : launch_bwd_g<B, 1, 16>(q, mode, units, cs);
