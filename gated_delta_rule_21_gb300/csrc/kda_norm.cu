@@ -47,13 +47,16 @@ struct Layout {
   int rg;       // rows per CTA
 };
 
-Layout layout_for(int D, int elt, bool vector_ok) {
+// Forward: 16 elements per thread, so that a row's two reductions weigh little
+// (at 8, 4096 bf16 elements took 87 us for 8192 rows, bound by issue).
+// Backward: 8, whose intermediate values then stay in registers.
+Layout layout_for(int D, int elt, bool vector_ok, bool forward) {
   Layout l;
   l.vec = !vector_ok ? 1 : D % (16 / elt) == 0 ? 16 / elt : elt == 2 && D % 2 == 0 ? 2 : 1;
   const int n = D / l.vec;
   const int most = l.vec > 2 ? 512 : 1024;     // threads of one row
-  // the kernels' numbers of accesses: 1, 2, 4, 8; 2, 8; 4, 16
-  l.items = l.vec > 2 ? 1 : l.vec == 2 ? 2 : 4;
+  // the kernels' numbers of accesses: 1, 2, 4, 8; vec 2: 2, 8; vec 1: 4, 16
+  l.items = l.vec > 2 ? (forward ? 16 / l.vec : 1) : l.vec == 2 ? 2 : 4;
   while (l.items * most < n) l.items *= l.vec > 2 ? 2 : 4;
   int t = (n + l.items - 1) / l.items;
   if (t > 32) {
@@ -149,23 +152,33 @@ struct Piece<T, 1> {
   static __device__ __forceinline__ void store(float *w, const P1 (&f)[1]) { *w = f[0].v; }
 };
 
-// act(a), and its derivative when DER.  The sigmoid takes the approximate
-// exp2 and reciprocal (a few fp32 ulp); tanh needs tanhf, whose relative
-// error holds near 0 too.
-template <bool DER>
-__device__ __forceinline__ void gate_value(float a, int act, float &v, float &d) {
-  if (act == KDA_GATE_TANH) {
-    v = tanhf(a);
+__device__ __forceinline__ float sfu_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sfu_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// act(a), and its derivative when DER, from the approximate exp2 and
+// reciprocal (a few fp32 ulp).  tanh a = 1 - 2 / (1 + e^2a) loses digits near
+// 0: below 0.3 it is its Taylor series to a^9, whose rest is 6e-8 of it.
+template <bool DER, int ACT>
+__device__ __forceinline__ void gate_one(float a, float &v, float &d) {
+  if (ACT == KDA_GATE_TANH) {
+    const float q = a * a;
+    const float s = a + a * q * (-1.f / 3 + q * (2.f / 15 + q * (-17.f / 315 + q * (62.f / 2835))));
+    const float l = 1.f - 2.f * sfu_rcp(1.f + sfu_ex2(2.f * kLog2e * a));
+    v = q < 0.09f ? s : l;
     if (DER) d = 1.f - v * v;
     return;
   }
-  if (act == KDA_GATE_NONE) {
-    v = a;
-    if (DER) d = 1.f;
-    return;
-  }
-  const float s = __fdividef(1.f, 1.f + __expf(-a));
-  if (act == KDA_GATE_SIGMOID) {
+  const float s = sfu_rcp(1.f + sfu_ex2(-kLog2e * a));
+  if (ACT == KDA_GATE_SIGMOID) {
     v = s;
     if (DER) d = s * (1.f - s);
   } else {
@@ -173,18 +186,35 @@ __device__ __forceinline__ void gate_value(float a, int act, float &v, float &d)
     if (DER) d = s * (1.f + a * (1.f - s));
   }
 }
-template <bool DER>
-__device__ __forceinline__ void gate_value(P1 a, int act, P1 &v, P1 &d) {
-  gate_value<DER>(a.v, act, v.v, d.v);
+template <bool DER, int ACT>
+__device__ __forceinline__ void gate_one(P1 a, P1 &v, P1 &d) {
+  gate_one<DER, ACT>(a.v, v.v, d.v);
 }
-template <bool DER>
-__device__ __forceinline__ void gate_value(P2 a, int act, P2 &v, P2 &d) {
+template <bool DER, int ACT>
+__device__ __forceinline__ void gate_one(P2 a, P2 &v, P2 &d) {
   float x, y, vx, vy, dx = 0.f, dy = 0.f;
   upk2(a.v, x, y);
-  gate_value<DER>(x, act, vx, dx);
-  gate_value<DER>(y, act, vy, dy);
+  gate_one<DER, ACT>(x, vx, dx);
+  gate_one<DER, ACT>(y, vy, dy);
   v.v = pk2(vx, vy);
   if (DER) d.v = pk2(dx, dy);
+}
+// a[] becomes act(a[]), d[] the derivative; one branch for all of them.
+template <bool DER, typename P, int E>
+__device__ __forceinline__ void gate_values(int act, P (&a)[E], P (&d)[E]) {
+  if (act == KDA_GATE_SILU) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) gate_one<DER, KDA_GATE_SILU>(a[e], a[e], d[e]);
+  } else if (act == KDA_GATE_SIGMOID) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) gate_one<DER, KDA_GATE_SIGMOID>(a[e], a[e], d[e]);
+  } else if (act == KDA_GATE_TANH) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) gate_one<DER, KDA_GATE_TANH>(a[e], a[e], d[e]);
+  } else if (DER) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) d[e] = both<P>(1.f);
+  }
 }
 
 // Sums of N values over the tpr threads of a row, in every thread of the
@@ -203,11 +233,20 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float (*red)[N][
     __syncthreads();
     const int nw = tpr >> 5, first = warp / nw * nw;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = lane < nw ? red[slot][i][first + lane] : 0.f;
+    for (int i = 0; i < N; ++i) v[i] = lane < nw ? red[slot][i][first + lane] : 0.f;
+    // the values lie in the first nw lanes; the sum is needed in all
+    if (nw <= 8) {
 #pragma unroll
-      for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      v[i] = s;
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int off = 4; off; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+        v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int off = 16; off; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     }
     slot ^= 1;
   }
@@ -271,8 +310,9 @@ struct Stage {
   }
 };
 
-// A CTA walks rows gridDim.x * rg apart, one row per row group at a time.
-template <typename T, int VEC, int ITEMS>
+// A CTA owns a contiguous range of rows, one row per row group at a time; of
+// a gate row shared by rows act(gate) is made once.
+template <typename T, int VEC, int ITEMS, int GATE>
 __global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_fwd_kernel(const NormParams p) {
   using Pc = Piece<T, VEC>;
   using P = typename Pc::P;
@@ -286,23 +326,37 @@ __global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_fwd_kernel(const No
                                    p.stages, p.D, lane, tpr};
   const int k_res = 1, k_gate = 1 + (p.res != nullptr);
   int slot = 0, st = 0;
-  const long long step = (long long)gridDim.x * rg;
-  auto gate_at = [&](long long row) {
-    return p.gate ? (const T *)p.gate + ((ptrdiff_t)((unsigned)row / p.rows_per_gate) - row) * p.D
-                  : (const T *)nullptr;    // as if it had a row for each
-  };
+  const long long lo = (long long)blockIdx.x * p.R / gridDim.x,
+                  hi = (long long)(blockIdx.x + 1) * p.R / gridDim.x;
   auto fetch = [&](long long row, int s) {
-    in.fetch(s, row < p.R, (size_t)row * p.D, (const T *)p.y, (const T *)p.res, gate_at(row));
+    in.fetch(s, row < hi, (size_t)row * p.D, (const T *)p.y, (const T *)p.res,
+             GATE == kGateEach ? (const T *)p.gate : (const T *)nullptr);
   };
-  const long long first = (long long)blockIdx.x * rg;
+  constexpr int GI = GATE == kGateGroup ? ITEMS : 1;
+  P ga[GI][E];
+  unsigned ga_row = ~0u;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(first + group + s * step, s);
-  for (long long r0 = first; r0 < p.R; r0 += step) {
+  for (int s = 0; s < kStages - 1; ++s) fetch(lo + group + s * rg, s);
+  for (long long r0 = lo; r0 < hi; r0 += rg) {
     const long long row = r0 + group;
-    const bool live = row < p.R;
+    const bool live = row < hi;
     const size_t at = (size_t)row * p.D;
-    const T *gate = gate_at(row);
-    fetch(row + (kStages - 1) * step, st == 0 ? kStages - 1 : st - 1);
+    fetch(row + (kStages - 1) * rg, st == 0 ? kStages - 1 : st - 1);
+    if (GATE == kGateGroup && live) {
+      const unsigned g = (unsigned)row / p.rows_per_gate;
+      if (g != ga_row) {
+        ga_row = g;
+#pragma unroll
+        for (int i = 0; i < GI; ++i) {
+          const int c = (lane + i * tpr) * VEC;
+          P d[E];
+          if (c < p.D) {
+            Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), ga[i]);
+            gate_values<false>(p.act, ga[i], d);
+          }
+        }
+      }
+    }
     if (in.kAsync) cp_async_wait<kStages - 1>();
     P v[ITEMS][E], acc = both<P>(0.f);
 #pragma unroll
@@ -326,15 +380,16 @@ __global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_fwd_kernel(const No
         Pc::weight(p.w_post + c, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[i][e] = mul(mul(v[i][e], k), w[e]);
-        if (gate) {
-          Pc::get(in.get(st, i, k_gate, gate, at), a);
+        if (GATE == kGateEach) {
+          Pc::get(in.get(st, i, k_gate, p.gate, at), a);
+          P d[E];
+          gate_values<false>(p.act, a, d);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            P d;
-            gate_value<false>(a[e], p.act, a[e], d);
-            v[i][e] = mul(v[i][e], a[e]);
-          }
+          for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], a[e]);
         }
+        if (GATE == kGateGroup)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], ga[i < GI ? i : 0][e]);
         if (p.res) {
           Pc::get(in.get(st, i, k_res, p.res, at), a);
 #pragma unroll
@@ -486,10 +541,9 @@ __global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_bwd_kernel(const No
 #pragma unroll
         for (int e = 0; e < E; ++e) es[i][e] = ga[i][e] = both<P>(0.f);
         if (c < p.D) {
-          P a[E], d;
-          Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), a);
-#pragma unroll
-          for (int e = 0; e < E; ++e) gate_value<false>(a[e], p.act, ga[i][e], d);
+          P d[E];
+          Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), ga[i]);
+          gate_values<false>(p.act, ga[i], d);
         }
       }
     }
@@ -530,8 +584,7 @@ __global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_bwd_kernel(const No
           for (int e = 0; e < E; ++e) m[e] = both<P>(0.f);
         if (GATE == kGateEach) {
           Pc::get(in.get(st, i, k_gate, p.gate, at), a);
-#pragma unroll
-          for (int e = 0; e < E; ++e) gate_value<true>(a[e], p.act, a[e], da[e]);
+          gate_values<true>(p.act, a, da);
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -609,15 +662,12 @@ __global__ void __launch_bounds__(VEC > 2 ? 512 : 1024) norm_bwd_kernel(const No
         for (int e = 0; e < E; ++e) dw1[i][e] = fma(ga[i][e], es[i][e], dw1[i][e]);
       if (q.d_gate)
         flush<Pc, GI, VEC>(es, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
-          P w1[E], w2[E], a[E];
+          P w1[E], w2[E], a[E], d[E];
           weights(i, w1, w2);
           Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), a);
+          gate_values<true>(p.act, a, d);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            P value, d;
-            gate_value<true>(a[e], p.act, value, d);
-            a[e] = mul(mul(w1[e], d), s[e]);
-          }
+          for (int e = 0; e < E; ++e) a[e] = mul(mul(w1[e], d[e]), s[e]);
           if (q.splits) Pc::store(q.part_gate + (size_t)blockIdx.x * p.D + c, a);
           else *reinterpret_cast<Raw *>((T *)q.d_gate + (size_t)g * p.D + c) = Pc::put(a);
         });
@@ -720,9 +770,9 @@ cudaError_t allow_smem(K kern, size_t smem) {
              : cudaSuccess;
 }
 
-template <typename T, int VEC, int ITEMS>
-cudaError_t launch_fwd_t(NormParams p, cudaStream_t stream) {
-  auto kern = norm_fwd_kernel<T, VEC, ITEMS>;
+template <typename T, int VEC, int ITEMS, int GATE>
+cudaError_t launch_fwd_g(NormParams p, cudaStream_t stream) {
+  auto kern = norm_fwd_kernel<T, VEC, ITEMS, GATE>;
   const int threads = p.tpr * p.rg;
   const size_t smem = stage_bytes<T, VEC, ITEMS>(p, threads);
   cudaError_t e = allow_smem(kern, smem);
@@ -733,6 +783,13 @@ cudaError_t launch_fwd_t(NormParams p, cudaStream_t stream) {
   const long long n = (p.R + p.rg - 1) / p.rg, most = (long long)num_sms() * per_sm;
   kern<<<(unsigned)(n < most ? n : most), threads, smem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T, int VEC, int ITEMS>
+cudaError_t launch_fwd_t(const NormParams &p, int gate, cudaStream_t stream) {
+  if (gate == kGateNone) return launch_fwd_g<T, VEC, ITEMS, kGateNone>(p, stream);
+  if (gate == kGateEach) return launch_fwd_g<T, VEC, ITEMS, kGateEach>(p, stream);
+  return launch_fwd_g<T, VEC, ITEMS, kGateGroup>(p, stream);
 }
 
 template <typename T, int VEC, int ITEMS, int GATE>
@@ -772,27 +829,24 @@ kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y, const float
   for (const void *ptr : {y, (const void *)w_post, residual, gate, (const void *)w_pre,
                           (const void *)out, (const void *)x})
     vec = vec && aligned16(ptr);
-  const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec);
+  const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec, true);
   NormParams p = params_of(d, l, y, w_post, residual, gate, w_pre);
   p.out = out; p.x = x; p.stats = stats;
-  p.n_in = 1 + (residual != nullptr) + (gate != nullptr);
+  const int mode = !gate ? kGateNone : d->gate_rows == d->rows ? kGateEach : kGateGroup;
+  p.n_in = 1 + (residual != nullptr) + (mode == kGateEach);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
   using B = __nv_bfloat16;
   if (l.vec > 2 && bf16)
-    e = l.items == 1 ? launch_fwd_t<B, 8, 1>(p, cs) : l.items == 2 ? launch_fwd_t<B, 8, 2>(p, cs)
-                                                                   : launch_fwd_t<B, 8, 4>(p, cs);
+    e = l.items == 2 ? launch_fwd_t<B, 8, 2>(p, mode, cs) : launch_fwd_t<B, 8, 4>(p, mode, cs);
   else if (l.vec > 2)
-    e = l.items == 1   ? launch_fwd_t<float, 4, 1>(p, cs)
-        : l.items == 2 ? launch_fwd_t<float, 4, 2>(p, cs)
-        : l.items == 4 ? launch_fwd_t<float, 4, 4>(p, cs)
-                       : launch_fwd_t<float, 4, 8>(p, cs);
+    e = l.items == 4 ? launch_fwd_t<float, 4, 4>(p, mode, cs) : launch_fwd_t<float, 4, 8>(p, mode, cs);
   else if (l.vec == 2)
-    e = l.items == 2 ? launch_fwd_t<B, 2, 2>(p, cs) : launch_fwd_t<B, 2, 8>(p, cs);
+    e = l.items == 2 ? launch_fwd_t<B, 2, 2>(p, mode, cs) : launch_fwd_t<B, 2, 8>(p, mode, cs);
   else if (bf16)
-    e = l.items == 4 ? launch_fwd_t<B, 1, 4>(p, cs) : launch_fwd_t<B, 1, 16>(p, cs);
+    e = l.items == 4 ? launch_fwd_t<B, 1, 4>(p, mode, cs) : launch_fwd_t<B, 1, 16>(p, mode, cs);
   else
-    e = l.items == 4 ? launch_fwd_t<float, 1, 4>(p, cs) : launch_fwd_t<float, 1, 16>(p, cs);
+    e = l.items == 4 ? launch_fwd_t<float, 1, 4>(p, mode, cs) : launch_fwd_t<float, 1, 16>(p, mode, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -801,7 +855,7 @@ size_t kda_block_norm_bwd_workspace_size(const kda_norm_desc *d, int has_gate) {
   // the largest over the layouts, since types and pointers choose between them
   size_t n = 0;
   for (int v = 0; v < 3; ++v) {
-    const Layout l = layout_for(d->dim, v == 1 ? 2 : 4, v != 0);
+    const Layout l = layout_for(d->dim, v == 1 ? 2 : 4, v != 0, false);
     size_t units = (size_t)units_for(d, l), gate_units = 0;
     if (has_gate && d->gate_rows < d->rows) {
       const int s = splits_for(d, l, (int)units);
@@ -831,7 +885,7 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
   for (const void *ptr : {y, (const void *)w_post, residual, gate, (const void *)w_pre, d_out, d_x,
                           (const void *)dy, (const void *)d_residual, (const void *)d_gate})
     vec = vec && aligned16(ptr);
-  const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec);
+  const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec, false);
   NormBwdParams q = {};
   q.f = params_of(d, l, y, w_post, residual, gate, w_pre);
   q.f.stats = const_cast<float *>(stats);

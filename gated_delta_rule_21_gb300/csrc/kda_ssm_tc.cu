@@ -87,6 +87,12 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------------------
 // The convolution of a tile of TP channels x 128 tokens by 256 threads.  The
 // tile's rows and the 3 before it are staged by cp.async; a warp owns 8
@@ -210,11 +216,6 @@ struct Conv {
       upk2(add2(pk2(1.f, 1.f), pk2(ex2(e0), ex2(e1))), d0, d1);
       upk2(mul2(v, pk2(rcp(d0), rcp(d1))), u[i], u[i + 1]);
     }
-  }
-  static __device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
   }
 };
 
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float y = fmaf(ein, yi[8 * q + e], yx[8 * q + e]) + D * x[e];
-          if (p.z) y *= z[e] * __fdividef(1.f, 1.f + ex2(-kLog2e * z[e]));
+          if (p.z) y *= z[e] * rcp(1.f + ex2(-kLog2e * z[e]));
           v[e] = run < 0 ? 0.f : y;
         }
         *reinterpret_cast<uint4 *>(zp) = pack8(v);
