@@ -14,8 +14,7 @@
 // A CTA of 256 threads owns a tile of TC columns of one (sequence, head).  A
 // thread owns 4 adjacent columns of every (1024 / TC)-th key row, so a warp's
 // 16-byte accesses cover whole row segments, and all of a thread's loads
-// are issued before anything else.  The tile is the full head, or 32 columns
-// when the heads would leave SMs without a CTA.
+// are issued before anything else.
 //
 // The short convolution's cache [3][channels] is moved on in place.  The
 // channels of B and C (of q and k) are read by several CTAs, so the last CTA
@@ -32,20 +31,17 @@ constexpr int kWave = kThreads * 4; // state elements per access of a CTA
 
 __device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
 
-// Thread 0 counts this CTA in; true in every thread of the last of `total`
-// CTAs, which also resets the counter.  Every read of the counted CTAs that
-// comes before the call is over when it returns true.
-__device__ __forceinline__ bool arrive_last(uint32_t *counter, uint32_t total, int *flag) {
-  __syncthreads();
+// Thread 0 counts its CTA in, after a barrier that ends the CTA's reads, and
+// sets *flag to whether it is the last of `total`, which also resets the
+// counter.  The CTA goes on meanwhile and reads the flag after a later barrier.
+__device__ __forceinline__ void arrive(uint32_t *counter, uint32_t total, int *flag) {
   if (threadIdx.x == 0) {
     __threadfence();
     const uint32_t n = atomicAdd(counter, 1u);
-    *flag = n + 1 == total;
     if (n + 1 == total) *counter = 0;
+    *flag = n + 1 == total;
     __threadfence();
   }
-  __syncthreads();
-  return *flag != 0;
 }
 
 // One channel of the convolution at the new token: c[3] are the cached
@@ -77,7 +73,7 @@ struct SsmStepParams {
 
 // IT = accesses per thread: N * TC / 1024.
 template <typename T, int N, int TC>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams p) {
+__global__ void __launch_bounds__(kThreads, 4) ssm_step_kernel(const SsmStepParams p) {
   constexpr int IT = N * TC / kWave, RG = kWave / TC;
   __shared__ float sB[N], sC[N], sx[TC], red[RG][TC];
   __shared__ int flag;
@@ -114,7 +110,8 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams 
   const float d = fmaxf(dr, 0.f) + log1pf(expf(-fabsf(dr)));
   const float a = expf(d * p.A[h]);
   uint32_t *counter = p.counters + (size_t)b * p.G + g;
-  const bool last = arrive_last(counter, (uint32_t)(p.H / p.G * p.tiles), &flag);
+  __syncthreads();
+  arrive(counter, (uint32_t)(p.H / p.G * p.tiles), &flag);
 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float x0 = d * sx[col], x1 = d * sx[col + 1], x2 = d * sx[col + 2], x3 = d * sx[col + 3];
@@ -132,13 +129,13 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams 
     acc.w += cn * v[i].w;
   }
   *reinterpret_cast<float4 *>(&red[row][col]) = acc;
-  if (last) {   // the group's B and C channels
+  __syncthreads();
+  if (flag) {   // the last of the group: its B and C channels
     for (int i = tid; i < 2 * N; i += kThreads) {
       const int c = i < N ? cb + i : cc + i - N;
       shift_channel(conv + c, p.channels, x[c]);
     }
   }
-  __syncthreads();
   if (tid < TC) {
     float o = 0.f;
 #pragma unroll
@@ -163,7 +160,7 @@ struct KdaStepParams {
 };
 
 template <typename T, int K, int TC>
-__global__ void __launch_bounds__(kThreads) kda_step_kernel(const KdaStepParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kda_step_kernel(const KdaStepParams p) {
   constexpr int IT = K * TC / kWave, RG = kWave / TC;
   __shared__ float sq[K], sk[K], sg[K], sv[TC], rk[RG][TC], rq[RG][TC], srk[TC], dots[3];
   __shared__ int flag;
@@ -201,11 +198,9 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const KdaStepParams 
   }
   for (int i = tid; i < K; i += kThreads) sg[i] = expf(p.g[((size_t)b * p.H + h) * K + i]);
   const float beta = p.beta[(size_t)b * p.H + h];
-  bool last = false;
-  if (conv)
-    last = arrive_last(p.counters + (size_t)b * p.H + h, (uint32_t)p.tiles, &flag);
-  else
-    __syncthreads();
+  if (tid == 0) flag = 0;
+  __syncthreads();
+  if (conv) arrive(p.counters + (size_t)b * p.H + h, (uint32_t)p.tiles, &flag);
 
   // sums of the decayed state against k and q, not yet normalised
   float4 ak = make_float4(0.f, 0.f, 0.f, 0.f), aq = ak;
@@ -232,11 +227,11 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const KdaStepParams 
       for (int j = 0; j < 3; ++j) n[j] += __shfl_xor_sync(0xffffffffu, n[j], off);
     if ((tid & 31) < 3) dots[tid & 31] = (tid & 31) == 0 ? n[0] : (tid & 31) == 1 ? n[1] : n[2];
   }
-  if (last) {
+  __syncthreads();
+  if (flag) {
     for (int i = tid; i < 2 * K; i += kThreads)
       shift_channel(conv + (i < K ? cq + i : ck + i - K), channels, i < K ? q[i] : k[i - K]);
   }
-  __syncthreads();
   const float nq = p.l2norm ? rsqrtf(dots[0] + 1e-6f) : 1.f;
   const float nk = p.l2norm ? rsqrtf(dots[1] + 1e-6f) : 1.f;
   if (tid < TC) {
@@ -260,11 +255,11 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const KdaStepParams 
   }
 }
 
-// Columns per CTA: the whole head, or 32 columns while that leaves no more
-// than two CTAs for each SM.
+// Columns per CTA: 32 while that leaves no more than two CTAs for each SM,
+// else up to 64 (a tile of 32 KB at 128 keys: four CTAs fit an SM).
 int tile_for(int B, int H, int cols) {
   const long long small = (long long)B * H * (cols / 32);
-  return small <= 2ll * num_sms() ? 32 : cols;
+  return small <= 2ll * num_sms() || cols == 32 ? 32 : 64;
 }
 
 template <typename T, int N>
@@ -273,8 +268,7 @@ cudaError_t launch_ssm_step(SsmStepParams p, int B, cudaStream_t cs) {
   p.tiles = p.P / tc;
   const unsigned grid = (unsigned)(B * p.H * p.tiles);
   if (tc == 32) ssm_step_kernel<T, N, 32><<<grid, kThreads, 0, cs>>>(p);
-  else if (tc == 64) ssm_step_kernel<T, N, 64><<<grid, kThreads, 0, cs>>>(p);
-  else ssm_step_kernel<T, N, 128><<<grid, kThreads, 0, cs>>>(p);
+  else ssm_step_kernel<T, N, 64><<<grid, kThreads, 0, cs>>>(p);
   return cudaGetLastError();
 }
 
@@ -284,8 +278,7 @@ cudaError_t launch_kda_step(KdaStepParams p, int B, cudaStream_t cs) {
   p.tiles = p.V / tc;
   const unsigned grid = (unsigned)(B * p.H * p.tiles);
   if (tc == 32) kda_step_kernel<T, K, 32><<<grid, kThreads, 0, cs>>>(p);
-  else if (tc == 64) kda_step_kernel<T, K, 64><<<grid, kThreads, 0, cs>>>(p);
-  else kda_step_kernel<T, K, 128><<<grid, kThreads, 0, cs>>>(p);
+  else kda_step_kernel<T, K, 64><<<grid, kThreads, 0, cs>>>(p);
   return cudaGetLastError();
 }
 
