@@ -11,10 +11,13 @@
 // The second form of o needs only sums over the decayed state, so each step
 // is one pass: load the tile, one reduction over the keys, store the tile.
 //
-// A CTA of 256 threads owns a tile of TC columns of one (sequence, head).  A
-// thread owns 4 adjacent columns of every (1024 / TC)-th key row, so a warp's
-// 16-byte accesses cover whole row segments, and all of a thread's loads
-// are issued before anything else.
+// A unit is a tile of TC columns of one (sequence, head); a CTA of 256 threads
+// walks units gridDim.x apart.  A thread owns 4 adjacent columns of every
+// (1024 / TC)-th key row, so a warp's 16-byte accesses cover whole row
+// segments.  While a unit is computed, the next one's state is on its way
+// to shared memory (each thread copies its own pieces, so no barrier guards
+// them) and its inputs to registers: without that the two barriers of a unit
+// left the memory idle (kda 119 us, ssm 112 us).
 //
 // The short convolution's cache [3][channels] is moved on in place.  The
 // channels of B and C (of q and k) are read by several CTAs, so the last CTA
@@ -29,29 +32,75 @@ constexpr int kThreads = 256;
 constexpr int kTap = 4;             // taps of the convolution
 constexpr int kWave = kThreads * 4; // state elements per access of a CTA
 
-__device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+// SiLU from the approximate exp2 and reciprocal (a few fp32 ulp).
+__device__ __forceinline__ float silu(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return x * r;
+}
+
+// The units of a CTA: a fixed column tile of the (sequence, head) pairs that
+// lie `pairs` apart (all without a division per unit).
+struct Walk {
+  int H, B, db, dh;       // pairs = db * H + dh
+  int tiles, log_tiles;
+};
+struct Place {
+  int b, h;
+  __device__ __forceinline__ void advance(const Walk &w) {
+    b += w.db;
+    h += w.dh;
+    if (h >= w.H) {
+      h -= w.H;
+      ++b;
+    }
+  }
+};
 
 // Thread 0 counts its CTA in, after a barrier that ends the CTA's reads, and
 // sets *flag to whether it is the last of `total`, which also resets the
 // counter.  The CTA goes on meanwhile and reads the flag after a later barrier.
+// No fence: what is ordered are reads before another CTA's writes, and the
+// reads are over when their values have gone through the barrier (fences
+// here cost 1 us of latency, and a unit's worth of time under load).
 __device__ __forceinline__ void arrive(uint32_t *counter, uint32_t total, int *flag) {
   if (threadIdx.x == 0) {
-    __threadfence();
     const uint32_t n = atomicAdd(counter, 1u);
     if (n + 1 == total) *counter = 0;
     *flag = n + 1 == total;
-    __threadfence();
   }
 }
 
-// One channel of the convolution at the new token: c[3] are the cached
-// inputs, oldest first.
+// One channel of the convolution at the new token: the input, the cached
+// ones (oldest first), the taps.
 template <typename T>
-__device__ __forceinline__ float conv_token(const T *cache, size_t stride, const float4 w, float b,
-                                            float x) {
-  const float a0 = to_f32(cache[0]), a1 = to_f32(cache[stride]), a2 = to_f32(cache[2 * stride]);
-  return silu(w.w * x + w.z * a2 + w.y * a1 + w.x * a0 + b);
-}
+struct Channel {
+  T x, c0, c1, c2;
+  float4 w;
+  float bias;
+
+  __device__ __forceinline__ void load(const T *px, const T *cache, size_t stride, const float *pw,
+                                       const float *pb) {
+    x = *px;
+    if (cache) {
+      c0 = cache[0];
+      c1 = cache[stride];
+      c2 = cache[2 * stride];
+      w = *reinterpret_cast<const float4 *>(pw);
+      bias = pb ? *pb : 0.f;
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    return silu(w.w * to_f32(x) + w.z * to_f32(c2) + w.y * to_f32(c1) + w.x * to_f32(c0) + bias);
+  }
+  __device__ __forceinline__ void shift(T *cache, size_t stride) const {
+    cache[0] = c1;
+    cache[stride] = c2;
+    cache[2 * stride] = x;
+  }
+};
+// Moves a channel that other CTAs have read too.
 template <typename T>
 __device__ __forceinline__ void shift_channel(T *cache, size_t stride, T x) {
   cache[0] = cache[stride];
@@ -59,8 +108,17 @@ __device__ __forceinline__ void shift_channel(T *cache, size_t stride, T x) {
   cache[2 * stride] = x;
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+
 struct SsmStepParams {
-  int H, P, N, G, tiles, n_slots, channels;
+  Walk walk;
+  int H, P, N, G, n_slots, channels;
+  float inv_hpg;          // G / H
   const void *xbc, *z, *dt;
   long long xbc_stride, z_stride, dt_stride;
   const float *w, *bias, *A, *D, *dt_bias;
@@ -73,81 +131,154 @@ struct SsmStepParams {
 
 // IT = accesses per thread: N * TC / 1024.
 template <typename T, int N, int TC>
-__global__ void __launch_bounds__(kThreads, 4) ssm_step_kernel(const SsmStepParams p) {
-  constexpr int IT = N * TC / kWave, RG = kWave / TC;
-  __shared__ float sB[N], sC[N], sx[TC], red[RG][TC];
+__global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(const SsmStepParams p) {
+  constexpr int IT = N * TC / kWave, RG = kWave / TC, CH = 2 * N + TC;
+  constexpr int NC = (CH + kThreads - 1) / kThreads;      // channels per thread
+  extern __shared__ __align__(16) float4 stage[];         // [2][IT][kThreads]
+  __shared__ float sB[2][N], sC[2][N], sx[2][TC], red[RG][TC];
   __shared__ int flag;
-  const int tid = threadIdx.x;
-  const int tile = blockIdx.x % p.tiles, bh = blockIdx.x / p.tiles;
-  const int h = bh % p.H, b = bh / p.H, c0 = tile * TC;
-  const int slot = p.slots ? p.slots[b] : b;
-  T *y = static_cast<T *>(p.y) + ((size_t)b * p.H + h) * p.P + c0;
-  if (slot < 0 || slot >= p.n_slots) {
-    if (tid < TC) y[tid] = from_f32<T>(0.f);
-    return;
-  }
-  const int col = (tid * 4) % TC, row = tid * 4 / TC;
-  float *s = p.state + (((size_t)slot * p.H + h) * N + row) * p.P + c0 + col;
-  float4 v[IT];
-#pragma unroll
-  for (int i = 0; i < IT; ++i)
-    v[i] = *reinterpret_cast<const float4 *>(s + (size_t)i * RG * p.P);
+  const int tid = threadIdx.x, col = (tid * 4) % TC, row = tid * 4 / TC;
 
-  const int g = h / (p.H / p.G);
-  const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_stride;
-  T *conv = static_cast<T *>(p.conv) + (size_t)slot * (kTap - 1) * p.channels;
-  const float dr = to_f32(static_cast<const T *>(p.dt)[(size_t)b * p.dt_stride + h]) +
-                   (p.dt_bias ? p.dt_bias[h] : 0.f);
-  const int cx = h * p.P + c0, cb = p.H * p.P + g * N, cc = cb + p.G * N;
-  for (int i = tid; i < 2 * N + TC; i += kThreads) {
-    const int c = i < N ? cb + i : i < 2 * N ? cc + i - N : cx + i - 2 * N;
-    const T xn = x[c];
-    const float u = conv_token(conv + c, p.channels, *reinterpret_cast<const float4 *>(p.w + 4 * c),
-                               p.bias ? p.bias[c] : 0.f, to_f32(xn));
-    (i < N ? sB[i] : i < 2 * N ? sC[i - N] : sx[i - 2 * N]) = u;
-    if (i >= 2 * N) shift_channel(conv + c, p.channels, xn);   // this CTA's own channels
-  }
-  const float d = fmaxf(dr, 0.f) + log1pf(expf(-fabsf(dr)));
-  const float a = expf(d * p.A[h]);
-  uint32_t *counter = p.counters + (size_t)b * p.G + g;
-  __syncthreads();
-  arrive(counter, (uint32_t)(p.H / p.G * p.tiles), &flag);
-
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float x0 = d * sx[col], x1 = d * sx[col + 1], x2 = d * sx[col + 2], x3 = d * sx[col + 3];
+  const int c0 = (blockIdx.x & (p.walk.tiles - 1)) * TC;
+  struct Unit {
+    Place at;
+    int slot, g;
+    Channel<T> ch[NC];
+    float dt, A, z;
+  };
+  // number of the unit's channel i: of B, of C, of the tile's columns of x
+  auto channel = [&](const Unit &n, int i) {
+    return i < 2 * N ? p.H * p.P + n.g * N + (i < N ? i : p.G * N + i - N)
+                     : n.at.h * p.P + c0 + i - 2 * N;
+  };
+  auto state_of = [&](const Unit &n) {
+    return p.state + (((size_t)n.slot * p.H + n.at.h) * N + row) * p.P + c0 + col;
+  };
+  auto conv_of = [&](const Unit &n) {
+    return static_cast<T *>(p.conv) + (size_t)n.slot * (kTap - 1) * p.channels;
+  };
+  auto slot_of = [&](const Place &w) {
+    int s = -1;
+    if (w.b < p.walk.B) s = p.slots ? p.slots[w.b] : w.b;
+    return s < p.n_slots ? s : -1;
+  };
+  auto load = [&](Unit &n, const Place &at, int slot, int st) {
+    n.at = at;
+    n.slot = slot;
+    if (slot >= 0) {
+      n.g = (int)((at.h + 0.5f) * p.inv_hpg);
+      const float *s = state_of(n);
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const float bn = sB[row + i * RG], cn = sC[row + i * RG];
-    v[i].x = a * v[i].x + bn * x0;
-    v[i].y = a * v[i].y + bn * x1;
-    v[i].z = a * v[i].z + bn * x2;
-    v[i].w = a * v[i].w + bn * x3;
-    *reinterpret_cast<float4 *>(s + (size_t)i * RG * p.P) = v[i];
-    acc.x += cn * v[i].x;
-    acc.y += cn * v[i].y;
-    acc.z += cn * v[i].z;
-    acc.w += cn * v[i].w;
-  }
-  *reinterpret_cast<float4 *>(&red[row][col]) = acc;
-  __syncthreads();
-  if (flag) {   // the last of the group: its B and C channels
-    for (int i = tid; i < 2 * N; i += kThreads) {
-      const int c = i < N ? cb + i : cc + i - N;
-      shift_channel(conv + c, p.channels, x[c]);
+      for (int i = 0; i < IT; ++i)
+        cp_async16(stage + (st * IT + i) * kThreads + tid, s + (size_t)i * RG * p.P);
+      const T *x = static_cast<const T *>(p.xbc) + (size_t)at.b * p.xbc_stride;
+      const T *conv = conv_of(n);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const int i = tid + k * kThreads;
+        if (i < CH) {
+          const int c = channel(n, i);
+          n.ch[k].load(x + c, conv + c, p.channels, p.w + 4 * (size_t)c,
+                       p.bias ? p.bias + c : nullptr);
+        }
+      }
+      n.dt = to_f32(static_cast<const T *>(p.dt)[(size_t)at.b * p.dt_stride + at.h]) +
+             (p.dt_bias ? p.dt_bias[at.h] : 0.f);
+      n.A = p.A[at.h];
+      if (p.z && tid < TC)
+        n.z = to_f32(static_cast<const T *>(
+            p.z)[(size_t)at.b * p.z_stride + at.h * p.P + c0 + tid]);
     }
-  }
-  if (tid < TC) {
-    float o = 0.f;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto work = [&](const Unit &now, int st) {
+    T *y = static_cast<T *>(p.y) + ((size_t)now.at.b * p.H + now.at.h) * p.P + c0;
+    if (now.slot < 0) {           // idle (uniform)
+      if (tid < TC) y[tid] = from_f32<T>(0.f);
+      return;
+    }
+    T *conv = conv_of(now);
 #pragma unroll
-    for (int r = 0; r < RG; ++r) o += red[r][tid];
-    if (p.D) o += p.D[h] * sx[tid];
-    if (p.z) o *= silu(to_f32(static_cast<const T *>(p.z)[(size_t)b * p.z_stride + cx + tid]));
-    y[tid] = from_f32<T>(o);
+    for (int k = 0; k < NC; ++k) {
+      const int i = tid + k * kThreads;
+      if (i < CH) {
+        const float v = now.ch[k].value();
+        (i < N ? sB[st][i] : i < 2 * N ? sC[st][i - N] : sx[st][i - 2 * N]) = v;
+        if (i >= 2 * N) now.ch[k].shift(conv + channel(now, i), p.channels);  // its own channels
+      }
+    }
+    const float d = fmaxf(now.dt, 0.f) + log1pf(expf(-fabsf(now.dt)));
+    const float a = expf(d * now.A);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    arrive(p.counters + (size_t)now.at.b * p.G + now.g, (uint32_t)(p.H / p.G * p.walk.tiles),
+           &flag);
+
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float x0 = d * sx[st][col], x1 = d * sx[st][col + 1], x2 = d * sx[st][col + 2],
+                x3 = d * sx[st][col + 3];
+    float *s = state_of(now);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      float4 v = stage[(st * IT + i) * kThreads + tid];
+      const float bn = sB[st][row + i * RG], cn = sC[st][row + i * RG];
+      v.x = a * v.x + bn * x0;
+      v.y = a * v.y + bn * x1;
+      v.z = a * v.z + bn * x2;
+      v.w = a * v.w + bn * x3;
+      *reinterpret_cast<float4 *>(s + (size_t)i * RG * p.P) = v;
+      acc.x += cn * v.x;
+      acc.y += cn * v.y;
+      acc.z += cn * v.z;
+      acc.w += cn * v.w;
+    }
+    *reinterpret_cast<float4 *>(&red[row][col]) = acc;
+    __syncthreads();
+    if (flag) {   // the last of the group: its B and C channels
+      const T *x = static_cast<const T *>(p.xbc) + (size_t)now.at.b * p.xbc_stride;
+      for (int i = tid; i < 2 * N; i += kThreads) {
+        const int c = channel(now, i);
+        shift_channel(conv + c, p.channels, x[c]);
+      }
+    }
+    if (tid < TC) {
+      float o = 0.f;
+#pragma unroll
+      for (int r = 0; r < RG; ++r) o += red[r][tid];
+      if (p.D) o += p.D[now.at.h] * sx[st][tid];
+      if (p.z) o *= silu(now.z);
+      y[tid] = from_f32<T>(o);
+    }
+  };
+
+  // the slot is read two units ahead, the rest one
+  Unit u0, u1;
+  Place at = {(int)(blockIdx.x >> p.walk.log_tiles) / p.H,
+              (int)(blockIdx.x >> p.walk.log_tiles) % p.H};
+  load(u0, at, slot_of(at), 0);
+  at.advance(p.walk);
+  int slot = slot_of(at);
+  auto next = [&](Unit &n, int st) {
+    const Place here = at;
+    const int s = slot;
+    at.advance(p.walk);
+    slot = slot_of(at);
+    load(n, here, s, st);
+  };
+  while (true) {
+    next(u1, 1);
+    work(u0, 0);
+    if (u1.at.b >= p.walk.B) break;
+    next(u0, 0);
+    work(u1, 1);
+    if (u0.at.b >= p.walk.B) break;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 struct KdaStepParams {
-  int H, K, V, tiles, n_slots, l2norm;
+  Walk walk;
+  int H, K, V, n_slots, l2norm;
   const void *q, *k, *v;
   long long q_stride, k_stride, v_stride;
   const float *g, *beta, *w;
@@ -160,126 +291,216 @@ struct KdaStepParams {
 };
 
 template <typename T, int K, int TC>
-__global__ void __launch_bounds__(kThreads, 4) kda_step_kernel(const KdaStepParams p) {
-  constexpr int IT = K * TC / kWave, RG = kWave / TC;
-  __shared__ float sq[K], sk[K], sg[K], sv[TC], rk[RG][TC], rq[RG][TC], srk[TC], dots[3];
+__global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepParams p) {
+  constexpr int IT = K * TC / kWave, RG = kWave / TC, CH = 2 * K + TC;
+  constexpr int NC = (CH + kThreads - 1) / kThreads;
+  extern __shared__ __align__(16) float4 stage[];         // [2][IT][kThreads]
+  __shared__ float sq[2][K], sk[2][K], sg[2][K], sv[2][TC], srk[TC], dots[3];
   __shared__ int flag;
-  const int tid = threadIdx.x;
-  const int tile = blockIdx.x % p.tiles, bh = blockIdx.x / p.tiles;
-  const int h = bh % p.H, b = bh / p.H, c0 = tile * TC;
-  const int slot = p.slots ? p.slots[b] : b;
-  T *o = static_cast<T *>(p.o) + ((size_t)b * p.H + h) * p.V + c0;
-  if (slot < 0 || slot >= p.n_slots) {
-    if (tid < TC) o[tid] = from_f32<T>(0.f);
-    return;
-  }
-  const int col = (tid * 4) % TC, row = tid * 4 / TC;
-  float *s = p.state + (((size_t)slot * p.H + h) * K + row) * p.V + c0 + col;
-  float4 v[IT];
-#pragma unroll
-  for (int i = 0; i < IT; ++i)
-    v[i] = *reinterpret_cast<const float4 *>(s + (size_t)i * RG * p.V);
-
-  const T *q = static_cast<const T *>(p.q) + (size_t)b * p.q_stride + h * K;
-  const T *k = static_cast<const T *>(p.k) + (size_t)b * p.k_stride + h * K;
-  const T *vv = static_cast<const T *>(p.v) + (size_t)b * p.v_stride + h * p.V + c0;
+  // the threads' sums take the place of their first two pieces of the tile
+  __shared__ float4 spare[IT < 2 ? 2 * kThreads : 1];
+  const int tid = threadIdx.x, col = (tid * 4) % TC, row = tid * 4 / TC;
   const int channels = p.H * (2 * K + p.V);
-  T *conv = p.conv ? static_cast<T *>(p.conv) + (size_t)slot * (kTap - 1) * channels : nullptr;
-  const int cq = h * K, ck = p.H * K + h * K, cv = 2 * p.H * K + h * p.V + c0;
-  for (int i = tid; i < 2 * K + TC; i += kThreads) {
-    const T xn = i < K ? q[i] : i < 2 * K ? k[i - K] : vv[i - 2 * K];
-    float u = to_f32(xn);
-    if (conv) {
-      const int c = i < K ? cq + i : i < 2 * K ? ck + i - K : cv + i - 2 * K;
-      u = conv_token(conv + c, channels, *reinterpret_cast<const float4 *>(p.w + 4 * c), 0.f, u);
-      if (i >= 2 * K) shift_channel(conv + c, channels, xn);
-    }
-    (i < K ? sq[i] : i < 2 * K ? sk[i - K] : sv[i - 2 * K]) = u;
-  }
-  for (int i = tid; i < K; i += kThreads) sg[i] = expf(p.g[((size_t)b * p.H + h) * K + i]);
-  const float beta = p.beta[(size_t)b * p.H + h];
-  if (tid == 0) flag = 0;
-  __syncthreads();
-  if (conv) arrive(p.counters + (size_t)b * p.H + h, (uint32_t)p.tiles, &flag);
 
-  // sums of the decayed state against k and q, not yet normalised
-  float4 ak = make_float4(0.f, 0.f, 0.f, 0.f), aq = ak;
+  const int c0 = (blockIdx.x & (p.walk.tiles - 1)) * TC;
+  struct Unit {
+    Place at;
+    int slot;
+    Channel<T> ch[NC];
+    float g, beta;
+  };
+  // input and number of channel i of the unit: of q, of k, of the tile's
+  // columns of v
+  auto input = [&](const Unit &n, int i) {
+    return i < K ? static_cast<const T *>(p.q) + (size_t)n.at.b * p.q_stride + n.at.h * K + i
+           : i < 2 * K
+               ? static_cast<const T *>(p.k) + (size_t)n.at.b * p.k_stride + n.at.h * K + i - K
+               : static_cast<const T *>(p.v) + (size_t)n.at.b * p.v_stride + n.at.h * p.V + c0 +
+                     i - 2 * K;
+  };
+  auto channel = [&](const Unit &n, int i) {
+    return i < K ? n.at.h * K + i
+           : i < 2 * K ? p.H * K + n.at.h * K + i - K
+                       : 2 * p.H * K + n.at.h * p.V + c0 + i - 2 * K;
+  };
+  auto state_of = [&](const Unit &n) {
+    return p.state + (((size_t)n.slot * p.H + n.at.h) * K + row) * p.V + c0 + col;
+  };
+  auto conv_of = [&](const Unit &n) {
+    return p.conv ? static_cast<T *>(p.conv) + (size_t)n.slot * (kTap - 1) * channels : nullptr;
+  };
+  auto slot_of = [&](const Place &w) {
+    int s = -1;
+    if (w.b < p.walk.B) s = p.slots ? p.slots[w.b] : w.b;
+    return s < p.n_slots ? s : -1;
+  };
+  auto load = [&](Unit &n, const Place &at, int slot, int st) {
+    n.at = at;
+    n.slot = slot;
+    if (slot >= 0) {
+      const float *s = state_of(n);
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int r = row + i * RG;
-    const float e = sg[r], kn = sk[r], qn = sq[r];
-    v[i].x *= e; v[i].y *= e; v[i].z *= e; v[i].w *= e;
-    ak.x += kn * v[i].x; ak.y += kn * v[i].y; ak.z += kn * v[i].z; ak.w += kn * v[i].w;
-    aq.x += qn * v[i].x; aq.y += qn * v[i].y; aq.z += qn * v[i].z; aq.w += qn * v[i].w;
-  }
-  *reinterpret_cast<float4 *>(&rk[row][col]) = ak;
-  *reinterpret_cast<float4 *>(&rq[row][col]) = aq;
-  if (tid >= kThreads - 32) {   // |q|^2, |k|^2, q . k
-    float n[3] = {0.f, 0.f, 0.f};
-    for (int i = tid & 31; i < K; i += 32) {
-      n[0] += sq[i] * sq[i];
-      n[1] += sk[i] * sk[i];
-      n[2] += sq[i] * sk[i];
+      for (int i = 0; i < IT; ++i)
+        cp_async16(stage + (st * IT + i) * kThreads + tid, s + (size_t)i * RG * p.V);
+      const T *conv = conv_of(n);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const int i = tid + k * kThreads;
+        if (i < CH) {
+          const int c = channel(n, i);
+          n.ch[k].load(input(n, i), conv ? conv + c : nullptr, channels, p.w + 4 * (size_t)c,
+                       nullptr);
+        }
+      }
+      const size_t bh = (size_t)at.b * p.H + at.h;
+      if (tid < K) n.g = p.g[bh * K + tid];
+      n.beta = p.beta[bh];
     }
-#pragma unroll
-    for (int off = 16; off; off >>= 1)
-#pragma unroll
-      for (int j = 0; j < 3; ++j) n[j] += __shfl_xor_sync(0xffffffffu, n[j], off);
-    if ((tid & 31) < 3) dots[tid & 31] = (tid & 31) == 0 ? n[0] : (tid & 31) == 1 ? n[1] : n[2];
-  }
-  __syncthreads();
-  if (flag) {
-    for (int i = tid; i < 2 * K; i += kThreads)
-      shift_channel(conv + (i < K ? cq + i : ck + i - K), channels, i < K ? q[i] : k[i - K]);
-  }
-  const float nq = p.l2norm ? rsqrtf(dots[0] + 1e-6f) : 1.f;
-  const float nk = p.l2norm ? rsqrtf(dots[1] + 1e-6f) : 1.f;
-  if (tid < TC) {
-    float ks = 0.f, qs = 0.f;
-#pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      ks += rk[r][tid];
-      qs += rq[r][tid];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto work = [&](const Unit &now, int st) {
+    T *o = static_cast<T *>(p.o) + ((size_t)now.at.b * p.H + now.at.h) * p.V + c0;
+    if (now.slot < 0) {           // idle (uniform)
+      if (tid < TC) o[tid] = from_f32<T>(0.f);
+      return;
     }
-    const float br = beta * (sv[tid] - nk * ks);     // beta times the residual
-    srk[tid] = nk * br;
-    o[tid] = from_f32<T>(p.scale * nq * (qs + nk * dots[2] * br));
-  }
-  __syncthreads();
-  const float4 r4 = *reinterpret_cast<const float4 *>(&srk[col]);
+    T *conv = conv_of(now);
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const float kn = sk[row + i * RG];
-    v[i].x += kn * r4.x; v[i].y += kn * r4.y; v[i].z += kn * r4.z; v[i].w += kn * r4.w;
-    *reinterpret_cast<float4 *>(s + (size_t)i * RG * p.V) = v[i];
+    for (int k = 0; k < NC; ++k) {
+      const int i = tid + k * kThreads;
+      if (i < CH) {
+        const float v = conv ? now.ch[k].value() : to_f32(now.ch[k].x);
+        (i < K ? sq[st][i] : i < 2 * K ? sk[st][i - K] : sv[st][i - 2 * K]) = v;
+        if (conv && i >= 2 * K) now.ch[k].shift(conv + channel(now, i), channels);
+      }
+    }
+    if (tid < K) sg[st][tid] = expf(now.g);
+    if (tid == 0) flag = 0;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+
+    if (conv)
+      arrive(p.counters + (size_t)now.at.b * p.H + now.at.h, (uint32_t)p.walk.tiles, &flag);
+
+    // sums of the decayed state against k and q, not yet normalised
+    float4 ak = make_float4(0.f, 0.f, 0.f, 0.f), aq = ak, v[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int r = row + i * RG;
+      const float e = sg[st][r], kn = sk[st][r], qn = sq[st][r];
+      v[i] = stage[(st * IT + i) * kThreads + tid];
+      v[i].x *= e; v[i].y *= e; v[i].z *= e; v[i].w *= e;
+      ak.x += kn * v[i].x; ak.y += kn * v[i].y; ak.z += kn * v[i].z; ak.w += kn * v[i].w;
+      aq.x += qn * v[i].x; aq.y += qn * v[i].y; aq.z += qn * v[i].z; aq.w += qn * v[i].w;
+    }
+    float4 *sums = IT < 2 ? spare : stage + st * IT * kThreads;   // [2][RG][TC]
+    sums[tid] = ak;
+    sums[kThreads + tid] = aq;
+    if (tid >= kThreads - 32) {   // |q|^2, |k|^2, q . k
+      float n[3] = {0.f, 0.f, 0.f};
+      for (int i = tid & 31; i < K; i += 32) {
+        n[0] += sq[st][i] * sq[st][i];
+        n[1] += sk[st][i] * sk[st][i];
+        n[2] += sq[st][i] * sk[st][i];
+      }
+#pragma unroll
+      for (int off = 16; off; off >>= 1)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) n[j] += __shfl_xor_sync(0xffffffffu, n[j], off);
+      if ((tid & 31) < 3) dots[tid & 31] = (tid & 31) == 0 ? n[0] : (tid & 31) == 1 ? n[1] : n[2];
+    }
+    __syncthreads();
+    if (flag) {   // the last tile of the head: its q and k channels
+      for (int i = tid; i < 2 * K; i += kThreads)
+        shift_channel(conv + channel(now, i), channels, *input(now, i));
+    }
+    const float nq = p.l2norm ? rsqrtf(dots[0] + 1e-6f) : 1.f;
+    const float nk = p.l2norm ? rsqrtf(dots[1] + 1e-6f) : 1.f;
+    if (tid < TC) {
+      float ks = 0.f, qs = 0.f;
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        ks += reinterpret_cast<const float *>(sums)[r * TC + tid];
+        qs += reinterpret_cast<const float *>(sums + kThreads)[r * TC + tid];
+      }
+      const float br = now.beta * (sv[st][tid] - nk * ks);     // beta times the residual
+      srk[tid] = nk * br;
+      o[tid] = from_f32<T>(p.scale * nq * (qs + nk * dots[2] * br));
+    }
+    __syncthreads();
+    const float4 r4 = *reinterpret_cast<const float4 *>(&srk[col]);
+    float *s = state_of(now);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const float kn = sk[st][row + i * RG];
+      v[i].x += kn * r4.x; v[i].y += kn * r4.y; v[i].z += kn * r4.z; v[i].w += kn * r4.w;
+      *reinterpret_cast<float4 *>(s + (size_t)i * RG * p.V) = v[i];
+    }
+  };
+
+  // the slot is read two units ahead, the rest one
+  Unit u0, u1;
+  Place at = {(int)(blockIdx.x >> p.walk.log_tiles) / p.H,
+              (int)(blockIdx.x >> p.walk.log_tiles) % p.H};
+  load(u0, at, slot_of(at), 0);
+  at.advance(p.walk);
+  int slot = slot_of(at);
+  auto next = [&](Unit &n, int st) {
+    const Place here = at;
+    const int s = slot;
+    at.advance(p.walk);
+    slot = slot_of(at);
+    load(n, here, s, st);
+  };
+  while (true) {
+    next(u1, 1);
+    work(u0, 0);
+    if (u1.at.b >= p.walk.B) break;
+    next(u0, 0);
+    work(u1, 1);
+    if (u0.at.b >= p.walk.B) break;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Columns per CTA: 32 while that leaves no more than two CTAs for each SM,
-// else up to 64 (a tile of 32 KB at 128 keys: four CTAs fit an SM).
-int tile_for(int B, int H, int cols) {
+// Columns per unit: 32 while that leaves no more than two units for each SM,
+// else up to 64 (a tile of 32 KB at 128 keys).
+int tile_for(int B, int H, int cols, int sms) {
   const long long small = (long long)B * H * (cols / 32);
-  return small <= 2ll * num_sms() || cols == 32 ? 32 : 64;
+  return small <= 2ll * sms || cols == 32 ? 32 : 64;
+}
+
+// Three CTAs fit an SM (registers, and two staged tiles each).
+template <typename K, typename P>
+cudaError_t launch(K kern, P &p, int B, int keys, int cols, int tc, int sms, cudaStream_t cs) {
+  const int tiles = cols / tc;
+  const long long units = (long long)B * p.H * tiles;
+  const int most = 3 * sms / tiles * tiles;
+  const int grid = (int)(units < most ? units : most), pairs = grid / tiles;
+  p.walk = {p.H, B, pairs / p.H, pairs % p.H, tiles, tiles == 1 ? 0 : tiles == 2 ? 1 : 2};
+  const size_t smem = (size_t)2 * keys * tc * sizeof(float);
+  if (smem > 16 * 1024) {   // with the static arrays, above the default 48 KB
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)grid, kThreads, smem, cs>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T, int N>
 cudaError_t launch_ssm_step(SsmStepParams p, int B, cudaStream_t cs) {
-  const int tc = tile_for(B, p.H, p.P);
-  p.tiles = p.P / tc;
-  const unsigned grid = (unsigned)(B * p.H * p.tiles);
-  if (tc == 32) ssm_step_kernel<T, N, 32><<<grid, kThreads, 0, cs>>>(p);
-  else ssm_step_kernel<T, N, 64><<<grid, kThreads, 0, cs>>>(p);
-  return cudaGetLastError();
+  const int sms = num_sms(), tc = tile_for(B, p.H, p.P, sms);
+  p.inv_hpg = (float)p.G / (float)p.H;
+  return tc == 32 ? launch(ssm_step_kernel<T, N, 32>, p, B, N, p.P, 32, sms, cs)
+                  : launch(ssm_step_kernel<T, N, 64>, p, B, N, p.P, 64, sms, cs);
 }
 
 template <typename T, int K>
 cudaError_t launch_kda_step(KdaStepParams p, int B, cudaStream_t cs) {
-  const int tc = tile_for(B, p.H, p.V);
-  p.tiles = p.V / tc;
-  const unsigned grid = (unsigned)(B * p.H * p.tiles);
-  if (tc == 32) kda_step_kernel<T, K, 32><<<grid, kThreads, 0, cs>>>(p);
-  else kda_step_kernel<T, K, 64><<<grid, kThreads, 0, cs>>>(p);
-  return cudaGetLastError();
+  const int sms = num_sms(), tc = tile_for(B, p.H, p.V, sms);
+  return tc == 32 ? launch(kda_step_kernel<T, K, 32>, p, B, K, p.V, 32, sms, cs)
+                  : launch(kda_step_kernel<T, K, 64>, p, B, K, p.V, 64, sms, cs);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
