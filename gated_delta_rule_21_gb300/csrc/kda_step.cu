@@ -100,12 +100,16 @@ struct Channel {
     cache[2 * stride] = x;
   }
 };
-// Moves a channel that other CTAs have read too.
-template <typename T>
-__device__ __forceinline__ void shift_channel(T *cache, size_t stride, T x) {
-  cache[0] = cache[stride];
-  cache[stride] = cache[2 * stride];
-  cache[2 * stride] = x;
+// Sums of `v` over the threads of a warp that own the same columns.
+template <int TC>
+__device__ __forceinline__ void sum_rows(float4 &v) {
+#pragma unroll
+  for (int off = TC / 4; off < 32; off <<= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, off);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, off);
+  }
 }
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(const SsmStepPara
   constexpr int IT = N * TC / kWave, RG = kWave / TC, CH = 2 * N + TC;
   constexpr int NC = (CH + kThreads - 1) / kThreads;      // channels per thread
   extern __shared__ __align__(16) float4 stage[];         // [2][IT][kThreads]
-  __shared__ float sB[2][N], sC[2][N], sx[2][TC], red[RG][TC];
+  __shared__ float sB[2][N], sC[2][N], sx[2][TC], red[kThreads / 32][TC];
   __shared__ int flag;
   const int tid = threadIdx.x, col = (tid * 4) % TC, row = tid * 4 / TC;
 
@@ -232,19 +236,19 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(const SsmStepPara
       acc.z += cn * v.z;
       acc.w += cn * v.w;
     }
-    *reinterpret_cast<float4 *>(&red[row][col]) = acc;
+    sum_rows<TC>(acc);
+    if ((tid & 31) < TC / 4) *reinterpret_cast<float4 *>(&red[tid >> 5][col]) = acc;
     __syncthreads();
     if (flag) {   // the last of the group: its B and C channels
-      const T *x = static_cast<const T *>(p.xbc) + (size_t)now.at.b * p.xbc_stride;
-      for (int i = tid; i < 2 * N; i += kThreads) {
-        const int c = channel(now, i);
-        shift_channel(conv + c, p.channels, x[c]);
-      }
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        if (tid + k * kThreads < 2 * N)
+          now.ch[k].shift(conv + channel(now, tid + k * kThreads), p.channels);
     }
     if (tid < TC) {
       float o = 0.f;
 #pragma unroll
-      for (int r = 0; r < RG; ++r) o += red[r][tid];
+      for (int r = 0; r < kThreads / 32; ++r) o += red[r][tid];
       if (p.D) o += p.D[now.at.h] * sx[st][tid];
       if (p.z) o *= silu(now.z);
       y[tid] = from_f32<T>(o);
@@ -295,10 +299,9 @@ __global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepPara
   constexpr int IT = K * TC / kWave, RG = kWave / TC, CH = 2 * K + TC;
   constexpr int NC = (CH + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) float4 stage[];         // [2][IT][kThreads]
-  __shared__ float sq[2][K], sk[2][K], sg[2][K], sv[2][TC], srk[TC], dots[3];
-  __shared__ int flag;
-  // the threads' sums take the place of their first two pieces of the tile
-  __shared__ float4 spare[IT < 2 ? 2 * kThreads : 1];
+  __shared__ float sq[2][K], sk[2][K], sg[2][K], sv[2][TC], dots[3];
+  __shared__ float4 sums[2][kThreads / 32][TC / 4];
+  __shared__ int flag[2];
   const int tid = threadIdx.x, col = (tid * 4) % TC, row = tid * 4 / TC;
   const int channels = p.H * (2 * K + p.V);
 
@@ -375,27 +378,30 @@ __global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepPara
       }
     }
     if (tid < K) sg[st][tid] = expf(now.g);
-    if (tid == 0) flag = 0;
+    if (tid == 0) flag[st] = 0;
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
 
     if (conv)
-      arrive(p.counters + (size_t)now.at.b * p.H + now.at.h, (uint32_t)p.walk.tiles, &flag);
+      arrive(p.counters + (size_t)now.at.b * p.H + now.at.h, (uint32_t)p.walk.tiles, &flag[st]);
 
     // sums of the decayed state against k and q, not yet normalised
-    float4 ak = make_float4(0.f, 0.f, 0.f, 0.f), aq = ak, v[IT];
+    float4 ak = make_float4(0.f, 0.f, 0.f, 0.f), aq = ak;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int r = row + i * RG;
       const float e = sg[st][r], kn = sk[st][r], qn = sq[st][r];
-      v[i] = stage[(st * IT + i) * kThreads + tid];
-      v[i].x *= e; v[i].y *= e; v[i].z *= e; v[i].w *= e;
-      ak.x += kn * v[i].x; ak.y += kn * v[i].y; ak.z += kn * v[i].z; ak.w += kn * v[i].w;
-      aq.x += qn * v[i].x; aq.y += qn * v[i].y; aq.z += qn * v[i].z; aq.w += qn * v[i].w;
+      const float4 v = stage[(st * IT + i) * kThreads + tid];
+      const float ek = e * kn, eq = e * qn;
+      ak.x += ek * v.x; ak.y += ek * v.y; ak.z += ek * v.z; ak.w += ek * v.w;
+      aq.x += eq * v.x; aq.y += eq * v.y; aq.z += eq * v.z; aq.w += eq * v.w;
     }
-    float4 *sums = IT < 2 ? spare : stage + st * IT * kThreads;   // [2][RG][TC]
-    sums[tid] = ak;
-    sums[kThreads + tid] = aq;
+    sum_rows<TC>(ak);
+    sum_rows<TC>(aq);
+    if ((tid & 31) < TC / 4) {
+      sums[0][tid >> 5][col / 4] = ak;
+      sums[1][tid >> 5][col / 4] = aq;
+    }
     if (tid >= kThreads - 32) {   // |q|^2, |k|^2, q . k
       float n[3] = {0.f, 0.f, 0.f};
       for (int i = tid & 31; i < K; i += 32) {
@@ -410,31 +416,43 @@ __global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepPara
       if ((tid & 31) < 3) dots[tid & 31] = (tid & 31) == 0 ? n[0] : (tid & 31) == 1 ? n[1] : n[2];
     }
     __syncthreads();
-    if (flag) {   // the last tile of the head: its q and k channels
-      for (int i = tid; i < 2 * K; i += kThreads)
-        shift_channel(conv + channel(now, i), channels, *input(now, i));
-    }
     const float nq = p.l2norm ? rsqrtf(dots[0] + 1e-6f) : 1.f;
     const float nk = p.l2norm ? rsqrtf(dots[1] + 1e-6f) : 1.f;
-    if (tid < TC) {
-      float ks = 0.f, qs = 0.f;
+    // every thread adds the sums of its own columns: no barrier after this
+    ak = aq = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int r = 0; r < RG; ++r) {
-        ks += reinterpret_cast<const float *>(sums)[r * TC + tid];
-        qs += reinterpret_cast<const float *>(sums + kThreads)[r * TC + tid];
-      }
-      const float br = now.beta * (sv[st][tid] - nk * ks);     // beta times the residual
-      srk[tid] = nk * br;
-      o[tid] = from_f32<T>(p.scale * nq * (qs + nk * dots[2] * br));
+    for (int r = 0; r < kThreads / 32; ++r) {
+      const float4 a = sums[0][r][col / 4], q = sums[1][r][col / 4];
+      ak.x += a.x; ak.y += a.y; ak.z += a.z; ak.w += a.w;
+      aq.x += q.x; aq.y += q.y; aq.z += q.z; aq.w += q.w;
     }
-    __syncthreads();
-    const float4 r4 = *reinterpret_cast<const float4 *>(&srk[col]);
+    const float4 v4 = *reinterpret_cast<const float4 *>(&sv[st][col]);
+    // nk times beta times the residual
+    const float bk = now.beta * nk, qk = p.scale * nq * dots[2], qs = p.scale * nq;
+    const float4 r4 = make_float4(bk * (v4.x - nk * ak.x), bk * (v4.y - nk * ak.y),
+                                  bk * (v4.z - nk * ak.z), bk * (v4.w - nk * ak.w));
+    if (row == 0) {
+      o[col] = from_f32<T>(qs * aq.x + qk * r4.x);
+      o[col + 1] = from_f32<T>(qs * aq.y + qk * r4.y);
+      o[col + 2] = from_f32<T>(qs * aq.z + qk * r4.z);
+      o[col + 3] = from_f32<T>(qs * aq.w + qk * r4.w);
+    }
     float *s = state_of(now);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const float kn = sk[st][row + i * RG];
-      v[i].x += kn * r4.x; v[i].y += kn * r4.y; v[i].z += kn * r4.z; v[i].w += kn * r4.w;
-      *reinterpret_cast<float4 *>(s + (size_t)i * RG * p.V) = v[i];
+      const float kn = sk[st][row + i * RG], e = sg[st][row + i * RG];
+      float4 v = stage[(st * IT + i) * kThreads + tid];   // (its registers are worth more)
+      v.x = e * v.x + kn * r4.x;
+      v.y = e * v.y + kn * r4.y;
+      v.z = e * v.z + kn * r4.z;
+      v.w = e * v.w + kn * r4.w;
+      *reinterpret_cast<float4 *>(s + (size_t)i * RG * p.V) = v;
+    }
+    if (flag[st]) {   // the last tile of the head: its q and k channels
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        if (tid + k * kThreads < 2 * K)
+          now.ch[k].shift(conv + channel(now, tid + k * kThreads), channels);
     }
   };
 
