@@ -26,6 +26,7 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -602,39 +603,62 @@ def clear_device_status(workspace, stream=None) -> None:
 
 # ---------------------------------------------------------------------------
 # one token per sequence, the state space operator, the norms around a block
+#
+# Single-token calls take a few microseconds on the GPU, so the host side of
+# these calls is kept short: descriptors are made once per shape, a tensor is
+# checked by four attribute reads, and messages are made only to be raised.
+
+_f32, _i32 = torch.float32, torch.int32
 
 
-def _data(t, name, shape, dtype, device, contiguous=True):
-    """Address of an optional tensor, checked."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _lib_now():
+    return _lib if _lib is not None else lib()
+
+
+def _refuse(t, name, shape, dtype, device, contiguous):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _at(t, name, shape, dtype, device):
+    """Address of a contiguous tensor of this shape, or None for None."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == device):
+        _refuse(t, name, shape, dtype, device, True)
     return t.data_ptr()
 
 
-def _inner(t, name, dims):
-    """The last ``dims`` dimensions of ``t`` must be contiguous; the outer
-    ones may have any stride."""
+def _rows(t, name, shape, dtype, device):
+    """Address and row stride of a tensor whose dimensions after the first
+    are contiguous (the rows may be slices of something wider)."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device):
+        _refuse(t, name, shape, dtype, device, False)
+    st = t.stride()
     n = 1
-    for size, stride in zip(reversed(t.shape[-dims:]), reversed(t.stride()[-dims:])):
-        if size != 1 and stride != n:
-            raise ValueError(f"the last {dims} dimension(s) of {name} must be contiguous")
-        n *= size
+    for d in range(len(shape) - 1, 0, -1):
+        if st[d] != n and shape[d] != 1:
+            raise ValueError(f"the dimensions of {name} after the first must be contiguous")
+        n *= shape[d]
+    return t.data_ptr(), st[0]
 
 
-def _cuda(t, where):
+def _start(t, where):
+    """Device index and dtype of a call's first tensor."""
     if not t.is_cuda:
         raise ValueError(f"{where} needs CUDA tensors")
     if t.dtype not in DTYPES:
         raise TypeError(f"{where}: dtype must be float32 or bfloat16, got {t.dtype}")
-    return t.device, t.dtype
+    return t.get_device(), t.dtype
 
 
 def _scratch(workspace, need, device, where, zeros):
@@ -645,13 +669,35 @@ def _scratch(workspace, need, device, where, zeros):
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if zeros:
             workspace[:zeros].zero_()
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace, workspace.numel() * workspace.element_size()
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape_ref(*fields):
+    return ctypes.byref(kda_shape(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _ssm_ref(*fields):
+    return ctypes.byref(kda_ssm_shape(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_ref(*fields):
+    return ctypes.byref(kda_norm_desc(*fields))
 
 
 def step_workspace_size(B, H) -> int:
@@ -679,35 +725,36 @@ def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_stat
     sequence, whose output is 0).  With ``conv_w`` (as short_conv_silu) and
     ``conv_state`` [n_slots,3,H*(2K+V)] (moved on in place) q, k, v are the
     inputs of the convolution.  Returns o [B,H,V]."""
-    dev, dt = _cuda(q, "step")
+    dev, dt = _start(q, "step")
     B, H, K = q.shape
     V = v.shape[-1]
-    n_slots = state.shape[0]
-    for t, name, width in ((q, "q", K), (k, "k", K), (v, "v", V)):
-        _data(t, name, (B, H, width), dt, dev, False)
-        _inner(t, name, 2)
-    f32 = torch.float32
-    if conv_w is not None and conv_w.numel() == 4 * H * (2 * K + V):
-        conv_w = conv_w.view(-1, 4)
-    o = torch.empty((B, H, V), dtype=dt, device=dev) if out is None else out
+    n_slots, C = state.shape[0], H * (2 * K + V)
+    qp, qs = _rows(q, "q", (B, H, K), dt, dev)
+    kp, ks = _rows(k, "k", (B, H, K), dt, dev)
+    vp, vs = _rows(v, "v", (B, H, V), dt, dev)
+    wp = None
+    if conv_w is not None:
+        if conv_w.numel() != 4 * C or not conv_w.is_contiguous():
+            raise ValueError(f"conv_w must be contiguous with 4*{C} elements")
+        wp = _at(conv_w, "conv_w", conv_w.shape, _f32, dev)
+    o = v.new_empty((B, H, V)) if out is None else out
     ws, n = _scratch(workspace, step_workspace_size(B, H) if workspace is None else 0, dev,
                      "kda_step_workspace_size", 1 << 40)
-    st = lib().kda_step(
-        kda_shape(B, 1, H, K, V, DTYPES[dt]), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        q.stride(0), k.stride(0), v.stride(0), _data(g, "g", (B, H, K), f32, dev),
-        _data(beta, "beta", (B, H), f32, dev), K ** -0.5 if scale is None else float(scale),
-        _data(conv_w, "conv_w", (H * (2 * K + V), 4), f32, dev),
-        _data(conv_state, "conv_state", (n_slots, 3, H * (2 * K + V)), dt, dev), int(l2norm_qk),
-        _data(slots, "slots", (B,), torch.int32, dev), n_slots,
-        _data(state, "state", (n_slots, H, K, V), f32, dev), _data(o, "out", (B, H, V), dt, dev),
+    st = _lib_now().kda_step(
+        _shape_ref(B, 1, H, K, V, DTYPES[dt]), qp, kp, vp, qs, ks, vs,
+        _at(g, "g", (B, H, K), _f32, dev), _at(beta, "beta", (B, H), _f32, dev),
+        K ** -0.5 if scale is None else scale, wp,
+        _at(conv_state, "conv_state", (n_slots, 3, C), dt, dev), 1 if l2norm_qk else 0,
+        _at(slots, "slots", (B,), _i32, dev), n_slots,
+        _at(state, "state", (n_slots, H, K, V), _f32, dev), _at(o, "out", (B, H, V), dt, dev),
         ws.data_ptr(), n, _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_step")
     return o
 
 
-def _ssm_dims(xbc, dt, A, head_dim, state_dim):
-    H, P, N = A.numel(), int(head_dim), int(state_dim)
+def _ssm_dims(xbc, A, head_dim, state_dim):
+    H, P, N = A.numel(), head_dim, state_dim
     C = xbc.shape[-1]
     groups, rest = divmod(C - H * P, 2 * N)
     if rest or groups < 1:
@@ -728,6 +775,16 @@ def alloc_ssm_workspace(B, T, H, P, N, G, dtype=torch.bfloat16, impl="auto",
                     "kda_ssm_fwd_workspace_size", 256)[0]
 
 
+def _tokens(t, name, shape, dtype, device):
+    """Address and strides of a [B,T,width] tensor with contiguous channels."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device):
+        _refuse(t, name, shape, dtype, device, False)
+    st = t.stride()
+    if st[2] != 1 and shape[2] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
 def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=None, D=None,
             z=None, initial_state=None, conv_state=None, segment_ids=None,
             output_final_state=False, out=None, workspace=None, impl="auto", stream=None):
@@ -739,35 +796,30 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     [H], all fp32; initial_state: [B,H,N,P] fp32; conv_state: [B,3,channels].
     Returns ``(y [B,T,H,P], final_state, conv_state_out)``, the last two None
     unless ``output_final_state``."""
-    dev, ty = _cuda(xbc, "ssm_fwd")
+    dev, ty = _start(xbc, "ssm_fwd")
     B, T, _ = xbc.shape
-    H, P, N, G, C = _ssm_dims(xbc, dt, A, head_dim, state_dim)
-    f32 = torch.float32
-    for t, name, width in ((xbc, "xbc", C), (dt, "dt", H), (z, "z", H * P)):
-        if t is not None:
-            _data(t, name, (B, T, width), ty, dev, False)
-            _inner(t, name, 1)
-    y = torch.empty((B, T, H, P), dtype=ty, device=dev) if out is None else out
-    fs = conv = None
+    H, P, N, G, C = _ssm_dims(xbc, A, head_dim, state_dim)
+    xp, xb, xt = _tokens(xbc, "xbc", (B, T, C), ty, dev)
+    dp, db, dtt = _tokens(dt, "dt", (B, T, H), ty, dev)
+    zp, zb, zt = (None, 0, 0) if z is None else _tokens(z, "z", (B, T, H * P), ty, dev)
+    y = xbc.new_empty((B, T, H, P)) if out is None else out
+    fs = conv = fp = cp = None
     if output_final_state:
-        fs = torch.empty((B, H, N, P), dtype=f32, device=dev)
-        conv = torch.empty((B, 3, C), dtype=ty, device=dev)
-    zs = z.stride() if z is not None else (0, 0)
-    xs, ds = xbc.stride(), dt.stride()
-    s = kda_ssm_shape(B, T, H, P, N, G, DTYPES[ty], xs[0], xs[1], zs[0], zs[1], ds[0], ds[1])
-    ws, n = _scratch(workspace, lib().kda_ssm_fwd_workspace_size(s, IMPLS[impl])
-                     if workspace is None else 0, dev, "kda_ssm_fwd_workspace_size", 256)
-    st = lib().kda_ssm_fwd(
-        s, xbc.data_ptr(), dt.data_ptr(), None if z is None else z.data_ptr(),
-        _data(conv_w, "conv_w", (C, 4), f32, dev), _data(conv_bias, "conv_bias", (C,), f32, dev),
-        _data(A, "A", (H,), f32, dev), _data(D, "D", (H,), f32, dev),
-        _data(dt_bias, "dt_bias", (H,), f32, dev),
-        _data(initial_state, "initial_state", (B, H, N, P), f32, dev),
-        _data(conv_state, "conv_state", (B, 3, C), ty, dev),
-        _data(segment_ids, "segment_ids", (B, T), torch.int32, dev),
-        _data(y, "out", (B, T, H, P), ty, dev), None if fs is None else fs.data_ptr(),
-        None if conv is None else conv.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
-        _raw_stream(stream, dev))
+        fs = A.new_empty((B, H, N, P))
+        conv = xbc.new_empty((B, 3, C))
+        fp, cp = fs.data_ptr(), conv.data_ptr()
+    s = _ssm_ref(B, T, H, P, N, G, DTYPES[ty], xb, xt, zb, zt, db, dtt)
+    L, way, one = _lib_now(), IMPLS[impl], (H,)
+    ws, n = _scratch(workspace, L.kda_ssm_fwd_workspace_size(s, way) if workspace is None else 0,
+                     dev, "kda_ssm_fwd_workspace_size", 256)
+    st = L.kda_ssm_fwd(
+        s, xp, dp, zp, _at(conv_w, "conv_w", (C, 4), _f32, dev),
+        _at(conv_bias, "conv_bias", (C,), _f32, dev), _at(A, "A", one, _f32, dev),
+        _at(D, "D", one, _f32, dev), _at(dt_bias, "dt_bias", one, _f32, dev),
+        _at(initial_state, "initial_state", (B, H, N, P), _f32, dev),
+        _at(conv_state, "conv_state", (B, 3, C), ty, dev),
+        _at(segment_ids, "segment_ids", (B, T), _i32, dev), _at(y, "out", (B, T, H, P), ty, dev),
+        fp, cp, ws.data_ptr(), n, way, _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_ssm_fwd")
     return y, fs, conv
@@ -779,26 +831,23 @@ def ssm_step(xbc, dt, conv_w, A, state, conv_state, *, head_dim, state_dim, conv
     states: xbc [B,H*P+2*G*N], z [B,H*P] or None, dt [B,H] (any stride between
     the rows); state [n_slots,H,N,P] fp32 and conv_state [n_slots,3,channels]
     are moved on in place; ``slots`` as :func:`step`.  Returns y [B,H,P]."""
-    dev, ty = _cuda(xbc, "ssm_step")
+    dev, ty = _start(xbc, "ssm_step")
     B = xbc.shape[0]
-    H, P, N, G, C = _ssm_dims(xbc, dt, A, head_dim, state_dim)
-    f32, n_slots = torch.float32, state.shape[0]
-    for t, name, width in ((xbc, "xbc", C), (dt, "dt", H), (z, "z", H * P)):
-        if t is not None:
-            _data(t, name, (B, width), ty, dev, False)
-            _inner(t, name, 1)
-    y = torch.empty((B, H, P), dtype=ty, device=dev) if out is None else out
+    H, P, N, G, C = _ssm_dims(xbc, A, head_dim, state_dim)
+    n_slots, one = state.shape[0], (H,)
+    xp, xs = _rows(xbc, "xbc", (B, C), ty, dev)
+    dp, ds = _rows(dt, "dt", (B, H), ty, dev)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", (B, H * P), ty, dev)
+    y = xbc.new_empty((B, H, P)) if out is None else out
     ws, n = _scratch(workspace, step_workspace_size(B, H) if workspace is None else 0, dev,
                      "kda_step_workspace_size", 1 << 40)
-    s = kda_ssm_shape(B, 1, H, P, N, G, DTYPES[ty], xbc.stride(0), 0,
-                      0 if z is None else z.stride(0), 0, dt.stride(0), 0)
-    st = lib().kda_ssm_step(
-        s, xbc.data_ptr(), dt.data_ptr(), None if z is None else z.data_ptr(),
-        _data(conv_w, "conv_w", (C, 4), f32, dev), _data(conv_bias, "conv_bias", (C,), f32, dev),
-        _data(A, "A", (H,), f32, dev), _data(D, "D", (H,), f32, dev),
-        _data(dt_bias, "dt_bias", (H,), f32, dev), _data(slots, "slots", (B,), torch.int32, dev),
-        n_slots, _data(conv_state, "conv_state", (n_slots, 3, C), ty, dev),
-        _data(state, "state", (n_slots, H, N, P), f32, dev), _data(y, "out", (B, H, P), ty, dev),
+    st = _lib_now().kda_ssm_step(
+        _ssm_ref(B, 1, H, P, N, G, DTYPES[ty], xs, 0, zs, 0, ds, 0), xp, dp, zp,
+        _at(conv_w, "conv_w", (C, 4), _f32, dev), _at(conv_bias, "conv_bias", (C,), _f32, dev),
+        _at(A, "A", one, _f32, dev), _at(D, "D", one, _f32, dev),
+        _at(dt_bias, "dt_bias", one, _f32, dev), _at(slots, "slots", (B,), _i32, dev), n_slots,
+        _at(conv_state, "conv_state", (n_slots, 3, C), ty, dev),
+        _at(state, "state", (n_slots, H, N, P), _f32, dev), _at(y, "out", (B, H, P), ty, dev),
         ws.data_ptr(), n, _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_ssm_step")
@@ -809,17 +858,19 @@ GATE_ACTS = {"none": 0, "sigmoid": 1, "silu": 2, "tanh": 3}
 
 
 def _norm_desc(y, gate, gate_act, scale, eps):
-    D = y.shape[-1]
-    if D == 0 or y.numel() == 0:
+    D, n = y.shape[-1], y.numel()
+    if n == 0:
         raise ValueError("y must not be empty")
-    rows = y.numel() // D
-    grows = gate.numel() // D if gate is not None else 0
-    if gate is not None and (gate.shape[-1] != D or grows == 0 or rows % grows):
-        raise ValueError(f"gate {tuple(gate.shape)} does not divide the rows of {tuple(y.shape)}")
-    if gate_act not in GATE_ACTS:
+    rows, grows = n // D, 0
+    if gate is not None:
+        grows = gate.numel() // D
+        if gate.shape[-1] != D or grows == 0 or rows % grows:
+            raise ValueError(
+                f"gate {tuple(gate.shape)} does not divide the rows of {tuple(y.shape)}")
+    act = GATE_ACTS.get(gate_act)
+    if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}, got {gate_act!r}")
-    return kda_norm_desc(rows, D, DTYPES[y.dtype], GATE_ACTS[gate_act], grows, float(scale),
-                         float(eps)), rows, D
+    return _norm_ref(rows, D, DTYPES[y.dtype], act, grows, scale, eps), rows, (D,)
 
 
 def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale=1.0, w_pre=None,
@@ -833,19 +884,24 @@ def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale
     consecutive rows); w_post, w_pre: [D] fp32.  residual, gate and w_pre may be
     None.  ``out`` may be the residual itself.  Returns ``(out, x or None)``, and
     the statistics block_norm_bwd reads when ``save_stats``."""
-    dev, ty = _cuda(y, "block_norm")
-    d, rows, D = _norm_desc(y, gate, gate_act, scale, eps)
-    f32 = torch.float32
+    dev, ty = _start(y, "block_norm")
+    shape = y.shape
+    d, rows, width = _norm_desc(y, gate, gate_act, scale, eps)
+    yp = _at(y, "y", shape, ty, dev)
     if out is None:
-        out = torch.empty(y.shape, dtype=ty, device=dev)
-    x = torch.empty(y.shape, dtype=ty, device=dev) if w_pre is not None else None
-    stats = torch.empty((2, rows), dtype=f32, device=dev) if save_stats else None
-    st = lib().kda_block_norm_fwd(
-        d, _data(y, "y", y.shape, ty, dev), _data(w_post, "w_post", (D,), f32, dev),
-        _data(residual, "residual", y.shape, ty, dev),
-        None if gate is None else _data(gate, "gate", gate.shape, ty, dev),
-        _data(w_pre, "w_pre", (D,), f32, dev), _data(out, "out", y.shape, ty, dev),
-        None if x is None else x.data_ptr(), None if stats is None else stats.data_ptr(),
+        out = torch.empty_like(y)
+    x = stats = xp = sp = None
+    if w_pre is not None:
+        x = torch.empty_like(y)
+        xp = x.data_ptr()
+    if save_stats:
+        stats = w_post.new_empty((2, rows))
+        sp = stats.data_ptr()
+    st = _lib_now().kda_block_norm_fwd(
+        d, yp, _at(w_post, "w_post", width, _f32, dev),
+        _at(residual, "residual", shape, ty, dev),
+        None if gate is None else _at(gate, "gate", gate.shape, ty, dev),
+        _at(w_pre, "w_pre", width, _f32, dev), _at(out, "out", shape, ty, dev), xp, sp,
         _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_block_norm_fwd")
@@ -861,10 +917,8 @@ def block_norm_workspace_size(rows, D, gate_rows=0) -> int:
 
 def alloc_block_norm_workspace(rows, D, gate_rows=0, device=None) -> torch.Tensor:
     """Workspace of :func:`block_norm_bwd` (needs no initialisation)."""
-    n = block_norm_workspace_size(rows, D, gate_rows)
-    if n == 0:
-        raise KdaError(2, "kda_block_norm_bwd_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return _scratch(None, block_norm_workspace_size(rows, D, gate_rows), device or "cuda",
+                    "kda_block_norm_bwd_workspace_size", 0)[0]
 
 
 def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=None,
@@ -873,32 +927,30 @@ def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=Non
     """Gradients of block_norm from its inputs and statistics, given the
     gradients of ``out`` and ``x`` (one of them may be None): ``(dy, d_residual,
     d_gate, dw_post, dw_pre)``, None in the place of an input that was None."""
-    dev, ty = _cuda(y, "block_norm_bwd")
-    d, rows, D = _norm_desc(y, gate, gate_act, scale, eps)
-    f32 = torch.float32
-
-    def like(t):
-        return None if t is None else torch.empty(t.shape, dtype=ty, device=dev)
-
-    dy, dres, dgate = like(y), like(residual), like(gate)
-    dw_post = torch.empty(D, dtype=f32, device=dev)
-    dw_pre = None if w_pre is None else torch.empty(D, dtype=f32, device=dev)
-    need = 0
-    if workspace is None:
-        need = lib().kda_block_norm_bwd_workspace_size(d, int(gate is not None))
-    ws, n = _scratch(workspace, need, dev, "kda_block_norm_bwd_workspace_size", 0)
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    st = lib().kda_block_norm_bwd(
-        d, _data(y, "y", y.shape, ty, dev), _data(w_post, "w_post", (D,), f32, dev),
-        _data(residual, "residual", y.shape, ty, dev),
-        None if gate is None else _data(gate, "gate", gate.shape, ty, dev),
-        _data(w_pre, "w_pre", (D,), f32, dev), _data(stats, "stats", (2, rows), f32, dev),
-        _data(d_out, "d_out", y.shape, ty, dev), _data(d_x, "d_x", y.shape, ty, dev),
-        ptr(dy), ptr(dres), ptr(dgate), ptr(dw_post), ptr(dw_pre), ws.data_ptr(), n,
-        _raw_stream(stream, dev))
+    dev, ty = _start(y, "block_norm_bwd")
+    shape = y.shape
+    d, rows, width = _norm_desc(y, gate, gate_act, scale, eps)
+    yp = _at(y, "y", shape, ty, dev)
+    dy, dw_post = torch.empty_like(y), torch.empty_like(w_post)
+    dres = dgate = dw_pre = rp = gp = gop = wp = None
+    if residual is not None:
+        dres = torch.empty_like(y)
+        rp = dres.data_ptr()
+    if gate is not None:
+        gp = _at(gate, "gate", gate.shape, ty, dev)
+        dgate = torch.empty_like(gate)
+        gop = dgate.data_ptr()
+    if w_pre is not None:
+        dw_pre = torch.empty_like(w_pre)
+        wp = dw_pre.data_ptr()
+    L = _lib_now()
+    ws, n = _scratch(workspace, L.kda_block_norm_bwd_workspace_size(d, int(gate is not None))
+                     if workspace is None else 0, dev, "kda_block_norm_bwd_workspace_size", 0)
+    st = L.kda_block_norm_bwd(
+        d, yp, _at(w_post, "w_post", width, _f32, dev), _at(residual, "residual", shape, ty, dev),
+        gp, _at(w_pre, "w_pre", width, _f32, dev), _at(stats, "stats", (2, rows), _f32, dev),
+        _at(d_out, "d_out", shape, ty, dev), _at(d_x, "d_x", shape, ty, dev), dy.data_ptr(), rp,
+        gop, dw_post.data_ptr(), wp, ws.data_ptr(), n, _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_block_norm_bwd")
     return dy, dres, dgate, dw_post, dw_pre
