@@ -20,6 +20,8 @@
 // to bf16 at the end, and its products' operands (C, B, x, S and the 128 x 128
 // matrix of factors) are bf16 too; their errors are of y's own rounding's
 // size and average out over the sums.
+#include <type_traits>
+
 #include "kda_ssm.cuh"
 #include "kda_tc_common.cuh"
 #include "kda_f32x2.cuh"
@@ -31,7 +33,8 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kQ = 128;            // tokens per block
-constexpr int kConv = 256;         // threads that run the convolution
+constexpr int kPrep = 256;         // threads of a prep CTA
+constexpr int kConv = 512;         // threads that run the convolution of x
 
 // What the kernels hand to one another, in the workspace.
 struct TcBufs {
@@ -94,35 +97,53 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// The convolution of a tile of TP channels x 128 tokens by 256 threads.  The
-// tile's rows and the 3 before it are staged by cp.async; a warp owns 8
+// The convolution of a tile of TP channels x 128 tokens by NT threads.  The
+// tile's rows and the 3 before it are staged by cp.async; a warp owns CH
 // channels and a lane a strip of consecutive tokens, an odd number of them,
-// so that the 16-byte reads of the staged rows and the 16-byte writes of the
-// operand tiles touch all banks.
-template <int TP>
+// so that the reads of the staged rows and the writes of the operand tiles
+// touch all banks.  Channels are kept in pairs for the packed arithmetic.
+template <int TP, int CH, int NT>
 struct Conv {
-  static constexpr int kPieces = TP / 8;                   // 8-channel pieces per row
-  static constexpr int kParts = kConv / 32 / kPieces;      // warps per piece
+  static constexpr int E = CH / 2;                         // pairs of channels per warp
+  static constexpr int kPieces = TP / CH;                  // warps across the channels
+  static constexpr int kParts = NT / 32 / kPieces;         // warps across the tokens
   static constexpr int kSpan = kQ / kParts;                // tokens per warp
   static constexpr int kStrip = (kSpan + 31) / 32 % 2 ? (kSpan + 31) / 32 : (kSpan + 31) / 32 + 1;
   static constexpr int kRows = kQ + kSsmTaps - 1;
   static constexpr uint32_t kBytes = TP == 64 ? kRows * 128u : kRows * 80u;
+  using Raw = typename std::conditional<CH == 8, uint4, uint2>::type;
 
-  // 64 channels: rows of 128 bytes whose pieces are permuted by the row;
-  // 32 channels: rows of 80 bytes.
-  static __device__ __forceinline__ uint32_t off(int row, int piece) {
-    return TP == 64 ? (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4))
-                    : (uint32_t)(row * 80 + piece * 16);
+  // 16-byte pieces.  64 channels: rows of 128 bytes whose pieces are
+  // permuted by the row; 32 channels: rows of 80 bytes.
+  static __device__ __forceinline__ uint32_t off(int row, int piece16) {
+    return TP == 64 ? (uint32_t)(row * 128 + ((piece16 ^ (row & 7)) << 4))
+                    : (uint32_t)(row * 80 + piece16 * 16);
+  }
+  // the warp's channels within the tile
+  static __device__ __forceinline__ int channel(int warp) { return warp % kPieces * CH; }
+  static __device__ __forceinline__ void read(const unsigned char *rows, int row, int ch,
+                                              u64 (&x)[E]) {
+    unpack(*reinterpret_cast<const Raw *>(rows + off(row, ch / 8) + ch % 8 * 2), x);
+  }
+  static __device__ __forceinline__ void unpack(const Raw &a, u64 (&x)[E]) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&a);
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      x[i] = pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 
-  float wt[8][kSsmTaps], bias[8];
+  u64 wt[kSsmTaps][E], bias[E];
 
   __device__ __forceinline__ void weights(const SsmParams &p, int channel) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float4 w = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)(channel + c));
-      wt[c][0] = w.x; wt[c][1] = w.y; wt[c][2] = w.z; wt[c][3] = w.w;
-      bias[c] = p.bias ? p.bias[channel + c] : 0.f;
+    for (int i = 0; i < E; ++i) {
+      const float4 a = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)(channel + 2 * i));
+      const float4 b = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)(channel + 2 * i + 1));
+      wt[0][i] = pk2(a.x, b.x);
+      wt[1][i] = pk2(a.y, b.y);
+      wt[2][i] = pk2(a.z, b.z);
+      wt[3][i] = pk2(a.w, b.w);
+      bias[i] = p.bias ? pk2(p.bias[channel + 2 * i], p.bias[channel + 2 * i + 1]) : pk2(0.f, 0.f);
     }
   }
 
@@ -131,8 +152,9 @@ struct Conv {
   static __device__ __forceinline__ void stage(uint32_t dst, const bf16 *x, long long st,
                                                const bf16 *past, int channels, int t0, int T,
                                                int tid) {
-    for (int i = tid; i < kRows * kPieces; i += kConv) {
-      const int row = i / kPieces, piece = i % kPieces, t = t0 - (kSsmTaps - 1) + row;
+    constexpr int kP16 = TP / 8;
+    for (int i = tid; i < kRows * kP16; i += NT) {
+      const int row = i / kP16, piece = i % kP16, t = t0 - (kSsmTaps - 1) + row;
       const bf16 *src = x;
       bool ok = t >= 0 && t < T;
       if (ok) {
@@ -146,21 +168,20 @@ struct Conv {
     cp_async_commit();
   }
 
-  // f(j, ok, u): u = SiLU(conv) of the warp's 8 channels at token j of the
+  // f(j, ok, u): u = SiLU(conv) of the warp's channels at token j of the
   // block.  Lanes past their warp's tokens repeat the last one with ok false:
   // without branches around them the tokens of a strip overlap.
   template <typename F>
   __device__ __forceinline__ void run(const unsigned char *rows, int tid, F f) const {
-    const int warp = tid >> 5, lane = tid & 31, piece = warp % kPieces;
+    const int warp = tid >> 5, lane = tid & 31, ch = channel(warp);
     const int part = warp / kPieces, begin = part * kSpan + lane * kStrip;
     const int end = (part + 1) * kSpan;
-    float x[kStrip + kSsmTaps - 1][8];
+    u64 x[kStrip + kSsmTaps - 1][E];
 #pragma unroll
-    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i)
-      ld_bf16x8(rows + off(min(begin + i, kRows - 1), piece), x[i]);
+    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i) read(rows, min(begin + i, kRows - 1), ch, x[i]);
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
-      float u[8];
+      u64 u[E];
       taps(x[i], x[i + 1], x[i + 2], x[i + 3], u);
       f(min(begin + i, end - 1), begin + i < end, u);
     }
@@ -172,64 +193,73 @@ struct Conv {
   __device__ __forceinline__ void run_cut(const unsigned char *rows, int tid,
                                           const unsigned char *tok, const bf16 *past,
                                           int channels, F f) const {
-    const int warp = tid >> 5, lane = tid & 31, piece = warp % kPieces;
+    const int warp = tid >> 5, lane = tid & 31, ch = channel(warp);
     const int part = warp / kPieces, begin = part * kSpan + lane * kStrip;
     const int end = min(begin + kStrip, (part + 1) * kSpan);
 #pragma unroll 1
     for (int j = begin; j < end; ++j) {
-      float a[kSsmTaps][8], u[8];
+      u64 a[kSsmTaps][E], u[E];
       const int k = tok[j], place = k & 3;
 #pragma unroll
       for (int age = 0; age < kSsmTaps; ++age) {
-        float(&w)[8] = a[kSsmTaps - 1 - age];
+        u64(&w)[E] = a[kSsmTaps - 1 - age];
         if (age <= place) {
-          ld_bf16x8(rows + off(j + kSsmTaps - 1 - age, piece), w);
+          read(rows, j + kSsmTaps - 1 - age, ch, w);
         } else if ((k & 4) && past) {
-          ld_bf16x8(reinterpret_cast<const unsigned char *>(
-                        past + (size_t)(kSsmTaps - 1 + place - age) * channels + piece * 8),
-                    w);
+          unpack(*reinterpret_cast<const Raw *>(
+                     past + (size_t)(kSsmTaps - 1 + place - age) * channels + ch),
+                 w);
         } else {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) w[c] = 0.f;
+          for (int c = 0; c < E; ++c) w[c] = pk2(0.f, 0.f);
         }
       }
       taps(a[0], a[1], a[2], a[3], u);
       if (!(k & 8))
 #pragma unroll
-        for (int c = 0; c < 8; ++c) u[c] = 0.f;
+        for (int c = 0; c < E; ++c) u[c] = pk2(0.f, 0.f);
       f(j, true, u);
     }
   }
 
  private:
-  __device__ __forceinline__ void taps(const float (&a)[8], const float (&b)[8],
-                                       const float (&c)[8], const float (&x)[8],
-                                       float (&u)[8]) const {
+  __device__ __forceinline__ void taps(const u64 (&a)[E], const u64 (&b)[E], const u64 (&c)[E],
+                                       const u64 (&x)[E], u64 (&u)[E]) const {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      u64 v = fma2(pk2(wt[i][3], wt[i + 1][3]), pk2(x[i], x[i + 1]), pk2(bias[i], bias[i + 1]));
-      v = fma2(pk2(wt[i][2], wt[i + 1][2]), pk2(c[i], c[i + 1]), v);
-      v = fma2(pk2(wt[i][1], wt[i + 1][1]), pk2(b[i], b[i + 1]), v);
-      v = fma2(pk2(wt[i][0], wt[i + 1][0]), pk2(a[i], a[i + 1]), v);
+    for (int i = 0; i < E; ++i) {
+      const u64 v = fma2(wt[0][i], a[i],
+                         fma2(wt[1][i], b[i], fma2(wt[2][i], c[i], fma2(wt[3][i], x[i], bias[i]))));
       float e0, e1, d0, d1;
       upk2(mul2(v, pk2(-kLog2e, -kLog2e)), e0, e1);
       upk2(add2(pk2(1.f, 1.f), pk2(ex2(e0), ex2(e1))), d0, d1);
-      upk2(mul2(v, pk2(rcp(d0), rcp(d1))), u[i], u[i + 1]);
+      u[i] = mul2(v, pk2(rcp(d0), rcp(d1)));
     }
   }
 };
 
-// 8 values as bf16, and what that leaves, again as bf16.
-__device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo) {
-  uint32_t h[4], l[4];
+// Pairs as bf16, and what that leaves, again as bf16 (R: uint4 or uint2).
+template <typename R, int E>
+__device__ __forceinline__ R pack(const u64 (&v)[E]) {
+  R r;
+  uint32_t *w = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    l[i] = pack_bf16(v[2 * i] - __uint_as_float(h[i] << 16),
-                     v[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+  for (int i = 0; i < E; ++i) {
+    float a, b;
+    upk2(v[i], a, b);
+    w[i] = pack_bf16(a, b);
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return r;
+}
+template <typename R, int E>
+__device__ __forceinline__ void split(const u64 (&v)[E], R &hi, R &lo) {
+  u64 rest[E];
+  hi = pack<R>(v);
+  const uint32_t *h = reinterpret_cast<const uint32_t *>(&hi);
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    rest[i] = fma2(pk2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)),
+                   pk2(-1.f, -1.f), v[i]);
+  lo = pack<R>(rest);
 }
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
@@ -302,7 +332,7 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
       sdt[tt * 33 + hh] = d;
     }
     __syncthreads();
-    for (int hh = warp; hh < nh; hh += kConv / 32) {
+    for (int hh = warp; hh < nh; hh += kPrep / 32) {
       const float a2 = p.A[h0 + hh] * kLog2e;
       float d[4], a[4], pre[4], suf[4];
 #pragma unroll
@@ -363,13 +393,14 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   const SsmRow row = row_of(p, b);
   const bf16 *past = past_of(p, b);
   const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
-  Conv<TP>::stage(smem_u32(smem), x, p.xbc_st, past && row.first == 0 ? past + ch : nullptr,
-                  p.channels, t0, p.T, tid);
-  Conv<TP> cv;
-  const int piece = (tid >> 5) % Conv<TP>::kPieces;
-  cv.weights(p, ch + piece * 8);
+  using Cv = Conv<TP, 8, kPrep>;
+  Cv::stage(smem_u32(smem), x, p.xbc_st, past && row.first == 0 ? past + ch : nullptr, p.channels,
+            t0, p.T, tid);
+  Cv cv;
+  const int wch = Cv::channel(tid >> 5);
+  cv.weights(p, ch + wch);
   // whether any token's window leaves the staged rows
-  unsigned char *stok = smem + Conv<TP>::kBytes;
+  unsigned char *stok = smem + Cv::kBytes;
   int plain = 1;
   if (tid < kQ) {
     const SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr,
@@ -381,12 +412,12 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   cp_async_wait_all();
   plain = __syncthreads_and(plain);
   const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2;
-  const uint32_t at = (uint32_t)((n0 / 8 + piece) * 128);
+  const uint32_t at = (uint32_t)((n0 + wch) / 8 * 128);
   unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile + at, *lo_tile = t.blo + tile + at;
-  auto put = [&](int j, bool ok, float(&u)[8]) {
+  auto put = [&](int j, bool ok, u64(&u)[4]) {
     const size_t o = (size_t)((j & 7) * 16) + (size_t)(j >> 3) * p.N * 16;
     uint4 hi, lo;
-    split8(u, hi, lo);
+    split(u, hi, lo);
     if (ok) *reinterpret_cast<uint4 *>(hi_tile + o) = hi;
     if (ok && !is_c) *reinterpret_cast<uint4 *>(lo_tile + o) = lo;
   };
@@ -400,7 +431,7 @@ __device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) 
   const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb, *past = past_of(p, b);
   SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr, row.last, p.T,
                          row);
-  const int c = part * kConv + threadIdx.x;
+  const int c = part * kPrep + threadIdx.x;
   if (c >= p.channels) return;
   bf16 *out = static_cast<bf16 *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels + c;
 #pragma unroll
@@ -411,7 +442,7 @@ __device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) 
 // CTAs [0, B nb) make the factors, the next ones a tile of B or C each, the
 // last ones the convolution's cache.
 template <int TP>
-__global__ void __launch_bounds__(kConv) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
+__global__ void __launch_bounds__(kPrep, 2) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
   extern __shared__ __align__(128) unsigned char smem[];
   int u = blockIdx.x;
   if (u < p.B * t.nb) {
@@ -430,14 +461,14 @@ __global__ void __launch_bounds__(kConv) ssm_prep_kernel(const SsmParams p, cons
   }
   // (the ids of these CTAs run on in the same order)
   u = blockIdx.x - p.B * t.nb * (1 + p.G * parts);
-  const int caches = (p.channels + kConv - 1) / kConv;
+  const int caches = (p.channels + kPrep - 1) / kPrep;
   prep_cache(p, u / caches, u % caches);
 }
 
 // ---------------------------------------------------------------------------
 // 2. states
 
-// Barrier of the 256 convolving threads; whether any of them says so.
+// Barrier of the convolving threads; whether any of them says so.
 __device__ __forceinline__ bool any_of_conv(bool v) {
   uint32_t r;
   asm volatile(
@@ -454,27 +485,30 @@ __device__ __forceinline__ bool any_of_conv(bool v) {
 // Shared memory of ssm_state_kernel.
 template <int TP>
 struct StateSmem {
+  using Cv = Conv<TP, 4, kConv>;
   static constexpr uint32_t kX = 0;                                 // 2 x [hi | lo] tiles
   static constexpr uint32_t kXBytes = kQ * TP * 2 * 2;
   static constexpr uint32_t kB = kX + 2 * kXBytes;                  // 2 x (hi, lo) tiles
   static constexpr uint32_t kBBytes = 2 * kQ * 128 * 2;
   static constexpr uint32_t kRows = kB + 2 * kBBytes;               // 2 staged tiles of x
-  static constexpr uint32_t kW = kRows + 2 * Conv<TP>::kBytes;      // 2 x wst
+  static constexpr uint32_t kW = kRows + 2 * Cv::kBytes;      // 2 x wst
   static constexpr uint32_t kBar = kW + 2 * kQ * 4;
   static constexpr uint32_t kBytes = kBar + 64;
 };
 
-// 256 threads run the convolution, keep S and write it; a ninth warp copies
+// 512 threads run the convolution, keep S and write it; one more warp copies
 // the tiles of B and issues the products.  Per block i the threads
 //   convolve x into the operand buffer i % 2 while the products of block
 //   i - 1 run, then wait for those, write the S that entered block i - 1 and
 //   update it.
-// A thread holds TP / 2 columns of one state row (its TMEM lane).
+// A thread holds TP / 4 columns of one state row (its TMEM lane).  (With 256
+// threads, two warps on a scheduler, a block took 3.7 us instead of STATE_US.)
 template <int TP>
 __global__ void __launch_bounds__(kConv + 32, 1)
     ssm_state_kernel(const SsmParams p, const TcBufs t) {
   using L = StateSmem<TP>;
-  constexpr int kCols = TP / 2;
+  using Cv = typename L::Cv;
+  constexpr int kCols = TP / 4;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_tmem;
   const uint32_t sb = smem_u32(smem);
@@ -548,9 +582,9 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     const bf16 *before = past && row.first == 0 ? past + ch : nullptr;
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
     const float *dec = t.dec + ((size_t)b * p.H + h) * nb;
-    Conv<TP> cv;
-    const int piece = warp % Conv<TP>::kPieces;
-    cv.weights(p, ch + piece * 8);
+    Cv cv;
+    const int wch = Cv::channel(warp);
+    cv.weights(p, ch + wch);
     const int n = 32 * (warp & 3) + lane, col0 = (warp >> 2) * kCols;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col0;
     const size_t state = (((size_t)b * p.H + h) * N + n) * p.P + c0 + col0;
@@ -567,8 +601,8 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       if (i < nb) {
         if (tid < kQ / 4)
           cp_async16(sb + L::kW + (i & 1) * kQ * 4 + tid * 16, wst + (size_t)i * kQ + tid * 4, true);
-        Conv<TP>::stage(sb + L::kRows + (i & 1) * Conv<TP>::kBytes, x, p.xbc_st, before,
-                        p.channels, i * kQ, p.T, tid);
+        Cv::stage(sb + L::kRows + (i & 1) * Cv::kBytes, x, p.xbc_st, before, p.channels, i * kQ,
+                  p.T, tid);
       }
     };
     bool bad = false;
@@ -590,16 +624,26 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         set_status(t.status, KDA_DEVICE_TIMEOUT);
       }
       tc_fence_after();
+      uint32_t hi[kCols / 8][8], lo[kCols / 8][8];
 #pragma unroll
-      for (int k = 0; k < kCols; k += 16) {
-        float hi[16], lo[16];
-        tmem_ld16x2(tl + (i & 1) * 2 * TP + k, tl + (i & 1) * 2 * TP + TP + k, hi, lo);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float d = hi[e] + lo[e];
-          s[k + e] = a < 0.f ? d : fmaf(a, s[k + e], d);
-        }
+      for (int k = 0; k < kCols / 8; ++k) {
+        tmem_ld8_nw(tl + (i & 1) * 2 * TP + 8 * k, hi[k]);
+        tmem_ld8_nw(tl + (i & 1) * 2 * TP + TP + 8 * k, lo[k]);
       }
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < kCols / 8; ++k) {
+        reg_fence8(hi[k]);
+        reg_fence8(lo[k]);
+      }
+      if (a < 0.f) {     // a reset drops the state whatever it holds
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) s[k] = 0.f;
+        a = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        s[k] = fmaf(a, s[k], __uint_as_float(hi[k / 8][k % 8]) + __uint_as_float(lo[k / 8][k % 8]));
       tc_fence_before();
     };
     stage(0);
@@ -614,28 +658,32 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
       const float a_next = i + 1 < nb ? dec[i + 1] : 0.f;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
-      unsigned char *xo = smem + L::kX + (i & 1) * L::kXBytes + piece * 2048;
+      const uint32_t at = (uint32_t)(wch / 8 * 2048 + wch % 8 * 2);
+      unsigned char *xo = smem + L::kX + (i & 1) * L::kXBytes + at;
       unsigned char *xt = t.xt + (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
-                          (size_t)(c0 / 8 + piece) * 2048;
-      auto put = [&](int j, bool ok, float(&u)[8]) {
+                          (size_t)(c0 / 8) * 2048 + at;
+      auto put = [&](int j, bool ok, u64(&u)[2], bool cut) {
         const int o = (j >> 3) * 128 + (j & 7) * 16;
-        const uint4 v = pack8(u);
+        const uint2 v = pack<uint2>(u);
         const float f = w[j];
-        // a token that does not reach the state adds nothing, whatever it holds
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = f != 0.f ? u[e] * f : 0.f;
-        uint4 hi, lo;
-        split8(u, hi, lo);
+        for (int e = 0; e < 2; ++e) u[e] = mul2(u[e], pk2(f, f));
+        if (cut && f == 0.f)    // a token that does not reach the state adds
+          u[0] = u[1] = pk2(0.f, 0.f);       // nothing, whatever it holds
+        uint2 hi, lo;
+        split(u, hi, lo);
         if (ok) {
-          *reinterpret_cast<uint4 *>(xt + o) = v;
-          *reinterpret_cast<uint4 *>(xo + o) = hi;
-          *reinterpret_cast<uint4 *>(xo + TP / 8 * 2048 + o) = lo;
+          *reinterpret_cast<uint2 *>(xt + o) = v;
+          *reinterpret_cast<uint2 *>(xo + o) = hi;
+          *reinterpret_cast<uint2 *>(xo + TP / 8 * 2048 + o) = lo;
         }
       };
-      const unsigned char *rows = smem + L::kRows + (i & 1) * Conv<TP>::kBytes;
-      if (flags & kPlain) cv.run(rows, tid, put);
-      else cv.run_cut(rows, tid, t.tok + ((size_t)b * nb + i) * kQ, past ? past + ch : nullptr,
-                      p.channels, put);
+      const unsigned char *rows = smem + L::kRows + (i & 1) * Cv::kBytes;
+      if (flags & kPlain)
+        cv.run(rows, tid, [&](int j, bool ok, u64(&u)[2]) { put(j, ok, u, false); });
+      else
+        cv.run_cut(rows, tid, t.tok + ((size_t)b * nb + i) * kQ, past ? past + ch : nullptr,
+                   p.channels, [&](int j, bool ok, u64(&u)[2]) { put(j, ok, u, true); });
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
@@ -879,12 +927,12 @@ __global__ void __launch_bounds__(256, 2)
 
 template <int TP>
 cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  size_t smem = Conv<TP>::kBytes + kQ;
+  size_t smem = Conv<TP, 8, kPrep>::kBytes + kQ;
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
-  const int caches = p.conv_out ? (p.channels + kConv - 1) / kConv : 0;
+  const int caches = p.conv_out ? (p.channels + kPrep - 1) / kPrep : 0;
   const unsigned grid = (unsigned)(p.B * (t.nb * (1 + p.G * (2 * p.N / TP)) + caches));
-  ssm_prep_kernel<TP><<<grid, kConv, smem, cs>>>(p, t);
+  ssm_prep_kernel<TP><<<grid, kPrep, smem, cs>>>(p, t);
   return cudaGetLastError();
 }
 
