@@ -33,19 +33,31 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kQ = 128;            // tokens per block
+
+// Tiles hold a block's tokens in slots, the 32 tokens of a quarter transposed
+// as 8 strips of 4: the products sum over tokens in any order, and so a lane
+// that convolves 4 consecutive tokens writes them 128 bytes apart while 8
+// lanes write 8 neighbouring slots (no bank conflicts, no index arithmetic).
+__host__ __device__ constexpr int slot_of(int token) {
+  return (token & ~31) + 8 * (token & 3) + (token >> 2 & 7);
+}
+__host__ __device__ constexpr int token_of(int slot) {
+  return (slot & ~31) + 4 * (slot & 7) + (slot >> 3 & 3);
+}
 constexpr int kPrep = 256;         // threads of a prep CTA
 constexpr int kConv = 512;         // threads that run the convolution of x
 
 // What the kernels hand to one another, in the workspace.
 struct TcBufs {
   int nb;                          // blocks per row
-  unsigned char *bhi, *blo, *ct;   // [B][nb][G] tiles (token, state), op_off(t, n, N)
-  unsigned char *xt;               // [B][nb][H] tiles of x, mn_off(p, t, 128)
+  unsigned char *bhi, *blo, *ct;   // [B][nb][G] tiles (slot, state), op_off(slot, n, N)
+  unsigned char *xt;               // [B][nb][H] tiles of x, mn_off(p, slot, 128)
   unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
-  float *ein, *wst, *cum, *cumj;   // [B][H][nb * 128], see prep_factors
+  float *ein, *cum, *cumj;         // [B][H][nb * 128] by slot, see prep_factors
+  float *wst;                      // likewise, by token
   float *dec;                      // [B][H][nb]: e^{c_127}, or -1: the block resets the state
-  int *run;                        // [B][nb * 128]: resets so far in the block, -1: padding
-  unsigned char *tok;              // [B][nb * 128]: place | first << 2 | live << 3
+  int *run;                        // [B][nb * 128] by slot: resets so far in the block, -1: padding
+  unsigned char *tok;              // [B][nb * 128] by token: place | first << 2 | live << 3
   int *flags;                      // [B][nb]: kPlain, kResets
   uint32_t *status;
 };
@@ -99,31 +111,24 @@ __device__ __forceinline__ float rcp(float x) {
 // ---------------------------------------------------------------------------
 // The convolution of a tile of TP channels x 128 tokens by NT threads.  The
 // tile's rows and the 3 before it are staged by cp.async; a warp owns CH
-// channels and a lane a strip of consecutive tokens, an odd number of them,
-// so that the reads of the staged rows and the writes of the operand tiles
-// touch all banks.  Channels are kept in pairs for the packed arithmetic.
+// channels and a lane 4 consecutive tokens.  Channels are kept in pairs for
+// the packed arithmetic.
 template <int TP, int CH, int NT>
 struct Conv {
-  static constexpr int E = CH / 2;                         // pairs of channels per warp
-  static constexpr int kPieces = TP / CH;                  // warps across the channels
-  static constexpr int kParts = NT / 32 / kPieces;         // warps across the tokens
-  static constexpr int kSpan = kQ / kParts;                // tokens per warp
-  static constexpr int kStrip = (kSpan + 31) / 32 % 2 ? (kSpan + 31) / 32 : (kSpan + 31) / 32 + 1;
+  static_assert(TP / CH * 32 == NT, "one warp per CH channels");
+  static constexpr int E = CH / 2;                         // pairs of channels per lane
+  static constexpr int kStrip = 4;
   static constexpr int kRows = kQ + kSsmTaps - 1;
-  static constexpr uint32_t kBytes = TP == 64 ? kRows * 128u : kRows * 80u;
-  using Raw = typename std::conditional<CH == 8, uint4, uint2>::type;
+  static constexpr uint32_t kRowBytes = TP * 2;
+  static constexpr uint32_t kBytes = kRows * kRowBytes;
+  using Raw = typename std::conditional<
+      CH == 8, uint4, typename std::conditional<CH == 4, uint2, uint32_t>::type>::type;
 
-  // 16-byte pieces.  64 channels: rows of 128 bytes whose pieces are
-  // permuted by the row; 32 channels: rows of 80 bytes.
+  // 16-byte pieces of a row, permuted by the row's strip: the lanes of a
+  // warp read rows 4 apart.
   static __device__ __forceinline__ uint32_t off(int row, int piece16) {
-    return TP == 64 ? (uint32_t)(row * 128 + ((piece16 ^ (row & 7)) << 4))
-                    : (uint32_t)(row * 80 + piece16 * 16);
-  }
-  // the warp's channels within the tile
-  static __device__ __forceinline__ int channel(int warp) { return warp % kPieces * CH; }
-  static __device__ __forceinline__ void read(const unsigned char *rows, int row, int ch,
-                                              u64 (&x)[E]) {
-    unpack(*reinterpret_cast<const Raw *>(rows + off(row, ch / 8) + ch % 8 * 2), x);
+    return (uint32_t)(row * kRowBytes) +
+           (uint32_t)((piece16 ^ (TP == 64 ? row >> 2 & 7 : row >> 3 & 3)) << 4);
   }
   static __device__ __forceinline__ void unpack(const Raw &a, u64 (&x)[E]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&a);
@@ -148,63 +153,66 @@ struct Conv {
   }
 
   // x: the row's token 0 at the tile's channel; past: the cached inputs that
-  // precede it (or null), for a row whose first run starts at token 0.
+  // precede it (or null), for a row whose first run starts at token 0.  A
+  // thread copies one 16-byte piece of every kStep-th row.
   static __device__ __forceinline__ void stage(uint32_t dst, const bf16 *x, long long st,
                                                const bf16 *past, int channels, int t0, int T,
                                                int tid) {
-    constexpr int kP16 = TP / 8;
-    for (int i = tid; i < kRows * kP16; i += NT) {
-      const int row = i / kP16, piece = i % kP16, t = t0 - (kSsmTaps - 1) + row;
-      const bf16 *src = x;
-      bool ok = t >= 0 && t < T;
-      if (ok) {
-        src = x + (long long)t * st + piece * 8;
-      } else if (t < 0 && past) {
-        src = past + (size_t)(kSsmTaps - 1 + t) * channels + piece * 8;
-        ok = true;
+    constexpr int kP16 = TP / 8, kStep = NT / kP16;
+    const int piece = tid % kP16, row0 = tid / kP16;
+    const bf16 *src = x + (long long)(t0 - (kSsmTaps - 1) + row0) * st + piece * 8;
+#pragma unroll
+    for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k) {
+      const int row = row0 + k * kStep, t = t0 - (kSsmTaps - 1) + row;
+      if (row < kRows) {
+        const bool ok = t >= 0 && t < T;
+        const bf16 *from = ok ? src + (long long)(k * kStep) * st : x;
+        if (t < 0 && past) from = past + (size_t)(kSsmTaps - 1 + t) * channels + piece * 8;
+        cp_async16(dst + off(row, piece), from, ok || (t < 0 && past));
       }
-      cp_async16(dst + off(row, piece), src, ok);
     }
     cp_async_commit();
   }
 
-  // f(j, ok, u): u = SiLU(conv) of the warp's channels at token j of the
-  // block.  Lanes past their warp's tokens repeat the last one with ok false:
-  // without branches around them the tokens of a strip overlap.
+  // f(i, u): u = SiLU(conv) of channels [CH warp, CH (warp + 1)) of the tile
+  // at the lane's i-th token, 4 lane + i.
   template <typename F>
-  __device__ __forceinline__ void run(const unsigned char *rows, int tid, F f) const {
-    const int warp = tid >> 5, lane = tid & 31, ch = channel(warp);
-    const int part = warp / kPieces, begin = part * kSpan + lane * kStrip;
-    const int end = (part + 1) * kSpan;
+  __device__ __forceinline__ void run(const unsigned char *rows, int warp, int lane, F f) const {
+    const int ch = warp * CH;
+    // rows 4 lane .. 4 lane + 6: two permutations
+    const unsigned char *lo = rows + off(4 * lane, ch / 8) + ch % 8 * 2;
+    const unsigned char *hi = rows + off(min(4 * lane + 4, kRows - 1), ch / 8) + ch % 8 * 2;
     u64 x[kStrip + kSsmTaps - 1][E];
 #pragma unroll
-    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i) read(rows, min(begin + i, kRows - 1), ch, x[i]);
+    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i)
+      unpack(*reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes),
+             x[i]);
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
       u64 u[E];
       taps(x[i], x[i + 1], x[i + 2], x[i + 3], u);
-      f(min(begin + i, end - 1), begin + i < end, u);
+      f(i, u);
     }
   }
 
   // The same where windows are cut by runs: tok holds the tokens' windows,
   // past the cached inputs of the row at the tile's channel (or null).
   template <typename F>
-  __device__ __forceinline__ void run_cut(const unsigned char *rows, int tid,
+  __device__ __forceinline__ void run_cut(const unsigned char *rows, int warp, int lane,
                                           const unsigned char *tok, const bf16 *past,
                                           int channels, F f) const {
-    const int warp = tid >> 5, lane = tid & 31, ch = channel(warp);
-    const int part = warp / kPieces, begin = part * kSpan + lane * kStrip;
-    const int end = min(begin + kStrip, (part + 1) * kSpan);
+    const int ch = warp * CH;
 #pragma unroll 1
-    for (int j = begin; j < end; ++j) {
+    for (int i = 0; i < kStrip; ++i) {
       u64 a[kSsmTaps][E], u[E];
-      const int k = tok[j], place = k & 3;
+      const int j = 4 * lane + i, k = tok[j], place = k & 3;
 #pragma unroll
       for (int age = 0; age < kSsmTaps; ++age) {
         u64(&w)[E] = a[kSsmTaps - 1 - age];
         if (age <= place) {
-          read(rows, j + kSsmTaps - 1 - age, ch, w);
+          unpack(*reinterpret_cast<const Raw *>(
+                     rows + off(j + kSsmTaps - 1 - age, ch / 8) + ch % 8 * 2),
+                 w);
         } else if ((k & 4) && past) {
           unpack(*reinterpret_cast<const Raw *>(
                      past + (size_t)(kSsmTaps - 1 + place - age) * channels + ch),
@@ -218,7 +226,7 @@ struct Conv {
       if (!(k & 8))
 #pragma unroll
         for (int c = 0; c < E; ++c) u[c] = pk2(0.f, 0.f);
-      f(j, true, u);
+      f(i, u);
     }
   }
 
@@ -236,6 +244,8 @@ struct Conv {
     }
   }
 };
+
+using Unpack8 = Conv<64, 8, 256>;
 
 // Pairs as bf16, and what that leaves, again as bf16 (R: uint4 or uint2).
 template <typename R, int E>
@@ -312,7 +322,7 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     for (int w = 0; w < warp; ++w) n += scount[w];
     srun[tid] = n;
     const size_t at = (size_t)b * t.nb * kQ + t0 + tid;
-    t.run[at] = k.live ? n : -1;
+    t.run[at - tid + slot_of(tid)] = k.live ? n : -1;
     t.tok[at] = (unsigned char)(k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0));
   }
   if (tid == 0) {
@@ -361,21 +371,20 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
       if (lane == 0) before = 0.f;
       if (lane == 31) after = 0.f;
       const int last = srun[kQ - 1];
-      float4 ein, wst, cum, cumj;
-      float *fe = &ein.x, *fw = &wst.x, *fc = &cum.x, *fj = &cumj.x;
+      const size_t at = (((size_t)b * p.H + h0 + hh) * t.nb + blk) * kQ;
+      float4 wst;
+      float *fw = &wst.x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int run = srun[lane * 4 + i];
-        fc[i] = before + pre[i];
-        fj[i] = fc[i] - log2f(d[i]);     // d = 0: +inf, a factor of 0
-        fe[i] = run == 0 ? exp2f(fc[i]) : 0.f;
+        const float c = before + pre[i];
+        const size_t s = at + slot_of(lane * 4 + i);
+        t.ein[s] = run == 0 ? exp2f(c) : 0.f;
+        t.cum[s] = c;
+        t.cumj[s] = c - log2f(d[i]);     // d = 0: +inf, a factor of 0
         fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : 0.f;
       }
-      const size_t at = (((size_t)b * p.H + h0 + hh) * t.nb + blk) * kQ + lane * 4;
-      *reinterpret_cast<float4 *>(t.ein + at) = ein;
-      *reinterpret_cast<float4 *>(t.wst + at) = wst;
-      *reinterpret_cast<float4 *>(t.cum + at) = cum;
-      *reinterpret_cast<float4 *>(t.cumj + at) = cumj;
+      *reinterpret_cast<float4 *>(t.wst + at + lane * 4) = wst;
       if (lane == 0)
         t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] = last == 0 ? exp2f(total) : -1.f;
     }
@@ -393,12 +402,15 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   const SsmRow row = row_of(p, b);
   const bf16 *past = past_of(p, b);
   const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
-  using Cv = Conv<TP, 8, kPrep>;
-  Cv::stage(smem_u32(smem), x, p.xbc_st, past && row.first == 0 ? past + ch : nullptr, p.channels,
-            t0, p.T, tid);
+  using Cv = Conv<TP, 8, TP * 4>;
+  const int warp = tid >> 5, lane = tid & 31, wch = warp * 8;
+  const bool mine = tid < TP * 4;           // 32 channels take half the threads
   Cv cv;
-  const int wch = Cv::channel(tid >> 5);
-  cv.weights(p, ch + wch);
+  if (mine) {
+    Cv::stage(smem_u32(smem), x, p.xbc_st, past && row.first == 0 ? past + ch : nullptr,
+              p.channels, t0, p.T, tid);
+    cv.weights(p, ch + wch);
+  }
   // whether any token's window leaves the staged rows
   unsigned char *stok = smem + Cv::kBytes;
   int plain = 1;
@@ -411,18 +423,19 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   }
   cp_async_wait_all();
   plain = __syncthreads_and(plain);
-  const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2;
-  const uint32_t at = (uint32_t)((n0 + wch) / 8 * 128);
-  unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile + at, *lo_tile = t.blo + tile + at;
-  auto put = [&](int j, bool ok, u64(&u)[4]) {
-    const size_t o = (size_t)((j & 7) * 16) + (size_t)(j >> 3) * p.N * 16;
+  if (!mine) return;
+  // the lane's i-th token: row 8 i + lane % 8 of quarter lane / 8
+  const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2 +
+                      (size_t)(lane >> 3) * 4 * p.N * 16 + (lane & 7) * 16 + (n0 + wch) / 8 * 128;
+  unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile, *lo_tile = t.blo + tile;
+  auto put = [&](int i, u64(&u)[4]) {
     uint4 hi, lo;
     split(u, hi, lo);
-    if (ok) *reinterpret_cast<uint4 *>(hi_tile + o) = hi;
-    if (ok && !is_c) *reinterpret_cast<uint4 *>(lo_tile + o) = lo;
+    *reinterpret_cast<uint4 *>(hi_tile + (size_t)i * p.N * 16) = hi;
+    if (!is_c) *reinterpret_cast<uint4 *>(lo_tile + (size_t)i * p.N * 16) = lo;
   };
-  if (plain) cv.run(smem, tid, put);
-  else cv.run_cut(smem, tid, stok, past ? past + ch : nullptr, p.channels, put);
+  if (plain) cv.run(smem, warp, lane, put);
+  else cv.run_cut(smem, warp, lane, stok, past ? past + ch : nullptr, p.channels, put);
 }
 
 // The inputs that the convolution's cache holds after the row.
@@ -485,7 +498,7 @@ __device__ __forceinline__ bool any_of_conv(bool v) {
 // Shared memory of ssm_state_kernel.
 template <int TP>
 struct StateSmem {
-  using Cv = Conv<TP, 4, kConv>;
+  using Cv = Conv<TP, TP / 16, kConv>;
   static constexpr uint32_t kX = 0;                                 // 2 x [hi | lo] tiles
   static constexpr uint32_t kXBytes = kQ * TP * 2 * 2;
   static constexpr uint32_t kB = kX + 2 * kXBytes;                  // 2 x (hi, lo) tiles
@@ -583,7 +596,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
     const float *dec = t.dec + ((size_t)b * p.H + h) * nb;
     Cv cv;
-    const int wch = Cv::channel(warp);
+    const int wch = warp * (TP / 16);
     cv.weights(p, ch + wch);
     const int n = 32 * (warp & 3) + lane, col0 = (warp >> 2) * kCols;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col0;
@@ -658,32 +671,35 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
       const float a_next = i + 1 < nb ? dec[i + 1] : 0.f;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
-      const uint32_t at = (uint32_t)(wch / 8 * 2048 + wch % 8 * 2);
+      // the lane's i-th token: slot 8 i + lane % 8 of quarter lane / 8
+      using Raw = typename Cv::Raw;
+      const uint32_t at = (uint32_t)(wch / 8 * 2048 + wch % 8 * 2 + (lane >> 3) * 512 +
+                                     (lane & 7) * 16);
       unsigned char *xo = smem + L::kX + (i & 1) * L::kXBytes + at;
       unsigned char *xt = t.xt + (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
                           (size_t)(c0 / 8) * 2048 + at;
-      auto put = [&](int j, bool ok, u64(&u)[2], bool cut) {
-        const int o = (j >> 3) * 128 + (j & 7) * 16;
-        const uint2 v = pack<uint2>(u);
-        const float f = w[j];
+      const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * lane);
+      auto put = [&](int k, u64(&u)[Cv::E], bool cut) {
+        *reinterpret_cast<Raw *>(xt + k * 128) = pack<Raw>(u);
+        const float f = k == 0 ? w4.x : k == 1 ? w4.y : k == 2 ? w4.z : w4.w;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) u[e] = mul2(u[e], pk2(f, f));
-        if (cut && f == 0.f)    // a token that does not reach the state adds
-          u[0] = u[1] = pk2(0.f, 0.f);       // nothing, whatever it holds
-        uint2 hi, lo;
-        split(u, hi, lo);
-        if (ok) {
-          *reinterpret_cast<uint2 *>(xt + o) = v;
-          *reinterpret_cast<uint2 *>(xo + o) = hi;
-          *reinterpret_cast<uint2 *>(xo + TP / 8 * 2048 + o) = lo;
+        for (int e = 0; e < Cv::E; ++e) {
+          u[e] = mul2(u[e], pk2(f, f));
+          // a token that does not reach the state adds nothing, whatever it holds
+          if (cut && f == 0.f) u[e] = pk2(0.f, 0.f);
         }
+        Raw hi, lo;
+        split(u, hi, lo);
+        *reinterpret_cast<Raw *>(xo + k * 128) = hi;
+        *reinterpret_cast<Raw *>(xo + TP / 8 * 2048 + k * 128) = lo;
       };
       const unsigned char *rows = smem + L::kRows + (i & 1) * Cv::kBytes;
       if (flags & kPlain)
-        cv.run(rows, tid, [&](int j, bool ok, u64(&u)[2]) { put(j, ok, u, false); });
+        cv.run(rows, warp, lane, [&](int k, u64(&u)[Cv::E]) { put(k, u, false); });
       else
-        cv.run_cut(rows, tid, t.tok + ((size_t)b * nb + i) * kQ, past ? past + ch : nullptr,
-                   p.channels, [&](int j, bool ok, u64(&u)[2]) { put(j, ok, u, true); });
+        cv.run_cut(rows, warp, lane, t.tok + ((size_t)b * nb + i) * kQ,
+                   past ? past + ch : nullptr, p.channels,
+                   [&](int k, u64(&u)[Cv::E]) { put(k, u, true); });
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
@@ -722,7 +738,9 @@ struct OutSmem {
   static constexpr uint32_t kBytes = kBar + 32;
 };
 
-// One CTA per (row, block, group, `heads` of its heads); TMEM holds C B^T of
+// A row is a slot, and so is a column of C B^T and of the factors; slot l of a
+// quarter is its token 4 (l % 8) + l / 8.  One CTA per (row, block, group,
+// `heads` of its heads); TMEM holds C B^T of
 // the block, shared by the heads, and the two parts of y of PT columns.  Two
 // CTAs fit an SM and fill each other's waits.
 template <int PT>
@@ -735,6 +753,7 @@ __global__ void __launch_bounds__(256, 2)
   const uint32_t bar_cb = sb + L::kBar, bar_xs = bar_cb + 8, bar_m = bar_cb + 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = warp & 3, half = warp >> 2, r = 32 * quad + lane;
+  const int r_token = token_of(lane);       // within the quarter
   const int nb = t.nb, N = p.N, hg = p.H / p.G, per = (hg + heads - 1) / heads;
   int u = blockIdx.x;
   const int part = u % per;
@@ -823,24 +842,34 @@ __global__ void __launch_bounds__(256, 2)
       mma_commit(bar_m);
     }
     if (c == 0) {
-      // factors of the head: rows r, 16 columns at a time, up to the diagonal
+      // factors of the head: row r, 16 columns at a time, up to the diagonal
       const float cr = scum[r];
+      const u64 cr2 = pk2(cr, cr), neg = pk2(-1.f, -1.f);
 #pragma unroll 1
       for (int q = half; q < 2 * quad + 2; q += 2) {
         float v[16];
         tmem_ld16(t_cb + lanes + 16 * q, v);
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const float4 cj = *reinterpret_cast<const float4 *>(scumj + 16 * q + e);
-          const float w[4] = {cj.x, cj.y, cj.z, cj.w};
+          const ulonglong2 cj = *reinterpret_cast<const ulonglong2 *>(scumj + 16 * q + e);
+          float f[4];
+          upk2(fma2(cj.x, neg, cr2), f[0], f[1]);
+          upk2(fma2(cj.y, neg, cr2), f[2], f[3]);
+          const u64 lo = mul2(pk2(v[e], v[e + 1]), pk2(ex2(f[0]), ex2(f[1])));
+          const u64 hi = mul2(pk2(v[e + 2], v[e + 3]), pk2(ex2(f[2]), ex2(f[3])));
+          upk2(lo, v[e], v[e + 1]);
+          upk2(hi, v[e + 2], v[e + 3]);
+        }
+        if (q >= 2 * quad) {     // the diagonal's quarter: later tokens do not count
+          const int last = r_token - 2 * (q & 1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = 16 * q + e + i;
-            bool on = j <= r;
-            if (flags & kResets) on = on && srun[j] == run;
-            const float f = ex2(cr - w[i]);
-            v[e + i] = on ? v[e + i] * f : 0.f;
-          }
+          for (int e = 0; e < 16; ++e)
+            if (token_of(e) > last) v[e] = 0.f;
+        }
+        if (flags & kResets) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (srun[16 * q + e] != run) v[e] = 0.f;
         }
         unsigned char *f = smem + L::kF + (r & 7) * 16 + (r >> 3) * 2048 + 2 * q * 128;
         float a[8];
@@ -865,12 +894,17 @@ __global__ void __launch_bounds__(256, 2)
     auto piece = [&](int row, int q) {   // 16-byte piece of the [128][PT] tile of z and y
       return (uint32_t)(L::kS + row * PT * 2 + ((q ^ (PT == 64 ? row & 7 : row >> 1 & 3)) << 4));
     };
+    // a thread copies piece q0 of slots s0, s0 + 256 / (PT / 8), ..
+    constexpr int kP16 = PT / 8, kStep = 256 / kP16;
+    const int q0 = tid % kP16, s0 = tid / kP16;
     if (p.z) {
-      const bf16 *z = static_cast<const bf16 *>(p.z) + (size_t)b * p.z_sb + ch;
-      for (int i = tid; i < kQ * PT / 8; i += 256) {
-        const int row = i / (PT / 8), q = i % (PT / 8);
-        const bool ok = t0 + row < p.T;
-        cp_async16(sb + piece(row, q), z + (ok ? (long long)(t0 + row) * p.z_st : 0) + q * 8, ok);
+      const bf16 *z = static_cast<const bf16 *>(p.z) + (size_t)b * p.z_sb +
+                      (long long)t0 * p.z_st + ch + q0 * 8;
+#pragma unroll
+      for (int s = s0; s < kQ; s += kStep) {
+        const int tok = token_of(s);
+        const bool ok = t0 + tok < p.T;
+        cp_async16(sb + piece(s, q0), z + (ok ? (long long)tok * p.z_st : 0), ok);
       }
       cp_async_commit();
     }
@@ -879,6 +913,7 @@ __global__ void __launch_bounds__(256, 2)
     __syncthreads();
     // y of row r, columns [half PT / 2, (half + 1) PT / 2)
     const float ein = sein[r], D = p.D ? p.D[h] : 0.f;
+    const u64 ein2 = pk2(ein, ein), D2 = pk2(D, D);
 #pragma unroll
     for (int e0 = 0; e0 < PT / 2; e0 += 16) {
       const int col = half * (PT / 2) + e0;
@@ -886,27 +921,37 @@ __global__ void __launch_bounds__(256, 2)
       tmem_ld16x2(t_yi + lanes + col, t_yx + lanes + col, yi, yx);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        float x[8], z[8], v[8];
-        ld_bf16x8(smem + L::kX + (col / 8 + q) * 2048 + (r >> 3) * 128 + (r & 7) * 16, x);
+        u64 x[4], z[4], y[4];
+        Unpack8::unpack(*reinterpret_cast<const uint4 *>(
+                            smem + L::kX + (col / 8 + q) * 2048 + (r >> 3) * 128 + (r & 7) * 16),
+                        x);
         unsigned char *zp = smem + piece(r, col / 8 + q);
-        if (p.z) ld_bf16x8(zp, z);
+        if (p.z) Unpack8::unpack(*reinterpret_cast<const uint4 *>(zp), z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float y = fmaf(ein, yi[8 * q + e], yx[8 * q + e]) + D * x[e];
-          if (p.z) y *= z[e] * rcp(1.f + ex2(-kLog2e * z[e]));
-          v[e] = run < 0 ? 0.f : y;
+        for (int e = 0; e < 4; ++e) {
+          const int i = 8 * q + 2 * e;
+          y[e] = fma2(D2, x[e], fma2(ein2, pk2(yi[i], yi[i + 1]), pk2(yx[i], yx[i + 1])));
+          if (p.z) {
+            float a, c, d0, d1;
+            upk2(mul2(z[e], pk2(-kLog2e, -kLog2e)), a, c);
+            upk2(add2(pk2(1.f, 1.f), pk2(ex2(a), ex2(c))), d0, d1);
+            y[e] = mul2(mul2(y[e], z[e]), pk2(rcp(d0), rcp(d1)));
+          }
         }
-        *reinterpret_cast<uint4 *>(zp) = pack8(v);
+        uint4 o = pack<uint4>(y);
+        if (run < 0) o = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(zp) = o;
       }
     }
     tc_fence_before();
     __syncthreads();
-    bf16 *y = static_cast<bf16 *>(p.y) + ((size_t)b * p.T + t0) * p.H * p.P + ch;
-    for (int i = tid; i < kQ * PT / 8; i += 256) {
-      const int row = i / (PT / 8), q = i % (PT / 8);
-      if (t0 + row < p.T)
-        *reinterpret_cast<uint4 *>(y + (size_t)row * p.H * p.P + q * 8) =
-            *reinterpret_cast<const uint4 *>(smem + piece(row, q));
+    bf16 *y = static_cast<bf16 *>(p.y) + ((size_t)b * p.T + t0) * p.H * p.P + ch + q0 * 8;
+#pragma unroll
+    for (int s = s0; s < kQ; s += kStep) {
+      const int tok = token_of(s);
+      if (t0 + tok < p.T)
+        *reinterpret_cast<uint4 *>(y + (size_t)tok * p.H * p.P) =
+            *reinterpret_cast<const uint4 *>(smem + piece(s, q0));
     }
     fence_proxy_async();
     __syncthreads();
@@ -927,7 +972,7 @@ __global__ void __launch_bounds__(256, 2)
 
 template <int TP>
 cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  size_t smem = Conv<TP, 8, kPrep>::kBytes + kQ;
+  size_t smem = Conv<TP, 8, TP * 4>::kBytes + kQ;
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
   const int caches = p.conv_out ? (p.channels + kPrep - 1) / kPrep : 0;
