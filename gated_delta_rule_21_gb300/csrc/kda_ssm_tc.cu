@@ -57,12 +57,13 @@ struct TcBufs {
   float *wst;                      // likewise, by token
   float *dec;                      // [B][H][nb]: e^{c_127}, or -1: the block resets the state
   int *run;                        // [B][nb * 128] by slot: resets so far in the block, -1: padding
-  unsigned char *tok;              // [B][nb * 128] by token: place | first << 2 | live << 3
+  unsigned char *tok;              // [B][nb * 128] by token: token_mark
   int *flags;                      // [B][nb]: kPlain, kResets
   uint32_t *status;
 };
+// flags of a block
 constexpr int kPlain = 1;          // every token has its whole window in the staged rows
-constexpr int kResets = 2;
+constexpr int kResets = 2;         // a run that is not the row's first starts in it
 
 size_t layout_bufs(const SsmParams &p, unsigned char *base, TcBufs *t) {
   const int nb = (p.T + kQ - 1) / kQ;
@@ -152,12 +153,14 @@ struct Conv {
     }
   }
 
-  // x: the row's token 0 at the tile's channel; past: the cached inputs that
-  // precede it (or null), for a row whose first run starts at token 0.  A
-  // thread copies one 16-byte piece of every kStep-th row.
+  // x: the row's token 0 at the tile's channel; past: the convolution's cache
+  // there, or null (zeros).  The rows before the row's first run (from token
+  // `first` on) are outside the row or padding, which nothing reads: they
+  // are staged from the cache, so that the first run's windows are whole.
+  // A thread copies one 16-byte piece of every kStep-th row.
   static __device__ __forceinline__ void stage(uint32_t dst, const bf16 *x, long long st,
                                                const bf16 *past, int channels, int t0, int T,
-                                               int tid) {
+                                               int first, int tid) {
     constexpr int kP16 = TP / 8, kStep = NT / kP16;
     const int piece = tid % kP16, row0 = tid / kP16;
     const bf16 *src = x + (long long)(t0 - (kSsmTaps - 1) + row0) * st + piece * 8;
@@ -165,67 +168,52 @@ struct Conv {
     for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k) {
       const int row = row0 + k * kStep, t = t0 - (kSsmTaps - 1) + row;
       if (row < kRows) {
-        const bool ok = t >= 0 && t < T;
+        bool ok = t >= first && t < T;
         const bf16 *from = ok ? src + (long long)(k * kStep) * st : x;
-        if (t < 0 && past) from = past + (size_t)(kSsmTaps - 1 + t) * channels + piece * 8;
-        cp_async16(dst + off(row, piece), from, ok || (t < 0 && past));
+        if (t < first && past && t >= first - (kSsmTaps - 1)) {
+          from = past + (size_t)(kSsmTaps - 1 + t - first) * channels + piece * 8;
+          ok = true;
+        }
+        cp_async16(dst + off(row, piece), from, ok);
       }
     }
     cp_async_commit();
   }
 
   // f(i, u): u = SiLU(conv) of channels [CH warp, CH (warp + 1)) of the tile
-  // at the lane's i-th token, 4 lane + i.
-  template <typename F>
-  __device__ __forceinline__ void run(const unsigned char *rows, int warp, int lane, F f) const {
+  // at the lane's i-th token, 4 lane + i.  CUT: windows end where a run
+  // starts, and padding gives 0; tok holds the tokens' windows.
+  template <bool CUT, typename F>
+  __device__ __forceinline__ void run(const unsigned char *rows, int warp, int lane,
+                                      const unsigned char *tok, F f) const {
     const int ch = warp * CH;
     // rows 4 lane .. 4 lane + 6: two permutations
     const unsigned char *lo = rows + off(4 * lane, ch / 8) + ch % 8 * 2;
-    const unsigned char *hi = rows + off(min(4 * lane + 4, kRows - 1), ch / 8) + ch % 8 * 2;
+    const unsigned char *hi = rows + off(4 * lane + 4, ch / 8) + ch % 8 * 2;
     u64 x[kStrip + kSsmTaps - 1][E];
 #pragma unroll
     for (int i = 0; i < kStrip + kSsmTaps - 1; ++i)
       unpack(*reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes),
              x[i]);
+    const uint32_t marks = CUT ? *reinterpret_cast<const uint32_t *>(tok + 4 * lane) : 0;
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
       u64 u[E];
-      taps(x[i], x[i + 1], x[i + 2], x[i + 3], u);
-      f(i, u);
-    }
-  }
-
-  // The same where windows are cut by runs: tok holds the tokens' windows,
-  // past the cached inputs of the row at the tile's channel (or null).
-  template <typename F>
-  __device__ __forceinline__ void run_cut(const unsigned char *rows, int warp, int lane,
-                                          const unsigned char *tok, const bf16 *past,
-                                          int channels, F f) const {
-    const int ch = warp * CH;
-#pragma unroll 1
-    for (int i = 0; i < kStrip; ++i) {
-      u64 a[kSsmTaps][E], u[E];
-      const int j = 4 * lane + i, k = tok[j], place = k & 3;
+      if (CUT) {
+        const int k = marks >> (8 * i), place = k & 3;
+        u64 a[3][E];
 #pragma unroll
-      for (int age = 0; age < kSsmTaps; ++age) {
-        u64(&w)[E] = a[kSsmTaps - 1 - age];
-        if (age <= place) {
-          unpack(*reinterpret_cast<const Raw *>(
-                     rows + off(j + kSsmTaps - 1 - age, ch / 8) + ch % 8 * 2),
-                 w);
-        } else if ((k & 4) && past) {
-          unpack(*reinterpret_cast<const Raw *>(
-                     past + (size_t)(kSsmTaps - 1 + place - age) * channels + ch),
-                 w);
-        } else {
-#pragma unroll
-          for (int c = 0; c < E; ++c) w[c] = pk2(0.f, 0.f);
+        for (int e = 0; e < E; ++e) {
+          a[0][e] = place >= 3 ? x[i][e] : 0;        // (0 is a pair of zeros)
+          a[1][e] = place >= 2 ? x[i + 1][e] : 0;
+          a[2][e] = place >= 1 ? x[i + 2][e] : 0;
         }
-      }
-      taps(a[0], a[1], a[2], a[3], u);
-      if (!(k & 8))
+        taps(a[0], a[1], a[2], x[i + 3], u);
 #pragma unroll
-        for (int c = 0; c < E; ++c) u[c] = pk2(0.f, 0.f);
+        for (int e = 0; e < E; ++e) u[e] = k & 8 ? u[e] : 0;
+      } else {
+        taps(x[i], x[i + 1], x[i + 2], x[i + 3], u);
+      }
       f(i, u);
     }
   }
@@ -287,6 +275,13 @@ __device__ __forceinline__ const bf16 *past_of(const SsmParams &p, int b) {
                       : nullptr;
 }
 
+// Token t's window in the staged rows: how many tokens of its run precede it
+// there (all 3 in the row's first run, see Conv::stage), whether it counts.
+__device__ __forceinline__ unsigned char token_mark(const SsmToken &k) {
+  return (unsigned char)((k.first ? kSsmTaps - 1 : k.place) | (k.live ? 8 : 0));
+}
+constexpr unsigned char kWhole = (kSsmTaps - 1) | 8;
+
 // ---------------------------------------------------------------------------
 // 1. prep
 
@@ -313,9 +308,7 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     const unsigned m = __ballot_sync(0xffffffffu, k.reset);
     n = __popc(m & (0xffffffffu >> (31 - lane)));
     if (lane == 0) scount[warp] = __popc(m);
-    // the rows before token 0 are staged from the cache
-    plain = t0 + tid >= p.T ||
-            (k.live && (k.place == kSsmTaps - 1 || (row.first == 0 && t0 + tid == k.place)));
+    plain = t0 + tid >= p.T || token_mark(k) == kWhole;
   }
   plain = __syncthreads_and(plain);
   if (tid < kQ) {
@@ -323,7 +316,7 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     srun[tid] = n;
     const size_t at = (size_t)b * t.nb * kQ + t0 + tid;
     t.run[at - tid + slot_of(tid)] = k.live ? n : -1;
-    t.tok[at] = (unsigned char)(k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0));
+    t.tok[at] = token_mark(k);
   }
   if (tid == 0) {
     const int resets = scount[0] + scount[1] + scount[2] + scount[3];
@@ -407,8 +400,8 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   const bool mine = tid < TP * 4;           // 32 channels take half the threads
   Cv cv;
   if (mine) {
-    Cv::stage(smem_u32(smem), x, p.xbc_st, past && row.first == 0 ? past + ch : nullptr,
-              p.channels, t0, p.T, tid);
+    Cv::stage(smem_u32(smem), x, p.xbc_st, past ? past + ch : nullptr, p.channels, t0, p.T,
+              row.first, tid);
     cv.weights(p, ch + wch);
   }
   // whether any token's window leaves the staged rows
@@ -417,9 +410,8 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   if (tid < kQ) {
     const SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr,
                                  t0 + tid, p.T, row);
-    stok[tid] = (unsigned char)(k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0));
-    plain = t0 + tid >= p.T ||
-            (k.live && (k.place == kSsmTaps - 1 || (row.first == 0 && t0 + tid == k.place)));
+    stok[tid] = token_mark(k);
+    plain = t0 + tid >= p.T || stok[tid] == kWhole;
   }
   cp_async_wait_all();
   plain = __syncthreads_and(plain);
@@ -434,8 +426,8 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
     *reinterpret_cast<uint4 *>(hi_tile + (size_t)i * p.N * 16) = hi;
     if (!is_c) *reinterpret_cast<uint4 *>(lo_tile + (size_t)i * p.N * 16) = lo;
   };
-  if (plain) cv.run(smem, warp, lane, put);
-  else cv.run_cut(smem, warp, lane, stok, past ? past + ch : nullptr, p.channels, put);
+  if (plain) cv.template run<false>(smem, warp, lane, stok, put);
+  else cv.template run<true>(smem, warp, lane, stok, put);
 }
 
 // The inputs that the convolution's cache holds after the row.
@@ -516,7 +508,9 @@ struct StateSmem {
 //   update it.
 // A thread holds TP / 4 columns of one state row (its TMEM lane).  (With 256
 // threads, two warps on a scheduler, a block took 3.7 us instead of STATE_US.)
-template <int TP>
+// IDS: rows have segment ids (without them every block is plain, and the
+// kernel keeps its registers).
+template <int TP, bool IDS>
 __global__ void __launch_bounds__(kConv + 32, 1)
     ssm_state_kernel(const SsmParams p, const TcBufs t) {
   using L = StateSmem<TP>;
@@ -588,11 +582,11 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     }
     __syncwarp();
   } else {
-    const SsmRow row = row_of(p, b);
+    const int first = IDS ? p.rows[b].first : 0;
     const bf16 *past = past_of(p, b);
     const int ch = h * p.P + c0;
     const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
-    const bf16 *before = past && row.first == 0 ? past + ch : nullptr;
+    const bf16 *before = past ? past + ch : nullptr;
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
     const float *dec = t.dec + ((size_t)b * p.H + h) * nb;
     Cv cv;
@@ -615,7 +609,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         if (tid < kQ / 4)
           cp_async16(sb + L::kW + (i & 1) * kQ * 4 + tid * 16, wst + (size_t)i * kQ + tid * 4, true);
         Cv::stage(sb + L::kRows + (i & 1) * Cv::kBytes, x, p.xbc_st, before, p.channels, i * kQ,
-                  p.T, tid);
+                  p.T, first, tid);
       }
     };
     bool bad = false;
@@ -649,7 +643,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         reg_fence8(hi[k]);
         reg_fence8(lo[k]);
       }
-      if (a < 0.f) {     // a reset drops the state whatever it holds
+      if (IDS && a < 0.f) {     // a reset drops the state whatever it holds
 #pragma unroll
         for (int k = 0; k < kCols; ++k) s[k] = 0.f;
         a = 0.f;
@@ -661,14 +655,14 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     };
     stage(0);
     // the next block's flags and this and the last block's decay, loaded early
-    int flags = t.flags[(size_t)b * nb], flags_next;
+    int flags = IDS ? t.flags[(size_t)b * nb] : kPlain, flags_next = kPlain;
     float a_prev = 0.f, a_now = dec[0];
     int i = 0;
     for (; i < nb; ++i, flags = flags_next) {
       cp_async_wait_all();
       if (any_of_conv(bad)) break;   // a wait ran out somewhere: all leave
       stage(i + 1);
-      flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
+      if (IDS) flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
       const float a_next = i + 1 < nb ? dec[i + 1] : 0.f;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
       // the lane's i-th token: slot 8 i + lane % 8 of quarter lane / 8
@@ -694,12 +688,13 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         *reinterpret_cast<Raw *>(xo + TP / 8 * 2048 + k * 128) = lo;
       };
       const unsigned char *rows = smem + L::kRows + (i & 1) * Cv::kBytes;
-      if (flags & kPlain)
-        cv.run(rows, warp, lane, [&](int k, u64(&u)[Cv::E]) { put(k, u, false); });
+      const unsigned char *tok = t.tok + ((size_t)b * nb + i) * kQ;
+      if (!IDS || (flags & kPlain))
+        cv.template run<false>(rows, warp, lane, tok,
+                               [&](int k, u64(&u)[Cv::E]) { put(k, u, false); });
       else
-        cv.run_cut(rows, warp, lane, t.tok + ((size_t)b * nb + i) * kQ,
-                   past ? past + ch : nullptr, p.channels,
-                   [&](int k, u64(&u)[Cv::E]) { put(k, u, true); });
+        cv.template run<true>(rows, warp, lane, tok,
+                              [&](int k, u64(&u)[Cv::E]) { put(k, u, true); });
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
@@ -833,6 +828,20 @@ __global__ void __launch_bounds__(256, 2)
       scum[tid] = t.cum[at + tid];
     } else {
       scumj[tid - kQ] = t.cumj[at + tid - kQ];
+    }
+    // into L2 while this item is computed: its rows of z, the next x and S
+    if (p.z && tid >= kQ) {
+      const int tok = tid - kQ;
+      if (t0 + tok < p.T)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            static_cast<const bf16 *>(p.z) + (size_t)b * p.z_sb + (long long)(t0 + tok) * p.z_st +
+            h * p.P + c));
+    }
+    if (tid == 0 && k + 1 < n_items) {
+      const int h1 = h_lo + (k + 1) / subs, c1 = (k + 1) % subs * PT;
+      const size_t at1 = ((size_t)b * nb + blk) * p.H + h1;
+      prefetch_l2(t.xt + at1 * kQ * p.P * 2 + (size_t)c1 * kQ * 2, kQ * PT * 2);
+      prefetch_l2(t.st + at1 * N * p.P * 2 + (size_t)c1 * N * 2, N * PT * 2);
     }
     if (!mbar_wait(bar_xs, k & 1)) give_up();
     if (__syncthreads_or(bad)) break;
@@ -981,14 +990,13 @@ cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
   return cudaGetLastError();
 }
 
-template <int TP>
+template <int TP, bool IDS>
 cudaError_t launch_state(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(ssm_state_kernel<TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)StateSmem<TP>::kBytes);
+  auto kern = ssm_state_kernel<TP, IDS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)StateSmem<TP>::kBytes);
   if (e != cudaSuccess) return e;
-  ssm_state_kernel<TP><<<(unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, StateSmem<TP>::kBytes,
-                         cs>>>(p, t);
+  kern<<<(unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, StateSmem<TP>::kBytes, cs>>>(p, t);
   return cudaGetLastError();
 }
 
@@ -1023,7 +1031,10 @@ cudaError_t launch_ssm_tc(const SsmParams &p, uint32_t *status, cudaStream_t cs)
   // 64-column tiles halve the traffic of B's tiles; 32 where they would
   // leave SMs without a CTA
   const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
-  e = narrow ? launch_state<32>(p, t, cs) : launch_state<64>(p, t, cs);
+  if (p.segment_ids)
+    e = narrow ? launch_state<32, true>(p, t, cs) : launch_state<64, true>(p, t, cs);
+  else
+    e = narrow ? launch_state<32, false>(p, t, cs) : launch_state<64, false>(p, t, cs);
   if (e != cudaSuccess) return e;
   return p.P == 32 ? launch_out<32>(p, t, cs) : launch_out<64>(p, t, cs);
 }
