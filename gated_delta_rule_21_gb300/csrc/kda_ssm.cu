@@ -56,19 +56,42 @@ __device__ __forceinline__ SsmRow simt_row(const SsmParams &p, int b) {
 
 constexpr int kThreads = 256, kCols = 32, kTok = 32, kWarps = kThreads / 32;
 
-// One CTA per (row, head, 32 columns), token by token in fp32.  Warp w holds
-// states [w N / 8, (w + 1) N / 8) of column `lane` in registers; 32 tokens of
-// B, C and d x are made in shared memory at a time, and the warps' shares of
-// y are added there.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p) {
+// How a row is cut for the CUDA-core kernel: `segs` segments of `len` tokens
+// (a multiple of kTok), as many as fill the GPU four times over and no shorter
+// than 64 tokens.  With more than one, a first pass runs every segment but the
+// last from a zero state, the states that enter the segments are chained,
+// and a second pass makes y: the sums a state takes part in grow, but a
+// short row of few heads no longer waits for one chain of tokens (3 rows of
+// 997 tokens, 6 heads: 576 us in one chain).
+struct SimtCut {
+  int segs, len;
+};
+SimtCut simt_cut(int B, int T, int H, int P) {
+  const long long chains = (long long)B * H * (P / kCols), want = (4 * 152 + chains - 1) / chains;
+  const int most = (T + 63) / 64;
+  const int n = (int)(want < most ? want : most);
+  SimtCut c;
+  c.len = ((T + n - 1) / n + kTok - 1) / kTok * kTok;
+  c.segs = (T + c.len - 1) / c.len;
+  return c;
+}
+
+// One CTA per (segment, row, head, 32 columns), token by token in fp32.  Warp
+// w holds states [w N / 8, (w + 1) N / 8) of column `lane` in registers; 32
+// tokens of B, C and x are made in shared memory at a time, a thread walking
+// one channel's tokens with its window in registers, and the warps' shares
+// of y are added there.  FIRST: the first pass (states and decays only).
+template <typename T, int N, bool FIRST>
+__global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, const SimtCut cut,
+                                                            float *seg_state, float *seg_decay) {
   constexpr int NS = N / kWarps;
   extern __shared__ __align__(16) float sm[];
   float *sB = sm, *sC = sB + kTok * N, *sX = sC + kTok * N, *sY = sX + kTok * kCols;
   __shared__ float sa[kTok], sd[kTok];
-  __shared__ int sreset[kTok], slive[kTok];
+  __shared__ int smark[kTok];            // place | first << 2 | live << 3 | reset << 4
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tiles = p.P / kCols, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int tiles = p.P / kCols, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles % (p.B * p.H);
+  const int seg = blockIdx.x / tiles / (p.B * p.H);
   const int h = bh % p.H, b = bh / p.H, c0 = tile * kCols, g = h / (p.H / p.G);
   const int32_t *ids = p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr;
   const SsmRow row = simt_row(p, b);
@@ -79,61 +102,98 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p) {
                       : nullptr;
   const int cx = h * p.P + c0, cb = p.H * p.P + g * N, cc = cb + p.G * N;
   const float A = p.A[h], D = p.D ? p.D[h] : 0.f, db = p.dt_bias ? p.dt_bias[h] : 0.f;
-  float s[NS];
-  const size_t state = (((size_t)b * p.H + h) * N + warp * NS) * p.P + c0 + lane;
+  const size_t mine = (size_t)(warp * NS) * p.P + c0 + lane, per = (size_t)N * p.P;
+  const float *enter = cut.segs > 1 ? seg_state + ((size_t)seg * p.B * p.H + bh) * per
+                       : p.initial_state ? p.initial_state + (size_t)bh * per : nullptr;
+  float s[NS], decay = 1.f;
 #pragma unroll
-  for (int j = 0; j < NS; ++j)
-    s[j] = p.initial_state ? p.initial_state[state + (size_t)j * p.P] : 0.f;
-  for (int t0 = 0; t0 < p.T; t0 += kTok) {
-    const int n = min(kTok, p.T - t0);
+  for (int j = 0; j < NS; ++j) s[j] = !FIRST && enter ? enter[mine + (size_t)j * p.P] : 0.f;
+  const int end = min(p.T, (seg + 1) * cut.len);
+  for (int t0 = seg * cut.len; t0 < end; t0 += kTok) {
+    const int n = min(kTok, end - t0);
     __syncthreads();
-    if (tid < n) {
-      const SsmToken k = ssm_token(ids, t0 + tid, p.T, row);
-      const T *dt = static_cast<const T *>(p.dt) + (size_t)b * p.dt_sb +
-                    (long long)(t0 + tid) * p.dt_st;
-      const float d = k.live ? ssm_softplus(to_f32(dt[h]) + db) : 0.f;
+    if (tid < kTok) {
+      SsmToken k = {};
+      float d = 0.f;
+      if (tid < n) {
+        k = ssm_token(ids, t0 + tid, p.T, row);
+        const T *dt = static_cast<const T *>(p.dt) + (size_t)b * p.dt_sb +
+                      (long long)(t0 + tid) * p.dt_st;
+        if (k.live) d = ssm_softplus(to_f32(dt[h]) + db);
+      }
       sd[tid] = d;
       sa[tid] = expf(d * A);
-      sreset[tid] = k.reset;
-      slive[tid] = k.live;
+      smark[tid] = k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0) | (k.reset ? 16 : 0);
     }
     __syncthreads();
-    for (int i = tid; i < n * (2 * N + kCols); i += kThreads) {
-      const int t = i / (2 * N + kCols), j = i - t * (2 * N + kCols);
+    for (int j = tid; j < 2 * N + kCols; j += kThreads) {
+      if (FIRST && j >= N && j < 2 * N) continue;      // C is not needed
       const int c = j < N ? cb + j : j < 2 * N ? cc + j - N : cx + j - 2 * N;
-      float u = 0.f;
-      if (slive[t]) {
-        const SsmToken k = ssm_token(ids, t0 + t, p.T, row);
-        u = p.bias ? p.bias[c] : 0.f;
+      const float4 w = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)c);
+      const float bias = p.bias ? p.bias[c] : 0.f;
+      float win[kSsmTaps - 1];                         // the 3 inputs before, oldest first
 #pragma unroll
-        for (int age = 0; age < kSsmTaps; ++age)
-          u += p.w[4 * c + 3 - age] *
-               ssm_tap(x, p.xbc_st, past, p.channels, c, t0 + t, age, k);
-        u = u / (1.f + expf(-u));
+      for (int i = 0; i < kSsmTaps - 1; ++i) {
+        const int t = t0 - (kSsmTaps - 1) + i;
+        win[i] = t >= 0 ? to_f32(x[(long long)t * p.xbc_st + c]) : 0.f;
       }
-      if (j < N) sB[t * N + j] = u * sd[t];
-      else if (j < 2 * N) sC[t * N + j - N] = u;
-      else sX[t * kCols + j - 2 * N] = u;
+      const T *xc = x + (long long)t0 * p.xbc_st + c;
+#pragma unroll 8
+      for (int t = 0; t < kTok; ++t) {
+        const float xv = t < n ? to_f32(xc[(long long)t * p.xbc_st]) : 0.f;
+        const int mark = smark[t], place = mark & 3;
+        float a[kSsmTaps - 1];
+#pragma unroll
+        for (int age = 1; age < kSsmTaps; ++age) {
+          float v = win[kSsmTaps - 1 - age];
+          if (place < age)
+            v = (mark & 4) && past
+                    ? to_f32(past[(size_t)(kSsmTaps - 1 + place - age) * p.channels + c])
+                    : 0.f;
+          a[kSsmTaps - 1 - age] = v;
+        }
+        float u = bias + w.w * xv + w.z * a[2] + w.y * a[1] + w.x * a[0];
+        u = mark & 8 ? u / (1.f + expf(-u)) : 0.f;
+        if (j < N) sB[t * N + j] = u * sd[t];
+        else if (j < 2 * N) sC[t * N + j - N] = u;
+        else sX[t * kCols + j - 2 * N] = u;
+        win[0] = win[1];
+        win[1] = win[2];
+        win[2] = xv;
+      }
     }
     __syncthreads();
     for (int t = 0; t < n; ++t) {
-      float a = sa[t], acc = 0.f;
-      if (sreset[t]) a = 0.f;
-      const float xv = sX[t * kCols + lane];
-      const float *pb = sB + t * N + warp * NS, *pc = sC + t * N + warp * NS;
+      const float a = sa[t], xv = sX[t * kCols + lane];
+      const float4 *pb = reinterpret_cast<const float4 *>(sB + t * N + warp * NS),
+                   *pc = reinterpret_cast<const float4 *>(sC + t * N + warp * NS);
+      float acc = 0.f;
+      if (smark[t] & 16) {       // a reset drops the state whatever it holds
+        decay = 0.f;
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        // a reset drops the state whatever it holds
-        s[j] = (sreset[t] ? 0.f : a * s[j]) + pb[j] * xv;
-        acc += pc[j] * s[j];
+        for (int j = 0; j < NS; ++j) s[j] = 0.f;
       }
-      sY[(warp * kTok + t) * kCols + lane] = acc;
+      if (FIRST) decay *= a;
+#pragma unroll
+      for (int j = 0; j < NS / 4; ++j) {
+        const float4 bv = pb[j];
+        s[4 * j] = fmaf(a, s[4 * j], bv.x * xv);
+        s[4 * j + 1] = fmaf(a, s[4 * j + 1], bv.y * xv);
+        s[4 * j + 2] = fmaf(a, s[4 * j + 2], bv.z * xv);
+        s[4 * j + 3] = fmaf(a, s[4 * j + 3], bv.w * xv);
+        if (!FIRST) {
+          const float4 cv = pc[j];
+          acc += cv.x * s[4 * j] + cv.y * s[4 * j + 1] + cv.z * s[4 * j + 2] + cv.w * s[4 * j + 3];
+        }
+      }
+      if (!FIRST) sY[(warp * kTok + t) * kCols + lane] = acc;
     }
+    if (FIRST) continue;
     __syncthreads();
     for (int i = tid; i < n * kCols; i += kThreads) {
       const int t = i / kCols, c = i % kCols;
       float v = 0.f;
-      if (slive[t]) {
+      if (smark[t] & 8) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += sY[(w * kTok + t) * kCols + c];
         v += D * sX[t * kCols + c];
@@ -147,7 +207,15 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p) {
           from_f32<T>(v);
     }
   }
-  if (p.conv_out) {      // head h moves its share of the channels
+  if (FIRST) {     // what the segment adds to the state that enters the next
+    float *out = seg_state + ((size_t)(seg + 1) * p.B * p.H + bh) * per;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) out[mine + (size_t)j * p.P] = s[j];
+    if (tid == 0 && tile == 0) seg_decay[(size_t)seg * p.B * p.H + bh] = decay;
+    return;
+  }
+  if (seg + 1 < cut.segs) return;
+  if (p.conv_out) {      // the last segments' CTAs share a row's channels
     const SsmToken k = ssm_token(ids, row.last, p.T, row);
     T *out = static_cast<T *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels;
     const int ctas = p.H * tiles, me = h * tiles + tile;
@@ -159,17 +227,49 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p) {
   }
   if (p.final_state) {
 #pragma unroll
-    for (int j = 0; j < NS; ++j) p.final_state[state + (size_t)j * p.P] = s[j];
+    for (int j = 0; j < NS; ++j) p.final_state[(size_t)bh * per + mine + (size_t)j * p.P] = s[j];
+  }
+}
+
+// The states that enter the segments, in place: S_0 is the initial state,
+// S_{i+1} = decay_i S_i + what segment i added.
+__global__ void __launch_bounds__(256)
+    ssm_simt_chain_kernel(const float *initial, float *seg_state, const float *seg_decay, int segs,
+                          int heads, size_t per) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, n = (size_t)heads * per;
+  if (i >= n) return;
+  const int bh = (int)(i / per);
+  float s = initial ? initial[i] : 0.f;
+  seg_state[i] = s;
+  for (int k = 0; k + 1 < segs; ++k) {
+    const float a = seg_decay[(size_t)k * heads + bh];
+    // decay 0 (a reset, or underflow) drops the state whatever it holds
+    s = (a == 0.f ? 0.f : a * s) + seg_state[(size_t)(k + 1) * n + i];
+    seg_state[(size_t)(k + 1) * n + i] = s;
   }
 }
 
 template <typename T, int N>
 cudaError_t launch_simt(const SsmParams &p, cudaStream_t cs) {
   const size_t smem = sizeof(float) * (2 * kTok * N + kTok * kCols * (1 + kWarps));
-  const cudaError_t e = cudaFuncSetAttribute(
-      ssm_simt_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const SimtCut cut = simt_cut(p.B, p.T, p.H, p.P);
+  const unsigned chains = (unsigned)(p.B * p.H * (p.P / kCols));
+  float *state = reinterpret_cast<float *>(p.ws);
+  float *decay = state + (size_t)cut.segs * p.B * p.H * N * p.P;
+  cudaError_t e = cudaFuncSetAttribute(ssm_simt_kernel<T, N, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(ssm_simt_kernel<T, N, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  ssm_simt_kernel<T, N><<<(unsigned)(p.B * p.H * (p.P / kCols)), kThreads, smem, cs>>>(p);
+  if (cut.segs > 1) {
+    ssm_simt_kernel<T, N, true>
+        <<<chains * (cut.segs - 1), kThreads, smem, cs>>>(p, cut, state, decay);
+    const size_t per = (size_t)N * p.P, n = (size_t)p.B * p.H * per;
+    ssm_simt_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, cs>>>(
+        p.initial_state, state, decay, cut.segs, p.B * p.H, per);
+  }
+  ssm_simt_kernel<T, N, false><<<chains * cut.segs, kThreads, smem, cs>>>(p, cut, state, decay);
   return cudaGetLastError();
 }
 
@@ -177,6 +277,13 @@ template <typename T>
 cudaError_t launch_simt_t(const SsmParams &p, cudaStream_t cs) {
   return p.N == 32 ? launch_simt<T, 32>(p, cs) : p.N == 64 ? launch_simt<T, 64>(p, cs)
                                                            : launch_simt<T, 128>(p, cs);
+}
+
+// The segments' states and decays.
+size_t simt_bytes(const kda_ssm_shape *s) {
+  const SimtCut cut = simt_cut(s->B, s->T, s->H, s->P);
+  if (cut.segs == 1) return 0;
+  return align_up(sizeof(float) * (size_t)cut.segs * s->B * s->H * ((size_t)s->N * s->P + 1), 256);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -193,7 +300,8 @@ extern "C" {
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape *s, kda_impl impl) {
   if (check_ssm_shape(s) != KDA_OK) return 0;
   const bool bf16 = s->dtype == KDA_DTYPE_BF16;
-  if (impl == KDA_IMPL_SIMT || (impl == KDA_IMPL_AUTO && !bf16)) return rows_bytes(s->B);
+  if (impl == KDA_IMPL_SIMT || (impl == KDA_IMPL_AUTO && !bf16))
+    return rows_bytes(s->B) + simt_bytes(s);
   if ((impl != KDA_IMPL_AUTO && impl != KDA_IMPL_TC) || !bf16) return 0;
   SsmParams p = {};
   p.B = s->B; p.T = s->T; p.H = s->H; p.P = s->P; p.N = s->N; p.G = s->G;
