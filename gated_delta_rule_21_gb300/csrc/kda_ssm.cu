@@ -288,6 +288,14 @@ size_t simt_bytes(const kda_ssm_shape *s) {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// AUTO: bf16 on the tensor cores.  fp32 there too from a size on that the CUDA
+// cores take longer for; below it they are as fast and round less.
+bool use_tc(const kda_ssm_shape *s, kda_impl impl) {
+  if (impl != KDA_IMPL_AUTO) return impl == KDA_IMPL_TC;
+  if (s->dtype == KDA_DTYPE_BF16) return true;
+  return (long long)s->B * s->T * s->H * s->P >= (1ll << 21);
+}
+
 size_t rows_bytes(int B) { return align_up(sizeof(WsHeader) + sizeof(SsmRow) * (size_t)B, 256); }
 
 }  // namespace
@@ -300,12 +308,11 @@ extern "C" {
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape *s, kda_impl impl) {
   if (check_ssm_shape(s) != KDA_OK) return 0;
   const bool bf16 = s->dtype == KDA_DTYPE_BF16;
-  if (impl == KDA_IMPL_SIMT || (impl == KDA_IMPL_AUTO && !bf16))
-    return rows_bytes(s->B) + simt_bytes(s);
-  if ((impl != KDA_IMPL_AUTO && impl != KDA_IMPL_TC) || !bf16) return 0;
+  if (impl != KDA_IMPL_AUTO && impl != KDA_IMPL_SIMT && impl != KDA_IMPL_TC) return 0;
+  if (!use_tc(s, impl)) return rows_bytes(s->B) + simt_bytes(s);
   SsmParams p = {};
   p.B = s->B; p.T = s->T; p.H = s->H; p.P = s->P; p.N = s->N; p.G = s->G;
-  return rows_bytes(s->B) + ssm_tc_bytes(p);
+  return rows_bytes(s->B) + ssm_tc_bytes(p, !bf16);
 }
 
 kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt, const void *z,
@@ -352,8 +359,8 @@ kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt, 
     e = cudaGetLastError();
     if (e != cudaSuccess) return KDA_ERR_CUDA;
   }
-  if (bf16 && impl != KDA_IMPL_SIMT)
-    e = launch_ssm_tc(p, &reinterpret_cast<WsHeader *>(workspace)->status, cs);
+  if (use_tc(s, impl))
+    e = launch_ssm_tc(p, !bf16, &reinterpret_cast<WsHeader *>(workspace)->status, cs);
   else
     e = bf16 ? launch_simt_t<__nv_bfloat16>(p, cs) : launch_simt_t<float>(p, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

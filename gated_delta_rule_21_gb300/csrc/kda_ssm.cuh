@@ -83,9 +83,9 @@ __device__ __forceinline__ float ssm_softplus(float x) {
 
 kda_status check_ssm_shape(const kda_ssm_shape *s);
 
-// Tensor-core path (kda_ssm_tc.cu), bf16: its workspace after the row table,
+// Tensor-core path (kda_ssm_tc.cu): its workspace after the row table,
 // and its launches (with segment ids the row table must be there).
-size_t ssm_tc_bytes(const SsmParams &p);
-cudaError_t launch_ssm_tc(const SsmParams &p, uint32_t *status, cudaStream_t cs);
+size_t ssm_tc_bytes(const SsmParams &p, bool f32);
+cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaStream_t cs);
 
 }  // namespace kda

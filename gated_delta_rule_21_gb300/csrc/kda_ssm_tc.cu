@@ -53,7 +53,9 @@ struct TcBufs {
   unsigned char *bhi, *blo, *ct;   // [B][nb][G] tiles (slot, state), op_off(slot, n, N)
   unsigned char *xt;               // [B][nb][H] tiles of x, mn_off(p, slot, 128)
   unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
+  unsigned char *clo, *xlo, *slo;  // fp32 inputs: the second parts of ct, xt and st
   float *ein, *cum, *cumj;         // [B][H][nb * 128] by slot, see prep_factors
+  float *cum_lo, *cumj_lo;         // fp32 inputs: what cum and cumj leave of the sums
   float *wst;                      // likewise, by token
   float *dec;                      // [B][H][nb]: e^{c_127}, or -1: the block resets the state
   int *run;                        // [B][nb * 128] by slot: resets so far in the block, -1: padding
@@ -65,7 +67,7 @@ struct TcBufs {
 constexpr int kPlain = 1;          // every token has its whole window in the staged rows
 constexpr int kResets = 2;         // a run that is not the row's first starts in it
 
-size_t layout_bufs(const SsmParams &p, unsigned char *base, TcBufs *t) {
+size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t) {
   const int nb = (p.T + kQ - 1) / kQ;
   const size_t bt = (size_t)p.B * nb, toks = bt * kQ;
   size_t off = 0;
@@ -80,6 +82,11 @@ size_t layout_bufs(const SsmParams &p, unsigned char *base, TcBufs *t) {
   t->ct = take(bt * p.G * kQ * p.N * 2);
   t->xt = take(bt * p.H * kQ * p.P * 2);
   t->st = take(bt * p.H * p.N * p.P * 2);
+  t->clo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
+  t->xlo = take(f32 ? bt * p.H * kQ * p.P * 2 : 0);
+  t->slo = take(f32 ? bt * p.H * p.N * p.P * 2 : 0);
+  t->cum_lo = (float *)take(f32 ? toks * p.H * 4 : 0);
+  t->cumj_lo = (float *)take(f32 ? toks * p.H * 4 : 0);
   t->ein = (float *)take(toks * p.H * 4);
   t->wst = (float *)take(toks * p.H * 4);
   t->cum = (float *)take(toks * p.H * 4);
@@ -114,28 +121,34 @@ __device__ __forceinline__ float rcp(float x) {
 // tile's rows and the 3 before it are staged by cp.async; a warp owns CH
 // channels and a lane 4 consecutive tokens.  Channels are kept in pairs for
 // the packed arithmetic.
-template <int TP, int CH, int NT>
+template <int BYTES>
+using Word = typename std::conditional<
+    BYTES == 16, uint4, typename std::conditional<BYTES == 8, uint2, uint32_t>::type>::type;
+
+template <typename T, int TP, int CH, int NT>
 struct Conv {
   static_assert(TP / CH * 32 == NT, "one warp per CH channels");
+  static_assert(TP * sizeof(T) == 128 || TP * sizeof(T) == 64, "row bytes");
   static constexpr int E = CH / 2;                         // pairs of channels per lane
   static constexpr int kStrip = 4;
   static constexpr int kRows = kQ + kSsmTaps - 1;
-  static constexpr uint32_t kRowBytes = TP * 2;
+  static constexpr uint32_t kRowBytes = TP * sizeof(T);
   static constexpr uint32_t kBytes = kRows * kRowBytes;
-  using Raw = typename std::conditional<
-      CH == 8, uint4, typename std::conditional<CH == 4, uint2, uint32_t>::type>::type;
+  using Raw = Word<CH * sizeof(T)>;
 
   // 16-byte pieces of a row, permuted by the row's strip: the lanes of a
   // warp read rows 4 apart.
   static __device__ __forceinline__ uint32_t off(int row, int piece16) {
     return (uint32_t)(row * kRowBytes) +
-           (uint32_t)((piece16 ^ (TP == 64 ? row >> 2 & 7 : row >> 3 & 3)) << 4);
+           (uint32_t)((piece16 ^ (kRowBytes == 128 ? row >> 2 & 7 : row >> 3 & 3)) << 4);
   }
   static __device__ __forceinline__ void unpack(const Raw &a, u64 (&x)[E]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&a);
 #pragma unroll
     for (int i = 0; i < E; ++i)
-      x[i] = pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      x[i] = sizeof(T) == 4
+                 ? pk2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]))
+                 : pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 
   u64 wt[kSsmTaps][E], bias[E];
@@ -158,20 +171,20 @@ struct Conv {
   // `first` on) are outside the row or padding, which nothing reads: they
   // are staged from the cache, so that the first run's windows are whole.
   // A thread copies one 16-byte piece of every kStep-th row.
-  static __device__ __forceinline__ void stage(uint32_t dst, const bf16 *x, long long st,
-                                               const bf16 *past, int channels, int t0, int T,
+  static __device__ __forceinline__ void stage(uint32_t dst, const T *x, long long st,
+                                               const T *past, int channels, int t0, int len,
                                                int first, int tid) {
-    constexpr int kP16 = TP / 8, kStep = NT / kP16;
+    constexpr int kP16 = kRowBytes / 16, kStep = NT / kP16, kEl = 16 / sizeof(T);
     const int piece = tid % kP16, row0 = tid / kP16;
-    const bf16 *src = x + (long long)(t0 - (kSsmTaps - 1) + row0) * st + piece * 8;
+    const T *src = x + (long long)(t0 - (kSsmTaps - 1) + row0) * st + piece * kEl;
 #pragma unroll
     for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k) {
       const int row = row0 + k * kStep, t = t0 - (kSsmTaps - 1) + row;
       if (row < kRows) {
-        bool ok = t >= first && t < T;
-        const bf16 *from = ok ? src + (long long)(k * kStep) * st : x;
+        bool ok = t >= first && t < len;
+        const T *from = ok ? src + (long long)(k * kStep) * st : x;
         if (t < first && past && t >= first - (kSsmTaps - 1)) {
-          from = past + (size_t)(kSsmTaps - 1 + t - first) * channels + piece * 8;
+          from = past + (size_t)(kSsmTaps - 1 + t - first) * channels + piece * kEl;
           ok = true;
         }
         cp_async16(dst + off(row, piece), from, ok);
@@ -186,10 +199,10 @@ struct Conv {
   template <bool CUT, typename F>
   __device__ __forceinline__ void run(const unsigned char *rows, int warp, int lane,
                                       const unsigned char *tok, F f) const {
-    const int ch = warp * CH;
+    const int at = warp * CH * (int)sizeof(T);
     // rows 4 lane .. 4 lane + 6: two permutations
-    const unsigned char *lo = rows + off(4 * lane, ch / 8) + ch % 8 * 2;
-    const unsigned char *hi = rows + off(4 * lane + 4, ch / 8) + ch % 8 * 2;
+    const unsigned char *lo = rows + off(4 * lane, at / 16) + at % 16;
+    const unsigned char *hi = rows + off(4 * lane + 4, at / 16) + at % 16;
     u64 x[kStrip + kSsmTaps - 1][E];
 #pragma unroll
     for (int i = 0; i < kStrip + kSsmTaps - 1; ++i)
@@ -233,7 +246,7 @@ struct Conv {
   }
 };
 
-using Unpack8 = Conv<64, 8, 256>;
+using Unpack8 = Conv<bf16, 64, 8, 256>;      // for its unpack
 
 // Pairs as bf16, and what that leaves, again as bf16 (R: uint4 or uint2).
 template <typename R, int E>
@@ -264,13 +277,24 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16(v[6], v[7]));
 }
 
+// What `hi` leaves of the values.
+__device__ __forceinline__ void rest8(const uint4 &hi, float (&v)[8]) {
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] -= __uint_as_float(h[i] << 16);
+    v[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+  }
+}
+
 __device__ __forceinline__ SsmRow row_of(const SsmParams &p, int b) {
   if (p.segment_ids) return p.rows[b];
   SsmRow r = {0, p.T, p.T - 1, 0};
   return r;
 }
-__device__ __forceinline__ const bf16 *past_of(const SsmParams &p, int b) {
-  return p.conv_state ? static_cast<const bf16 *>(p.conv_state) +
+template <typename T>
+__device__ __forceinline__ const T *past_of(const SsmParams &p, int b) {
+  return p.conv_state ? static_cast<const T *>(p.conv_state) +
                             (size_t)b * (kSsmTaps - 1) * p.channels
                       : nullptr;
 }
@@ -291,7 +315,10 @@ constexpr unsigned char kWhole = (kSsmTaps - 1) | 8;
 //   wst  = d 2^(sum of a after the token) where the token reaches the state
 //          that leaves the block, else 0 (summed from the end: exact where
 //          it matters)
-// A warp takes a head, a lane 4 tokens.
+// A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums are made in
+// 64 bits and cum, cumj kept in two floats: a factor e^(c_r - c_j) is as exact
+// as the difference, however far the sums have run.
+template <typename T>
 __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t, int b, int blk,
                                              unsigned char *smem) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -322,7 +349,9 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     const int resets = scount[0] + scount[1] + scount[2] + scount[3];
     t.flags[(size_t)b * t.nb + blk] = (plain ? kPlain : 0) | (resets ? kResets : 0);
   }
-  const bf16 *dt = static_cast<const bf16 *>(p.dt) + (size_t)b * p.dt_sb;
+  constexpr bool kF32 = sizeof(T) == 4;
+  using R = typename std::conditional<kF32, double, float>::type;
+  const T *dt = static_cast<const T *>(p.dt) + (size_t)b * p.dt_sb;
   for (int h0 = 0; h0 < p.H; h0 += 32) {
     const int nh = min(32, p.H - h0);
     __syncthreads();
@@ -336,33 +365,34 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     }
     __syncthreads();
     for (int hh = warp; hh < nh; hh += kPrep / 32) {
-      const float a2 = p.A[h0 + hh] * kLog2e;
-      float d[4], a[4], pre[4], suf[4];
+      const R a2 = (R)p.A[h0 + hh] * (R)1.4426950408889634;
+      float d[4];
+      R a[4], pre[4], suf[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         d[i] = sdt[(lane * 4 + i) * 33 + hh];
-        a[i] = d[i] > 0.f ? d[i] * a2 : 0.f;
+        a[i] = d[i] > 0.f ? d[i] * a2 : (R)0;
       }
       pre[0] = a[0];
 #pragma unroll
       for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + a[i];
-      suf[3] = 0.f;
+      suf[3] = 0;
 #pragma unroll
       for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + a[i + 1];
-      const float sum = pre[3];
-      float before = sum, after = sum;
+      const R sum = pre[3];
+      R before = sum, after = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, before, o);
-        const float v = __shfl_down_sync(0xffffffffu, after, o);
+        const R u = __shfl_up_sync(0xffffffffu, before, o);
+        const R v = __shfl_down_sync(0xffffffffu, after, o);
         if (lane >= o) before += u;
         if (lane + o < 32) after += v;
       }
-      const float total = __shfl_sync(0xffffffffu, before, 31);
+      const R total = __shfl_sync(0xffffffffu, before, 31);
       before = __shfl_up_sync(0xffffffffu, before, 1);
       after = __shfl_down_sync(0xffffffffu, after, 1);
-      if (lane == 0) before = 0.f;
-      if (lane == 31) after = 0.f;
+      if (lane == 0) before = 0;
+      if (lane == 31) after = 0;
       const int last = srun[kQ - 1];
       const size_t at = (((size_t)b * p.H + h0 + hh) * t.nb + blk) * kQ;
       float4 wst;
@@ -370,22 +400,36 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int run = srun[lane * 4 + i];
-        const float c = before + pre[i];
+        const R c = before + pre[i];
         const size_t s = at + slot_of(lane * 4 + i);
-        t.ein[s] = run == 0 ? exp2f(c) : 0.f;
-        t.cum[s] = c;
-        t.cumj[s] = c - log2f(d[i]);     // d = 0: +inf, a factor of 0
-        fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : 0.f;
+        t.ein[s] = run == 0 ? exp2f((float)c) : 0.f;
+        t.cum[s] = (float)c;
+        if constexpr (kF32) {
+          const double j = c - log2((double)d[i]);     // d = 0: +inf, a factor of 0
+          t.cum_lo[s] = (float)(c - (double)(float)c);
+          t.cumj[s] = (float)j;
+          t.cumj_lo[s] = d[i] > 0.f ? (float)(j - (double)(float)j) : 0.f;
+        } else {
+          t.cumj[s] = c - log2f(d[i]);
+        }
+        fw[i] = run == last ? d[i] * exp2f((float)(suf[i] + after)) : 0.f;
       }
       *reinterpret_cast<float4 *>(t.wst + at + lane * 4) = wst;
       if (lane == 0)
-        t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] = last == 0 ? exp2f(total) : -1.f;
+        t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] =
+            last == 0 ? exp2f((float)total) : -1.f;
     }
   }
 }
 
+// Channels per warp in prep: 16 bytes of them.
+template <typename T>
+constexpr int kPrepCh = 16 / (int)sizeof(T);
+template <typename T, int TP>
+using PrepConv = Conv<T, TP, kPrepCh<T>, TP / kPrepCh<T> * 32>;
+
 // The convolution of TP channels of B or C into its operand tiles.
-template <int TP>
+template <typename T, int TP>
 __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, int b, int blk,
                                           int g, int part, unsigned char *smem) {
   const int tid = threadIdx.x, t0 = blk * kQ;
@@ -393,11 +437,12 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   const int n0 = (is_c ? part - p.N / TP : part) * TP;
   const int ch = p.H * p.P + (is_c ? p.G * p.N : 0) + g * p.N + n0;
   const SsmRow row = row_of(p, b);
-  const bf16 *past = past_of(p, b);
-  const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
-  using Cv = Conv<TP, 8, TP * 4>;
-  const int warp = tid >> 5, lane = tid & 31, wch = warp * 8;
-  const bool mine = tid < TP * 4;           // 32 channels take half the threads
+  const T *past = past_of<T>(p, b);
+  const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
+  using Cv = PrepConv<T, TP>;
+  using Out = Word<2 * kPrepCh<T>>;
+  const int warp = tid >> 5, lane = tid & 31, wch = warp * kPrepCh<T>;
+  const bool mine = warp < TP / kPrepCh<T>;   // 32 bf16 channels take half the warps
   Cv cv;
   if (mine) {
     Cv::stage(smem_u32(smem), x, p.xbc_st, past ? past + ch : nullptr, p.channels, t0, p.T,
@@ -418,27 +463,30 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   if (!mine) return;
   // the lane's i-th token: row 8 i + lane % 8 of quarter lane / 8
   const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2 +
-                      (size_t)(lane >> 3) * 4 * p.N * 16 + (lane & 7) * 16 + (n0 + wch) / 8 * 128;
-  unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile, *lo_tile = t.blo + tile;
-  auto put = [&](int i, u64(&u)[4]) {
-    uint4 hi, lo;
+                      (size_t)(lane >> 3) * 4 * p.N * 16 + (lane & 7) * 16 +
+                      (n0 + wch) / 8 * 128 + wch % 8 * 2;
+  unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile, *lo_tile = (is_c ? t.clo : t.blo) + tile;
+  const bool two = !is_c || sizeof(T) == 4;
+  auto put = [&](int i, u64(&u)[Cv::E]) {
+    Out hi, lo;
     split(u, hi, lo);
-    *reinterpret_cast<uint4 *>(hi_tile + (size_t)i * p.N * 16) = hi;
-    if (!is_c) *reinterpret_cast<uint4 *>(lo_tile + (size_t)i * p.N * 16) = lo;
+    *reinterpret_cast<Out *>(hi_tile + (size_t)i * p.N * 16) = hi;
+    if (two) *reinterpret_cast<Out *>(lo_tile + (size_t)i * p.N * 16) = lo;
   };
   if (plain) cv.template run<false>(smem, warp, lane, stok, put);
   else cv.template run<true>(smem, warp, lane, stok, put);
 }
 
 // The inputs that the convolution's cache holds after the row.
+template <typename T>
 __device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) {
   const SsmRow row = row_of(p, b);
-  const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb, *past = past_of(p, b);
+  const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb, *past = past_of<T>(p, b);
   SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr, row.last, p.T,
                          row);
   const int c = part * kPrep + threadIdx.x;
   if (c >= p.channels) return;
-  bf16 *out = static_cast<bf16 *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels + c;
+  T *out = static_cast<T *>(p.conv_out) + (size_t)b * (kSsmTaps - 1) * p.channels + c;
 #pragma unroll
   for (int i = 0; i < kSsmTaps - 1; ++i)
     out[(size_t)i * p.channels] = ssm_cached(x, p.xbc_st, past, p.channels, c, i, row.last, k);
@@ -446,12 +494,12 @@ __device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) 
 
 // CTAs [0, B nb) make the factors, the next ones a tile of B or C each, the
 // last ones the convolution's cache.
-template <int TP>
+template <typename T, int TP>
 __global__ void __launch_bounds__(kPrep, 2) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
   extern __shared__ __align__(128) unsigned char smem[];
   int u = blockIdx.x;
   if (u < p.B * t.nb) {
-    prep_factors(p, t, u / t.nb, u % t.nb, smem);
+    prep_factors<T>(p, t, u / t.nb, u % t.nb, smem);
     return;
   }
   u -= p.B * t.nb;
@@ -461,13 +509,13 @@ __global__ void __launch_bounds__(kPrep, 2) ssm_prep_kernel(const SsmParams p, c
   const int g = u % p.G;
   u /= p.G;
   if (u < p.B * t.nb) {
-    prep_conv<TP>(p, t, u / t.nb, u % t.nb, g, part, smem);
+    prep_conv<T, TP>(p, t, u / t.nb, u % t.nb, g, part, smem);
     return;
   }
   // (the ids of these CTAs run on in the same order)
   u = blockIdx.x - p.B * t.nb * (1 + p.G * parts);
   const int caches = (p.channels + kPrep - 1) / kPrep;
-  prep_cache(p, u / caches, u % caches);
+  prep_cache<T>(p, u / caches, u % caches);
 }
 
 // ---------------------------------------------------------------------------
@@ -488,9 +536,9 @@ __device__ __forceinline__ bool any_of_conv(bool v) {
 }
 
 // Shared memory of ssm_state_kernel.
-template <int TP>
+template <typename T, int TP>
 struct StateSmem {
-  using Cv = Conv<TP, TP / 16, kConv>;
+  using Cv = Conv<T, TP, TP / 16, kConv>;
   static constexpr uint32_t kX = 0;                                 // 2 x [hi | lo] tiles
   static constexpr uint32_t kXBytes = kQ * TP * 2 * 2;
   static constexpr uint32_t kB = kX + 2 * kXBytes;                  // 2 x (hi, lo) tiles
@@ -510,11 +558,12 @@ struct StateSmem {
 // threads, two warps on a scheduler, a block took 3.7 us instead of STATE_US.)
 // IDS: rows have segment ids (without them every block is plain, and the
 // kernel keeps its registers).
-template <int TP, bool IDS>
+template <typename T, int TP, bool IDS>
 __global__ void __launch_bounds__(kConv + 32, 1)
     ssm_state_kernel(const SsmParams p, const TcBufs t) {
-  using L = StateSmem<TP>;
+  using L = StateSmem<T, TP>;
   using Cv = typename L::Cv;
+  constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kCols = TP / 4;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_tmem;
@@ -583,10 +632,10 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     __syncwarp();
   } else {
     const int first = IDS ? p.rows[b].first : 0;
-    const bf16 *past = past_of(p, b);
+    const T *past = past_of<T>(p, b);
     const int ch = h * p.P + c0;
-    const bf16 *x = static_cast<const bf16 *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
-    const bf16 *before = past ? past + ch : nullptr;
+    const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
+    const T *before = past ? past + ch : nullptr;
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
     const float *dec = t.dec + ((size_t)b * p.H + h) * nb;
     Cv cv;
@@ -616,14 +665,20 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     // the state after block i, once its products are done
     auto finish = [&](int i, float a) {
       if (n < N) {
-        unsigned char *st = t.st + ((((size_t)b * nb + i) * p.H + h) * N) * p.P * 2 +
-                            (size_t)((c0 + col0) / 8) * N * 16 + (n >> 3) * 128 + (n & 7) * 16;
+        const size_t at = ((((size_t)b * nb + i) * p.H + h) * N) * p.P * 2 +
+                          (size_t)((c0 + col0) / 8) * N * 16 + (n >> 3) * 128 + (n & 7) * 16;
 #pragma unroll
         for (int k = 0; k < kCols; k += 8) {
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = s[k + e];
-          *reinterpret_cast<uint4 *>(st + (size_t)(k / 8) * N * 16) = pack8(v);
+          const size_t o = at + (size_t)(k / 8) * N * 16;
+          const uint4 hi = pack8(v);
+          *reinterpret_cast<uint4 *>(t.st + o) = hi;
+          if constexpr (kF32) {
+            rest8(hi, v);
+            *reinterpret_cast<uint4 *>(t.slo + o) = pack8(v);
+          }
         }
       }
       if (!mbar_wait(bar_d + 8u * (i & 1), (i >> 1) & 1)) {
@@ -666,15 +721,22 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       const float a_next = i + 1 < nb ? dec[i + 1] : 0.f;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
       // the lane's i-th token: slot 8 i + lane % 8 of quarter lane / 8
-      using Raw = typename Cv::Raw;
+      using Out = Word<2 * (TP / 16)>;
       const uint32_t at = (uint32_t)(wch / 8 * 2048 + wch % 8 * 2 + (lane >> 3) * 512 +
                                      (lane & 7) * 16);
       unsigned char *xo = smem + L::kX + (i & 1) * L::kXBytes + at;
-      unsigned char *xt = t.xt + (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
-                          (size_t)(c0 / 8) * 2048 + at;
+      const size_t xt = (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
+                        (size_t)(c0 / 8) * 2048 + at;
       const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * lane);
       auto put = [&](int k, u64(&u)[Cv::E], bool cut) {
-        *reinterpret_cast<Raw *>(xt + k * 128) = pack<Raw>(u);
+        Out hi, lo;
+        if constexpr (kF32) {
+          split(u, hi, lo);
+          *reinterpret_cast<Out *>(t.xlo + xt + k * 128) = lo;
+        } else {
+          hi = pack<Out>(u);
+        }
+        *reinterpret_cast<Out *>(t.xt + xt + k * 128) = hi;
         const float f = k == 0 ? w4.x : k == 1 ? w4.y : k == 2 ? w4.z : w4.w;
 #pragma unroll
         for (int e = 0; e < Cv::E; ++e) {
@@ -682,10 +744,9 @@ __global__ void __launch_bounds__(kConv + 32, 1)
           // a token that does not reach the state adds nothing, whatever it holds
           if (cut && f == 0.f) u[e] = pk2(0.f, 0.f);
         }
-        Raw hi, lo;
         split(u, hi, lo);
-        *reinterpret_cast<Raw *>(xo + k * 128) = hi;
-        *reinterpret_cast<Raw *>(xo + TP / 8 * 2048 + k * 128) = lo;
+        *reinterpret_cast<Out *>(xo + k * 128) = hi;
+        *reinterpret_cast<Out *>(xo + TP / 8 * 2048 + k * 128) = lo;
       };
       const unsigned char *rows = smem + L::kRows + (i & 1) * Cv::kBytes;
       const unsigned char *tok = t.tok + ((size_t)b * nb + i) * kQ;
@@ -722,14 +783,18 @@ __global__ void __launch_bounds__(kConv + 32, 1)
 
 // Shared memory of ssm_out_kernel: C; B, then the matrix of factors; x; the
 // entering state, then z and y.
-template <int PT>
+// With fp32 inputs every operand has a second part right after it (C, F at kQ *
+// 128 * 2 bytes, x and S next to each other as PT more columns).
+template <typename T, int PT>
 struct OutSmem {
+  static constexpr uint32_t kParts = sizeof(T) == 4 ? 2 : 1;
+  static constexpr uint32_t kPart = kQ * 128 * 2;
   static constexpr uint32_t kC = 0;
-  static constexpr uint32_t kF = kC + kQ * 128 * 2;
-  static constexpr uint32_t kX = kF + kQ * kQ * 2;
-  static constexpr uint32_t kS = kX + kQ * PT * 2;
-  static constexpr uint32_t kV = kS + kQ * PT * 2;     // ein, cum, cumj, run: 128 each
-  static constexpr uint32_t kBar = kV + 4 * kQ * 4;
+  static constexpr uint32_t kF = kC + kParts * kPart;
+  static constexpr uint32_t kX = kF + kParts * kPart;
+  static constexpr uint32_t kS = kX + kParts * kQ * PT * 2;
+  static constexpr uint32_t kV = kS + kParts * kQ * PT * 2;   // ein, cum, cumj, run: 128 each,
+  static constexpr uint32_t kBar = kV + 6 * kQ * 4;           // and the rest of cum and cumj
   static constexpr uint32_t kBytes = kBar + 32;
 };
 
@@ -738,10 +803,12 @@ struct OutSmem {
 // `heads` of its heads); TMEM holds C B^T of
 // the block, shared by the heads, and the two parts of y of PT columns.  Two
 // CTAs fit an SM and fill each other's waits.
-template <int PT>
-__global__ void __launch_bounds__(256, 2)
+template <typename T, int PT>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     ssm_out_kernel(const SsmParams p, const TcBufs t, int heads) {
-  using L = OutSmem<PT>;
+  using L = OutSmem<T, PT>;
+  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int kCols = PT * L::kParts;      // TMEM columns of each part of y
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_tmem;
   const uint32_t sb = smem_u32(smem);
@@ -759,7 +826,7 @@ __global__ void __launch_bounds__(256, 2)
   const int h_lo = g * hg + part * heads, h_hi = min(h_lo + heads, (g + 1) * hg);
   const int subs = p.P / PT;
   const int n_items = (h_hi - h_lo) * subs;
-  if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 128 + 2 * PT > 256 ? 512 : 256);
+  if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 256);
   if (tid == 0) {
     mbar_init(bar_cb, 1);
     mbar_init(bar_xs, 1);
@@ -770,7 +837,8 @@ __global__ void __launch_bounds__(256, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
-  const uint32_t t_cb = tmem, t_yi = tmem + 128, t_yx = tmem + 128 + PT;
+  static_assert(128 + 2 * kCols <= 256, "tensor memory");
+  const uint32_t t_cb = tmem, t_yi = tmem + 128, t_yx = tmem + 128 + kCols;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   uint32_t n_m = 0;       // commits waited for
   bool bad = false;
@@ -784,19 +852,29 @@ __global__ void __launch_bounds__(256, 2)
     tc_fence_after();
   };
   const uint32_t tile = (uint32_t)(kQ * N * 2);
-  const uint32_t xs_bytes = (uint32_t)(kQ * PT * 2 + N * PT * 2);
+  const uint32_t xs_bytes = (uint32_t)(kQ * PT * 2 + N * PT * 2) * L::kParts;
   auto load_item = [&](int k) {      // thread 0: x and S of item k
     const int h = h_lo + k / subs, c = k % subs * PT;
     const size_t at = ((size_t)b * nb + blk) * p.H + h;
     mbar_expect_tx(bar_xs, xs_bytes);
-    bulk_load(sb + L::kX, t.xt + at * kQ * p.P * 2 + (size_t)c * kQ * 2, kQ * PT * 2, bar_xs);
-    bulk_load(sb + L::kS, t.st + at * N * p.P * 2 + (size_t)c * N * 2, N * PT * 2, bar_xs);
+    const size_t ox = at * kQ * p.P * 2 + (size_t)c * kQ * 2;
+    const size_t os = at * N * p.P * 2 + (size_t)c * N * 2;
+    bulk_load(sb + L::kX, t.xt + ox, kQ * PT * 2, bar_xs);
+    bulk_load(sb + L::kS, t.st + os, N * PT * 2, bar_xs);
+    if (kF32) {
+      bulk_load(sb + L::kX + kQ * PT * 2, t.xlo + ox, kQ * PT * 2, bar_xs);
+      bulk_load(sb + L::kS + N * PT * 2, t.slo + os, N * PT * 2, bar_xs);
+    }
   };
   if (tid == 0) {
     const size_t o = (((size_t)b * nb + blk) * p.G + g) * tile;
-    mbar_expect_tx(bar_cb, 2 * tile);
+    mbar_expect_tx(bar_cb, 2 * tile * L::kParts);
     bulk_load(sb + L::kC, t.ct + o, tile, bar_cb);
     bulk_load(sb + L::kF, t.bhi + o, tile, bar_cb);
+    if (kF32) {
+      bulk_load(sb + L::kC + L::kPart, t.clo + o, tile, bar_cb);
+      bulk_load(sb + L::kF + L::kPart, t.blo + o, tile, bar_cb);
+    }
     load_item(0);
   }
   const int flags = t.flags[(size_t)b * nb + blk];
@@ -804,20 +882,26 @@ __global__ void __launch_bounds__(256, 2)
   int *srun = reinterpret_cast<int *>(smem + L::kV + 3 * kQ * 4);
   if (half == 0) srun[r] = run;
   const Opnd opC = {sb + L::kC, 128, (uint32_t)N * 16};
+  const Opnd opC2 = {sb + L::kC + L::kPart, 128, (uint32_t)N * 16};
   if (!mbar_wait(bar_cb, 0)) give_up();
   if (tid == 0 && !bad) {
     const Opnd opB = {sb + L::kF, 128, (uint32_t)N * 16};
     mma_k(t_cb, opC, 0, opB, 0, N / 16, 128, false);
+    if (kF32) {
+      const Opnd opB2 = {sb + L::kF + L::kPart, 128, (uint32_t)N * 16};
+      mma_k(t_cb, opC, 0, opB2, 0, N / 16, 128, true);
+      mma_k(t_cb, opC2, 0, opB, 0, N / 16, 128, true);
+    }
     mma_commit(bar_m);
   }
   wait_mma();
   __syncthreads();
   // entries above the diagonal's 32-row steps are never written again
-  for (int i = tid; i < kQ * kQ * 2 / 16; i += 256)
+  for (int i = tid; i < (int)(L::kParts * L::kPart / 16); i += 256)
     *reinterpret_cast<uint4 *>(smem + L::kF + i * 16) = make_uint4(0, 0, 0, 0);
 
   float *sein = reinterpret_cast<float *>(smem + L::kV);
-  float *scum = sein + kQ, *scumj = scum + kQ;
+  float *scum = sein + kQ, *scumj = scum + kQ, *scum_lo = sein + 4 * kQ, *scumj_lo = sein + 5 * kQ;
   int k = 0;
   for (; k < n_items; ++k) {
     const int h = h_lo + k / subs, c = k % subs * PT;
@@ -826,15 +910,17 @@ __global__ void __launch_bounds__(256, 2)
     if (tid < kQ) {
       sein[tid] = t.ein[at + tid];
       scum[tid] = t.cum[at + tid];
+      if (kF32) scum_lo[tid] = t.cum_lo[at + tid];
     } else {
       scumj[tid - kQ] = t.cumj[at + tid - kQ];
+      if (kF32) scumj_lo[tid - kQ] = t.cumj_lo[at + tid - kQ];
     }
     // into L2 while this item is computed: its rows of z, the next x and S
     if (p.z && tid >= kQ) {
       const int tok = tid - kQ;
       if (t0 + tok < p.T)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            static_cast<const bf16 *>(p.z) + (size_t)b * p.z_sb + (long long)(t0 + tok) * p.z_st +
+            static_cast<const T *>(p.z) + (size_t)b * p.z_sb + (long long)(t0 + tok) * p.z_st +
             h * p.P + c));
     }
     if (tid == 0 && k + 1 < n_items) {
@@ -842,18 +928,25 @@ __global__ void __launch_bounds__(256, 2)
       const size_t at1 = ((size_t)b * nb + blk) * p.H + h1;
       prefetch_l2(t.xt + at1 * kQ * p.P * 2 + (size_t)c1 * kQ * 2, kQ * PT * 2);
       prefetch_l2(t.st + at1 * N * p.P * 2 + (size_t)c1 * N * 2, N * PT * 2);
+      if (kF32) {
+        prefetch_l2(t.xlo + at1 * kQ * p.P * 2 + (size_t)c1 * kQ * 2, kQ * PT * 2);
+        prefetch_l2(t.slo + at1 * N * p.P * 2 + (size_t)c1 * N * 2, N * PT * 2);
+      }
     }
     if (!mbar_wait(bar_xs, k & 1)) give_up();
     if (__syncthreads_or(bad)) break;
     if (tid == 0) {
       const Opnd opS = {sb + L::kS, 128, (uint32_t)N * 16};
-      mma_k(t_yi, opC, 0, opS, 1, N / 16, PT, false);
+      mma_k(t_yi, opC, 0, opS, 1, N / 16, kCols, false);
+      if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, PT, true);
       mma_commit(bar_m);
     }
     if (c == 0) {
       // factors of the head: row r, 16 columns at a time, up to the diagonal
       const float cr = scum[r];
       const u64 cr2 = pk2(cr, cr), neg = pk2(-1.f, -1.f);
+      const float cl = kF32 ? scum_lo[r] : 0.f;
+      const u64 cl2 = pk2(cl, cl);
 #pragma unroll 1
       for (int q = half; q < 2 * quad + 2; q += 2) {
         float v[16];
@@ -862,8 +955,14 @@ __global__ void __launch_bounds__(256, 2)
         for (int e = 0; e < 16; e += 4) {
           const ulonglong2 cj = *reinterpret_cast<const ulonglong2 *>(scumj + 16 * q + e);
           float f[4];
-          upk2(fma2(cj.x, neg, cr2), f[0], f[1]);
-          upk2(fma2(cj.y, neg, cr2), f[2], f[3]);
+          u64 d0 = fma2(cj.x, neg, cr2), d1 = fma2(cj.y, neg, cr2);
+          if (kF32) {
+            const ulonglong2 jl = *reinterpret_cast<const ulonglong2 *>(scumj_lo + 16 * q + e);
+            d0 = add2(d0, fma2(jl.x, neg, cl2));
+            d1 = add2(d1, fma2(jl.y, neg, cl2));
+          }
+          upk2(d0, f[0], f[1]);
+          upk2(d1, f[2], f[3]);
           const u64 lo = mul2(pk2(v[e], v[e + 1]), pk2(ex2(f[0]), ex2(f[1])));
           const u64 hi = mul2(pk2(v[e + 2], v[e + 3]), pk2(ex2(f[2]), ex2(f[3])));
           upk2(lo, v[e], v[e + 1]);
@@ -881,13 +980,18 @@ __global__ void __launch_bounds__(256, 2)
             if (srun[16 * q + e] != run) v[e] = 0.f;
         }
         unsigned char *f = smem + L::kF + (r & 7) * 16 + (r >> 3) * 2048 + 2 * q * 128;
-        float a[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = v[e];
-        *reinterpret_cast<uint4 *>(f) = pack8(a);
+        for (int o = 0; o < 2; ++o) {
+          float a[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = v[8 + e];
-        *reinterpret_cast<uint4 *>(f + 128) = pack8(a);
+          for (int e = 0; e < 8; ++e) a[e] = v[8 * o + e];
+          const uint4 hi = pack8(a);
+          *reinterpret_cast<uint4 *>(f + 128 * o) = hi;
+          if constexpr (kF32) {
+            rest8(hi, a);
+            *reinterpret_cast<uint4 *>(f + L::kPart + 128 * o) = pack8(a);
+          }
+        }
       }
       fence_proxy_async();
     }
@@ -896,19 +1000,23 @@ __global__ void __launch_bounds__(256, 2)
     if (__syncthreads_or(bad)) break;
     if (tid == 0) {
       const Opnd opF = {sb + L::kF, 128, kQ * 16}, opX = {sb + L::kX, 128, kQ * 16};
-      mma_k(t_yx, opF, 0, opX, 1, kQ / 16, PT, false);
+      mma_k(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
+      if (kF32) {
+        const Opnd opF2 = {sb + L::kF + L::kPart, 128, kQ * 16};
+        mma_k(t_yx, opF2, 0, opX, 1, kQ / 16, PT, true);
+      }
       mma_commit(bar_m);
     }
     const int ch = h * p.P + c;
+    constexpr int kP16 = PT * (int)sizeof(T) / 16, kStep = 256 / kP16, kEl = 16 / (int)sizeof(T);
     auto piece = [&](int row, int q) {   // 16-byte piece of the [128][PT] tile of z and y
-      return (uint32_t)(L::kS + row * PT * 2 + ((q ^ (PT == 64 ? row & 7 : row >> 1 & 3)) << 4));
+      return (uint32_t)(L::kS + row * kP16 * 16 + ((q ^ (kP16 == 8 ? row & 7 : row >> 1 & 3)) << 4));
     };
-    // a thread copies piece q0 of slots s0, s0 + 256 / (PT / 8), ..
-    constexpr int kP16 = PT / 8, kStep = 256 / kP16;
+    // a thread copies piece q0 of slots s0, s0 + kStep, ..
     const int q0 = tid % kP16, s0 = tid / kP16;
     if (p.z) {
-      const bf16 *z = static_cast<const bf16 *>(p.z) + (size_t)b * p.z_sb +
-                      (long long)t0 * p.z_st + ch + q0 * 8;
+      const T *z = static_cast<const T *>(p.z) + (size_t)b * p.z_sb + (long long)t0 * p.z_st + ch +
+                   q0 * kEl;
 #pragma unroll
       for (int s = s0; s < kQ; s += kStep) {
         const int tok = token_of(s);
@@ -928,14 +1036,37 @@ __global__ void __launch_bounds__(256, 2)
       const int col = half * (PT / 2) + e0;
       float yi[16], yx[16];
       tmem_ld16x2(t_yi + lanes + col, t_yx + lanes + col, yi, yx);
+      if (kF32) {           // the products with the second parts
+        float vi[16], vx[16];
+        tmem_ld16x2(t_yi + lanes + PT + col, t_yx + lanes + PT + col, vi, vx);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          yi[e] += vi[e];
+          yx[e] += vx[e];
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         u64 x[4], z[4], y[4];
-        Unpack8::unpack(*reinterpret_cast<const uint4 *>(
-                            smem + L::kX + (col / 8 + q) * 2048 + (r >> 3) * 128 + (r & 7) * 16),
-                        x);
-        unsigned char *zp = smem + piece(r, col / 8 + q);
-        if (p.z) Unpack8::unpack(*reinterpret_cast<const uint4 *>(zp), z);
+        const unsigned char *xp = smem + L::kX + (col / 8 + q) * 2048 + (r >> 3) * 128 + (r & 7) * 16;
+        Unpack8::unpack(*reinterpret_cast<const uint4 *>(xp), x);
+        if (kF32) {
+          Unpack8::unpack(*reinterpret_cast<const uint4 *>(xp + kQ * PT * 2), z);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = add2(x[e], z[e]);
+        }
+        // the 8 columns are one piece of z and y, or two of fp32
+        unsigned char *zp = smem + piece(r, (col / 8 + q) * (8 / kEl));
+        unsigned char *zp2 = smem + piece(r, (col / 8 + q) * (8 / kEl) + (kF32 ? 1 : 0));
+        if (p.z) {
+          if constexpr (kF32) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(zp),
+                             c = *reinterpret_cast<const ulonglong2 *>(zp2);
+            z[0] = a.x; z[1] = a.y; z[2] = c.x; z[3] = c.y;
+          } else {
+            Unpack8::unpack(*reinterpret_cast<const uint4 *>(zp), z);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 8 * q + 2 * e;
@@ -946,15 +1077,19 @@ __global__ void __launch_bounds__(256, 2)
             upk2(add2(pk2(1.f, 1.f), pk2(ex2(a), ex2(c))), d0, d1);
             y[e] = mul2(mul2(y[e], z[e]), pk2(rcp(d0), rcp(d1)));
           }
+          if (run < 0) y[e] = 0;
         }
-        uint4 o = pack<uint4>(y);
-        if (run < 0) o = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(zp) = o;
+        if constexpr (kF32) {
+          *reinterpret_cast<ulonglong2 *>(zp) = make_ulonglong2(y[0], y[1]);
+          *reinterpret_cast<ulonglong2 *>(zp2) = make_ulonglong2(y[2], y[3]);
+        } else {
+          *reinterpret_cast<uint4 *>(zp) = pack<uint4>(y);
+        }
       }
     }
     tc_fence_before();
     __syncthreads();
-    bf16 *y = static_cast<bf16 *>(p.y) + ((size_t)b * p.T + t0) * p.H * p.P + ch + q0 * 8;
+    T *y = static_cast<T *>(p.y) + ((size_t)b * p.T + t0) * p.H * p.P + ch + q0 * kEl;
 #pragma unroll
     for (int s = s0; s < kQ; s += kStep) {
       const int tok = token_of(s);
@@ -976,67 +1111,76 @@ __global__ void __launch_bounds__(256, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, 128 + 2 * PT > 256 ? 512 : 256);
+  if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
-template <int TP>
+template <typename T, int TP>
 cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  size_t smem = Conv<TP, 8, TP * 4>::kBytes + kQ;
+  size_t smem = PrepConv<T, TP>::kBytes + kQ;
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
   const int caches = p.conv_out ? (p.channels + kPrep - 1) / kPrep : 0;
   const unsigned grid = (unsigned)(p.B * (t.nb * (1 + p.G * (2 * p.N / TP)) + caches));
-  ssm_prep_kernel<TP><<<grid, kPrep, smem, cs>>>(p, t);
+  ssm_prep_kernel<T, TP><<<grid, kPrep, smem, cs>>>(p, t);
   return cudaGetLastError();
 }
 
-template <int TP, bool IDS>
-cudaError_t launch_state(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  auto kern = ssm_state_kernel<TP, IDS>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)StateSmem<TP>::kBytes);
-  if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, StateSmem<TP>::kBytes, cs>>>(p, t);
-  return cudaGetLastError();
-}
-
-template <int PT>
-cudaError_t launch_out(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+template <typename T, int TP, bool IDS>
+cudaError_t launch_state_i(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+  auto kern = ssm_state_kernel<T, TP, IDS>;
+  constexpr int smem = (int)StateSmem<T, TP>::kBytes;
   const cudaError_t e =
-      cudaFuncSetAttribute(ssm_out_kernel<PT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)OutSmem<PT>::kBytes);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, smem, cs>>>(p, t);
+  return cudaGetLastError();
+}
+template <typename T, int TP>
+cudaError_t launch_state(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+  return p.segment_ids ? launch_state_i<T, TP, true>(p, t, cs)
+                       : launch_state_i<T, TP, false>(p, t, cs);
+}
+
+template <typename T, int PT>
+cudaError_t launch_out(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
+  constexpr int smem = (int)OutSmem<T, PT>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(ssm_out_kernel<T, PT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // heads per CTA: up to 4, as long as the CTAs fill the GPU twice over
   const int hg = p.H / p.G;
   int heads = 4;
   auto ctas = [&](int n) { return (long long)p.B * t.nb * p.G * ((hg + n - 1) / n); };
   while (heads > 1 && ctas(heads) < 4ll * num_sms()) heads /= 2;
-  ssm_out_kernel<PT><<<(unsigned)ctas(heads), 256, OutSmem<PT>::kBytes, cs>>>(p, t, heads);
+  ssm_out_kernel<T, PT><<<(unsigned)ctas(heads), 256, smem, cs>>>(p, t, heads);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t ssm_tc_bytes(const SsmParams &p) {
+size_t ssm_tc_bytes(const SsmParams &p, bool f32) {
   TcBufs t;
-  return layout_bufs(p, nullptr, &t);
+  return layout_bufs(p, f32, nullptr, &t);
 }
 
-cudaError_t launch_ssm_tc(const SsmParams &p, uint32_t *status, cudaStream_t cs) {
+cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaStream_t cs) {
   TcBufs t;
-  layout_bufs(p, p.ws, &t);
+  layout_bufs(p, f32, p.ws, &t);
   t.status = status;
-  cudaError_t e = p.N == 32 ? launch_prep<32>(p, t, cs) : launch_prep<64>(p, t, cs);
+  cudaError_t e;
+  if (f32) {       // twice the operands: tiles of 32 columns throughout
+    e = launch_prep<float, 32>(p, t, cs);
+    if (e == cudaSuccess) e = launch_state<float, 32>(p, t, cs);
+    return e == cudaSuccess ? launch_out<float, 32>(p, t, cs) : e;
+  }
+  e = p.N == 32 ? launch_prep<bf16, 32>(p, t, cs) : launch_prep<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;
   // 64-column tiles halve the traffic of B's tiles; 32 where they would
   // leave SMs without a CTA
   const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
-  if (p.segment_ids)
-    e = narrow ? launch_state<32, true>(p, t, cs) : launch_state<64, true>(p, t, cs);
-  else
-    e = narrow ? launch_state<32, false>(p, t, cs) : launch_state<64, false>(p, t, cs);
+  e = narrow ? launch_state<bf16, 32>(p, t, cs) : launch_state<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;
-  return p.P == 32 ? launch_out<32>(p, t, cs) : launch_out<64>(p, t, cs);
+  return p.P == 32 ? launch_out<bf16, 32>(p, t, cs) : launch_out<bf16, 64>(p, t, cs);
 }
 
 }  // namespace kda

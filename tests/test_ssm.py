@@ -93,7 +93,8 @@ class Case:
             assert not y.cpu()[self.ids == 0].any()
 
 
-IMPLS = [(torch.float32, "simt"), (torch.bfloat16, "simt"), (torch.bfloat16, "auto")]
+IMPLS = [(torch.float32, "simt"), (torch.float32, "tc"), (torch.bfloat16, "simt"),
+         (torch.bfloat16, "auto")]
 DIMS = [(1, 1, 1, 32, 32, 1), (2, 3, 2, 64, 64, 1), (1, 65, 3, 128, 32, 3), (2, 128, 4, 32, 128, 2),
         (1, 129, 8, 64, 128, 1), (1, 300, 2, 128, 128, 1), (3, 257, 5, 64, 64, 5),
         (1, 640, 4, 32, 64, 2)]
