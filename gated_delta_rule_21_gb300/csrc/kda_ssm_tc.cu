@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         const Opnd x = {sb + L::kX + (i & 1) * L::kXBytes, 128, kQ * 16};
         const Opnd bh_ = {bt, (uint32_t)N * 16, 128}, bl_ = {bt + tb, (uint32_t)N * 16, 128};
         mma_k(d, bh_, 1, x, 1, kQ / 16, 2 * TP, false);
-        mma_k(d, bl_, 1, x, 1, kQ / 16, TP, true);
+        mma_k(d, bl_, 1, x, 1, kQ / 16, 2 * TP, true);
         mma_commit(bar_d + 8u * (i & 1));
         ++issued;
         if (i > 0 && loaded < nb) {      // block i - 1's tiles are free once it is done
