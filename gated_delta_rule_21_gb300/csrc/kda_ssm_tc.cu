@@ -44,7 +44,7 @@ __host__ __device__ constexpr int slot_of(int token) {
 __host__ __device__ constexpr int token_of(int slot) {
   return (slot & ~31) + 4 * (slot & 7) + (slot >> 3 & 3);
 }
-constexpr int kPrep = 256;         // threads of a prep CTA
+constexpr int kPrep = 512;         // threads of a prep CTA
 constexpr int kConv = 512;         // threads that run the convolution of x
 
 // What the kernels hand to one another, in the workspace.
@@ -422,9 +422,9 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
   }
 }
 
-// Channels per warp in prep: 16 bytes of them.
+// Channels per warp in prep: 8 bytes of them.
 template <typename T>
-constexpr int kPrepCh = 16 / (int)sizeof(T);
+constexpr int kPrepCh = 8 / (int)sizeof(T);
 template <typename T, int TP>
 using PrepConv = Conv<T, TP, kPrepCh<T>, TP / kPrepCh<T> * 32>;
 
