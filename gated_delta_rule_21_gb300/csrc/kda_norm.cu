@@ -20,8 +20,8 @@
 // so a row costs one reduction and its inputs are read once.
 //
 // Both kernels are bound by HBM.  Rows whose length or pointers do not allow
-// 16-byte accesses take the same code with VEC = 2 (bf16 rows of even length)
-// or 1.  This file: the forward; kda_norm_bwd.cu: the backward.
+// 16-byte accesses take the same code with pieces of 4 bytes, and bf16 rows of
+// odd length with single elements.  This file: the forward; kda_norm_bwd.cu: the backward.
 #include "kda_norm.cuh"
 
 namespace kda {
@@ -46,7 +46,10 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
   const int step = tpr * VEC * (int)sizeof(T);        // bytes between a thread's pieces
   const long long row_bytes = (long long)p.D * sizeof(T);
   In in;
-  in.base = reinterpret_cast<Raw *>(smem) + tid;
+  in.lane = lane;
+  in.tpr = tpr;
+  in.D = p.D;
+  in.init(smem, tid, group, rg);
   in.src[0] = (const char *)p.y;
   in.src[kRes] = (const char *)p.res;
   if constexpr (GATE == kGateEach) in.src[kGate] = (const char *)p.gate;
@@ -65,10 +68,13 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
   const long long advance = rg * row_bytes;
 #pragma unroll
   for (int s = 0; s < kAhead; ++s)
-    in.fetch(s, lo + group + s * rg < hi, has, at + s * advance, step);
+    in.fetch(s, lo + group + s * rg < hi, has, lo + group + s * rg, at + s * advance, step);
   for (long long row = lo + group; row - group < hi; row += rg, at += advance) {
     const bool live = row < hi;
-    in.fetch(st == 0 ? kAhead : st - 1, row + kAhead * rg < hi, has, at + kAhead * advance, step);
+    in.turn([&]() {
+      in.fetch(st == 0 ? kAhead : st - 1, row + kAhead * rg < hi, has, row + kAhead * rg,
+               at + kAhead * advance, step);
+    });
     if (GATE == kGateGroup && live) {
       const unsigned g = (unsigned)row / p.rows_per_gate;
       if (g != ga_row) {
@@ -85,13 +91,12 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
         }
       }
     }
-    if (NS > 0) cp_async_wait<kAhead>();
     P v[ITEMS][E], acc = both<P>(0.f);
     if (live) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
         if (has[i]) {
-          Pc::get(in.get(st, 0, i, at, step), v[i]);
+          Pc::get(in.get(st, 0, i, row, at, step), v[i]);
 #pragma unroll
           for (int e = 0; e < E; ++e) acc = fma(v[i][e], v[i][e], acc);
         }
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
           for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], mul(w[e], k));
           if (GATE == kGateEach) {
             P d[E];
-            Pc::get(in.get(st, kGate < (GATE == kGateEach ? 3 : 2) ? kGate : 0, i, at, step), a);
+            Pc::get(in.get(st, kGate < (GATE == kGateEach ? 3 : 2) ? kGate : 0, i, row, at, step), a);
             gate_values<false>(p.act, a, d);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], a[e]);
@@ -118,7 +123,7 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], ga[i < GI ? i : 0][e]);
           if (p.res) {
-            Pc::get(in.get(st, kRes, i, at, step), a);
+            Pc::get(in.get(st, kRes, i, row, at, step), a);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = add(v[i][e], a[e]);
           }
@@ -155,7 +160,7 @@ template <typename T, int VEC, int ITEMS, int GATE, int BS, int NS>
 cudaError_t launch_g(const NormParams &p, cudaStream_t stream) {
   auto kern = norm_fwd_kernel<T, VEC, ITEMS, GATE, BS, NS>;
   const int threads = p.tpr * p.rg;
-  const size_t smem = Stage<T, VEC, ITEMS, GATE == kGateEach ? 3 : 2, BS, NS>::kBytes;
+  const size_t smem = Stage<T, VEC, ITEMS, GATE == kGateEach ? 3 : 2, BS, NS>::bytes(p.D, p.rg);
   cudaError_t e = allow_smem(kern, smem);
   int per_sm = 1;
   if (e == cudaSuccess)
@@ -202,30 +207,34 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
   for (const void *ptr : {y, (const void *)w_post, residual, gate, (const void *)w_pre,
                           (const void *)out, (const void *)x})
     vec = vec && aligned16(ptr);
-  const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec, 2);
+  static const Built built[] = {{2, 8, 2, 256}, {2, 8, 2, 512}, {2, 8, 4, 512},
+                                {2, 2, 8, 256}, {2, 2, 8, 1024}, {2, 1, 16, 256}, {2, 1, 16, 1024},
+                                {4, 4, 2, 256}, {4, 4, 2, 512}, {4, 4, 4, 512}, {4, 4, 8, 512},
+                                {4, 1, 8, 256}, {4, 1, 8, 512}, {4, 1, 16, 1024}};
+  const Layout l = layout_for(built, d->dim, bf16 ? 2 : 4, vec);
   NormParams p = params_of(d, l, y, w_post, residual, gate, w_pre);
   p.out = out; p.x = x; p.stats = stats;
   const int mode = gate_mode(d, gate);
-  const bool small = l.tpr * l.rg <= kBlock;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   using B = __nv_bfloat16;
   if (l.vec == 8)
-    e = l.items == 2 ? (small ? launch<B, 8, 2, 256, 3>(p, mode, cs)
-                              : launch<B, 8, 2, 512, 3>(p, mode, cs))
-                     : launch<B, 8, 4, 512, 0>(p, mode, cs);
+    e = l.items == 4   ? launch<B, 8, 4, 512, 0>(p, mode, cs)
+        : l.bs == 256  ? launch<B, 8, 2, 256, 3>(p, mode, cs)
+                       : launch<B, 8, 2, 512, 3>(p, mode, cs);
   else if (l.vec == 4)
-    e = l.items == 2   ? (small ? launch<float, 4, 2, 256, 3>(p, mode, cs)
-                                : launch<float, 4, 2, 512, 3>(p, mode, cs))
+    e = l.items == 8   ? launch<float, 4, 8, 512, 0>(p, mode, cs)
         : l.items == 4 ? launch<float, 4, 4, 512, 0>(p, mode, cs)
-                       : launch<float, 4, 8, 512, 0>(p, mode, cs);
+        : l.bs == 256  ? launch<float, 4, 2, 256, 3>(p, mode, cs)
+                       : launch<float, 4, 2, 512, 3>(p, mode, cs);
   else if (l.vec == 2)
-    e = l.items == 2 ? launch<B, 2, 2, 1024, 0>(p, mode, cs) : launch<B, 2, 8, 1024, 0>(p, mode, cs);
+    e = l.bs == 256 ? launch<B, 2, 8, 256, 3>(p, mode, cs) : launch<B, 2, 8, 1024, 0>(p, mode, cs);
   else if (bf16)
-    e = l.items == 4 ? launch<B, 1, 4, 1024, 0>(p, mode, cs)
-                     : launch<B, 1, 16, 1024, 0>(p, mode, cs);
+    e = l.bs == 256 ? launch<B, 1, 16, 256, 2>(p, mode, cs)
+                    : launch<B, 1, 16, 1024, 2>(p, mode, cs);
   else
-    e = l.items == 4 ? launch<float, 1, 4, 1024, 0>(p, mode, cs)
-                     : launch<float, 1, 16, 1024, 0>(p, mode, cs);
+    e = l.items == 16 ? launch<float, 1, 16, 1024, 0>(p, mode, cs)
+        : l.bs == 256 ? launch<float, 1, 8, 256, 3>(p, mode, cs)
+                      : launch<float, 1, 8, 512, 2>(p, mode, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -22,16 +22,27 @@ enum { kGateNone = 0, kGateEach = 1, kGateGroup = 2 };
 struct Layout {
   int vec;      // elements per access: 16 bytes, 2 (bf16, even rows) or 1
   int items, tpr, rg;
+  int bs;       // most threads of the kernel
 };
 
-inline Layout layout_for(int D, int elt, bool vector_ok, int items16) {
+// A kernel that is built: pieces of `vec` elements, `items` of them per thread,
+// CTAs of up to `bs` threads.
+struct Built {
+  int elt, vec, items, bs;
+};
+
+// The first kernel whose CTA covers a row.
+template <int N>
+Layout layout_for(const Built (&built)[N], int D, int elt, bool vector_ok) {
   Layout l;
   l.vec = !vector_ok ? 1 : D % (16 / elt) == 0 ? 16 / elt : elt == 2 && D % 2 == 0 ? 2 : 1;
   const int n = D / l.vec;
-  const int most = l.vec > 2 ? 512 : 1024;     // threads of one row
-  // the kernels' numbers of pieces: items16 and its doubles; 2, 8; 4, 16
-  l.items = l.vec > 2 ? items16 : l.vec == 2 ? 2 : 4;
-  while (l.items * most < n) l.items *= l.vec > 2 ? 2 : 4;
+  for (const Built &k : built)
+    if (k.elt == elt && k.vec == l.vec && k.items * k.bs >= n) {
+      l.items = k.items;
+      l.bs = k.bs;
+      break;
+    }
   int t = (n + l.items - 1) / l.items;
   if (t > 32) {
     t = (t + 31) / 32 * 32;
@@ -287,40 +298,107 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's own pieces of NIN inputs of the rows to come, copied to shared
-// memory NS - 1 rows ahead ([stage][input][item][BS threads]).  NS = 0 (rows
-// too long, or accesses of less than 16 bytes): read where they are used.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The rows to come, copied to shared memory NS - 1 ahead (NS = 0: inputs are
+// read where they are used).  Pieces of 4 or 16 bytes: a thread copies its
+// own, [stage][input][item][BS threads], and no barrier guards them.  bf16
+// rows of odd length start in the middle of a word: their words are copied
+// by whoever comes, [stage][input][row group][row], and one barrier per row
+// lets every thread read its elements.
 template <typename T, int VEC, int ITEMS, int NIN, int BS, int NS>
 struct Stage {
   using Raw = typename Piece<T, VEC>::Raw;
-  static constexpr size_t kBytes = (size_t)NS * NIN * ITEMS * BS * sizeof(Raw);
-  Raw *base;            // of this thread
+  static constexpr bool kShared = sizeof(Raw) == 2;
+  Raw *base;            // of this thread, or of its row group
   const char *src[NIN]; // the inputs, null where absent
+  int lane, tpr, D;
+  int pitch;            // kShared: bytes between the stages' inputs
 
-  // bytes: the thread's first piece of the row; step: bytes between pieces
-  __device__ __forceinline__ void fetch(int st, bool live, const bool (&has)[ITEMS],
+  static __host__ __device__ int row_pitch(int D) { return (2 * D + 2 + 15) / 16 * 16; }
+  static size_t bytes(int D, int rg) {
+    if (NS == 0) return 0;
+    return kShared ? (size_t)NS * NIN * rg * row_pitch(D)
+                   : (size_t)NS * NIN * ITEMS * BS * sizeof(Raw);
+  }
+  __device__ __forceinline__ void init(unsigned char *smem, int tid, int group, int rg) {
+    base = kShared ? reinterpret_cast<Raw *>(smem + (size_t)group * row_pitch(D))
+                   : reinterpret_cast<Raw *>(smem) + tid;
+    pitch = rg * row_pitch(D);
+  }
+
+  // row: its number; bytes: the thread's first piece; step: between pieces
+  __device__ __forceinline__ void fetch(int st, bool live, const bool (&has)[ITEMS], long long row,
                                         long long bytes, int step) const {
     if constexpr (NS > 0) {
       if (live) {
-        const uint32_t d = (uint32_t)__cvta_generic_to_shared(base + st * NIN * ITEMS * BS);
+        if constexpr (kShared) {
+          const long long start = row * D * 2;
 #pragma unroll
-        for (int k = 0; k < NIN; ++k)
-          if (src[k]) {
+          for (int k = 0; k < NIN; ++k)
+            if (src[k]) {
+              const char *s = src[k] + start;
+              // whole words by cp.async, a half word at either end by hand;
+              // element c lies at byte 2 c + (address of the row & 2)
+              const int odd = (int)(reinterpret_cast<uintptr_t>(s) & 2);
+              char *d = reinterpret_cast<char *>(base) + (st * NIN + k) * pitch;
+              const int words = (2 * D - odd) / 4;
+              const uint32_t ds = (uint32_t)__cvta_generic_to_shared(d) + 2 * odd;
+              for (int w = lane; w < words; w += tpr) cp_async4(ds + 4 * w, s + odd + 4 * w);
+              if (odd && lane == 0)
+                *reinterpret_cast<T *>(d + 2) = *reinterpret_cast<const T *>(s);
+              if (2 * D - odd - 4 * words && lane == tpr - 1)
+                *reinterpret_cast<T *>(d + odd + 2 * D - 2) =
+                    *reinterpret_cast<const T *>(s + 2 * D - 2);
+            }
+        } else {
+          const uint32_t d = (uint32_t)__cvta_generic_to_shared(base + st * NIN * ITEMS * BS);
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-              if (has[i])
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 d + (uint32_t)((k * ITEMS + i) * BS * sizeof(Raw))),
-                             "l"(src[k] + bytes + (long long)i * step)
-                             : "memory");
-          }
+          for (int k = 0; k < NIN; ++k)
+            if (src[k]) {
+#pragma unroll
+              for (int i = 0; i < ITEMS; ++i)
+                if (has[i]) {
+                  const uint32_t to = d + (uint32_t)((k * ITEMS + i) * BS * sizeof(Raw));
+                  const char *from = src[k] + bytes + (long long)i * step;
+                  if constexpr (sizeof(Raw) == 16) cp_async16(to, from);
+                  else cp_async4(to, from);
+                }
+            }
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
-  __device__ __forceinline__ Raw get(int st, int k, int i, long long bytes, int step) const {
-    if constexpr (NS > 0) return base[((st * NIN + k) * ITEMS + i) * BS];
-    else return *reinterpret_cast<const Raw *>(src[k] + bytes + (long long)i * step);
+  // Asks for a row to come and waits for the present one.
+  template <typename F>
+  __device__ __forceinline__ void turn(F ask) const {
+    if constexpr (NS > 0 && kShared) {
+      static_assert(NS == 2, "one row ahead");
+      cp_async_wait<0>();
+      __syncthreads();       // the row is there, the one before is read
+      ask();
+    } else if constexpr (NS > 0) {
+      ask();
+      cp_async_wait<NS - 1>();
+    }
+  }
+  __device__ __forceinline__ Raw get(int st, int k, int i, long long row, long long bytes,
+                                     int step) const {
+    if constexpr (NS > 0 && kShared) {
+      const int odd = (int)(reinterpret_cast<uintptr_t>(src[k] + row * D * 2) & 2);
+      return *reinterpret_cast<const Raw *>(reinterpret_cast<const char *>(base) +
+                                            (st * NIN + k) * pitch + odd + 2 * (lane + i * tpr));
+    } else if constexpr (NS > 0) {
+      return base[((st * NIN + k) * ITEMS + i) * BS];
+    } else {
+      return *reinterpret_cast<const Raw *>(src[k] + bytes + (long long)i * step);
+    }
   }
 };
 

@@ -12,6 +12,7 @@ struct NormBwdParams {
   void *dy, *d_res, *d_gate;
   float *part_post, *part_pre, *part_gate;   // [units][D]
   long long gate_rows;
+  int staged;      // bytes of staged rows
   int splits;      // units per gate row (group gates), 0: whole gate rows per unit
 };
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ void flush(typename Pc::P (&acc)[ITEMS][Pc::E], int t
 //
 // With m = out, v = d_out + s2 d_x w_pre and q = aw n1 (aw = scale act(gate)
 // w_post), a row needs sum(d_x w_pre m), sum(q v) and sum(q m); then
-//   r = v - k m,  dy = s1 (aw r - c1 n1),
+//   r = v - s2^3 mean(d_x w_pre m) m,  dy = s1 (aw r - c1 n1),
 // and the column sums of r n1 give dw_post and (gate rows shared by rows,
 // where act(gate) is a factor of the column) d_gate at once.  One piece per
 // thread keeps these values for the second pass over the row, more pieces
@@ -55,7 +56,8 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   using P = typename Pc::P;
   using Raw = typename Pc::Raw;
   constexpr int E = Pc::E, kOut = 1, kX = 2, kRes = 3, kGate = GATE == kGateEach ? 4 : 0;
-  constexpr bool kKeep = ITEMS == 1;
+  constexpr bool kKeep = ITEMS * VEC <= 8;      // these stay in registers between the passes
+  constexpr int KI = kKeep ? ITEMS : 1;
   using In = Stage<T, VEC, ITEMS, GATE == kGateEach ? 5 : 4, BS, NS>;
   constexpr int kAhead = NS > 0 ? NS - 1 : 0;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -63,11 +65,14 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   const NormParams &p = q.f;
   const int tid = threadIdx.x, tpr = p.tpr, rg = p.rg;
   const int group = tid / tpr, lane = tid - group * tpr;
-  P *buf = reinterpret_cast<P *>(smem + In::kBytes);       // for flush, when rg > 1
+  P *buf = reinterpret_cast<P *>(smem + q.staged);         // for flush, when rg > 1
   const int step = tpr * VEC * (int)sizeof(T);             // bytes between a thread's pieces
   const long long row_bytes = (long long)p.D * sizeof(T);
   In in;
-  in.base = reinterpret_cast<Raw *>(smem) + tid;
+  in.lane = lane;
+  in.tpr = tpr;
+  in.D = p.D;
+  in.init(smem, tid, group, rg);
   in.src[0] = (const char *)p.y;
   in.src[kOut] = (const char *)q.d_out;
   in.src[kX] = (const char *)q.d_x;
@@ -78,7 +83,7 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   for (int i = 0; i < ITEMS; ++i) has[i] = (lane + i * tpr) * VEC < p.D;
   int slot = 0;
 
-  P dw1[ITEMS][E], dw2[ITEMS][E], w1k[1][E], w2k[1][E];
+  P dw1[ITEMS][E], dw2[ITEMS][E], w1k[KI][E], w2k[KI][E];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
@@ -96,7 +101,9 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
 #pragma unroll
     for (int e = 0; e < E; ++e) w1[e] = mul(w1[e], scale);
   };
-  if (kKeep) weights(0, w1k[0], w2k[0]);
+  if (kKeep)
+#pragma unroll
+    for (int i = 0; i < KI; ++i) weights(i, w1k[i], w2k[i]);
 
   // the gate rows [g_lo, g_hi) of this unit, or its part of one gate row
   long long g_lo = 0, g_hi = 1;
@@ -141,7 +148,7 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
     const long long advance = rg * row_bytes;
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
-      in.fetch(s, lo + group + s * rg < hi, has, at + s * advance, step);
+      in.fetch(s, lo + group + s * rg < hi, has, lo + group + s * rg, at + s * advance, step);
     for (long long row = lo + group; row - group < hi; row += rg, at += advance) {
       const bool live = row < hi;
       float s1 = 0.f, s2 = 0.f;
@@ -149,27 +156,28 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
         s1 = p.stats[row];
         s2 = p.stats[p.R + row];
       }
-      in.fetch(st == 0 ? kAhead : st - 1, row + kAhead * rg < hi, has, at + kAhead * advance,
-               step);
-      if (NS > 0) cp_async_wait<kAhead>();
+      in.turn([&]() {
+        in.fetch(st == 0 ? kAhead : st - 1, row + kAhead * rg < hi, has, row + kAhead * rg,
+                 at + kAhead * advance, step);
+      });
       // n1, m, v, d_x, act(gate) and its derivative of a piece
       auto front = [&](int i, const P(&w1)[E], const P(&w2)[E], P(&n1)[E], P(&m)[E], P(&v)[E],
                        P(&gx)[E], P(&a)[E], P(&da)[E], P(&qv)[E]) {
-        Pc::get(in.get(st, 0, i, at, step), n1);
-        if (q.d_out) Pc::get(in.get(st, kOut, i, at, step), v);
+        Pc::get(in.get(st, 0, i, row, at, step), n1);
+        if (q.d_out) Pc::get(in.get(st, kOut, i, row, at, step), v);
         else
 #pragma unroll
           for (int e = 0; e < E; ++e) v[e] = both<P>(0.f);
-        if (q.d_x) Pc::get(in.get(st, kX, i, at, step), gx);
+        if (q.d_x) Pc::get(in.get(st, kX, i, row, at, step), gx);
         else
 #pragma unroll
           for (int e = 0; e < E; ++e) gx[e] = both<P>(0.f);
-        if (p.res) Pc::get(in.get(st, kRes, i, at, step), m);
+        if (p.res) Pc::get(in.get(st, kRes, i, row, at, step), m);
         else
 #pragma unroll
           for (int e = 0; e < E; ++e) m[e] = both<P>(0.f);
         if (GATE == kGateEach) {
-          Pc::get(in.get(st, kGate, i, at, step), a);
+          Pc::get(in.get(st, kGate, i, row, at, step), a);
           gate_values<true>(p.act, a, da);
         }
 #pragma unroll
@@ -182,58 +190,60 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
           v[e] = fma(mul(gx[e], w2[e]), both<P>(s2), v[e]);
         }
       };
-      P n1[1][E], m[1][E], v[1][E], gx[1][E], a[1][E], da[1][E];
+      P n1[KI][E], m[KI][E], v[KI][E], gx[KI][E], a[KI][E], da[KI][E];
       P acc0 = both<P>(0.f), acc1 = acc0, acc2 = acc0;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         if (live && has[i]) {
+          const int k = kKeep ? i : 0;
           P w1[E], w2[E], qv[E];
           if (!kKeep) weights(i, w1, w2);
-          front(i, kKeep ? w1k[0] : w1, kKeep ? w2k[0] : w2, n1[0], m[0], v[0], gx[0], a[0], da[0],
+          front(i, kKeep ? w1k[k] : w1, kKeep ? w2k[k] : w2, n1[k], m[k], v[k], gx[k], a[k], da[k],
                 qv);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            acc0 = fma(mul(gx[0][e], kKeep ? w2k[0][e] : w2[e]), m[0][e], acc0);
-            acc1 = fma(qv[e], v[0][e], acc1);
-            acc2 = fma(qv[e], m[0][e], acc2);
+            acc0 = fma(mul(gx[k][e], kKeep ? w2k[k][e] : w2[e]), m[k][e], acc0);
+            acc1 = fma(qv[e], v[k][e], acc1);
+            acc2 = fma(qv[e], m[k][e], acc2);
           }
         }
       }
       float sum[3] = {total(acc0), total(acc1), total(acc2)};
       row_sum3(sum, tpr, red, slot);
-      const float k = s2 * s2 * s2 * sum[0] * p.inv_d;   // s2 c2, times s2: r = v - k m
-      const float c1 = (sum[1] - k * sum[2]) * p.inv_d;
-      const P nk = both<P>(-k), nc = both<P>(-c1 * s1), ps1 = both<P>(s1), ps2 = both<P>(s2);
+      const float kc = s2 * s2 * s2 * sum[0] * p.inv_d;   // s2 c2, times s2: r = v - kc m
+      const float c1 = (sum[1] - kc * sum[2]) * p.inv_d;
+      const P nk = both<P>(-kc), nc = both<P>(-c1 * s1), ps1 = both<P>(s1), ps2 = both<P>(s2);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         const long long o = at + (long long)i * step;
         if (live && has[i]) {
+          const int k = kKeep ? i : 0;
           P w1[E], w2[E], oy[E], og[E], qv[E];
           if (!kKeep) {
             weights(i, w1, w2);
-            front(i, w1, w2, n1[0], m[0], v[0], gx[0], a[0], da[0], qv);
+            front(i, w1, w2, n1[k], m[k], v[k], gx[k], a[k], da[k], qv);
           }
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const P w = kKeep ? w1k[0][e] : w1[e];
-            dw2[i][e] = fma(mul(gx[0][e], ps2), m[0][e], dw2[i][e]);
-            v[0][e] = fma(m[0][e], nk, v[0][e]);            // r
+            const P w = kKeep ? w1k[k][e] : w1[e];
+            dw2[i][e] = fma(mul(gx[k][e], ps2), m[k][e], dw2[i][e]);
+            v[k][e] = fma(m[k][e], nk, v[k][e]);            // r
             P aw = w;
             if (GATE == kGateEach) {
-              const P x = mul(v[0][e], n1[0][e]);
-              dw1[i][e] = fma(a[0][e], x, dw1[i][e]);
-              og[e] = mul(mul(w, da[0][e]), x);
-              aw = mul(w, a[0][e]);
+              const P x = mul(v[k][e], n1[k][e]);
+              dw1[i][e] = fma(a[k][e], x, dw1[i][e]);
+              og[e] = mul(mul(w, da[k][e]), x);
+              aw = mul(w, a[k][e]);
             } else if (GATE == kGateGroup) {
-              es[i < GI ? i : 0][e] = fma(v[0][e], n1[0][e], es[i < GI ? i : 0][e]);
+              es[i < GI ? i : 0][e] = fma(v[k][e], n1[k][e], es[i < GI ? i : 0][e]);
               aw = mul(w, ga[i < GI ? i : 0][e]);
             } else {
-              dw1[i][e] = fma(v[0][e], n1[0][e], dw1[i][e]);
+              dw1[i][e] = fma(v[k][e], n1[k][e], dw1[i][e]);
             }
-            oy[e] = fma(mul(aw, v[0][e]), ps1, mul(n1[0][e], nc));
+            oy[e] = fma(mul(aw, v[k][e]), ps1, mul(n1[k][e], nc));
           }
           *reinterpret_cast<Raw *>((char *)q.dy + o) = Pc::put(oy);
-          if (q.d_res) *reinterpret_cast<Raw *>((char *)q.d_res + o) = Pc::put(v[0]);
+          if (q.d_res) *reinterpret_cast<Raw *>((char *)q.d_res + o) = Pc::put(v[k]);
           if (GATE == kGateEach && q.d_gate)
             *reinterpret_cast<Raw *>((char *)q.d_gate + o) = Pc::put(og);
         }
@@ -241,6 +251,7 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
       st = st == kAhead ? 0 : st + 1;
     }
     if (NS > 0) cp_async_wait<0>();
+    if (In::kShared && NS > 0) __syncthreads();     // the last row is read
     if constexpr (GATE == kGateGroup) {
 #pragma unroll
       for (int i = 0; i < GI; ++i)
@@ -300,6 +311,12 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+constexpr Built kBuilt[] = {{2, 8, 1, 256}, {2, 8, 1, 512}, {2, 8, 2, 512}, {2, 8, 4, 512},
+                            {2, 2, 4, 256}, {2, 2, 4, 512}, {2, 2, 8, 1024},
+                            {2, 1, 8, 256}, {2, 1, 8, 512}, {2, 1, 16, 1024},
+                            {4, 4, 1, 256}, {4, 4, 1, 512}, {4, 4, 2, 512}, {4, 4, 4, 512},
+                            {4, 4, 8, 512}, {4, 1, 4, 256}, {4, 1, 4, 512}, {4, 1, 16, 1024}};
+
 // Units (CTAs) of the backward: as many as are resident on 152 SMs at up to
 // 128 registers per thread, and no more than there are row groups.
 int units_for(const kda_norm_desc *d, const Layout &l) {
@@ -318,11 +335,11 @@ int splits_for(const kda_norm_desc *d, const Layout &l, int units) {
 }
 
 template <typename T, int VEC, int ITEMS, int GATE, int BS, int NS>
-cudaError_t launch_g(const NormBwdParams &q, int units, cudaStream_t stream) {
+cudaError_t launch_g(NormBwdParams q, int units, cudaStream_t stream) {
   auto kern = norm_bwd_kernel<T, VEC, ITEMS, GATE, BS, NS>;
   const int threads = q.f.tpr * q.f.rg;
-  const size_t smem = Stage<T, VEC, ITEMS, GATE == kGateEach ? 5 : 4, BS, NS>::kBytes +
-                      (q.f.rg > 1 ? sizeof(float) * threads * VEC : 0);
+  q.staged = (int)Stage<T, VEC, ITEMS, GATE == kGateEach ? 5 : 4, BS, NS>::bytes(q.f.D, q.f.rg);
+  const size_t smem = q.staged + (q.f.rg > 1 ? sizeof(float) * threads * VEC : 0);
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<units, threads, smem, stream>>>(q);
@@ -348,8 +365,8 @@ size_t kda_block_norm_bwd_workspace_size(const kda_norm_desc *d, int has_gate) {
   if (check_desc(d, has_gate != 0) != KDA_OK) return 0;
   // the largest over the layouts, since types and pointers choose between them
   size_t n = 0;
-  for (int v = 0; v < 3; ++v) {
-    const Layout l = layout_for(d->dim, v == 1 ? 2 : 4, v != 0, 1);
+  for (int v = 0; v < 4; ++v) {
+    const Layout l = layout_for(kBuilt, d->dim, v < 2 ? 2 : 4, v % 2 != 0);
     size_t units = (size_t)units_for(d, l), gate_units = 0;
     if (has_gate && d->gate_rows < d->rows) {
       const int s = splits_for(d, l, (int)units);
@@ -379,14 +396,13 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
   for (const void *ptr : {y, (const void *)w_post, residual, gate, (const void *)w_pre, d_out, d_x,
                           (const void *)dy, (const void *)d_residual, (const void *)d_gate})
     vec = vec && aligned16(ptr);
-  const Layout l = layout_for(d->dim, bf16 ? 2 : 4, vec, 1);
+  const Layout l = layout_for(kBuilt, d->dim, bf16 ? 2 : 4, vec);
   NormBwdParams q = {};
   q.f = params_of(d, l, y, w_post, residual, gate, w_pre);
   q.f.stats = const_cast<float *>(stats);
   q.d_out = d_out; q.d_x = d_x; q.dy = dy; q.d_res = d_residual; q.d_gate = d_gate;
   q.gate_rows = gate ? d->gate_rows : 0;
   const int mode = gate_mode(d, gate);
-  const bool small = l.tpr * l.rg <= kBlock;
   int units = units_for(d, l);
   if (mode == kGateGroup) {
     q.splits = splits_for(d, l, units);
@@ -399,26 +415,30 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
   using B = __nv_bfloat16;
+  const bool small = l.bs == 256;
   if (l.vec == 8)
-    e = l.items == 1   ? (small ? launch<B, 8, 1, 256, 3>(q, mode, units, cs)
-                                : launch<B, 8, 1, 512, 3>(q, mode, units, cs))
+    e = l.items == 4   ? launch<B, 8, 4, 512, 0>(q, mode, units, cs)
         : l.items == 2 ? launch<B, 8, 2, 512, 2>(q, mode, units, cs)
-                       : launch<B, 8, 4, 512, 0>(q, mode, units, cs);
+        : small        ? launch<B, 8, 1, 256, 3>(q, mode, units, cs)
+                       : launch<B, 8, 1, 512, 3>(q, mode, units, cs);
   else if (l.vec == 4)
-    e = l.items == 1   ? (small ? launch<float, 4, 1, 256, 3>(q, mode, units, cs)
-                                : launch<float, 4, 1, 512, 3>(q, mode, units, cs))
-        : l.items == 2 ? launch<float, 4, 2, 512, 2>(q, mode, units, cs)
+    e = l.items == 8   ? launch<float, 4, 8, 512, 0>(q, mode, units, cs)
         : l.items == 4 ? launch<float, 4, 4, 512, 0>(q, mode, units, cs)
-                       : launch<float, 4, 8, 512, 0>(q, mode, units, cs);
+        : l.items == 2 ? launch<float, 4, 2, 512, 2>(q, mode, units, cs)
+        : small        ? launch<float, 4, 1, 256, 3>(q, mode, units, cs)
+                       : launch<float, 4, 1, 512, 3>(q, mode, units, cs);
   else if (l.vec == 2)
-    e = l.items == 2 ? launch<B, 2, 2, 1024, 0>(q, mode, units, cs)
-                     : launch<B, 2, 8, 1024, 0>(q, mode, units, cs);
+    e = l.items == 8 ? launch<B, 2, 8, 1024, 0>(q, mode, units, cs)
+        : small      ? launch<B, 2, 4, 256, 3>(q, mode, units, cs)
+                     : launch<B, 2, 4, 512, 3>(q, mode, units, cs);
   else if (bf16)
-    e = l.items == 4 ? launch<B, 1, 4, 1024, 0>(q, mode, units, cs)
-                     : launch<B, 1, 16, 1024, 0>(q, mode, units, cs);
+    e = l.items == 16 ? launch<B, 1, 16, 1024, 0>(q, mode, units, cs)
+        : small       ? launch<B, 1, 8, 256, 2>(q, mode, units, cs)
+                      : launch<B, 1, 8, 512, 2>(q, mode, units, cs);
   else
-    e = l.items == 4 ? launch<float, 1, 4, 1024, 0>(q, mode, units, cs)
-                     : launch<float, 1, 16, 1024, 0>(q, mode, units, cs);
+    e = l.items == 16 ? launch<float, 1, 16, 1024, 0>(q, mode, units, cs)
+        : small       ? launch<float, 1, 4, 256, 3>(q, mode, units, cs)
+                      : launch<float, 1, 4, 512, 2>(q, mode, units, cs);
   if (e != cudaSuccess) return KDA_ERR_CUDA;
   const bool gate_parts = mode == kGateGroup && q.splits && d_gate;
   const dim3 grid((d->dim + 31) / 32, 2 + (gate_parts ? (unsigned)d->gate_rows : 0));
