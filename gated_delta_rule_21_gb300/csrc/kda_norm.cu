@@ -20,8 +20,9 @@
 // so a row costs one reduction and its inputs are read once.
 //
 // Both kernels are bound by HBM.  Rows whose length or pointers do not allow
-// 16-byte accesses take the same code with pieces of 4 bytes, and bf16 rows of
-// odd length with single elements.  This file: the forward; kda_norm_bwd.cu: the backward.
+// 16-byte accesses take the same code with pieces of 4 bytes; bf16 rows of odd
+// length, which begin in the middle of a word, are joined in shared memory.
+// This file: the forward; kda_norm_bwd.cu: the backward.
 #include "kda_norm.cuh"
 
 namespace kda {
@@ -36,14 +37,13 @@ template <typename T, int VEC, int ITEMS, int GATE, int BS, int NS>
 __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
   using Pc = Piece<T, VEC>;
   using P = typename Pc::P;
-  using Raw = typename Pc::Raw;
-  constexpr int E = Pc::E, kRes = 1, kGate = 2;
+  constexpr int E = Pc::E, W = Pc::kStep, kRes = 1, kGate = 2;
   using In = Stage<T, VEC, ITEMS, GATE == kGateEach ? 3 : 2, BS, NS>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float red[2][32];
   const int tid = threadIdx.x, tpr = p.tpr, rg = p.rg;
   const int group = tid / tpr, lane = tid - group * tpr;
-  const int step = tpr * VEC * (int)sizeof(T);        // bytes between a thread's pieces
+  const int step = tpr * W * (int)sizeof(T);        // bytes between a thread's pieces
   const long long row_bytes = (long long)p.D * sizeof(T);
   In in;
   in.lane = lane;
@@ -53,18 +53,21 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
   in.src[0] = (const char *)p.y;
   in.src[kRes] = (const char *)p.res;
   if constexpr (GATE == kGateEach) in.src[kGate] = (const char *)p.gate;
-  bool has[ITEMS];
+  bool has[ITEMS], whole[ITEMS];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) has[i] = (lane + i * tpr) * VEC < p.D;
-  const float *w_post = p.w_post + lane * VEC, *w_pre = p.w_pre ? p.w_pre + lane * VEC : nullptr;
-  const int wstep = tpr * VEC;
+  for (int i = 0; i < ITEMS; ++i) {
+    has[i] = (lane + i * tpr) * W < p.D;
+    whole[i] = !Pc::kRagged || (lane + i * tpr) * W + W <= p.D;
+  }
+  const float *w_post = p.w_post + lane * W, *w_pre = p.w_pre ? p.w_pre + lane * W : nullptr;
+  const int wstep = tpr * W;
   int slot = 0, st = 0;
   const long long lo = (long long)blockIdx.x * p.R / gridDim.x,
                   hi = (long long)(blockIdx.x + 1) * p.R / gridDim.x;
   constexpr int GI = GATE == kGateGroup ? ITEMS : 1, kAhead = NS > 0 ? NS - 1 : 0;
   P ga[GI][E];
   unsigned ga_row = ~0u;
-  long long at = (lo + group) * row_bytes + (long long)lane * VEC * sizeof(T);
+  long long at = (lo + group) * row_bytes + (long long)lane * W * sizeof(T);
   const long long advance = rg * row_bytes;
 #pragma unroll
   for (int s = 0; s < kAhead; ++s)
@@ -83,8 +86,9 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
         for (int i = 0; i < GI; ++i) {
           P d[E];
           if (has[i]) {
-            Pc::get(*reinterpret_cast<const Raw *>((const char *)p.gate + g * row_bytes +
-                                                   (long long)lane * VEC * sizeof(T) + i * step),
+            Pc::get(Pc::read((const char *)p.gate + g * row_bytes +
+                                 (long long)lane * W * sizeof(T) + i * step,
+                             whole[i]),
                     ga[i]);
             gate_values<false>(p.act, ga[i], d);
           }
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
         if (has[i]) {
-          Pc::get(in.get(st, 0, i, row, at, step), v[i]);
+          Pc::get(in.get(st, 0, i, whole[i], row, at, step), v[i]);
 #pragma unroll
           for (int e = 0; e < E; ++e) acc = fma(v[i][e], v[i][e], acc);
         }
@@ -109,12 +113,12 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
       for (int i = 0; i < ITEMS; ++i)
         if (has[i]) {
           P w[E], a[E];
-          Pc::weight(w_post + i * wstep, w);
+          Pc::weight(w_post + i * wstep, w, whole[i]);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], mul(w[e], k));
           if (GATE == kGateEach) {
             P d[E];
-            Pc::get(in.get(st, kGate < (GATE == kGateEach ? 3 : 2) ? kGate : 0, i, row, at, step), a);
+            Pc::get(in.get(st, kGate < (GATE == kGateEach ? 3 : 2) ? kGate : 0, i, whole[i], row, at, step), a);
             gate_values<false>(p.act, a, d);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], a[e]);
@@ -123,11 +127,11 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], ga[i < GI ? i : 0][e]);
           if (p.res) {
-            Pc::get(in.get(st, kRes, i, row, at, step), a);
+            Pc::get(in.get(st, kRes, i, whole[i], row, at, step), a);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = add(v[i][e], a[e]);
           }
-          *reinterpret_cast<Raw *>((char *)p.out + at + (long long)i * step) = Pc::put(v[i]);
+          Pc::write((char *)p.out + at + (long long)i * step, v[i], whole[i]);
 #pragma unroll
           for (int e = 0; e < E; ++e) acc = fma(v[i][e], v[i][e], acc);
         }
@@ -140,10 +144,10 @@ __global__ void __launch_bounds__(BS) norm_fwd_kernel(const NormParams p) {
         for (int i = 0; i < ITEMS; ++i)
           if (has[i]) {
             P w[E];
-            Pc::weight(w_pre + i * wstep, w);
+            Pc::weight(w_pre + i * wstep, w, whole[i]);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[i][e] = mul(v[i][e], mul(w[e], both<P>(s2)));
-            *reinterpret_cast<Raw *>((char *)p.x + at + (long long)i * step) = Pc::put(v[i]);
+            Pc::write((char *)p.x + at + (long long)i * step, v[i], whole[i]);
           }
       }
     }
@@ -208,7 +212,7 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
                           (const void *)out, (const void *)x})
     vec = vec && aligned16(ptr);
   static const Built built[] = {{2, 8, 2, 256}, {2, 8, 2, 512}, {2, 8, 4, 512},
-                                {2, 2, 8, 256}, {2, 2, 8, 1024}, {2, 1, 16, 256}, {2, 1, 16, 1024},
+                                {2, 2, 8, 256}, {2, 2, 8, 1024}, {2, 1, 8, 256}, {2, 1, 8, 1024},
                                 {4, 4, 2, 256}, {4, 4, 2, 512}, {4, 4, 4, 512}, {4, 4, 8, 512},
                                 {4, 1, 8, 256}, {4, 1, 8, 512}, {4, 1, 16, 1024}};
   const Layout l = layout_for(built, d->dim, bf16 ? 2 : 4, vec);
@@ -230,8 +234,7 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
   else if (l.vec == 2)
     e = l.bs == 256 ? launch<B, 2, 8, 256, 3>(p, mode, cs) : launch<B, 2, 8, 1024, 0>(p, mode, cs);
   else if (bf16)
-    e = l.bs == 256 ? launch<B, 1, 16, 256, 2>(p, mode, cs)
-                    : launch<B, 1, 16, 1024, 2>(p, mode, cs);
+    e = l.bs == 256 ? launch<B, 1, 8, 256, 2>(p, mode, cs) : launch<B, 1, 8, 1024, 2>(p, mode, cs);
   else
     e = l.items == 16 ? launch<float, 1, 16, 1024, 0>(p, mode, cs)
         : l.bs == 256 ? launch<float, 1, 8, 256, 3>(p, mode, cs)

@@ -20,7 +20,8 @@ enum { kGateNone = 0, kGateEach = 1, kGateGroup = 2 };
 // warps), each owning `items` pieces of `vec` elements that lie tpr pieces
 // apart; a CTA holds `rg` rows when a row needs fewer than 256 threads.
 struct Layout {
-  int vec;      // elements per access: 16 bytes, 2 (bf16, even rows) or 1
+  int vec;      // elements per access: 16 bytes, 2 (bf16, even rows); 1: fp32, or pairs
+                // of bf16 whose rows need not begin on a word
   int items, tpr, rg;
   int bs;       // most threads of the kernel
 };
@@ -36,7 +37,7 @@ template <int N>
 Layout layout_for(const Built (&built)[N], int D, int elt, bool vector_ok) {
   Layout l;
   l.vec = !vector_ok ? 1 : D % (16 / elt) == 0 ? 16 / elt : elt == 2 && D % 2 == 0 ? 2 : 1;
-  const int n = D / l.vec;
+  const int n = l.vec == 1 && elt == 2 ? (D + 1) / 2 : D / l.vec;
   for (const Built &k : built)
     if (k.elt == elt && k.vec == l.vec && k.items * k.bs >= n) {
       l.items = k.items;
@@ -110,13 +111,16 @@ template <typename P> __device__ __forceinline__ P both(float a);
 template <> __device__ __forceinline__ P1 both<P1>(float a) { return {a}; }
 template <> __device__ __forceinline__ P2 both<P2>(float a) { return {pk2(a, a)}; }
 
-// VEC elements in memory (Raw) and in registers (E values of type P).
+// A piece of kStep elements in memory (Raw) and in registers (E values of type
+// P).  `whole` is false for a ragged piece of which only the first element lies
+// in the row; its second one reads as 0 and is not written.
 template <typename T, int VEC>
 struct Piece {
   static_assert(VEC * sizeof(T) == 16 || (VEC == 2 && sizeof(T) == 2), "accesses");
   using Raw = typename std::conditional<VEC * sizeof(T) == 16, uint4, uint32_t>::type;
   using P = P2;
-  static constexpr int E = VEC / 2;
+  static constexpr int E = VEC / 2, kStep = VEC;
+  static constexpr bool kRagged = false;
   static __device__ __forceinline__ void get(const Raw &a, P2 (&f)[E]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&a);
 #pragma unroll
@@ -125,7 +129,10 @@ struct Piece {
                    ? pk2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]))
                    : pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ Raw put(const P2 (&f)[E]) {
+  static __device__ __forceinline__ Raw read(const void *p, bool) {
+    return *static_cast<const Raw *>(p);
+  }
+  static __device__ __forceinline__ void write(void *p, const P2 (&f)[E], bool) {
     Raw a;
     uint32_t *w = reinterpret_cast<uint32_t *>(&a);
 #pragma unroll
@@ -140,9 +147,9 @@ struct Piece {
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
       }
     }
-    return a;
+    *static_cast<Raw *>(p) = a;
   }
-  static __device__ __forceinline__ void weight(const float *w, P2 (&f)[E]) {
+  static __device__ __forceinline__ void weight(const float *w, P2 (&f)[E], bool) {
     if constexpr (VEC == 2) {
       const float2 a = *reinterpret_cast<const float2 *>(w);
       f[0].v = pk2(a.x, a.y);
@@ -155,20 +162,62 @@ struct Piece {
       }
     }
   }
-  static __device__ __forceinline__ void store(float *w, const P2 (&f)[E]) {
+  static __device__ __forceinline__ void store(float *w, const P2 (&f)[E], bool) {
 #pragma unroll
     for (int i = 0; i < E; ++i) upk2(f[i].v, w[2 * i], w[2 * i + 1]);
   }
 };
-template <typename T>
-struct Piece<T, 1> {
-  using Raw = T;
+template <>
+struct Piece<float, 1> {
+  using Raw = float;
   using P = P1;
-  static constexpr int E = 1;
-  static __device__ __forceinline__ void get(const Raw &a, P1 (&f)[1]) { f[0].v = to_f32(a); }
-  static __device__ __forceinline__ Raw put(const P1 (&f)[1]) { return from_f32<T>(f[0].v); }
-  static __device__ __forceinline__ void weight(const float *w, P1 (&f)[1]) { f[0].v = *w; }
-  static __device__ __forceinline__ void store(float *w, const P1 (&f)[1]) { *w = f[0].v; }
+  static constexpr int E = 1, kStep = 1;
+  static constexpr bool kRagged = false;
+  static __device__ __forceinline__ void get(const Raw &a, P1 (&f)[1]) { f[0].v = a; }
+  static __device__ __forceinline__ Raw read(const void *p, bool) {
+    return *static_cast<const float *>(p);
+  }
+  static __device__ __forceinline__ void write(void *p, const P1 (&f)[1], bool) {
+    *static_cast<float *>(p) = f[0].v;
+  }
+  static __device__ __forceinline__ void weight(const float *w, P1 (&f)[1], bool) { f[0].v = *w; }
+  static __device__ __forceinline__ void store(float *w, const P1 (&f)[1], bool) { *w = f[0].v; }
+};
+template <>
+struct Piece<__nv_bfloat16, 1> {
+  using Raw = uint32_t;
+  using P = P2;
+  static constexpr int E = 1, kStep = 2;
+  static constexpr bool kRagged = true;
+  static __device__ __forceinline__ void get(const Raw &a, P2 (&f)[1]) {
+    f[0].v = pk2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
+  static __device__ __forceinline__ Raw read(const void *p, bool whole) {
+    const unsigned short *h = static_cast<const unsigned short *>(p);
+    return (uint32_t)h[0] | (whole ? (uint32_t)h[1] << 16 : 0u);
+  }
+  static __device__ __forceinline__ void write(void *p, const P2 (&f)[1], bool whole) {
+    float x, y;
+    upk2(f[0].v, x, y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const uint32_t a = *reinterpret_cast<const uint32_t *>(&h);
+    unsigned short *o = static_cast<unsigned short *>(p);
+    if (whole && (reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+      *reinterpret_cast<uint32_t *>(o) = a;
+    } else {
+      o[0] = (unsigned short)a;
+      if (whole) o[1] = (unsigned short)(a >> 16);
+    }
+  }
+  static __device__ __forceinline__ void weight(const float *w, P2 (&f)[1], bool whole) {
+    f[0].v = pk2(w[0], whole ? w[1] : 0.f);
+  }
+  static __device__ __forceinline__ void store(float *w, const P2 (&f)[1], bool whole) {
+    float x, y;
+    upk2(f[0].v, x, y);
+    w[0] = x;
+    if (whole) w[1] = y;
+  }
 };
 
 __device__ __forceinline__ float sfu_ex2(float x) {
@@ -307,15 +356,16 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 
 // The rows to come, copied to shared memory NS - 1 ahead (NS = 0: inputs are
 // read where they are used).  Pieces of 4 or 16 bytes: a thread copies its
-// own, [stage][input][item][BS threads], and no barrier guards them.  bf16
-// rows of odd length start in the middle of a word: their words are copied
-// by whoever comes, [stage][input][row group][row], and one barrier per row
-// lets every thread read its elements.
+// own, [stage][input][item][BS threads], and no barrier guards them.  Ragged
+// rows start in the middle of a word: their words are copied by whoever
+// comes, [stage][input][row group][row], and one barrier per row lets every
+// thread read its elements.
 template <typename T, int VEC, int ITEMS, int NIN, int BS, int NS>
 struct Stage {
-  using Raw = typename Piece<T, VEC>::Raw;
-  static constexpr bool kShared = sizeof(Raw) == 2;
-  Raw *base;            // of this thread, or of its row group
+  using Pc = Piece<T, VEC>;
+  using Raw = typename Pc::Raw;
+  static constexpr bool kShared = Pc::kRagged;
+  unsigned char *base;  // of this thread, or of its row group
   const char *src[NIN]; // the inputs, null where absent
   int lane, tpr, D;
   int pitch;            // kShared: bytes between the stages' inputs
@@ -327,11 +377,14 @@ struct Stage {
                    : (size_t)NS * NIN * ITEMS * BS * sizeof(Raw);
   }
   __device__ __forceinline__ void init(unsigned char *smem, int tid, int group, int rg) {
-    base = kShared ? reinterpret_cast<Raw *>(smem + (size_t)group * row_pitch(D))
-                   : reinterpret_cast<Raw *>(smem) + tid;
+    base = kShared ? smem + (size_t)group * row_pitch(D) : smem + tid * sizeof(Raw);
     pitch = rg * row_pitch(D);
   }
 
+  // Byte of a ragged row's first element within its first word.
+  __device__ __forceinline__ int odd(int k, long long row) const {
+    return (int)((reinterpret_cast<uintptr_t>(src[k]) ^ (uintptr_t)((row & D) << 1)) & 2);
+  }
   // row: its number; bytes: the thread's first piece; step: between pieces
   __device__ __forceinline__ void fetch(int st, bool live, const bool (&has)[ITEMS], long long row,
                                         long long bytes, int step) const {
@@ -345,19 +398,19 @@ struct Stage {
               const char *s = src[k] + start;
               // whole words by cp.async, a half word at either end by hand;
               // element c lies at byte 2 c + (address of the row & 2)
-              const int odd = (int)(reinterpret_cast<uintptr_t>(s) & 2);
-              char *d = reinterpret_cast<char *>(base) + (st * NIN + k) * pitch;
-              const int words = (2 * D - odd) / 4;
-              const uint32_t ds = (uint32_t)__cvta_generic_to_shared(d) + 2 * odd;
-              for (int w = lane; w < words; w += tpr) cp_async4(ds + 4 * w, s + odd + 4 * w);
-              if (odd && lane == 0)
-                *reinterpret_cast<T *>(d + 2) = *reinterpret_cast<const T *>(s);
-              if (2 * D - odd - 4 * words && lane == tpr - 1)
-                *reinterpret_cast<T *>(d + odd + 2 * D - 2) =
+              const int o = odd(k, row);
+              unsigned char *d = base + (st * NIN + k) * pitch;
+              const int words = (2 * D - o) / 4;
+              const uint32_t ds = (uint32_t)__cvta_generic_to_shared(d) + 2 * o;
+              for (int w = lane; w < words; w += tpr) cp_async4(ds + 4 * w, s + o + 4 * w);
+              if (o && lane == 0) *reinterpret_cast<T *>(d + 2) = *reinterpret_cast<const T *>(s);
+              if (2 * D - o - 4 * words && lane == tpr - 1)
+                *reinterpret_cast<T *>(d + o + 2 * D - 2) =
                     *reinterpret_cast<const T *>(s + 2 * D - 2);
             }
         } else {
-          const uint32_t d = (uint32_t)__cvta_generic_to_shared(base + st * NIN * ITEMS * BS);
+          const uint32_t d = (uint32_t)__cvta_generic_to_shared(base) +
+                             (uint32_t)(st * NIN * ITEMS * BS * sizeof(Raw));
 #pragma unroll
           for (int k = 0; k < NIN; ++k)
             if (src[k]) {
@@ -388,17 +441,14 @@ struct Stage {
       cp_async_wait<NS - 1>();
     }
   }
-  __device__ __forceinline__ Raw get(int st, int k, int i, long long row, long long bytes,
-                                     int step) const {
-    if constexpr (NS > 0 && kShared) {
-      const int odd = (int)(reinterpret_cast<uintptr_t>(src[k] + row * D * 2) & 2);
-      return *reinterpret_cast<const Raw *>(reinterpret_cast<const char *>(base) +
-                                            (st * NIN + k) * pitch + odd + 2 * (lane + i * tpr));
-    } else if constexpr (NS > 0) {
-      return base[((st * NIN + k) * ITEMS + i) * BS];
-    } else {
-      return *reinterpret_cast<const Raw *>(src[k] + bytes + (long long)i * step);
-    }
+  __device__ __forceinline__ Raw get(int st, int k, int i, bool whole, long long row,
+                                     long long bytes, int step) const {
+    if constexpr (NS > 0 && kShared)
+      return Pc::read(base + (st * NIN + k) * pitch + odd(k, row) + 4 * (lane + i * tpr), whole);
+    else if constexpr (NS > 0)
+      return Pc::read(base + ((st * NIN + k) * ITEMS + i) * BS * sizeof(Raw), true);
+    else
+      return Pc::read(src[k] + bytes + (long long)i * step, whole);
   }
 };
 

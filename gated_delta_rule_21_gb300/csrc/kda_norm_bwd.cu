@@ -18,12 +18,12 @@ struct NormBwdParams {
 
 // Sums `acc` over the CTA's row groups and hands the totals to the first
 // group's threads: put(column, values).  Uniform over the CTA.
-template <typename Pc, int ITEMS, int VEC, typename F>
+template <typename Pc, int ITEMS, typename F>
 __device__ __forceinline__ void flush(typename Pc::P (&acc)[ITEMS][Pc::E], int tpr, int rg,
                                       int group, int lane, int D, typename Pc::P *buf, F put) {
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int c = (lane + i * tpr) * VEC;
+    const int c = (lane + i * tpr) * Pc::kStep;
     if (rg > 1) {
       __syncthreads();
 #pragma unroll
@@ -54,9 +54,8 @@ template <typename T, int VEC, int ITEMS, int GATE, int BS, int NS>
 __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   using Pc = Piece<T, VEC>;
   using P = typename Pc::P;
-  using Raw = typename Pc::Raw;
-  constexpr int E = Pc::E, kOut = 1, kX = 2, kRes = 3, kGate = GATE == kGateEach ? 4 : 0;
-  constexpr bool kKeep = ITEMS * VEC <= 8;      // these stay in registers between the passes
+  constexpr int E = Pc::E, W = Pc::kStep, kOut = 1, kX = 2, kRes = 3, kGate = GATE == kGateEach ? 4 : 0;
+  constexpr bool kKeep = ITEMS * W <= 8;      // these stay in registers between the passes
   constexpr int KI = kKeep ? ITEMS : 1;
   using In = Stage<T, VEC, ITEMS, GATE == kGateEach ? 5 : 4, BS, NS>;
   constexpr int kAhead = NS > 0 ? NS - 1 : 0;
@@ -66,7 +65,7 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   const int tid = threadIdx.x, tpr = p.tpr, rg = p.rg;
   const int group = tid / tpr, lane = tid - group * tpr;
   P *buf = reinterpret_cast<P *>(smem + q.staged);         // for flush, when rg > 1
-  const int step = tpr * VEC * (int)sizeof(T);             // bytes between a thread's pieces
+  const int step = tpr * W * (int)sizeof(T);             // bytes between a thread's pieces
   const long long row_bytes = (long long)p.D * sizeof(T);
   In in;
   in.lane = lane;
@@ -78,9 +77,12 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   in.src[kX] = (const char *)q.d_x;
   in.src[kRes] = (const char *)p.res;
   if constexpr (GATE == kGateEach) in.src[kGate] = (const char *)p.gate;
-  bool has[ITEMS];
+  bool has[ITEMS], whole[ITEMS];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) has[i] = (lane + i * tpr) * VEC < p.D;
+  for (int i = 0; i < ITEMS; ++i) {
+    has[i] = (lane + i * tpr) * W < p.D;
+    whole[i] = !Pc::kRagged || (lane + i * tpr) * W + W <= p.D;
+  }
   int slot = 0;
 
   P dw1[ITEMS][E], dw2[ITEMS][E], w1k[KI][E], w2k[KI][E];
@@ -91,12 +93,12 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   const P scale = both<P>(p.scale);
   // scale * w_post and w_pre of a piece
   auto weights = [&](int i, P(&w1)[E], P(&w2)[E]) {
-    const int c = (lane + i * tpr) * VEC;
+    const int c = (lane + i * tpr) * W;
 #pragma unroll
     for (int e = 0; e < E; ++e) w1[e] = w2[e] = both<P>(0.f);
     if (c < p.D) {
-      Pc::weight(p.w_post + c, w1);
-      if (p.w_pre) Pc::weight(p.w_pre + c, w2);
+      Pc::weight(p.w_post + c, w1, whole[i]);
+      if (p.w_pre) Pc::weight(p.w_pre + c, w2, whole[i]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) w1[e] = mul(w1[e], scale);
@@ -133,18 +135,18 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
     if (GATE == kGateGroup) {
 #pragma unroll
       for (int i = 0; i < GI; ++i) {
-        const int c = (lane + i * tpr) * VEC;
+        const int c = (lane + i * tpr) * W;
 #pragma unroll
         for (int e = 0; e < E; ++e) es[i][e] = ga[i][e] = both<P>(0.f);
         if (c < p.D) {
           P d[E];
-          Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), ga[i]);
+          Pc::get(Pc::read((const T *)p.gate + (size_t)g * p.D + c, whole[i]), ga[i]);
           gate_values<false>(p.act, ga[i], d);
         }
       }
     }
     int st = 0;
-    long long at = (lo + group) * row_bytes + (long long)lane * VEC * sizeof(T);
+    long long at = (lo + group) * row_bytes + (long long)lane * W * sizeof(T);
     const long long advance = rg * row_bytes;
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
@@ -163,21 +165,21 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
       // n1, m, v, d_x, act(gate) and its derivative of a piece
       auto front = [&](int i, const P(&w1)[E], const P(&w2)[E], P(&n1)[E], P(&m)[E], P(&v)[E],
                        P(&gx)[E], P(&a)[E], P(&da)[E], P(&qv)[E]) {
-        Pc::get(in.get(st, 0, i, row, at, step), n1);
-        if (q.d_out) Pc::get(in.get(st, kOut, i, row, at, step), v);
+        Pc::get(in.get(st, 0, i, whole[i], row, at, step), n1);
+        if (q.d_out) Pc::get(in.get(st, kOut, i, whole[i], row, at, step), v);
         else
 #pragma unroll
           for (int e = 0; e < E; ++e) v[e] = both<P>(0.f);
-        if (q.d_x) Pc::get(in.get(st, kX, i, row, at, step), gx);
+        if (q.d_x) Pc::get(in.get(st, kX, i, whole[i], row, at, step), gx);
         else
 #pragma unroll
           for (int e = 0; e < E; ++e) gx[e] = both<P>(0.f);
-        if (p.res) Pc::get(in.get(st, kRes, i, row, at, step), m);
+        if (p.res) Pc::get(in.get(st, kRes, i, whole[i], row, at, step), m);
         else
 #pragma unroll
           for (int e = 0; e < E; ++e) m[e] = both<P>(0.f);
         if (GATE == kGateEach) {
-          Pc::get(in.get(st, kGate, i, row, at, step), a);
+          Pc::get(in.get(st, kGate, i, whole[i], row, at, step), a);
           gate_values<true>(p.act, a, da);
         }
 #pragma unroll
@@ -242,10 +244,10 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
             }
             oy[e] = fma(mul(aw, v[k][e]), ps1, mul(n1[k][e], nc));
           }
-          *reinterpret_cast<Raw *>((char *)q.dy + o) = Pc::put(oy);
-          if (q.d_res) *reinterpret_cast<Raw *>((char *)q.d_res + o) = Pc::put(v[k]);
+          Pc::write((char *)q.dy + o, oy, whole[i]);
+          if (q.d_res) Pc::write((char *)q.d_res + o, v[k], whole[i]);
           if (GATE == kGateEach && q.d_gate)
-            *reinterpret_cast<Raw *>((char *)q.d_gate + o) = Pc::put(og);
+            Pc::write((char *)q.d_gate + o, og, whole[i]);
         }
       }
       st = st == kAhead ? 0 : st + 1;
@@ -258,26 +260,26 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
 #pragma unroll
         for (int e = 0; e < E; ++e) dw1[i][e] = fma(ga[i][e], es[i][e], dw1[i][e]);
       if (q.d_gate)
-        flush<Pc, GI, VEC>(es, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
+        flush<Pc, GI>(es, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
           P w1[E], w2[E], a[E], d[E];
           weights(i, w1, w2);
-          Pc::get(*reinterpret_cast<const Raw *>((const T *)p.gate + (size_t)g * p.D + c), a);
+          Pc::get(Pc::read((const T *)p.gate + (size_t)g * p.D + c, whole[i]), a);
           gate_values<true>(p.act, a, d);
 #pragma unroll
           for (int e = 0; e < E; ++e) a[e] = mul(mul(w1[e], d[e]), s[e]);
-          if (q.splits) Pc::store(q.part_gate + (size_t)blockIdx.x * p.D + c, a);
-          else *reinterpret_cast<Raw *>((T *)q.d_gate + (size_t)g * p.D + c) = Pc::put(a);
+          if (q.splits) Pc::store(q.part_gate + (size_t)blockIdx.x * p.D + c, a, whole[i]);
+          else Pc::write((T *)q.d_gate + (size_t)g * p.D + c, a, whole[i]);
         });
     }
   }
-  flush<Pc, ITEMS, VEC>(dw1, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
+  flush<Pc, ITEMS>(dw1, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
 #pragma unroll
     for (int e = 0; e < E; ++e) s[e] = mul(s[e], scale);
-    Pc::store(q.part_post + (size_t)blockIdx.x * p.D + c, s);
+    Pc::store(q.part_post + (size_t)blockIdx.x * p.D + c, s, whole[i]);
   });
   if (p.w_pre)
-    flush<Pc, ITEMS, VEC>(dw2, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
-      Pc::store(q.part_pre + (size_t)blockIdx.x * p.D + c, s);
+    flush<Pc, ITEMS>(dw2, tpr, rg, group, lane, p.D, buf, [&](int i, int c, P(&s)[E]) {
+      Pc::store(q.part_pre + (size_t)blockIdx.x * p.D + c, s, whole[i]);
     });
 }
 
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(1024)
 
 constexpr Built kBuilt[] = {{2, 8, 1, 256}, {2, 8, 1, 512}, {2, 8, 2, 512}, {2, 8, 4, 512},
                             {2, 2, 4, 256}, {2, 2, 4, 512}, {2, 2, 8, 1024},
-                            {2, 1, 8, 256}, {2, 1, 8, 512}, {2, 1, 16, 1024},
+                            {2, 1, 4, 256}, {2, 1, 4, 512}, {2, 1, 8, 1024},
                             {4, 4, 1, 256}, {4, 4, 1, 512}, {4, 4, 2, 512}, {4, 4, 4, 512},
                             {4, 4, 8, 512}, {4, 1, 4, 256}, {4, 1, 4, 512}, {4, 1, 16, 1024}};
 
@@ -339,7 +341,7 @@ cudaError_t launch_g(NormBwdParams q, int units, cudaStream_t stream) {
   auto kern = norm_bwd_kernel<T, VEC, ITEMS, GATE, BS, NS>;
   const int threads = q.f.tpr * q.f.rg;
   q.staged = (int)Stage<T, VEC, ITEMS, GATE == kGateEach ? 5 : 4, BS, NS>::bytes(q.f.D, q.f.rg);
-  const size_t smem = q.staged + (q.f.rg > 1 ? sizeof(float) * threads * VEC : 0);
+  const size_t smem = q.staged + (q.f.rg > 1 ? sizeof(float) * threads * Piece<T, VEC>::kStep : 0);
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<units, threads, smem, stream>>>(q);
@@ -432,9 +434,9 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
         : small      ? launch<B, 2, 4, 256, 3>(q, mode, units, cs)
                      : launch<B, 2, 4, 512, 3>(q, mode, units, cs);
   else if (bf16)
-    e = l.items == 16 ? launch<B, 1, 16, 1024, 0>(q, mode, units, cs)
-        : small       ? launch<B, 1, 8, 256, 2>(q, mode, units, cs)
-                      : launch<B, 1, 8, 512, 2>(q, mode, units, cs);
+    e = l.items == 8 ? launch<B, 1, 8, 1024, 0>(q, mode, units, cs)
+        : small      ? launch<B, 1, 4, 256, 2>(q, mode, units, cs)
+                     : launch<B, 1, 4, 512, 2>(q, mode, units, cs);
   else
     e = l.items == 16 ? launch<float, 1, 16, 1024, 0>(q, mode, units, cs)
         : small       ? launch<float, 1, 4, 256, 3>(q, mode, units, cs)
