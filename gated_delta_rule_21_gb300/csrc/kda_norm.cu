@@ -212,7 +212,7 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
                           (const void *)out, (const void *)x})
     vec = vec && aligned16(ptr);
   static const Built built[] = {{2, 8, 2, 256}, {2, 8, 2, 512}, {2, 8, 4, 512},
-                                {2, 2, 8, 256}, {2, 2, 8, 1024}, {2, 1, 8, 256}, {2, 1, 8, 1024},
+                                {2, 2, 4, 512}, {2, 2, 8, 1024}, {2, 1, 4, 512}, {2, 1, 8, 1024},
                                 {4, 4, 2, 256}, {4, 4, 2, 512}, {4, 4, 4, 512}, {4, 4, 8, 512},
                                 {4, 1, 8, 256}, {4, 1, 8, 512}, {4, 1, 16, 1024}};
   const Layout l = layout_for(built, d->dim, bf16 ? 2 : 4, vec);
@@ -224,7 +224,7 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
   using B = __nv_bfloat16;
   if (l.vec == 8)
     e = l.items == 4   ? launch<B, 8, 4, 512, 0>(p, mode, cs)
-        : l.bs == 256  ? launch<B, 8, 2, 256, 3>(p, mode, cs)
+        : l.bs == 256  ? launch<B, 8, 2, 256, 2>(p, mode, cs)
                        : launch<B, 8, 2, 512, 3>(p, mode, cs);
   else if (l.vec == 4)
     e = l.items == 8   ? launch<float, 4, 8, 512, 0>(p, mode, cs)
@@ -232,9 +232,9 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
         : l.bs == 256  ? launch<float, 4, 2, 256, 3>(p, mode, cs)
                        : launch<float, 4, 2, 512, 3>(p, mode, cs);
   else if (l.vec == 2)
-    e = l.bs == 256 ? launch<B, 2, 8, 256, 3>(p, mode, cs) : launch<B, 2, 8, 1024, 0>(p, mode, cs);
+    e = l.bs == 512 ? launch<B, 2, 4, 512, 2>(p, mode, cs) : launch<B, 2, 8, 1024, 0>(p, mode, cs);
   else if (bf16)
-    e = l.bs == 256 ? launch<B, 1, 8, 256, 2>(p, mode, cs) : launch<B, 1, 8, 1024, 2>(p, mode, cs);
+    e = l.bs == 512 ? launch<B, 1, 4, 512, 2>(p, mode, cs) : launch<B, 1, 8, 1024, 2>(p, mode, cs);
   else
     e = l.items == 16 ? launch<float, 1, 16, 1024, 0>(p, mode, cs)
         : l.bs == 256 ? launch<float, 1, 8, 256, 3>(p, mode, cs)

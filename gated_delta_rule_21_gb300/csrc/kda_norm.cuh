@@ -288,8 +288,12 @@ __device__ __forceinline__ void gate_values(int act, P (&a)[E], P (&d)[E]) {
 // Sums over the tpr threads of a row, in every thread of the row.  `slot`
 // alternates between two buffers, so one barrier is enough.
 __device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[32], int &slot) {
-  const int lim = tpr < 32 ? tpr : 32;
-  for (int off = lim >> 1; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (tpr < 32) {
+    for (int off = tpr >> 1; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   if (tpr > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[slot][warp] = v;
