@@ -555,7 +555,7 @@ struct StateSmem {
 //   i - 1 run, then wait for those, write the S that entered block i - 1 and
 //   update it.
 // A thread holds TP / 4 columns of one state row (its TMEM lane).  (With 256
-// threads, two warps on a scheduler, a block took 3.7 us instead of STATE_US.)
+// threads, two warps on a scheduler, a block took 3.7 us instead of 2.2.)
 // IDS: rows have segment ids (without them every block is plain, and the
 // kernel keeps its registers).
 template <typename T, int TP, bool IDS>
@@ -1045,6 +1045,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
           yx[e] += vx[e];
         }
       }
+      if ((flags & kResets) && ein == 0.f)     // the entering state does not reach the
+#pragma unroll
+        for (int e = 0; e < 16; ++e) yi[e] = 0.f;  // token, whatever it holds
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         u64 x[4], z[4], y[4];

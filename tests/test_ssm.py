@@ -178,3 +178,49 @@ def test_calls_repeat_bit_for_bit_and_run_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(want, held)
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_padding_may_hold_anything(dtype, impl):
+    """NaN and infinities at padding change nothing, bit for bit."""
+    ids = torch.ones(3, 300, dtype=torch.int32)
+    ids[0, 250:] = 0
+    ids[1, :70] = 0
+    ids[1, 200:230] = 0
+    ids[2] = 0
+    clean = Case(3, 300, 2, 64, 64, 1, dtype, ids=ids, init=True)
+    want = clean.gpu(impl)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        c = Case(3, 300, 2, 64, 64, 1, dtype, ids=ids, init=True)
+        c.proj[0][ids == 0] = bad
+        got = c.gpu(impl)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+def test_a_reset_ends_what_came_before(dtype, impl):
+    """A run of NaN leaves the blocks after it untouched."""
+    ids = torch.ones(1, 600, dtype=torch.int32)
+    ids[0, 128:] = 2
+    c = Case(1, 600, 2, 32, 64, 1, dtype, ids=ids)
+    want = c.gpu(impl)
+    c.proj[0][0, :128] = float("nan")
+    got = c.gpu(impl)
+    assert torch.equal(want[0][0, 128:], got[0][0, 128:]) and torch.equal(want[1], got[1])
+
+
+def test_segments_of_the_fp32_kernel_agree_with_one_chain():
+    """Few heads and a long row (many segments) against many rows (one)."""
+    import gated_delta_rule_21_gb300 as kda
+    c = Case(1, 1500, 1, 32, 32, 1, torch.float32, init=True)
+    c.check("simt")
+    assert kda.ssm_workspace_size(1, 1500, 1, 32, 32, 1, torch.float32, "simt") > \
+        kda.ssm_workspace_size(1, 60, 1, 32, 32, 1, torch.float32, "simt")
+
+
+def test_device_status_is_clean():
+    import gated_delta_rule_21_gb300 as kda
+    c = Case(2, 300, 4, 64, 128, 2, torch.bfloat16)
+    ws = kda.alloc_ssm_workspace(*c.dims)
+    c.gpu(workspace=ws)
+    assert kda.read_device_status(ws) == 0
