@@ -57,18 +57,18 @@ __device__ __forceinline__ SsmRow simt_row(const SsmParams &p, int b) {
 constexpr int kThreads = 256, kCols = 32, kTok = 32, kWarps = kThreads / 32;
 
 // How a row is cut for the CUDA-core kernel: `segs` segments of `len` tokens
-// (a multiple of kTok), as many as fill the GPU four times over and no shorter
-// than 64 tokens.  With more than one, a first pass runs every segment but the
-// last from a zero state, the states that enter the segments are chained,
-// and a second pass makes y: the sums a state takes part in grow, but a
-// short row of few heads no longer waits for one chain of tokens (3 rows of
-// 997 tokens, 6 heads: 576 us in one chain).
+// (a multiple of kTok), as many as fill the GPU four times over.  With more
+// than one, a first pass runs every segment but the last from a zero state,
+// the states that enter the segments are chained, and a second pass makes y:
+// twice the work on the states, but a short row of few heads no longer waits
+// for one chain of tokens (3 rows of 997 tokens, 6 heads: 576 us in one chain,
+// 71 us in segments of 64 tokens).
 struct SimtCut {
   int segs, len;
 };
 SimtCut simt_cut(int B, int T, int H, int P) {
   const long long chains = (long long)B * H * (P / kCols), want = (4 * 152 + chains - 1) / chains;
-  const int most = (T + 63) / 64;
+  const int most = (T + kTok - 1) / kTok;
   const int n = (int)(want < most ? want : most);
   SimtCut c;
   c.len = ((T + n - 1) / n + kTok - 1) / kTok * kTok;
@@ -78,9 +78,8 @@ SimtCut simt_cut(int B, int T, int H, int P) {
 
 // One CTA per (segment, row, head, 32 columns), token by token in fp32.  Warp
 // w holds states [w N / 8, (w + 1) N / 8) of column `lane` in registers; 32
-// tokens of B, C and x are made in shared memory at a time, a thread walking
-// one channel's tokens with its window in registers, and the warps' shares
-// of y are added there.  FIRST: the first pass (states and decays only).
+// tokens of B, C and x are made in shared memory at a time, and the warps'
+// shares of y are added there.  FIRST: the first pass (states and decays only).
 template <typename T, int N, bool FIRST>
 __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, const SimtCut cut,
                                                             float *seg_state, float *seg_decay) {
@@ -125,55 +124,60 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
       sa[tid] = expf(d * A);
       smark[tid] = k.place | (k.first ? 4 : 0) | (k.live ? 8 : 0) | (k.reset ? 16 : 0);
     }
-    __syncthreads();
-    for (int j = tid; j < 2 * N + kCols; j += kThreads) {
+    // any token that cuts a window or drops the state?
+    const bool cut_here = __syncthreads_or(tid < n && smark[tid] != (8 | (kSsmTaps - 1)) &&
+                                           smark[tid] != (12 | (kSsmTaps - 1)));
+    // a thread takes a channel and 8 tokens at a time
+    constexpr int kStrip = 8, CH = 2 * N + kCols;
+    for (int i = tid; i < CH * (kTok / kStrip); i += kThreads) {
+      const int j = i % CH, s0 = i / CH * kStrip;
       if (FIRST && j >= N && j < 2 * N) continue;      // C is not needed
       const int c = j < N ? cb + j : j < 2 * N ? cc + j - N : cx + j - 2 * N;
       const float4 w = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)c);
       const float bias = p.bias ? p.bias[c] : 0.f;
-      float win[kSsmTaps - 1];                         // the 3 inputs before, oldest first
+      const T *xc = x + (long long)(t0 + s0) * p.xbc_st + c;
+      float in[kStrip + kSsmTaps - 1];                 // with the 3 inputs before
 #pragma unroll
-      for (int i = 0; i < kSsmTaps - 1; ++i) {
-        const int t = t0 - (kSsmTaps - 1) + i;
-        win[i] = t >= 0 ? to_f32(x[(long long)t * p.xbc_st + c]) : 0.f;
+      for (int k = 0; k < kStrip + kSsmTaps - 1; ++k) {
+        const int t = s0 + k - (kSsmTaps - 1);
+        in[k] = t0 + t >= 0 && t < n
+                    ? to_f32(xc[(long long)(k - (kSsmTaps - 1)) * p.xbc_st]) : 0.f;
       }
-      const T *xc = x + (long long)t0 * p.xbc_st + c;
-#pragma unroll 8
-      for (int t = 0; t < kTok; ++t) {
-        const float xv = t < n ? to_f32(xc[(long long)t * p.xbc_st]) : 0.f;
-        const int mark = smark[t], place = mark & 3;
-        float a[kSsmTaps - 1];
 #pragma unroll
-        for (int age = 1; age < kSsmTaps; ++age) {
-          float v = win[kSsmTaps - 1 - age];
-          if (place < age)
-            v = (mark & 4) && past
-                    ? to_f32(past[(size_t)(kSsmTaps - 1 + place - age) * p.channels + c])
-                    : 0.f;
-          a[kSsmTaps - 1 - age] = v;
+      for (int k = 0; k < kStrip; ++k) {
+        const int t = s0 + k;
+        float a0 = in[k], a1 = in[k + 1], a2 = in[k + 2];
+        const int mark = smark[t];
+        if (cut_here) {
+          const int place = mark & 3;
+          const bool old = (mark & 4) && past;
+          auto cached = [&](int age) {
+            return old ? to_f32(past[(size_t)(kSsmTaps - 1 + place - age) * p.channels + c]) : 0.f;
+          };
+          if (place < 3) a0 = cached(3);
+          if (place < 2) a1 = cached(2);
+          if (place < 1) a2 = cached(1);
         }
-        float u = bias + w.w * xv + w.z * a[2] + w.y * a[1] + w.x * a[0];
+        float u = bias + w.w * in[k + 3] + w.z * a2 + w.y * a1 + w.x * a0;
         u = mark & 8 ? u / (1.f + expf(-u)) : 0.f;
         if (j < N) sB[t * N + j] = u * sd[t];
         else if (j < 2 * N) sC[t * N + j - N] = u;
         else sX[t * kCols + j - 2 * N] = u;
-        win[0] = win[1];
-        win[1] = win[2];
-        win[2] = xv;
       }
     }
     __syncthreads();
-    for (int t = 0; t < n; ++t) {
+    // tokens past the segment's end have d = 0: they leave the state alone
+    auto scan = [&](int t, bool reset) {
       const float a = sa[t], xv = sX[t * kCols + lane];
       const float4 *pb = reinterpret_cast<const float4 *>(sB + t * N + warp * NS),
                    *pc = reinterpret_cast<const float4 *>(sC + t * N + warp * NS);
-      float acc = 0.f;
-      if (smark[t] & 16) {       // a reset drops the state whatever it holds
+      if (reset) {               // drops the state whatever it holds
         decay = 0.f;
 #pragma unroll
         for (int j = 0; j < NS; ++j) s[j] = 0.f;
       }
       if (FIRST) decay *= a;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < NS / 4; ++j) {
         const float4 bv = pb[j];
@@ -183,10 +187,20 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
         s[4 * j + 3] = fmaf(a, s[4 * j + 3], bv.w * xv);
         if (!FIRST) {
           const float4 cv = pc[j];
-          acc += cv.x * s[4 * j] + cv.y * s[4 * j + 1] + cv.z * s[4 * j + 2] + cv.w * s[4 * j + 3];
+          acc.x += cv.x * s[4 * j];
+          acc.y += cv.y * s[4 * j + 1];
+          acc.z += cv.z * s[4 * j + 2];
+          acc.w += cv.w * s[4 * j + 3];
         }
       }
-      if (!FIRST) sY[(warp * kTok + t) * kCols + lane] = acc;
+      if (!FIRST) sY[(warp * kTok + t) * kCols + lane] = (acc.x + acc.y) + (acc.z + acc.w);
+    };
+    if (cut_here) {
+#pragma unroll 1
+      for (int t = 0; t < kTok; ++t) scan(t, (smark[t] & 16) != 0);
+    } else {
+#pragma unroll 4
+      for (int t = 0; t < kTok; ++t) scan(t, false);
     }
     if (FIRST) continue;
     __syncthreads();
@@ -241,11 +255,22 @@ __global__ void __launch_bounds__(256)
   const int bh = (int)(i / per);
   float s = initial ? initial[i] : 0.f;
   seg_state[i] = s;
-  for (int k = 0; k + 1 < segs; ++k) {
-    const float a = seg_decay[(size_t)k * heads + bh];
-    // decay 0 (a reset, or underflow) drops the state whatever it holds
-    s = (a == 0.f ? 0.f : a * s) + seg_state[(size_t)(k + 1) * n + i];
-    seg_state[(size_t)(k + 1) * n + i] = s;
+  constexpr int kBatch = 8;          // loads in flight
+  for (int k0 = 0; k0 + 1 < segs; k0 += kBatch) {
+    float a[kBatch], v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k + 1 < segs) {
+        a[k] = seg_decay[(size_t)(k0 + k) * heads + bh];
+        v[k] = seg_state[(size_t)(k0 + k + 1) * n + i];
+      }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k + 1 < segs) {
+        // decay 0 (a reset, or underflow) drops the state whatever it holds
+        s = (a[k] == 0.f ? 0.f : a[k] * s) + v[k];
+        seg_state[(size_t)(k0 + k + 1) * n + i] = s;
+      }
   }
 }
 

@@ -20,6 +20,8 @@
 // to bf16 at the end, and its products' operands (C, B, x, S and the 128 x 128
 // matrix of factors) are bf16 too; their errors are of y's own rounding's
 // size and average out over the sums.
+#include <math_constants.h>
+
 #include <type_traits>
 
 #include "kda_ssm.cuh"
@@ -315,9 +317,20 @@ constexpr unsigned char kWhole = (kSsmTaps - 1) | 8;
 //   wst  = d 2^(sum of a after the token) where the token reaches the state
 //          that leaves the block, else 0 (summed from the end: exact where
 //          it matters)
-// A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums are made in
-// 64 bits and cum, cumj kept in two floats: a factor e^(c_r - c_j) is as exact
-// as the difference, however far the sums have run.
+// A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums up to a token
+// are made and kept in two floats: a factor e^(c_r - c_j) is as exact as the
+// difference, however far the sums have run.  (64-bit sums took 40 us.)
+struct Two {       // hi + lo, |lo| at most half a step of hi
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
 template <typename T>
 __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t, int b, int blk,
                                              unsigned char *smem) {
@@ -350,7 +363,6 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     t.flags[(size_t)b * t.nb + blk] = (plain ? kPlain : 0) | (resets ? kResets : 0);
   }
   constexpr bool kF32 = sizeof(T) == 4;
-  using R = typename std::conditional<kF32, double, float>::type;
   const T *dt = static_cast<const T *>(p.dt) + (size_t)b * p.dt_sb;
   for (int h0 = 0; h0 < p.H; h0 += 32) {
     const int nh = min(32, p.H - h0);
@@ -365,34 +377,45 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
     }
     __syncthreads();
     for (int hh = warp; hh < nh; hh += kPrep / 32) {
-      const R a2 = (R)p.A[h0 + hh] * (R)1.4426950408889634;
-      float d[4];
-      R a[4], pre[4], suf[4];
+      // A log2(e) in two floats
+      const float A = p.A[h0 + hh], a2 = A * kLog2e;
+      const float a2_lo = fmaf(A, kLog2e, -a2) + A * 1.9259629911266175e-8f;
+      float d[4], suf[4];
+      Two a[4], pre[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         d[i] = sdt[(lane * 4 + i) * 33 + hh];
-        a[i] = d[i] > 0.f ? d[i] * a2 : (R)0;
+        a[i].hi = d[i] > 0.f ? d[i] * a2 : 0.f;
+        a[i].lo = kF32 && d[i] > 0.f ? fmaf(d[i], a2, -a[i].hi) + d[i] * a2_lo : 0.f;
       }
       pre[0] = a[0];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + a[i];
-      suf[3] = 0;
+      for (int i = 1; i < 4; ++i) {
+        if (kF32) pre[i] = add(pre[i - 1], a[i]);
+        else pre[i].hi = pre[i - 1].hi + a[i].hi;
+      }
+      suf[3] = 0.f;
 #pragma unroll
-      for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + a[i + 1];
-      const R sum = pre[3];
-      R before = sum, after = sum;
+      for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + a[i + 1].hi;
+      Two before = pre[3];
+      float after = pre[3].hi;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const R u = __shfl_up_sync(0xffffffffu, before, o);
-        const R v = __shfl_down_sync(0xffffffffu, after, o);
-        if (lane >= o) before += u;
+        Two u = {__shfl_up_sync(0xffffffffu, before.hi, o), 0.f};
+        if (kF32) u.lo = __shfl_up_sync(0xffffffffu, before.lo, o);
+        const float v = __shfl_down_sync(0xffffffffu, after, o);
+        if (lane >= o) {
+          if (kF32) before = add(before, u);
+          else before.hi += u.hi;
+        }
         if (lane + o < 32) after += v;
       }
-      const R total = __shfl_sync(0xffffffffu, before, 31);
-      before = __shfl_up_sync(0xffffffffu, before, 1);
+      const float total = __shfl_sync(0xffffffffu, before.hi, 31);
+      before.hi = __shfl_up_sync(0xffffffffu, before.hi, 1);
+      if (kF32) before.lo = __shfl_up_sync(0xffffffffu, before.lo, 1);
       after = __shfl_down_sync(0xffffffffu, after, 1);
-      if (lane == 0) before = 0;
-      if (lane == 31) after = 0;
+      if (lane == 0) before = {0.f, 0.f};
+      if (lane == 31) after = 0.f;
       const int last = srun[kQ - 1];
       const size_t at = (((size_t)b * p.H + h0 + hh) * t.nb + blk) * kQ;
       float4 wst;
@@ -400,24 +423,27 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int run = srun[lane * 4 + i];
-        const R c = before + pre[i];
         const size_t s = at + slot_of(lane * 4 + i);
-        t.ein[s] = run == 0 ? exp2f((float)c) : 0.f;
-        t.cum[s] = (float)c;
+        const float l = log2f(d[i]);           // d = 0: -inf, a factor of 0
         if constexpr (kF32) {
-          const double j = c - log2((double)d[i]);     // d = 0: +inf, a factor of 0
-          t.cum_lo[s] = (float)(c - (double)(float)c);
-          t.cumj[s] = (float)j;
-          t.cumj_lo[s] = d[i] > 0.f ? (float)(j - (double)(float)j) : 0.f;
+          const Two c = add(before, pre[i]), j = two_sum(c.hi, -l);
+          t.ein[s] = run == 0 ? exp2f(c.hi) : 0.f;
+          t.cum[s] = c.hi;
+          t.cum_lo[s] = c.lo;
+          t.cumj[s] = d[i] > 0.f ? j.hi : CUDART_INF_F;
+          t.cumj_lo[s] = d[i] > 0.f ? j.lo + c.lo : 0.f;
         } else {
-          t.cumj[s] = c - log2f(d[i]);
+          const float c = before.hi + pre[i].hi;
+          t.ein[s] = run == 0 ? exp2f(c) : 0.f;
+          t.cum[s] = c;
+          t.cumj[s] = c - l;
         }
-        fw[i] = run == last ? d[i] * exp2f((float)(suf[i] + after)) : 0.f;
+        fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : 0.f;
       }
       *reinterpret_cast<float4 *>(t.wst + at + lane * 4) = wst;
       if (lane == 0)
         t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] =
-            last == 0 ? exp2f((float)total) : -1.f;
+            last == 0 ? exp2f(total) : -1.f;
     }
   }
 }
