@@ -311,15 +311,6 @@ constexpr unsigned char kWhole = (kSsmTaps - 1) | 8;
 // ---------------------------------------------------------------------------
 // 1. prep
 
-// Per token and head of a block, a = d A log2(e):
-//   cum  = sum of a up to the token            cumj = cum - log2 d
-//   ein  = 2^cum where the entering state reaches the token, else 0
-//   wst  = d 2^(sum of a after the token) where the token reaches the state
-//          that leaves the block, else 0 (summed from the end: exact where
-//          it matters)
-// A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums up to a token
-// are made and kept in two floats: a factor e^(c_r - c_j) is as exact as the
-// difference, however far the sums have run.  (64-bit sums took 40 us.)
 struct Two {       // hi + lo, |lo| at most half a step of hi
   float hi, lo;
 };
@@ -331,6 +322,16 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   const Two s = two_sum(a.hi, b.hi);
   return two_sum(s.hi, s.lo + (a.lo + b.lo));
 }
+
+// Per token and head of a block, a = d A log2(e):
+//   cum  = sum of a up to the token            cumj = cum - log2 d
+//   ein  = 2^cum where the entering state reaches the token, else 0
+//   wst  = d 2^(sum of a after the token) where the token reaches the state
+//          that leaves the block, else 0 (summed from the end: exact where
+//          it matters)
+// A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums up to a token
+// are made and kept in two floats: a factor e^(c_r - c_j) is as exact as the
+// difference, however far the sums have run.  (64-bit sums took 40 us.)
 template <typename T>
 __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t, int b, int blk,
                                              unsigned char *smem) {
@@ -808,9 +809,9 @@ __global__ void __launch_bounds__(kConv + 32, 1)
 // 3. outputs
 
 // Shared memory of ssm_out_kernel: C; B, then the matrix of factors; x; the
-// entering state, then z and y.
-// With fp32 inputs every operand has a second part right after it (C, F at kQ *
-// 128 * 2 bytes, x and S next to each other as PT more columns).
+// entering state; z, then y.  With fp32 inputs every operand has a second part
+// right after it (C, F at kPart bytes, x and S next to each other as PT more
+// columns).
 template <typename T, int PT>
 struct OutSmem {
   static constexpr uint32_t kParts = sizeof(T) == 4 ? 2 : 1;
@@ -819,26 +820,38 @@ struct OutSmem {
   static constexpr uint32_t kF = kC + kParts * kPart;
   static constexpr uint32_t kX = kF + kParts * kPart;
   static constexpr uint32_t kS = kX + kParts * kQ * PT * 2;
-  static constexpr uint32_t kV = kS + kParts * kQ * PT * 2;   // ein, cum, cumj, run: 128 each,
-  static constexpr uint32_t kBar = kV + 6 * kQ * 4;           // and the rest of cum and cumj
-  static constexpr uint32_t kBytes = kBar + 32;
+  static constexpr uint32_t kZ = kS + kParts * kQ * PT * 2;
+  static constexpr uint32_t kCum = kZ + kQ * PT * sizeof(T);        // cumj [128]
+  static constexpr uint32_t kCumLo = kCum + kQ * 4;                 // its rest, fp32 inputs
+  static constexpr uint32_t kRun = kCumLo + (kParts - 1) * kQ * 4;  // runs, one byte each
+  static constexpr uint32_t kBar = kRun + kQ;
+  static constexpr uint32_t kTmem = kBar + 32;
+  static constexpr uint32_t kBytes = kTmem + 16;
 };
+// Two CTAs of bf16 inputs on an SM (1 KB of each is the system's).
+static_assert(2 * (OutSmem<bf16, 64>::kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 
 // A row is a slot, and so is a column of C B^T and of the factors; slot l of a
 // quarter is its token 4 (l % 8) + l / 8.  One CTA per (row, block, group,
-// `heads` of its heads); TMEM holds C B^T of
-// the block, shared by the heads, and the two parts of y of PT columns.  Two
-// CTAs fit an SM and fill each other's waits.
+// `heads` of its heads); TMEM holds C B^T of the block, shared by the heads,
+// and the two parts of y of PT columns.  Two CTAs fit an SM.
+//
+// An item is PT columns of a head.  What it needs is asked for an item ahead,
+// each buffer as soon as its last reader is done: S after C S, x after the
+// epilogue, z after the last y has left, the row's factors into registers.
+// (With S, x and z asked for when they were needed an item took 5 us of a
+// CTA's time; two waves of CTAs on 8192 tokens of 64 heads 151 us.)
 template <typename T, int PT>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     ssm_out_kernel(const SsmParams p, const TcBufs t, int heads) {
   using L = OutSmem<T, PT>;
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kCols = PT * L::kParts;      // TMEM columns of each part of y
+  static_assert(128 + 2 * kCols <= 256, "tensor memory");
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint32_t s_tmem;
   const uint32_t sb = smem_u32(smem);
-  const uint32_t bar_cb = sb + L::kBar, bar_xs = bar_cb + 8, bar_m = bar_cb + 16;
+  const uint32_t bar_cb = sb + L::kBar, bar_x = bar_cb + 8, bar_s = bar_cb + 16,
+                 bar_m = bar_cb + 24;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = warp & 3, half = warp >> 2, r = 32 * quad + lane;
   const int r_token = token_of(lane);       // within the quarter
@@ -852,22 +865,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
   const int h_lo = g * hg + part * heads, h_hi = min(h_lo + heads, (g + 1) * hg);
   const int subs = p.P / PT;
   const int n_items = (h_hi - h_lo) * subs;
-  if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 256);
+  if (warp == 0) tmem_alloc(sb + L::kTmem, 256);
   if (tid == 0) {
     mbar_init(bar_cb, 1);
-    mbar_init(bar_xs, 1);
+    mbar_init(bar_x, 1);
+    mbar_init(bar_s, 1);
     mbar_init(bar_m, 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
-  static_assert(128 + 2 * kCols <= 256, "tensor memory");
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
   const uint32_t t_cb = tmem, t_yi = tmem + 128, t_yx = tmem + 128 + kCols;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   uint32_t n_m = 0;       // commits waited for
-  bool bad = false;
+  bool bad = false;       // a wait ran out
   auto give_up = [&]() {
     bad = true;
     set_status(t.status, KDA_DEVICE_TIMEOUT);
@@ -878,20 +891,23 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     tc_fence_after();
   };
   const uint32_t tile = (uint32_t)(kQ * N * 2);
-  const uint32_t xs_bytes = (uint32_t)(kQ * PT * 2 + N * PT * 2) * L::kParts;
-  auto load_item = [&](int k) {      // thread 0: x and S of item k
-    const int h = h_lo + k / subs, c = k % subs * PT;
-    const size_t at = ((size_t)b * nb + blk) * p.H + h;
-    mbar_expect_tx(bar_xs, xs_bytes);
-    const size_t ox = at * kQ * p.P * 2 + (size_t)c * kQ * 2;
-    const size_t os = at * N * p.P * 2 + (size_t)c * N * 2;
-    bulk_load(sb + L::kX, t.xt + ox, kQ * PT * 2, bar_xs);
-    bulk_load(sb + L::kS, t.st + os, N * PT * 2, bar_xs);
-    if (kF32) {
-      bulk_load(sb + L::kX + kQ * PT * 2, t.xlo + ox, kQ * PT * 2, bar_xs);
-      bulk_load(sb + L::kS + N * PT * 2, t.slo + os, N * PT * 2, bar_xs);
-    }
+  auto x_of = [&](int k) {      // item k's x, in the buffers of x
+    const size_t at = ((size_t)b * nb + blk) * p.H + h_lo + k / subs;
+    return at * kQ * p.P * 2 + (size_t)(k % subs * PT) * kQ * 2;
   };
+  auto load_x = [&](int k) {
+    mbar_expect_tx(bar_x, (uint32_t)(kQ * PT * 2) * L::kParts);
+    bulk_load(sb + L::kX, t.xt + x_of(k), kQ * PT * 2, bar_x);
+    if (kF32) bulk_load(sb + L::kX + kQ * PT * 2, t.xlo + x_of(k), kQ * PT * 2, bar_x);
+  };
+  auto load_s = [&](int k) {
+    const size_t at = ((size_t)b * nb + blk) * p.H + h_lo + k / subs;
+    const size_t os = at * N * p.P * 2 + (size_t)(k % subs * PT) * N * 2;
+    mbar_expect_tx(bar_s, (uint32_t)(N * PT * 2) * L::kParts);
+    bulk_load(sb + L::kS, t.st + os, N * PT * 2, bar_s);
+    if (kF32) bulk_load(sb + L::kS + N * PT * 2, t.slo + os, N * PT * 2, bar_s);
+  };
+  int n_x = 0, n_s = 0;         // thread 0: loads of x and S asked for
   if (tid == 0) {
     const size_t o = (((size_t)b * nb + blk) * p.G + g) * tile;
     mbar_expect_tx(bar_cb, 2 * tile * L::kParts);
@@ -901,12 +917,28 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       bulk_load(sb + L::kC + L::kPart, t.clo + o, tile, bar_cb);
       bulk_load(sb + L::kF + L::kPart, t.blo + o, tile, bar_cb);
     }
-    load_item(0);
+    load_s(n_s++);
+    load_x(n_x++);
   }
   const int flags = t.flags[(size_t)b * nb + blk];
   const int run = t.run[((size_t)b * nb + blk) * kQ + r];
-  int *srun = reinterpret_cast<int *>(smem + L::kV + 3 * kQ * 4);
-  if (half == 0) srun[r] = run;
+  signed char *srun = reinterpret_cast<signed char *>(smem + L::kRun);   // at most 128 resets
+  if (half == 0) srun[r] = (signed char)run;
+  float *scumj = reinterpret_cast<float *>(smem + L::kCum);
+  float *scumj_lo = reinterpret_cast<float *>(smem + L::kCumLo);
+  // the factors of the next item's head: of row r, and of column tid
+  float ein = 0.f, cr = 0.f, cl = 0.f, cj = 0.f, cjl = 0.f;
+  auto factors = [&](int k) {
+    const size_t at = (((size_t)b * p.H + h_lo + k / subs) * nb + blk) * kQ;
+    ein = t.ein[at + r];
+    cr = t.cum[at + r];
+    if (kF32) cl = t.cum_lo[at + r];
+    if (tid < kQ) {
+      cj = t.cumj[at + tid];
+      if (kF32) cjl = t.cumj_lo[at + tid];
+    }
+  };
+  factors(0);
   const Opnd opC = {sb + L::kC, 128, (uint32_t)N * 16};
   const Opnd opC2 = {sb + L::kC + L::kPart, 128, (uint32_t)N * 16};
   if (!mbar_wait(bar_cb, 0)) give_up();
@@ -926,62 +958,54 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
   for (int i = tid; i < (int)(L::kParts * L::kPart / 16); i += 256)
     *reinterpret_cast<uint4 *>(smem + L::kF + i * 16) = make_uint4(0, 0, 0, 0);
 
-  float *sein = reinterpret_cast<float *>(smem + L::kV);
-  float *scum = sein + kQ, *scumj = scum + kQ, *scum_lo = sein + 4 * kQ, *scumj_lo = sein + 5 * kQ;
-  int k = 0;
-  for (; k < n_items; ++k) {
-    const int h = h_lo + k / subs, c = k % subs * PT;
-    if (__syncthreads_or(bad)) break;      // the last item's arrays are read
-    const size_t at = (((size_t)b * p.H + h) * nb + blk) * kQ;
-    if (tid < kQ) {
-      sein[tid] = t.ein[at + tid];
-      scum[tid] = t.cum[at + tid];
-      if (kF32) scum_lo[tid] = t.cum_lo[at + tid];
-    } else {
-      scumj[tid - kQ] = t.cumj[at + tid - kQ];
-      if (kF32) scumj_lo[tid - kQ] = t.cumj_lo[at + tid - kQ];
-    }
-    // into L2 while this item is computed: its rows of z, the next x and S
-    if (p.z && tid >= kQ) {
-      const int tok = tid - kQ;
-      if (t0 + tok < p.T)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            static_cast<const T *>(p.z) + (size_t)b * p.z_sb + (long long)(t0 + tok) * p.z_st +
-            h * p.P + c));
-    }
-    if (tid == 0 && k + 1 < n_items) {
-      const int h1 = h_lo + (k + 1) / subs, c1 = (k + 1) % subs * PT;
-      const size_t at1 = ((size_t)b * nb + blk) * p.H + h1;
-      prefetch_l2(t.xt + at1 * kQ * p.P * 2 + (size_t)c1 * kQ * 2, kQ * PT * 2);
-      prefetch_l2(t.st + at1 * N * p.P * 2 + (size_t)c1 * N * 2, N * PT * 2);
-      if (kF32) {
-        prefetch_l2(t.xlo + at1 * kQ * p.P * 2 + (size_t)c1 * kQ * 2, kQ * PT * 2);
-        prefetch_l2(t.slo + at1 * N * p.P * 2 + (size_t)c1 * N * 2, N * PT * 2);
+  // z and y: 16-byte pieces of a [128][PT] tile, a thread copies piece q0 of
+  // slots s0, s0 + kStep, ..
+  constexpr int kP16 = PT * (int)sizeof(T) / 16, kStep = 256 / kP16, kEl = 16 / (int)sizeof(T);
+  auto piece = [&](int row, int q) {
+    return (uint32_t)(L::kZ + row * kP16 * 16 + ((q ^ (kP16 == 8 ? row & 7 : row >> 1 & 3)) << 4));
+  };
+  const int q0 = tid % kP16, s0 = tid / kP16;
+  for (int k = 0; k < n_items; ++k) {
+    const int h = h_lo + k / subs, c = k % subs * PT, ch = h * p.P + c;
+    if (tid == 0 && !bad) {
+      if (mbar_wait(bar_s, k & 1)) {
+        const Opnd opS = {sb + L::kS, 128, (uint32_t)N * 16};
+        mma_k(t_yi, opC, 0, opS, 1, N / 16, kCols, false);
+        if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, PT, true);
+        mma_commit(bar_m);
+      } else {
+        give_up();
       }
     }
-    if (!mbar_wait(bar_xs, k & 1)) give_up();
-    if (__syncthreads_or(bad)) break;
-    if (tid == 0) {
-      const Opnd opS = {sb + L::kS, 128, (uint32_t)N * 16};
-      mma_k(t_yi, opC, 0, opS, 1, N / 16, kCols, false);
-      if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, PT, true);
-      mma_commit(bar_m);
+    if (c == 0 && tid < kQ) {
+      scumj[tid] = cj;
+      if (kF32) scumj_lo[tid] = cjl;
     }
+    if (__syncthreads_or(bad)) break;         // cumj is there, the last y has left
+    if (p.z) {
+      const T *z = static_cast<const T *>(p.z) + (size_t)b * p.z_sb + (long long)t0 * p.z_st + ch +
+                   q0 * kEl;
+#pragma unroll
+      for (int s = s0; s < kQ; s += kStep) {
+        const int tok = token_of(s);
+        const bool ok = t0 + tok < p.T;
+        cp_async16(sb + piece(s, q0), z + (ok ? (long long)tok * p.z_st : 0), ok);
+      }
+      cp_async_commit();
+    }
+    const float ein_now = ein;
     if (c == 0) {
       // factors of the head: row r, 16 columns at a time, up to the diagonal
-      const float cr = scum[r];
-      const u64 cr2 = pk2(cr, cr), neg = pk2(-1.f, -1.f);
-      const float cl = kF32 ? scum_lo[r] : 0.f;
-      const u64 cl2 = pk2(cl, cl);
+      const u64 cr2 = pk2(cr, cr), cl2 = pk2(cl, cl), neg = pk2(-1.f, -1.f);
 #pragma unroll 1
       for (int q = half; q < 2 * quad + 2; q += 2) {
         float v[16];
         tmem_ld16(t_cb + lanes + 16 * q, v);
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const ulonglong2 cj = *reinterpret_cast<const ulonglong2 *>(scumj + 16 * q + e);
+          const ulonglong2 j = *reinterpret_cast<const ulonglong2 *>(scumj + 16 * q + e);
           float f[4];
-          u64 d0 = fma2(cj.x, neg, cr2), d1 = fma2(cj.y, neg, cr2);
+          u64 d0 = fma2(j.x, neg, cr2), d1 = fma2(j.y, neg, cr2);
           if (kF32) {
             const ulonglong2 jl = *reinterpret_cast<const ulonglong2 *>(scumj_lo + 16 * q + e);
             d0 = add2(d0, fma2(jl.x, neg, cl2));
@@ -1003,7 +1027,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
         if (flags & kResets) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (srun[16 * q + e] != run) v[e] = 0.f;
+            if (srun[16 * q + e] != (signed char)run) v[e] = 0.f;
         }
         unsigned char *f = smem + L::kF + (r & 7) * 16 + (r >> 3) * 2048 + 2 * q * 128;
 #pragma unroll
@@ -1021,42 +1045,35 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       }
       fence_proxy_async();
     }
-    wait_mma();                    // C S is done: its tile makes room for z
+    if (k + 1 < n_items) factors(k + 1);
+    wait_mma();                    // C S is done
     tc_fence_before();
     if (__syncthreads_or(bad)) break;
     if (tid == 0) {
-      const Opnd opF = {sb + L::kF, 128, kQ * 16}, opX = {sb + L::kX, 128, kQ * 16};
-      mma_k(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
-      if (kF32) {
-        const Opnd opF2 = {sb + L::kF + L::kPart, 128, kQ * 16};
-        mma_k(t_yx, opF2, 0, opX, 1, kQ / 16, PT, true);
+      if (k + 1 < n_items) load_s(n_s++);
+      if (mbar_wait(bar_x, k & 1)) {
+        const Opnd opF = {sb + L::kF, 128, kQ * 16}, opX = {sb + L::kX, 128, kQ * 16};
+        mma_k(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
+        if (kF32) {
+          const Opnd opF2 = {sb + L::kF + L::kPart, 128, kQ * 16};
+          mma_k(t_yx, opF2, 0, opX, 1, kQ / 16, PT, true);
+        }
+        mma_commit(bar_m);
+        if (k + 1 < n_items) {
+          prefetch_l2(t.xt + x_of(k + 1), kQ * PT * 2);
+          if (kF32) prefetch_l2(t.xlo + x_of(k + 1), kQ * PT * 2);
+        }
+      } else {
+        give_up();
       }
-      mma_commit(bar_m);
-    }
-    const int ch = h * p.P + c;
-    constexpr int kP16 = PT * (int)sizeof(T) / 16, kStep = 256 / kP16, kEl = 16 / (int)sizeof(T);
-    auto piece = [&](int row, int q) {   // 16-byte piece of the [128][PT] tile of z and y
-      return (uint32_t)(L::kS + row * kP16 * 16 + ((q ^ (kP16 == 8 ? row & 7 : row >> 1 & 3)) << 4));
-    };
-    // a thread copies piece q0 of slots s0, s0 + kStep, ..
-    const int q0 = tid % kP16, s0 = tid / kP16;
-    if (p.z) {
-      const T *z = static_cast<const T *>(p.z) + (size_t)b * p.z_sb + (long long)t0 * p.z_st + ch +
-                   q0 * kEl;
-#pragma unroll
-      for (int s = s0; s < kQ; s += kStep) {
-        const int tok = token_of(s);
-        const bool ok = t0 + tok < p.T;
-        cp_async16(sb + piece(s, q0), z + (ok ? (long long)tok * p.z_st : 0), ok);
-      }
-      cp_async_commit();
     }
     wait_mma();
+    if (!mbar_wait(bar_x, k & 1)) give_up();      // (x is there: it is read below)
     cp_async_wait_all();
-    __syncthreads();
+    if (__syncthreads_or(bad)) break;
     // y of row r, columns [half PT / 2, (half + 1) PT / 2)
-    const float ein = sein[r], D = p.D ? p.D[h] : 0.f;
-    const u64 ein2 = pk2(ein, ein), D2 = pk2(D, D);
+    const float D = p.D ? p.D[h] : 0.f;
+    const u64 ein2 = pk2(ein_now, ein_now), D2 = pk2(D, D);
 #pragma unroll
     for (int e0 = 0; e0 < PT / 2; e0 += 16) {
       const int col = half * (PT / 2) + e0;
@@ -1071,7 +1088,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
           yx[e] += vx[e];
         }
       }
-      if ((flags & kResets) && ein == 0.f)     // the entering state does not reach the
+      if ((flags & kResets) && ein_now == 0.f)     // the entering state does not reach the
 #pragma unroll
         for (int e = 0; e < 16; ++e) yi[e] = 0.f;  // token, whatever it holds
 #pragma unroll
@@ -1090,8 +1107,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
         if (p.z) {
           if constexpr (kF32) {
             const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(zp),
-                             c = *reinterpret_cast<const ulonglong2 *>(zp2);
-            z[0] = a.x; z[1] = a.y; z[2] = c.x; z[3] = c.y;
+                             d = *reinterpret_cast<const ulonglong2 *>(zp2);
+            z[0] = a.x; z[1] = a.y; z[2] = d.x; z[3] = d.y;
           } else {
             Unpack8::unpack(*reinterpret_cast<const uint4 *>(zp), z);
           }
@@ -1101,9 +1118,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
           const int i = 8 * q + 2 * e;
           y[e] = fma2(D2, x[e], fma2(ein2, pk2(yi[i], yi[i + 1]), pk2(yx[i], yx[i + 1])));
           if (p.z) {
-            float a, c, d0, d1;
-            upk2(mul2(z[e], pk2(-kLog2e, -kLog2e)), a, c);
-            upk2(add2(pk2(1.f, 1.f), pk2(ex2(a), ex2(c))), d0, d1);
+            float a, d, d0, d1;
+            upk2(mul2(z[e], pk2(-kLog2e, -kLog2e)), a, d);
+            upk2(add2(pk2(1.f, 1.f), pk2(ex2(a), ex2(d))), d0, d1);
             y[e] = mul2(mul2(y[e], z[e]), pk2(rcp(d0), rcp(d1)));
           }
           if (run < 0) y[e] = 0;
@@ -1117,7 +1134,12 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       }
     }
     tc_fence_before();
-    __syncthreads();
+    fence_proxy_async();
+    __syncthreads();               // x is read, y is whole
+    if (tid == 0) {
+      tc_fence_after();
+      if (k + 1 < n_items) load_x(n_x++);
+    }
     T *y = static_cast<T *>(p.y) + ((size_t)b * p.T + t0) * p.H * p.P + ch + q0 * kEl;
 #pragma unroll
     for (int s = s0; s < kQ; s += kStep) {
@@ -1126,14 +1148,13 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
         *reinterpret_cast<uint4 *>(y + (size_t)tok * p.H * p.P) =
             *reinterpret_cast<const uint4 *>(smem + piece(s, q0));
     }
-    fence_proxy_async();
-    __syncthreads();
-    if (tid == 0 && k + 1 < n_items) load_item(k + 1);
   }
-  // After a wait that ran out: nothing is in flight when the CTA leaves.
-  if (k < n_items) {
-    mbar_wait(bar_cb, 0);
-    mbar_wait(bar_xs, k & 1);
+  if (__syncthreads_or(bad)) {     // nothing is in flight when the CTA leaves
+    if (tid == 0) {
+      mbar_wait(bar_cb, 0);
+      mbar_wait(bar_x, (n_x - 1) & 1);
+      mbar_wait(bar_s, (n_s - 1) & 1);
+    }
     mbar_wait(bar_m, (n_m - 1) & 1);
     cp_async_wait_all();
   }
