@@ -62,7 +62,7 @@ constexpr int kThreads = 256, kCols = 32, kTok = 32, kWarps = kThreads / 32;
 // the states that enter the segments are chained, and a second pass makes y:
 // twice the work on the states, but a short row of few heads no longer waits
 // for one chain of tokens (3 rows of 997 tokens, 6 heads: 576 us in one chain,
-// 71 us in segments of 64 tokens).
+// 42 us in segments of 32 tokens).
 struct SimtCut {
   int segs, len;
 };
@@ -313,12 +313,17 @@ size_t simt_bytes(const kda_ssm_shape *s) {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// AUTO: bf16 on the tensor cores.  fp32 there too from a size on that the CUDA
-// cores take longer for; below it they are as fast and round less.
+// AUTO: the tensor cores (fp32, one row of 8192 tokens, 32 heads of 128: 0.37 ms
+// against 3.1; 3 rows of 997 tokens, 6 heads of 32: 38 us against 42), but for
+// long rows of few heads, whose chain of blocks no other CTA hides (bf16, one row
+// of 8192 tokens, N = 64: 1 head of 32 122 us against 47 on the CUDA cores, 8
+// heads 130 against 111, 18 heads 144 against 206; 4 heads of 1024 tokens 28
+// against 26, of 700 24 against 25; N = 128, 2000 tokens 44 against 44), and for
+// fp32 rows of one segment (64 heads of 64, N = 128: 32 tokens 30 us against 18).
 bool use_tc(const kda_ssm_shape *s, kda_impl impl) {
   if (impl != KDA_IMPL_AUTO) return impl == KDA_IMPL_TC;
-  if (s->dtype == KDA_DTYPE_BF16) return true;
-  return (long long)s->B * s->T * s->H * s->P >= (1ll << 21);
+  if (s->dtype == KDA_DTYPE_F32 && s->T <= kTok) return false;
+  return s->T < 16 * s->N || (long long)s->B * s->H * s->P * s->N > (1ll << 14);
 }
 
 size_t rows_bytes(int B) { return align_up(sizeof(WsHeader) + sizeof(SsmRow) * (size_t)B, 256); }

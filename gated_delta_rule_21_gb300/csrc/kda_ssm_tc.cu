@@ -1,5 +1,5 @@
 // kda_ssm_tc.cu -- the selective state space operator on prompts, on the
-// tensor cores (tcgen05): bf16 activations, every N, P in {32, 64, 128}.
+// tensor cores (tcgen05): bf16 or fp32 activations, N, P in {32, 64, 128}.
 //
 // In blocks of 128 tokens, with c_r the sum of d A over a block's tokens up to
 // r and S the state that enters the block,
@@ -14,12 +14,21 @@
 //   3. ssm_out_kernel: y of every (block, head), all in parallel.
 //
 // Rounding.  The final state is carried to tokens and on, so S' is formed to
-// fp32 grade: B and the scaled x are each split into two bf16 parts, three
-// of the four products are kept (the dropped one is below 2^-16 of a term)
-// and S is updated in fp32 registers, never in the accumulator.  y is rounded
-// to bf16 at the end, and its products' operands (C, B, x, S and the 128 x 128
-// matrix of factors) are bf16 too; their errors are of y's own rounding's
-// size and average out over the sums.
+// fp32 grade: B and the scaled x are each split into two bf16 parts (16 bits of
+// each), all four products are added and S is updated in fp32 registers, never
+// in the accumulator: 3.4e-6 of the state's norm off, either type.  With bf16
+// inputs y is rounded to bf16 at the end and its products' operands (C, B, x, S
+// and the 128 x 128 matrix of factors) are bf16 too; their errors are of y's own
+// rounding's size and average out over the sums (2.6e-3 in all; y's own rounding
+// alone is 1.7e-3).  With fp32 inputs these operands are split in two as well,
+// and three of the four products added (3.2e-6).
+//
+// What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 62 us,
+// state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
+// segments: 12, 125 and 74 us.  The state kernel is a chain of 64 blocks on 128
+// SMs, each its convolution's instructions and two barriers long; the other two
+// are at the rate of their instructions and of exp2 and reciprocals.  (The
+// first kernels of this form took 9.8 and 9.5 ms on the CUDA cores.)
 #include <math_constants.h>
 
 #include <type_traits>
@@ -1197,7 +1206,8 @@ cudaError_t launch_out(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
   const cudaError_t e = cudaFuncSetAttribute(ssm_out_kernel<T, PT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // heads per CTA: up to 4, as long as the CTAs fill the GPU twice over
+  // heads per CTA: up to 4, as long as the CTAs fill the GPU twice over (8 and
+  // 16 take as long: 140 us for 2 rows of 8192 tokens of 64 heads)
   const int hg = p.H / p.G;
   int heads = 4;
   auto ctas = [&](int n) { return (long long)p.B * t.nb * p.G * ((hg + n - 1) / n); };
@@ -1225,8 +1235,9 @@ cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaSt
   }
   e = p.N == 32 ? launch_prep<bf16, 32>(p, t, cs) : launch_prep<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;
-  // 64-column tiles halve the traffic of B's tiles; 32 where they would
-  // leave SMs without a CTA
+  // 64-column tiles halve the traffic of B's tiles (2 rows of 64 heads of 64
+  // columns: 141 us, 32 columns 246); 32 where half the SMs would have no CTA
+  // (a packed row of 32 heads of 128 columns: 125 us, 64 columns 156)
   const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
   e = narrow ? launch_state<bf16, 32>(p, t, cs) : launch_state<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;

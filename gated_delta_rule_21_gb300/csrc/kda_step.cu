@@ -17,7 +17,12 @@
 // segments.  While a unit is computed, the next one's state is on its way
 // to shared memory (each thread copies its own pieces, so no barrier guards
 // them) and its inputs to registers: without that the two barriers of a unit
-// left the memory idle (kda 119 us, ssm 112 us).
+// left the memory idle (119 and 112 us for the sizes below).
+//
+// Measured: ssm_step, 128 sequences of 64 heads, 128 x 64 states (537 MB of
+// states read and written): 90 us, 88 % of the copy bandwidth; kda_step, 120
+// sequences of 32 heads, 128 x 128 (503 MB): 93 us, 80 %; what is left there is
+// the two sums of a unit, which have to end before its first store.
 //
 // The short convolution's cache [3][channels] is moved on in place.  The
 // channels of B and C (of q and k) are read by several CTAs, so the last CTA
@@ -481,11 +486,13 @@ __global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepPara
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Columns per unit: 32 while that leaves no more than two units for each SM,
-// else up to 64 (a tile of 32 KB at 128 keys).
+// Columns per unit: 32 while that leaves no more than one unit for each SM (one
+// sequence of 32 heads of 128: 3.3 and 3.5 us, with 64 columns 3.5 and 3.7), else
+// up to 64, a tile of 32 KB at 128 keys (4 sequences: 4.6 and 5.1 us, with 32
+// columns 5.7 and 6.4; the sizes above 102 and 129 us with 32).
 int tile_for(int B, int H, int cols, int sms) {
   const long long small = (long long)B * H * (cols / 32);
-  return small <= 2ll * sms || cols == 32 ? 32 : 64;
+  return small <= sms || cols == 32 ? 32 : 64;
 }
 
 // Three CTAs fit an SM (registers, and two staged tiles each).

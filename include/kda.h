@@ -531,8 +531,9 @@ typedef struct kda_ssm_shape {
  * conv_out (NULL: not wanted) after the row's last token that is not
  * padding, for kda_ssm_step to go on from; a row without one passes its
  * states on.  conv_out must not be conv_state's buffer.
- *   impl          KDA_IMPL_SIMT: fp32 CUDA cores, every shape; KDA_IMPL_TC: the
- *                 tensor cores, bf16; KDA_IMPL_AUTO: TC for bf16, else SIMT.
+ *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores; KDA_IMPL_TC: the tensor
+ *                 cores; both serve every shape and type.  KDA_IMPL_AUTO: TC, or
+ *                 SIMT for long rows of few heads and fp32 rows of up to 32 tokens.
  *   workspace     device, kda_ssm_fwd_workspace_size bytes, 256-byte aligned,
  *                 its first 256 bytes zero-filled before its first use (the
  *                 device status word, see kda_read_device_status).

@@ -80,7 +80,7 @@ def test_ssm_step(B, H, P, N, G, dtype, slim):
     assert int(ws.sum()) == 0      # the counters are left as they were found
 
 
-KDA = [(1, 1, 32, 32), (3, 4, 64, 128), (2, 6, 128, 64), (40, 8, 128, 128), (160, 2, 32, 64),
+KDA = [(1, 1, 32, 32), (3, 4, 64, 128), (2, 6, 128, 64), (40, 7, 128, 128), (160, 2, 32, 64),
        (1, 32, 128, 128), (5, 3, 64, 32)]
 
 
