@@ -31,6 +31,35 @@ struct WsHeader {
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
+// A kernel launched by launch_next may start once every CTA of the kernel before
+// it in the stream has called start_next (or left): its CTAs take the room that
+// is free and prepare what does not depend on that kernel, until after_previous
+// returns, when the kernel before has ended and what it wrote is visible.  Every
+// CTA calls after_previous, so "ended" covers the kernels before that one too.
+// A kernel that allocates tensor memory calls start_next after that: the next
+// kernel's CTAs, which hold theirs until this one ends, must not come first.
+__device__ __forceinline__ void start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem,
+                        cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, static_cast<P>(args)...);
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 inline size_t ws_row_offsets_bytes(int B) {

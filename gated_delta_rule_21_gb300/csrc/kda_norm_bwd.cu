@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
   const NormParams &p = q.f;
   const int tid = threadIdx.x, tpr = p.tpr, rg = p.rg;
   const int group = tid / tpr, lane = tid - group * tpr;
+  start_next();          // norm_sum_kernel
   P *buf = reinterpret_cast<P *>(smem + q.staged);         // for flush, when rg > 1
   const int step = tpr * W * (int)sizeof(T);             // bytes between a thread's pieces
   const long long row_bytes = (long long)p.D * sizeof(T);
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(1024)
     norm_sum_kernel(const float *part_post, const float *part_pre, const float *part_gate,
                     float *dw_post, float *dw_pre, T *d_gate, int units, int splits, int D) {
   __shared__ float s[32][33];
+  after_previous();
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   const int what = blockIdx.y;
   if (what == 1 && !part_pre) return;
@@ -445,13 +447,11 @@ kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, const float
   const bool gate_parts = mode == kGateGroup && q.splits && d_gate;
   const dim3 grid((d->dim + 31) / 32, 2 + (gate_parts ? (unsigned)d->gate_rows : 0));
   const float *pre = w_pre ? q.part_pre : nullptr;
-  if (bf16)
-    norm_sum_kernel<B><<<grid, 1024, 0, cs>>>(q.part_post, pre, q.part_gate, dw_post, dw_pre,
-                                              (B *)d_gate, units, q.splits, d->dim);
-  else
-    norm_sum_kernel<float><<<grid, 1024, 0, cs>>>(q.part_post, pre, q.part_gate, dw_post, dw_pre,
-                                                  (float *)d_gate, units, q.splits, d->dim);
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  e = bf16 ? launch_next(norm_sum_kernel<B>, grid, 1024, 0, cs, q.part_post, pre, q.part_gate,
+                         dw_post, dw_pre, (B *)d_gate, units, q.splits, d->dim)
+           : launch_next(norm_sum_kernel<float>, grid, 1024, 0, cs, q.part_post, pre, q.part_gate,
+                         dw_post, dw_pre, (float *)d_gate, units, q.splits, d->dim);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -26,6 +26,7 @@ __device__ __forceinline__ int block_min(int v, int *red) {
 __global__ void __launch_bounds__(1024) ssm_rows_kernel(const SsmParams p) {
   __shared__ int red[32];
   const int b = blockIdx.x;
+  start_next();
   const int32_t *ids = p.segment_ids + (size_t)b * p.T;
   SsmRow row = {0, p.T, p.T - 1, 0};
   int f = p.T, l = p.T;   // l: T - 1 - last
@@ -93,6 +94,7 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
   const int seg = blockIdx.x / tiles / (p.B * p.H);
   const int h = bh % p.H, b = bh / p.H, c0 = tile * kCols, g = h / (p.H / p.G);
   const int32_t *ids = p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr;
+  if (FIRST) start_next();
   const SsmRow row = simt_row(p, b);
   const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb;
   const T *past = p.conv_state
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
                        : p.initial_state ? p.initial_state + (size_t)bh * per : nullptr;
   float s[NS], decay = 1.f;
 #pragma unroll
-  for (int j = 0; j < NS; ++j) s[j] = !FIRST && enter ? enter[mine + (size_t)j * p.P] : 0.f;
+  for (int j = 0; j < NS; ++j) s[j] = 0.f;
   const int end = min(p.T, (seg + 1) * cut.len);
   for (int t0 = seg * cut.len; t0 < end; t0 += kTok) {
     const int n = min(kTok, end - t0);
@@ -166,6 +168,12 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
       }
     }
     __syncthreads();
+    if (!FIRST && t0 == seg * cut.len) {
+      after_previous();          // the states of the segments
+      if (enter)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) s[j] = enter[mine + (size_t)j * p.P];
+    }
     // tokens past the segment's end have d = 0: they leave the state alone
     auto scan = [&](int t, bool reset) {
       const float a = sa[t], xv = sX[t * kCols + lane];
@@ -250,6 +258,8 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
 __global__ void __launch_bounds__(256)
     ssm_simt_chain_kernel(const float *initial, float *seg_state, const float *seg_decay, int segs,
                           int heads, size_t per) {
+  start_next();
+  after_previous();
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, n = (size_t)heads * per;
   if (i >= n) return;
   const int bh = (int)(i / per);
@@ -291,8 +301,13 @@ cudaError_t launch_simt(const SsmParams &p, cudaStream_t cs) {
     ssm_simt_kernel<T, N, true>
         <<<chains * (cut.segs - 1), kThreads, smem, cs>>>(p, cut, state, decay);
     const size_t per = (size_t)N * p.P, n = (size_t)p.B * p.H * per;
-    ssm_simt_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, cs>>>(
-        p.initial_state, state, decay, cut.segs, p.B * p.H, per);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+      e = launch_next(ssm_simt_chain_kernel, (unsigned)((n + 255) / 256), 256, 0, cs,
+                      p.initial_state, state, decay, cut.segs, p.B * p.H, per);
+    return e != cudaSuccess ? e
+                            : launch_next(ssm_simt_kernel<T, N, false>, chains * cut.segs,
+                                          kThreads, smem, cs, p, cut, state, decay);
   }
   ssm_simt_kernel<T, N, false><<<chains * cut.segs, kThreads, smem, cs>>>(p, cut, state, decay);
   return cudaGetLastError();

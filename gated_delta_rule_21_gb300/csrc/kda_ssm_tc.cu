@@ -533,6 +533,8 @@ __device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) 
 template <typename T, int TP>
 __global__ void __launch_bounds__(kPrep, 2) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
   extern __shared__ __align__(128) unsigned char smem[];
+  start_next();
+  after_previous();      // the row table
   int u = blockIdx.x;
   if (u < p.B * t.nb) {
     prep_factors<T>(p, t, u / t.nb, u % t.nb, smem);
@@ -623,9 +625,11 @@ __global__ void __launch_bounds__(kConv + 32, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
+  start_next();
 
   if (warp == kConv / 32) {
     if (lane == 0) {
+      after_previous();
       const uint32_t tb = (uint32_t)(kQ * N * 2);
       auto load = [&](int i) {
         const size_t o = (((size_t)b * nb + i) * p.G + g) * tb;
@@ -667,7 +671,6 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     }
     __syncwarp();
   } else {
-    const int first = IDS ? p.rows[b].first : 0;
     const T *past = past_of<T>(p, b);
     const int ch = h * p.P + c0;
     const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
@@ -689,6 +692,8 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         *reinterpret_cast<float4 *>(s + i) =
             *reinterpret_cast<const float4 *>(p.initial_state + state + i);
     }
+    after_previous();
+    const int first = IDS ? p.rows[b].first : 0;
     auto stage = [&](int i) {
       if (i < nb) {
         if (tid < kQ / 4)
@@ -886,6 +891,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
+  after_previous();
   const uint32_t t_cb = tmem, t_yi = tmem + 128, t_yx = tmem + 128 + kCols;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   uint32_t n_m = 0;       // commits waited for
@@ -1180,6 +1186,7 @@ cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
   if (f > smem) smem = f;
   const int caches = p.conv_out ? (p.channels + kPrep - 1) / kPrep : 0;
   const unsigned grid = (unsigned)(p.B * (t.nb * (1 + p.G * (2 * p.N / TP)) + caches));
+  if (p.segment_ids) return launch_next(ssm_prep_kernel<T, TP>, grid, kPrep, smem, cs, p, t);
   ssm_prep_kernel<T, TP><<<grid, kPrep, smem, cs>>>(p, t);
   return cudaGetLastError();
 }
@@ -1191,8 +1198,7 @@ cudaError_t launch_state_i(const SsmParams &p, const TcBufs &t, cudaStream_t cs)
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, smem, cs>>>(p, t);
-  return cudaGetLastError();
+  return launch_next(kern, (unsigned)(p.B * p.H * (p.P / TP)), kConv + 32, smem, cs, p, t);
 }
 template <typename T, int TP>
 cudaError_t launch_state(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
@@ -1212,8 +1218,7 @@ cudaError_t launch_out(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
   int heads = 4;
   auto ctas = [&](int n) { return (long long)p.B * t.nb * p.G * ((hg + n - 1) / n); };
   while (heads > 1 && ctas(heads) < 4ll * num_sms()) heads /= 2;
-  ssm_out_kernel<T, PT><<<(unsigned)ctas(heads), 256, smem, cs>>>(p, t, heads);
-  return cudaGetLastError();
+  return launch_next(ssm_out_kernel<T, PT>, (unsigned)ctas(heads), 256, smem, cs, p, t, heads);
 }
 
 }  // namespace
