@@ -23,7 +23,7 @@
 // alone is 1.7e-3).  With fp32 inputs these operands are split in two as well,
 // and three of the four products added (3.2e-6).
 //
-// What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 62 us,
+// What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 49 us,
 // state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
 // segments: 12, 125 and 74 us.  The state kernel is a chain of 64 blocks on 128
 // SMs, each its convolution's instructions and two barriers long; the other two
@@ -114,6 +114,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool o
                "r"(ok ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -186,19 +189,28 @@ struct Conv {
                                                const T *past, int channels, int t0, int len,
                                                int first, int tid) {
     constexpr int kP16 = kRowBytes / 16, kStep = NT / kP16, kEl = 16 / sizeof(T);
+    static_assert(kStep % 32 == 0, "the rows of a thread are permuted alike");
     const int piece = tid % kP16, row0 = tid / kP16;
     const T *src = x + (long long)(t0 - (kSsmTaps - 1) + row0) * st + piece * kEl;
+    dst += off(row0, piece);
+    if (t0 - (kSsmTaps - 1) >= first && t0 + kQ <= len) {       // every row is there
 #pragma unroll
-    for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k) {
-      const int row = row0 + k * kStep, t = t0 - (kSsmTaps - 1) + row;
-      if (row < kRows) {
-        bool ok = t >= first && t < len;
-        const T *from = ok ? src + (long long)(k * kStep) * st : x;
-        if (t < first && past && t >= first - (kSsmTaps - 1)) {
-          from = past + (size_t)(kSsmTaps - 1 + t - first) * channels + piece * kEl;
-          ok = true;
+      for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k, src += (long long)kStep * st)
+        if ((k + 1) * kStep <= kRows || row0 + k * kStep < kRows)
+          cp_async16(dst + k * kStep * kRowBytes, src);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k, src += (long long)kStep * st) {
+        const int row = row0 + k * kStep, t = t0 - (kSsmTaps - 1) + row;
+        if (row < kRows) {
+          bool ok = t >= first && t < len;
+          const T *from = ok ? src : x;
+          if (t < first && past && t >= first - (kSsmTaps - 1)) {
+            from = past + (size_t)(kSsmTaps - 1 + t - first) * channels + piece * kEl;
+            ok = true;
+          }
+          cp_async16(dst + k * kStep * kRowBytes, from, ok);
         }
-        cp_async16(dst + off(row, piece), from, ok);
       }
     }
     cp_async_commit();
@@ -464,11 +476,12 @@ constexpr int kPrepCh = 8 / (int)sizeof(T);
 template <typename T, int TP>
 using PrepConv = Conv<T, TP, kPrepCh<T>, TP / kPrepCh<T> * 32>;
 
-// The convolution of TP channels of B or C into its operand tiles.
+// The convolution of TP channels of B or C of the blocks [blk, end) into their
+// operand tiles, the next block's rows on their way.
 template <typename T, int TP>
 __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, int b, int blk,
-                                          int g, int part, unsigned char *smem) {
-  const int tid = threadIdx.x, t0 = blk * kQ;
+                                          int end, int g, int part, unsigned char *smem) {
+  const int tid = threadIdx.x;
   const bool is_c = part >= p.N / TP;
   const int n0 = (is_c ? part - p.N / TP : part) * TP;
   const int ch = p.H * p.P + (is_c ? p.G * p.N : 0) + g * p.N + n0;
@@ -479,38 +492,43 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   using Out = Word<2 * kPrepCh<T>>;
   const int warp = tid >> 5, lane = tid & 31, wch = warp * kPrepCh<T>;
   const bool mine = warp < TP / kPrepCh<T>;   // 32 bf16 channels take half the warps
-  Cv cv;
-  if (mine) {
-    Cv::stage(smem_u32(smem), x, p.xbc_st, past ? past + ch : nullptr, p.channels, t0, p.T,
-              row.first, tid);
-    cv.weights(p, ch + wch);
-  }
-  // whether any token's window leaves the staged rows
-  unsigned char *stok = smem + Cv::kBytes;
-  int plain = 1;
-  if (tid < kQ) {
-    const SsmToken k = ssm_token(p.segment_ids ? p.segment_ids + (size_t)b * p.T : nullptr,
-                                 t0 + tid, p.T, row);
-    stok[tid] = token_mark(k);
-    plain = t0 + tid >= p.T || stok[tid] == kWhole;
-  }
-  cp_async_wait_all();
-  plain = __syncthreads_and(plain);
-  if (!mine) return;
-  // the lane's i-th token: row 8 i + lane % 8 of quarter lane / 8
-  const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2 +
-                      (size_t)(lane >> 3) * 4 * p.N * 16 + (lane & 7) * 16 +
-                      (n0 + wch) / 8 * 128 + wch % 8 * 2;
-  unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile, *lo_tile = (is_c ? t.clo : t.blo) + tile;
-  const bool two = !is_c || sizeof(T) == 4;
-  auto put = [&](int i, u64(&u)[Cv::E]) {
-    Out hi, lo;
-    split(u, hi, lo);
-    *reinterpret_cast<Out *>(hi_tile + (size_t)i * p.N * 16) = hi;
-    if (two) *reinterpret_cast<Out *>(lo_tile + (size_t)i * p.N * 16) = lo;
+  auto stage = [&](int i) {
+    if (mine && i < end)
+      Cv::stage(smem_u32(smem) + (i & 1) * Cv::kBytes, x, p.xbc_st, past ? past + ch : nullptr,
+                p.channels, i * kQ, p.T, row.first, tid);
   };
-  if (plain) cv.template run<false>(smem, warp, lane, stok, put);
-  else cv.template run<true>(smem, warp, lane, stok, put);
+  stage(blk);
+  Cv cv;
+  if (mine) cv.weights(p, ch + wch);
+  const bool two = !is_c || sizeof(T) == 4;
+  for (; blk < end; ++blk) {
+    // whether any token's window leaves the staged rows
+    unsigned char *stok = smem + 2 * Cv::kBytes + (blk & 1) * kQ;
+    int plain = 1;
+    if (p.segment_ids && tid < kQ) {
+      const int at = blk * kQ + tid;
+      stok[tid] = token_mark(ssm_token(p.segment_ids + (size_t)b * p.T, at, p.T, row));
+      plain = at >= p.T || stok[tid] == kWhole;
+    }
+    cp_async_wait_all();
+    plain = __syncthreads_and(plain);
+    stage(blk + 1);
+    if (!mine) continue;
+    // the lane's i-th token: row 8 i + lane % 8 of quarter lane / 8
+    const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2 +
+                        (size_t)(lane >> 3) * 4 * p.N * 16 + (lane & 7) * 16 +
+                        (n0 + wch) / 8 * 128 + wch % 8 * 2;
+    unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile, *lo_tile = (is_c ? t.clo : t.blo) + tile;
+    auto put = [&](int i, u64(&u)[Cv::E]) {
+      Out hi, lo;
+      split(u, hi, lo);
+      *reinterpret_cast<Out *>(hi_tile + (size_t)i * p.N * 16) = hi;
+      if (two) *reinterpret_cast<Out *>(lo_tile + (size_t)i * p.N * 16) = lo;
+    };
+    const unsigned char *rows = smem + (blk & 1) * Cv::kBytes;
+    if (plain) cv.template run<false>(rows, warp, lane, stok, put);
+    else cv.template run<true>(rows, warp, lane, stok, put);
+  }
 }
 
 // The inputs that the convolution's cache holds after the row.
@@ -528,10 +546,11 @@ __device__ __forceinline__ void prep_cache(const SsmParams &p, int b, int part) 
     out[(size_t)i * p.channels] = ssm_cached(x, p.xbc_st, past, p.channels, c, i, row.last, k);
 }
 
-// CTAs [0, B nb) make the factors, the next ones a tile of B or C each, the
-// last ones the convolution's cache.
+// CTAs [0, B nb) make the factors, the next ones the tiles of B or C of `run`
+// blocks each, the last ones the convolution's cache.
 template <typename T, int TP>
-__global__ void __launch_bounds__(kPrep, 2) ssm_prep_kernel(const SsmParams p, const TcBufs t) {
+__global__ void __launch_bounds__(kPrep, 2)
+    ssm_prep_kernel(const SsmParams p, const TcBufs t, int run) {
   extern __shared__ __align__(128) unsigned char smem[];
   start_next();
   after_previous();      // the row table
@@ -541,17 +560,17 @@ __global__ void __launch_bounds__(kPrep, 2) ssm_prep_kernel(const SsmParams p, c
     return;
   }
   u -= p.B * t.nb;
-  const int parts = 2 * p.N / TP;
-  const int part = u % parts;
-  u /= parts;
-  const int g = u % p.G;
-  u /= p.G;
-  if (u < p.B * t.nb) {
-    prep_conv<T, TP>(p, t, u / t.nb, u % t.nb, g, part, smem);
+  const int runs = (t.nb + run - 1) / run, parts = 2 * p.N / TP, tiles = p.B * runs * p.G * parts;
+  if (u < tiles) {
+    const int part = u % parts;
+    u /= parts;
+    const int g = u % p.G;
+    u /= p.G;
+    const int blk = u % runs * run;
+    prep_conv<T, TP>(p, t, u / runs, blk, min(blk + run, t.nb), g, part, smem);
     return;
   }
-  // (the ids of these CTAs run on in the same order)
-  u = blockIdx.x - p.B * t.nb * (1 + p.G * parts);
+  u -= tiles;
   const int caches = (p.channels + kPrep - 1) / kPrep;
   prep_cache<T>(p, u / caches, u % caches);
 }
@@ -1181,13 +1200,21 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
 
 template <typename T, int TP>
 cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  size_t smem = PrepConv<T, TP>::kBytes + kQ;
+  size_t smem = 2 * (PrepConv<T, TP>::kBytes + kQ);
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
+  // blocks per CTA: up to 8, as long as three waves of CTAs are left (2 rows of
+  // 8192 tokens, 8 groups: 1 block 63 us, 4 49 us; one row, one group: 1 block 12
+  // us, 8 20 us)
+  const long long tiles = (long long)p.B * t.nb * p.G * (2 * p.N / TP);
+  long long run = tiles / (6ll * num_sms());
+  run = run < 1 ? 1 : run > 8 ? 8 : run;
+  const int runs = (int)((t.nb + run - 1) / run);
   const int caches = p.conv_out ? (p.channels + kPrep - 1) / kPrep : 0;
-  const unsigned grid = (unsigned)(p.B * (t.nb * (1 + p.G * (2 * p.N / TP)) + caches));
-  if (p.segment_ids) return launch_next(ssm_prep_kernel<T, TP>, grid, kPrep, smem, cs, p, t);
-  ssm_prep_kernel<T, TP><<<grid, kPrep, smem, cs>>>(p, t);
+  const unsigned grid = (unsigned)(p.B * (t.nb + runs * p.G * (2 * p.N / TP) + caches));
+  if (p.segment_ids)
+    return launch_next(ssm_prep_kernel<T, TP>, grid, kPrep, smem, cs, p, t, (int)run);
+  ssm_prep_kernel<T, TP><<<grid, kPrep, smem, cs>>>(p, t, (int)run);
   return cudaGetLastError();
 }
 

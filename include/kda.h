@@ -533,7 +533,7 @@ typedef struct kda_ssm_shape {
  * states on.  conv_out must not be conv_state's buffer.
  *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores; KDA_IMPL_TC: the tensor
  *                 cores; both serve every shape and type.  KDA_IMPL_AUTO: TC, or
- *                 SIMT for long rows of few heads and fp32 rows of up to 32 tokens.
+ *                 SIMT for long rows of few heads and for small fp32 problems.
  *   workspace     device, kda_ssm_fwd_workspace_size bytes, 256-byte aligned,
  *                 its first 256 bytes zero-filled before its first use (the
  *                 device status word, see kda_read_device_status).
