@@ -25,7 +25,7 @@
 //
 // What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 49 us,
 // state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
-// segments: 12, 125 and 74 us.  The state kernel is a chain of 64 blocks on 128
+// segments: 12, 118 and 74 us.  The state kernel is a chain of 64 blocks on 128
 // SMs, each its convolution's instructions and two barriers long; the other two
 // are at the rate of their instructions and of exp2 and reciprocals.  (The
 // first kernels of this form took 9.8 and 9.5 ms on the CUDA cores.)
@@ -147,14 +147,18 @@ struct Conv {
   static constexpr int kStrip = 4;
   static constexpr int kRows = kQ + kSsmTaps - 1;
   static constexpr uint32_t kRowBytes = TP * sizeof(T);
-  static constexpr uint32_t kBytes = kRows * kRowBytes;
+  static constexpr uint32_t kPad = kRowBytes == 128 ? 0 : 4;       // bytes per row, off()
+  static constexpr uint32_t kBytes = kRows * kRowBytes + (kRows + 3) / 4 * 4 * kPad;
   using Raw = Word<CH * sizeof(T)>;
 
-  // 16-byte pieces of a row, permuted by the row's strip: the lanes of a
-  // warp read rows 4 apart.
+  // The lanes of a warp read rows 4 apart: rows of 128 bytes are permuted in
+  // 16-byte pieces by the row's strip, strips of 64-byte rows lie 16 bytes
+  // further apart than their rows fill (either way over 8 places of 16
+  // bytes; over 4, the packed row of 32 heads took 125 us instead of 118).
   static __device__ __forceinline__ uint32_t off(int row, int piece16) {
-    return (uint32_t)(row * kRowBytes) +
-           (uint32_t)((piece16 ^ (kRowBytes == 128 ? row >> 2 & 7 : row >> 3 & 3)) << 4);
+    return kRowBytes == 128
+               ? (uint32_t)(row * 128 + ((piece16 ^ (row >> 2 & 7)) << 4))
+               : (uint32_t)(row * 64 + (row >> 2) * 16 + (piece16 << 4));
   }
   static __device__ __forceinline__ void unpack(const Raw &a, u64 (&x)[E]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&a);
@@ -197,7 +201,7 @@ struct Conv {
 #pragma unroll
       for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k, src += (long long)kStep * st)
         if ((k + 1) * kStep <= kRows || row0 + k * kStep < kRows)
-          cp_async16(dst + k * kStep * kRowBytes, src);
+          cp_async16(dst + k * kStep * (kRowBytes + kPad), src);
     } else {
 #pragma unroll 1
       for (int k = 0; k < (kRows + kStep - 1) / kStep; ++k, src += (long long)kStep * st) {
@@ -209,7 +213,7 @@ struct Conv {
             from = past + (size_t)(kSsmTaps - 1 + t - first) * channels + piece * kEl;
             ok = true;
           }
-          cp_async16(dst + k * kStep * kRowBytes, from, ok);
+          cp_async16(dst + k * kStep * (kRowBytes + kPad), from, ok);
         }
       }
     }
@@ -1269,7 +1273,7 @@ cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaSt
   if (e != cudaSuccess) return e;
   // 64-column tiles halve the traffic of B's tiles (2 rows of 64 heads of 64
   // columns: 141 us, 32 columns 246); 32 where half the SMs would have no CTA
-  // (a packed row of 32 heads of 128 columns: 125 us, 64 columns 156)
+  // (a packed row of 32 heads of 128 columns: 118 us, 64 columns 156)
   const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
   e = narrow ? launch_state<bf16, 32>(p, t, cs) : launch_state<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;
