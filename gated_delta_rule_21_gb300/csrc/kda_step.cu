@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepPara
   auto work = [&](const Unit &now, int st) {
     T *o = static_cast<T *>(p.o) + ((size_t)now.at.b * p.H + now.at.h) * p.V + c0;
     if (now.slot < 0) {           // idle (uniform)
+      // the next unit writes the arrays that the one before this still reads
+      __syncthreads();
       if (tid < TC) o[tid] = from_f32<T>(0.f);
       return;
     }
