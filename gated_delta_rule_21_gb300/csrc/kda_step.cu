@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(const SsmStepPara
   auto work = [&](const Unit &now, int st) {
     T *y = static_cast<T *>(p.y) + ((size_t)now.at.b * p.H + now.at.h) * p.P + c0;
     if (now.slot < 0) {           // idle (uniform)
+      // the next unit writes the sx that the one before this still reads
+      __syncthreads();
       if (tid < TC) y[tid] = from_f32<T>(0.f);
       return;
     }

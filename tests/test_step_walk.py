@@ -90,3 +90,54 @@ def test_kda_step_walks(B, H, K, V, conv, dtype, pattern):
         near(state, state64, f32, "state")
         assert torch.equal(cache.double(), cache64)
     assert int(ws.sum()) == 0
+
+
+SSM = [(1400, 2, 32, 32, 1), (128, 33, 64, 64, 3), (96, 24, 128, 128, 2), (330, 8, 64, 128, 8)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,H,P,N,G", SSM)
+@pytest.mark.parametrize("pattern", PATTERNS)
+def test_ssm_step_walks(B, H, P, N, G, dtype, pattern):
+    import gated_delta_rule_21_gb300 as kda
+    cpu = torch.Generator().manual_seed(B * 3 + H)
+    gen = torch.Generator(device="cuda").manual_seed(B * 3 + H)
+    f32 = torch.float32
+
+    def rand(*s, std=1.0, mean=0.0, to=f32):
+        return plain64.cast(mean + std * torch.randn(*s, generator=gen, device="cuda"), to)
+
+    n_slots, hp, ch = B + 5, H * P, H * P + 2 * G * N
+    idle = idle_rows(pattern, B, H, 2 if P == 128 else 1, cpu)
+    slots = slots_of(idle, n_slots, cpu)
+    on = (~idle).cuda()
+    at = slots[on].long()
+    state, state64 = rand(n_slots, H, N, P, std=0.3)
+    conv, conv64 = rand(n_slots, 3, ch, to=dtype)
+    (w, w64), (bias, bias64) = rand(ch, 4, std=0.5), rand(ch, std=0.1)
+    (db, db64), (D, D64) = rand(H, mean=-3.0), rand(H, mean=1.0)
+    A, A64 = plain64.cast(-(1 + 15 * torch.rand(H, generator=gen, device="cuda")), f32)
+    ws = kda.alloc_step_workspace(B, H)
+    for _ in range(3):
+        proj, proj64 = rand(B, hp + ch + H + 3, to=dtype)
+        z, x, dt = proj[:, :hp], proj[:, hp:hp + ch], proj[:, hp + ch:hp + ch + H]
+        y = kda.ssm_step(x, dt, w, A, state, conv, head_dim=P, state_dim=N, conv_bias=bias,
+                         dt_bias=db, D=D, z=z, slots=slots, workspace=ws)
+        z, x, dt = (t[on] for t in proj64.split([hp, ch, H, 3], 1)[:3])
+        full = torch.cat([conv64[at], x[:, None]], 1)
+        conv64[at] = full[:, 1:]
+        u = plain64.silu((full * w64.t()).sum(1) + bias64)
+        xs = u[:, :hp].unflatten(1, (H, P))
+        bs, cs = (t.unflatten(1, (G, N)).repeat_interleave(H // G, 1)
+                  for t in u[:, hp:].split([G * N, G * N], 1))
+        d = plain64.softplus(dt + db64)
+        s = torch.exp(d * A64)[..., None, None] * state64[at] \
+            + (d[..., None] * bs)[..., None] * xs[:, :, None]
+        state64[at] = s
+        want = torch.zeros(B, H, P, dtype=torch.float64, device="cuda")
+        want[on] = ((cs[..., None] * s).sum(2) + D64[:, None] * xs) \
+            * plain64.silu(z).unflatten(1, (H, P))
+        near(y, want, dtype, "y")
+        near(state, state64, f32, "state")
+        assert torch.equal(conv.double(), conv64)
+    assert int(ws.sum()) == 0
