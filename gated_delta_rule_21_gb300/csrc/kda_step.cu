@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(const SsmStepPara
   constexpr int IT = N * TC / kWave, RG = kWave / TC, CH = 2 * N + TC;
   constexpr int NC = (CH + kThreads - 1) / kThreads;      // channels per thread
   extern __shared__ __align__(16) float4 stage[];         // [2][IT][kThreads]
-  __shared__ float sB[2][N], sC[2][N], sx[2][TC], red[kThreads / 32][TC];
+  __shared__ float sB[2][N], sC[2][N], sx[2][TC];
+  __shared__ __align__(16) float red[kThreads / 32][TC];   // written as float4
   __shared__ int flag;
   const int tid = threadIdx.x, col = (tid * 4) % TC, row = tid * 4 / TC;
 
@@ -306,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, 3) kda_step_kernel(const KdaStepPara
   constexpr int IT = K * TC / kWave, RG = kWave / TC, CH = 2 * K + TC;
   constexpr int NC = (CH + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) float4 stage[];         // [2][IT][kThreads]
-  __shared__ float sq[2][K], sk[2][K], sg[2][K], sv[2][TC], dots[3];
+  __shared__ float sq[2][K], sk[2][K], sg[2][K], dots[3];
+  __shared__ __align__(16) float sv[2][TC];                // read as float4
   __shared__ float4 sums[2][kThreads / 32][TC / 4];
   __shared__ int flag[2];
   const int tid = threadIdx.x, col = (tid * 4) % TC, row = tid * 4 / TC;
