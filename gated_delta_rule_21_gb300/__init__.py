@@ -22,11 +22,16 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix):
 * :func:`workspace_size`, :func:`read_device_status`,
   :func:`clear_device_status`, :func:`status_string`, :func:`version`.
 * :func:`lib` -- the raw ctypes library with typed signatures.
+
+``stream`` is a ``torch.cuda.Stream`` (None: the current one).  What a call
+allocates belongs to that stream, as under ``torch.cuda.stream(stream)``: wait
+for it, and ``record_stream`` outputs that another stream goes on to use.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import threading
 
@@ -248,6 +253,24 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _on_its_stream(f):
+    """A call with ``stream`` is the call made under ``torch.cuda.stream(stream)``:
+    the outputs and scratch memory that it allocates belong to that stream, and
+    scratch memory is zeroed there before the kernels that count on it."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None or stream == torch.cuda.current_stream(stream.device):
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+
+    return call
+
+
+@_on_its_stream
 def chunk_fwd(q, k, v, g, beta, scale=None, chunk_size=CHUNK, initial_state=None,
               segment_ids=None, output_final_state=False, out=None,
               final_state_out=None, workspace=None, impl="auto", v_tile=0,
@@ -309,6 +332,7 @@ def scan_segments(B, T, H, K, V, dtype=torch.bfloat16, n_segments=0) -> int:
     return int(lib().kda_chunk_fwd_scan_segments(ctypes.byref(s), int(n_segments)))
 
 
+@_on_its_stream
 def chunk_fwd_scan(q, k, v, g, beta, scale=None, chunk_size=CHUNK, initial_state=None,
                    output_final_state=False, n_segments=0, out=None, final_state_out=None,
                    workspace=None, stream=None):
@@ -371,6 +395,7 @@ def bwd_workspace_size_packed(B, T, H, K, V, max_runs_per_row, dtype=torch.bfloa
     return int(lib().kda_chunk_bwd_workspace_size_packed(ctypes.byref(s), int(max_runs_per_row)))
 
 
+@_on_its_stream
 def chunk_bwd(q, k, v, g, beta, d_o, scale=None, chunk_size=CHUNK, initial_state=None,
               segment_ids=None, d_final=None, want_d_initial=True, workspace=None,
               stream=None, impl="auto"):
@@ -424,6 +449,7 @@ def fwd_save_workspace_size(B, T, H, K, V, dtype=torch.bfloat16, has_segment_ids
     return int(lib().kda_chunk_fwd_save_workspace_size(ctypes.byref(s), int(bool(has_segment_ids))))
 
 
+@_on_its_stream
 def chunk_fwd_save(q, k, v, g, beta, scale=None, chunk_size=CHUNK, initial_state=None,
                    segment_ids=None, output_final_state=True, workspace=None, stream=None):
     """The forward of a training step (``kda_chunk_fwd_save``): returns
@@ -463,6 +489,7 @@ def chunk_fwd_save(q, k, v, g, beta, scale=None, chunk_size=CHUNK, initial_state
     return o, fs, workspace
 
 
+@_on_its_stream
 def chunk_bwd_from_saved(q, k, v, g, beta, d_o, workspace, scale=None, chunk_size=CHUNK,
                          initial_state=None, segment_ids=None, d_final=None,
                          want_d_initial=True, stream=None):
@@ -493,6 +520,7 @@ def chunk_bwd_from_saved(q, k, v, g, beta, d_o, workspace, scale=None, chunk_siz
     return dq, dk, dv, dg, dbeta, d_init
 
 
+@_on_its_stream
 def short_conv_silu(x_q, x_k, x_v, w, segment_ids=None, l2norm_qk=True,
                     stream=None):
     """Segment-aware causal depthwise conv (width 4) + SiLU on q, k, v, then
@@ -528,6 +556,7 @@ def host_buffer_size(B, T, H, K, V, dtype=torch.bfloat16, has_segment_ids=False)
     return int(lib().kda_chunk_fwd_host_buffer_size(ctypes.byref(s), 1 if has_segment_ids else 0))
 
 
+@_on_its_stream
 def chunk_fwd_host(q, k, v, g, beta, scale=None, chunk_size=CHUNK, initial_state=None,
                    segment_ids=None, output_final_state=False, out=None,
                    final_state_out=None, device_buffer=None, stream=None):
@@ -714,6 +743,7 @@ def alloc_step_workspace(B, H, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
+@_on_its_stream
 def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_state=None,
          l2norm_qk=False, out=None, workspace=None, stream=None):
     """One token per sequence through the delta rule, on cached states.
@@ -785,6 +815,7 @@ def _tokens(t, name, shape, dtype, device):
     return t.data_ptr(), st[0], st[1]
 
 
+@_on_its_stream
 def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=None, D=None,
             z=None, initial_state=None, conv_state=None, segment_ids=None,
             output_final_state=False, out=None, workspace=None, impl="auto", stream=None):
@@ -825,6 +856,7 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     return y, fs, conv
 
 
+@_on_its_stream
 def ssm_step(xbc, dt, conv_w, A, state, conv_state, *, head_dim, state_dim, conv_bias=None,
              dt_bias=None, D=None, z=None, slots=None, out=None, workspace=None, stream=None):
     """One token per sequence through the state space operator, on cached
@@ -873,6 +905,7 @@ def _norm_desc(y, gate, gate_act, scale, eps):
     return _norm_ref(rows, D, DTYPES[y.dtype], act, grows, scale, eps), rows, (D,)
 
 
+@_on_its_stream
 def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale=1.0, w_pre=None,
                eps=1e-6, save_stats=False, out=None, stream=None):
     """The norm after a block, its gate and residual scale, and the norm
@@ -921,6 +954,7 @@ def alloc_block_norm_workspace(rows, D, gate_rows=0, device=None) -> torch.Tenso
                     "kda_block_norm_bwd_workspace_size", 0)[0]
 
 
+@_on_its_stream
 def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=None,
                    gate_act="sigmoid", scale=1.0, w_pre=None, eps=1e-6, workspace=None,
                    stream=None):
