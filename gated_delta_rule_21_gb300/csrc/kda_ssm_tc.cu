@@ -411,8 +411,11 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         d[i] = sdt[(lane * 4 + i) * 33 + hh];
-        a[i].hi = d[i] > 0.f ? d[i] * a2 : 0.f;
-        a[i].lo = kF32 && d[i] > 0.f ? fmaf(d[i], a2, -a[i].hi) + d[i] * a2_lo : 0.f;
+        // a width that is not finite reaches its run's tokens by cumj and wst; in
+        // the sums it would reach every token after it
+        const bool in = d[i] > 0.f && d[i] < CUDART_INF_F;
+        a[i].hi = in ? d[i] * a2 : 0.f;
+        a[i].lo = kF32 && in ? fmaf(d[i], a2, -a[i].hi) + d[i] * a2_lo : 0.f;
       }
       pre[0] = a[0];
 #pragma unroll
@@ -456,8 +459,8 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
           t.ein[s] = run == 0 ? exp2f(c.hi) : 0.f;
           t.cum[s] = c.hi;
           t.cum_lo[s] = c.lo;
-          t.cumj[s] = d[i] > 0.f ? j.hi : CUDART_INF_F;
-          t.cumj_lo[s] = d[i] > 0.f ? j.lo + c.lo : 0.f;
+          t.cumj[s] = d[i] == 0.f ? CUDART_INF_F : j.hi;
+          t.cumj_lo[s] = d[i] == 0.f ? 0.f : j.lo + c.lo;
         } else {
           const float c = before.hi + pre[i].hi;
           t.ein[s] = run == 0 ? exp2f(c) : 0.f;

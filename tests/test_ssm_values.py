@@ -1,0 +1,63 @@
+"""GPU tests of the state space operator on values at the edges: step widths,
+inputs and cached states that are not finite, decays of any size.
+
+What is not finite may reach only what the recurrence lets it reach: tokens of
+its own run from its own place on, and the state if that run is the last.
+Everything else stays within the tolerances of test_ssm.py."""
+import pytest
+import torch
+
+from test_ssm import IMPLS, Case
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def near(got, ref, dtype, what):
+    """Finite exactly where the plain form is, and near it there."""
+    got = got.double().cpu()
+    ok = ref.isfinite()
+    assert torch.equal(got.isfinite(), ok), \
+        f"{what}: {int((got.isfinite() != ok).sum())} of {ok.numel()} finite in one form only"
+    got, ref = got[ok], ref[ok]
+    if ref.numel() == 0:
+        return
+    d = (got - ref).abs()
+    if dtype == torch.float32:
+        assert d.max() <= 2e-5 * ref.abs().max() + 1e-30, (what, d.max())
+    else:
+        assert d.max() <= 2 ** -5 * ref.abs().max() + 1e-30, (what, d.max())
+        assert d.norm() <= 5e-3 * ref.norm() + 1e-30, (what, d.norm() / ref.norm())
+
+
+def check(c, impl):
+    (y, s, conv), (yr, sr, cr) = c.gpu(impl), c.plain()
+    near(y, yr, c.dtype, "y")
+    near(s, sr, torch.float32, "state")
+    assert torch.equal(conv.double().cpu().nan_to_num(9.0), cr.nan_to_num(9.0))
+
+
+def put(c, part, b, t, index, value):
+    """Sets one input of token t of row b: part 0 xbc, 1 dt, 2 z."""
+    for proj in c.proj:
+        c.parts(proj[b])[part][t, index] = value
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS[1::2])     # the tensor cores
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_step_widths_that_are_not_finite(dtype, impl, value):
+    """In one head, at the first and a later token, in a row of one run and in
+    a row of several that share blocks.  (-inf is a step of width 0.)"""
+    T = 300
+    ids = torch.ones(4, T, dtype=torch.int32)
+    ids[2, 40:60], ids[2, 60:] = 2, 3
+    ids[3, 30:200], ids[3, 200:] = 0, 2
+    c = Case(4, T, 3, 32, 64, 1, dtype, ids=ids, init=True)
+    put(c, 1, 0, 0, 1, value)
+    put(c, 1, 1, 77, 0, value)
+    put(c, 1, 2, 45, 2, value)
+    put(c, 1, 2, 61, 0, value)
+    put(c, 1, 3, 7, 1, value)
+    put(c, 1, 3, 90, 1, value)          # padding: nothing
+    check(c, impl)
