@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
   const float *enter = cut.segs > 1 ? seg_state + ((size_t)seg * p.B * p.H + bh) * per
                        : p.initial_state ? p.initial_state + (size_t)bh * per : nullptr;
   float s[NS], decay = 1.f;
+  bool dropped = false;
 #pragma unroll
   for (int j = 0; j < NS; ++j) s[j] = 0.f;
   const int end = min(p.T, (seg + 1) * cut.len);
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
       const float4 *pb = reinterpret_cast<const float4 *>(sB + t * N + warp * NS),
                    *pc = reinterpret_cast<const float4 *>(sC + t * N + warp * NS);
       if (reset) {               // drops the state whatever it holds
-        decay = 0.f;
+        dropped = true;
 #pragma unroll
         for (int j = 0; j < NS; ++j) s[j] = 0.f;
       }
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
     float *out = seg_state + ((size_t)(seg + 1) * p.B * p.H + bh) * per;
 #pragma unroll
     for (int j = 0; j < NS; ++j) out[mine + (size_t)j * p.P] = s[j];
-    if (tid == 0 && tile == 0) seg_decay[(size_t)seg * p.B * p.H + bh] = decay;
+    if (tid == 0 && tile == 0)
+      seg_decay[(size_t)seg * p.B * p.H + bh] = dropped ? -1.f : decay;
     return;
   }
   if (seg + 1 < cut.segs) return;
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) ssm_simt_kernel(const SsmParams p, c
 }
 
 // The states that enter the segments, in place: S_0 is the initial state,
-// S_{i+1} = decay_i S_i + what segment i added.
+// S_{i+1} = decay_i S_i + what segment i added.  A decay of -1: a reset.
 __global__ void __launch_bounds__(256)
     ssm_simt_chain_kernel(const float *initial, float *seg_state, const float *seg_decay, int segs,
                           int heads, size_t per) {
@@ -277,8 +279,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (k0 + k + 1 < segs) {
-        // decay 0 (a reset, or underflow) drops the state whatever it holds
-        s = (a[k] == 0.f ? 0.f : a[k] * s) + v[k];
+        // a reset drops the state whatever it holds; a decay that underflows
+        // does not: a NaN stays one
+        s = (a[k] < 0.f ? 0.f : a[k] * s) + v[k];
         seg_state[(size_t)(k0 + k + 1) * n + i] = s;
       }
   }

@@ -44,7 +44,7 @@ def put(c, part, b, t, index, value):
         c.parts(proj[b])[part][t, index] = value
 
 
-@pytest.mark.parametrize("dtype,impl", IMPLS[1::2])     # the tensor cores
+@pytest.mark.parametrize("dtype,impl", IMPLS)
 @pytest.mark.parametrize("value", [NAN, INF, -INF])
 def test_step_widths_that_are_not_finite(dtype, impl, value):
     """In one head, at the first and a later token, in a row of one run and in
