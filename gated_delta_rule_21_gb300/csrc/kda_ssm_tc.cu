@@ -20,8 +20,9 @@
 // inputs y is rounded to bf16 at the end and its products' operands (C, B, x, S
 // and the 128 x 128 matrix of factors) are bf16 too; their errors are of y's own
 // rounding's size and average out over the sums (2.6e-3 in all; y's own rounding
-// alone is 1.7e-3).  With fp32 inputs these operands are split in two as well,
-// and three of the four products added (3.2e-6).
+// alone is 1.7e-3).  With fp32 inputs these operands are split in two as well
+// and all four products added (2.8e-6; an output that one term dominates up to
+// 1.1e-5, without the product of the second parts 2.3e-5).
 //
 // What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 49 us,
 // state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
@@ -990,6 +991,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       const Opnd opB2 = {sb + L::kF + L::kPart, 128, (uint32_t)N * 16};
       mma_k(t_cb, opC, 0, opB2, 0, N / 16, 128, true);
       mma_k(t_cb, opC2, 0, opB, 0, N / 16, 128, true);
+      mma_k(t_cb, opC2, 0, opB2, 0, N / 16, 128, true);
     }
     mma_commit(bar_m);
   }
@@ -1012,7 +1014,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       if (mbar_wait(bar_s, k & 1)) {
         const Opnd opS = {sb + L::kS, 128, (uint32_t)N * 16};
         mma_k(t_yi, opC, 0, opS, 1, N / 16, kCols, false);
-        if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, PT, true);
+        if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, kCols, true);
         mma_commit(bar_m);
       } else {
         give_up();
@@ -1097,7 +1099,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
         mma_k(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
         if (kF32) {
           const Opnd opF2 = {sb + L::kF + L::kPart, 128, kQ * 16};
-          mma_k(t_yx, opF2, 0, opX, 1, kQ / 16, PT, true);
+          mma_k(t_yx, opF2, 0, opX, 1, kQ / 16, kCols, true);
         }
         mma_commit(bar_m);
         if (k + 1 < n_items) {

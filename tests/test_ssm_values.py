@@ -61,3 +61,19 @@ def test_step_widths_that_are_not_finite(dtype, impl, value):
     put(c, 1, 3, 7, 1, value)
     put(c, 1, 3, 90, 1, value)          # padding: nothing
     check(c, impl)
+
+
+def between(dtype, every, size):
+    """Widths of about 1e-3 and 8 by turns: short runs of tokens that remember
+    each other behind sums of decays that have run far, and outputs of which one
+    term is nearly all."""
+    c = Case(2, 400, 3, 32, 64, 1, dtype, init=True, A=(size, 2 * size), dt=(0.0, 0.0))
+    for proj in c.proj:
+        dt = c.parts(proj)[1]
+        dt[...] = -7.0 if size < 1e3 else -14.0      # |A| d near 0.3 and 1
+        dt[:, ::every] = 8.0
+    return c
+
+
+def test_outputs_of_one_term_in_fp32():
+    check(between(torch.float32, 2, 300.0), "tc")
