@@ -357,7 +357,13 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 //          it matters)
 // A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums up to a token
 // are made and kept in two floats: a factor e^(c_r - c_j) is as exact as the
-// difference, however far the sums have run.  (64-bit sums took 40 us.)
+// difference, however far the sums have run.  (64-bit sums took 40 us.)  For bf16
+// inputs they are kept in one, so c_r - c_j is off by a step of the sum or a few:
+// 6e-5 each at kWide.  Beyond it the sums are made in two floats and rounded
+// once, and a token's a counts down to kFar only: the sum stays above -2^15, one
+// step is 2^-9 and a factor off by 1.4e-3 at most, less than half a step of bf16.
+constexpr float kFar = -256.f;     // 2^kFar is 0 beside any fp32 value, as 2^a below it is
+constexpr float kWide = 1024.f;
 template <typename T>
 __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t, int b, int blk,
                                              unsigned char *smem) {
@@ -408,43 +414,49 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
       const float A = p.A[h0 + hh], a2 = A * kLog2e;
       const float a2_lo = fmaf(A, kLog2e, -a2) + A * 1.9259629911266175e-8f;
       float d[4], suf[4];
-      Two a[4], pre[4];
+      Two a[4], pre[4], before;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         d[i] = sdt[(lane * 4 + i) * 33 + hh];
         // a width that is not finite reaches its run's tokens by cumj and wst; in
         // the sums it would reach every token after it
-        const bool in = d[i] > 0.f && d[i] < CUDART_INF_F;
-        a[i].hi = in ? d[i] * a2 : 0.f;
-        a[i].lo = kF32 && in ? fmaf(d[i], a2, -a[i].hi) + d[i] * a2_lo : 0.f;
+        const float f = d[i] * a2;
+        const bool in = d[i] > 0.f && d[i] < CUDART_INF_F, far = f < kFar;
+        a[i].hi = !in ? 0.f : far ? kFar : f;
+        a[i].lo = kF32 && in && !far ? fmaf(d[i], a2, -f) + d[i] * a2_lo : 0.f;
       }
-      pre[0] = a[0];
+      float total;
+      auto prefix = [&](auto two) {      // pre: in the lane; before: the lanes before
+        constexpr bool k2 = decltype(two)::value;
+        auto plus = [](Two u, Two v) { return k2 ? add(u, v) : Two{u.hi + v.hi, 0.f}; };
+        pre[0] = a[0];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) {
-        if (kF32) pre[i] = add(pre[i - 1], a[i]);
-        else pre[i].hi = pre[i - 1].hi + a[i].hi;
-      }
+        for (int i = 1; i < 4; ++i) pre[i] = plus(pre[i - 1], a[i]);
+        before = pre[3];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          Two u = {__shfl_up_sync(0xffffffffu, before.hi, o), 0.f};
+          if (k2) u.lo = __shfl_up_sync(0xffffffffu, before.lo, o);
+          if (lane >= o) before = plus(before, u);
+        }
+        total = __shfl_sync(0xffffffffu, before.hi, 31);
+        before.hi = __shfl_up_sync(0xffffffffu, before.hi, 1);
+        if (k2) before.lo = __shfl_up_sync(0xffffffffu, before.lo, 1);
+        if (lane == 0) before = {0.f, 0.f};
+      };
+      prefix(std::integral_constant<bool, kF32>{});
+      const bool wide = !kF32 && total < -kWide;
+      if (wide) prefix(std::true_type{});
       suf[3] = 0.f;
 #pragma unroll
       for (int i = 2; i >= 0; --i) suf[i] = suf[i + 1] + a[i + 1].hi;
-      Two before = pre[3];
       float after = pre[3].hi;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        Two u = {__shfl_up_sync(0xffffffffu, before.hi, o), 0.f};
-        if (kF32) u.lo = __shfl_up_sync(0xffffffffu, before.lo, o);
         const float v = __shfl_down_sync(0xffffffffu, after, o);
-        if (lane >= o) {
-          if (kF32) before = add(before, u);
-          else before.hi += u.hi;
-        }
         if (lane + o < 32) after += v;
       }
-      const float total = __shfl_sync(0xffffffffu, before.hi, 31);
-      before.hi = __shfl_up_sync(0xffffffffu, before.hi, 1);
-      if (kF32) before.lo = __shfl_up_sync(0xffffffffu, before.lo, 1);
       after = __shfl_down_sync(0xffffffffu, after, 1);
-      if (lane == 0) before = {0.f, 0.f};
       if (lane == 31) after = 0.f;
       const int last = srun[kQ - 1];
       const size_t at = (((size_t)b * p.H + h0 + hh) * t.nb + blk) * kQ;
@@ -455,13 +467,16 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
         const int run = srun[lane * 4 + i];
         const size_t s = at + slot_of(lane * 4 + i);
         const float l = log2f(d[i]);           // d = 0: -inf, a factor of 0
-        if constexpr (kF32) {
+        if (kF32 || wide) {
           const Two c = add(before, pre[i]), j = two_sum(c.hi, -l);
+          const float rest = j.lo + c.lo;
           t.ein[s] = run == 0 ? exp2f(c.hi) : 0.f;
           t.cum[s] = c.hi;
-          t.cum_lo[s] = c.lo;
-          t.cumj[s] = d[i] == 0.f ? CUDART_INF_F : j.hi;
-          t.cumj_lo[s] = d[i] == 0.f ? 0.f : j.lo + c.lo;
+          t.cumj[s] = d[i] == 0.f ? CUDART_INF_F : kF32 ? j.hi : j.hi + rest;
+          if (kF32) {
+            t.cum_lo[s] = c.lo;
+            t.cumj_lo[s] = d[i] == 0.f ? 0.f : rest;
+          }
         } else {
           const float c = before.hi + pre[i].hi;
           t.ein[s] = run == 0 ? exp2f(c) : 0.f;

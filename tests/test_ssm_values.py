@@ -77,3 +77,19 @@ def between(dtype, every, size):
 
 def test_outputs_of_one_term_in_fp32():
     check(between(torch.float32, 2, 300.0), "tc")
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("size", [40.0, 400.0, 4000.0, 3e37])
+def test_decays_of_any_size(dtype, impl, size):
+    """|A| d of 80 to 1e38 at every token: only a token's own term is left, and
+    its factor d must not carry the rounding of the sums around it."""
+    c = Case(2, 260, 3, 64, 64, 1, dtype, init=True, A=(size, 1.5 * size), dt=(2.0, 1.0))
+    check(c, impl)
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("every", [2, 5])
+@pytest.mark.parametrize("size", [300.0, 1e6])
+def test_small_decays_between_total_ones(dtype, impl, every, size):
+    check(between(dtype, every, size), impl)
