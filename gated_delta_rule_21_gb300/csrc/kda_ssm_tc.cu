@@ -353,7 +353,7 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 //   cum  = sum of a up to the token            cumj = cum - log2 d
 //   ein  = 2^cum where the entering state reaches the token, else 0
 //   wst  = d 2^(sum of a after the token) where the token reaches the state
-//          that leaves the block, else 0 (summed from the end: exact where
+//          that leaves the block, else -0 (summed from the end: exact where
 //          it matters)
 // A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums up to a token
 // are made and kept in two floats: a factor e^(c_r - c_j) is as exact as the
@@ -483,7 +483,7 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
           t.cum[s] = c;
           t.cumj[s] = c - l;
         }
-        fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : 0.f;
+        fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : -0.f;
       }
       *reinterpret_cast<float4 *>(t.wst + at + lane * 4) = wst;
       if (lane == 0)
@@ -628,6 +628,35 @@ struct StateSmem {
   static constexpr uint32_t kBar = kW + 2 * kQ * 4;
   static constexpr uint32_t kBytes = kBar + 64;
 };
+
+// Whether a token's wst says that its run ends before the block does.
+__device__ __forceinline__ bool ends_before(float wst) {
+  return __float_as_uint(wst) == 0x80000000u;
+}
+
+// What the tokens that reach the state (f: wst, by token) add to row n of it in
+// the columns of the operand tile at x, in place of the products.
+template <int TP, int COLS>
+__device__ __forceinline__ void tokens_of_state(const unsigned char *x, const unsigned char *bhi,
+                                                const unsigned char *blo, const float *f, int n,
+                                                int N, float (&add)[COLS]) {
+#pragma unroll
+  for (int k = 0; k < COLS; ++k) add[k] = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < kQ; ++j) {
+    if (ends_before(f[token_of(j)])) continue;
+    const uint32_t o = op_off(j, n, N);
+    const float b = __bfloat162float(*reinterpret_cast<const bf16 *>(bhi + o)) +
+                    __bfloat162float(*reinterpret_cast<const bf16 *>(blo + o));
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) {
+      const unsigned char *v = x + mn_off(k, j, kQ);
+      add[k] = fmaf(b, __bfloat162float(*reinterpret_cast<const bf16 *>(v)) +
+                           __bfloat162float(*reinterpret_cast<const bf16 *>(v + TP / 8 * 2048)),
+                    add[k]);
+    }
+  }
+}
 
 // 512 threads run the convolution, keep S and write it; one more warp copies
 // the tiles of B and issues the products.  Per block i the threads
@@ -781,14 +810,27 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         reg_fence8(hi[k]);
         reg_fence8(lo[k]);
       }
+      float add[kCols];
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        add[k] = __uint_as_float(hi[k / 8][k % 8]) + __uint_as_float(lo[k / 8][k % 8]);
       if (IDS && a < 0.f) {     // a reset drops the state whatever it holds
 #pragma unroll
         for (int k = 0; k < kCols; ++k) s[k] = 0.f;
         a = 0.f;
+        // B of a run that ended may be NaN or infinite, which times 0 is NaN: then
+        // the tokens that reach the state are added up one by one
+        float odd = 0.f;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) odd = fmaf(add[k], 0.f, odd);
+        if (__any_sync(0xffffffffu, odd != 0.f) && n < N)
+          tokens_of_state<TP>(smem + L::kX + (i & 1) * L::kXBytes + col0 / 8 * 2048,
+                              t.bhi + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
+                              t.blo + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
+                              wst + (size_t)i * kQ, n, N, add);
       }
 #pragma unroll
-      for (int k = 0; k < kCols; ++k)
-        s[k] = fmaf(a, s[k], __uint_as_float(hi[k / 8][k % 8]) + __uint_as_float(lo[k / 8][k % 8]));
+      for (int k = 0; k < kCols; ++k) s[k] = fmaf(a, s[k], add[k]);
       tc_fence_before();
     };
     stage(0);
@@ -825,7 +867,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         for (int e = 0; e < Cv::E; ++e) {
           u[e] = mul2(u[e], pk2(f, f));
           // a token that does not reach the state adds nothing, whatever it holds
-          if (cut && f == 0.f) u[e] = pk2(0.f, 0.f);
+          if (cut && ends_before(f)) u[e] = pk2(0.f, 0.f);
         }
         split(u, hi, lo);
         *reinterpret_cast<Out *>(xo + k * 128) = hi;
@@ -847,7 +889,10 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       a_now = a_next;
     }
     cp_async_wait_all();
-    if (i == nb) finish(nb - 1, a_prev);
+    if (i == nb) {
+      if (IDS) any_of_conv(false);   // x of the last block, which finish may read
+      finish(nb - 1, a_prev);
+    }
     if (p.final_state && n < N) {
 #pragma unroll
       for (int k = 0; k < kCols; k += 4)
@@ -1146,9 +1191,35 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
           yx[e] += vx[e];
         }
       }
-      if ((flags & kResets) && ein_now == 0.f)     // the entering state does not reach the
+      if ((flags & kResets) && run > 0)            // the entering state does not reach the
 #pragma unroll
         for (int e = 0; e < 16; ++e) yi[e] = 0.f;  // token, whatever it holds
+      // x of a later token or another run may be NaN or infinite, which times 0 is
+      // NaN: then the tokens that reach row r are added up one by one
+      u64 odd = 0;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) odd = fma2(pk2(yx[e], yx[e + 1]), 0, odd);
+      if (__any_sync(0xffffffffu, (odd & 0x7fffffff7fffffffull) != 0)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) yx[e] = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < kQ; ++j) {
+          if (token_of(j) > 32 * quad + r_token ||
+              ((flags & kResets) && srun[j] != (signed char)run))
+            continue;
+          const unsigned char *fp = smem + L::kF + op_off(r, j, kQ),
+                              *xp = smem + L::kX + mn_off(col, j, kQ);
+          float f = __bfloat162float(*reinterpret_cast<const bf16 *>(fp));
+          if (kF32) f += __bfloat162float(*reinterpret_cast<const bf16 *>(fp + L::kPart));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const unsigned char *v = xp + mn_off(e, 0, kQ);
+            float x = __bfloat162float(*reinterpret_cast<const bf16 *>(v));
+            if (kF32) x += __bfloat162float(*reinterpret_cast<const bf16 *>(v + kQ * PT * 2));
+            yx[e] = fmaf(f, x, yx[e]);
+          }
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         u64 x[4], z[4], y[4];

@@ -537,8 +537,8 @@ typedef struct kda_ssm_shape {
  *   workspace     device, kda_ssm_fwd_workspace_size bytes, 256-byte aligned,
  *                 its first 256 bytes zero-filled before its first use (the
  *                 device status word, see kda_read_device_status).
- * TC computes a row in blocks of 128 tokens: a value that is not finite
- * spreads to other runs that share a block with it (never from padding).
+ * A value that is not finite reaches its own run from its token on, and the
+ * final state if that run is the row's last; no other run, no earlier token.
  * xbc, z and the states are 16-byte aligned and the strides of xbc and z
  * multiples of 16 bytes (KDA_ERR_ALIGNMENT).  Asynchronous on `stream`.
  */

@@ -93,3 +93,39 @@ def test_decays_of_any_size(dtype, impl, size):
 @pytest.mark.parametrize("size", [300.0, 1e6])
 def test_small_decays_between_total_ones(dtype, impl, every, size):
     check(between(dtype, every, size), impl)
+
+
+def runs(T):
+    """A whole row, runs that share blocks, runs and padding."""
+    ids = torch.ones(3, T, dtype=torch.int32)
+    ids[1, 40:60], ids[1, 60:150], ids[1, 150:] = 2, 3, 4
+    ids[2, :9], ids[2, 100:140], ids[2, 140:260], ids[2, 260:] = 0, 0, 2, 0
+    return ids
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("what", ["x", "B", "C", "z"])
+@pytest.mark.parametrize("G", [1, 2])
+def test_inputs_that_are_not_finite(dtype, impl, value, what, G):
+    """Neither earlier tokens nor other runs of the same block see them."""
+    T, H, P, N = 300, 4, 64, 32
+    c = Case(3, T, H, P, N, G, dtype, ids=runs(T), init=True)
+    part, at = {"x": (0, P + 5), "B": (0, H * P + 3), "C": (0, H * P + G * N + 17),
+                "z": (2, 2 * P + 40)}[what]
+    for b, t in ((0, 130), (0, 290), (1, 30), (1, 45), (1, 170), (2, 90), (2, 115), (2, 150)):
+        put(c, part, b, t, at, value)
+    check(c, impl)
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_caches_that_are_not_finite(dtype, impl, value):
+    """A state and a convolution cache reach the row's first run only."""
+    T, H, P, N = 300, 4, 32, 64
+    c = Case(3, T, H, P, N, 1, dtype, ids=runs(T), init=True)
+    for i in range(2):
+        c.s0[i][:, 1, 7, 20] = value
+        c.c0[i][1, 1, H * P + 9] = value
+        c.c0[i][2, 2, 2 * P + 3] = value
+    check(c, impl)
