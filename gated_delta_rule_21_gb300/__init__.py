@@ -915,8 +915,9 @@ def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale
     y, residual: [..., D] (bf16 or fp32, contiguous); gate: [..., D] with as
     many rows as y, or fewer that divide them (each then serves as many
     consecutive rows); w_post, w_pre: [D] fp32.  residual, gate and w_pre may be
-    None.  ``out`` may be the residual itself.  Returns ``(out, x or None)``, and
-    the statistics block_norm_bwd reads when ``save_stats``."""
+    None.  ``out`` may be the residual itself, but not with ``save_stats``:
+    block_norm_bwd reads the residual.  Returns ``(out, x or None)``, and the
+    statistics block_norm_bwd reads when ``save_stats``."""
     dev, ty = _start(y, "block_norm")
     shape = y.shape
     d, rows, width = _norm_desc(y, gate, gate_act, scale, eps)

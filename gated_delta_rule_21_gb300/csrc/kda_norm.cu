@@ -210,6 +210,8 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_desc *d, const void *y,
   const kda_status st = check_desc(d, gate != nullptr);
   if (st != KDA_OK) return st;
   if (!y || !w_post || !out || (w_pre != nullptr) != (x != nullptr)) return KDA_ERR_INVALID_ARG;
+  // stats are for the backward, which reads the residual: it must outlive this call
+  if (stats && out == residual) return KDA_ERR_INVALID_ARG;
   const bool bf16 = d->dtype == KDA_DTYPE_BF16;
   bool vec = true;
   for (const void *ptr : {y, (const void *)w_post, residual, gate, (const void *)w_pre,

@@ -602,7 +602,9 @@ KDA_API kda_status kda_step(const kda_shape *s, const void *q, const void *k, co
  *     x   = out * (mean(out^2) + eps)^-1/2 * w_pre
  * in fp32, rounded once at out and x (x is made from the unrounded out).
  *   y, residual, out, x   device [rows, dim] of d->dtype, contiguous; residual
- *                 NULL: no residual (zeros); out may be the residual's buffer.
+ *                 NULL: no residual (zeros); out may be the residual's buffer where
+ *                 no stats are wanted (KDA_ERR_INVALID_ARG with them: the
+ *                 backward makes out again from the residual).
  *   gate          device [gate_rows, dim] of d->dtype or NULL (act(gate) = 1);
  *                 gate row g serves rows [g, g + 1) * rows / gate_rows.
  *   w_post, w_pre device float32 [dim]; w_pre and x both NULL: no second norm.

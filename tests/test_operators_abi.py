@@ -95,6 +95,12 @@ def test_block_norm_refuses(L, kw, want):
     assert norm(L, **kw) == want
 
 
+def test_block_norm_in_place_keeps_nothing_for_the_backward(L):
+    """The backward reads the residual, so out cannot replace it then."""
+    args = [desc(), FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, None]
+    assert L.kda_block_norm_fwd(*args) == 1
+
+
 def norm_bwd(L, stats=FAKE, res=None, gate=None, w_pre=None, d_out=FAKE, d_x=None, dy=FAKE,
              d_res=None, d_gate=None, dw=FAKE, dw_pre=None, ws=FAKE, nbytes=1 << 30, **d):
     return L.kda_block_norm_bwd(desc(**d), FAKE, FAKE, res, gate, w_pre, stats, d_out, d_x, dy,
