@@ -812,7 +812,8 @@ def _tokens(t, name, shape, dtype, device):
     st = t.stride()
     if st[2] != 1 and shape[2] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr(), st[0], st[1]
+    # the stride of a dimension of 1 means nothing
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
 
 
 @_on_its_stream
@@ -823,7 +824,8 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
 
     xbc: [B,T,H*P+2*G*N], z: [B,T,H*P] or None, dt: [B,T,H], all of one dtype
     (bf16 or fp32) and possibly slices of one projection (last dimension
-    contiguous); conv_w: [channels,4], conv_bias: [channels], A, D, dt_bias:
+    contiguous; xbc and z begin and lie on multiples of 16 bytes unless
+    ``impl="simt"``, which serves any place and width); conv_w: [channels,4], conv_bias: [channels], A, D, dt_bias:
     [H], all fp32; initial_state: [B,H,N,P] fp32; conv_state: [B,3,channels].
     Returns ``(y [B,T,H,P], final_state, conv_state_out)``, the last two None
     unless ``output_final_state``."""

@@ -379,13 +379,18 @@ kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt, 
     return KDA_ERR_INVALID_ARG;
   const size_t need = kda_ssm_fwd_workspace_size(s, impl);
   if (need == 0) return KDA_ERR_UNSUPPORTED;
-  for (const void *ptr : {xbc, z, (const void *)w, (const void *)initial_state, conv_state,
-                          (const void *)y, (const void *)final_state, (const void *)conv_out})
-    if (!aligned(ptr, 16)) return KDA_ERR_ALIGNMENT;
-  const int per16 = s->dtype == KDA_DTYPE_BF16 ? 8 : 4;
-  for (long long stride : {s->xbc_stride_b, s->xbc_stride_t, z ? s->z_stride_b : 0,
-                           z ? s->z_stride_t : 0})
-    if (stride % per16) return KDA_ERR_ALIGNMENT;
+  // the CUDA-core kernel reads single elements but for w; AUTO asks for what the
+  // tensor cores need at any size
+  if (!aligned(w, 16)) return KDA_ERR_ALIGNMENT;
+  if (impl != KDA_IMPL_SIMT) {
+    for (const void *ptr : {xbc, z, (const void *)initial_state, conv_state, (const void *)y,
+                            (const void *)final_state, (const void *)conv_out})
+      if (!aligned(ptr, 16)) return KDA_ERR_ALIGNMENT;
+    const int per16 = s->dtype == KDA_DTYPE_BF16 ? 8 : 4;
+    for (long long stride : {s->xbc_stride_b, s->xbc_stride_t, z ? s->z_stride_b : 0,
+                             z ? s->z_stride_t : 0})
+      if (stride % per16) return KDA_ERR_ALIGNMENT;
+  }
   if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return KDA_ERR_ALIGNMENT;
   SsmParams p;

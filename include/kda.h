@@ -539,8 +539,10 @@ typedef struct kda_ssm_shape {
  *                 device status word, see kda_read_device_status).
  * A value that is not finite reaches its own run from its token on, and the
  * final state if that run is the row's last; no other run, no earlier token.
- * xbc, z and the states are 16-byte aligned and the strides of xbc and z
- * multiples of 16 bytes (KDA_ERR_ALIGNMENT).  Asynchronous on `stream`.
+ * w is 16-byte aligned; for TC and AUTO also xbc, z, y and the states, and the
+ * strides of xbc and z are multiples of 16 bytes (KDA_ERR_ALIGNMENT): give a
+ * projection such a width, or ask for SIMT, which serves any.  Asynchronous
+ * on `stream`.
  */
 KDA_API size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape *s, kda_impl impl);
 KDA_API kda_status kda_ssm_fwd(const kda_ssm_shape *s, const void *xbc, const void *dt,

@@ -45,6 +45,14 @@ def test_ssm_fwd_strides_of_a_gate_that_is_absent_are_not_read(L):
     assert ssm_fwd(L, z=None, zs=(3, 5), nbytes=64) == 4
 
 
+def test_ssm_fwd_on_the_cuda_cores_needs_no_alignment(L):
+    odd = dict(xbc=FAKE + 2, z=FAKE + 6, s0=FAKE + 4, c0=FAKE + 2, y=FAKE + 2, fs=FAKE + 4,
+               co=FAKE + 2, xs=(40001, 517), zs=(40001, 517))
+    assert ssm_fwd(L, impl=kda.IMPLS["simt"], nbytes=64, **odd) == 4
+    assert ssm_fwd(L, impl=kda.IMPLS["simt"], nbytes=64, w=FAKE + 4) == 3
+    assert ssm_fwd(L, impl=kda.IMPLS["tc"], nbytes=64, **odd) == 3
+
+
 def ssm_step(L, xbc=FAKE, dt=FAKE, w=FAKE, A=FAKE, slots=None, n_slots=4, conv=FAKE, state=FAKE,
              y=FAKE, ws=FAKE, nbytes=1 << 20, **shape):
     return L.kda_ssm_step(ssm_shape(**dict(dict(T=1), **shape)), xbc, dt, None, w, None, A, None,

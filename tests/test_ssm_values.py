@@ -129,3 +129,29 @@ def test_caches_that_are_not_finite(dtype, impl, value):
         c.c0[i][1, 1, H * P + 9] = value
         c.c0[i][2, 2, 2 * P + 3] = value
     check(c, impl)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [200, 1])
+def test_slices_of_a_projection_of_any_width(dtype, T):
+    """3 heads: the slices begin and lie at odd places.  The CUDA cores serve
+    them; the strides of one token or one row mean nothing on either path."""
+    H, P, N = 3, 32, 64
+    c = Case(2, T, H, P, N, 1, dtype, init=True)
+    width = 2 * H * P + 2 * N + H
+    for i, to in enumerate((dtype, torch.float64)):
+        room = torch.zeros(2, T, width + 1, dtype=to)
+        room[..., 1:] = c.proj[i][..., :width]
+        c.proj = (*c.proj[:i], room[..., 1:], *c.proj[i + 1:])
+    c.check("simt")
+
+
+def test_strides_of_a_dimension_of_one_are_not_read():
+    import gated_delta_rule_21_gb300 as kda
+    c = Case(1, 1, 2, 32, 32, 1, torch.bfloat16)
+    x, dt, z = c.parts(c.proj[0].cuda())
+    w, A = c.w[0].cuda(), c.A[0].cuda()
+    want = kda.ssm_fwd(x, dt, w, A, head_dim=32, state_dim=32, z=z)[0]
+    x, z = (t.as_strided(t.shape, (7, 13, 1)) for t in (x, z))
+    got = kda.ssm_fwd(x, dt, w, A, head_dim=32, state_dim=32, z=z)[0]
+    assert torch.equal(got, want)
