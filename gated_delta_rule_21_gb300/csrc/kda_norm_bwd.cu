@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(BS) norm_bwd_kernel(const NormBwdParams q) {
       }
       float sum[3] = {total(acc0), total(acc1), total(acc2)};
       row_sum3(sum, tpr, red, slot);
-      const float kc = s2 * s2 * s2 * sum[0] * p.inv_d;   // s2 c2, times s2: r = v - kc m
+      // s2 c2, times s2: r = v - kc m (in this order: the cube of s2 may overflow)
+      const float kc = s2 * (s2 * (s2 * sum[0] * p.inv_d));
       const float c1 = (sum[1] - kc * sum[2]) * p.inv_d;
       const P nk = both<P>(-kc), nc = both<P>(-c1 * s1), ps1 = both<P>(s1), ps2 = both<P>(s2);
 #pragma unroll

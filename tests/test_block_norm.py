@@ -235,3 +235,12 @@ def test_another_stream_and_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [1e-14, 1e14])
+def test_outputs_of_any_size_before_the_second_norm(dtype, scale):
+    """The second norm takes the scale out again: gradients of size 1 from
+    statistics whose cube fp32 does not hold."""
+    dev, ref = make(21, 264, dtype, 21, False, True, seed=10)
+    check(dev, ref, dtype, "sigmoid", scale=scale, eps=0.0, d_out=False)
