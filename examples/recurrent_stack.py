@@ -90,10 +90,16 @@ class Stack:
     def _ssm_inputs(self, x):
         return (x @ self.proj).split([SSM_HEADS * SSM_DIM, self.channels, SSM_HEADS], -1)
 
+    def _workspace(self, rows):
+        """One for each stream that makes tokens of so many sequences."""
+        key = rows, torch.cuda.current_stream().cuda_stream
+        if key not in self.workspace:
+            self.workspace[key] = kda.alloc_step_workspace(rows, max(HEADS, SSM_HEADS))
+        return self.workspace[key]
+
     # -- one token per sequence: [B, WIDTH]; the states move on in place ------
     def token(self, h, states, slots=None):
-        ws = self.workspace.setdefault(
-            h.shape[0], kda.alloc_step_workspace(h.shape[0], max(HEADS, SSM_HEADS)))
+        ws = self._workspace(h.shape[0])
         x = self._enter(h)
         q, k, v, g, beta, z = self._delta_inputs(x)
         o = kda.step(q, k, v, g, beta, states["delta"], slots=slots, conv_w=self.conv_w,

@@ -21,3 +21,30 @@ def test_recurrent_stack():
     spec.loader.exec_module(mod)
     assert mod.compare() < 2e-2
     assert mod.compare(batch=1, length=3, tokens=3, seed=5) < 2e-2
+
+
+def load(name):
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "examples", name + ".py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_tokens_share_a_workspace_per_stream(monkeypatch):
+    import torch
+    mod = load("recurrent_stack")
+    made = []
+    alloc = mod.kda.alloc_step_workspace
+    monkeypatch.setattr(mod.kda, "alloc_step_workspace", lambda *a: made.append(a) or alloc(*a))
+    stack = mod.Stack()
+    h = torch.randn(3, 8, mod.WIDTH, device="cuda").bfloat16()
+    _, _, states = stack.prompt(h)
+    for _ in range(3):
+        stack.token(h[:, 0].contiguous(), states)
+    assert len(made) == 1
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        stack.token(h[:, 0].contiguous(), states)
+    side.synchronize()
+    assert len(made) == 2
