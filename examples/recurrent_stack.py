@@ -70,11 +70,14 @@ class Stack:
     def _enter(self, h):
         return kda.block_norm(h, self.norms[0])[0]
 
-    # -- a prompt: [B, T, WIDTH], T >= 3 ---------------------------------------
+    # -- a prompt: [B, T, WIDTH] ------------------------------------------------
     def prompt(self, h):
         x = self._enter(h)
         q, k, v, g, beta, z = self._delta_inputs(x)
         raw = torch.cat([t.flatten(-2) for t in (q, k, v)], -1)
+        # the convolution goes on from the last three inputs, zeros before the prompt
+        # (a row of several sequences or with padding has them elsewhere)
+        conv = torch.nn.functional.pad(raw, (0, 0, 3, 0))[:, -3:].contiguous()
         q, k, v = kda.short_conv_silu(q.contiguous(), k.contiguous(), v.contiguous(),
                                       self.conv_w, l2norm_qk=True)
         o, state = kda.chunk_fwd(q, k, v, g, beta, output_final_state=True)
@@ -84,8 +87,7 @@ class Stack:
             xbc, dt, self.ssm_conv, self.A, head_dim=SSM_DIM, state_dim=STATES,
             dt_bias=self.dt_bias, D=self.D, z=zz, output_final_state=True)
         h, x = self._around(1, y.flatten(-2) @ self.ssm_out, h)
-        return x, h, {"delta": state, "delta_conv": raw[:, -3:].contiguous(), "ssm": ssm_state,
-                      "ssm_conv": ssm_conv}
+        return x, h, {"delta": state, "delta_conv": conv, "ssm": ssm_state, "ssm_conv": ssm_conv}
 
     def _ssm_inputs(self, x):
         return (x @ self.proj).split([SSM_HEADS * SSM_DIM, self.channels, SSM_HEADS], -1)

@@ -754,7 +754,9 @@ def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_stat
     the cache (None: its row; a place outside the cache marks an idle
     sequence, whose output is 0).  With ``conv_w`` (as short_conv_silu) and
     ``conv_state`` [n_slots,3,H*(2K+V)] (moved on in place) q, k, v are the
-    inputs of the convolution.  Returns o [B,H,V]."""
+    inputs of the convolution; after a prompt it holds the last three inputs of
+    short_conv_silu of each sequence, zeros where there were fewer.  Returns o
+    [B,H,V]."""
     dev, dt = _start(q, "step")
     B, H, K = q.shape
     V = v.shape[-1]

@@ -30,6 +30,11 @@ def load(name):
     return mod
 
 
+@pytest.mark.parametrize("length", [1, 2])
+def test_prompts_shorter_than_the_convolution(length):
+    assert load("recurrent_stack").compare(batch=2, length=length, tokens=4, seed=6) < 2e-2
+
+
 def test_tokens_share_a_workspace_per_stream(monkeypatch):
     import torch
     mod = load("recurrent_stack")
