@@ -907,6 +907,13 @@ def _norm_desc(y, gate, gate_act, scale, eps):
         if gate.shape[-1] != D or grows == 0 or rows % grows:
             raise ValueError(
                 f"gate {tuple(gate.shape)} does not divide the rows of {tuple(y.shape)}")
+        if grows != rows and gate.dim() == y.dim():
+            # [1, T, D] beside [B, T, D] would serve other rows than broadcasting does
+            g, n = gate.shape[:-1], y.shape[:-1]
+            k = next(i for i in range(len(n)) if g[i] != n[i])
+            if g[k] == 1 and any(v != 1 for v in g[k:]):
+                raise ValueError(f"gate {tuple(gate.shape)} does not serve consecutive rows of "
+                                 f"{tuple(y.shape)}")
     act = GATE_ACTS.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}, got {gate_act!r}")
@@ -922,7 +929,7 @@ def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale
 
     y, residual: [..., D] (bf16 or fp32, contiguous); gate: [..., D] with as
     many rows as y, or fewer that divide them (each then serves as many
-    consecutive rows); w_post, w_pre: [D] fp32.  residual, gate and w_pre may be
+    consecutive rows: [B, 1, D] beside [B, T, D], not [1, T, D]); w_post, w_pre: [D] fp32.  residual, gate and w_pre may be
     None.  ``out`` may be the residual itself, but not with ``save_stats``:
     block_norm_bwd reads the residual.  Returns ``(out, x or None)``, and the
     statistics block_norm_bwd reads when ``save_stats``."""

@@ -147,3 +147,19 @@ def test_python_checks_come_before_the_library():
     with pytest.raises(ValueError, match="CUDA"):
         kda.step(cpu[None], cpu[None], cpu[None], cpu[None], cpu, cpu)
     assert ctypes.sizeof(kda.kda_ssm_shape) == 80 and ctypes.sizeof(kda.kda_norm_desc) == 40
+
+
+def test_a_gate_that_is_broadcast_over_leading_rows_is_refused():
+    """Each gate row serves consecutive rows: [B,1,D] and [1,1,D] beside
+    [B,T,D] are what broadcasting means, [1,T,D] is not; [B,T/2,D] can only
+    mean consecutive rows."""
+    y = torch.zeros(2, 6, 8)
+    for shape in ((2, 6, 8), (2, 1, 8), (1, 1, 8), (2, 3, 8), (2, 8), (4, 8), (1, 8), (8,)):
+        kda._norm_desc(y, torch.zeros(shape), "silu", 1.0, 1e-6)
+    for shape in ((1, 6, 8), (1, 2, 8)):
+        with pytest.raises(ValueError, match="consecutive"):
+            kda._norm_desc(y, torch.zeros(shape), "silu", 1.0, 1e-6)
+    kda._norm_desc(torch.zeros(12, 8), torch.zeros(4, 8), "silu", 1.0, 1e-6)
+    with pytest.raises(ValueError, match="consecutive"):
+        kda._norm_desc(torch.zeros(2, 3, 4, 8), torch.zeros(2, 1, 4, 8), "silu", 1.0, 1e-6)
+    kda._norm_desc(torch.zeros(2, 3, 4, 8), torch.zeros(2, 3, 1, 8), "silu", 1.0, 1e-6)
