@@ -14,10 +14,12 @@
 //   3. ssm_out_kernel: y of every (block, head), all in parallel.
 //
 // Rounding.  The final state is carried to tokens and on, so S' is formed to
-// fp32 grade: B and the scaled x are each split into two bf16 parts (16 bits of
-// each), all four products are added and S is updated in fp32 registers, never
-// in the accumulator: 3.4e-6 of the state's norm off, either type.  With bf16
-// inputs y is rounded to bf16 at the end and its products' operands (C, B, x, S
+// fp32 grade: B and the scaled x are each split into two fp16 parts, scaled by
+// powers of two for each few channels of a block (22 bits of what is not 2^18 times
+// smaller than the largest), all four products are added and S is updated in fp32
+// registers, never in the accumulator: 1.5e-7 of the state's norm off, either type,
+// as fp32 arithmetic is (two bf16 parts: 3.4e-6, and 24 us less of the 330 below).
+// With bf16 inputs y is rounded to bf16 at the end and its products' operands (C, B, x, S
 // and the 128 x 128 matrix of factors) are bf16 too; their errors are of y's own
 // rounding's size and average out over the sums (2.6e-3 in all; y's own rounding
 // alone is 1.7e-3).  With fp32 inputs these operands are split in two as well
@@ -30,6 +32,7 @@
 // SMs, each its convolution's instructions and two barriers long; the other two
 // are at the rate of their instructions and of exp2 and reciprocals.  (The
 // first kernels of this form took 9.8 and 9.5 ms on the CUDA cores.)
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include <type_traits>
@@ -62,14 +65,18 @@ constexpr int kConv = 512;         // threads that run the convolution of x
 // What the kernels hand to one another, in the workspace.
 struct TcBufs {
   int nb;                          // blocks per row
-  unsigned char *bhi, *blo, *ct;   // [B][nb][G] tiles (slot, state), op_off(slot, n, N)
+  unsigned char *bhi, *blo;        // [B][nb][G] tiles (slot, state), op_off(slot, n, N): B
+                                   // in two scaled fp16 parts, for the state
+  unsigned char *bt, *ct;          // likewise B and C in bf16, for y
   unsigned char *xt;               // [B][nb][H] tiles of x, mn_off(p, slot, 128)
   unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
-  unsigned char *clo, *xlo, *slo;  // fp32 inputs: the second parts of ct, xt and st
+  unsigned char *btlo, *clo, *xlo, *slo;  // fp32 inputs: the second parts of bt, ct, xt, st
+  float *binv;                     // [B][nb][G][N]: what 1 in bhi and blo stands for
   float *ein, *cum, *cumj;         // [B][H][nb * 128] by slot, see prep_factors
   float *cum_lo, *cumj_lo;         // fp32 inputs: what cum and cumj leave of the sums
   float *wst;                      // likewise, by token
-  float *dec;                      // [B][H][nb]: e^{c_127}, or -1: the block resets the state
+  float2 *dec;                     // [B][H][nb]: e^{c_127}, or -1: the block resets the state;
+                                   // what 1 in wst stands for
   int *run;                        // [B][nb * 128] by slot: resets so far in the block, -1: padding
   unsigned char *tok;              // [B][nb * 128] by token: token_mark
   int *flags;                      // [B][nb]: kPlain, kResets
@@ -91,9 +98,12 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->nb = nb;
   t->bhi = take(bt * p.G * kQ * p.N * 2);
   t->blo = take(bt * p.G * kQ * p.N * 2);
+  t->bt = take(bt * p.G * kQ * p.N * 2);
   t->ct = take(bt * p.G * kQ * p.N * 2);
+  t->binv = (float *)take(bt * p.G * p.N * 4);
   t->xt = take(bt * p.H * kQ * p.P * 2);
   t->st = take(bt * p.H * p.N * p.P * 2);
+  t->btlo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
   t->clo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
   t->xlo = take(f32 ? bt * p.H * kQ * p.P * 2 : 0);
   t->slo = take(f32 ? bt * p.H * p.N * p.P * 2 : 0);
@@ -103,7 +113,7 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->wst = (float *)take(toks * p.H * 4);
   t->cum = (float *)take(toks * p.H * 4);
   t->cumj = (float *)take(toks * p.H * 4);
-  t->dec = (float *)take(bt * p.H * 4);
+  t->dec = (float2 *)take(bt * p.H * 8);
   t->run = (int *)take(toks * 4);
   t->tok = take(toks);
   t->flags = (int *)take(bt * 4);
@@ -118,6 +128,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool o
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -129,6 +142,12 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^k with `bound` / 2^k in [2^14, 2^15), as far as 2^k and its inverse are normal.
+__device__ __forceinline__ float to_2p15(float bound) {
+  const int e = (int)(__float_as_uint(bound) >> 23 & 255u) - 14;
+  return __uint_as_float((uint32_t)min(max(e, 14), 240) << 23);
 }
 
 // ---------------------------------------------------------------------------
@@ -171,8 +190,10 @@ struct Conv {
   }
 
   u64 wt[kSsmTaps][E], bias[E];
+  float gain, base;     // |u| <= gain max|x| + base: sums of |w|, |bias| of the channels
 
   __device__ __forceinline__ void weights(const SsmParams &p, int channel) {
+    gain = base = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float4 a = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)(channel + 2 * i));
@@ -181,7 +202,12 @@ struct Conv {
       wt[1][i] = pk2(a.y, b.y);
       wt[2][i] = pk2(a.z, b.z);
       wt[3][i] = pk2(a.w, b.w);
-      bias[i] = p.bias ? pk2(p.bias[channel + 2 * i], p.bias[channel + 2 * i + 1]) : pk2(0.f, 0.f);
+      const float b0 = p.bias ? p.bias[channel + 2 * i] : 0.f,
+                  b1 = p.bias ? p.bias[channel + 2 * i + 1] : 0.f;
+      bias[i] = pk2(b0, b1);
+      gain = fmaxf(gain, fmaxf(fabsf(a.x) + fabsf(a.y) + fabsf(a.z) + fabsf(a.w),
+                               fabsf(b.x) + fabsf(b.y) + fabsf(b.z) + fabsf(b.w)));
+      base = fmaxf(base, fmaxf(fabsf(b0), fabsf(b1)));
     }
   }
 
@@ -221,22 +247,51 @@ struct Conv {
     cp_async_commit();
   }
 
-  // f(i, u): u = SiLU(conv) of channels [CH warp, CH (warp + 1)) of the tile
-  // at the lane's i-th token, 4 lane + i.  CUT: windows end where a run
+  // f(i, u, inv): u inv = SiLU(conv) of channels [CH warp, CH (warp + 1)) of the
+  // tile at the lane's i-th token, 4 lane + i.  CUT: windows end where a run
   // starts, and padding gives 0; tok holds the tokens' windows.
+  //
+  // inv is 1, or with `scaled` a power of two that keeps |u| of the warp's channels
+  // and the block's tokens below 2^15, by the largest finite input: what u is in
+  // fp16 then has 11 bits, and two parts of it 22, down to 2^-29 of the largest.
+  // The scale costs no instruction per value (1 / (1 + e) is made with it).
+  // Returns inv.
   template <bool CUT, typename F>
-  __device__ __forceinline__ void run(const unsigned char *rows, int warp, int lane,
-                                      const unsigned char *tok, F f) const {
+  __device__ __forceinline__ float run(const unsigned char *rows, int warp, int lane,
+                                       const unsigned char *tok, bool scaled, F f) const {
     const int at = warp * CH * (int)sizeof(T);
     // rows 4 lane .. 4 lane + 6: two permutations
     const unsigned char *lo = rows + off(4 * lane, at / 16) + at % 16;
     const unsigned char *hi = rows + off(4 * lane + 4, at / 16) + at % 16;
-    u64 x[kStrip + kSsmTaps - 1][E];
-#pragma unroll
-    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i)
-      unpack(*reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes),
-             x[i]);
     const uint32_t marks = CUT ? *reinterpret_cast<const uint32_t *>(tok + 4 * lane) : 0;
+    uint32_t live = 0x7f;                 // rows that a token's window holds
+    if (CUT && scaled) {
+      live = 0;
+#pragma unroll
+      for (int i = 0; i < kStrip; ++i) {
+        const int k = marks >> (8 * i), place = k & 3;
+        if (k & 8) live |= ((2u << place) - 1) << (i + 3 - place);
+      }
+    }
+    u64 x[kStrip + kSsmTaps - 1][E];
+    uint32_t top = 0, top2 = 0;           // of |x|: a float's bits, or two bf16
+#pragma unroll
+    for (int i = 0; i < kStrip + kSsmTaps - 1; ++i) {
+      const Raw r =
+          *reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes);
+      unpack(r, x[i]);
+      if (scaled && (live >> i & 1)) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
+        constexpr int kWords = (int)sizeof(Raw) / 4;
+#pragma unroll
+        for (int e = 0; e < kWords; e += 2) {
+          top = larger(top, w[e]);
+          if (e + 1 < kWords) top2 = larger(top2, w[e + 1]);
+        }
+      }
+    }
+    const float inv = scaled ? fit(larger(top, top2), lo, hi, live) : 1.f;
+    const u64 one = pk2(inv, inv);
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
       u64 u[E];
@@ -249,26 +304,59 @@ struct Conv {
           a[1][e] = place >= 2 ? x[i + 1][e] : 0;
           a[2][e] = place >= 1 ? x[i + 2][e] : 0;
         }
-        taps(a[0], a[1], a[2], x[i + 3], u);
+        taps(a[0], a[1], a[2], x[i + 3], one, u);
 #pragma unroll
         for (int e = 0; e < E; ++e) u[e] = k & 8 ? u[e] : 0;
       } else {
-        taps(x[i], x[i + 1], x[i + 2], x[i + 3], u);
+        taps(x[i], x[i + 1], x[i + 2], x[i + 3], one, u);
       }
-      f(i, u);
+      f(i, u, inv);
     }
+    return inv;
   }
 
  private:
+  // inv for the largest |x| of the warp: top, or where that is not finite what the
+  // live rows hold.
+  __device__ __forceinline__ float fit(uint32_t top, const unsigned char *lo,
+                                       const unsigned char *hi, uint32_t live) const {
+    if (sizeof(T) == 2) top = max(top << 16, top & 0xffff0000u);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (top >= 0x7f800000u) {
+      top = 0;
+#pragma unroll 1
+      for (int i = 0; i < kStrip + kSsmTaps - 1; ++i) {
+        u64 x[E];
+        unpack(*reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes),
+               x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t a = (uint32_t)x[e] & 0x7fffffffu, b = (uint32_t)(x[e] >> 32) & 0x7fffffffu;
+          if (live >> i & 1)
+            top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+    }
+    return to_2p15(fmaf(gain, __uint_as_float(top), base));
+  }
+  // The larger magnitudes: bits of a float, or two bf16.  NaN loses or comes out
+  // above every number.
+  static __device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t w) {
+    if (sizeof(T) == 4) return max(m, w & 0x7fffffffu);
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
+                                     __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  }
   __device__ __forceinline__ void taps(const u64 (&a)[E], const u64 (&b)[E], const u64 (&c)[E],
-                                       const u64 (&x)[E], u64 (&u)[E]) const {
+                                       const u64 (&x)[E], u64 one, u64 (&u)[E]) const {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const u64 v = fma2(wt[0][i], a[i],
                          fma2(wt[1][i], b[i], fma2(wt[2][i], c[i], fma2(wt[3][i], x[i], bias[i]))));
       float e0, e1, d0, d1;
       upk2(mul2(v, pk2(-kLog2e, -kLog2e)), e0, e1);
-      upk2(add2(pk2(1.f, 1.f), pk2(ex2(e0), ex2(e1))), d0, d1);
+      upk2(fma2(pk2(ex2(e0), ex2(e1)), one, one), d0, d1);
       u[i] = mul2(v, pk2(rcp(d0), rcp(d1)));
     }
   }
@@ -299,6 +387,20 @@ __device__ __forceinline__ void split(const u64 (&v)[E], R &hi, R &lo) {
     rest[i] = fma2(pk2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)),
                    pk2(-1.f, -1.f), v[i]);
   lo = pack<R>(rest);
+}
+// Pairs as two parts in fp16.
+template <typename R, int E>
+__device__ __forceinline__ void split16(const u64 (&v)[E], R &hi, R &lo) {
+  __half2 *h = reinterpret_cast<__half2 *>(&hi), *l = reinterpret_cast<__half2 *>(&lo);
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    float a, b;
+    upk2(v[i], a, b);
+    h[i] = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h[i]);
+    upk2(fma2(pk2(f.x, f.y), pk2(-1.f, -1.f), v[i]), a, b);
+    l[i] = __floats2half2_rn(a, b);
+  }
 }
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
@@ -354,7 +456,7 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 //   ein  = 2^cum where the entering state reaches the token, else 0
 //   wst  = d 2^(sum of a after the token) where the token reaches the state
 //          that leaves the block, else -0 (summed from the end: exact where
-//          it matters)
+//          it matters); over a power of two that leaves the largest below 1
 // A warp takes a head, a lane 4 tokens.  For fp32 inputs the sums up to a token
 // are made and kept in two floats: a factor e^(c_r - c_j) is as exact as the
 // difference, however far the sums have run.  (64-bit sums took 40 us.)  For bf16
@@ -362,6 +464,12 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 // 6e-5 each at kWide.  Beyond it the sums are made in two floats and rounded
 // once, and a token's a counts down to kFar only: the sum stays above -2^15, one
 // step is 2^-9 and a factor off by 1.4e-3 at most, less than half a step of bf16.
+// The largest finite width of four.
+__device__ __forceinline__ float finite_max(const float4 &w) {
+  auto in = [](float v) { return v > 0.f && v < CUDART_INF_F ? v : 0.f; };
+  return fmaxf(fmaxf(in(w.x), in(w.y)), fmaxf(in(w.z), in(w.w)));
+}
+
 constexpr float kFar = -256.f;     // 2^kFar is 0 beside any fp32 value, as 2^a below it is
 constexpr float kWide = 1024.f;
 template <typename T>
@@ -485,10 +593,14 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
         }
         fw[i] = run == last ? d[i] * exp2f(suf[i] + after) : -0.f;
       }
-      *reinterpret_cast<float4 *>(t.wst + at + lane * 4) = wst;
+      const float winv = 32768.f * to_2p15(__uint_as_float(__reduce_max_sync(
+                                       0xffffffffu, __float_as_uint(finite_max(wst)))));
+      const float scale = __uint_as_float((254u << 23) - __float_as_uint(winv));
+      *reinterpret_cast<float4 *>(t.wst + at + lane * 4) =
+          make_float4(wst.x * scale, wst.y * scale, wst.z * scale, wst.w * scale);
       if (lane == 0)
         t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] =
-            last == 0 ? exp2f(total) : -1.f;
+            make_float2(last == 0 ? exp2f(total) : -1.f, winv);
     }
   }
 }
@@ -501,12 +613,11 @@ using PrepConv = Conv<T, TP, kPrepCh<T>, TP / kPrepCh<T> * 32>;
 
 // The convolution of TP channels of B or C of the blocks [blk, end) into their
 // operand tiles, the next block's rows on their way.
-template <typename T, int TP>
+template <typename T, int TP, bool is_c>
 __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, int b, int blk,
                                           int end, int g, int part, unsigned char *smem) {
   const int tid = threadIdx.x;
-  const bool is_c = part >= p.N / TP;
-  const int n0 = (is_c ? part - p.N / TP : part) * TP;
+  const int n0 = part * TP;
   const int ch = p.H * p.P + (is_c ? p.G * p.N : 0) + g * p.N + n0;
   const SsmRow row = row_of(p, b);
   const T *past = past_of<T>(p, b);
@@ -523,7 +634,6 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   stage(blk);
   Cv cv;
   if (mine) cv.weights(p, ch + wch);
-  const bool two = !is_c || sizeof(T) == 4;
   for (; blk < end; ++blk) {
     // whether any token's window leaves the staged rows
     unsigned char *stok = smem + 2 * Cv::kBytes + (blk & 1) * kQ;
@@ -541,16 +651,26 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
     const size_t tile = (((size_t)b * t.nb + blk) * p.G + g) * kQ * p.N * 2 +
                         (size_t)(lane >> 3) * 4 * p.N * 16 + (lane & 7) * 16 +
                         (n0 + wch) / 8 * 128 + wch % 8 * 2;
-    unsigned char *hi_tile = (is_c ? t.ct : t.bhi) + tile, *lo_tile = (is_c ? t.clo : t.blo) + tile;
-    auto put = [&](int i, u64(&u)[Cv::E]) {
+    auto put = [&](int i, u64(&u)[Cv::E], float inv) {
+      const size_t o = tile + (size_t)i * p.N * 16;
       Out hi, lo;
+      if (!is_c) {
+        split16(u, hi, lo);
+        *reinterpret_cast<Out *>(t.bhi + o) = hi;
+        *reinterpret_cast<Out *>(t.blo + o) = lo;
+#pragma unroll
+        for (int e = 0; e < Cv::E; ++e) u[e] = mul2(u[e], pk2(inv, inv));
+      }
       split(u, hi, lo);
-      *reinterpret_cast<Out *>(hi_tile + (size_t)i * p.N * 16) = hi;
-      if (two) *reinterpret_cast<Out *>(lo_tile + (size_t)i * p.N * 16) = lo;
+      *reinterpret_cast<Out *>((is_c ? t.ct : t.bt) + o) = hi;
+      if (sizeof(T) == 4) *reinterpret_cast<Out *>((is_c ? t.clo : t.btlo) + o) = lo;
     };
     const unsigned char *rows = smem + (blk & 1) * Cv::kBytes;
-    if (plain) cv.template run<false>(rows, warp, lane, stok, put);
-    else cv.template run<true>(rows, warp, lane, stok, put);
+    const float inv =
+        plain ? cv.template run<false>(rows, warp, lane, stok, !is_c, put)
+              : cv.template run<true>(rows, warp, lane, stok, !is_c, put);
+    if (!is_c && lane < kPrepCh<T>)
+      t.binv[(((size_t)b * t.nb + blk) * p.G + g) * p.N + n0 + wch + lane] = inv;
   }
 }
 
@@ -590,7 +710,10 @@ __global__ void __launch_bounds__(kPrep, 2)
     const int g = u % p.G;
     u /= p.G;
     const int blk = u % runs * run;
-    prep_conv<T, TP>(p, t, u / runs, blk, min(blk + run, t.nb), g, part, smem);
+    if (part < p.N / TP)
+      prep_conv<T, TP, false>(p, t, u / runs, blk, min(blk + run, t.nb), g, part, smem);
+    else
+      prep_conv<T, TP, true>(p, t, u / runs, blk, min(blk + run, t.nb), g, part - p.N / TP, smem);
     return;
   }
   u -= tiles;
@@ -625,8 +748,13 @@ struct StateSmem {
   static constexpr uint32_t kBBytes = 2 * kQ * 128 * 2;
   static constexpr uint32_t kRows = kB + 2 * kBBytes;               // 2 staged tiles of x
   static constexpr uint32_t kW = kRows + 2 * Cv::kBytes;      // 2 x wst
-  static constexpr uint32_t kBar = kW + 2 * kQ * 4;
-  static constexpr uint32_t kBytes = kBar + 64;
+  static constexpr uint32_t kXinv = kW + 2 * kQ * 4;          // 2 x [16]: 1 in kX, by warp
+  static constexpr uint32_t kBinv = kXinv + 2 * 16 * 4;       // 2 x [128]: 1 in kB, by row
+  static constexpr uint32_t kDec = kBinv + 2 * 128 * 4;       // 2 x dec
+  static constexpr uint32_t kBar = kDec + 2 * 8;
+  static constexpr uint32_t kTmem = kBar + 48;
+  static constexpr uint32_t kBytes = kTmem + 16;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Whether a token's wst says that its run ends before the block does.
@@ -646,13 +774,13 @@ __device__ __forceinline__ void tokens_of_state(const unsigned char *x, const un
   for (int j = 0; j < kQ; ++j) {
     if (ends_before(f[token_of(j)])) continue;
     const uint32_t o = op_off(j, n, N);
-    const float b = __bfloat162float(*reinterpret_cast<const bf16 *>(bhi + o)) +
-                    __bfloat162float(*reinterpret_cast<const bf16 *>(blo + o));
+    const float b = __half2float(*reinterpret_cast<const __half *>(bhi + o)) +
+                    __half2float(*reinterpret_cast<const __half *>(blo + o));
 #pragma unroll
     for (int k = 0; k < COLS; ++k) {
       const unsigned char *v = x + mn_off(k, j, kQ);
-      add[k] = fmaf(b, __bfloat162float(*reinterpret_cast<const bf16 *>(v)) +
-                           __bfloat162float(*reinterpret_cast<const bf16 *>(v + TP / 8 * 2048)),
+      add[k] = fmaf(b, __half2float(*reinterpret_cast<const __half *>(v)) +
+                           __half2float(*reinterpret_cast<const __half *>(v + TP / 8 * 2048)),
                     add[k]);
     }
   }
@@ -675,14 +803,13 @@ __global__ void __launch_bounds__(kConv + 32, 1)
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kCols = TP / 4;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint32_t s_tmem;
   const uint32_t sb = smem_u32(smem);
   const uint32_t bar_x = sb + L::kBar, bar_b = bar_x + 16, bar_d = bar_x + 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = p.P / TP, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % p.H, b = bh / p.H, g = h / (p.H / p.G), c0 = tile * TP;
   const int nb = t.nb, N = p.N;
-  if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 4 * TP);
+  if (warp == 0) tmem_alloc(sb + L::kTmem, 4 * TP);
   if (tid == 0) {
     mbar_init(bar_x, kConv);
     mbar_init(bar_x + 8, kConv);
@@ -695,7 +822,7 @@ __global__ void __launch_bounds__(kConv + 32, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
   start_next();
 
   if (warp == kConv / 32) {
@@ -723,8 +850,8 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         const uint32_t bt = sb + L::kB + (i & 1) * L::kBBytes;
         const Opnd x = {sb + L::kX + (i & 1) * L::kXBytes, 128, kQ * 16};
         const Opnd bh_ = {bt, (uint32_t)N * 16, 128}, bl_ = {bt + tb, (uint32_t)N * 16, 128};
-        mma_k(d, bh_, 1, x, 1, kQ / 16, 2 * TP, false);
-        mma_k(d, bl_, 1, x, 1, kQ / 16, 2 * TP, true);
+        mma_k<true>(d, bh_, 1, x, 1, kQ / 16, 2 * TP, false);
+        mma_k<true>(d, bl_, 1, x, 1, kQ / 16, 2 * TP, true);
         mma_commit(bar_d + 8u * (i & 1));
         ++issued;
         if (i > 0 && loaded < nb) {      // block i - 1's tiles are free once it is done
@@ -747,7 +874,8 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
     const T *before = past ? past + ch : nullptr;
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
-    const float *dec = t.dec + ((size_t)b * p.H + h) * nb;
+    const float2 *dec = t.dec + ((size_t)b * p.H + h) * nb;
+    const float *binv = t.binv + ((size_t)b * nb * p.G + g) * N;
     Cv cv;
     const int wch = warp * (TP / 16);
     cv.weights(p, ch + wch);
@@ -768,14 +896,30 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     auto stage = [&](int i) {
       if (i < nb) {
         if (tid < kQ / 4)
-          cp_async16(sb + L::kW + (i & 1) * kQ * 4 + tid * 16, wst + (size_t)i * kQ + tid * 4, true);
+          cp_async16(sb + L::kW + (i & 1) * kQ * 4 + tid * 16, wst + (size_t)i * kQ + tid * 4);
         Cv::stage(sb + L::kRows + (i & 1) * Cv::kBytes, x, p.xbc_st, before, p.channels, i * kQ,
                   p.T, first, tid);
       }
     };
+    // what finish(i) needs (a block later than the rows, in the place of block i - 2)
+    auto stage_finish = [&](int i) {
+      if (tid >= kConv - N / 4) {
+        const int k = (tid - (kConv - N / 4)) * 4;
+        cp_async16(sb + L::kBinv + (i & 1) * 512 + k * 4, binv + (size_t)i * p.G * N + k);
+      }
+      if (tid == 0) cp_async8(sb + L::kDec + (i & 1) * 8, dec + i);
+      cp_async_commit();
+    };
     bool bad = false;
     // the state after block i, once its products are done
-    auto finish = [&](int i, float a) {
+    auto finish = [&](int i) {
+      const float2 d = *reinterpret_cast<const float2 *>(smem + L::kDec + (i & 1) * 8);
+      float a = d.x;
+      // the columns are those that four warps convolve
+      const float4 xi = *reinterpret_cast<const float4 *>(
+          smem + L::kXinv + ((i & 1) * 16 + col0 / (TP / 16)) * 4);
+      const float bi =
+          d.y * *reinterpret_cast<const float *>(smem + L::kBinv + (i & 1) * 512 + (n & (N - 1)) * 4);
       if (n < N) {
         const size_t at = ((((size_t)b * nb + i) * p.H + h) * N) * p.P * 2 +
                           (size_t)((c0 + col0) / 8) * N * 16 + (n >> 3) * 128 + (n & 7) * 16;
@@ -829,21 +973,26 @@ __global__ void __launch_bounds__(kConv + 32, 1)
                               t.blo + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
                               wst + (size_t)i * kQ, n, N, add);
       }
+      const float inv[4] = {bi * xi.x, bi * xi.y, bi * xi.z, bi * xi.w};
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) s[k] = fmaf(a, s[k], add[k]);
+      for (int k = 0; k < kCols; k += 2) {
+        const float v = inv[k / (kCols / 4)];
+        const u64 r = fma2(pk2(a, a), pk2(s[k], s[k + 1]),
+                           mul2(pk2(v, v), pk2(add[k], add[k + 1])));
+        upk2(r, s[k], s[k + 1]);
+      }
       tc_fence_before();
     };
     stage(0);
-    // the next block's flags and this and the last block's decay, loaded early
+    // the next block's flags, loaded early
     int flags = IDS ? t.flags[(size_t)b * nb] : kPlain, flags_next = kPlain;
-    float a_prev = 0.f, a_now = dec[0];
     int i = 0;
     for (; i < nb; ++i, flags = flags_next) {
       cp_async_wait_all();
       if (any_of_conv(bad)) break;   // a wait ran out somewhere: all leave
+      stage_finish(i);
       stage(i + 1);
       if (IDS) flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
-      const float a_next = i + 1 < nb ? dec[i + 1] : 0.f;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
       // the lane's i-th token: slot 8 i + lane % 8 of quarter lane / 8
       using Out = Word<2 * (TP / 16)>;
@@ -853,13 +1002,16 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       const size_t xt = (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
                         (size_t)(c0 / 8) * 2048 + at;
       const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * lane);
-      auto put = [&](int k, u64(&u)[Cv::E], bool cut) {
+      auto put = [&](int k, u64(&u)[Cv::E], float inv, bool cut) {
         Out hi, lo;
+        u64 v[Cv::E];
+#pragma unroll
+        for (int e = 0; e < Cv::E; ++e) v[e] = mul2(u[e], pk2(inv, inv));
         if constexpr (kF32) {
-          split(u, hi, lo);
+          split(v, hi, lo);
           *reinterpret_cast<Out *>(t.xlo + xt + k * 128) = lo;
         } else {
-          hi = pack<Out>(u);
+          hi = pack<Out>(v);
         }
         *reinterpret_cast<Out *>(t.xt + xt + k * 128) = hi;
         const float f = k == 0 ? w4.x : k == 1 ? w4.y : k == 2 ? w4.z : w4.w;
@@ -869,29 +1021,30 @@ __global__ void __launch_bounds__(kConv + 32, 1)
           // a token that does not reach the state adds nothing, whatever it holds
           if (cut && ends_before(f)) u[e] = pk2(0.f, 0.f);
         }
-        split(u, hi, lo);
+        split16(u, hi, lo);
         *reinterpret_cast<Out *>(xo + k * 128) = hi;
         *reinterpret_cast<Out *>(xo + TP / 8 * 2048 + k * 128) = lo;
       };
       const unsigned char *rows = smem + L::kRows + (i & 1) * Cv::kBytes;
       const unsigned char *tok = t.tok + ((size_t)b * nb + i) * kQ;
-      if (!IDS || (flags & kPlain))
-        cv.template run<false>(rows, warp, lane, tok,
-                               [&](int k, u64(&u)[Cv::E]) { put(k, u, false); });
-      else
-        cv.template run<true>(rows, warp, lane, tok,
-                              [&](int k, u64(&u)[Cv::E]) { put(k, u, true); });
+      const float inv =
+          !IDS || (flags & kPlain)
+              ? cv.template run<false>(
+                    rows, warp, lane, tok, true,
+                    [&](int k, u64(&u)[Cv::E], float v) { put(k, u, v, false); })
+              : cv.template run<true>(
+                    rows, warp, lane, tok, true,
+                    [&](int k, u64(&u)[Cv::E], float v) { put(k, u, v, true); });
+      if (lane == 0) reinterpret_cast<float *>(smem + L::kXinv)[(i & 1) * 16 + warp] = inv;
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
-      if (i > 0) finish(i - 1, a_prev);
-      a_prev = a_now;
-      a_now = a_next;
+      if (i > 0) finish(i - 1);
     }
     cp_async_wait_all();
     if (i == nb) {
-      if (IDS) any_of_conv(false);   // x of the last block, which finish may read
-      finish(nb - 1, a_prev);
+      any_of_conv(false);            // what the other threads made of the last block's x
+      finish(nb - 1);
     }
     if (p.final_state && n < N) {
 #pragma unroll
@@ -1014,10 +1167,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     const size_t o = (((size_t)b * nb + blk) * p.G + g) * tile;
     mbar_expect_tx(bar_cb, 2 * tile * L::kParts);
     bulk_load(sb + L::kC, t.ct + o, tile, bar_cb);
-    bulk_load(sb + L::kF, t.bhi + o, tile, bar_cb);
+    bulk_load(sb + L::kF, t.bt + o, tile, bar_cb);
     if (kF32) {
       bulk_load(sb + L::kC + L::kPart, t.clo + o, tile, bar_cb);
-      bulk_load(sb + L::kF + L::kPart, t.blo + o, tile, bar_cb);
+      bulk_load(sb + L::kF + L::kPart, t.btlo + o, tile, bar_cb);
     }
     load_s(n_s++);
     load_x(n_x++);

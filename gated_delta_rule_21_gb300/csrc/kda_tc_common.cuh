@@ -169,6 +169,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int ta, int tb) 
          ((uint32_t)(M >> 4) << 24);
 }
 
+// The same for fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int ta, int tb) {
+  return idesc_bf16(M, N, ta, tb) & ~((1u << 7) | (1u << 10));
+}
+
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b,
                                          uint32_t idesc, uint32_t accum) {
   asm volatile(
@@ -220,10 +225,12 @@ __device__ __forceinline__ uint64_t smem_desc_ls(uint32_t addr, uint32_t lbo, ui
 }
 
 // D (M = 128, N columns) (+)= A B^T over `ksteps` steps of K = 16; each step
-// moves both operands two core matrices along K.  ta / tb: MN-major.
+// moves both operands two core matrices along K.  ta / tb: MN-major.  F16: both
+// operands are fp16 (else bf16).
+template <bool F16 = false>
 __device__ __forceinline__ void mma_k(uint32_t d_tmem, Opnd a, int ta, Opnd b, int tb,
                                       int ksteps, int N, bool accumulate) {
-  const uint32_t id = idesc_bf16(128, N, ta, tb);
+  const uint32_t id = F16 ? idesc_f16(128, N, ta, tb) : idesc_bf16(128, N, ta, tb);
   for (int s = 0; s < ksteps; ++s)
     mma_bf16(d_tmem, smem_desc_ls(a.addr + 2u * a.lbo * (uint32_t)s, a.lbo, a.sbo),
              smem_desc_ls(b.addr + 2u * b.lbo * (uint32_t)s, b.lbo, b.sbo), id,

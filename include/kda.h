@@ -534,10 +534,11 @@ typedef struct kda_ssm_shape {
  *   impl          KDA_IMPL_SIMT: fp32 arithmetic on the CUDA cores (y and the state
  *                 1e-7 off in the 2-norm).  KDA_IMPL_TC: the tensor cores.  Both
  *                 serve every shape and type.  On the tensor cores the operands
- *                 of the final state, and of y of fp32 inputs, are two bf16
- *                 parts of 16 bits together (3.5e-6 and 3e-6 off; a single
- *                 value up to 1.1e-5 of the largest); of y of bf16 inputs they
- *                 are bf16 (2.6e-3 off, its own rounding being 1.7e-3).
+ *                 of the final state are two fp16 parts of 22 bits together
+ *                 (1.5e-7 off); of y of fp32 inputs two bf16 parts of 16 bits
+ *                 (3e-6 off; a single value up to 1.1e-5 of the largest); of y of
+ *                 bf16 inputs they are bf16 (2.6e-3 off, its own rounding being
+ *                 1.7e-3).
  *                 KDA_IMPL_AUTO: SIMT for rows of T >= 16 N tokens where B H P N
  *                 is at most 2^14, and for fp32 where B H P N T is at most
  *                 2^26; else TC.  A caller who wants one arithmetic at every

@@ -155,3 +155,41 @@ def test_strides_of_a_dimension_of_one_are_not_read():
     x, z = (t.as_strided(t.shape, (7, 13, 1)) for t in (x, z))
     got = kda.ssm_fwd(x, dt, w, A, head_dim=32, state_dim=32, z=z)[0]
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("scale", [1.0, 3e4, 2e-5])
+@pytest.mark.parametrize("dims", [(2, 300, 4, 64, 128, 2), (3, 257, 5, 128, 32, 1)])
+def test_states_are_formed_to_fp32_grade(dtype, impl, scale, dims):
+    """In the 2-norm, for inputs of any size: operands of 22 bits are off by 2^-23
+    each, products and sums by 2^-24 a step; 1e-6 covers ten of them."""
+    c = Case(*dims, dtype, init=True)
+    for i in range(2):
+        for part in c.parts(c.proj[i])[::2]:
+            part *= scale
+    c.proj = (c.proj[0], c.proj[0].double())
+    (_, s, _), (_, sr, _) = c.gpu(impl), c.plain()
+    d = s.double().cpu() - sr
+    assert d.norm() <= 1e-6 * sr.norm(), d.norm() / sr.norm()
+
+
+@pytest.mark.parametrize("dtype,impl", IMPLS)
+@pytest.mark.parametrize("size", [1e30, 1e4])
+def test_what_is_masked_scales_nothing(dtype, impl, size):
+    """Large finite values at padding, and (up to 1e4 times the others) in another
+    run of the same block, cost the rest no digits."""
+    T = 300
+    ids = torch.ones(2, T, dtype=torch.int32)
+    ids[:, 60:100], ids[:, 100:] = 2, 3
+    ids[:, 20:30] = 0
+    ids[:, 290:] = 0
+    c = Case(2, T, 3, 64, 64, 1, dtype, ids=ids)
+    big = ids == (0 if size > 1e5 else 2)
+    for proj in c.proj:
+        proj[..., 3 * 64:2 * 3 * 64 + 2 * 64][big] = size        # xbc
+    c.proj = (c.proj[0], c.proj[0].double())
+    (y, s, _), (yr, sr, _) = c.gpu(impl), c.plain()
+    d = s.double().cpu() - sr
+    assert d.norm() <= 1e-6 * sr.norm(), d.norm() / sr.norm()
+    for run in (1, 3):
+        near(y.cpu()[ids == run], yr[ids == run], dtype, "y")
