@@ -829,10 +829,11 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     contiguous; xbc and z begin and lie on multiples of 16 bytes unless
     ``impl="simt"``, which serves any place and width); conv_w: [channels,4], conv_bias: [channels], A, D, dt_bias:
     [H], all fp32; initial_state: [B,H,N,P] fp32; conv_state: [B,3,channels].
-    ``impl``: "simt" computes in fp32 on the CUDA cores, "tc" on the tensor cores
-    from operands of two fp16 parts (the state: as fp32), two bf16 parts (y of fp32
-    inputs: 3e-6 off) or one (y of bf16 inputs: 2.6e-3); "auto" takes "tc" but for long rows of
-    few heads and fp32 problems of up to 2^26 products of states and tokens.
+    ``impl``: "simt" computes in fp32 on the CUDA cores, "tc" on the tensor cores,
+    the state as fp32 arithmetic does (1.5e-7 off), y from operands of fewer bits
+    (of bf16 inputs 1.8e-3 to 2.2e-3 off, 1.7e-3 of it its own rounding; of fp32
+    inputs 1.2e-6 to 2.5e-6); "auto" takes "tc" but for long rows of few heads
+    and fp32 problems of up to 2^26 products of states and tokens.
     Returns ``(y [B,T,H,P], final_state, conv_state_out)``, the last two None
     unless ``output_final_state``."""
     dev, ty = _start(xbc, "ssm_fwd")

@@ -19,12 +19,13 @@
 // smaller than the largest), all four products are added and S is updated in fp32
 // registers, never in the accumulator: 1.5e-7 of the state's norm off, either type,
 // as fp32 arithmetic is (two bf16 parts: 3.4e-6, and 24 us less of the 330 below).
-// With bf16 inputs y is rounded to bf16 at the end and its products' operands (C, B, x, S
-// and the 128 x 128 matrix of factors) are bf16 too; their errors are of y's own
-// rounding's size and average out over the sums (2.6e-3 in all; y's own rounding
-// alone is 1.7e-3).  With fp32 inputs these operands are split in two as well
-// and all four products added (2.8e-6; an output that one term dominates up to
-// 1.1e-5, without the product of the second parts 2.3e-5).
+// y of bf16 inputs is rounded to bf16 at the end (1.7e-3).  Of its products'
+// operands x and the 128 x 128 matrix of factors, scaled by rows, are fp16 (2^-12
+// each; x is also what D multiplies), C, B and S bf16, whose errors average out
+// over the sums: 1.8e-3 to 2.2e-3 in all (all in bf16: 2.5e-3 to 2.9e-3, half of it
+// from D x).  With fp32 inputs each is split in two of its kind and all four
+// products added (1.2e-6 to 2.5e-6; a value that one term dominates up to 3.2e-6
+// of the largest).
 //
 // What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 49 us,
 // state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
@@ -68,13 +69,15 @@ struct TcBufs {
   unsigned char *bhi, *blo;        // [B][nb][G] tiles (slot, state), op_off(slot, n, N): B
                                    // in two scaled fp16 parts, for the state
   unsigned char *bt, *ct;          // likewise B and C in bf16, for y
-  unsigned char *xt;               // [B][nb][H] tiles of x, mn_off(p, slot, 128)
+  unsigned char *xt;               // [B][nb][H] tiles of x in scaled fp16, mn_off(p, slot, 128)
+  float *xinv;                     // [B][nb][H][P / 2]: what 1 in xt stands for
   unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
   unsigned char *btlo, *clo, *xlo, *slo;  // fp32 inputs: the second parts of bt, ct, xt, st
   float *binv;                     // [B][nb][G][N]: what 1 in bhi and blo stands for
   float *ein, *cum, *cumj;         // [B][H][nb * 128] by slot, see prep_factors
   float *cum_lo, *cumj_lo;         // fp32 inputs: what cum and cumj leave of the sums
   float *wst;                      // likewise, by token
+  float *dlog;                     // [B][H][nb]: a whole log2 above the finite d
   float2 *dec;                     // [B][H][nb]: e^{c_127}, or -1: the block resets the state;
                                    // what 1 in wst stands for
   int *run;                        // [B][nb * 128] by slot: resets so far in the block, -1: padding
@@ -102,6 +105,7 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->ct = take(bt * p.G * kQ * p.N * 2);
   t->binv = (float *)take(bt * p.G * p.N * 4);
   t->xt = take(bt * p.H * kQ * p.P * 2);
+  t->xinv = (float *)take(bt * p.H * p.P * 2);
   t->st = take(bt * p.H * p.N * p.P * 2);
   t->btlo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
   t->clo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
@@ -113,6 +117,7 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->wst = (float *)take(toks * p.H * 4);
   t->cum = (float *)take(toks * p.H * 4);
   t->cumj = (float *)take(toks * p.H * 4);
+  t->dlog = (float *)take(bt * p.H * 4);
   t->dec = (float2 *)take(bt * p.H * 8);
   t->run = (int *)take(toks * 4);
   t->tok = take(toks);
@@ -402,6 +407,26 @@ __device__ __forceinline__ void split16(const u64 (&v)[E], R &hi, R &lo) {
     l[i] = __floats2half2_rn(a, b);
   }
 }
+template <typename R, int E>
+__device__ __forceinline__ R pack16(const u64 (&v)[E]) {
+  R r;
+  __half2 *h = reinterpret_cast<__half2 *>(&r);
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    float a, b;
+    upk2(v[i], a, b);
+    h[i] = __floats2half2_rn(a, b);
+  }
+  return r;
+}
+__device__ __forceinline__ void unpack16(const uint4 &a, u64 (&x)[4]) {
+  const __half2 *h = reinterpret_cast<const __half2 *>(&a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    x[i] = pk2(f.x, f.y);
+  }
+}
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                     pack_bf16(v[6], v[7]));
@@ -598,9 +623,13 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
       const float scale = __uint_as_float((254u << 23) - __float_as_uint(winv));
       *reinterpret_cast<float4 *>(t.wst + at + lane * 4) =
           make_float4(wst.x * scale, wst.y * scale, wst.z * scale, wst.w * scale);
-      if (lane == 0)
-        t.dec[((size_t)b * p.H + h0 + hh) * t.nb + blk] =
-            make_float2(last == 0 ? exp2f(total) : -1.f, winv);
+      const uint32_t widest = __reduce_max_sync(
+          0xffffffffu, __float_as_uint(finite_max(make_float4(d[0], d[1], d[2], d[3]))));
+      if (lane == 0) {
+        const size_t o = ((size_t)b * p.H + h0 + hh) * t.nb + blk;
+        t.dec[o] = make_float2(last == 0 ? exp2f(total) : -1.f, winv);
+        t.dlog[o] = (float)((int)(widest >> 23) - 126);
+      }
     }
   }
 }
@@ -937,6 +966,9 @@ __global__ void __launch_bounds__(kConv + 32, 1)
           }
         }
       }
+      if (tid < TP / 2)
+        t.xinv[((((size_t)b * nb + i) * p.H + h) * p.P + c0) / 2 + tid] =
+            reinterpret_cast<const float *>(smem + L::kXinv)[(i & 1) * 16 + tid / (TP / 32)];
       if (!mbar_wait(bar_d + 8u * (i & 1), (i >> 1) & 1)) {
         bad = true;
         set_status(t.status, KDA_DEVICE_TIMEOUT);
@@ -1002,16 +1034,13 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       const size_t xt = (((size_t)b * nb + i) * p.H + h) * kQ * p.P * 2 +
                         (size_t)(c0 / 8) * 2048 + at;
       const float4 w4 = *reinterpret_cast<const float4 *>(w + 4 * lane);
-      auto put = [&](int k, u64(&u)[Cv::E], float inv, bool cut) {
+      auto put = [&](int k, u64(&u)[Cv::E], bool cut) {
         Out hi, lo;
-        u64 v[Cv::E];
-#pragma unroll
-        for (int e = 0; e < Cv::E; ++e) v[e] = mul2(u[e], pk2(inv, inv));
         if constexpr (kF32) {
-          split(v, hi, lo);
+          split16(u, hi, lo);
           *reinterpret_cast<Out *>(t.xlo + xt + k * 128) = lo;
         } else {
-          hi = pack<Out>(v);
+          hi = pack16<Out>(u);
         }
         *reinterpret_cast<Out *>(t.xt + xt + k * 128) = hi;
         const float f = k == 0 ? w4.x : k == 1 ? w4.y : k == 2 ? w4.z : w4.w;
@@ -1031,14 +1060,14 @@ __global__ void __launch_bounds__(kConv + 32, 1)
           !IDS || (flags & kPlain)
               ? cv.template run<false>(
                     rows, warp, lane, tok, true,
-                    [&](int k, u64(&u)[Cv::E], float v) { put(k, u, v, false); })
+                    [&](int k, u64(&u)[Cv::E], float) { put(k, u, false); })
               : cv.template run<true>(
                     rows, warp, lane, tok, true,
-                    [&](int k, u64(&u)[Cv::E], float v) { put(k, u, v, true); });
-      if (lane == 0) reinterpret_cast<float *>(smem + L::kXinv)[(i & 1) * 16 + warp] = inv;
+                    [&](int k, u64(&u)[Cv::E], float) { put(k, u, true); });
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
+      if (lane == 0) reinterpret_cast<float *>(smem + L::kXinv)[(i & 1) * 16 + warp] = inv;
       if (i > 0) finish(i - 1);
     }
     cp_async_wait_all();
@@ -1078,7 +1107,8 @@ struct OutSmem {
   static constexpr uint32_t kCum = kZ + kQ * PT * sizeof(T);        // cumj [128]
   static constexpr uint32_t kCumLo = kCum + kQ * 4;                 // its rest, fp32 inputs
   static constexpr uint32_t kRun = kCumLo + (kParts - 1) * kQ * 4;  // runs, one byte each
-  static constexpr uint32_t kBar = kRun + kQ;
+  static constexpr uint32_t kXinv = kRun + kQ;                      // [PT / 2]: 1 in x
+  static constexpr uint32_t kBar = kXinv + PT * 2;
   static constexpr uint32_t kTmem = kBar + 32;
   static constexpr uint32_t kBytes = kTmem + 16;
 };
@@ -1182,7 +1212,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
   float *scumj = reinterpret_cast<float *>(smem + L::kCum);
   float *scumj_lo = reinterpret_cast<float *>(smem + L::kCumLo);
   // the factors of the next item's head: of row r, and of column tid
-  float ein = 0.f, cr = 0.f, cl = 0.f, cj = 0.f, cjl = 0.f;
+  float ein = 0.f, cr = 0.f, cl = 0.f, cj = 0.f, cjl = 0.f, dlog = 0.f, xi = 0.f;
   auto factors = [&](int k) {
     const size_t at = (((size_t)b * p.H + h_lo + k / subs) * nb + blk) * kQ;
     ein = t.ein[at + r];
@@ -1192,6 +1222,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       cj = t.cumj[at + tid];
       if (kF32) cjl = t.cumj_lo[at + tid];
     }
+    dlog = t.dlog[((size_t)b * p.H + h_lo + k / subs) * nb + blk];
+    if (tid < PT / 2)
+      xi = t.xinv[((((size_t)b * nb + blk) * p.H + h_lo + k / subs) * p.P + k % subs * PT) / 2 + tid];
   };
   factors(0);
   const Opnd opC = {sb + L::kC, 128, (uint32_t)N * 16};
@@ -1209,7 +1242,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     mma_commit(bar_m);
   }
   wait_mma();
+  // A row's factors are kept in fp16, over the power of two that leaves the row of
+  // C B^T below 2^15 times the head's widest d: 11 bits of what is not 2^29 times
+  // smaller.  The row's largest finite value, by its two threads:
+  float *stop = reinterpret_cast<float *>(smem + L::kZ);      // [2][128]
+  auto row_top = [&](bool filter) {
+    float m = 0.f;
+#pragma unroll 1
+    for (int q = half; q < 2 * quad + 2; q += 2) {
+      float v[16];
+      tmem_ld16(t_cb + lanes + 16 * q, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (!filter || fabsf(v[e]) < CUDART_INF_F) m = fmaxf(m, fabsf(v[e]));
+    }
+    return m;
+  };
+  float top = row_top(false);
+  if (__any_sync(0xffffffffu, !(top < CUDART_INF_F))) top = row_top(true);
+  stop[half * kQ + r] = top;
   __syncthreads();
+  const float row_inv = to_2p15(fmaxf(top, stop[(half ^ 1) * kQ + r]));
+  const float row_log = (float)((int)(__float_as_uint(row_inv) >> 23) - 127);
+  float f_inv = 0.f;            // what 1 in the factors of row r stands for
   // entries above the diagonal's 32-row steps are never written again
   for (int i = tid; i < (int)(L::kParts * L::kPart / 16); i += 256)
     *reinterpret_cast<uint4 *>(smem + L::kF + i * 16) = make_uint4(0, 0, 0, 0);
@@ -1237,6 +1292,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       scumj[tid] = cj;
       if (kF32) scumj_lo[tid] = cjl;
     }
+    if (tid < PT / 2) reinterpret_cast<float *>(smem + L::kXinv)[tid] = xi;
     if (__syncthreads_or(bad)) break;         // cumj is there, the last y has left
     if (p.z) {
       const T *z = static_cast<const T *>(p.z) + (size_t)b * p.z_sb + (long long)t0 * p.z_st + ch +
@@ -1252,7 +1308,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     const float ein_now = ein;
     if (c == 0) {
       // factors of the head: row r, 16 columns at a time, up to the diagonal
-      const u64 cr2 = pk2(cr, cr), cl2 = pk2(cl, cl), neg = pk2(-1.f, -1.f);
+      // over f_inv, the row's and the head's power of two
+      f_inv = row_inv * __uint_as_float((uint32_t)(127 + (int)dlog) << 23);
+      const Two cs = kF32 ? two_sum(cr, -(row_log + dlog)) : Two{cr - (row_log + dlog), 0.f};
+      const float cls = cl + cs.lo;
+      const u64 cr2 = pk2(cs.hi, cs.hi), cl2 = pk2(cls, cls), neg = pk2(-1.f, -1.f);
 #pragma unroll 1
       for (int q = half; q < 2 * quad + 2; q += 2) {
         float v[16];
@@ -1291,12 +1351,15 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
           float a[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) a[e] = v[8 * o + e];
-          const uint4 hi = pack8(a);
-          *reinterpret_cast<uint4 *>(f + 128 * o) = hi;
+          const u64 w[4] = {pk2(a[0], a[1]), pk2(a[2], a[3]), pk2(a[4], a[5]), pk2(a[6], a[7])};
+          uint4 hi, lo;
           if constexpr (kF32) {
-            rest8(hi, a);
-            *reinterpret_cast<uint4 *>(f + L::kPart + 128 * o) = pack8(a);
+            split16(w, hi, lo);
+            *reinterpret_cast<uint4 *>(f + L::kPart + 128 * o) = lo;
+          } else {
+            hi = pack16<uint4>(w);
           }
+          *reinterpret_cast<uint4 *>(f + 128 * o) = hi;
         }
       }
       fence_proxy_async();
@@ -1309,10 +1372,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       if (k + 1 < n_items) load_s(n_s++);
       if (mbar_wait(bar_x, k & 1)) {
         const Opnd opF = {sb + L::kF, 128, kQ * 16}, opX = {sb + L::kX, 128, kQ * 16};
-        mma_k(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
+        mma_k<true>(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
         if (kF32) {
           const Opnd opF2 = {sb + L::kF + L::kPart, 128, kQ * 16};
-          mma_k(t_yx, opF2, 0, opX, 1, kQ / 16, kCols, true);
+          mma_k<true>(t_yx, opF2, 0, opX, 1, kQ / 16, kCols, true);
         }
         mma_commit(bar_m);
         if (k + 1 < n_items) {
@@ -1329,7 +1392,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     if (__syncthreads_or(bad)) break;
     // y of row r, columns [half PT / 2, (half + 1) PT / 2)
     const float D = p.D ? p.D[h] : 0.f;
-    const u64 ein2 = pk2(ein_now, ein_now), D2 = pk2(D, D);
+    const u64 ein2 = pk2(ein_now, ein_now), D2 = pk2(D, D), f_inv2 = pk2(f_inv, f_inv);
 #pragma unroll
     for (int e0 = 0; e0 < PT / 2; e0 += 16) {
       const int col = half * (PT / 2) + e0;
@@ -1362,24 +1425,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
             continue;
           const unsigned char *fp = smem + L::kF + op_off(r, j, kQ),
                               *xp = smem + L::kX + mn_off(col, j, kQ);
-          float f = __bfloat162float(*reinterpret_cast<const bf16 *>(fp));
-          if (kF32) f += __bfloat162float(*reinterpret_cast<const bf16 *>(fp + L::kPart));
+          float f = __half2float(*reinterpret_cast<const __half *>(fp));
+          if (kF32) f += __half2float(*reinterpret_cast<const __half *>(fp + L::kPart));
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const unsigned char *v = xp + mn_off(e, 0, kQ);
-            float x = __bfloat162float(*reinterpret_cast<const bf16 *>(v));
-            if (kF32) x += __bfloat162float(*reinterpret_cast<const bf16 *>(v + kQ * PT * 2));
+            float x = __half2float(*reinterpret_cast<const __half *>(v));
+            if (kF32) x += __half2float(*reinterpret_cast<const __half *>(v + kQ * PT * 2));
             yx[e] = fmaf(f, x, yx[e]);
           }
         }
       }
+      float xinv[8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float4 *>(xinv + 4 * q) =
+            *reinterpret_cast<const float4 *>(smem + L::kXinv + col * 2 + 16 * q);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         u64 x[4], z[4], y[4];
         const unsigned char *xp = smem + L::kX + (col / 8 + q) * 2048 + (r >> 3) * 128 + (r & 7) * 16;
-        Unpack8::unpack(*reinterpret_cast<const uint4 *>(xp), x);
+        unpack16(*reinterpret_cast<const uint4 *>(xp), x);
         if (kF32) {
-          Unpack8::unpack(*reinterpret_cast<const uint4 *>(xp + kQ * PT * 2), z);
+          unpack16(*reinterpret_cast<const uint4 *>(xp + kQ * PT * 2), z);
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = add2(x[e], z[e]);
         }
@@ -1398,7 +1466,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 8 * q + 2 * e;
-          y[e] = fma2(D2, x[e], fma2(ein2, pk2(yi[i], yi[i + 1]), pk2(yx[i], yx[i + 1])));
+          const u64 v = fma2(f_inv2, pk2(yx[i], yx[i + 1]), mul2(D2, x[e]));
+          y[e] = fma2(pk2(xinv[4 * q + e], xinv[4 * q + e]), v, mul2(ein2, pk2(yi[i], yi[i + 1])));
           if (p.z) {
             float a, d, d0, d1;
             upk2(mul2(z[e], pk2(-kLog2e, -kLog2e)), a, d);

@@ -535,10 +535,10 @@ typedef struct kda_ssm_shape {
  *                 1e-7 off in the 2-norm).  KDA_IMPL_TC: the tensor cores.  Both
  *                 serve every shape and type.  On the tensor cores the operands
  *                 of the final state are two fp16 parts of 22 bits together
- *                 (1.5e-7 off); of y of fp32 inputs two bf16 parts of 16 bits
- *                 (3e-6 off; a single value up to 1.1e-5 of the largest); of y of
- *                 bf16 inputs they are bf16 (2.6e-3 off, its own rounding being
- *                 1.7e-3).
+ *                 (1.5e-7 off).  Those of y are one fp16 or bf16 part of bf16
+ *                 inputs (1.8e-3 to 2.2e-3 off, its own rounding being 1.7e-3; up
+ *                 to 2.9e-3 where an entering state is most of y) and two of
+ *                 fp32 inputs (1.2e-6 to 2.5e-6).
  *                 KDA_IMPL_AUTO: SIMT for rows of T >= 16 N tokens where B H P N
  *                 is at most 2^14, and for fp32 where B H P N T is at most
  *                 2^26; else TC.  A caller who wants one arithmetic at every
