@@ -832,7 +832,7 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     ``impl``: "simt" computes in fp32 on the CUDA cores, "tc" on the tensor cores,
     the state as fp32 arithmetic does (1.5e-7 off), y from operands of fewer bits
     (of bf16 inputs 1.8e-3 to 2.2e-3 off, 1.7e-3 of it its own rounding; of fp32
-    inputs 1.2e-6 to 2.5e-6); "auto" takes "tc" but for long rows of few heads
+    inputs 2e-7 to 7e-7); "auto" takes "tc" but for long rows of few heads
     and fp32 problems of up to 2^26 products of states and tokens.
     Returns ``(y [B,T,H,P], final_state, conv_state_out)``, the last two None
     unless ``output_final_state``."""

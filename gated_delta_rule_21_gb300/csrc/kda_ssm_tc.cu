@@ -24,8 +24,9 @@
 // each; x is also what D multiplies), C, B and S bf16, whose errors average out
 // over the sums: 1.8e-3 to 2.2e-3 in all (all in bf16: 2.5e-3 to 2.9e-3, half of it
 // from D x).  With fp32 inputs each is split in two of its kind and all four
-// products added (1.2e-6 to 2.5e-6; a value that one term dominates up to 3.2e-6
-// of the largest).
+// products added, C and B of C B^T in three, the small products first, since the
+// accumulator loses bits at its own size (2e-7 to 7e-7, where an entering state
+// is most of y; C and B in two parts 2.5e-6, the large products first 1.2e-6).
 //
 // What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 49 us,
 // state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
@@ -73,6 +74,7 @@ struct TcBufs {
   float *xinv;                     // [B][nb][H][P / 2]: what 1 in xt stands for
   unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
   unsigned char *btlo, *clo, *xlo, *slo;  // fp32 inputs: the second parts of bt, ct, xt, st
+  unsigned char *bt3, *c3;                // and the third of bt and ct
   float *binv;                     // [B][nb][G][N]: what 1 in bhi and blo stands for
   float *ein, *cum, *cumj;         // [B][H][nb * 128] by slot, see prep_factors
   float *cum_lo, *cumj_lo;         // fp32 inputs: what cum and cumj leave of the sums
@@ -108,6 +110,8 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->xinv = (float *)take(bt * p.H * p.P * 2);
   t->st = take(bt * p.H * p.N * p.P * 2);
   t->btlo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
+  t->bt3 = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
+  t->c3 = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
   t->clo = take(f32 ? bt * p.G * kQ * p.N * 2 : 0);
   t->xlo = take(f32 ? bt * p.H * kQ * p.P * 2 : 0);
   t->slo = take(f32 ? bt * p.H * p.N * p.P * 2 : 0);
@@ -369,7 +373,7 @@ struct Conv {
 
 using Unpack8 = Conv<bf16, 64, 8, 256>;      // for its unpack
 
-// Pairs as bf16, and what that leaves, again as bf16 (R: uint4 or uint2).
+// Pairs as bf16 (R: uint4 or uint2), and v less what such a part holds.
 template <typename R, int E>
 __device__ __forceinline__ R pack(const u64 (&v)[E]) {
   R r;
@@ -383,16 +387,14 @@ __device__ __forceinline__ R pack(const u64 (&v)[E]) {
   return r;
 }
 template <typename R, int E>
-__device__ __forceinline__ void split(const u64 (&v)[E], R &hi, R &lo) {
-  u64 rest[E];
-  hi = pack<R>(v);
-  const uint32_t *h = reinterpret_cast<const uint32_t *>(&hi);
+__device__ __forceinline__ void less(const R &part, u64 (&v)[E]) {
+  const uint32_t *h = reinterpret_cast<const uint32_t *>(&part);
 #pragma unroll
   for (int i = 0; i < E; ++i)
-    rest[i] = fma2(pk2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)),
-                   pk2(-1.f, -1.f), v[i]);
-  lo = pack<R>(rest);
+    v[i] = fma2(pk2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)),
+                pk2(-1.f, -1.f), v[i]);
 }
+
 // Pairs as two parts in fp16.
 template <typename R, int E>
 __device__ __forceinline__ void split16(const u64 (&v)[E], R &hi, R &lo) {
@@ -690,9 +692,15 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
 #pragma unroll
         for (int e = 0; e < Cv::E; ++e) u[e] = mul2(u[e], pk2(inv, inv));
       }
-      split(u, hi, lo);
+      hi = pack<Out>(u);
       *reinterpret_cast<Out *>((is_c ? t.ct : t.bt) + o) = hi;
-      if (sizeof(T) == 4) *reinterpret_cast<Out *>((is_c ? t.clo : t.btlo) + o) = lo;
+      if (sizeof(T) == 4) {
+        less(hi, u);
+        lo = pack<Out>(u);
+        *reinterpret_cast<Out *>((is_c ? t.clo : t.btlo) + o) = lo;
+        less(lo, u);
+        *reinterpret_cast<Out *>((is_c ? t.c3 : t.bt3) + o) = pack<Out>(u);
+      }
     };
     const unsigned char *rows = smem + (blk & 1) * Cv::kBytes;
     const float inv =
@@ -879,8 +887,9 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         const uint32_t bt = sb + L::kB + (i & 1) * L::kBBytes;
         const Opnd x = {sb + L::kX + (i & 1) * L::kXBytes, 128, kQ * 16};
         const Opnd bh_ = {bt, (uint32_t)N * 16, 128}, bl_ = {bt + tb, (uint32_t)N * 16, 128};
-        mma_k<true>(d, bh_, 1, x, 1, kQ / 16, 2 * TP, false);
-        mma_k<true>(d, bl_, 1, x, 1, kQ / 16, 2 * TP, true);
+        // the small products first: a sum in the accumulator loses bits at its size
+        mma_k<true>(d, bl_, 1, x, 1, kQ / 16, 2 * TP, false);
+        mma_k<true>(d, bh_, 1, x, 1, kQ / 16, 2 * TP, true);
         mma_commit(bar_d + 8u * (i & 1));
         ++issued;
         if (i > 0 && loaded < nb) {      // block i - 1's tiles are free once it is done
@@ -1104,7 +1113,11 @@ struct OutSmem {
   static constexpr uint32_t kX = kF + kParts * kPart;
   static constexpr uint32_t kS = kX + kParts * kQ * PT * 2;
   static constexpr uint32_t kZ = kS + kParts * kQ * PT * 2;
-  static constexpr uint32_t kCum = kZ + kQ * PT * sizeof(T);        // cumj [128]
+  // fp32 inputs: until C B^T is made, the third parts of C and B lie from kX on
+  static constexpr uint32_t kThird = kX;
+  static constexpr uint32_t kEnd = kZ + kQ * PT * sizeof(T),
+                            kFull = kThird + (kParts - 1) * 2 * kPart;
+  static constexpr uint32_t kCum = kEnd > kFull ? kEnd : kFull;     // cumj [128]
   static constexpr uint32_t kCumLo = kCum + kQ * 4;                 // its rest, fp32 inputs
   static constexpr uint32_t kRun = kCumLo + (kParts - 1) * kQ * 4;  // runs, one byte each
   static constexpr uint32_t kXinv = kRun + kQ;                      // [PT / 2]: 1 in x
@@ -1195,15 +1208,18 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
   int n_x = 0, n_s = 0;         // thread 0: loads of x and S asked for
   if (tid == 0) {
     const size_t o = (((size_t)b * nb + blk) * p.G + g) * tile;
-    mbar_expect_tx(bar_cb, 2 * tile * L::kParts);
+    mbar_expect_tx(bar_cb, 2 * tile * (kF32 ? 3 : 1));
     bulk_load(sb + L::kC, t.ct + o, tile, bar_cb);
     bulk_load(sb + L::kF, t.bt + o, tile, bar_cb);
     if (kF32) {
       bulk_load(sb + L::kC + L::kPart, t.clo + o, tile, bar_cb);
       bulk_load(sb + L::kF + L::kPart, t.btlo + o, tile, bar_cb);
+      bulk_load(sb + L::kThird, t.c3 + o, tile, bar_cb);
+      bulk_load(sb + L::kThird + L::kPart, t.bt3 + o, tile, bar_cb);
+    } else {
+      load_s(n_s++);
+      load_x(n_x++);
     }
-    load_s(n_s++);
-    load_x(n_x++);
   }
   const int flags = t.flags[(size_t)b * nb + blk];
   const int run = t.run[((size_t)b * nb + blk) * kQ + r];
@@ -1232,16 +1248,24 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
   if (!mbar_wait(bar_cb, 0)) give_up();
   if (tid == 0 && !bad) {
     const Opnd opB = {sb + L::kF, 128, (uint32_t)N * 16};
-    mma_k(t_cb, opC, 0, opB, 0, N / 16, 128, false);
-    if (kF32) {
+    if (kF32) {        // (the small products first)
       const Opnd opB2 = {sb + L::kF + L::kPart, 128, (uint32_t)N * 16};
+      const Opnd opC3 = {sb + L::kThird, 128, (uint32_t)N * 16};
+      const Opnd opB3 = {sb + L::kThird + L::kPart, 128, (uint32_t)N * 16};
+      mma_k(t_cb, opC, 0, opB3, 0, N / 16, 128, false);
+      mma_k(t_cb, opC3, 0, opB, 0, N / 16, 128, true);
+      mma_k(t_cb, opC2, 0, opB2, 0, N / 16, 128, true);
       mma_k(t_cb, opC, 0, opB2, 0, N / 16, 128, true);
       mma_k(t_cb, opC2, 0, opB, 0, N / 16, 128, true);
-      mma_k(t_cb, opC2, 0, opB2, 0, N / 16, 128, true);
     }
+    mma_k(t_cb, opC, 0, opB, 0, N / 16, 128, kF32);
     mma_commit(bar_m);
   }
   wait_mma();
+  if (kF32 && tid == 0 && !bad) {      // where the third parts were
+    load_s(n_s++);
+    load_x(n_x++);
+  }
   // A row's factors are kept in fp16, over the power of two that leaves the row of
   // C B^T below 2^15 times the head's widest d: 11 bits of what is not 2^29 times
   // smaller.  The row's largest finite value, by its two threads:
@@ -1281,8 +1305,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     if (tid == 0 && !bad) {
       if (mbar_wait(bar_s, k & 1)) {
         const Opnd opS = {sb + L::kS, 128, (uint32_t)N * 16};
-        mma_k(t_yi, opC, 0, opS, 1, N / 16, kCols, false);
-        if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, kCols, true);
+        if (kF32) mma_k(t_yi, opC2, 0, opS, 1, N / 16, kCols, false);
+        mma_k(t_yi, opC, 0, opS, 1, N / 16, kCols, kF32);
         mma_commit(bar_m);
       } else {
         give_up();
@@ -1372,11 +1396,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
       if (k + 1 < n_items) load_s(n_s++);
       if (mbar_wait(bar_x, k & 1)) {
         const Opnd opF = {sb + L::kF, 128, kQ * 16}, opX = {sb + L::kX, 128, kQ * 16};
-        mma_k<true>(t_yx, opF, 0, opX, 1, kQ / 16, kCols, false);
         if (kF32) {
           const Opnd opF2 = {sb + L::kF + L::kPart, 128, kQ * 16};
-          mma_k<true>(t_yx, opF2, 0, opX, 1, kQ / 16, kCols, true);
+          mma_k<true>(t_yx, opF2, 0, opX, 1, kQ / 16, kCols, false);
         }
+        mma_k<true>(t_yx, opF, 0, opX, 1, kQ / 16, kCols, kF32);
         mma_commit(bar_m);
         if (k + 1 < n_items) {
           prefetch_l2(t.xt + x_of(k + 1), kQ * PT * 2);

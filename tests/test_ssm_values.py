@@ -210,3 +210,14 @@ def test_outputs_are_off_by_little_more_than_their_own_rounding(T, scale, init, 
     y, yr = c.gpu("tc")[0], c.plain()[0]
     d = y.double().cpu() - yr
     assert d.norm() <= tol * yr.norm(), d.norm() / yr.norm()
+
+
+@pytest.mark.parametrize("impl", ["simt", "tc"])
+@pytest.mark.parametrize("dims", [(2, 300, 4, 64, 128, 2), (1, 400, 3, 128, 64, 1)])
+def test_fp32_outputs_are_formed_to_fp32_grade(dims, impl):
+    """From zero states, in the 2-norm: x and the factors are two parts of 22 bits,
+    C and B three of 24, a factor's exponential is off by 2^-22: below 1e-6."""
+    c = Case(*dims, torch.float32)
+    y, yr = c.gpu(impl)[0], c.plain()[0]
+    d = y.double().cpu() - yr
+    assert d.norm() <= 1e-6 * yr.norm(), d.norm() / yr.norm()
