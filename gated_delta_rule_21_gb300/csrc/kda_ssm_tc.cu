@@ -71,17 +71,19 @@ struct TcBufs {
                                    // in two scaled fp16 parts, for the state
   unsigned char *bt, *ct;          // likewise B and C in bf16, for y
   unsigned char *xt;               // [B][nb][H] tiles of x in scaled fp16, mn_off(p, slot, 128)
-  float *xinv;                     // [B][nb][H][P / 2]: what 1 in xt stands for
+  int xch;                         // channels that share a scale of x
+  float *xinv;                     // [B][nb][H][P / xch]: what 1 in xt stands for
   unsigned char *st;               // [B][nb][H] tiles of entering states, mn_off(p, n, N)
   unsigned char *btlo, *clo, *xlo, *slo;  // fp32 inputs: the second parts of bt, ct, xt, st
   unsigned char *bt3, *c3;                // and the third of bt and ct
-  float *binv;                     // [B][nb][G][N]: what 1 in bhi and blo stands for
+  unsigned char *bexp;             // [B][nb][G][N]: the exponent (as in a float) of what 1 in
+                                   // bhi and blo stands for
   float *ein, *cum, *cumj;         // [B][H][nb * 128] by slot, see prep_factors
   float *cum_lo, *cumj_lo;         // fp32 inputs: what cum and cumj leave of the sums
   float *wst;                      // likewise, by token
   float *dlog;                     // [B][H][nb]: a whole log2 above the finite d
-  float2 *dec;                     // [B][H][nb]: e^{c_127}, or -1: the block resets the state;
-                                   // what 1 in wst stands for
+  float4 *dec;                     // [B][H][nb]: e^{c_127}, or -1: the block resets the state;
+                                   // what 1 in wst stands for; 0, 0
   int *run;                        // [B][nb * 128] by slot: resets so far in the block, -1: padding
   unsigned char *tok;              // [B][nb * 128] by token: token_mark
   int *flags;                      // [B][nb]: kPlain, kResets
@@ -105,7 +107,7 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->blo = take(bt * p.G * kQ * p.N * 2);
   t->bt = take(bt * p.G * kQ * p.N * 2);
   t->ct = take(bt * p.G * kQ * p.N * 2);
-  t->binv = (float *)take(bt * p.G * p.N * 4);
+  t->bexp = take(bt * p.G * p.N);
   t->xt = take(bt * p.H * kQ * p.P * 2);
   t->xinv = (float *)take(bt * p.H * p.P * 2);
   t->st = take(bt * p.H * p.N * p.P * 2);
@@ -122,7 +124,7 @@ size_t layout_bufs(const SsmParams &p, bool f32, unsigned char *base, TcBufs *t)
   t->cum = (float *)take(toks * p.H * 4);
   t->cumj = (float *)take(toks * p.H * 4);
   t->dlog = (float *)take(bt * p.H * 4);
-  t->dec = (float2 *)take(bt * p.H * 8);
+  t->dec = (float4 *)take(bt * p.H * 16);
   t->run = (int *)take(toks * 4);
   t->tok = take(toks);
   t->flags = (int *)take(bt * 4);
@@ -136,9 +138,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool o
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -199,10 +198,11 @@ struct Conv {
   }
 
   u64 wt[kSsmTaps][E], bias[E];
-  float gain, base;     // |u| <= gain max|x| + base: sums of |w|, |bias| of the channels
 
-  __device__ __forceinline__ void weights(const SsmParams &p, int channel) {
-    gain = base = 0.f;
+  // Returns the sum of |w| and the |bias|, the largest of the channels':
+  // |u| <= .x max|x| + .y.
+  __device__ __forceinline__ float2 weights(const SsmParams &p, int channel) {
+    float gain = 0.f, base = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float4 a = *reinterpret_cast<const float4 *>(p.w + 4 * (size_t)(channel + 2 * i));
@@ -218,6 +218,7 @@ struct Conv {
                                fabsf(b.x) + fabsf(b.y) + fabsf(b.z) + fabsf(b.w)));
       base = fmaxf(base, fmaxf(fabsf(b0), fabsf(b1)));
     }
+    return make_float2(gain, base);
   }
 
   // x: the row's token 0 at the tile's channel; past: the convolution's cache
@@ -260,21 +261,22 @@ struct Conv {
   // tile at the lane's i-th token, 4 lane + i.  CUT: windows end where a run
   // starts, and padding gives 0; tok holds the tokens' windows.
   //
-  // inv is 1, or with `scaled` a power of two that keeps |u| of the warp's channels
+  // inv is 1, or with `bound` (what weights returned) a power of two that keeps |u| of the warp's channels
   // and the block's tokens below 2^15, by the largest finite input: what u is in
   // fp16 then has 11 bits, and two parts of it 22, down to 2^-29 of the largest.
   // The scale costs no instruction per value (1 / (1 + e) is made with it).
   // Returns inv.
   template <bool CUT, typename F>
   __device__ __forceinline__ float run(const unsigned char *rows, int warp, int lane,
-                                       const unsigned char *tok, bool scaled, F f) const {
+                                       const unsigned char *tok, const float2 *bound,
+                                       F f) const {
     const int at = warp * CH * (int)sizeof(T);
     // rows 4 lane .. 4 lane + 6: two permutations
     const unsigned char *lo = rows + off(4 * lane, at / 16) + at % 16;
     const unsigned char *hi = rows + off(4 * lane + 4, at / 16) + at % 16;
     const uint32_t marks = CUT ? *reinterpret_cast<const uint32_t *>(tok + 4 * lane) : 0;
     uint32_t live = 0x7f;                 // rows that a token's window holds
-    if (CUT && scaled) {
+    if (CUT && bound) {
       live = 0;
 #pragma unroll
       for (int i = 0; i < kStrip; ++i) {
@@ -289,7 +291,7 @@ struct Conv {
       const Raw r =
           *reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes);
       unpack(r, x[i]);
-      if (scaled && (live >> i & 1)) {
+      if (bound && (live >> i & 1)) {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
         constexpr int kWords = (int)sizeof(Raw) / 4;
 #pragma unroll
@@ -299,7 +301,7 @@ struct Conv {
         }
       }
     }
-    const float inv = scaled ? fit(larger(top, top2), lo, hi, live) : 1.f;
+    const float inv = bound ? fit(larger(top, top2), lo, hi, live, *bound) : 1.f;
     const u64 one = pk2(inv, inv);
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
@@ -328,7 +330,8 @@ struct Conv {
   // inv for the largest |x| of the warp: top, or where that is not finite what the
   // live rows hold.
   __device__ __forceinline__ float fit(uint32_t top, const unsigned char *lo,
-                                       const unsigned char *hi, uint32_t live) const {
+                                       const unsigned char *hi, uint32_t live,
+                                       float2 bound) const {
     if (sizeof(T) == 2) top = max(top << 16, top & 0xffff0000u);
     top = __reduce_max_sync(0xffffffffu, top);
     if (top >= 0x7f800000u) {
@@ -347,7 +350,7 @@ struct Conv {
       }
       top = __reduce_max_sync(0xffffffffu, top);
     }
-    return to_2p15(fmaf(gain, __uint_as_float(top), base));
+    return to_2p15(fmaf(bound.x, __uint_as_float(top), bound.y));
   }
   // The larger magnitudes: bits of a float, or two bf16.  NaN loses or comes out
   // above every number.
@@ -629,7 +632,7 @@ __device__ __forceinline__ void prep_factors(const SsmParams &p, const TcBufs &t
           0xffffffffu, __float_as_uint(finite_max(make_float4(d[0], d[1], d[2], d[3]))));
       if (lane == 0) {
         const size_t o = ((size_t)b * p.H + h0 + hh) * t.nb + blk;
-        t.dec[o] = make_float2(last == 0 ? exp2f(total) : -1.f, winv);
+        t.dec[o] = make_float4(last == 0 ? exp2f(total) : -1.f, winv, 0.f, 0.f);
         t.dlog[o] = (float)((int)(widest >> 23) - 126);
       }
     }
@@ -664,7 +667,11 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   };
   stage(blk);
   Cv cv;
-  if (mine) cv.weights(p, ch + wch);
+  float2 *bound = reinterpret_cast<float2 *>(smem + 2 * (Cv::kBytes + kQ)) + warp;
+  if (mine) {
+    const float2 v = cv.weights(p, ch + wch);
+    if (lane == 0) *bound = v;         // (read after a barrier)
+  }
   for (; blk < end; ++blk) {
     // whether any token's window leaves the staged rows
     unsigned char *stok = smem + 2 * Cv::kBytes + (blk & 1) * kQ;
@@ -704,10 +711,11 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
     };
     const unsigned char *rows = smem + (blk & 1) * Cv::kBytes;
     const float inv =
-        plain ? cv.template run<false>(rows, warp, lane, stok, !is_c, put)
-              : cv.template run<true>(rows, warp, lane, stok, !is_c, put);
+        plain ? cv.template run<false>(rows, warp, lane, stok, is_c ? nullptr : bound, put)
+              : cv.template run<true>(rows, warp, lane, stok, is_c ? nullptr : bound, put);
     if (!is_c && lane < kPrepCh<T>)
-      t.binv[(((size_t)b * t.nb + blk) * p.G + g) * p.N + n0 + wch + lane] = inv;
+      t.bexp[(((size_t)b * t.nb + blk) * p.G + g) * p.N + n0 + wch + lane] =
+          (unsigned char)(__float_as_uint(inv) >> 23);
   }
 }
 
@@ -785,10 +793,11 @@ struct StateSmem {
   static constexpr uint32_t kBBytes = 2 * kQ * 128 * 2;
   static constexpr uint32_t kRows = kB + 2 * kBBytes;               // 2 staged tiles of x
   static constexpr uint32_t kW = kRows + 2 * Cv::kBytes;      // 2 x wst
-  static constexpr uint32_t kXinv = kW + 2 * kQ * 4;          // 2 x [16]: 1 in kX, by warp
-  static constexpr uint32_t kBinv = kXinv + 2 * 16 * 4;       // 2 x [128]: 1 in kB, by row
-  static constexpr uint32_t kDec = kBinv + 2 * 128 * 4;       // 2 x dec
-  static constexpr uint32_t kBar = kDec + 2 * 8;
+  static constexpr uint32_t kXinv = kW + 2 * kQ * 4;          // 4 x [16]: 1 in kX, by warp
+  static constexpr uint32_t kBexp = kXinv + 4 * 16 * 4;       // 4 x [128]: bexp
+  static constexpr uint32_t kDec = kBexp + 4 * 128;           // 4 x dec
+  static constexpr uint32_t kBound = kDec + 4 * 16;           // [16] float2, by warp
+  static constexpr uint32_t kBar = kBound + 16 * 8;
   static constexpr uint32_t kTmem = kBar + 48;
   static constexpr uint32_t kBytes = kTmem + 16;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -852,8 +861,8 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     mbar_init(bar_x + 8, kConv);
     mbar_init(bar_b, 1);
     mbar_init(bar_b + 8, 1);
-    mbar_init(bar_d, 1);
-    mbar_init(bar_d + 8, 1);
+    mbar_init(bar_d, 2);           // the products, and that what came with B is there
+    mbar_init(bar_d + 8, 2);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -869,10 +878,18 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       auto load = [&](int i) {
         const size_t o = (((size_t)b * nb + i) * p.G + g) * tb;
         const uint32_t bar = bar_b + 8u * (i & 1), dst = sb + L::kB + (i & 1) * L::kBBytes;
-        mbar_expect_tx(bar, 2 * tb);
+        mbar_expect_tx(bar, 2 * tb + N + 16);
         bulk_load(dst, t.bhi + o, tb, bar);
         bulk_load(dst + tb, t.blo + o, tb, bar);
+        // what finish(i) needs; block i - 4's is read by then (as is its xinv)
+        bulk_load(sb + L::kBexp + (i & 3) * 128, t.bexp + (((size_t)b * nb + i) * p.G + g) * N, N,
+                  bar);
+        bulk_load(sb + L::kDec + (i & 3) * 16, t.dec + ((size_t)b * p.H + h) * nb + i, 16, bar);
       };
+      const float4 *xinv = reinterpret_cast<const float4 *>(smem + L::kXinv);
+      const int scales = p.P / (TP / 16);          // of a head: P / xch
+      float4 *xinv_out =
+          reinterpret_cast<float4 *>(t.xinv + ((size_t)b * nb * p.H + h) * scales + tile * 16);
       int loaded = 0, landed = 0, issued = 0, done = 0;
       bool ok = true;
       for (; loaded < 2 && loaded < nb; ++loaded) load(loaded);
@@ -891,7 +908,11 @@ __global__ void __launch_bounds__(kConv + 32, 1)
         mma_k<true>(d, bl_, 1, x, 1, kQ / 16, 2 * TP, false);
         mma_k<true>(d, bh_, 1, x, 1, kQ / 16, 2 * TP, true);
         mma_commit(bar_d + 8u * (i & 1));
+        mbar_arrive(bar_d + 8u * (i & 1));
         ++issued;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)      // the scales of x, for ssm_out_kernel
+          xinv_out[(size_t)i * p.H * scales / 4 + k] = xinv[(i & 3) * 4 + k];
         if (i > 0 && loaded < nb) {      // block i - 1's tiles are free once it is done
           ok = mbar_wait(bar_d + 8u * ((i - 1) & 1), ((i - 1) >> 1) & 1);
           if (!ok) break;
@@ -912,11 +933,11 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     const T *x = static_cast<const T *>(p.xbc) + (size_t)b * p.xbc_sb + ch;
     const T *before = past ? past + ch : nullptr;
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
-    const float2 *dec = t.dec + ((size_t)b * p.H + h) * nb;
-    const float *binv = t.binv + ((size_t)b * nb * p.G + g) * N;
     Cv cv;
     const int wch = warp * (TP / 16);
-    cv.weights(p, ch + wch);
+    float2 *bound = reinterpret_cast<float2 *>(smem + L::kBound) + warp;
+    const float2 bound_v = cv.weights(p, ch + wch);
+    if (lane == 0) *bound = bound_v;   // (read after a barrier)
     const int n = 32 * (warp & 3) + lane, col0 = (warp >> 2) * kCols;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col0;
     const size_t state = (((size_t)b * p.H + h) * N + n) * p.P + c0 + col0;
@@ -939,25 +960,9 @@ __global__ void __launch_bounds__(kConv + 32, 1)
                   p.T, first, tid);
       }
     };
-    // what finish(i) needs (a block later than the rows, in the place of block i - 2)
-    auto stage_finish = [&](int i) {
-      if (tid >= kConv - N / 4) {
-        const int k = (tid - (kConv - N / 4)) * 4;
-        cp_async16(sb + L::kBinv + (i & 1) * 512 + k * 4, binv + (size_t)i * p.G * N + k);
-      }
-      if (tid == 0) cp_async8(sb + L::kDec + (i & 1) * 8, dec + i);
-      cp_async_commit();
-    };
     bool bad = false;
     // the state after block i, once its products are done
     auto finish = [&](int i) {
-      const float2 d = *reinterpret_cast<const float2 *>(smem + L::kDec + (i & 1) * 8);
-      float a = d.x;
-      // the columns are those that four warps convolve
-      const float4 xi = *reinterpret_cast<const float4 *>(
-          smem + L::kXinv + ((i & 1) * 16 + col0 / (TP / 16)) * 4);
-      const float bi =
-          d.y * *reinterpret_cast<const float *>(smem + L::kBinv + (i & 1) * 512 + (n & (N - 1)) * 4);
       if (n < N) {
         const size_t at = ((((size_t)b * nb + i) * p.H + h) * N) * p.P * 2 +
                           (size_t)((c0 + col0) / 8) * N * 16 + (n >> 3) * 128 + (n & 7) * 16;
@@ -975,52 +980,54 @@ __global__ void __launch_bounds__(kConv + 32, 1)
           }
         }
       }
-      if (tid < TP / 2)
-        t.xinv[((((size_t)b * nb + i) * p.H + h) * p.P + c0) / 2 + tid] =
-            reinterpret_cast<const float *>(smem + L::kXinv)[(i & 1) * 16 + tid / (TP / 32)];
       if (!mbar_wait(bar_d + 8u * (i & 1), (i >> 1) & 1)) {
         bad = true;
         set_status(t.status, KDA_DEVICE_TIMEOUT);
       }
       tc_fence_after();
-      uint32_t hi[kCols / 8][8], lo[kCols / 8][8];
-#pragma unroll
-      for (int k = 0; k < kCols / 8; ++k) {
-        tmem_ld8_nw(tl + (i & 1) * 2 * TP + 8 * k, hi[k]);
-        tmem_ld8_nw(tl + (i & 1) * 2 * TP + TP + 8 * k, lo[k]);
-      }
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < kCols / 8; ++k) {
-        reg_fence8(hi[k]);
-        reg_fence8(lo[k]);
-      }
-      float add[kCols];
-#pragma unroll
-      for (int k = 0; k < kCols; ++k)
-        add[k] = __uint_as_float(hi[k / 8][k % 8]) + __uint_as_float(lo[k / 8][k % 8]);
-      if (IDS && a < 0.f) {     // a reset drops the state whatever it holds
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) s[k] = 0.f;
-        a = 0.f;
-        // B of a run that ended may be NaN or infinite, which times 0 is NaN: then
-        // the tokens that reach the state are added up one by one
-        float odd = 0.f;
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) odd = fmaf(add[k], 0.f, odd);
-        if (__any_sync(0xffffffffu, odd != 0.f) && n < N)
-          tokens_of_state<TP>(smem + L::kX + (i & 1) * L::kXBytes + col0 / 8 * 2048,
-                              t.bhi + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
-                              t.blo + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
-                              wst + (size_t)i * kQ, n, N, add);
-      }
+      const float2 d = *reinterpret_cast<const float2 *>(smem + L::kDec + (i & 3) * 16);
+      const bool drop = IDS && d.x < 0.f;      // a reset drops the state whatever it holds
+      const float a = drop ? 0.f : d.x;
+      // the columns are those that four warps convolve
+      const float4 xi = *reinterpret_cast<const float4 *>(
+          smem + L::kXinv + ((i & 3) * 16 + col0 / (TP / 16)) * 4);
+      const float bi = d.y * __uint_as_float((uint32_t)smem[L::kBexp + (i & 3) * 128 + (n & (N - 1))]
+                                             << 23);
       const float inv[4] = {bi * xi.x, bi * xi.y, bi * xi.z, bi * xi.w};
+      // 8 columns at a time: all 16 at once cost the convolution its registers
 #pragma unroll
-      for (int k = 0; k < kCols; k += 2) {
-        const float v = inv[k / (kCols / 4)];
-        const u64 r = fma2(pk2(a, a), pk2(s[k], s[k + 1]),
-                           mul2(pk2(v, v), pk2(add[k], add[k + 1])));
-        upk2(r, s[k], s[k + 1]);
+      for (int k0 = 0; k0 < kCols; k0 += 8) {
+        uint32_t hi[8], lo[8];
+        tmem_ld8_nw(tl + (i & 1) * 2 * TP + k0, hi);
+        tmem_ld8_nw(tl + (i & 1) * 2 * TP + TP + k0, lo);
+        tmem_wait_ld();
+        reg_fence8(hi);
+        reg_fence8(lo);
+        float add[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add[k] = __uint_as_float(hi[k]) + __uint_as_float(lo[k]);
+        if (drop) {
+          // B of a run that ended may be NaN or infinite, which times 0 is NaN: then
+          // the tokens that reach the state are added up one by one
+          float odd = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            s[k0 + k] = 0.f;
+            odd = fmaf(add[k], 0.f, odd);
+          }
+          if (__any_sync(0xffffffffu, odd != 0.f) && n < N)
+            tokens_of_state<TP>(smem + L::kX + (i & 1) * L::kXBytes + (col0 + k0) / 8 * 2048,
+                                t.bhi + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
+                                t.blo + (((size_t)b * nb + i) * p.G + g) * kQ * N * 2,
+                                wst + (size_t)i * kQ, n, N, add);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          const float v = inv[(k0 + k) / (kCols / 4)];
+          const u64 r = fma2(pk2(a, a), pk2(s[k0 + k], s[k0 + k + 1]),
+                             mul2(pk2(v, v), pk2(add[k], add[k + 1])));
+          upk2(r, s[k0 + k], s[k0 + k + 1]);
+        }
       }
       tc_fence_before();
     };
@@ -1031,7 +1038,6 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     for (; i < nb; ++i, flags = flags_next) {
       cp_async_wait_all();
       if (any_of_conv(bad)) break;   // a wait ran out somewhere: all leave
-      stage_finish(i);
       stage(i + 1);
       if (IDS) flags_next = i + 1 < nb ? t.flags[(size_t)b * nb + i + 1] : 0;
       const float *w = reinterpret_cast<const float *>(smem + L::kW + (i & 1) * kQ * 4);
@@ -1068,15 +1074,15 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       const float inv =
           !IDS || (flags & kPlain)
               ? cv.template run<false>(
-                    rows, warp, lane, tok, true,
+                    rows, warp, lane, tok, bound,
                     [&](int k, u64(&u)[Cv::E], float) { put(k, u, false); })
               : cv.template run<true>(
-                    rows, warp, lane, tok, true,
+                    rows, warp, lane, tok, bound,
                     [&](int k, u64(&u)[Cv::E], float) { put(k, u, true); });
+      if (lane == 0) reinterpret_cast<float *>(smem + L::kXinv)[(i & 3) * 16 + warp] = inv;
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(bar_x + 8u * (i & 1));
-      if (lane == 0) reinterpret_cast<float *>(smem + L::kXinv)[(i & 1) * 16 + warp] = inv;
       if (i > 0) finish(i - 1);
     }
     cp_async_wait_all();
@@ -1240,7 +1246,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
     }
     dlog = t.dlog[((size_t)b * p.H + h_lo + k / subs) * nb + blk];
     if (tid < PT / 2)
-      xi = t.xinv[((((size_t)b * nb + blk) * p.H + h_lo + k / subs) * p.P + k % subs * PT) / 2 + tid];
+      xi = t.xinv[((((size_t)b * nb + blk) * p.H + h_lo + k / subs) * p.P + k % subs * PT + 2 * tid) /
+                  t.xch];
   };
   factors(0);
   const Opnd opC = {sb + L::kC, 128, (uint32_t)N * 16};
@@ -1541,7 +1548,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
 
 template <typename T, int TP>
 cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  size_t smem = 2 * (PrepConv<T, TP>::kBytes + kQ);
+  size_t smem = 2 * (PrepConv<T, TP>::kBytes + kQ) + 16 * sizeof(float2);
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
   // blocks per CTA: up to 8, as long as three waves of CTAs are left (2 rows of
@@ -1601,6 +1608,7 @@ cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaSt
   layout_bufs(p, f32, p.ws, &t);
   t.status = status;
   cudaError_t e;
+  t.xch = 2;
   if (f32) {       // twice the operands: tiles of 32 columns throughout
     e = launch_prep<float, 32>(p, t, cs);
     if (e == cudaSuccess) e = launch_state<float, 32>(p, t, cs);
@@ -1612,6 +1620,7 @@ cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaSt
   // columns: 141 us, 32 columns 246); 32 where half the SMs would have no CTA
   // (a packed row of 32 heads of 128 columns: 118 us, 64 columns 156)
   const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
+  t.xch = narrow ? 2 : 4;            // a state kernel's warp's channels
   e = narrow ? launch_state<bf16, 32>(p, t, cs) : launch_state<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;
   return p.P == 32 ? launch_out<bf16, 32>(p, t, cs) : launch_out<bf16, 64>(p, t, cs);
