@@ -197,11 +197,19 @@ struct Conv {
                  : pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 
-  u64 wt[kSsmTaps][E], bias[E];
+  // A warp's bound on its values and its bias, in shared memory: with 64 columns the
+  // state kernel has no register left for them, and with all of the SM's shared
+  // memory taken a spilled one comes from L2 (2 x 8192 tokens: 158 us, with
+  // seven of them spilled 167).  Two channels keep their bias.
+  struct Consts {
+    float2 bound;        // |u| <= bound.x max|x| + bound.y
+    float bias[CH];
+  };
+  static constexpr bool kKeep = E == 1;
+  u64 wt[kSsmTaps][E], kept;
 
-  // Returns the sum of |w| and the |bias|, the largest of the channels':
-  // |u| <= .x max|x| + .y.
-  __device__ __forceinline__ float2 weights(const SsmParams &p, int channel) {
+  // Loads the weights; lane 0 writes *c, to be read after a barrier.
+  __device__ __forceinline__ void weights(const SsmParams &p, int channel, int lane, Consts *c) {
     float gain = 0.f, base = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -213,12 +221,13 @@ struct Conv {
       wt[3][i] = pk2(a.w, b.w);
       const float b0 = p.bias ? p.bias[channel + 2 * i] : 0.f,
                   b1 = p.bias ? p.bias[channel + 2 * i + 1] : 0.f;
-      bias[i] = pk2(b0, b1);
+      if (kKeep) kept = pk2(b0, b1);
+      else if (lane == 0) c->bias[2 * i] = b0, c->bias[2 * i + 1] = b1;
       gain = fmaxf(gain, fmaxf(fabsf(a.x) + fabsf(a.y) + fabsf(a.z) + fabsf(a.w),
                                fabsf(b.x) + fabsf(b.y) + fabsf(b.z) + fabsf(b.w)));
       base = fmaxf(base, fmaxf(fabsf(b0), fabsf(b1)));
     }
-    return make_float2(gain, base);
+    if (lane == 0) c->bound = make_float2(gain, base);
   }
 
   // x: the row's token 0 at the tile's channel; past: the convolution's cache
@@ -261,22 +270,22 @@ struct Conv {
   // tile at the lane's i-th token, 4 lane + i.  CUT: windows end where a run
   // starts, and padding gives 0; tok holds the tokens' windows.
   //
-  // inv is 1, or with `bound` (what weights returned) a power of two that keeps |u| of the warp's channels
+  // inv is 1, or with `scaled` a power of two that keeps |u| of the warp's channels
   // and the block's tokens below 2^15, by the largest finite input: what u is in
   // fp16 then has 11 bits, and two parts of it 22, down to 2^-29 of the largest.
   // The scale costs no instruction per value (1 / (1 + e) is made with it).
   // Returns inv.
   template <bool CUT, typename F>
   __device__ __forceinline__ float run(const unsigned char *rows, int warp, int lane,
-                                       const unsigned char *tok, const float2 *bound,
-                                       F f) const {
+                                       const unsigned char *tok, const Consts *c,
+                                       bool scaled, F f) const {
     const int at = warp * CH * (int)sizeof(T);
     // rows 4 lane .. 4 lane + 6: two permutations
     const unsigned char *lo = rows + off(4 * lane, at / 16) + at % 16;
     const unsigned char *hi = rows + off(4 * lane + 4, at / 16) + at % 16;
     const uint32_t marks = CUT ? *reinterpret_cast<const uint32_t *>(tok + 4 * lane) : 0;
     uint32_t live = 0x7f;                 // rows that a token's window holds
-    if (CUT && bound) {
+    if (CUT && scaled) {
       live = 0;
 #pragma unroll
       for (int i = 0; i < kStrip; ++i) {
@@ -291,7 +300,7 @@ struct Conv {
       const Raw r =
           *reinterpret_cast<const Raw *>(i < 4 ? lo + i * kRowBytes : hi + (i - 4) * kRowBytes);
       unpack(r, x[i]);
-      if (bound && (live >> i & 1)) {
+      if (scaled && (live >> i & 1)) {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
         constexpr int kWords = (int)sizeof(Raw) / 4;
 #pragma unroll
@@ -301,7 +310,8 @@ struct Conv {
         }
       }
     }
-    const float inv = bound ? fit(larger(top, top2), lo, hi, live, *bound) : 1.f;
+    const float inv = scaled ? fit(larger(top, top2), lo, hi, live, c->bound) : 1.f;
+    const uint32_t bias = smem_u32(c->bias);
     const u64 one = pk2(inv, inv);
 #pragma unroll
     for (int i = 0; i < kStrip; ++i) {
@@ -315,11 +325,11 @@ struct Conv {
           a[1][e] = place >= 2 ? x[i + 1][e] : 0;
           a[2][e] = place >= 1 ? x[i + 2][e] : 0;
         }
-        taps(a[0], a[1], a[2], x[i + 3], one, u);
+        taps(a[0], a[1], a[2], x[i + 3], bias, one, u);
 #pragma unroll
         for (int e = 0; e < E; ++e) u[e] = k & 8 ? u[e] : 0;
       } else {
-        taps(x[i], x[i + 1], x[i + 2], x[i + 3], one, u);
+        taps(x[i], x[i + 1], x[i + 2], x[i + 3], bias, one, u);
       }
       f(i, u, inv);
     }
@@ -361,11 +371,14 @@ struct Conv {
     return *reinterpret_cast<const uint32_t *>(&r);
   }
   __device__ __forceinline__ void taps(const u64 (&a)[E], const u64 (&b)[E], const u64 (&c)[E],
-                                       const u64 (&x)[E], u64 one, u64 (&u)[E]) const {
+                                       const u64 (&x)[E], uint32_t bias, u64 one,
+                                       u64 (&u)[E]) const {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const u64 v = fma2(wt[0][i], a[i],
-                         fma2(wt[1][i], b[i], fma2(wt[2][i], c[i], fma2(wt[3][i], x[i], bias[i]))));
+      u64 v = kept;
+      if (!kKeep)    // (volatile: read for each token)
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(bias + 8 * i));
+      v = fma2(wt[0][i], a[i], fma2(wt[1][i], b[i], fma2(wt[2][i], c[i], fma2(wt[3][i], x[i], v))));
       float e0, e1, d0, d1;
       upk2(mul2(v, pk2(-kLog2e, -kLog2e)), e0, e1);
       upk2(fma2(pk2(ex2(e0), ex2(e1)), one, one), d0, d1);
@@ -667,11 +680,8 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
   };
   stage(blk);
   Cv cv;
-  float2 *bound = reinterpret_cast<float2 *>(smem + 2 * (Cv::kBytes + kQ)) + warp;
-  if (mine) {
-    const float2 v = cv.weights(p, ch + wch);
-    if (lane == 0) *bound = v;         // (read after a barrier)
-  }
+  auto *consts = reinterpret_cast<typename Cv::Consts *>(smem + 2 * (Cv::kBytes + kQ)) + warp;
+  if (mine) cv.weights(p, ch + wch, lane, consts);
   for (; blk < end; ++blk) {
     // whether any token's window leaves the staged rows
     unsigned char *stok = smem + 2 * Cv::kBytes + (blk & 1) * kQ;
@@ -711,8 +721,8 @@ __device__ __forceinline__ void prep_conv(const SsmParams &p, const TcBufs &t, i
     };
     const unsigned char *rows = smem + (blk & 1) * Cv::kBytes;
     const float inv =
-        plain ? cv.template run<false>(rows, warp, lane, stok, is_c ? nullptr : bound, put)
-              : cv.template run<true>(rows, warp, lane, stok, is_c ? nullptr : bound, put);
+        plain ? cv.template run<false>(rows, warp, lane, stok, consts, !is_c, put)
+              : cv.template run<true>(rows, warp, lane, stok, consts, !is_c, put);
     if (!is_c && lane < kPrepCh<T>)
       t.bexp[(((size_t)b * t.nb + blk) * p.G + g) * p.N + n0 + wch + lane] =
           (unsigned char)(__float_as_uint(inv) >> 23);
@@ -796,8 +806,8 @@ struct StateSmem {
   static constexpr uint32_t kXinv = kW + 2 * kQ * 4;          // 4 x [16]: 1 in kX, by warp
   static constexpr uint32_t kBexp = kXinv + 4 * 16 * 4;       // 4 x [128]: bexp
   static constexpr uint32_t kDec = kBexp + 4 * 128;           // 4 x dec
-  static constexpr uint32_t kBound = kDec + 4 * 16;           // [16] float2, by warp
-  static constexpr uint32_t kBar = kBound + 16 * 8;
+  static constexpr uint32_t kConsts = kDec + 4 * 16;          // by warp
+  static constexpr uint32_t kBar = kConsts + 16 * sizeof(typename Cv::Consts);
   static constexpr uint32_t kTmem = kBar + 48;
   static constexpr uint32_t kBytes = kTmem + 16;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -935,9 +945,8 @@ __global__ void __launch_bounds__(kConv + 32, 1)
     const float *wst = t.wst + ((size_t)b * p.H + h) * nb * kQ;
     Cv cv;
     const int wch = warp * (TP / 16);
-    float2 *bound = reinterpret_cast<float2 *>(smem + L::kBound) + warp;
-    const float2 bound_v = cv.weights(p, ch + wch);
-    if (lane == 0) *bound = bound_v;   // (read after a barrier)
+    auto *consts = reinterpret_cast<typename Cv::Consts *>(smem + L::kConsts) + warp;
+    cv.weights(p, ch + wch, lane, consts);
     const int n = 32 * (warp & 3) + lane, col0 = (warp >> 2) * kCols;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col0;
     const size_t state = (((size_t)b * p.H + h) * N + n) * p.P + c0 + col0;
@@ -1074,10 +1083,10 @@ __global__ void __launch_bounds__(kConv + 32, 1)
       const float inv =
           !IDS || (flags & kPlain)
               ? cv.template run<false>(
-                    rows, warp, lane, tok, bound,
+                    rows, warp, lane, tok, consts, true,
                     [&](int k, u64(&u)[Cv::E], float) { put(k, u, false); })
               : cv.template run<true>(
-                    rows, warp, lane, tok, bound,
+                    rows, warp, lane, tok, consts, true,
                     [&](int k, u64(&u)[Cv::E], float) { put(k, u, true); });
       if (lane == 0) reinterpret_cast<float *>(smem + L::kXinv)[(i & 3) * 16 + warp] = inv;
       fence_proxy_async();
@@ -1548,7 +1557,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2)
 
 template <typename T, int TP>
 cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
-  size_t smem = 2 * (PrepConv<T, TP>::kBytes + kQ) + 16 * sizeof(float2);
+  size_t smem = 2 * (PrepConv<T, TP>::kBytes + kQ) + 16 * sizeof(typename PrepConv<T, TP>::Consts);
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
   // blocks per CTA: up to 8, as long as three waves of CTAs are left (2 rows of
