@@ -332,13 +332,12 @@ size_t simt_bytes(const kda_ssm_shape *s) {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // AUTO: the tensor cores, but for long rows of few heads, whose chain of blocks
-// no other CTA hides (bf16, one row of 8192 tokens, N = 64: 1 head of 32 122 us
-// against 47 on the CUDA cores, 8 heads 130 against 111, 18 heads 144 against 206;
-// 4 heads of 1024 tokens 28 against 26, of 700 24 against 25; N = 128, 2000 tokens
-// 44 against 44).  In fp32, where they round more (3e-6 against 1e-7), from the
+// no other CTA hides (bf16, one row of 8192 tokens, N = 64: 1 head of 32 115 us
+// against 43 on the CUDA cores, 8 heads 119 against 125, 18 heads 133 against 240;
+// 4 heads of 1024 tokens 28 against 24; N = 128, 2000 tokens 43 against 43).  In fp32, where they round more (4e-7 against 1e-7), from the
 // size on at which they take about half the time (one row of 8192 tokens, 32 heads
-// of 128, N = 128: 0.37 ms against 3.1; 3 rows of 700 tokens, 6 heads of 64: 36 us
-// against 77; of 997 tokens, heads of 32, N = 64: 38 against 42).
+// of 128, N = 128: 0.40 ms against 3.6; 3 rows of 700 tokens, 6 heads of 64: 39 us
+// against 98; of 997 tokens, heads of 32, N = 64: 37 against 39).
 bool use_tc(const kda_ssm_shape *s, kda_impl impl) {
   if (impl != KDA_IMPL_AUTO) return impl == KDA_IMPL_TC;
   const long long states = (long long)s->B * s->H * s->P * s->N;

@@ -18,7 +18,7 @@
 // powers of two for each few channels of a block (22 bits of what is not 2^18 times
 // smaller than the largest), all four products are added and S is updated in fp32
 // registers, never in the accumulator: 1.5e-7 of the state's norm off, either type,
-// as fp32 arithmetic is (two bf16 parts: 3.4e-6, and 24 us less of the 330 below).
+// as fp32 arithmetic is (two bf16 parts: 3.4e-6, and 20 us less of the 361 below).
 // y of bf16 inputs is rounded to bf16 at the end (1.7e-3).  Of its products'
 // operands x and the 128 x 128 matrix of factors, scaled by rows, are fp16 (2^-12
 // each; x is also what D multiplies), C, B and S bf16, whose errors average out
@@ -28,9 +28,9 @@
 // accumulator loses bits at its own size (2e-7 to 7e-7, where an entering state
 // is most of y; C and B in two parts 2.5e-6, the large products first 1.2e-6).
 //
-// What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 49 us,
-// state 141 us, out 141 us; the row of 8192 tokens of 32 heads of 128 in 25
-// segments: 12, 118 and 74 us.  The state kernel is a chain of 64 blocks on 128
+// What bounds it: 2 rows of 8192 tokens, 64 heads of 64, N = 128: prep 61 us,
+// state 158 us, out 142 us; the row of 8192 tokens of 32 heads of 128 in 25
+// segments: 16, 129 and 70 us.  The state kernel is a chain of 64 blocks on 128
 // SMs, each its convolution's instructions and two barriers long; the other two
 // are at the rate of their instructions and of exp2 and reciprocals.  (The
 // first kernels of this form took 9.8 and 9.5 ms on the CUDA cores.)
@@ -182,7 +182,7 @@ struct Conv {
   // The lanes of a warp read rows 4 apart: rows of 128 bytes are permuted in
   // 16-byte pieces by the row's strip, strips of 64-byte rows lie 16 bytes
   // further apart than their rows fill (either way over 8 places of 16
-  // bytes; over 4, the packed row of 32 heads took 125 us instead of 118).
+  // bytes; over 4, the packed row of 32 heads took 7 us longer).
   static __device__ __forceinline__ uint32_t off(int row, int piece16) {
     return kRowBytes == 128
                ? (uint32_t)(row * 128 + ((piece16 ^ (row >> 2 & 7)) << 4))
@@ -506,7 +506,8 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 // inputs they are kept in one, so c_r - c_j is off by a step of the sum or a few:
 // 6e-5 each at kWide.  Beyond it the sums are made in two floats and rounded
 // once, and a token's a counts down to kFar only: the sum stays above -2^15, one
-// step is 2^-9 and a factor off by 1.4e-3 at most, less than half a step of bf16.
+// step is 2^-9 and a factor, of three sums rounded so, off by 2e-3 at most, half a
+// step of bf16.
 // The largest finite width of four.
 __device__ __forceinline__ float finite_max(const float4 &w) {
   auto in = [](float v) { return v > 0.f && v < CUDART_INF_F ? v : 0.f; };
@@ -1561,8 +1562,8 @@ cudaError_t launch_prep(const SsmParams &p, const TcBufs &t, cudaStream_t cs) {
   const size_t f = (kQ + 8) * 4 + kQ * 33 * 4;
   if (f > smem) smem = f;
   // blocks per CTA: up to 8, as long as three waves of CTAs are left (2 rows of
-  // 8192 tokens, 8 groups: 1 block 63 us, 4 49 us; one row, one group: 1 block 12
-  // us, 8 20 us)
+  // 8192 tokens, 8 groups: 4 blocks take 14 us less than 1; one row, one group: 8
+  // take 8 us more)
   const long long tiles = (long long)p.B * t.nb * p.G * (2 * p.N / TP);
   long long run = tiles / (6ll * num_sms());
   run = run < 1 ? 1 : run > 8 ? 8 : run;
@@ -1626,8 +1627,9 @@ cudaError_t launch_ssm_tc(const SsmParams &p, bool f32, uint32_t *status, cudaSt
   e = p.N == 32 ? launch_prep<bf16, 32>(p, t, cs) : launch_prep<bf16, 64>(p, t, cs);
   if (e != cudaSuccess) return e;
   // 64-column tiles halve the traffic of B's tiles (2 rows of 64 heads of 64
-  // columns: 141 us, 32 columns 246); 32 where half the SMs would have no CTA
-  // (a packed row of 32 heads of 128 columns: 118 us, 64 columns 156)
+  // columns: 158 us; measured before the scales 141, with 32 columns 246); 32
+  // where half the SMs would have no CTA (a packed row of 32 heads of 128 columns:
+  // 129 us; before the scales 118, with 64 columns 156)
   const bool narrow = p.P == 32 || (long long)p.B * p.H * (p.P / 64) * 2 <= num_sms();
   t.xch = narrow ? 2 : 4;            // a state kernel's warp's channels
   e = narrow ? launch_state<bf16, 32>(p, t, cs) : launch_state<bf16, 64>(p, t, cs);
