@@ -539,6 +539,9 @@ typedef struct kda_ssm_shape {
  *                 inputs (1.8e-3 to 2.2e-3 off, its own rounding being 1.7e-3; up
  *                 to 2.9e-3 where an entering state is most of y) and two of
  *                 fp32 inputs, three of B and C (2e-7 to 7e-7).
+ *                 A channel's values in 128 tokens share a power of two there:
+ *                 what is 2^29 times smaller than its largest finite neighbour
+ *                 (padding aside) loses digits.
  *                 KDA_IMPL_AUTO: SIMT for rows of T >= 16 N tokens where B H P N
  *                 is at most 2^14, and for fp32 where B H P N T is at most
  *                 2^26; else TC.  A caller who wants one arithmetic at every
