@@ -262,12 +262,16 @@ def _on_its_stream(f):
     @functools.wraps(f)
     def call(*args, **kw):
         stream = args[at] if len(args) > at else kw.get("stream")
-        if stream is None or stream == torch.cuda.current_stream(stream.device):
+        if stream is None or not _elsewhere(stream):
             return f(*args, **kw)
         with torch.cuda.stream(stream):
             return f(*args, **kw)
 
     return call
+
+
+def _elsewhere(stream):
+    return stream != torch.cuda.current_stream(stream.device)
 
 
 @_on_its_stream
@@ -635,7 +639,8 @@ def clear_device_status(workspace, stream=None) -> None:
 #
 # Single-token calls take a few microseconds on the GPU, so the host side of
 # these calls is kept short: descriptors are made once per shape, a tensor is
-# checked by four attribute reads, and messages are made only to be raised.
+# checked by four attribute reads, messages are made only to be raised, and a
+# call with a stream calls itself under it instead of being wrapped.
 
 _f32, _i32 = torch.float32, torch.int32
 
@@ -743,7 +748,6 @@ def alloc_step_workspace(B, H, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-@_on_its_stream
 def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_state=None,
          l2norm_qk=False, out=None, workspace=None, stream=None):
     """One token per sequence through the delta rule, on cached states.
@@ -757,6 +761,10 @@ def step(q, k, v, g, beta, state, scale=None, slots=None, conv_w=None, conv_stat
     inputs of the convolution; after a prompt it holds the last three inputs of
     short_conv_silu of each sequence, zeros where there were fewer.  Returns o
     [B,H,V]."""
+    if stream is not None and _elsewhere(stream):
+        with torch.cuda.stream(stream):
+            return step(q, k, v, g, beta, state, scale, slots, conv_w, conv_state, l2norm_qk, out,
+                        workspace)
     dev, dt = _start(q, "step")
     B, H, K = q.shape
     V = v.shape[-1]
@@ -818,7 +826,6 @@ def _tokens(t, name, shape, dtype, device):
     return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
 
 
-@_on_its_stream
 def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=None, D=None,
             z=None, initial_state=None, conv_state=None, segment_ids=None,
             output_final_state=False, out=None, workspace=None, impl="auto", stream=None):
@@ -836,6 +843,13 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     and fp32 problems of up to 2^26 products of states and tokens.
     Returns ``(y [B,T,H,P], final_state, conv_state_out)``, the last two None
     unless ``output_final_state``."""
+    if stream is not None and _elsewhere(stream):
+        with torch.cuda.stream(stream):
+            return ssm_fwd(xbc, dt, conv_w, A, head_dim=head_dim, state_dim=state_dim,
+                           conv_bias=conv_bias, dt_bias=dt_bias, D=D, z=z,
+                           initial_state=initial_state, conv_state=conv_state,
+                           segment_ids=segment_ids, output_final_state=output_final_state,
+                           out=out, workspace=workspace, impl=impl)
     dev, ty = _start(xbc, "ssm_fwd")
     B, T, _ = xbc.shape
     H, P, N, G, C = _ssm_dims(xbc, A, head_dim, state_dim)
@@ -865,13 +879,17 @@ def ssm_fwd(xbc, dt, conv_w, A, *, head_dim, state_dim, conv_bias=None, dt_bias=
     return y, fs, conv
 
 
-@_on_its_stream
 def ssm_step(xbc, dt, conv_w, A, state, conv_state, *, head_dim, state_dim, conv_bias=None,
              dt_bias=None, D=None, z=None, slots=None, out=None, workspace=None, stream=None):
     """One token per sequence through the state space operator, on cached
     states: xbc [B,H*P+2*G*N], z [B,H*P] or None, dt [B,H] (any stride between
     the rows); state [n_slots,H,N,P] fp32 and conv_state [n_slots,3,channels]
     are moved on in place; ``slots`` as :func:`step`.  Returns y [B,H,P]."""
+    if stream is not None and _elsewhere(stream):
+        with torch.cuda.stream(stream):
+            return ssm_step(xbc, dt, conv_w, A, state, conv_state, head_dim=head_dim,
+                            state_dim=state_dim, conv_bias=conv_bias, dt_bias=dt_bias, D=D, z=z,
+                            slots=slots, out=out, workspace=workspace)
     dev, ty = _start(xbc, "ssm_step")
     B = xbc.shape[0]
     H, P, N, G, C = _ssm_dims(xbc, A, head_dim, state_dim)
@@ -921,7 +939,6 @@ def _norm_desc(y, gate, gate_act, scale, eps):
     return _norm_ref(rows, D, DTYPES[y.dtype], act, grows, scale, eps), rows, (D,)
 
 
-@_on_its_stream
 def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale=1.0, w_pre=None,
                eps=1e-6, save_stats=False, out=None, stream=None):
     """The norm after a block, its gate and residual scale, and the norm
@@ -934,6 +951,10 @@ def block_norm(y, w_post, *, residual=None, gate=None, gate_act="sigmoid", scale
     None.  ``out`` may be the residual itself, but not with ``save_stats``:
     block_norm_bwd reads the residual.  Returns ``(out, x or None)``, and the
     statistics block_norm_bwd reads when ``save_stats``."""
+    if stream is not None and _elsewhere(stream):
+        with torch.cuda.stream(stream):
+            return block_norm(y, w_post, residual=residual, gate=gate, gate_act=gate_act,
+                              scale=scale, w_pre=w_pre, eps=eps, save_stats=save_stats, out=out)
     dev, ty = _start(y, "block_norm")
     shape = y.shape
     d, rows, width = _norm_desc(y, gate, gate_act, scale, eps)
@@ -971,13 +992,17 @@ def alloc_block_norm_workspace(rows, D, gate_rows=0, device=None) -> torch.Tenso
                     "kda_block_norm_bwd_workspace_size", 0)[0]
 
 
-@_on_its_stream
 def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=None,
                    gate_act="sigmoid", scale=1.0, w_pre=None, eps=1e-6, workspace=None,
                    stream=None):
     """Gradients of block_norm from its inputs and statistics, given the
     gradients of ``out`` and ``x`` (one of them may be None): ``(dy, d_residual,
     d_gate, dw_post, dw_pre)``, None in the place of an input that was None."""
+    if stream is not None and _elsewhere(stream):
+        with torch.cuda.stream(stream):
+            return block_norm_bwd(y, w_post, stats, d_out, d_x=d_x, residual=residual, gate=gate,
+                                  gate_act=gate_act, scale=scale, w_pre=w_pre, eps=eps,
+                                  workspace=workspace)
     dev, ty = _start(y, "block_norm_bwd")
     shape = y.shape
     d, rows, width = _norm_desc(y, gate, gate_act, scale, eps)
