@@ -323,7 +323,9 @@ constexpr Built kBuilt[] = {{2, 8, 1, 256}, {2, 8, 1, 512}, {2, 8, 2, 512}, {2, 
                             {4, 4, 8, 512}, {4, 1, 4, 256}, {4, 1, 4, 512}, {4, 1, 16, 1024}};
 
 // Units (CTAs) of the backward: as many as are resident on 152 SMs at up to
-// 128 registers per thread, and no more than there are row groups.
+// 128 registers per thread, and no more than there are row groups.  (152 and not
+// what this device has: the workspace's size goes by it, and may be asked for
+// where there is no device.)
 int units_for(const kda_norm_desc *d, const Layout &l) {
   const long long most = 152ll * (l.tpr * l.rg > 256 ? 1 : 2);
   const long long n = (d->rows + l.rg - 1) / l.rg;

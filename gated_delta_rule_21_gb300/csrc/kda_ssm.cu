@@ -63,7 +63,8 @@ constexpr int kThreads = 256, kCols = 32, kTok = 32, kWarps = kThreads / 32;
 // the states that enter the segments are chained, and a second pass makes y:
 // twice the work on the states, but a short row of few heads no longer waits
 // for one chain of tokens (3 rows of 997 tokens, 6 heads: 576 us in one chain,
-// 42 us in segments of 32 tokens).
+// 42 us in segments of 32 tokens).  152 SMs, and not what this device has: the
+// workspace's size goes by it, which may be asked for where there is no device.
 struct SimtCut {
   int segs, len;
 };
