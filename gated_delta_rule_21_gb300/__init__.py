@@ -19,6 +19,11 @@ Entry points (same names as the C ABI, minus the ``kda_`` prefix):
   with its short convolution, on prompts and on single tokens.
 * :func:`block_norm`, :func:`block_norm_bwd` -- the norms before and after a
   block fused with its gate and residual scale, and their gradients.
+* :func:`rotate` -- the position rotation of queries and keys, and back.
+* :func:`latent_fwd`, :func:`latent_bwd` -- attention with keys and values from
+  one latent vector a token, expanded per head: prompts, and the gradients.
+* :func:`latent_append`, :func:`latent_step` -- the latents of new tokens into a
+  paged cache, and the absorbed form of that attention over it.
 * :func:`workspace_size`, :func:`read_device_status`,
   :func:`clear_device_status`, :func:`status_string`, :func:`version`.
 * :func:`lib` -- the raw ctypes library with typed signatures.
@@ -66,6 +71,29 @@ class kda_norm_desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_longlong), ("dim", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("gate_act", ctypes.c_int), ("gate_rows", ctypes.c_longlong),
                 ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class kda_rotate_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "dim", "dtype", "pairs", "inverse")] + \
+        [(n, ctypes.c_longlong) for n in ("x_stride_b", "x_stride_t", "x_stride_h", "y_stride_b",
+                                          "y_stride_t", "y_stride_h")]
+
+
+class kda_latent_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "max_pages", "n_pages", "page_size",
+                                            "C", "R", "dtype")] + \
+        [(n, ctypes.c_longlong) for n in (
+            "page_stride", "token_stride", "q_stride_b", "q_stride_t", "q_stride_h",
+            "q_rope_stride_b", "q_rope_stride_t", "q_rope_stride_h", "latent_stride_b",
+            "latent_stride_t", "k_rope_stride_b", "k_rope_stride_t")]
+
+
+class kda_latent_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "K", "R", "V", "dtype")] + \
+        [(n, ctypes.c_longlong) for n in (
+            "q_stride_b", "q_stride_t", "q_stride_h", "q_rope_stride_b", "q_rope_stride_t",
+            "q_rope_stride_h", "k_stride_b", "k_stride_t", "k_stride_h", "k_rope_stride_b",
+            "k_rope_stride_t", "v_stride_b", "v_stride_t", "v_stride_h")]
 
 
 class kda_shape(ctypes.Structure):
@@ -169,6 +197,22 @@ def lib():
         L.kda_block_norm_bwd_workspace_size.restype = u64
         L.kda_block_norm_bwd.argtypes = [ndp] + [vp] * 14 + [u64, vp]
         L.kda_block_norm_bwd.restype = i
+        rdp, lcp, lsp = (ctypes.POINTER(c) for c in (kda_rotate_desc, kda_latent_cache,
+                                                     kda_latent_shape))
+        L.kda_rotate.argtypes = [rdp] + [vp] * 5
+        L.kda_rotate.restype = i
+        L.kda_latent_append.argtypes = [lcp] + [vp] * 4 + [i] + [vp] * 6
+        L.kda_latent_append.restype = i
+        L.kda_latent_step_workspace_size.argtypes = [lcp]
+        L.kda_latent_step_workspace_size.restype = u64
+        L.kda_latent_step.argtypes = [lcp] + [vp] * 6 + [f] + [vp] * 3 + [u64, i, vp]
+        L.kda_latent_step.restype = i
+        L.kda_latent_workspace_size.argtypes = [lsp, i]
+        L.kda_latent_workspace_size.restype = u64
+        L.kda_latent_fwd.argtypes = [lsp] + [vp] * 5 + [f] + [vp] * 4 + [u64, i, vp]
+        L.kda_latent_fwd.restype = i
+        L.kda_latent_bwd.argtypes = [lsp] + [vp] * 5 + [f] + [vp] * 10 + [u64, i, vp]
+        L.kda_latent_bwd.restype = i
         L.kda_selftest_wait_timeout.argtypes = [vp, ctypes.c_longlong, vp]
         L.kda_selftest_wait_timeout.restype = i
         _lib = L
@@ -1030,3 +1074,317 @@ def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=Non
     if st != KDA_OK:
         raise KdaError(st, "kda_block_norm_bwd")
     return dy, dres, dgate, dw_post, dw_pre
+
+
+# ---------------------------------------------------------------------------
+# attention over one shared latent vector a token
+#
+# A call goes to the device of its tensors, whichever is current.
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotate_ref(*fields):
+    return ctypes.byref(kda_rotate_desc(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_ref(*fields):
+    return ctypes.byref(kda_latent_cache(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _latent_ref(*fields):
+    return ctypes.byref(kda_latent_shape(*fields))
+
+
+def _strided(t, name, shape, dtype, device):
+    """Address and strides of a tensor whose last dimension is contiguous; the
+    stride of a dimension of 1 means nothing and is given as 0."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device):
+        _refuse(t, name, shape, dtype, device, False)
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), tuple([s if n > 1 else 0 for s, n in zip(st[:-1], shape)])
+
+
+def _moved(f, x, stream, args, kw):
+    """The call made on ``stream`` or on the tensors' device where either is not
+    the current one; None where both are."""
+    if stream is not None and _elsewhere(stream):
+        with torch.cuda.stream(stream):
+            return (f(*args, **kw),)
+    if x.is_cuda and x.get_device() != torch.cuda.current_device():
+        with torch.cuda.device(x.get_device()):
+            return (f(*args, **kw),)
+    return None
+
+
+_NONE3, _NONE2 = (0, 0, 0), (0, 0)
+
+
+def _scratch_here(workspace, need, device, where):
+    """_scratch of a device, with a header of 256 bytes."""
+    ws, n = _scratch(workspace, need, device, where, 256)
+    if ws.get_device() != device:
+        raise ValueError(f"workspace is on {ws.device}, expected cuda:{device}")
+    return ws, n
+
+
+def rotate(x, inv_freq, *, positions=None, pairs=True, inverse=False, out=None, stream=None):
+    """The position rotation: pairs (a, b) of the last dimension turned by
+    ``positions * inv_freq`` to ``(a cos - b sin, b cos + a sin)``, or back with
+    ``inverse`` (its gradient).
+
+    x: [B,T,H,dim] or [B,T,dim] (bf16 or fp32, the last dimension contiguous, any
+    other strides); inv_freq: [dim/2] fp32; positions: [B,T] int32 (None: 0 ..
+    T-1).  ``pairs``: (x[2i], x[2i+1]), else (x[i], x[i+dim/2]).  ``out`` may be x
+    itself; returns it, or a new contiguous tensor."""
+    moved = _moved(rotate, x, stream, (x, inv_freq), dict(positions=positions, pairs=pairs,
+                                                          inverse=inverse, out=out))
+    if moved:
+        return moved[0]
+    dev, ty = _start(x, "rotate")
+    if x.dim() not in (3, 4) or x.numel() == 0:
+        raise ValueError(f"x must be [B,T,H,dim] or [B,T,dim] and not empty, got {tuple(x.shape)}")
+    B, T, dim = x.shape[0], x.shape[1], x.shape[-1]
+    H = x.shape[2] if x.dim() == 4 else 1
+    if dim % 2:
+        raise ValueError(f"the last dimension of x must be even, got {dim}")
+    xp, xs = _strided(x, "x", x.shape, ty, dev)
+    if out is None:
+        out = x.new_empty(x.shape)
+    yp, ys = _strided(out, "out", x.shape, ty, dev)
+    if x.dim() == 3:
+        xs, ys = xs + (0,), ys + (0,)
+    d = _rotate_ref(B, T, H, dim, DTYPES[ty], int(bool(pairs)), int(bool(inverse)), *xs, *ys)
+    st = _lib_now().kda_rotate(d, xp, _at(positions, "positions", (B, T), _i32, dev),
+                               _at(inv_freq, "inv_freq", (dim // 2,), _f32, dev), yp,
+                               _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rotate")
+    return out
+
+
+def _cache_dims(cache, page_table, T, H, C, dev, ty, where):
+    """What a call reads off its cache and page table: the leading fields of the
+    descriptor, its strides, and the addresses of both."""
+    if cache.dim() != 3:
+        raise ValueError(f"cache must be [n_pages, page_size, C + R], got {tuple(cache.shape)}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [B, max_pages], got {tuple(page_table.shape)}")
+    R = cache.shape[2] - C
+    if R < 0:
+        raise ValueError(f"{where}: the cache holds {cache.shape[2]} values a token, "
+                         f"less than a latent's {C}")
+    cp, cs = _strided(cache, "cache", cache.shape, ty, dev)
+    B, M = page_table.shape
+    return (B, T, H, M, cache.shape[0], cache.shape[1], C, R, DTYPES[ty]), cs, cp, \
+        _at(page_table, "page_table", (B, M), _i32, dev), R
+
+
+def latent_append(latent, k_rope, cache, page_table, lengths, *, inv_freq=None, new=None,
+                  q_rope=None, pairs=True, q_out=None, stream=None):
+    """New tokens' latents and keys into a paged cache, the keys (and queries)
+    rotated at the tokens' positions on the way.
+
+    latent: [B,T,C], k_rope: [B,T,R] or None (R = 0), q_rope: [B,T,H,R] or None, of
+    the cache's dtype (bf16 or fp32), the last dimension contiguous; cache:
+    [n_pages, page_size, C + R], written in place; page_table: [B,max_pages] int32
+    (a page outside the cache takes nothing); lengths: [B] int32, each sequence's
+    tokens with its new ones; ``new`` [B] int32: how many of the T tokens are
+    there (None: all).  inv_freq [R/2] fp32 and ``pairs`` as :func:`rotate` (None:
+    keys are copied).  No page that is written may belong to two sequences.
+    Returns the rotated queries [B,T,H,R] (``q_out``, contiguous), or None."""
+    moved = _moved(latent_append, latent, stream, (latent, k_rope, cache, page_table, lengths),
+                   dict(inv_freq=inv_freq, new=new, q_rope=q_rope, pairs=pairs, q_out=q_out))
+    if moved:
+        return moved[0]
+    dev, ty = _start(latent, "latent_append")
+    if latent.dim() != 3:
+        raise ValueError(f"latent must be [B,T,C], got {tuple(latent.shape)}")
+    B, T, C = latent.shape
+    H = 1 if q_rope is None else q_rope.shape[-2]
+    head, cs, cp, tp, R = _cache_dims(cache, page_table, T, H, C, dev, ty, "latent_append")
+    lp, ls = _strided(latent, "latent", (head[0], T, C), ty, dev)
+    kp, ks, qp, qs, op = None, _NONE2, None, _NONE3, None
+    if k_rope is None:
+        if R:
+            raise ValueError(f"k_rope is missing: the cache holds {R} values beside the latent")
+    else:
+        kp, ks = _strided(k_rope, "k_rope", (B, T, R), ty, dev)
+    if q_rope is not None:
+        qp, qs = _strided(q_rope, "q_rope", (B, T, H, R), ty, dev)
+        if q_out is None:
+            q_out = q_rope.new_empty((B, T, H, R))
+        op = _at(q_out, "q_out", (B, T, H, R), ty, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q_rope")
+    d = _cache_ref(*head, *cs, *_NONE3, *qs, *ls, *ks)
+    st = _lib_now().kda_latent_append(
+        d, lp, kp, qp, _at(inv_freq, "inv_freq", (R // 2,), _f32, dev), int(bool(pairs)), tp,
+        _at(lengths, "lengths", (B,), _i32, dev), _at(new, "new", (B,), _i32, dev), cp, op,
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_append")
+    return q_out
+
+
+def latent_step_workspace_size(B, T, H, C) -> int:
+    """Workspace bytes of :func:`latent_step` (0 when the shape is not served)."""
+    s = kda_latent_cache(int(B), int(T), int(H), 1, 1, 1, int(C))
+    return int(lib().kda_latent_step_workspace_size(s))
+
+
+def alloc_latent_step_workspace(B, T, H, C, device=None) -> torch.Tensor:
+    """Workspace of :func:`latent_step`, its header zero-filled (one for each
+    stream that makes such calls)."""
+    return _scratch(None, latent_step_workspace_size(B, T, H, C), device or "cuda",
+                    "kda_latent_step_workspace_size", 256)[0]
+
+
+def latent_step(q, q_rope, cache, page_table, lengths, *, scale, new=None, return_lse=False,
+                out=None, workspace=None, impl="auto", stream=None):
+    """The absorbed form over a paged cache: a few new tokens of each sequence
+    attend to all latents up to themselves, which :func:`latent_append` has put
+    into the cache, the new ones among them.
+
+    q: [B,T,H,C] (queries moved to the latents' side), q_rope: [B,T,H,R] or None,
+    of the cache's dtype, the last dimension contiguous; cache, page_table, lengths
+    and ``new`` as :func:`latent_append`.  ``scale`` is that of the scores (of the
+    expanded form, (K+R)**-0.5).  ``impl``: "simt" computes in fp32 on the CUDA
+    cores, "tc" on the tensor cores (bf16; the softmax's weights are rounded to
+    bf16), "auto" takes "tc" where it serves the layout.  Returns o [B,T,H,C], the
+    weighted latents, 0 for a token that is not there, and with ``return_lse`` the
+    log sum of exp of the scores [B,H,T] fp32."""
+    moved = _moved(latent_step, q, stream, (q, q_rope, cache, page_table, lengths),
+                   dict(scale=scale, new=new, return_lse=return_lse, out=out,
+                        workspace=workspace, impl=impl))
+    if moved:
+        return moved[0]
+    dev, ty = _start(q, "latent_step")
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B,T,H,C], got {tuple(q.shape)}")
+    B, T, H, C = q.shape
+    head, cs, cp, tp, R = _cache_dims(cache, page_table, T, H, C, dev, ty, "latent_step")
+    qp, qs = _strided(q, "q", (head[0], T, H, C), ty, dev)
+    rp, rs = None, _NONE3
+    if q_rope is None:
+        if R:
+            raise ValueError(f"q_rope is missing: the cache holds {R} values beside the latent")
+    else:
+        rp, rs = _strided(q_rope, "q_rope", (B, T, H, R), ty, dev)
+    o = q.new_empty((B, T, H, C)) if out is None else out
+    lse = torch.empty((B, H, T), dtype=_f32, device=q.device) if return_lse else None
+    d = _cache_ref(*head, *cs, *qs, *rs, 0, 0, 0, 0)
+    L = _lib_now()
+    ws, n = _scratch_here(workspace, L.kda_latent_step_workspace_size(d) if workspace is None else 0, dev,
+                          "kda_latent_step_workspace_size")
+    st = L.kda_latent_step(
+        d, qp, rp, cp, tp, _at(lengths, "lengths", (B,), _i32, dev),
+        _at(new, "new", (B,), _i32, dev), scale, _at(o, "out", (B, T, H, C), ty, dev),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_step")
+    return (o, lse) if return_lse else o
+
+
+def latent_workspace_size(B, T, H, R, backward=False) -> int:
+    """Workspace bytes of :func:`latent_fwd`, or with ``backward`` of both it and
+    :func:`latent_bwd` (0 when the shape is not served)."""
+    s = kda_latent_shape(int(B), int(T), int(H), 32, int(R), 32)
+    return int(lib().kda_latent_workspace_size(s, int(bool(backward))))
+
+
+def alloc_latent_workspace(B, T, H, R, backward=False, device=None) -> torch.Tensor:
+    """Workspace of :func:`latent_fwd` and :func:`latent_bwd`, its header
+    zero-filled (one for each stream that makes such calls)."""
+    return _scratch(None, latent_workspace_size(B, T, H, R, backward), device or "cuda",
+                    "kda_latent_workspace_size", 256)[0]
+
+
+def _latent_inputs(q, k, v, q_rope, k_rope, where):
+    dev, ty = _start(q, where)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"{where}: q and v must be [B,T,H,K] and [B,T,H,V]")
+    B, T, H, K = q.shape
+    V, R = v.shape[3], 0
+    qp, qs = _strided(q, "q", q.shape, ty, dev)
+    kp, ks = _strided(k, "k", (B, T, H, K), ty, dev)
+    vp, vs = _strided(v, "v", (B, T, H, V), ty, dev)
+    rp = sp = None
+    rs, ss = _NONE3, _NONE2
+    if (q_rope is None) != (k_rope is None):
+        raise ValueError("q_rope and k_rope come together")
+    if q_rope is not None:
+        R = q_rope.shape[-1]
+        rp, rs = _strided(q_rope, "q_rope", (B, T, H, R), ty, dev)
+        sp, ss = _strided(k_rope, "k_rope", (B, T, R), ty, dev)
+    d = _latent_ref(B, T, H, K, R, V, DTYPES[ty], *qs, *rs, *ks, *ss, *vs)
+    return dev, ty, (B, T, H, K, R, V), d, (qp, rp, kp, sp, vp)
+
+
+def latent_fwd(q, k, v, *, q_rope=None, k_rope=None, scale=None, segment_ids=None,
+               save_lse=False, out=None, workspace=None, impl="auto", stream=None):
+    """The expanded form on prompts: causal attention with keys ``[k | k_rope]``,
+    k_rope shared by the heads.
+
+    q, k: [B,T,H,K], v: [B,T,H,V], q_rope: [B,T,H,R], k_rope: [B,T,R] (both None:
+    R = 0), bf16 or fp32, the last dimension contiguous and the others at any
+    stride, so slices of projections will do; segment_ids as :func:`chunk_fwd`
+    (a token sees its own run up to itself).  ``scale`` None means (K+R)**-0.5.
+    ``impl``: "simt" computes in fp32 on the CUDA cores, "tc" on the tensor cores
+    (bf16; the softmax's weights are rounded to bf16), "auto" takes "tc" where it
+    serves the layout.  Returns o [B,T,H,V], and with ``save_lse`` also what
+    :func:`latent_bwd` reads, the log sum of exp of the scores [B,H,T] fp32."""
+    moved = _moved(latent_fwd, q, stream, (q, k, v),
+                   dict(q_rope=q_rope, k_rope=k_rope, scale=scale, segment_ids=segment_ids,
+                        save_lse=save_lse, out=out, workspace=workspace, impl=impl))
+    if moved:
+        return moved[0]
+    dev, ty, (B, T, H, K, R, V), d, ptrs = _latent_inputs(q, k, v, q_rope, k_rope, "latent_fwd")
+    o = q.new_empty((B, T, H, V)) if out is None else out
+    lse = torch.empty((B, H, T), dtype=_f32, device=q.device) if save_lse else None
+    L = _lib_now()
+    ws, n = _scratch_here(workspace, L.kda_latent_workspace_size(d, 0) if workspace is None else 0, dev,
+                          "kda_latent_workspace_size")
+    st = L.kda_latent_fwd(
+        d, *ptrs, (K + R) ** -0.5 if scale is None else scale,
+        _at(segment_ids, "segment_ids", (B, T), _i32, dev), _at(o, "out", (B, T, H, V), ty, dev),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_fwd")
+    return (o, lse) if save_lse else o
+
+
+def latent_bwd(q, k, v, o, lse, d_o, *, q_rope=None, k_rope=None, scale=None, segment_ids=None,
+               workspace=None, impl="auto", stream=None):
+    """Gradients of latent_fwd from its inputs, its o and lse, and the gradient
+    ``d_o`` [B,T,H,V] of o: ``(dq, dk, dv, dq_rope, dk_rope)``, contiguous, of the
+    inputs' dtype (the last two None without a rope part; dk_rope [B,T,R] is the
+    sum over the heads).  Repeated calls agree bit for bit."""
+    moved = _moved(latent_bwd, q, stream, (q, k, v, o, lse, d_o),
+                   dict(q_rope=q_rope, k_rope=k_rope, scale=scale, segment_ids=segment_ids,
+                        workspace=workspace, impl=impl))
+    if moved:
+        return moved[0]
+    dev, ty, (B, T, H, K, R, V), d, ptrs = _latent_inputs(q, k, v, q_rope, k_rope, "latent_bwd")
+    dq, dk, dv = (q.new_empty((B, T, H, n)) for n in (K, K, V))
+    dqr = dkr = None
+    if R:
+        dqr, dkr = q.new_empty((B, T, H, R)), q.new_empty((B, T, R))
+    L = _lib_now()
+    ws, n = _scratch_here(workspace, L.kda_latent_workspace_size(d, 1) if workspace is None else 0, dev,
+                          "kda_latent_workspace_size")
+    st = L.kda_latent_bwd(
+        d, *ptrs, (K + R) ** -0.5 if scale is None else scale,
+        _at(segment_ids, "segment_ids", (B, T), _i32, dev), _at(o, "o", (B, T, H, V), ty, dev),
+        _at(lse, "lse", (B, H, T), _f32, dev), _at(d_o, "d_o", (B, T, H, V), ty, dev),
+        dq.data_ptr(), None if dqr is None else dqr.data_ptr(), dk.data_ptr(),
+        None if dkr is None else dkr.data_ptr(), dv.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_bwd")
+    return dq, dk, dv, dqr, dkr

@@ -1,0 +1,706 @@
+// kda_latent.cu -- the expanded latent attention: entry points, the table of
+// runs, the small kernels around the backward, and the fp32 kernels on the
+// CUDA cores, which serve every type and layout.
+//
+// CUDA cores: a CTA of 256 threads holds 64 queries (forward, gradient of the
+// queries) or 64 keys (gradients of keys and values) of one head in shared
+// memory as fp32 and walks the other side in tiles of 64.  A thread makes a
+// 4 x 4 piece of the tile of scores with packed multiply-adds (two terms of the
+// sum at once) and 4 rows of the outputs.  What bounds it: shared memory, 3 of
+// 4 cycles of the multiply-adds.
+#include <string.h>
+
+#include "kda_f32x2.cuh"
+#include "kda_latent.cuh"
+
+namespace kda {
+namespace latent {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlk = 64;          // rows of a tile, either side
+constexpr int kLdP = kBlk + 4;    // of a tile of weights
+
+// Rows t0 .. t0 + 63 of [x | xr] (n and nr values) as fp32, zeros from row `lim` on.
+template <typename T>
+__device__ __forceinline__ void load_rows(float *dst, int ld, const T *x, long long st, int n,
+                                          const T *xr, long long str, int nr, int t0, int lim) {
+  const int w = n + nr;
+  for (int i = threadIdx.x; i < kBlk * w; i += kThreads) {
+    const int r = i / w, c = i % w;
+    float v = 0.f;
+    if (t0 + r < lim) v = to_f32(c < n ? x[(t0 + r) * st + c] : xr[(t0 + r) * str + c - n]);
+    dst[r * ld + c] = v;
+  }
+}
+
+// s[i][j] = sum_c a[4 ty + i][c] b[tx + 16 j][c] over n (a multiple of 4) values.
+__device__ __forceinline__ void rows_by_rows(const float *a, int lda, const float *b, int ldb,
+                                             int n, int ty, int tx, float (&s)[4][4]) {
+  u64 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+  a += 4 * ty * lda;
+  b += tx * ldb;
+#pragma unroll 2
+  for (int c = 0; c < n; c += 4) {
+    ulonglong2 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2 *>(a + i * lda + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2 *>(b + 16 * j * ldb + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fma2(x[i].x, y[j].x, acc[i][j]);
+        acc[i][j] = fma2(x[i].y, y[j].y, acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      upk2(acc[i][j], lo, hi);
+      s[i][j] = lo + hi;
+    }
+}
+
+// acc[i][q] += sum_k w[4 ty + i][k] y[k][4 tx + 64 q ..] over the tile's 64 k.
+template <int N>
+__device__ __forceinline__ void weights_by_rows(const float *w, const float *y, int ld, int n,
+                                                int ty, int tx, u64 (&acc)[4][N][2]) {
+  w += 4 * ty * kLdP;
+  y += 4 * tx;
+#pragma unroll 1
+  for (int k = 0; k < kBlk; k += 4) {
+    float4 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const float4 *>(w + i * kLdP + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        if (4 * tx + 64 * q >= n) continue;
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(y + (k + kk) * ld + 64 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = kk == 0 ? c[i].x : kk == 1 ? c[i].y : kk == 2 ? c[i].z : c[i].w;
+          const u64 ff = pk2(f, f);
+          acc[i][q][0] = fma2(ff, v.x, acc[i][q][0]);
+          acc[i][q][1] = fma2(ff, v.y, acc[i][q][1]);
+        }
+      }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void clear(u64 (&acc)[4][N][2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < N; ++q) acc[i][q][0] = acc[i][q][1] = 0;
+}
+
+// Maximum and sum over the 16 threads that share rows.
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// A CTA's tile, head and row; the longest rows of tiles come first.
+struct Where {
+  int t0, h, b;
+};
+__device__ __forceinline__ Where where(const Prompt &p, bool last_first) {
+  const int tiles = (p.T + kBlk - 1) / kBlk;
+  const unsigned x = blockIdx.x, per = (unsigned)(p.B * p.H);
+  const int tile = (int)(x / per), r = (int)(x % per);
+  return {(last_first ? tiles - 1 - tile : tile) * kBlk, r % p.H, r / p.H};
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
+  extern __shared__ __align__(16) float sm[];
+  const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
+  float *sq = sm, *sk = sq + kBlk * ldq, *sv = sk + kBlk * ldq, *sp = sv + kBlk * ldv;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const Where at0 = where(p, true);
+  const int b = at0.b, h = at0.h, t0 = at0.t0;
+  load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
+               p.qr_s.t, p.R, t0, p.T);
+  int lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    lo[i] = t0 + 4 * ty + i < p.T ? run_start(p, b, t0 + 4 * ty + i) : 0x7fffffff;
+  float m[4], l[4];
+  u64 acc[4][2][2];
+  clear(acc);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  const float scale = p.scale * kLog2e;
+  const int last = min(p.T, t0 + kBlk);
+  for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
+    __syncthreads();
+    load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
+                 p.kr_s.t, p.R, j0, p.T);
+    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0,
+                 p.T);
+    __syncthreads();
+    float s[4][4];
+    rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 4 * ty + i;
+      float top = m[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = j0 + tx + 16 * j;
+        s[i][j] = k >= lo[i] && k <= t ? s[i][j] * scale : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+      top = row_max(top);
+      const float base = top == -INFINITY ? 0.f : top, f = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = exp2f(s[i][j] - base);
+        sum += w;
+        sp[(4 * ty + i) * kLdP + tx + 16 * j] = w;
+      }
+      l[i] = l[i] * f + row_sum(sum);
+      m[i] = top;
+      const u64 ff = pk2(f, f);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        acc[i][q][0] = mul2(acc[i][q][0], ff);
+        acc[i][q][1] = mul2(acc[i][q][1], ff);
+      }
+    }
+    __syncwarp();   // the rows of a warp are its own
+    weights_by_rows<2>(sp, sv, ldv, p.V, ty, tx, acc);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 4 * ty + i;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    bool bad = false;
+    if (t < p.T) {
+      T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.V;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (4 * tx + 64 * q >= p.V) continue;
+        float x[4];
+        upk2(acc[i][q][0], x[0], x[1]);
+        upk2(acc[i][q][1], x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = l[i] == 0.f ? 0.f : x[e] * inv;
+          bad |= !finite(y);
+          o[4 * tx + 64 * q + e] = from_f32<T>(y);
+        }
+      }
+      if (p.lse && tx == 0)
+        p.lse[((size_t)b * p.H + h) * p.T + t] =
+            l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+    }
+    const unsigned which = __ballot_sync(0xffffffffu, bad);
+    __syncwarp();
+    if (which & 0xffffu) forward_row<T>(p, b, h, t0 + 8 * (tid >> 5) + i, tid & 31);
+    if (which & 0xffff0000u) forward_row<T>(p, b, h, t0 + 8 * (tid >> 5) + 4 + i, tid & 31);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
+  extern __shared__ __align__(16) float sm[];
+  const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
+  float *sk = sm, *sv = sk + kBlk * ldq, *sq = sv + kBlk * ldv, *su = sq + kBlk * ldq,
+        *sp = su + kBlk * ldv, *sd = sp + kBlk * kLdP;
+  __shared__ float s_lse[kBlk], s_delta[kBlk];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const Where at0 = where(p, false);
+  const int b = at0.b, h = at0.h, t0 = at0.t0;
+  load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
+               p.kr_s.t, p.R, t0, p.T);
+  load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, t0,
+               p.T);
+  int end[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    end[i] = t0 + 4 * ty + i < p.T ? run_end(p, b, t0 + 4 * ty + i) : 0;
+  const int last = run_end(p, b, min(p.T, t0 + kBlk) - 1);
+  u64 ak[4][3][2], av[4][2][2];
+  clear(ak);
+  clear(av);
+  const float scale = p.scale * kLog2e;
+  for (int i0 = t0; i0 < last; i0 += kBlk) {
+    __syncthreads();
+    load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
+                 p.qr_s.t, p.R, i0, p.T);
+    load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
+                 (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, i0, p.T);
+    if (tid < kBlk && i0 + tid < p.T) {
+      const size_t r = ((size_t)b * p.H + h) * p.T + i0 + tid;
+      s_lse[tid] = p.lse[r] * kLog2e;
+      s_delta[tid] = p.delta[r];
+    }
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    rows_by_rows(sk, ldq, sq, ldq, D, ty, tx, s);
+    rows_by_rows(sv, ldv, su, ldv, p.V, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = tx + 16 * j, t = i0 + c;
+        const bool on = t >= t0 + 4 * ty + i && t < end[i];
+        const float w = on ? exp2f(s[i][j] * scale - s_lse[c]) : 0.f;
+        sp[(4 * ty + i) * kLdP + c] = w;
+        sd[(4 * ty + i) * kLdP + c] = on ? w * (dp[i][j] - s_delta[c]) : 0.f;
+      }
+    __syncwarp();
+    weights_by_rows<2>(sp, su, ldv, p.V, ty, tx, av);
+    weights_by_rows<3>(sd, sq, ldq, D, ty, tx, ak);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 4 * ty + i;
+    const size_t row = ((size_t)b * p.T + t) * p.H + h;
+    bool bad = false;
+    if (t < p.T) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 4 * tx + 64 * q + e;
+          float x[2];
+          upk2(ak[i][q][e >> 1], x[0], x[1]);
+          const float y = x[e & 1] * p.scale;
+          if (c < D) bad |= !finite(y);
+          if (c < p.K) static_cast<T *>(p.dk)[row * p.K + c] = from_f32<T>(y);
+          else if (c < D) p.dkr_part[row * p.R + c - p.K] = y;
+          if (q < 2 && c < p.V) {
+            upk2(av[i][q < 2 ? q : 0][e >> 1], x[0], x[1]);
+            bad |= !finite(x[e & 1]);
+            static_cast<T *>(p.dv)[row * p.V + c] = from_f32<T>(x[e & 1]);
+          }
+        }
+    }
+    const unsigned which = __ballot_sync(0xffffffffu, bad);
+    __syncwarp();
+    if (which & 0xffffu) key_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + i, tid & 31);
+    if (which & 0xffff0000u) key_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + 4 + i, tid & 31);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
+  extern __shared__ __align__(16) float sm[];
+  const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
+  float *sq = sm, *su = sq + kBlk * ldq, *sk = su + kBlk * ldv, *sv = sk + kBlk * ldq,
+        *sd = sv + kBlk * ldv;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const Where at0 = where(p, true);
+  const int b = at0.b, h = at0.h, t0 = at0.t0;
+  load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
+               p.qr_s.t, p.R, t0, p.T);
+  load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
+               (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, t0, p.T);
+  int lo[4];
+  float lse[4], delta[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 4 * ty + i;
+    lo[i] = t < p.T ? run_start(p, b, t) : 0x7fffffff;
+    const size_t r = ((size_t)b * p.H + h) * p.T + min(t, p.T - 1);
+    lse[i] = p.lse[r] * kLog2e;
+    delta[i] = p.delta[r];
+  }
+  u64 acc[4][3][2];
+  clear(acc);
+  const float scale = p.scale * kLog2e;
+  const int last = min(p.T, t0 + kBlk);
+  for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
+    __syncthreads();
+    load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
+                 p.kr_s.t, p.R, j0, p.T);
+    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0,
+                 p.T);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
+    rows_by_rows(su, ldv, sv, ldv, p.V, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = j0 + tx + 16 * j;
+        const bool on = k >= lo[i] && k <= t0 + 4 * ty + i;
+        sd[(4 * ty + i) * kLdP + tx + 16 * j] =
+            on ? exp2f(s[i][j] * scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
+      }
+    __syncwarp();
+    weights_by_rows<3>(sd, sk, ldq, D, ty, tx, acc);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 4 * ty + i;
+    const size_t row = ((size_t)b * p.T + t) * p.H + h;
+    bool bad = false;
+    if (t < p.T) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 4 * tx + 64 * q + e;
+          float x[2];
+          upk2(acc[i][q][e >> 1], x[0], x[1]);
+          const float y = x[e & 1] * p.scale;
+          if (c < D) bad |= !finite(y);
+          if (c < p.K) static_cast<T *>(p.dq)[row * p.K + c] = from_f32<T>(y);
+          else if (c < D) static_cast<T *>(p.dqr)[row * p.R + c - p.K] = from_f32<T>(y);
+        }
+    }
+    const unsigned which = __ballot_sync(0xffffffffu, bad);
+    __syncwarp();
+    if (which & 0xffffu) query_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + i, tid & 31);
+    if (which & 0xffff0000u) query_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + 4 + i, tid & 31);
+  }
+}
+
+// ---- runs -------------------------------------------------------------------
+// Where each token's run begins and ends, one CTA a row: a running maximum of
+// the starts from the left, a running minimum of the ends from the right, 8
+// tokens a thread at a time.
+constexpr int kRunThreads = 1024, kRunTokens = 8;
+
+template <bool kMax>
+__device__ __forceinline__ int scan(int x, int *tmp) {   // inclusive, in thread order
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = kMax ? max(x, y) : min(x, y);
+  }
+  __syncthreads();
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) x = kMax ? max(x, tmp[w]) : min(x, tmp[w]);
+  return x;
+}
+
+__global__ void __launch_bounds__(kRunThreads) runs_kernel(const int *ids, int T, int *start,
+                                                           int *end) {
+  __shared__ int tmp[kRunThreads / 32], edge[kRunThreads];
+  const size_t row = (size_t)blockIdx.x * T;
+  ids += row;
+  start += row;
+  end += row;
+  const int per = kRunThreads * kRunTokens, tid = threadIdx.x;
+  int carry = 0;
+  for (int t0 = 0; t0 < T; t0 += per) {
+    const int a = t0 + tid * kRunTokens;
+    int v[kRunTokens], id[kRunTokens];
+    int prev = a > 0 && a <= T ? ids[a - 1] : 0, top = 0;
+#pragma unroll
+    for (int i = 0; i < kRunTokens; ++i) {
+      id[i] = a + i < T ? ids[a + i] : 0;
+      if (a + i < T && id[i] != prev) top = a + i;
+      prev = id[i];
+      v[i] = top;
+    }
+    const int sum = scan<true>(top, tmp);
+    edge[tid] = sum;
+    __syncthreads();
+    const int in = max(carry, tid ? edge[tid - 1] : 0);
+    carry = max(carry, edge[kRunThreads - 1]);
+#pragma unroll
+    for (int i = 0; i < kRunTokens; ++i)
+      if (a + i < T) start[a + i] = id[i] ? max(in, v[i]) : a + i + 1;
+    __syncthreads();
+  }
+  carry = T;
+  for (int t0 = (T - 1) / per * per; t0 >= 0; t0 -= per) {
+    const int z = t0 + (kRunThreads - 1 - tid) * kRunTokens;   // from the right
+    int v[kRunTokens], id[kRunTokens];
+    int next = z + kRunTokens < T ? ids[z + kRunTokens] : 0, low = T;
+#pragma unroll
+    for (int i = kRunTokens - 1; i >= 0; --i) {
+      id[i] = z + i < T ? ids[z + i] : 0;
+      if (z + i < T && (z + i == T - 1 || id[i] != next)) low = z + i + 1;
+      next = id[i];
+      v[i] = low;
+    }
+    const int sum = scan<false>(low, tmp);
+    edge[tid] = sum;
+    __syncthreads();
+    const int in = min(carry, tid ? edge[tid - 1] : T);
+    carry = min(carry, edge[kRunThreads - 1]);
+#pragma unroll
+    for (int i = 0; i < kRunTokens; ++i)
+      if (z + i < T) end[z + i] = id[i] ? min(in, v[i]) : z + i;
+    __syncthreads();
+  }
+}
+
+// ---- around the backward ----------------------------------------------------
+// delta[b][h][t] = d_o . o, 8 lanes a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) delta_kernel(Prompt p) {
+  const long long rows = (long long)p.B * p.T * p.H;
+  const long long r = (long long)blockIdx.x * (kThreads / 8) + threadIdx.x / 8;
+  float s = 0.f;
+  if (r < rows) {
+    const T *o = static_cast<const T *>(p.o) + r * p.V,
+            *u = static_cast<const T *>(p.d_o) + r * p.V;
+    constexpr int W = 16 / (int)sizeof(T);
+    struct alignas(16) Piece {
+      T v[W];
+    };
+    for (int c = (threadIdx.x & 7) * W; c < p.V; c += 8 * W) {
+      const Piece x = *reinterpret_cast<const Piece *>(o + c);
+      const Piece y = *reinterpret_cast<const Piece *>(u + c);
+#pragma unroll
+      for (int e = 0; e < W; ++e) s = fmaf(to_f32(x.v[e]), to_f32(y.v[e]), s);
+    }
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (r < rows && (threadIdx.x & 7) == 0) {
+    const int h = (int)(r % p.H);
+    const long long bt = r / p.H;
+    const int t = (int)(bt % p.T), b = (int)(bt / p.T);
+    const_cast<float *>(p.delta)[((size_t)b * p.H + h) * p.T + t] = s;
+  }
+}
+
+// dk_rope = the sum of the heads' parts, in the order of the heads.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_sum_kernel(Prompt p) {
+  const int quads = p.R / 4;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= (long long)p.B * p.T * quads) return;
+  const float4 *x = reinterpret_cast<const float4 *>(p.dkr_part) + i / quads * p.H * quads +
+                    i % quads;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int h = 0; h < p.H; ++h) {
+    const float4 y = x[(size_t)h * quads];
+    s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+  }
+  T *d = static_cast<T *>(p.dkr) + 4 * i;
+  d[0] = from_f32<T>(s.x);
+  d[1] = from_f32<T>(s.y);
+  d[2] = from_f32<T>(s.z);
+  d[3] = from_f32<T>(s.w);
+}
+
+template <typename K>
+cudaError_t launch_tiles(K kern, const Prompt &p, size_t floats, cudaStream_t cs) {
+  const size_t smem = floats * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  const unsigned tiles = (unsigned)((p.T + kBlk - 1) / kBlk);
+  kern<<<tiles * p.B * p.H, kThreads, smem, cs>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_simt(const Prompt &p, cudaStream_t cs) {
+  const size_t q = (size_t)kBlk * (p.K + p.R + 4), v = (size_t)kBlk * (p.V + 4);
+  return launch_tiles(prompt_fwd_kernel<T>, p, 2 * q + v + kBlk * kLdP, cs);
+}
+
+template <typename T>
+cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
+  const long long rows = (long long)p.B * p.T * p.H;
+  delta_kernel<T><<<(unsigned)((rows + kThreads / 8 - 1) / (kThreads / 8)), kThreads, 0, cs>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (tc) {
+    e = launch_prompt_bwd_tc(p, cs);
+  } else {
+    const size_t q = (size_t)kBlk * (p.K + p.R + 4), v = (size_t)kBlk * (p.V + 4),
+                 w = (size_t)kBlk * kLdP;
+    e = launch_tiles(prompt_dkv_kernel<T>, p, 2 * q + 2 * v + 2 * w, cs);
+    if (e == cudaSuccess) e = launch_tiles(prompt_dq_kernel<T>, p, 2 * q + 2 * v + w, cs);
+  }
+  if (e != cudaSuccess || p.R == 0) return e;
+  const long long quads = (long long)p.B * p.T * (p.R / 4);
+  rope_sum_kernel<T><<<(unsigned)((quads + kThreads - 1) / kThreads), kThreads, 0, cs>>>(p);
+  return cudaGetLastError();
+}
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+kda_status check(const kda_latent_shape *s) {
+  if (!s || s->B < 1 || s->T < 1 || s->H < 1) return KDA_ERR_INVALID_ARG;
+  if (s->dtype != KDA_DTYPE_F32 && s->dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARG;
+  for (int d : {s->K, s->V})
+    if (d != 32 && d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
+  if (s->R != 0 && s->R != 32 && s->R != 64) return KDA_ERR_UNSUPPORTED;
+  if ((long long)s->B * s->T >= (1ll << 31) || (long long)s->B * s->H >= (1ll << 31) ||
+      (double)s->B * s->T * s->H * (s->K + s->R) >= 2147483648.0)
+    return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// Of the workspace, after its header.
+size_t table_bytes(const kda_latent_shape *s) {
+  return align_up(sizeof(int) * (size_t)s->B * s->T, 256);
+}
+size_t delta_bytes(const kda_latent_shape *s) {
+  return align_up(sizeof(float) * (size_t)s->B * s->T * s->H, 256);
+}
+
+Prompt make(const kda_latent_shape *s, const void *q, const void *q_rope, const void *k,
+            const void *k_rope, const void *v, float scale, void *workspace) {
+  Prompt p;
+  memset(&p, 0, sizeof(p));
+  p.B = s->B; p.T = s->T; p.H = s->H; p.K = s->K; p.R = s->R; p.V = s->V;
+  p.q = q; p.qr = q_rope; p.k = k; p.kr = k_rope; p.v = v;
+  p.q_s = {s->q_stride_b, s->q_stride_t, s->q_stride_h};
+  p.k_s = {s->k_stride_b, s->k_stride_t, s->k_stride_h};
+  p.v_s = {s->v_stride_b, s->v_stride_t, s->v_stride_h};
+  if (s->R) {
+    p.qr_s = {s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h};
+    p.kr_s = {s->k_rope_stride_b, s->k_rope_stride_t, 0};
+  }
+  p.scale = scale;
+  p.status = &static_cast<WsHeader *>(workspace)->status;
+  return p;
+}
+
+kda_status check_call(const kda_latent_shape *s, const void *q, const void *q_rope, const void *k,
+                      const void *k_rope, const void *v, float scale, const int32_t *segment_ids,
+                      kda_impl impl) {
+  const kda_status st = check(s);
+  if (st != KDA_OK) return st;
+  if (!q || !k || !v || !(fabsf(scale) < INFINITY)) return KDA_ERR_INVALID_ARG;
+  if ((s->R > 0) != (q_rope != nullptr) || (s->R > 0) != (k_rope != nullptr))
+    return KDA_ERR_INVALID_ARG;
+  if (impl != KDA_IMPL_AUTO && impl != KDA_IMPL_SIMT && impl != KDA_IMPL_TC)
+    return KDA_ERR_INVALID_ARG;
+  if (impl == KDA_IMPL_TC && s->dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
+  const uintptr_t es = s->dtype == KDA_DTYPE_BF16 ? 2 : 4;
+  for (const void *x : {q, q_rope, k, k_rope, v})
+    if (!aligned(x, es)) return KDA_ERR_ALIGNMENT;
+  if (!aligned(segment_ids, 4)) return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+kda_status check_workspace(const kda_latent_shape *s, int backward, const void *workspace,
+                           size_t bytes) {
+  if (!workspace || bytes < kda_latent_workspace_size(s, backward)) return KDA_ERR_WORKSPACE;
+  return aligned(workspace, 256) ? KDA_OK : KDA_ERR_ALIGNMENT;
+}
+
+cudaError_t find_runs(Prompt &p, const int32_t *segment_ids, const kda_latent_shape *s,
+                      void *workspace, cudaStream_t cs) {
+  if (!segment_ids) return cudaSuccess;
+  int *start = reinterpret_cast<int *>(static_cast<char *>(workspace) + sizeof(WsHeader));
+  int *end = start + table_bytes(s) / sizeof(int);
+  runs_kernel<<<(unsigned)s->B, kRunThreads, 0, cs>>>(segment_ids, s->T, start, end);
+  p.start = start;
+  p.end = end;
+  return cudaGetLastError();
+}
+
+// 0: the CUDA cores, 1: the tensor cores, else a refusal.
+int choose(const kda_latent_shape *s, const Prompt &p, kda_impl impl) {
+  if (impl == KDA_IMPL_SIMT || s->dtype != KDA_DTYPE_BF16) return 0;
+  if (prompt_tc_ok(p)) return 1;
+  return impl == KDA_IMPL_TC ? -1 : 0;
+}
+
+}  // namespace
+}  // namespace latent
+}  // namespace kda
+
+using namespace kda;
+using namespace kda::latent;
+
+extern "C" {
+
+size_t kda_latent_workspace_size(const kda_latent_shape *s, int backward) {
+  if (check(s) != KDA_OK) return 0;
+  size_t n = sizeof(WsHeader) + 2 * table_bytes(s);
+  if (backward)
+    n += delta_bytes(s) + align_up(sizeof(float) * (size_t)s->B * s->T * s->H * s->R, 256);
+  return n;
+}
+
+kda_status kda_latent_fwd(const kda_latent_shape *s, const void *q, const void *q_rope,
+                          const void *k, const void *k_rope, const void *v, float scale,
+                          const int32_t *segment_ids, void *o, float *lse, void *workspace,
+                          size_t workspace_bytes, kda_impl impl, kda_stream_t stream) {
+  kda_status st = check_call(s, q, q_rope, k, k_rope, v, scale, segment_ids, impl);
+  if (st != KDA_OK) return st;
+  if (!o) return KDA_ERR_INVALID_ARG;
+  if (!aligned(o, 16) || !aligned(lse, 4)) return KDA_ERR_ALIGNMENT;
+  st = check_workspace(s, 0, workspace, workspace_bytes);
+  if (st != KDA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  Prompt p = make(s, q, q_rope, k, k_rope, v, scale, workspace);
+  p.o = o;
+  p.lse = lse;
+  const int way = choose(s, p, impl);
+  if (way < 0) return KDA_ERR_ALIGNMENT;
+  cudaError_t e = find_runs(p, segment_ids, s, workspace, cs);
+  if (e != cudaSuccess) return KDA_ERR_CUDA;
+  e = way ? launch_prompt_tc(p, cs)
+      : s->dtype == KDA_DTYPE_BF16 ? forward_simt<__nv_bfloat16>(p, cs)
+                                   : forward_simt<float>(p, cs);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_latent_bwd(const kda_latent_shape *s, const void *q, const void *q_rope,
+                          const void *k, const void *k_rope, const void *v, float scale,
+                          const int32_t *segment_ids, const void *o, const float *lse,
+                          const void *d_o, void *dq, void *dq_rope, void *dk, void *dk_rope,
+                          void *dv, void *workspace, size_t workspace_bytes, kda_impl impl,
+                          kda_stream_t stream) {
+  kda_status st = check_call(s, q, q_rope, k, k_rope, v, scale, segment_ids, impl);
+  if (st != KDA_OK) return st;
+  if (!o || !lse || !d_o || !dq || !dk || !dv) return KDA_ERR_INVALID_ARG;
+  if ((s->R > 0) != (dq_rope != nullptr) || (s->R > 0) != (dk_rope != nullptr))
+    return KDA_ERR_INVALID_ARG;
+  for (const void *x : {o, d_o, (const void *)dq, (const void *)dq_rope, (const void *)dk,
+                        (const void *)dk_rope, (const void *)dv})
+    if (!aligned(x, 16)) return KDA_ERR_ALIGNMENT;
+  if (!aligned(lse, 4)) return KDA_ERR_ALIGNMENT;
+  st = check_workspace(s, 1, workspace, workspace_bytes);
+  if (st != KDA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  Prompt p = make(s, q, q_rope, k, k_rope, v, scale, workspace);
+  p.o = const_cast<void *>(o);
+  p.lse = const_cast<float *>(lse);
+  p.d_o = d_o;
+  p.dq = dq; p.dqr = dq_rope; p.dk = dk; p.dkr = dk_rope; p.dv = dv;
+  char *ws = static_cast<char *>(workspace) + sizeof(WsHeader) + 2 * table_bytes(s);
+  p.delta = reinterpret_cast<float *>(ws);
+  p.dkr_part = reinterpret_cast<float *>(ws + delta_bytes(s));
+  const int way = choose(s, p, impl);
+  if (way < 0) return KDA_ERR_ALIGNMENT;
+  cudaError_t e = find_runs(p, segment_ids, s, workspace, cs);
+  if (e != cudaSuccess) return KDA_ERR_CUDA;
+  e = s->dtype == KDA_DTYPE_BF16 ? backward<__nv_bfloat16>(p, way == 1, cs)
+                                 : backward<float>(p, false, cs);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

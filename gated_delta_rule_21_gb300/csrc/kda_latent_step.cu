@@ -1,0 +1,384 @@
+// kda_latent_step.cu -- the absorbed latent attention over the paged cache:
+// entry point, the kernel on the CUDA cores and the one that joins the parts.
+//
+// The tokens of all sequences are cut into tiles of 128, and the tiles evenly
+// into one part for each SM, so a part may hold the end of one sequence, whole
+// ones and the beginning of another.  Whole sequences are written at once;
+// of the others each part leaves its sums with the softmax's maximum and sum, and
+// a second kernel joins them.  The cut goes by the lengths on the device: a call
+// that was captured into a graph follows the lengths that it finds.
+#include <string.h>
+
+#include "kda_f32x2.cuh"
+#include "kda_latent.cuh"
+
+namespace kda {
+namespace latent {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSub = 32;          // tokens in shared memory at once
+constexpr int kLdW = kSub + 4;
+
+// CUDA cores, fp32.  The 32 rows of queries and 32 tokens lie in shared memory;
+// a warp makes the scores of its 4 rows and their sums over the latents.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ long long tmp[36];
+  __shared__ int ok[kSub];
+  const int D = p.C + p.R, ld = D + 4;
+  float *sq = sm, *sc = sq + kRows * ld, *sw = sc + kSub * ld;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
+  Work x = find_work(p, tmp);
+  const float scale = p.scale * kLog2e;
+  bool first = true;
+  while (x.unit < x.end) {
+    const Seq s = seq_of(p, x.b);
+    const int tiles = tiles_of(s);
+    if (x.off >= (long long)tiles * p.row_tiles) {
+      ++x.b;
+      x.off = 0;
+      continue;
+    }
+    const int rt = (int)(x.off / tiles), j0 = (int)(x.off % tiles);
+    const int n = (int)min((long long)(tiles - j0), x.end - x.unit);
+    const bool whole = n == tiles;
+    const int r0 = rt * kRows, rows = p.T * p.H;
+    __syncthreads();
+    for (int i = tid; i < kRows * D; i += kThreads) {
+      const int r = r0 + i / D, c = i % D;
+      float v = 0.f;
+      if (r < rows)
+        v = to_f32(c < p.C ? at<T>(p.q, p.q_s, x.b, r / p.H, r % p.H)[c]
+                           : at<T>(p.qr, p.qr_s, x.b, r / p.H, r % p.H)[c - p.C]);
+      sq[i / D * ld + c] = v;
+    }
+    int lim[2];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 2 * ty + i;
+      lim[i] = r < rows ? seen(p, s, r) : 0;
+    }
+    u64 acc[4][4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i][q][0] = acc[i][q][1] = 0;
+    const int stop = min(s.held, (j0 + n) * kTile);
+    for (int k0 = j0 * kTile; k0 < stop; k0 += kSub) {
+      __syncthreads();
+      for (int i = warp; i < kSub; i += kThreads / 32) {   // a warp a token
+        const int k = k0 + i;
+        int pg = -1;
+        if (k < s.held) pg = p.table[(size_t)x.b * p.max_pages + k / p.page];
+        const bool there = pg >= 0 && pg < p.n_pages;
+        const T *c = static_cast<const T *>(p.cache) + (there ? pg * p.page_stride : 0) +
+                     (there ? (long long)(k % p.page) * p.token_stride : 0);
+        for (int e = lane; e < D; e += 32) sc[i * ld + e] = there ? to_f32(c[e]) : 0.f;
+        if (lane == 0) ok[i] = there;
+      }
+      __syncthreads();
+      u64 a2[2][2] = {{0, 0}, {0, 0}};
+      const float *a = sq + 2 * ty * ld, *b = sc + tx * ld;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        ulonglong2 u[2], v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          u[i] = *reinterpret_cast<const ulonglong2 *>(a + i * ld + c);
+          v[i] = *reinterpret_cast<const ulonglong2 *>(b + 16 * i * ld + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            a2[i][j] = fma2(u[i].x, v[j].x, a2[i][j]);
+            a2[i][j] = fma2(u[i].y, v[j].y, a2[i][j]);
+          }
+      }
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[2], top = m[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float lo, hi;
+          upk2(a2[i][j], lo, hi);
+          const int k = tx + 16 * j;
+          v[j] = k0 + k < lim[i] && ok[k] ? (lo + hi) * scale : -INFINITY;
+          top = fmaxf(top, v[j]);
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -INFINITY ? 0.f : top;
+        f[i] = exp2f(m[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float w = exp2f(v[j] - base);
+          sum += w;
+          sw[(2 * ty + i) * kLdW + tx + 16 * j] = w;
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = l[i] * f[i] + sum;
+        m[i] = top;
+      }
+      __syncwarp();
+      // rows 4 warp + i: their factors stand in lanes 0 (i < 2) and 16
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float g = __shfl_sync(0xffffffffu, f[i & 1], (i >> 1) * 16);
+        const u64 gg = pk2(g, g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[i][q][0] = mul2(acc[i][q][0], gg);
+          acc[i][q][1] = mul2(acc[i][q][1], gg);
+        }
+      }
+      const float *w = sw + 4 * warp * kLdW, *y = sc + 4 * lane;
+#pragma unroll 2
+      for (int k = 0; k < kSub; ++k) {
+        u64 ww[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = w[i * kLdW + k];
+          ww[i] = pk2(e, e);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (128 * q >= p.C) continue;
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(y + k * ld + 128 * q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[i][q][0] = fma2(ww[i], v.x, acc[i][q][0]);
+            acc[i][q][1] = fma2(ww[i], v.y, acc[i][q][1]);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rr = 4 * warp + i, r = r0 + rr;
+      const float mi = __shfl_sync(0xffffffffu, m[i & 1], (i >> 1) * 16);
+      const float li = __shfl_sync(0xffffffffu, l[i & 1], (i >> 1) * 16);
+      if (r >= rows) continue;
+      bool bad = false;
+      const int t = r / p.H, h = r % p.H;
+      T *o = static_cast<T *>(p.o) + (((size_t)x.b * p.T + t) * p.H + h) * p.C;
+      float *part = p.parts + ((size_t)slot * kRows + rr) * p.C;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (128 * q >= p.C) continue;
+        float v[4];
+        upk2(acc[i][q][0], v[0], v[1]);
+        upk2(acc[i][q][1], v[2], v[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 128 * q + 4 * lane + e;
+          if (whole) {
+            const float z = li == 0.f ? 0.f : v[e] / li;
+            bad |= !finite(z);
+            o[c] = from_f32<T>(z);
+          } else {
+            part[c] = v[e];
+          }
+        }
+      }
+      if (lane == 0) {
+        if (!whole) {
+          p.stats[2 * ((size_t)slot * kRows + rr)] = mi;
+          p.stats[2 * ((size_t)slot * kRows + rr) + 1] = li;
+        } else if (p.lse) {
+          p.lse[((size_t)x.b * p.H + h) * p.T + t] =
+              li == 0.f ? -INFINITY : (mi + log2f(li)) * kLn2;
+        }
+      }
+      if (whole && p.T > 1 && __any_sync(0xffffffffu, bad)) {
+        __syncwarp();
+        step_row<T>(p, x.b, r, seen(p, s, r), lane);
+      }
+    }
+    first = false;
+    x.unit += n;
+    x.off += n;
+  }
+}
+
+// Joins the parts of one row: its threads are p.C / 4 columns of four channels, and
+// groups that share the parts.
+template <typename T>
+__global__ void __launch_bounds__(512) join_kernel(Step p) {
+  __shared__ float4 sums[512];
+  __shared__ float s_l[4];
+  __shared__ int s_bad;
+  const int cols = p.C / 4, groups = blockDim.x / cols, col = threadIdx.x % cols,
+            group = threadIdx.x / cols;
+  const int rows = p.T * p.H, b = (int)(blockIdx.x / (unsigned)rows),
+            r = (int)(blockIdx.x % (unsigned)rows);
+  const int t = r / p.H, h = r % p.H;
+  after_previous();
+  const Seq s = seq_of(p, b);
+  const int tiles = tiles_of(s);
+  const long long total = p.plan[p.B];
+  T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.C;
+  float *lse = p.lse ? p.lse + ((size_t)b * p.H + h) * p.T + t : nullptr;
+  if (tiles == 0) {
+    if (group == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[4 * col + e] = from_f32<T>(0.f);
+      if (col == 0 && lse) *lse = -INFINITY;
+    }
+    return;
+  }
+  const long long u0 = p.plan[b] + (long long)(r / kRows) * tiles;
+  const int g0 = part_of(total, u0), g1 = part_of(total, u0 + tiles - 1);
+  if (g0 == g1) return;
+  auto slot = [&](int g) {
+    return (size_t)(2 * g + (part_begin(total, g) >= u0 ? 0 : 1)) * kRows + r % kRows;
+  };
+  float m = -INFINITY;
+  for (int g = g0; g <= g1; ++g) m = fmaxf(m, p.stats[2 * slot(g)]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int g = g0 + group; g <= g1; g += groups) {
+    const size_t k = slot(g);
+    const float f = exp2f(p.stats[2 * k] - base);
+    const float4 x = reinterpret_cast<const float4 *>(p.parts)[k * cols + col];
+    l = fmaf(f, p.stats[2 * k + 1], l);
+    a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y);
+    a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
+  }
+  sums[threadIdx.x] = a;
+  if (col == 0) s_l[group] = l;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  if (group == 0) {
+    for (int g = 1; g < groups; ++g) {
+      const float4 x = sums[g * cols + col];
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      l += s_l[g];
+    }
+    const float v[4] = {a.x, a.y, a.z, a.w};
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float z = l == 0.f ? 0.f : v[e] / l;
+      bad |= !finite(z);
+      o[4 * col + e] = from_f32<T>(z);
+    }
+    if (col == 0 && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (bad) s_bad = 1;
+  }
+  if (p.T == 1) return;   // every row sees what the others see
+  __syncthreads();
+  if (s_bad && threadIdx.x < 32) step_row<T>(p, b, r, seen(p, s, r), threadIdx.x);
+}
+
+template <typename T>
+cudaError_t launch_simt(const Step &p, cudaStream_t cs) {
+  const size_t smem = sizeof(float) * ((size_t)(kRows + kSub) * (p.C + p.R + 4) + kRows * kLdW);
+  cudaError_t e = cudaFuncSetAttribute(step_simt_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  step_simt_kernel<T><<<kParts, kThreads, smem, cs>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join(const Step &p, cudaStream_t cs) {
+  const int cols = p.C / 4, groups = 4;
+  return launch_next(join_kernel<T>, dim3((unsigned)((long long)p.B * p.T * p.H)),
+                     (unsigned)(cols * groups), 0, cs, p);
+}
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+kda_status check(const kda_latent_cache *s) {
+  if (!s || s->B < 1 || s->T < 1 || s->H < 1 || s->max_pages < 1 || s->n_pages < 1 ||
+      s->page_size < 1)
+    return KDA_ERR_INVALID_ARG;
+  if (s->dtype != KDA_DTYPE_F32 && s->dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARG;
+  if (s->C != 128 && s->C != 256 && s->C != 512) return KDA_ERR_UNSUPPORTED;
+  if (s->R != 0 && s->R != 32 && s->R != 64) return KDA_ERR_UNSUPPORTED;
+  if ((double)s->B * s->T * s->H >= 2147483648.0 || (long long)s->T * s->H >= (1ll << 24) ||
+      (double)s->max_pages * s->page_size >= 2147483000.0)
+    return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+size_t plan_bytes(const kda_latent_cache *s) {
+  return align_up(sizeof(long long) * ((size_t)s->B + 1), 256);
+}
+
+}  // namespace
+}  // namespace latent
+}  // namespace kda
+
+using namespace kda;
+using namespace kda::latent;
+
+extern "C" {
+
+size_t kda_latent_step_workspace_size(const kda_latent_cache *s) {
+  if (!s || s->B < 1 || s->T < 1 || s->H < 1) return 0;
+  if (s->C != 128 && s->C != 256 && s->C != 512) return 0;
+  return sizeof(WsHeader) + plan_bytes(s) + sizeof(float) * 2 * kParts * kRows * (s->C + 2);
+}
+
+kda_status kda_latent_step(const kda_latent_cache *s, const void *q, const void *q_rope,
+                           const void *cache, const int32_t *page_table, const int32_t *lengths,
+                           const int32_t *new_tokens, float scale, void *o, float *lse,
+                           void *workspace, size_t workspace_bytes, kda_impl impl,
+                           kda_stream_t stream) {
+  const kda_status st = check(s);
+  if (st != KDA_OK) return st;
+  if (!q || !cache || !page_table || !lengths || !o || !(fabsf(scale) < INFINITY))
+    return KDA_ERR_INVALID_ARG;
+  if ((s->R > 0) != (q_rope != nullptr)) return KDA_ERR_INVALID_ARG;
+  if (impl != KDA_IMPL_AUTO && impl != KDA_IMPL_SIMT && impl != KDA_IMPL_TC)
+    return KDA_ERR_INVALID_ARG;
+  const bool bf16 = s->dtype == KDA_DTYPE_BF16;
+  for (const void *x : {q, q_rope, cache})
+    if (!aligned(x, bf16 ? 2 : 4)) return KDA_ERR_ALIGNMENT;
+  for (const void *x : {(const void *)page_table, (const void *)lengths,
+                        (const void *)new_tokens, (const void *)lse})
+    if (!aligned(x, 4)) return KDA_ERR_ALIGNMENT;
+  if (!aligned(o, 16)) return KDA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kda_latent_step_workspace_size(s)) return KDA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return KDA_ERR_ALIGNMENT;
+  Step p;
+  memset(&p, 0, sizeof(p));
+  p.B = s->B; p.T = s->T; p.H = s->H; p.C = s->C; p.R = s->R;
+  p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page = s->page_size;
+  p.row_tiles = (int)(((long long)s->T * s->H + kRows - 1) / kRows);
+  p.page_stride = s->page_stride; p.token_stride = s->token_stride;
+  p.q = q; p.qr = q_rope; p.cache = cache;
+  p.q_s = {s->q_stride_b, s->q_stride_t, s->q_stride_h};
+  if (q_rope) p.qr_s = {s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h};
+  p.table = page_table; p.lengths = lengths; p.fresh = new_tokens;
+  p.scale = scale;
+  p.o = o; p.lse = lse;
+  char *ws = static_cast<char *>(workspace);
+  p.status = &reinterpret_cast<WsHeader *>(ws)->status;
+  p.plan = reinterpret_cast<long long *>(ws + sizeof(WsHeader));
+  p.parts = reinterpret_cast<float *>(ws + sizeof(WsHeader) + plan_bytes(s));
+  p.stats = p.parts + (size_t)2 * kParts * kRows * s->C;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool can = bf16 && step_tc_ok(p);
+  if (impl == KDA_IMPL_TC && !can) return KDA_ERR_UNSUPPORTED;
+  cudaError_t e = can && impl != KDA_IMPL_SIMT ? launch_step_tc(p, cs)
+                  : bf16 ? launch_simt<__nv_bfloat16>(p, cs)
+                         : launch_simt<float>(p, cs);
+  if (e != cudaSuccess) return KDA_ERR_CUDA;
+  e = bf16 ? launch_join<__nv_bfloat16>(p, cs) : launch_join<float>(p, cs);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

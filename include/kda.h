@@ -666,6 +666,163 @@ KDA_API kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, con
                                       float *dw_pre, void *workspace, size_t workspace_bytes,
                                       kda_stream_t stream);
 
+/*
+ * Attention over one shared latent vector a token: the attention layers that
+ * stand between a stack's recurrent ones.  A token's keys and values are made
+ * from a latent c of C values that all heads share, beside a key r of R values
+ * that is shared too and carries the position (rotated; R = 0: none).  In the
+ * expanded form the projections of c are made: keys k [H, K] and values
+ * v [H, V] a token, for prompts and training.  In the absorbed form they are
+ * moved to the query and the output, and the heads attend to the latents
+ * themselves, which is what single tokens do over a cache:
+ *     expanded  s_ij = scale (q_i . k_j + q_rope_i . r_j),  o_i = sum_j p_ij v_j
+ *     absorbed  s_ij = scale (q_i . c_j + q_rope_i . r_j),  o_i = sum_j p_ij c_j
+ * with p_ij = softmax over the tokens j <= i of the sequence.
+ *
+ * kda_rotate turns the pairs (a, b) of a vector of `dim` values at position t
+ * by the angle t * inv_freq[i] (or back: `inverse`, its gradient):
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * pairs != 0: (x[2i], x[2i+1]), else (x[i], x[i + dim/2]).  The angle is reduced
+ * exactly, so far positions lose nothing; cos, sin and the products are fp32.
+ *   x             device [B,T,H,dim] of d->dtype, the last dimension contiguous.
+ *   positions     device int32 [B,T] or NULL (t = 0 .. T-1).
+ *   inv_freq      device float32 [dim/2].
+ *   y             device [B,T,H,dim] at its own strides; may be x at x's strides.
+ * dim is even, 2 to 256 (KDA_ERR_UNSUPPORTED above).  Asynchronous on `stream`.
+ */
+typedef struct kda_rotate_desc {
+  int B, T, H, dim;
+  kda_dtype dtype;
+  int pairs, inverse;
+  /* element strides */
+  long long x_stride_b, x_stride_t, x_stride_h, y_stride_b, y_stride_t, y_stride_h;
+} kda_rotate_desc;
+KDA_API kda_status kda_rotate(const kda_rotate_desc *d, const void *x, const int32_t *positions,
+                              const float *inv_freq, void *y, kda_stream_t stream);
+
+/*
+ * The paged cache [n_pages, page_size, C + R] of s->dtype (a token's latent, then
+ * its key r; pages and tokens at the shape's strides), and the new tokens of
+ * B sequences that a call works on.
+ *   page_table    device int32 [B, max_pages]: the page of each page_size
+ *                 tokens of a sequence.  A page outside [0, n_pages) holds no
+ *                 tokens: nothing is written to it, nothing read from it.
+ *   lengths       device int32 [B]: tokens of each sequence, the new ones of
+ *                 this call among them (what the table has no room for is not
+ *                 there).
+ *   new_tokens    device int32 [B] or NULL (T for all): how many of the T tokens
+ *                 of each row are there (0 .. T; the first ones).  Token t of row
+ *                 b stands at position lengths[b] - new_tokens[b] + t; one
+ *                 before position 0 is not there.
+ */
+typedef struct kda_latent_cache {
+  int B, T, H;                        /* of the new tokens */
+  int max_pages, n_pages, page_size;
+  int C, R;
+  kda_dtype dtype;
+  /* element strides */
+  long long page_stride, token_stride;
+  long long q_stride_b, q_stride_t, q_stride_h;           /* q */
+  long long q_rope_stride_b, q_rope_stride_t, q_rope_stride_h;
+  long long latent_stride_b, latent_stride_t, k_rope_stride_b, k_rope_stride_t;
+} kda_latent_cache;
+/*
+ * Appends the new tokens, their keys and queries rotated on the way.
+ *   latent        device [B,T,C]; k_rope [B,T,R] (NULL when R = 0).
+ *   q_rope        device [B,T,H,R] or NULL; q_out [B,T,H,R] contiguous: the
+ *                 queries rotated at their tokens' positions (those of tokens that
+ *                 are not there as they came).
+ *   inv_freq      device float32 [R/2] or NULL: nothing is rotated (then no q_rope).
+ *   cache         written at the new tokens' places alone.  The places of one call
+ *                 must differ (no page that is written is shared).
+ * C is 1 to 4096, R even and at most 256.  Asynchronous on `stream`.
+ */
+KDA_API kda_status kda_latent_append(const kda_latent_cache *s, const void *latent,
+                                     const void *k_rope, const void *q_rope,
+                                     const float *inv_freq, int pairs, const int32_t *page_table,
+                                     const int32_t *lengths, const int32_t *new_tokens,
+                                     void *cache, void *q_out, kda_stream_t stream);
+/*
+ * The absorbed form over the cache, which holds the new tokens already.
+ *   q             device [B,T,H,C], q_rope [B,T,H,R] (NULL when R = 0), the last
+ *                 dimension contiguous.  Rows of a projection's output serve.
+ *   o             device [B,T,H,C] contiguous, of s->dtype; 0 for a token that
+ *                 is not there or sees nothing.
+ *   lse           device float32 [B,H,T] or NULL: log sum_j exp(s_ij), -inf for
+ *                 those tokens.
+ *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores, every type and layout.
+ *                 KDA_IMPL_TC: the tensor cores (bf16; p is rounded to bf16, sums
+ *                 and the softmax's statistics are fp32): cache 16-byte aligned,
+ *                 its strides multiples of 8, pages of a power of two of at least 8
+ *                 tokens (KDA_ERR_UNSUPPORTED otherwise).
+ *                 KDA_IMPL_AUTO: TC where that holds.
+ *   workspace     device, kda_latent_step_workspace_size bytes, 256-byte
+ *                 aligned, its first 256 bytes zero-filled before its first use
+ *                 (the device status word).  Calls on different streams need
+ *                 their own.
+ * C is 128, 256 or 512, R 0, 32 or 64.  Values that are not finite reach the tokens
+ * that see them alone.  The work is cut evenly over the SMs by the lengths on the
+ * device, so a captured call serves whatever lengths it finds.  Asynchronous.
+ */
+KDA_API size_t kda_latent_step_workspace_size(const kda_latent_cache *s);
+KDA_API kda_status kda_latent_step(const kda_latent_cache *s, const void *q, const void *q_rope,
+                                   const void *cache, const int32_t *page_table,
+                                   const int32_t *lengths, const int32_t *new_tokens,
+                                   float scale, void *o, float *lse, void *workspace,
+                                   size_t workspace_bytes, kda_impl impl, kda_stream_t stream);
+
+/*
+ * The expanded form on prompts, and its gradients.
+ *   q, k          device [B,T,H,K], v [B,T,H,V], q_rope [B,T,H,R], k_rope [B,T,R]
+ *                 (both NULL when R = 0) of s->dtype, the last dimension contiguous,
+ *                 the others at the shape's strides: slices of projections serve.
+ *   segment_ids   as kda_chunk_fwd: a token sees those of its own run up to
+ *                 itself; padding (id 0) sees nothing, its o is 0.
+ *   o             device [B,T,H,V] contiguous, of s->dtype.
+ *   lse           device float32 [B,H,T] or NULL: log sum_j exp(s_ij) (-inf for
+ *                 padding), which the backward reads.
+ *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores, every type and layout.
+ *                 KDA_IMPL_TC: the tensor cores (bf16; p and the gradient of s are
+ *                 rounded to bf16, sums and statistics fp32); pointers 16-byte
+ *                 aligned and strides multiples of 8 (KDA_ERR_ALIGNMENT).
+ *                 KDA_IMPL_AUTO: TC where that holds, else SIMT.
+ *   workspace     device, kda_latent_workspace_size bytes, 256-byte aligned,
+ *                 its first 256 bytes zero-filled before its first use.  Calls
+ *                 on different streams need their own.
+ * K and V are 32, 64 or 128, R 0, 32 or 64; B*T*H*(K+R) < 2^31.  Values that are not
+ * finite reach the tokens that see them alone.  Asynchronous on `stream`.
+ */
+typedef struct kda_latent_shape {
+  int B, T, H, K, R, V;
+  kda_dtype dtype;
+  /* element strides */
+  long long q_stride_b, q_stride_t, q_stride_h;
+  long long q_rope_stride_b, q_rope_stride_t, q_rope_stride_h;
+  long long k_stride_b, k_stride_t, k_stride_h;
+  long long k_rope_stride_b, k_rope_stride_t;
+  long long v_stride_b, v_stride_t, v_stride_h;
+} kda_latent_shape;
+KDA_API size_t kda_latent_workspace_size(const kda_latent_shape *s, int backward);
+KDA_API kda_status kda_latent_fwd(const kda_latent_shape *s, const void *q, const void *q_rope,
+                                  const void *k, const void *k_rope, const void *v, float scale,
+                                  const int32_t *segment_ids, void *o, float *lse,
+                                  void *workspace, size_t workspace_bytes, kda_impl impl,
+                                  kda_stream_t stream);
+/*
+ * The gradients, from the inputs, the forward's o and lse, and the gradient of o.
+ *   o, d_o        device [B,T,H,V] contiguous, of s->dtype.
+ *   dq, dk, dv, dq_rope, dk_rope   device, contiguous, of s->dtype, the shapes of
+ *                 q, k, v, q_rope, k_rope; dk_rope is the sum over the heads.
+ * Padding tokens get zeros.  No atomics: repeated calls agree bit for bit.
+ * workspace as above, of kda_latent_workspace_size(s, 1) bytes.
+ */
+KDA_API kda_status kda_latent_bwd(const kda_latent_shape *s, const void *q, const void *q_rope,
+                                  const void *k, const void *k_rope, const void *v, float scale,
+                                  const int32_t *segment_ids, const void *o, const float *lse,
+                                  const void *d_o, void *dq, void *dq_rope, void *dk,
+                                  void *dk_rope, void *dv, void *workspace,
+                                  size_t workspace_bytes, kda_impl impl, kda_stream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 KDA_API const char *kda_status_string(kda_status status);
 
