@@ -4,7 +4,5 @@ namespace latent {
 bool prompt_tc_ok(const Prompt &) { return false; }
 cudaError_t launch_prompt_tc(const Prompt &, cudaStream_t) { return cudaErrorNotSupported; }
 cudaError_t launch_prompt_bwd_tc(const Prompt &, cudaStream_t) { return cudaErrorNotSupported; }
-bool step_tc_ok(const Step &) { return false; }
-cudaError_t launch_step_tc(const Step &, cudaStream_t) { return cudaErrorNotSupported; }
 }  // namespace latent
 }  // namespace kda

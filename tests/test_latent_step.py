@@ -8,7 +8,7 @@ from test_latent_rotate import frequencies
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
-WAYS = [("simt", F32), ("simt", BF)]
+WAYS = [("simt", F32), ("simt", BF), ("tc", BF)]
 
 
 def places(lengths, page, wide, gen, spare=3):
@@ -155,7 +155,7 @@ def test_values_that_are_not_finite_reach_the_tokens_that_see_them(impl, dtype):
     assert torch.equal(got[1, 1, 3:], clean[1, 1, 3:])
 
 
-@pytest.mark.parametrize("impl", ["simt"])
+@pytest.mark.parametrize("impl", ["simt", "tc"])
 def test_cache_with_strides_and_past_32_bits(impl):
     """Pages of a cache that holds several layers, behind 2^31 values."""
     import gated_delta_rule_21_gb300 as kda
