@@ -1,8 +1,401 @@
-#include "kda_latent.cuh"
+// kda_latent_tc.cu -- the expanded latent attention on the tensor cores, forward.
+//
+// A CTA has 256 queries of one head, as two tiles A and B of 128, and walks the
+// keys in tiles of 128:
+//     S = [Q | Qr] [K | Kr]^T    128 x 128, K: up to 192 channels
+//     O += P V                   128 x V, P (bf16) in tensor memory over S
+// One thread issues the products in the order PV_A, S_A of the next keys, PV_B, S_B of
+// the next keys, so that the softmax of one tile runs beside the products of the
+// other.  A softmax thread has a row of its own; the maximum that a row is scaled by
+// moves only when a score exceeds it by 2^8, so O is hardly ever scaled.
+//
+// Shared memory (224 KB): the queries (3 chunks of 16 KB a tile), 4 chunks of keys, 2
+// tiles of values.  Tensor memory: S_A, S_B, O_A, O_B, 128 columns each.
+#include "kda_f32x2.cuh"
+#include "kda_latent_tc.cuh"
+
 namespace kda {
 namespace latent {
-bool prompt_tc_ok(const Prompt &) { return false; }
-cudaError_t launch_prompt_tc(const Prompt &, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+constexpr int kRowsQ = 128;                     // of a tile, queries and keys
+constexpr uint32_t kChunkB = kRowsQ * kRowBytes;   // 16 KB
+constexpr int kKSlots = 4, kVSlots = 2;
+constexpr int kThreads = 384;                   // A, B, copies and products (4 warps, two of them idle)
+constexpr uint32_t kOffK = 6 * kChunkB, kOffV = kOffK + kKSlots * kChunkB;
+constexpr uint32_t kOffC = kOffV + kVSlots * 2 * kChunkB;
+constexpr uint32_t kFwdSmem = kOffC + 1024 + 1024;
+constexpr float kSlack = 8.f;                   // octaves
+
+struct Maps {
+  CUtensorMap q, qr, k, kr, v;
+};
+
+// The launch's 384 threads have 168 registers each (504 of three warpgroups); the two
+// that work on rows take 216, the third keeps 56: 488.
+__device__ __forceinline__ void few_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+}
+__device__ __forceinline__ void many_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+}
+
+struct FwdControl {
+  uint64_t q_full[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+  uint64_t s_full[2], p_ready[2], o_done[2], drain;
+  uint32_t tmem;
+  int fail;
+};
+
+// Key tiles [lo, hi) that query tile t (of 128 rows) sees.
+struct Range {
+  int lo, hi;
+};
+__device__ __forceinline__ Range keys_of(const Prompt &p, int b, int t) {
+  if (t * kRowsQ >= p.T) return {0, 0};
+  const int lo = run_start(p, b, t * kRowsQ) / kRowsQ;
+  return {lo, lo > t ? lo : t + 1};
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  unsigned char *smem = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
+  FwdControl &c = *reinterpret_cast<FwdControl *>(smem + kOffC);
+  const uint32_t s0 = tc::smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pairs = (p.T + 2 * kRowsQ - 1) / (2 * kRowsQ);
+  // a head's keys stay in L2 while its queries are worked on, the longest first
+  const int bh = (int)(blockIdx.x / (unsigned)pairs),
+            pair = pairs - 1 - (int)(blockIdx.x % (unsigned)pairs);
+  const int b = bh / p.H, h = bh % p.H;
+  const int nk = (p.K + kChunkCols - 1) / kChunkCols, nc = nk + (p.R > 0 ? 1 : 0);
+  const int nv = (p.V + kChunkCols - 1) / kChunkCols;
+  const Range ra = keys_of(p, b, 2 * pair), rb = keys_of(p, b, 2 * pair + 1);
+  const bool has_a = ra.lo < ra.hi, has_b = rb.lo < rb.hi;
+  const int jl = has_a && has_b ? min(ra.lo, rb.lo) : has_a ? ra.lo : has_b ? rb.lo : 0;
+  const int jh = has_a && has_b ? max(ra.hi, rb.hi) : has_a ? ra.hi : has_b ? rb.hi : 0;
+  auto active = [&](int x, int j) {
+    return x ? j >= rb.lo && j < rb.hi : j >= ra.lo && j < ra.hi;
+  };
+  auto bar = [](uint64_t &x) { return tc::smem_u32(&x); };
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(c.q_full[i]), 1);
+      tc::mbar_init(bar(c.v_full[i]), 1);
+      tc::mbar_init(bar(c.v_empty[i]), 1);
+      tc::mbar_init(bar(c.s_full[i]), 1);
+      tc::mbar_init(bar(c.p_ready[i]), 128);
+      tc::mbar_init(bar(c.o_done[i]), 1);
+    }
+    for (int i = 0; i < kKSlots; ++i) {
+      tc::mbar_init(bar(c.k_full[i]), 1);
+      tc::mbar_init(bar(c.k_empty[i]), 1);
+    }
+    tc::mbar_init(bar(c.drain), 1);
+    c.fail = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 9) tc::tmem_alloc(tc::smem_u32(&c.tmem), 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  volatile int *fail = &c.fail;
+
+  if (warp >= 8) {
+    few_registers();
+    if (warp == 8) {
+    // ---- copies ----
+    if (lane == 0) {
+      int kn = 0, vn = 0;
+      bool ok = true;
+      auto load_q = [&](int x) {
+        const int t = (2 * pair + x) * kRowsQ;
+        if (t >= p.T) return;
+        tc::mbar_expect_tx(bar(c.q_full[x]), (uint32_t)nc * kChunkB);
+        for (int i = 0; i < nk; ++i)
+          tma_load_4d(s0 + (uint32_t)(3 * x + i) * kChunkB, &maps.q, i * kChunkCols, h, t, b,
+                      bar(c.q_full[x]));
+        if (nc > nk)
+          tma_load_4d(s0 + (uint32_t)(3 * x + nk) * kChunkB, &maps.qr, 0, h, t, b,
+                      bar(c.q_full[x]));
+      };
+      auto load_k = [&](int j) {
+        for (int i = 0; ok && i < nc; ++i, ++kn) {
+          const int s = kn % kKSlots;
+          ok = wait_or_fail(bar(c.k_empty[s]), (uint32_t)(kn / kKSlots + 1) & 1, fail);
+          if (!ok) return;
+          tc::mbar_expect_tx(bar(c.k_full[s]), kChunkB);
+          const uint32_t d = s0 + kOffK + (uint32_t)s * kChunkB;
+          if (i < nk)
+            tma_load_4d(d, &maps.k, i * kChunkCols, h, j * kRowsQ, b, bar(c.k_full[s]));
+          else
+            tma_load_3d(d, &maps.kr, 0, j * kRowsQ, b, bar(c.k_full[s]));
+        }
+      };
+      if (jl < jh) {
+        if (has_a) load_q(0);
+        load_k(jl);
+        if (has_b) load_q(1);
+        for (int j = jl; ok && j < jh; ++j, ++vn) {
+          const int s = vn % kVSlots;
+          ok = wait_or_fail(bar(c.v_empty[s]), (uint32_t)(vn / kVSlots + 1) & 1, fail);
+          if (!ok) break;
+          tc::mbar_expect_tx(bar(c.v_full[s]), (uint32_t)nv * kChunkB);
+          for (int i = 0; i < nv; ++i)
+            tma_load_4d(s0 + kOffV + (uint32_t)(2 * s + i) * kChunkB, &maps.v, i * kChunkCols, h,
+                        j * kRowsQ, b, bar(c.v_full[s]));
+          if (j + 1 < jh) load_k(j + 1);
+        }
+      }
+      if (*fail) {   // what is on its way comes in before the CTA ends
+        if (has_a) tc::mbar_wait(bar(c.q_full[0]), 0);
+        if (has_b) tc::mbar_wait(bar(c.q_full[1]), 0);
+        for (int k = max(0, kn - kKSlots); k < kn; ++k)
+          tc::mbar_wait(bar(c.k_full[k % kKSlots]), (uint32_t)(k / kKSlots) & 1);
+        for (int k = max(0, vn - kVSlots); k < vn; ++k)
+          tc::mbar_wait(bar(c.v_full[k % kVSlots]), (uint32_t)(k / kVSlots) & 1);
+      }
+    }
+    __syncwarp();
+    } else if (warp == 9) {
+    // ---- products: one thread ----
+    if (lane == 0 && jl < jh) {
+      const uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0),
+                     id_o = tc::idesc_bf16(128, nv * kChunkCols, 0, 1);
+      bool ok = true;
+      int count[2] = {0, 0};
+      for (int j = jl - 1; ok && j < jh; ++j) {
+        const int kbase = (j + 1 - jl) * nc, vn = j - jl;
+        for (int x = 0; ok && x < 2; ++x) {
+          if (j >= jl && active(x, j)) {
+            ok = wait_or_fail(bar(c.p_ready[x]), (uint32_t)(count[x] - 1) & 1, fail) &&
+                 wait_or_fail(bar(c.v_full[vn % kVSlots]), (uint32_t)(vn / kVSlots) & 1, fail);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t v = s0 + kOffV + (uint32_t)(2 * (vn % kVSlots)) * kChunkB;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e,
+                          swizzled_desc(v + 2048u * e, kChunkB), id_o,
+                          (count[x] > 1 || e > 0) ? 1u : 0u);
+          }
+          if (j + 1 < jh && active(x, j + 1)) {
+            if (count[x] == 0) {
+              ok = wait_or_fail(bar(c.q_full[x]), 0, fail);
+              if (!ok) break;
+            }
+            const bool last = x == 1 || !active(1, j + 1);
+            for (int i = 0; i < nc; ++i) {
+              const int s = (kbase + i) % kKSlots;
+              ok = wait_or_fail(bar(c.k_full[s]), (uint32_t)((kbase + i) / kKSlots) & 1, fail);
+              if (!ok) break;
+              const uint32_t a = s0 + (uint32_t)(3 * x + i) * kChunkB,
+                             k = s0 + kOffK + (uint32_t)s * kChunkB;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                tc::mma_bf16(tmem + 128 * x, swizzled_desc(a + 32u * e, 16),
+                             swizzled_desc(k + 32u * e, 16), id_s, (i > 0 || e > 0) ? 1u : 0u);
+              if (last) tc::mma_commit(bar(c.k_empty[s]));
+            }
+            if (!ok) break;
+            tc::mma_commit(bar(c.s_full[x]));
+            ++count[x];
+          } else if (j >= jl && active(x, j)) {
+            tc::mma_commit(bar(c.o_done[x]));      // its last
+          }
+        }
+        if (ok && j >= jl) tc::mma_commit(bar(c.v_empty[vn % kVSlots]));
+      }
+      if (*fail) {
+        tc::mma_commit(bar(c.drain));
+        tc::mbar_wait(bar(c.drain), 0);
+      }
+    }
+    __syncwarp();
+    }
+  } else {
+    many_registers();
+    // ---- softmax: a row a thread ----
+    const int x = warp >> 2, tile = 2 * pair + x;
+    const int row = tile * kRowsQ + (tid & 127);
+    const Range r = x ? rb : ra;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t t_s = tmem + 128 * x + lanes, t_o = tmem + 256 + 128 * x + lanes;
+    const float sign = p.scale < 0.f ? -1.f : 1.f, scale = fabsf(p.scale) * kLog2e;
+    const u64 scale2 = pk2(scale, scale);
+    const int lo = row < p.T ? run_start(p, b, row) : 0x7fffffff;
+    // the tiles that all rows see whole
+    const int all_lo = tile * kRowsQ < p.T ? run_start(p, b, min(p.T, (tile + 1) * kRowsQ) - 1) : 0;
+    float m = -INFINITY, l = 0.f;
+    for (int j = r.lo; j < r.hi; ++j) {
+      wait_or_fail(bar(c.s_full[x]), (uint32_t)(j - r.lo) & 1, fail);
+      tc::tc_fence_after();
+      uint32_t u[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32_nw(t_s + 32 * i, u[i]);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reg_fence32(u[i]);
+      if (sign < 0.f) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) u[i >> 5][i & 31] ^= 0x80000000u;
+      }
+      if (j == tile || j * kRowsQ < all_lo) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          const int k = j * kRowsQ + i;
+          if (k < lo || k > row) u[i >> 5][i & 31] = 0xff800000u;   // -inf
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 128; ++i) top = fmaxf(top, __uint_as_float(u[i >> 5][i & 31]));
+      top *= scale;
+      if (scale == 0.f) top = 0.f;
+      const bool over = top > m + kSlack;
+      if (__any_sync(0xffffffffu, over)) {
+        const float now = over ? top : m;
+        const float f = over ? exp2f(m - now) : 1.f;
+        m = now;
+        l *= f;
+        if (j > r.lo) {      // PV of the keys before is done: S of these came after it
+          for (int q = 0; q < 2 * nv; ++q) {
+            uint32_t o[32];
+            tmem_ld32_wait(t_o + 32 * q, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(t_o + 32 * q, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      const u64 nb = pk2(-base, -base);
+      u64 sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float a, d;
+          upk2(fma2(pk2(__uint_as_float(u[i][2 * e]), __uint_as_float(u[i][2 * e + 1])), scale2, nb),
+               a, d);
+          a = tc::ex2(a);
+          d = tc::ex2(d);
+          sum = add2(sum, pk2(a, d));
+          w[e] = tc::pack_bf16(a, d);
+        }
+        tmem_st16(t_s + 16 * i, w);
+      }
+      float a, d;
+      upk2(sum, a, d);
+      l += a + d;
+      tmem_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(bar(c.p_ready[x]));
+    }
+    // ---- the rows ----
+    const bool any = r.lo < r.hi;
+    if (any) {
+      wait_or_fail(bar(c.o_done[x]), 0, fail);
+      tc::tc_fence_after();
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    bool bad = false;
+    __nv_bfloat16 *o =
+        static_cast<__nv_bfloat16 *>(p.o) + (((size_t)b * p.T + row) * p.H + h) * p.V;
+    for (int q = 0; q < p.V / 32; ++q) {
+      uint32_t y[32];
+      if (any) {
+        tmem_ld32_wait(t_o + 32 * q, y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = 0;
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float a = l == 0.f ? 0.f : __uint_as_float(y[2 * i]) * inv;
+        const float d = l == 0.f ? 0.f : __uint_as_float(y[2 * i + 1]) * inv;
+        bad |= !finite(a) || !finite(d);
+        w[i] = tc::pack_bf16(a, d);
+      }
+      if (row < p.T) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<uint4 *>(o + 32 * q)[i] =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+    }
+    if (p.lse && row < p.T)
+      p.lse[((size_t)b * p.H + h) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    unsigned which = __ballot_sync(0xffffffffu, bad && row < p.T);
+    __syncwarp();
+    for (; which; which &= which - 1)
+      forward_row<__nv_bfloat16>(p, b, h, row - lane + __ffs(which) - 1, lane);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (tid == 0 && c.fail) set_status(p.status, KDA_DEVICE_TIMEOUT);
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+bool stride_ok(long long s, int n) { return n == 1 || (s > 0 && s % 8 == 0 && s < (1ll << 38)); }
+bool tensor_ok(const void *x, const Strides &s, const Prompt &p, bool heads) {
+  return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && stride_ok(s.b, p.B) &&
+         stride_ok(s.t, p.T) && (!heads || stride_ok(s.h, p.H));
+}
+
+// [B,T,H,n] as {n, H, T, B}; without heads {n, T, B}.  The stride of a dimension of 1
+// is never used.
+bool map_of(CUtensorMap *m, const void *x, const Strides &s, const Prompt &p, int n, bool heads,
+            int rows) {
+  const long long sb = p.B > 1 ? s.b : 8, st = p.T > 1 ? s.t : 8, sh = p.H > 1 ? s.h : 8;
+  if (heads) {
+    const uint64_t dims[4] = {(uint64_t)n, (uint64_t)p.H, (uint64_t)p.T, (uint64_t)p.B};
+    const long long strides[3] = {sh, st, sb};
+    const uint32_t box[4] = {kChunkCols, 1, (uint32_t)rows, 1};
+    return make_swizzled_map(m, x, 4, dims, strides, box);
+  }
+  const uint64_t dims[3] = {(uint64_t)n, (uint64_t)p.T, (uint64_t)p.B};
+  const long long strides[2] = {st, sb};
+  const uint32_t box[3] = {kChunkCols, (uint32_t)rows, 1};
+  return make_swizzled_map(m, x, 3, dims, strides, box);
+}
+
+}  // namespace
+
+bool prompt_tc_ok(const Prompt &p) {
+  return tensor_ok(p.q, p.q_s, p, true) && tensor_ok(p.k, p.k_s, p, true) &&
+         tensor_ok(p.v, p.v_s, p, true) &&
+         (p.R == 0 || (tensor_ok(p.qr, p.qr_s, p, true) && tensor_ok(p.kr, p.kr_s, p, false)));
+}
+
+cudaError_t launch_prompt_tc(const Prompt &p, cudaStream_t s) {
+  Maps m;
+  if (!map_of(&m.q, p.q, p.q_s, p, p.K, true, kRowsQ) ||
+      !map_of(&m.k, p.k, p.k_s, p, p.K, true, kRowsQ) ||
+      !map_of(&m.v, p.v, p.v_s, p, p.V, true, kRowsQ))
+    return cudaErrorInvalidValue;
+  if (p.R) {
+    if (!map_of(&m.qr, p.qr, p.qr_s, p, p.R, true, kRowsQ) ||
+        !map_of(&m.kr, p.kr, p.kr_s, p, p.R, false, kRowsQ))
+      return cudaErrorInvalidValue;
+  } else {
+    m.qr = m.q;
+    m.kr = m.q;
+  }
+  cudaError_t e = cudaFuncSetAttribute(prompt_fwd_tc_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned pairs = (unsigned)((p.T + 2 * kRowsQ - 1) / (2 * kRowsQ));
+  prompt_fwd_tc_kernel<<<pairs * (unsigned)(p.B * p.H), kThreads, kFwdSmem, s>>>(m, p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_prompt_bwd_tc(const Prompt &, cudaStream_t) { return cudaErrorNotSupported; }
+
 }  // namespace latent
 }  // namespace kda

@@ -7,7 +7,7 @@ import latent64
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
-WAYS = [("simt", F32), ("simt", BF)]
+WAYS = [("simt", F32), ("simt", BF), ("tc", BF)]
 
 
 def ids_of(kind, B, T, gen):
