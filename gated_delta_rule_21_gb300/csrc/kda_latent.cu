@@ -698,7 +698,7 @@ kda_status kda_latent_bwd(const kda_latent_shape *s, const void *q, const void *
   if (way < 0) return KDA_ERR_ALIGNMENT;
   cudaError_t e = find_runs(p, segment_ids, s, workspace, cs);
   if (e != cudaSuccess) return KDA_ERR_CUDA;
-  e = s->dtype == KDA_DTYPE_BF16 ? backward<__nv_bfloat16>(p, false && way == 1, cs)
+  e = s->dtype == KDA_DTYPE_BF16 ? backward<__nv_bfloat16>(p, way == 1, cs)
                                  : backward<float>(p, false, cs);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -300,6 +300,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         if (k < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + k / p.page];
         const bool there = pg >= 0 && pg < p.n_pages;
         wait_or_fail(bar(c.s_full[nt & 1]), (uint32_t)(nt >> 1) & 1, fail);
+        __syncwarp();
         tc::tc_fence_after();
         uint32_t u[32];
         tmem_ld32_wait(tmem + (uint32_t)(nt & 1) * kRows + my_lane, u);
@@ -320,6 +321,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         const bool over = top > mine + kSlack;
         // O^T of the tile before has read P, and its sums stand still
         if (i > 0) wait_or_fail(bar(c.o_done), (uint32_t)(nt - 1) & 1, fail);
+        __syncwarp();
         if (__any_sync(0xffffffffu, over)) {
           const float now = fmaxf(mine, top);
           const float f = now == mine ? 1.f : exp2f(mine - now);

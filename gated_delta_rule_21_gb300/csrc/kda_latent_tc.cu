@@ -106,114 +106,114 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   if (warp >= 8) {
     few_registers();
     if (warp == 8) {
-    // ---- copies ----
-    if (lane == 0) {
-      int kn = 0, vn = 0;
-      bool ok = true;
-      auto load_q = [&](int x) {
-        const int t = (2 * pair + x) * kRowsQ;
-        if (t >= p.T) return;
-        tc::mbar_expect_tx(bar(c.q_full[x]), (uint32_t)nc * kChunkB);
-        for (int i = 0; i < nk; ++i)
-          tma_load_4d(s0 + (uint32_t)(3 * x + i) * kChunkB, &maps.q, i * kChunkCols, h, t, b,
-                      bar(c.q_full[x]));
-        if (nc > nk)
-          tma_load_4d(s0 + (uint32_t)(3 * x + nk) * kChunkB, &maps.qr, 0, h, t, b,
-                      bar(c.q_full[x]));
-      };
-      auto load_k = [&](int j) {
-        for (int i = 0; ok && i < nc; ++i, ++kn) {
-          const int s = kn % kKSlots;
-          ok = wait_or_fail(bar(c.k_empty[s]), (uint32_t)(kn / kKSlots + 1) & 1, fail);
-          if (!ok) return;
-          tc::mbar_expect_tx(bar(c.k_full[s]), kChunkB);
-          const uint32_t d = s0 + kOffK + (uint32_t)s * kChunkB;
-          if (i < nk)
-            tma_load_4d(d, &maps.k, i * kChunkCols, h, j * kRowsQ, b, bar(c.k_full[s]));
-          else
-            tma_load_3d(d, &maps.kr, 0, j * kRowsQ, b, bar(c.k_full[s]));
+      // ---- copies ----
+      if (lane == 0) {
+        int kn = 0, vn = 0;
+        bool ok = true;
+        auto load_q = [&](int x) {
+          const int t = (2 * pair + x) * kRowsQ;
+          if (t >= p.T) return;
+          tc::mbar_expect_tx(bar(c.q_full[x]), (uint32_t)nc * kChunkB);
+          for (int i = 0; i < nk; ++i)
+            tma_load_4d(s0 + (uint32_t)(3 * x + i) * kChunkB, &maps.q, i * kChunkCols, h, t, b,
+                        bar(c.q_full[x]));
+          if (nc > nk)
+            tma_load_4d(s0 + (uint32_t)(3 * x + nk) * kChunkB, &maps.qr, 0, h, t, b,
+                        bar(c.q_full[x]));
+        };
+        auto load_k = [&](int j) {
+          for (int i = 0; ok && i < nc; ++i, ++kn) {
+            const int s = kn % kKSlots;
+            ok = wait_or_fail(bar(c.k_empty[s]), (uint32_t)(kn / kKSlots + 1) & 1, fail);
+            if (!ok) return;
+            tc::mbar_expect_tx(bar(c.k_full[s]), kChunkB);
+            const uint32_t d = s0 + kOffK + (uint32_t)s * kChunkB;
+            if (i < nk)
+              tma_load_4d(d, &maps.k, i * kChunkCols, h, j * kRowsQ, b, bar(c.k_full[s]));
+            else
+              tma_load_4d(d, &maps.kr, 0, 0, j * kRowsQ, b, bar(c.k_full[s]));
+          }
+        };
+        if (jl < jh) {
+          if (has_a) load_q(0);
+          load_k(jl);
+          if (has_b) load_q(1);
+          for (int j = jl; ok && j < jh; ++j, ++vn) {
+            const int s = vn % kVSlots;
+            ok = wait_or_fail(bar(c.v_empty[s]), (uint32_t)(vn / kVSlots + 1) & 1, fail);
+            if (!ok) break;
+            tc::mbar_expect_tx(bar(c.v_full[s]), (uint32_t)nv * kChunkB);
+            for (int i = 0; i < nv; ++i)
+              tma_load_4d(s0 + kOffV + (uint32_t)(2 * s + i) * kChunkB, &maps.v, i * kChunkCols, h,
+                          j * kRowsQ, b, bar(c.v_full[s]));
+            if (j + 1 < jh) load_k(j + 1);
+          }
         }
-      };
-      if (jl < jh) {
-        if (has_a) load_q(0);
-        load_k(jl);
-        if (has_b) load_q(1);
-        for (int j = jl; ok && j < jh; ++j, ++vn) {
-          const int s = vn % kVSlots;
-          ok = wait_or_fail(bar(c.v_empty[s]), (uint32_t)(vn / kVSlots + 1) & 1, fail);
-          if (!ok) break;
-          tc::mbar_expect_tx(bar(c.v_full[s]), (uint32_t)nv * kChunkB);
-          for (int i = 0; i < nv; ++i)
-            tma_load_4d(s0 + kOffV + (uint32_t)(2 * s + i) * kChunkB, &maps.v, i * kChunkCols, h,
-                        j * kRowsQ, b, bar(c.v_full[s]));
-          if (j + 1 < jh) load_k(j + 1);
+        if (*fail) {   // what is on its way comes in before the CTA ends
+          if (has_a) tc::mbar_wait(bar(c.q_full[0]), 0);
+          if (has_b) tc::mbar_wait(bar(c.q_full[1]), 0);
+          for (int k = max(0, kn - kKSlots); k < kn; ++k)
+            tc::mbar_wait(bar(c.k_full[k % kKSlots]), (uint32_t)(k / kKSlots) & 1);
+          for (int k = max(0, vn - kVSlots); k < vn; ++k)
+            tc::mbar_wait(bar(c.v_full[k % kVSlots]), (uint32_t)(k / kVSlots) & 1);
         }
       }
-      if (*fail) {   // what is on its way comes in before the CTA ends
-        if (has_a) tc::mbar_wait(bar(c.q_full[0]), 0);
-        if (has_b) tc::mbar_wait(bar(c.q_full[1]), 0);
-        for (int k = max(0, kn - kKSlots); k < kn; ++k)
-          tc::mbar_wait(bar(c.k_full[k % kKSlots]), (uint32_t)(k / kKSlots) & 1);
-        for (int k = max(0, vn - kVSlots); k < vn; ++k)
-          tc::mbar_wait(bar(c.v_full[k % kVSlots]), (uint32_t)(k / kVSlots) & 1);
-      }
-    }
-    __syncwarp();
+      __syncwarp();
     } else if (warp == 9) {
-    // ---- products: one thread ----
-    if (lane == 0 && jl < jh) {
-      const uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0),
-                     id_o = tc::idesc_bf16(128, nv * kChunkCols, 0, 1);
-      bool ok = true;
-      int count[2] = {0, 0};
-      for (int j = jl - 1; ok && j < jh; ++j) {
-        const int kbase = (j + 1 - jl) * nc, vn = j - jl;
-        for (int x = 0; ok && x < 2; ++x) {
-          if (j >= jl && active(x, j)) {
-            ok = wait_or_fail(bar(c.p_ready[x]), (uint32_t)(count[x] - 1) & 1, fail) &&
-                 wait_or_fail(bar(c.v_full[vn % kVSlots]), (uint32_t)(vn / kVSlots) & 1, fail);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint32_t v = s0 + kOffV + (uint32_t)(2 * (vn % kVSlots)) * kChunkB;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e,
-                          swizzled_desc(v + 2048u * e, kChunkB), id_o,
-                          (count[x] > 1 || e > 0) ? 1u : 0u);
-          }
-          if (j + 1 < jh && active(x, j + 1)) {
-            if (count[x] == 0) {
-              ok = wait_or_fail(bar(c.q_full[x]), 0, fail);
+      // ---- products: one thread ----
+      if (lane == 0 && jl < jh) {
+        const uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0),
+                       id_o = tc::idesc_bf16(128, nv * kChunkCols, 0, 1);
+        bool ok = true;
+        int count[2] = {0, 0};
+        for (int j = jl - 1; ok && j < jh; ++j) {
+          const int kbase = (j + 1 - jl) * nc, vn = j - jl;
+          for (int x = 0; ok && x < 2; ++x) {
+            if (j >= jl && active(x, j)) {
+              ok = wait_or_fail(bar(c.p_ready[x]), (uint32_t)(count[x] - 1) & 1, fail) &&
+                   wait_or_fail(bar(c.v_full[vn % kVSlots]), (uint32_t)(vn / kVSlots) & 1, fail);
               if (!ok) break;
+              tc::tc_fence_after();
+              const uint32_t v = s0 + kOffV + (uint32_t)(2 * (vn % kVSlots)) * kChunkB;
+  #pragma unroll
+              for (int e = 0; e < 8; ++e)
+                mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e,
+                            swizzled_desc(v + 2048u * e, kChunkB), id_o,
+                            (count[x] > 1 || e > 0) ? 1u : 0u);
             }
-            const bool last = x == 1 || !active(1, j + 1);
-            for (int i = 0; i < nc; ++i) {
-              const int s = (kbase + i) % kKSlots;
-              ok = wait_or_fail(bar(c.k_full[s]), (uint32_t)((kbase + i) / kKSlots) & 1, fail);
+            if (j + 1 < jh && active(x, j + 1)) {
+              if (count[x] == 0) {
+                ok = wait_or_fail(bar(c.q_full[x]), 0, fail);
+                if (!ok) break;
+              }
+              const bool last = x == 1 || !active(1, j + 1);
+              for (int i = 0; i < nc; ++i) {
+                const int s = (kbase + i) % kKSlots;
+                ok = wait_or_fail(bar(c.k_full[s]), (uint32_t)((kbase + i) / kKSlots) & 1, fail);
+                if (!ok) break;
+                const uint32_t a = s0 + (uint32_t)(3 * x + i) * kChunkB,
+                               k = s0 + kOffK + (uint32_t)s * kChunkB;
+  #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  tc::mma_bf16(tmem + 128 * x, swizzled_desc(a + 32u * e, 16),
+                               swizzled_desc(k + 32u * e, 16), id_s, (i > 0 || e > 0) ? 1u : 0u);
+                if (last) tc::mma_commit(bar(c.k_empty[s]));
+              }
               if (!ok) break;
-              const uint32_t a = s0 + (uint32_t)(3 * x + i) * kChunkB,
-                             k = s0 + kOffK + (uint32_t)s * kChunkB;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                tc::mma_bf16(tmem + 128 * x, swizzled_desc(a + 32u * e, 16),
-                             swizzled_desc(k + 32u * e, 16), id_s, (i > 0 || e > 0) ? 1u : 0u);
-              if (last) tc::mma_commit(bar(c.k_empty[s]));
+              tc::mma_commit(bar(c.s_full[x]));
+              ++count[x];
+            } else if (j >= jl && active(x, j)) {
+              tc::mma_commit(bar(c.o_done[x]));      // its last
             }
-            if (!ok) break;
-            tc::mma_commit(bar(c.s_full[x]));
-            ++count[x];
-          } else if (j >= jl && active(x, j)) {
-            tc::mma_commit(bar(c.o_done[x]));      // its last
           }
+          if (ok && j >= jl) tc::mma_commit(bar(c.v_empty[vn % kVSlots]));
         }
-        if (ok && j >= jl) tc::mma_commit(bar(c.v_empty[vn % kVSlots]));
+        if (*fail) {
+          tc::mma_commit(bar(c.drain));
+          tc::mbar_wait(bar(c.drain), 0);
+        }
       }
-      if (*fail) {
-        tc::mma_commit(bar(c.drain));
-        tc::mbar_wait(bar(c.drain), 0);
-      }
-    }
-    __syncwarp();
+      __syncwarp();
     }
   } else {
     many_registers();
@@ -231,6 +231,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
     float m = -INFINITY, l = 0.f;
     for (int j = r.lo; j < r.hi; ++j) {
       wait_or_fail(bar(c.s_full[x]), (uint32_t)(j - r.lo) & 1, fail);
+      __syncwarp();
       tc::tc_fence_after();
       uint32_t u[4][32];
 #pragma unroll
@@ -299,6 +300,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
     const bool any = r.lo < r.hi;
     if (any) {
       wait_or_fail(bar(c.o_done[x]), 0, fail);
+      __syncwarp();
       tc::tc_fence_after();
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -327,6 +329,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           reinterpret_cast<uint4 *>(o + 32 * q)[i] =
               make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
       }
+      __syncwarp();
     }
     if (p.lse && row < p.T)
       p.lse[((size_t)b * p.H + h) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -348,24 +351,16 @@ bool tensor_ok(const void *x, const Strides &s, const Prompt &p, bool heads) {
          stride_ok(s.t, p.T) && (!heads || stride_ok(s.h, p.H));
 }
 
-// [B,T,H,n] as {n, H, T, B}; without heads {n, T, B}.  The stride of a dimension of 1
-// is never used.
-bool map_of(CUtensorMap *m, const void *x, const Strides &s, const Prompt &p, int n, bool heads,
-            int rows) {
-  const long long sb = p.B > 1 ? s.b : 8, st = p.T > 1 ? s.t : 8, sh = p.H > 1 ? s.h : 8;
-  if (heads) {
-    const uint64_t dims[4] = {(uint64_t)n, (uint64_t)p.H, (uint64_t)p.T, (uint64_t)p.B};
-    const long long strides[3] = {sh, st, sb};
-    const uint32_t box[4] = {kChunkCols, 1, (uint32_t)rows, 1};
-    return make_swizzled_map(m, x, 4, dims, strides, box);
-  }
-  const uint64_t dims[3] = {(uint64_t)n, (uint64_t)p.T, (uint64_t)p.B};
-  const long long strides[2] = {st, sb};
-  const uint32_t box[3] = {kChunkCols, (uint32_t)rows, 1};
-  return make_swizzled_map(m, x, 3, dims, strides, box);
-}
-
 }  // namespace
+
+// (The stride of a dimension of 1 is never used.)
+bool prompt_map(CUtensorMap *m, const void *x, const Strides &s, const Prompt &p, int heads, int n,
+                int rows) {
+  const uint64_t dims[4] = {(uint64_t)n, (uint64_t)heads, (uint64_t)p.T, (uint64_t)p.B};
+  const long long strides[3] = {heads > 1 ? s.h : 8, p.T > 1 ? s.t : 8, p.B > 1 ? s.b : 8};
+  const uint32_t box[4] = {kChunkCols, 1, (uint32_t)rows, 1};
+  return make_swizzled_map(m, x, 4, dims, strides, box);
+}
 
 bool prompt_tc_ok(const Prompt &p) {
   return tensor_ok(p.q, p.q_s, p, true) && tensor_ok(p.k, p.k_s, p, true) &&
@@ -375,18 +370,14 @@ bool prompt_tc_ok(const Prompt &p) {
 
 cudaError_t launch_prompt_tc(const Prompt &p, cudaStream_t s) {
   Maps m;
-  if (!map_of(&m.q, p.q, p.q_s, p, p.K, true, kRowsQ) ||
-      !map_of(&m.k, p.k, p.k_s, p, p.K, true, kRowsQ) ||
-      !map_of(&m.v, p.v, p.v_s, p, p.V, true, kRowsQ))
+  if (!prompt_map(&m.q, p.q, p.q_s, p, p.H, p.K, kRowsQ) ||
+      !prompt_map(&m.k, p.k, p.k_s, p, p.H, p.K, kRowsQ) ||
+      !prompt_map(&m.v, p.v, p.v_s, p, p.H, p.V, kRowsQ))
     return cudaErrorInvalidValue;
-  if (p.R) {
-    if (!map_of(&m.qr, p.qr, p.qr_s, p, p.R, true, kRowsQ) ||
-        !map_of(&m.kr, p.kr, p.kr_s, p, p.R, false, kRowsQ))
-      return cudaErrorInvalidValue;
-  } else {
-    m.qr = m.q;
-    m.kr = m.q;
-  }
+  m.qr = m.kr = m.q;
+  if (p.R && (!prompt_map(&m.qr, p.qr, p.qr_s, p, p.H, p.R, kRowsQ) ||
+              !prompt_map(&m.kr, p.kr, p.kr_s, p, 1, p.R, kRowsQ)))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prompt_fwd_tc_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem);
   if (e != cudaSuccess) return e;
@@ -394,8 +385,6 @@ cudaError_t launch_prompt_tc(const Prompt &p, cudaStream_t s) {
   prompt_fwd_tc_kernel<<<pairs * (unsigned)(p.B * p.H), kThreads, kFwdSmem, s>>>(m, p);
   return cudaGetLastError();
 }
-
-cudaError_t launch_prompt_bwd_tc(const Prompt &, cudaStream_t) { return cudaErrorNotSupported; }
 
 }  // namespace latent
 }  // namespace kda

@@ -140,5 +140,9 @@ __device__ __forceinline__ void tmem_wait_st() {
 bool make_swizzled_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
                        const long long *strides, const uint32_t *box);
 
+// The map of a prompt's tensor [B,T,heads,n], boxes of `rows` tokens of one head.
+bool prompt_map(CUtensorMap *m, const void *x, const Strides &s, const Prompt &p, int heads, int n,
+                int rows);
+
 }  // namespace latent
 }  // namespace kda
