@@ -50,7 +50,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   unsigned char *smem = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
   Control &c = *reinterpret_cast<Control *>(smem + kOffC);
   const uint32_t s0 = tc::smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int tiles = (p.T + kOuter - 1) / kOuter;
   // one head after another, its longest rows first
   const int bh = (int)(blockIdx.x / (unsigned)tiles), order = (int)(blockIdx.x % (unsigned)tiles);
@@ -124,29 +124,33 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
     __syncwarp();
   } else if (warp == 9) {
     // ---- products: one thread ----
-    if (lane == 0 && n > 0) {
+    if (n > 0 && elect_one()) {
       const uint32_t id_s = tc::idesc_bf16(kOuter, kInner, 0, 0),
                      id_x1 = tc::idesc_bf16(kOuter, nc * kChunkCols, 0, 1),
                      id_x2 = tc::idesc_bf16(kOuter, nv * kChunkCols, 0, 1);
       auto scores = [&](int i) {        // S of tile i
         const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
-        for (int e = 0; e < nc; ++e)
+        const uint64_t dx = swizzled_desc(s0, 16), dy = swizzled_desc(y, 16);
+        for (int e = 0; e < nc; ++e) {
+          const uint64_t x = dx + kXChunkB / 16 * e, z = dy + kYChunkB / 16 * e;
+          const uint32_t old = e > 0 ? 1u : 0u;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_bf16(tmem + kInner * (i & 1),
-                         swizzled_desc(s0 + (uint32_t)e * kXChunkB + 32u * k, 16),
-                         swizzled_desc(y + (uint32_t)e * kYChunkB + 32u * k, 16), id_s,
-                         (e > 0 || k > 0) ? 1u : 0u);
+            tc::mma_bf16(tmem + kInner * (i & 1), x + kStepK * k, z + kStepK * k, id_s,
+                         k > 0 ? 1u : old);
+        }
       };
       auto dp = [&](int i) {
         const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
-        for (int e = 0; e < nv; ++e)
+        const uint64_t dx = swizzled_desc(s0 + 3 * kXChunkB, 16),
+                       dy = swizzled_desc(y + 3 * kYChunkB, 16);
+        for (int e = 0; e < nv; ++e) {
+          const uint64_t x = dx + kXChunkB / 16 * e, z = dy + kYChunkB / 16 * e;
+          const uint32_t old = e > 0 ? 1u : 0u;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_bf16(tmem + kTdP,
-                         swizzled_desc(s0 + (uint32_t)(3 + e) * kXChunkB + 32u * k, 16),
-                         swizzled_desc(y + (uint32_t)(3 + e) * kYChunkB + 32u * k, 16), id_s,
-                         (e > 0 || k > 0) ? 1u : 0u);
+            tc::mma_bf16(tmem + kTdP, x + kStepK * k, z + kStepK * k, id_s, k > 0 ? 1u : old);
+        }
       };
       auto loaded = [&](int i) {
         return wait_or_fail(bar(c.y_full[i % kStages]), (uint32_t)(i / kStages) & 1, fail);
@@ -172,18 +176,18 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         }
         // steps of 16 rows of Y: the two halves of 32 stand 32 columns apart
         const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
-        const uint32_t w = tmem + kInner * (i & 1);
+        const uint32_t w = tmem + kInner * (i & 1), old = i > 0 ? 1u : 0u;
+        const uint64_t dy = swizzled_desc(y, kYChunkB);
         if (kKeys) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mma_bf16_ts(tmem + kTX2, w + 32 * (e >> 1) + 8 * (e & 1),
-                        swizzled_desc(y + 3 * kYChunkB + 2048u * e, kYChunkB), id_x2,
-                        (i > 0 || e > 0) ? 1u : 0u);
+                        dy + 3 * kYChunkB / 16 + kStepRows * e, id_x2, e > 0 ? 1u : old);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          mma_bf16_ts(tmem + kTX1, w + 16 + 32 * (e >> 1) + 8 * (e & 1),
-                      swizzled_desc(y + 2048u * e, kYChunkB), id_x1, (i > 0 || e > 0) ? 1u : 0u);
+          mma_bf16_ts(tmem + kTX1, w + 16 + 32 * (e >> 1) + 8 * (e & 1), dy + kStepRows * e, id_x1,
+                      e > 0 ? 1u : old);
         tc::mma_commit(bar(c.y_empty[i % kStages]));
       }
       if (ok) tc::mma_commit(bar(c.done));

@@ -209,22 +209,25 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
   }
 }
 
-// Joins the parts of one row: its threads are p.C / 4 columns of four channels, and
-// groups that share the parts.
-template <typename T>
-__global__ void __launch_bounds__(512) join_kernel(Step p) {
-  __shared__ float4 sums[512];
-  __shared__ float s_l[4];
-  __shared__ int s_bad;
-  const int cols = p.C / 4, groups = blockDim.x / cols, col = threadIdx.x % cols,
-            group = threadIdx.x / cols;
-  const int rows = p.T * p.H, b = (int)(blockIdx.x / (unsigned)rows),
-            r = (int)(blockIdx.x % (unsigned)rows);
-  const int t = r / p.H, h = r % p.H;
+// Joins the parts of one row, p.C / 4 threads a row with four channels each.  kGroups
+// of them share the parts of one row (where there are few rows with many parts), or
+// with kGroups 1 take a row each.
+template <typename T, int kGroups>
+__global__ void __launch_bounds__(512) join_kernel(Step p, int block_rows) {
+  __shared__ float4 sums[kGroups > 1 ? 512 : 1];
+  __shared__ float s_l[kGroups];
+  const int cols = p.C / 4, lane = threadIdx.x & 31, col = threadIdx.x % cols,
+            group = kGroups > 1 ? threadIdx.x / cols : 0;
+  const int rows = p.T * p.H;
+  const unsigned index = blockIdx.x * (unsigned)block_rows +
+                         (kGroups > 1 ? 0u : threadIdx.x / (unsigned)cols);
   after_previous();
+  if (index >= (unsigned)p.B * (unsigned)rows) return;    // (a row's threads are whole warps)
+  const int b = (int)(index / (unsigned)rows), r = (int)(index % (unsigned)rows);
+  const int t = r / p.H, h = r % p.H;
   const Seq s = seq_of(p, b);
+  const long long total = p.plan[p.B], before = p.plan[b];
   const int tiles = tiles_of(s);
-  const long long total = p.plan[p.B];
   T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.C;
   float *lse = p.lse ? p.lse + ((size_t)b * p.H + h) * p.T + t : nullptr;
   if (tiles == 0) {
@@ -235,50 +238,66 @@ __global__ void __launch_bounds__(512) join_kernel(Step p) {
     }
     return;
   }
-  const long long u0 = p.plan[b] + (long long)(r / kRows) * tiles;
+  const long long u0 = before + (long long)(r / kRows) * tiles;
   const int g0 = part_of(total, u0), g1 = part_of(total, u0 + tiles - 1);
   if (g0 == g1) return;
-  auto slot = [&](int g) {
-    return (size_t)(2 * g + (part_begin(total, g) >= u0 ? 0 : 1)) * kRows + r % kRows;
-  };
+  // only the first part can begin before the row's first tile
+  const bool late = part_begin(total, g0) < u0;
+  auto slot = [&](int g) { return (size_t)(2 * g + (g == g0 && late ? 1 : 0)) * kRows + r % kRows; };
+  const float2 *stats = reinterpret_cast<const float2 *>(p.stats);
   float m = -INFINITY;
-  for (int g = g0; g <= g1; ++g) m = fmaxf(m, p.stats[2 * slot(g)]);
+  for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, stats[slot(g)].x);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   const float base = m == -INFINITY ? 0.f : m;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-#pragma unroll 4
-  for (int g = g0 + group; g <= g1; g += groups) {
+#pragma unroll 8
+  for (int g = g0 + group; g <= g1; g += kGroups) {
     const size_t k = slot(g);
-    const float f = exp2f(p.stats[2 * k] - base);
+    const float2 z = stats[k];
     const float4 x = reinterpret_cast<const float4 *>(p.parts)[k * cols + col];
-    l = fmaf(f, p.stats[2 * k + 1], l);
+    const float f = exp2f(z.x - base);
+    l = fmaf(f, z.y, l);
     a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y);
     a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
   }
-  sums[threadIdx.x] = a;
-  if (col == 0) s_l[group] = l;
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  if (group == 0) {
-    for (int g = 1; g < groups; ++g) {
+  if (kGroups > 1) {
+    sums[threadIdx.x] = a;
+    if (col == 0) s_l[group] = l;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
       const float4 x = sums[g * cols + col];
       a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
       l += s_l[g];
     }
-    const float v[4] = {a.x, a.y, a.z, a.w};
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float z = l == 0.f ? 0.f : v[e] / l;
-      bad |= !finite(z);
-      o[4 * col + e] = from_f32<T>(z);
-    }
-    if (col == 0 && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    if (bad) s_bad = 1;
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float v[4] = {a.x, a.y, a.z, a.w};
+  bool bad = false;
+  struct alignas(4 * sizeof(T)) Four {
+    T x[4];
+  } w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float z = l == 0.f ? 0.f : v[e] * inv;
+    bad |= !finite(z);
+    w.x[e] = from_f32<T>(z);
+  }
+  *reinterpret_cast<Four *>(o + 4 * col) = w;
+  if (col == 0 && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   if (p.T == 1) return;   // every row sees what the others see
-  __syncthreads();
-  if (s_bad && threadIdx.x < 32) step_row<T>(p, b, r, seen(p, s, r), threadIdx.x);
+  // a row with a value that is not finite, again; its warps write the same values
+  const int named = 1 + (kGroups > 1 ? 0 : threadIdx.x / cols);
+  int any = bad ? 1 : 0;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+               "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+               : "=r"(any)
+               : "r"(any), "r"(named), "r"(cols)
+               : "memory");
+  if (any) step_row<T>(p, b, r, seen(p, s, r), lane);
 }
 
 template <typename T>
@@ -291,11 +310,18 @@ cudaError_t launch_simt(const Step &p, cudaStream_t cs) {
   return cudaGetLastError();
 }
 
+// Rows with many parts (fewer than 38 sequences and row tiles, so 4 parts or more each
+// where the texts are long) share them among 4 groups: two texts of 131072 tokens,
+// TODO.  More rows take a row each.
 template <typename T>
 cudaError_t launch_join(const Step &p, cudaStream_t cs) {
-  const int cols = p.C / 4, groups = 4;
-  return launch_next(join_kernel<T>, dim3((unsigned)((long long)p.B * p.T * p.H)),
-                     (unsigned)(cols * groups), 0, cs, p);
+  const int cols = p.C / 4;
+  const long long rows = (long long)p.B * p.T * p.H;
+  if ((long long)p.B * p.row_tiles * 4 <= kParts)
+    return launch_next(join_kernel<T, 4>, dim3((unsigned)rows), (unsigned)(cols * 4), 0, cs, p, 1);
+  const int block_rows = 256 / cols;
+  return launch_next(join_kernel<T, 1>, dim3((unsigned)((rows + block_rows - 1) / block_rows)), 256u,
+                     0, cs, p, block_rows);
 }
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

@@ -112,7 +112,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
   const uint32_t s_ring = tc::smem_u32(smem);
   const uint32_t s_rope = s_ring + (uint32_t)ring.pairs * kPairB;
   const uint32_t s_q = s_ring + kRing * kChunkB, s_p = s_q + kQB;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   if (tid == 0) {
     for (int i = 0; i < kMaxPairs; ++i) {
@@ -146,105 +146,113 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
   if (warp == 4) {
     // ---- copies: lane k has the tile's k-th box of tokens ----
     const int boxes = kTile / ring.box;
-    long long np = 0, nr = 0;
+    const int log_page = __ffs(p.page) - 1;
+    Slot pr = {0, 0}, rr = {0, 0};
+    int np = 0, nr = 0;                    // copied, up to the slots there are
     bool ok = true;
     while (ok && cur.next(p, g)) {
       for (int i = 0; ok && i < g.n; ++i) {
         const int t0 = (g.j0 + i) * kTile + lane * ring.box;
         int pg = -1;
-        if (lane < boxes && t0 < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + t0 / p.page];
+        if (lane < boxes && t0 < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + (t0 >> log_page)];
         const bool there = pg >= 0 && pg < p.n_pages;
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, there)) *
                                (uint32_t)ring.box * kRowBytes;
-        const int in_page = t0 % p.page;
-        for (int k = 0; ok && k < ring.npair + (rope ? 1 : 0); ++k) {
-          // the first pair, the rope chunk, the other pairs
-          const bool is_rope = rope && k == 1;
-          const int pair = k == 0 ? 0 : rope ? k - 1 : k;
-          uint32_t full, dst;
-          if (is_rope) {
-            const int s = (int)(nr % ring.ropes);
-            ok = wait_or_fail(bar(c.rempty[s]), (uint32_t)(nr / ring.ropes + 1) & 1, fail);
-            full = bar(c.rfull[s]);
-            dst = s_rope + (uint32_t)s * kChunkB;
-          } else {
-            const int s = (int)(np % ring.pairs);
-            ok = wait_or_fail(bar(c.empty[s]), (uint32_t)(np / ring.pairs + 1) & 1, fail);
-            full = bar(c.full[s]);
-            dst = s_ring + (uint32_t)s * kPairB;
-          }
-          ok = __all_sync(0xffffffffu, ok);
+        const int in_page = t0 & (p.page - 1);
+        // the first pair, the rope chunk, the other pairs
+        for (int k = 0; k < ring.npair; ++k) {
+          ok = __all_sync(0xffffffffu, wait_or_fail(bar(c.empty[pr.at]), pr.lap ^ 1u, fail));
           if (!ok) break;
-          if (lane == 0) tc::mbar_expect_tx(full, is_rope ? bytes : 2 * bytes);
+          const uint32_t full = bar(c.full[pr.at]);
+          if (lane == 0) tc::mbar_expect_tx(full, 2 * bytes);
           __syncwarp();
           if (there) {
-            dst += (uint32_t)lane * (uint32_t)ring.box * kRowBytes;
-            const int x = is_rope ? p.C : pair * 2 * kChunkCols;
-            tma_load_3d(dst, &map, x, in_page, pg, full);
-            if (!is_rope) tma_load_3d(dst + kChunkB, &map, x + kChunkCols, in_page, pg, full);
+            const uint32_t dst = s_ring + (uint32_t)pr.at * kPairB + (uint32_t)lane * (uint32_t)ring.box * kRowBytes;
+            tma_load_3d(dst, &map, k * 2 * kChunkCols, in_page, pg, full);
+            tma_load_3d(dst + kChunkB, &map, (k * 2 + 1) * kChunkCols, in_page, pg, full);
           }
-          if (is_rope) ++nr;
-          else ++np;
+          pr.next(ring.pairs);
+          np = min(np + 1, ring.pairs);
+          if (k > 0 || !rope) continue;
+          ok = __all_sync(0xffffffffu, wait_or_fail(bar(c.rempty[rr.at]), rr.lap ^ 1u, fail));
+          if (!ok) break;
+          const uint32_t rfull = bar(c.rfull[rr.at]);
+          if (lane == 0) tc::mbar_expect_tx(rfull, bytes);
+          __syncwarp();
+          if (there)
+            tma_load_3d(s_rope + (uint32_t)rr.at * kChunkB + (uint32_t)lane * (uint32_t)ring.box * kRowBytes,
+                        &map, p.C, in_page, pg, rfull);
+          rr.next(ring.ropes);
+          nr = min(nr + 1, ring.ropes);
         }
       }
     }
     if (*fail) {   // what is on its way comes in before the CTA ends
-      for (long long k = np > ring.pairs ? np - ring.pairs : 0; k < np; ++k)
-        tc::mbar_wait(bar(c.full[k % ring.pairs]), (uint32_t)(k / ring.pairs) & 1);
-      for (long long k = nr > ring.ropes ? nr - ring.ropes : 0; k < nr; ++k)
-        tc::mbar_wait(bar(c.rfull[k % ring.ropes]), (uint32_t)(k / ring.ropes) & 1);
+      auto drain = [](uint64_t *full, Slot s, int slots, int n) {
+        for (; n > 0; --n) {               // the last n, from the latest back
+          if (--s.at < 0) {
+            s.at = slots - 1;
+            s.lap ^= 1u;
+          }
+          tc::mbar_wait(tc::smem_u32(full + s.at), s.lap);
+        }
+      };
+      drain(c.full, pr, ring.pairs, np);
+      drain(c.rfull, rr, ring.ropes, nr);
     }
   } else if (warp == 5) {
     // ---- products: one thread ----
-    if (lane == 0) {
-      const uint32_t id_s = tc::idesc_bf16(kTile, kRows, 0, 0),
-                     id_o = tc::idesc_bf16(128, kRows, 1, 1);
-      long long np = 0, nr = 0, nt = 0;
-      int ns = 0;
+    if (elect_one()) {
+      constexpr uint32_t id_s = tc::idesc_bf16(kTile, kRows, 0, 0),
+                         id_o = tc::idesc_bf16(128, kRows, 1, 1);
+      const uint64_t dp = tc::smem_desc(s_p, kTile * 16), dq0 = swizzled_desc(s_q, 16);
+      // S (+)= a chunk of 64 channels
+      auto chunk = [&](uint32_t t_s, uint32_t a, uint64_t dq, uint32_t old) {
+        const uint64_t da = swizzled_desc(a, 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          tc::mma_bf16(t_s, da + kStepK * e, dq + kStepK * e, id_s, e > 0 ? 1u : old);
+      };
+      Slot pr = {0, 0}, rr = {0, 0};
+      uint32_t nt = 0, ns = 0;
       bool ok = true;
       while (ok && cur.next(p, g)) {
-        ok = wait_or_fail(bar(c.q_ready), (uint32_t)ns & 1, fail);
+        ok = wait_or_fail(bar(c.q_ready), ns & 1, fail);
         ++ns;
         tc::tc_fence_after();
         for (int i = 0; ok && i < g.n; ++i, ++nt) {
-          const uint32_t t_s = tmem + (uint32_t)(nt & 1) * kRows;
-          bool more = false;
-          for (int k = 0; ok && k < ring.npair + (rope ? 1 : 0); ++k) {
-            const bool is_rope = rope && k == 1;
-            const int pair = k == 0 ? 0 : rope ? k - 1 : k;
-            const int s = is_rope ? (int)(nr % ring.ropes) : (int)((np + pair) % ring.pairs);
-            ok = is_rope ? wait_or_fail(bar(c.rfull[s]), (uint32_t)(nr / ring.ropes) & 1, fail)
-                         : wait_or_fail(bar(c.full[s]),
-                                        (uint32_t)((np + pair) / ring.pairs) & 1, fail);
+          const uint32_t t_s = tmem + (nt & 1) * kRows;
+          Slot in = pr;
+          for (int k = 0; k < ring.npair; ++k) {
+            ok = wait_or_fail(bar(c.full[in.at]), in.lap, fail);
             if (!ok) break;
-            const uint32_t a = is_rope ? s_rope + (uint32_t)s * kChunkB
-                                       : s_ring + (uint32_t)s * kPairB;
-            const int chunk = is_rope ? 2 * ring.npair : 2 * pair;
-            for (int h = 0; h < (is_rope ? 1 : 2); ++h)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                tc::mma_bf16(t_s, swizzled_desc(a + (uint32_t)h * kChunkB + 32u * e, 16),
-                             swizzled_desc(s_q + (uint32_t)(chunk + h) * kQChunkB + 32u * e, 16),
-                             id_s, more ? 1u : 0u);
-                more = true;
-              }
-            if (is_rope) tc::mma_commit(bar(c.rempty[s]));
+            const uint32_t a = s_ring + (uint32_t)in.at * kPairB;
+            const uint64_t dq = dq0 + (uint64_t)(2 * k) * (kQChunkB / 16);
+            chunk(t_s, a, dq, k > 0 ? 1u : 0u);
+            chunk(t_s, a + kChunkB, dq + kQChunkB / 16, 1u);
+            in.next(ring.pairs);
+            if (k > 0 || !rope) continue;
+            ok = wait_or_fail(bar(c.rfull[rr.at]), rr.lap, fail);
+            if (!ok) break;
+            chunk(t_s, s_rope + (uint32_t)rr.at * kChunkB,
+                  dq0 + (uint64_t)(2 * ring.npair) * (kQChunkB / 16), 1u);
+            tc::mma_commit(bar(c.rempty[rr.at]));
+            rr.next(ring.ropes);
           }
           if (!ok) break;
-          if (rope) ++nr;
           tc::mma_commit(bar(c.s_full[nt & 1]));
-          ok = wait_or_fail(bar(c.p_ready), (uint32_t)nt & 1, fail);
+          ok = wait_or_fail(bar(c.p_ready), nt & 1, fail);
           if (!ok) break;
           tc::tc_fence_after();
-          for (int m = 0; m < ring.npair; ++m, ++np) {
-            const int s = (int)(np % ring.pairs);
-            const uint32_t a = s_ring + (uint32_t)s * kPairB;
+          const uint32_t old = i > 0 ? 1u : 0u;
+          for (int m = 0; m < ring.npair; ++m) {
+            const uint64_t da = swizzled_desc(s_ring + (uint32_t)pr.at * kPairB, kChunkB);
 #pragma unroll
             for (int e = 0; e < kTile / 16; ++e)
-              tc::mma_bf16(t_o + (uint32_t)m * kRows, swizzled_desc(a + 2048u * e, kChunkB),
-                           tc::smem_desc(s_p + 256u * e, kTile * 16), id_o,
-                           (i > 0 || e > 0) ? 1u : 0u);
-            tc::mma_commit(bar(c.empty[s]));
+              tc::mma_bf16(t_o + (uint32_t)m * kRows, da + kStepRows * e, dp + 256 / 16 * e, id_o,
+                           e > 0 ? 1u : old);
+            tc::mma_commit(bar(c.empty[pr.at]));
+            pr.next(ring.pairs);
           }
           tc::mma_commit(bar(c.o_done));
         }
@@ -260,32 +268,40 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
     const float scale = p.scale * kLog2e;
     const int rows = p.T * p.H;
     const uint32_t my_lane = (uint32_t)warp << 21;       // 32 lanes a warp
-    long long nt = 0, np = 0;
+    const int log_page = __ffs(p.page) - 1;
+    Slot pr = {0, 0};
+    uint32_t nt = 0;
     while (cur.next(p, g)) {
       const int r0 = g.rt * kRows;
-      // the queries, 8 channels a thread at a time
+      // the queries, 8 channels a thread at a time, all on their way at once
       const int pieces = (p.C + (rope ? kChunkCols : 0)) / 8;
-      for (int i = tid; i < kRows * pieces; i += kSoftmax) {
-        const int rr = i / pieces, ch = (i % pieces) * 8, r = r0 + rr;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (r < rows && ch < p.C + p.R) {
-          const int t = r / p.H, h = r % p.H;
-          const __nv_bfloat16 *q = ch < p.C
-              ? at<__nv_bfloat16>(p.q, p.q_s, g.b, t, h) + ch
-              : at<__nv_bfloat16>(p.qr, p.qr_s, g.b, t, h) + (ch - p.C);
-          if ((reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(q);
-            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-          } else {
-            const unsigned short *u = reinterpret_cast<const unsigned short *>(q);
+      for (int rr = warp; rr < kRows; rr += 4) {
+        const int r = r0 + rr, t = r / p.H, h = r % p.H;
+        const bool live = r < rows;
+        const __nv_bfloat16 *q = live ? at<__nv_bfloat16>(p.q, p.q_s, g.b, t, h) : nullptr;
+        const __nv_bfloat16 *qr =
+            live && rope ? at<__nv_bfloat16>(p.qr, p.qr_s, g.b, t, h) : nullptr;
+        const bool wide = ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(qr)) & 15) == 0;
+        for (int i = lane; i < pieces; i += 32) {
+          const int ch = i * 8;
+          const __nv_bfloat16 *x = ch < p.C ? q + ch : qr + (ch - p.C);
+          const uint32_t off = (s_q - s_ring) + (uint32_t)(ch / kChunkCols) * kQChunkB +
+                               piece_off(rr, (ch % kChunkCols) / 8);
+          if (live && ch < p.C + p.R && wide) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s_ring + off), "l"(x)
+                         : "memory");
+            continue;
+          }
+          uint32_t w[4] = {0, 0, 0, 0};
+          if (live && ch < p.C + p.R) {
+            const unsigned short *u = reinterpret_cast<const unsigned short *>(x);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = u[2 * e] | (uint32_t)u[2 * e + 1] << 16;
           }
+          *reinterpret_cast<uint4 *>(smem + off) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4 *>(smem + (s_q - s_ring) + (uint32_t)(ch / kChunkCols) * kQChunkB +
-                                   piece_off(rr, (ch % kChunkCols) / 8)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (tid < kRows) c.lim[tid] = r0 + tid < rows ? seen(p, g.s, r0 + tid) : 0;
       tc::fence_proxy_async();
       tc::mbar_arrive(bar(c.q_ready));
@@ -297,13 +313,13 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
       for (int i = 0; i < g.n; ++i, ++nt) {
         const int k = (g.j0 + i) * kTile + tid;
         int pg = -1;
-        if (k < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + k / p.page];
+        if (k < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + (k >> log_page)];
         const bool there = pg >= 0 && pg < p.n_pages;
-        wait_or_fail(bar(c.s_full[nt & 1]), (uint32_t)(nt >> 1) & 1, fail);
+        wait_or_fail(bar(c.s_full[nt & 1]), (nt >> 1) & 1, fail);
         __syncwarp();
         tc::tc_fence_after();
         uint32_t u[32];
-        tmem_ld32_wait(tmem + (uint32_t)(nt & 1) * kRows + my_lane, u);
+        tmem_ld32_wait(tmem + (nt & 1) * kRows + my_lane, u);
         float v[kRows], w[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) v[r] = there ? __uint_as_float(u[r]) * scale : -INFINITY;
@@ -320,7 +336,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
                                 fmaxf(c.top[2][lane], c.top[3][lane]));
         const bool over = top > mine + kSlack;
         // O^T of the tile before has read P, and its sums stand still
-        if (i > 0) wait_or_fail(bar(c.o_done), (uint32_t)(nt - 1) & 1, fail);
+        if (i > 0) wait_or_fail(bar(c.o_done), (nt - 1) & 1, fail);
         __syncwarp();
         if (__any_sync(0xffffffffu, over)) {
           const float now = fmaxf(mine, top);
@@ -363,17 +379,18 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         // not be NaN
         if (!there) {
           const uint4 zero = make_uint4(0, 0, 0, 0);
+          Slot in = pr;
           for (int m = 0; m < ring.npair; ++m) {
-            const long long n = np + m;
-            wait_or_fail(bar(c.full[n % ring.pairs]), (uint32_t)(n / ring.pairs) & 1, fail);
-            unsigned char *d = smem + (uint32_t)(n % ring.pairs) * kPairB + (uint32_t)tid * kRowBytes;
+            wait_or_fail(bar(c.full[in.at]), in.lap, fail);
+            unsigned char *d = smem + (uint32_t)in.at * kPairB + (uint32_t)tid * kRowBytes;
             for (int e = 0; e < 8; ++e) {
               *reinterpret_cast<uint4 *>(d + 16 * e) = zero;
               *reinterpret_cast<uint4 *>(d + kChunkB + 16 * e) = zero;
             }
+            in.next(ring.pairs);
           }
         }
-        np += ring.npair;
+        for (int m = 0; m < ring.npair; ++m) pr.next(ring.pairs);
         tc::fence_proxy_async();
         tc::tc_fence_before();
         tc::mbar_arrive(bar(c.p_ready));
@@ -397,7 +414,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         }
         c.val[lane] = g.whole ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
       }
-      wait_or_fail(bar(c.o_done), (uint32_t)(nt - 1) & 1, fail);
+      wait_or_fail(bar(c.o_done), (nt - 1) & 1, fail);
       softmax_barrier();
       tc::tc_fence_after();
       unsigned bad = 0;

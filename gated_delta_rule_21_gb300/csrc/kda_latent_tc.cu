@@ -63,7 +63,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   unsigned char *smem = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
   FwdControl &c = *reinterpret_cast<FwdControl *>(smem + kOffC);
   const uint32_t s0 = tc::smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int pairs = (p.T + 2 * kRowsQ - 1) / (2 * kRowsQ);
   // a head's keys stay in L2 while its queries are worked on, the longest first
   const int bh = (int)(blockIdx.x / (unsigned)pairs),
@@ -161,9 +161,9 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       __syncwarp();
     } else if (warp == 9) {
       // ---- products: one thread ----
-      if (lane == 0 && jl < jh) {
-        const uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0),
-                       id_o = tc::idesc_bf16(128, nv * kChunkCols, 0, 1);
+      if (jl < jh && elect_one()) {
+        constexpr uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0);
+        const uint32_t id_o = tc::idesc_bf16(128, nv * kChunkCols, 0, 1);
         bool ok = true;
         int count[2] = {0, 0};
         for (int j = jl - 1; ok && j < jh; ++j) {
@@ -174,12 +174,13 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
                    wait_or_fail(bar(c.v_full[vn % kVSlots]), (uint32_t)(vn / kVSlots) & 1, fail);
               if (!ok) break;
               tc::tc_fence_after();
-              const uint32_t v = s0 + kOffV + (uint32_t)(2 * (vn % kVSlots)) * kChunkB;
-  #pragma unroll
+              const uint64_t dv =
+                  swizzled_desc(s0 + kOffV + (uint32_t)(2 * (vn % kVSlots)) * kChunkB, kChunkB);
+              const uint32_t old = count[x] > 1 ? 1u : 0u;
+#pragma unroll
               for (int e = 0; e < 8; ++e)
-                mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e,
-                            swizzled_desc(v + 2048u * e, kChunkB), id_o,
-                            (count[x] > 1 || e > 0) ? 1u : 0u);
+                mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e, dv + kStepRows * e, id_o,
+                            e > 0 ? 1u : old);
             }
             if (j + 1 < jh && active(x, j + 1)) {
               if (count[x] == 0) {
@@ -191,12 +192,13 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
                 const int s = (kbase + i) % kKSlots;
                 ok = wait_or_fail(bar(c.k_full[s]), (uint32_t)((kbase + i) / kKSlots) & 1, fail);
                 if (!ok) break;
-                const uint32_t a = s0 + (uint32_t)(3 * x + i) * kChunkB,
-                               k = s0 + kOffK + (uint32_t)s * kChunkB;
-  #pragma unroll
+                const uint64_t da = swizzled_desc(s0 + (uint32_t)(3 * x + i) * kChunkB, 16),
+                               dk = swizzled_desc(s0 + kOffK + (uint32_t)s * kChunkB, 16);
+                const uint32_t old = i > 0 ? 1u : 0u;
+#pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  tc::mma_bf16(tmem + 128 * x, swizzled_desc(a + 32u * e, 16),
-                               swizzled_desc(k + 32u * e, 16), id_s, (i > 0 || e > 0) ? 1u : 0u);
+                  tc::mma_bf16(tmem + 128 * x, da + kStepK * e, dk + kStepK * e, id_s,
+                               e > 0 ? 1u : old);
                 if (last) tc::mma_commit(bar(c.k_empty[s]));
               }
               if (!ok) break;

@@ -26,7 +26,10 @@ __device__ __forceinline__ uint32_t piece_off(int row, int piece) {
 }
 
 // Operand descriptor in the 128-byte swizzle.  lbo: bytes to the next 64 channels
-// (MN-major); 8 rows are 1024 bytes.
+// (MN-major); 8 rows are 1024 bytes.  A step through shared memory adds its bytes / 16:
+// the one thread that issues the products makes a descriptor per chunk, not per
+// instruction (made for each of them, an instruction took 146 cycles to issue).
+constexpr uint64_t kStepK = 32 / 16, kStepRows = 2048 / 16;   // K = 16, K-major and MN-major
 __device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t lbo) {
   uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
   d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
@@ -59,7 +62,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // that share barriers of their own go on all the same, without waiting, so that all of
 // them come to the end.
 __device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, volatile int *fail) {
-  if (*fail) return false;
   if (tc::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!tc::mbar_try_wait(bar, parity)) {
@@ -71,6 +73,33 @@ __device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, vola
   }
   return true;
 }
+
+// One thread of a warp that is whole.  (The compiler then knows that the branch holds
+// one thread; behind `lane == 0` it readies each product's uniform registers for many.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+
+// A place in a ring of slots: the slot and how many times it has been used, modulo 2.
+struct Slot {
+  int at;
+  uint32_t lap;
+  __device__ __forceinline__ void next(int slots) {
+    if (++at == slots) {
+      at = 0;
+      lap ^= 1u;
+    }
+  }
+};
 
 // D (+)= A B over one K = 16 step, A in tensor memory (bf16, two a column).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
