@@ -168,7 +168,6 @@ __device__ __noinline__ void key_grad_row(const Prompt &p, int b, int h, int j, 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 // ---- the absorbed form ------------------------------------------------------
-constexpr int kTile = 128;       // tokens of the cache in one unit of work
 constexpr int kRows = 32;        // rows (new token, head) that share a pass over the cache
 constexpr int kParts = 152;      // CTAs the work is cut for: one for each SM of a GB300
 
@@ -176,6 +175,8 @@ struct Step {
   int B, T, H, C, R;
   int max_pages, n_pages, page;
   int row_tiles;                 // ceil(T * H / kRows)
+  int tile;                      // tokens of the cache in one unit of work
+  int extra;                     // units that beginning and ending a row tile is worth
   long long page_stride, token_stride;
   const void *q, *qr, *cache;
   Strides q_s, qr_s;
@@ -183,7 +184,8 @@ struct Step {
   float scale;
   void *o;
   float *lse;
-  long long *plan;               // [B + 1]: units before each sequence, and of all
+  int2 *plan;                    // [B][row_tiles]: the first and last part of a row tile, the
+                                 // first one as its slot; {-1, -1}: it was written whole
   float *parts;                  // [2 * kParts][kRows][C]: sums, not yet divided
   float *stats;                  // [2 * kParts][kRows][2]: maximum (of scale log2e s) and sum
   uint32_t *status;
@@ -210,10 +212,13 @@ __device__ __forceinline__ int seen(const Step &p, const Seq &s, int r) {
   const long long n = (long long)s.length - s.fresh + t + 1;
   return n < 0 ? 0 : n > s.held ? s.held : (int)n;
 }
-__device__ __forceinline__ int tiles_of(const Seq &s) { return (s.held + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(const Step &p, const Seq &s) {
+  return (s.held + p.tile - 1) / p.tile;
+}
 
-// Units are numbered by sequence, row tile and tile of tokens; CTA g takes
-// [begin(g), begin(g + 1)) of `total`.  No CTA between two that have work is idle.
+// Units are numbered by sequence, row tile and tile of tokens, `extra` ones in front of
+// a row tile's first; CTA g takes [begin(g), begin(g + 1)) of `total`.  No CTA between
+// two that have work is idle.
 __device__ __forceinline__ long long parts_used(long long total) {
   return total < kParts ? total : kParts;
 }
@@ -221,13 +226,12 @@ __device__ __forceinline__ long long part_begin(long long total, int g) {
   const long long n = parts_used(total);
   return g >= n ? total : total * g / n;
 }
-__device__ __forceinline__ int part_of(long long total, long long unit) {
-  return (int)(((unit + 1) * parts_used(total) - 1) / total);
+__device__ __forceinline__ long long units_of(const Step &p, const Seq &s) {
+  return s.held ? (long long)(tiles_of(p, s) + p.extra) * p.row_tiles : 0;
 }
 
 // The first unit of this CTA: sequence, and units into it.  All threads call; `tmp`
-// has 36 words.  CTA 0 leaves the table of all sequences for the kernel that joins
-// the parts.  Returns the CTA's number of units.
+// has 36 words.
 struct Work {
   long long unit, end;
   int b;
@@ -236,21 +240,21 @@ struct Work {
 __device__ __forceinline__ Work find_work(const Step &p, long long *tmp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x, g = blockIdx.x;
   long long total = 0;
-  for (int b = tid; b < p.B; b += n) total += tiles_of(seq_of(p, b));
+  if (p.B > n) {            // else one pass over the sequences shows the total too
+    for (int b = tid; b < p.B; b += n) total += units_of(p, seq_of(p, b));
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) tmp[warp] = total;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < (n >> 5); ++w) total += tmp[w];
-  total *= p.row_tiles;
-  Work x = {part_begin(total, g), part_begin(total, g + 1), 0, 0};
-  if (g == 0 && tid == 0) p.plan[p.B] = total;
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) tmp[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < (n >> 5); ++w) total += tmp[w];
+  }
+  Work x = {0, 0, 0, 0};
   long long base = 0;
   for (int b0 = 0; b0 < p.B; b0 += n) {
-    __syncthreads();
+    if (b0 || p.B > n) __syncthreads();
     const int b = b0 + tid;
-    const long long mine = b < p.B ? (long long)tiles_of(seq_of(p, b)) * p.row_tiles : 0;
+    const long long mine = b < p.B ? units_of(p, seq_of(p, b)) : 0;
     long long up = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -264,8 +268,12 @@ __device__ __forceinline__ Work find_work(const Step &p, long long *tmp) {
       if (w < warp) up += tmp[w];
       all += tmp[w];
     }
+    if (p.B <= n) total = all;
+    if (b0 == 0) {
+      x.unit = part_begin(total, g);
+      x.end = part_begin(total, g + 1);
+    }
     const long long before = base + up - mine;
-    if (g == 0 && b < p.B) p.plan[b] = before;
     if (mine && x.unit >= before && x.unit < before + mine) {
       tmp[33] = b;
       tmp[34] = x.unit - before;
@@ -279,6 +287,55 @@ __device__ __forceinline__ Work find_work(const Step &p, long long *tmp) {
   }
   return x;
 }
+
+// A sequence's tiles [j0, j0 + n) for the rows of row tile rt.
+struct Segment {
+  int b, rt, j0, n;
+  bool whole;
+  int slot;                      // where a part leaves its sums
+  Seq s;
+};
+struct Cursor {
+  Work x;
+  bool first;
+  __device__ __forceinline__ bool next(const Step &p, Segment &g) {
+    while (x.unit < x.end) {
+      g.s = seq_of(p, x.b);
+      if (x.off >= units_of(p, g.s)) {
+        ++x.b;
+        x.off = 0;
+        continue;
+      }
+      const int tiles = tiles_of(p, g.s), per = tiles + p.extra;
+      g.b = x.b;
+      g.rt = 0;
+      int at = (int)x.off;
+      if (p.row_tiles > 1) {
+        g.rt = (int)(x.off / per);
+        at = (int)(x.off % per);
+      }
+      const int n = (int)min((long long)(per - at), x.end - x.unit);
+      x.unit += n;
+      x.off += n;
+      g.j0 = max(at - p.extra, 0);
+      g.n = max(at + n - p.extra, 0) - g.j0;
+      if (g.n == 0) continue;
+      g.whole = g.n == tiles;
+      // a part that does not begin its CTA's work ends it
+      g.slot = 2 * blockIdx.x + (first ? 0 : 1);
+      first = false;
+      return true;
+    }
+    return false;
+  }
+  // What the kernel that joins the parts has to know (one thread).
+  __device__ __forceinline__ static void note(const Step &p, const Segment &g) {
+    int2 *d = p.plan + (size_t)g.b * p.row_tiles + g.rt;
+    if (g.whole) *d = make_int2(-1, -1);
+    else if (g.j0 == 0) d->x = g.slot;
+    else if (g.j0 + g.n == tiles_of(p, g.s)) d->y = blockIdx.x;
+  }
+};
 
 // The absorbed form's counterpart of forward_row: row r of sequence b, which sees n
 // tokens.  One warp.

@@ -17,8 +17,8 @@ namespace latent {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSub = 32;          // tokens in shared memory at once
-constexpr int kLdW = kSub + 4;
+constexpr int kTokens = 32;          // tokens in shared memory at once
+constexpr int kLdW = kTokens + 4;
 
 // CUDA cores, fp32.  The 32 rows of queries and 32 tokens lie in shared memory;
 // a warp makes the scores of its 4 rows and their sums over the latents.
@@ -26,32 +26,25 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
   extern __shared__ __align__(16) float sm[];
   __shared__ long long tmp[36];
-  __shared__ int ok[kSub];
+  __shared__ int place[kTokens];
   const int D = p.C + p.R, ld = D + 4;
-  float *sq = sm, *sc = sq + kRows * ld, *sw = sc + kSub * ld;
+  float *sq = sm, *sc = sq + kRows * ld, *sw = sc + kTokens * ld;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
-  Work x = find_work(p, tmp);
+  Cursor cur = {find_work(p, tmp), true};
   const float scale = p.scale * kLog2e;
-  bool first = true;
-  while (x.unit < x.end) {
-    const Seq s = seq_of(p, x.b);
-    const int tiles = tiles_of(s);
-    if (x.off >= (long long)tiles * p.row_tiles) {
-      ++x.b;
-      x.off = 0;
-      continue;
-    }
-    const int rt = (int)(x.off / tiles), j0 = (int)(x.off % tiles);
-    const int n = (int)min((long long)(tiles - j0), x.end - x.unit);
-    const bool whole = n == tiles;
-    const int r0 = rt * kRows, rows = p.T * p.H;
+  Segment g{};
+  while (cur.next(p, g)) {
+    const Seq &s = g.s;
+    const bool whole = g.whole;
+    const int r0 = g.rt * kRows, rows = p.T * p.H;
+    if (tid == 0) Cursor::note(p, g);
     __syncthreads();
     for (int i = tid; i < kRows * D; i += kThreads) {
       const int r = r0 + i / D, c = i % D;
       float v = 0.f;
       if (r < rows)
-        v = to_f32(c < p.C ? at<T>(p.q, p.q_s, x.b, r / p.H, r % p.H)[c]
-                           : at<T>(p.qr, p.qr_s, x.b, r / p.H, r % p.H)[c - p.C]);
+        v = to_f32(c < p.C ? at<T>(p.q, p.q_s, g.b, r / p.H, r % p.H)[c]
+                           : at<T>(p.qr, p.qr_s, g.b, r / p.H, r % p.H)[c - p.C]);
       sq[i / D * ld + c] = v;
     }
     int lim[2];
@@ -66,18 +59,22 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][q][0] = acc[i][q][1] = 0;
-    const int stop = min(s.held, (j0 + n) * kTile);
-    for (int k0 = j0 * kTile; k0 < stop; k0 += kSub) {
+    const int stop = min(s.held, (g.j0 + g.n) * p.tile);
+    for (int k0 = g.j0 * p.tile; k0 < stop; k0 += kTokens) {
       __syncthreads();
-      for (int i = warp; i < kSub; i += kThreads / 32) {   // a warp a token
-        const int k = k0 + i;
-        int pg = -1;
-        if (k < s.held) pg = p.table[(size_t)x.b * p.max_pages + k / p.page];
-        const bool there = pg >= 0 && pg < p.n_pages;
-        const T *c = static_cast<const T *>(p.cache) + (there ? pg * p.page_stride : 0) +
-                     (there ? (long long)(k % p.page) * p.token_stride : 0);
+      if (tid < kTokens) {      // -1: not there
+        const int k = k0 + tid;
+        const int pg = k < s.held ? p.table[(size_t)g.b * p.max_pages + k / p.page] : -1;
+        place[tid] = pg >= 0 && pg < p.n_pages ? pg : -1;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = warp; i < kTokens; i += kThreads / 32) {   // a warp a token
+        const bool there = place[i] >= 0;
+        const T *c = static_cast<const T *>(p.cache) + (there ? place[i] * p.page_stride : 0) +
+                     (there ? (long long)((k0 + i) % p.page) * p.token_stride : 0);
+#pragma unroll 5
         for (int e = lane; e < D; e += 32) sc[i * ld + e] = there ? to_f32(c[e]) : 0.f;
-        if (lane == 0) ok[i] = there;
       }
       __syncthreads();
       u64 a2[2][2] = {{0, 0}, {0, 0}};
@@ -107,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
           float lo, hi;
           upk2(a2[i][j], lo, hi);
           const int k = tx + 16 * j;
-          v[j] = k0 + k < lim[i] && ok[k] ? (lo + hi) * scale : -INFINITY;
+          v[j] = k0 + k < lim[i] && place[k] >= 0 ? (lo + hi) * scale : -INFINITY;
           top = fmaxf(top, v[j]);
         }
 #pragma unroll
@@ -140,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
       }
       const float *w = sw + 4 * warp * kLdW, *y = sc + 4 * lane;
 #pragma unroll 2
-      for (int k = 0; k < kSub; ++k) {
+      for (int k = 0; k < kTokens; ++k) {
         u64 ww[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -160,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
       }
       __syncwarp();
     }
-    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+    const int slot = g.slot;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int rr = 4 * warp + i, r = r0 + rr;
@@ -169,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
       if (r >= rows) continue;
       bool bad = false;
       const int t = r / p.H, h = r % p.H;
-      T *o = static_cast<T *>(p.o) + (((size_t)x.b * p.T + t) * p.H + h) * p.C;
+      T *o = static_cast<T *>(p.o) + (((size_t)g.b * p.T + t) * p.H + h) * p.C;
       float *part = p.parts + ((size_t)slot * kRows + rr) * p.C;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -194,18 +191,15 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
           p.stats[2 * ((size_t)slot * kRows + rr)] = mi;
           p.stats[2 * ((size_t)slot * kRows + rr) + 1] = li;
         } else if (p.lse) {
-          p.lse[((size_t)x.b * p.H + h) * p.T + t] =
+          p.lse[((size_t)g.b * p.H + h) * p.T + t] =
               li == 0.f ? -INFINITY : (mi + log2f(li)) * kLn2;
         }
       }
       if (whole && p.T > 1 && __any_sync(0xffffffffu, bad)) {
         __syncwarp();
-        step_row<T>(p, x.b, r, seen(p, s, r), lane);
+        step_row<T>(p, g.b, r, seen(p, s, r), lane);
       }
     }
-    first = false;
-    x.unit += n;
-    x.off += n;
   }
 }
 
@@ -226,11 +220,10 @@ __global__ void __launch_bounds__(512) join_kernel(Step p, int block_rows) {
   const int b = (int)(index / (unsigned)rows), r = (int)(index % (unsigned)rows);
   const int t = r / p.H, h = r % p.H;
   const Seq s = seq_of(p, b);
-  const long long total = p.plan[p.B], before = p.plan[b];
-  const int tiles = tiles_of(s);
+  const int2 range = p.plan[(size_t)b * p.row_tiles + r / kRows];
   T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.C;
   float *lse = p.lse ? p.lse + ((size_t)b * p.H + h) * p.T + t : nullptr;
-  if (tiles == 0) {
+  if (s.held == 0) {
     if (group == 0) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[4 * col + e] = from_f32<T>(0.f);
@@ -238,12 +231,9 @@ __global__ void __launch_bounds__(512) join_kernel(Step p, int block_rows) {
     }
     return;
   }
-  const long long u0 = before + (long long)(r / kRows) * tiles;
-  const int g0 = part_of(total, u0), g1 = part_of(total, u0 + tiles - 1);
-  if (g0 == g1) return;
-  // only the first part can begin before the row's first tile
-  const bool late = part_begin(total, g0) < u0;
-  auto slot = [&](int g) { return (size_t)(2 * g + (g == g0 && late ? 1 : 0)) * kRows + r % kRows; };
+  if (range.x < 0) return;
+  const int first = range.x, g0 = first >> 1, g1 = range.y;
+  auto slot = [&](int g) { return (size_t)(g == g0 ? first : 2 * g) * kRows + r % kRows; };
   const float2 *stats = reinterpret_cast<const float2 *>(p.stats);
   float m = -INFINITY;
   for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, stats[slot(g)].x);
@@ -302,7 +292,7 @@ __global__ void __launch_bounds__(512) join_kernel(Step p, int block_rows) {
 
 template <typename T>
 cudaError_t launch_simt(const Step &p, cudaStream_t cs) {
-  const size_t smem = sizeof(float) * ((size_t)(kRows + kSub) * (p.C + p.R + 4) + kRows * kLdW);
+  const size_t smem = sizeof(float) * ((size_t)(kRows + kTokens) * (p.C + p.R + 4) + kRows * kLdW);
   cudaError_t e = cudaFuncSetAttribute(step_simt_kernel<T>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -340,7 +330,7 @@ kda_status check(const kda_latent_cache *s) {
 }
 
 size_t plan_bytes(const kda_latent_cache *s) {
-  return align_up(sizeof(long long) * ((size_t)s->B + 1), 256);
+  return align_up(sizeof(int2) * (size_t)s->B * (((size_t)s->T * s->H + kRows - 1) / kRows), 256);
 }
 
 }  // namespace
@@ -393,13 +383,16 @@ kda_status kda_latent_step(const kda_latent_cache *s, const void *q, const void 
   p.o = o; p.lse = lse;
   char *ws = static_cast<char *>(workspace);
   p.status = &reinterpret_cast<WsHeader *>(ws)->status;
-  p.plan = reinterpret_cast<long long *>(ws + sizeof(WsHeader));
+  p.plan = reinterpret_cast<int2 *>(ws + sizeof(WsHeader));
   p.parts = reinterpret_cast<float *>(ws + sizeof(WsHeader) + plan_bytes(s));
   p.stats = p.parts + (size_t)2 * kParts * kRows * s->C;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool can = bf16 && step_tc_ok(p);
   if (impl == KDA_IMPL_TC && !can) return KDA_ERR_UNSUPPORTED;
-  cudaError_t e = can && impl != KDA_IMPL_SIMT ? launch_step_tc(p, cs)
+  const bool tc = can && impl != KDA_IMPL_SIMT;
+  p.tile = tc ? 128 : kTokens;
+  p.extra = 3;
+  cudaError_t e = tc ? launch_step_tc(p, cs)
                   : bf16 ? launch_simt<__nv_bfloat16>(p, cs)
                          : launch_simt<float>(p, cs);
   if (e != cudaSuccess) return KDA_ERR_CUDA;

@@ -11,18 +11,20 @@
 // ring; a slot is free when O^T's block has read it, so the next tile comes in
 // while this one is worked on.
 //
-// Threads: warps 0 to 3 the softmax, a thread a token (the running maxima of the 32
-// rows are the same in all of them, and only move when a score exceeds them by
-// 2^8, so the sums in tensor memory are hardly ever scaled); warp 4 the copies; warp
-// 5 the products.
+// Threads: warps 0 to 7 the softmax, two threads a token with 16 rows each (the running
+// maxima of the rows are the same in all of them, and only move when a score exceeds
+// them by 2^8, so the sums in tensor memory are hardly ever scaled); warp 8 the copies;
+// warp 9 the products.
 #include "kda_latent_tc.cuh"
 
 namespace kda {
 namespace latent {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kSoftmax = 128;            // threads
+constexpr int kTile = 128;               // tokens
+constexpr int kThreads = 320;
+constexpr int kSoftmax = 256;            // threads
+constexpr int kMine = kRows / 2;         // rows of a softmax thread
 constexpr uint32_t kChunkB = kTile * kRowBytes;        // 16 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kRing = 11;                // chunks in shared memory
@@ -45,50 +47,17 @@ struct Control {
   uint64_t s_full[2], q_ready, p_ready, o_done, drain;
   uint32_t tmem;
   int fail;
-  unsigned bad[4];
+  unsigned bad[8];
   float top[4][kRows], sum[4][kRows], val[kRows];
   int lim[kRows];
   long long tmp[36];
 };
 
-// A sequence's tiles [j0, j0 + n) for the rows of row tile rt.
-struct Segment {
-  int b, rt, j0, n;
-  bool whole, first;
-  Seq s;
-};
-struct Cursor {
-  Work x;
-  bool first;
-  __device__ __forceinline__ bool next(const Step &p, Segment &g) {
-    while (x.unit < x.end) {
-      g.s = seq_of(p, x.b);
-      const int tiles = tiles_of(g.s);
-      if (x.off >= (long long)tiles * p.row_tiles) {
-        ++x.b;
-        x.off = 0;
-        continue;
-      }
-      g.b = x.b;
-      g.rt = (int)(x.off / tiles);
-      g.j0 = (int)(x.off % tiles);
-      g.n = (int)min((long long)(tiles - g.j0), x.end - x.unit);
-      g.whole = g.n == tiles;
-      g.first = first;
-      first = false;
-      x.unit += g.n;
-      x.off += g.n;
-      return true;
-    }
-    return false;
-  }
-};
-
-// 32 values a lane, reduced over the warp: lane l gets column l's.
+// 16 values a lane, reduced over the warp: lanes l and l + 16 get column l's.
 template <bool kMax>
-__device__ __forceinline__ float columns(float (&v)[kRows], int lane) {
+__device__ __forceinline__ float columns(float (&v)[kMine], int lane) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int o = kMine / 2; o; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -97,11 +66,16 @@ __device__ __forceinline__ float columns(float (&v)[kRows], int lane) {
       v[i] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  return v[0];
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
 __device__ __forceinline__ void softmax_barrier() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+// Of the threads that have the same rows.
+__device__ __forceinline__ void half_barrier(int half) {
+  asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -132,7 +106,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
     c.fail = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 5) tc::tmem_alloc(tc::smem_u32(&c.tmem), kTmemCols);
+  if (warp == 9) tc::tmem_alloc(tc::smem_u32(&c.tmem), kTmemCols);
   Cursor cur = {find_work(p, c.tmp), true};     // (its barriers cover the above)
   tc::tc_fence_before();
   __syncthreads();
@@ -141,21 +115,27 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
   const uint32_t tmem = c.tmem, t_o = tmem + 2 * kRows;
   const bool rope = p.R > 0;
   volatile int *fail = &c.fail;
-  Segment g;
+  Segment g{};
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---- copies: lane k has the tile's k-th box of tokens ----
     const int boxes = kTile / ring.box;
     const int log_page = __ffs(p.page) - 1;
     Slot pr = {0, 0}, rr = {0, 0};
     int np = 0, nr = 0;                    // copied, up to the slots there are
     bool ok = true;
+    auto page_of = [&](int t) {            // -1: not there
+      int pg = -1;
+      if (lane < boxes && t < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + (t >> log_page)];
+      return pg >= 0 && pg < p.n_pages ? pg : -1;
+    };
+    int next = -1;
     while (ok && cur.next(p, g)) {
       for (int i = 0; ok && i < g.n; ++i) {
         const int t0 = (g.j0 + i) * kTile + lane * ring.box;
-        int pg = -1;
-        if (lane < boxes && t0 < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + (t0 >> log_page)];
-        const bool there = pg >= 0 && pg < p.n_pages;
+        if (i == 0) next = page_of(t0);
+        const int pg = next;
+        const bool there = pg >= 0;
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, there)) *
                                (uint32_t)ring.box * kRowBytes;
         const int in_page = t0 & (p.page - 1);
@@ -173,7 +153,13 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           }
           pr.next(ring.pairs);
           np = min(np + 1, ring.pairs);
-          if (k > 0 || !rope) continue;
+          if (k > 0) continue;
+          // the next tile comes into L2 while the slots that it will take are in use
+          next = i + 1 < g.n ? page_of(t0 + kTile) : -1;
+          if (next >= 0)
+            for (int x = 0; x < p.C + p.R; x += kChunkCols)
+              tma_prefetch_3d(&map, x, (t0 + kTile) & (p.page - 1), next);
+          if (!rope) continue;
           ok = __all_sync(0xffffffffu, wait_or_fail(bar(c.rempty[rr.at]), rr.lap ^ 1u, fail));
           if (!ok) break;
           const uint32_t rfull = bar(c.rfull[rr.at]);
@@ -200,7 +186,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
       drain(c.full, pr, ring.pairs, np);
       drain(c.rfull, rr, ring.ropes, nr);
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---- products: one thread ----
     if (elect_one()) {
       constexpr uint32_t id_s = tc::idesc_bf16(kTile, kRows, 0, 0),
@@ -220,28 +206,40 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         ok = wait_or_fail(bar(c.q_ready), ns & 1, fail);
         ++ns;
         tc::tc_fence_after();
+        // S of the next tile begins (its first pair and its rope chunk) while the
+        // softmax works on this one, and goes on when O^T has made room for the rest
+        Slot in = pr;
+        auto begin = [&](uint32_t t) {
+          const uint32_t t_s = tmem + (t & 1) * kRows;
+          if (!wait_or_fail(bar(c.full[in.at]), in.lap, fail)) return false;
+          const uint32_t a = s_ring + (uint32_t)in.at * kPairB;
+          chunk(t_s, a, dq0, 0u);
+          chunk(t_s, a + kChunkB, dq0 + kQChunkB / 16, 1u);
+          in.next(ring.pairs);
+          if (!rope) return true;
+          if (!wait_or_fail(bar(c.rfull[rr.at]), rr.lap, fail)) return false;
+          chunk(t_s, s_rope + (uint32_t)rr.at * kChunkB,
+                dq0 + (uint64_t)(2 * ring.npair) * (kQChunkB / 16), 1u);
+          tc::mma_commit(bar(c.rempty[rr.at]));
+          rr.next(ring.ropes);
+          return true;
+        };
+        ok = ok && begin(nt);
         for (int i = 0; ok && i < g.n; ++i, ++nt) {
           const uint32_t t_s = tmem + (nt & 1) * kRows;
-          Slot in = pr;
-          for (int k = 0; k < ring.npair; ++k) {
+          for (int k = 1; k < ring.npair; ++k) {
             ok = wait_or_fail(bar(c.full[in.at]), in.lap, fail);
             if (!ok) break;
             const uint32_t a = s_ring + (uint32_t)in.at * kPairB;
             const uint64_t dq = dq0 + (uint64_t)(2 * k) * (kQChunkB / 16);
-            chunk(t_s, a, dq, k > 0 ? 1u : 0u);
+            chunk(t_s, a, dq, 1u);
             chunk(t_s, a + kChunkB, dq + kQChunkB / 16, 1u);
             in.next(ring.pairs);
-            if (k > 0 || !rope) continue;
-            ok = wait_or_fail(bar(c.rfull[rr.at]), rr.lap, fail);
-            if (!ok) break;
-            chunk(t_s, s_rope + (uint32_t)rr.at * kChunkB,
-                  dq0 + (uint64_t)(2 * ring.npair) * (kQChunkB / 16), 1u);
-            tc::mma_commit(bar(c.rempty[rr.at]));
-            rr.next(ring.ropes);
           }
           if (!ok) break;
           tc::mma_commit(bar(c.s_full[nt & 1]));
-          ok = wait_or_fail(bar(c.p_ready), nt & 1, fail);
+          if (i + 1 < g.n) ok = begin(nt + 1);
+          ok = ok && wait_or_fail(bar(c.p_ready), nt & 1, fail);
           if (!ok) break;
           tc::tc_fence_after();
           const uint32_t old = i > 0 ? 1u : 0u;
@@ -264,76 +262,86 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
     }
     __syncwarp();
   } else {
-    // ---- softmax: thread tid has token tid of a tile ----
+    // ---- softmax: token tid & 127 of a tile, rows 16 half .. ----
+    const int half = warp >> 2, token = tid & 127, quad = warp & 3;
     const float scale = p.scale * kLog2e;
-    const int rows = p.T * p.H;
-    const uint32_t my_lane = (uint32_t)warp << 21;       // 32 lanes a warp
-    const int log_page = __ffs(p.page) - 1;
+    const int rows = p.T * p.H, log_page = __ffs(p.page) - 1;
+    const uint32_t lanes = (uint32_t)quad << 21, col0 = (uint32_t)(kMine * half);
     Slot pr = {0, 0};
     uint32_t nt = 0;
     while (cur.next(p, g)) {
       const int r0 = g.rt * kRows;
+      if (tid == 0) Cursor::note(p, g);
       // the queries, 8 channels a thread at a time, all on their way at once
-      const int pieces = (p.C + (rope ? kChunkCols : 0)) / 8;
-      for (int rr = warp; rr < kRows; rr += 4) {
-        const int r = r0 + rr, t = r / p.H, h = r % p.H;
+      {
+        const int r = r0 + lane, t = r / p.H, h = r - t * p.H;
         const bool live = r < rows;
-        const __nv_bfloat16 *q = live ? at<__nv_bfloat16>(p.q, p.q_s, g.b, t, h) : nullptr;
-        const __nv_bfloat16 *qr =
-            live && rope ? at<__nv_bfloat16>(p.qr, p.qr_s, g.b, t, h) : nullptr;
-        const bool wide = ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(qr)) & 15) == 0;
-        for (int i = lane; i < pieces; i += 32) {
-          const int ch = i * 8;
-          const __nv_bfloat16 *x = ch < p.C ? q + ch : qr + (ch - p.C);
-          const uint32_t off = (s_q - s_ring) + (uint32_t)(ch / kChunkCols) * kQChunkB +
-                               piece_off(rr, (ch % kChunkCols) / 8);
-          if (live && ch < p.C + p.R && wide) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s_ring + off), "l"(x)
-                         : "memory");
-            continue;
-          }
-          uint32_t w[4] = {0, 0, 0, 0};
-          if (live && ch < p.C + p.R) {
-            const unsigned short *u = reinterpret_cast<const unsigned short *>(x);
+        const unsigned long long q = live ? (unsigned long long)at<__nv_bfloat16>(p.q, p.q_s, g.b, t, h) : 0;
+        const unsigned long long qr =
+            live && rope ? (unsigned long long)at<__nv_bfloat16>(p.qr, p.qr_s, g.b, t, h) : 0;
+        if (warp == 0) c.lim[lane] = live ? seen(p, g.s, r) : 0;
+        const bool wide = __all_sync(0xffffffffu, ((q | qr) & 15) == 0);
+        const int pieces = (p.C + (rope ? kChunkCols : 0)) / 8, held = (p.C + p.R) / 8;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = u[2 * e] | (uint32_t)u[2 * e + 1] << 16;
+        for (int k = 0; k < kRows / 8; ++k) {
+          const int rr = warp + 8 * k;
+          const unsigned long long q1 = __shfl_sync(0xffffffffu, q, rr),
+                                   r1 = __shfl_sync(0xffffffffu, qr, rr);
+          const uint32_t dst = s_q + (uint32_t)rr * kRowBytes;
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const int i = lane + 32 * e;
+            if (i >= pieces) break;
+            const unsigned long long x = (i < p.C / 8 ? q1 + 16ull * i : r1 + 16ull * (i - p.C / 8));
+            const uint32_t d = dst + (uint32_t)(i >> 3) * kQChunkB + (((i & 7) ^ (rr & 7)) << 4);
+            if (q1 == 0 || i >= held) {
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d), "r"(0) : "memory");
+            } else if (wide) {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(x) : "memory");
+            } else {
+              const unsigned short *u = reinterpret_cast<const unsigned short *>(x);
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) w[y] = u[2 * y] | (uint32_t)u[2 * y + 1] << 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
           }
-          *reinterpret_cast<uint4 *>(smem + off) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (tid < kRows) c.lim[tid] = r0 + tid < rows ? seen(p, g.s, r0 + tid) : 0;
       tc::fence_proxy_async();
       tc::mbar_arrive(bar(c.q_ready));
       softmax_barrier();
-      float nb[kRows], l[kRows];
+      float nb[kMine], l[kMine];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) nb[r] = 0.f, l[r] = 0.f;
-      float mine = -INFINITY;             // the maximum that row `lane` is scaled by
+      for (int r = 0; r < kMine; ++r) nb[r] = 0.f, l[r] = 0.f;
+      float mine = -INFINITY;       // the maximum that row col0 + (lane & 15) is scaled by
       for (int i = 0; i < g.n; ++i, ++nt) {
-        const int k = (g.j0 + i) * kTile + tid;
+        const int k = (g.j0 + i) * kTile + token;
         int pg = -1;
         if (k < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + (k >> log_page)];
         const bool there = pg >= 0 && pg < p.n_pages;
         wait_or_fail(bar(c.s_full[nt & 1]), (nt >> 1) & 1, fail);
         __syncwarp();
         tc::tc_fence_after();
-        uint32_t u[32];
-        tmem_ld32_wait(tmem + (nt & 1) * kRows + my_lane, u);
-        float v[kRows], w[kRows];
+        float v[kMine], w[kMine];
+        tc::tmem_ld16(tmem + (nt & 1) * kRows + col0 + lanes, v);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) v[r] = there ? __uint_as_float(u[r]) * scale : -INFINITY;
+        for (int r = 0; r < kMine; ++r) v[r] = there ? v[r] * scale : -INFINITY;
         if (p.T > 1) {
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) v[r] = k < c.lim[r] ? v[r] : -INFINITY;
+          for (int r = 0; r < kMine; ++r) v[r] = k < c.lim[col0 + r] ? v[r] : -INFINITY;
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) w[r] = v[r];
+        for (int r = 0; r < kMine; ++r) w[r] = v[r];
         const float top1 = columns<true>(w, lane);
-        c.top[warp][lane] = top1;
-        softmax_barrier();
-        const float top = fmaxf(fmaxf(c.top[0][lane], c.top[1][lane]),
-                                fmaxf(c.top[2][lane], c.top[3][lane]));
+        c.top[quad][col0 + (lane & 15)] = top1;
+        half_barrier(half);
+        const int mc = (int)col0 + (lane & 15);
+        const float top = fmaxf(fmaxf(c.top[0][mc], c.top[1][mc]),
+                                fmaxf(c.top[2][mc], c.top[3][mc]));
         const bool over = top > mine + kSlack;
         // O^T of the tile before has read P, and its sums stand still
         if (i > 0) wait_or_fail(bar(c.o_done), (nt - 1) & 1, fail);
@@ -343,9 +351,9 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           const float f = now == mine ? 1.f : exp2f(mine - now);
           mine = now;
           const float base = now == -INFINITY ? 0.f : now;
-          float fr[kRows];
+          float fr[kMine];
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
+          for (int r = 0; r < kMine; ++r) {
             fr[r] = __shfl_sync(0xffffffffu, f, r);
             nb[r] = __shfl_sync(0xffffffffu, base, r);
             l[r] *= fr[r];
@@ -353,40 +361,39 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           if (i > 0) {
             tc::tc_fence_after();
             for (int m = 0; m < ring.npair; ++m) {
-              uint32_t x[32];
-              tmem_ld32_wait(t_o + (uint32_t)m * kRows + my_lane, x);
+              float x[kMine];
+              uint32_t y[kMine];
+              const uint32_t t = t_o + (uint32_t)m * kRows + col0 + lanes;
+              tc::tmem_ld16(t, x);
 #pragma unroll
-              for (int r = 0; r < kRows; ++r)
-                x[r] = __float_as_uint(__uint_as_float(x[r]) * fr[r]);
-              tmem_st32(t_o + (uint32_t)m * kRows + my_lane, x);
+              for (int r = 0; r < kMine; ++r) y[r] = __float_as_uint(x[r] * fr[r]);
+              tmem_st16(t, y);
             }
             tmem_wait_st();
             tc::tc_fence_before();
           }
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < kMine; ++r) {
           v[r] = tc::ex2(v[r] - nb[r]);
           l[r] += v[r];
         }
 #pragma unroll
-        for (int e = 0; e < kRows / 8; ++e) {
+        for (int e = 0; e < kMine / 8; ++e) {
           const float x[8] = {v[8 * e],     v[8 * e + 1], v[8 * e + 2], v[8 * e + 3],
                               v[8 * e + 4], v[8 * e + 5], v[8 * e + 6], v[8 * e + 7]};
-          tc::st_bf16x8(smem, (s_p - s_ring) + tc::mn_off(8 * e, tid, kTile), x);
+          tc::st_bf16x8(smem, (s_p - s_ring) + tc::mn_off((int)col0 + 8 * e, token, kTile), x);
         }
         // a token that is not there has a weight of 0: what lies in its place must
-        // not be NaN
+        // not be NaN (a chunk of each pair by either thread)
         if (!there) {
           const uint4 zero = make_uint4(0, 0, 0, 0);
           Slot in = pr;
           for (int m = 0; m < ring.npair; ++m) {
             wait_or_fail(bar(c.full[in.at]), in.lap, fail);
-            unsigned char *d = smem + (uint32_t)in.at * kPairB + (uint32_t)tid * kRowBytes;
-            for (int e = 0; e < 8; ++e) {
-              *reinterpret_cast<uint4 *>(d + 16 * e) = zero;
-              *reinterpret_cast<uint4 *>(d + kChunkB + 16 * e) = zero;
-            }
+            unsigned char *d = smem + (uint32_t)in.at * kPairB + (uint32_t)half * kChunkB +
+                               (uint32_t)token * kRowBytes;
+            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(d + 16 * e) = zero;
             in.next(ring.pairs);
           }
         }
@@ -395,47 +402,47 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         tc::tc_fence_before();
         tc::mbar_arrive(bar(c.p_ready));
       }
-      // ---- the segment's end: O^T lane tid of block m is latent 128 m + tid ----
+      // ---- the segment's end: O^T lane `token` of block m is latent 128 m + token ----
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) nb[r] = l[r];
+      for (int r = 0; r < kMine; ++r) nb[r] = l[r];
       const float part_l = columns<false>(nb, lane);
-      c.sum[warp][lane] = part_l;
-      softmax_barrier();
-      const float total = c.sum[0][lane] + c.sum[1][lane] + c.sum[2][lane] + c.sum[3][lane];
-      const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
-      if (warp == 0) {
-        const int r = r0 + lane;
+      const int mc = (int)col0 + (lane & 15);
+      c.sum[quad][mc] = part_l;
+      half_barrier(half);
+      const float total = c.sum[0][mc] + c.sum[1][mc] + c.sum[2][mc] + c.sum[3][mc];
+      if (quad == 0 && lane < 16) {
+        const int r = r0 + mc;
         if (!g.whole) {
-          p.stats[2 * ((size_t)slot * kRows + lane)] = mine;
-          p.stats[2 * ((size_t)slot * kRows + lane) + 1] = total;
+          reinterpret_cast<float2 *>(p.stats)[(size_t)g.slot * kRows + mc] = make_float2(mine, total);
         } else if (p.lse && r < rows) {
           p.lse[((size_t)g.b * p.H + r % p.H) * p.T + r / p.H] =
               total == 0.f ? -INFINITY : (mine + log2f(total)) * kLn2;
         }
-        c.val[lane] = g.whole ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
+        c.val[mc] = g.whole ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
       }
       wait_or_fail(bar(c.o_done), (nt - 1) & 1, fail);
-      softmax_barrier();
+      half_barrier(half);
       tc::tc_fence_after();
       unsigned bad = 0;
       for (int m = 0; m < ring.npair; ++m) {
-        uint32_t x[32];
-        tmem_ld32_wait(t_o + (uint32_t)m * kRows + my_lane, x);
-        const int ch = m * 128 + tid;
+        float x[kMine];
+        tc::tmem_ld16(t_o + (uint32_t)m * kRows + col0 + lanes, x);
+        const int ch = m * 128 + token;
         if (g.whole) {
-          __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)g.b * rows + r0) * p.C + ch;
+          __nv_bfloat16 *o =
+              static_cast<__nv_bfloat16 *>(p.o) + ((size_t)g.b * rows + r0 + col0) * p.C + ch;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            if (r0 + r >= rows) break;
-            const float f = c.val[r];
-            const float y = f == 0.f ? 0.f : __uint_as_float(x[r]) * f;
+          for (int r = 0; r < kMine; ++r) {
+            if (r0 + (int)col0 + r >= rows) break;
+            const float f = c.val[col0 + r];
+            const float y = f == 0.f ? 0.f : x[r] * f;
             if (!finite(y)) bad |= 1u << r;
             o[(size_t)r * p.C] = __float2bfloat16_rn(y);
           }
         } else {
-          float *d = p.parts + (size_t)slot * kRows * p.C + ch;
+          float *d = p.parts + ((size_t)g.slot * kRows + col0) * p.C + ch;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) d[(size_t)r * p.C] = __uint_as_float(x[r]);
+          for (int r = 0; r < kMine; ++r) d[(size_t)r * p.C] = x[r];
         }
       }
       tc::tc_fence_before();
@@ -443,8 +450,9 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         bad = __reduce_or_sync(0xffffffffu, bad);
         if (lane == 0) c.bad[warp] = bad;
         softmax_barrier();
-        bad = c.bad[0] | c.bad[1] | c.bad[2] | c.bad[3];
-        for (int r = warp; r < kRows; r += 4)
+        bad = c.bad[0] | c.bad[1] | c.bad[2] | c.bad[3] |
+              (c.bad[4] | c.bad[5] | c.bad[6] | c.bad[7]) << kMine;
+        for (int r = warp; r < kRows; r += 8)
           if (bad >> r & 1) step_row<__nv_bfloat16>(p, g.b, r0 + r, c.lim[r], lane);
       }
       softmax_barrier();      // c.lim, c.val and c.sum are written again
@@ -454,7 +462,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
   __syncthreads();
   tc::tc_fence_after();
   if (tid == 0 && c.fail) set_status(p.status, KDA_DEVICE_TIMEOUT);
-  if (warp == 5) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == 9) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
