@@ -1098,26 +1098,30 @@ def _latent_ref(*fields):
 
 
 def _strided(t, name, shape, dtype, device):
-    """Address and strides of a tensor whose last dimension is contiguous; the
-    stride of a dimension of 1 means nothing and is given as 0."""
+    """Address and strides of a tensor whose last dimension is contiguous (the
+    library does not read the stride of a dimension of 1)."""
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == device):
         _refuse(t, name, shape, dtype, device, False)
     st = t.stride()
     if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr(), tuple([s if n > 1 else 0 for s, n in zip(st[:-1], shape)])
+    return t.data_ptr(), st[:-1]
 
 
-def _moved(f, x, stream, args, kw):
-    """The call made on ``stream`` or on the tensors' device where either is not
-    the current one; None where both are."""
-    if stream is not None and _elsewhere(stream):
-        with torch.cuda.stream(stream):
-            return (f(*args, **kw),)
-    if x.is_cuda and x.get_device() != torch.cuda.current_device():
-        with torch.cuda.device(x.get_device()):
-            return (f(*args, **kw),)
-    return None
+_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+
+
+def _away(x, stream):
+    """Whether a call has to be made under another stream or device."""
+    return stream is not None and _elsewhere(stream) or \
+        x.is_cuda and x.get_device() != _device_now()
+
+
+def _moved(f, x, stream, *args, **kw):
+    """The call made on ``stream`` or on the tensors' device."""
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.get_device()):
+        return f(*args, **kw)
 
 
 _NONE3, _NONE2 = (0, 0, 0), (0, 0)
@@ -1128,7 +1132,7 @@ def _scratch_here(workspace, need, device, where):
     ws, n = _scratch(workspace, need, device, where, 256)
     if ws.get_device() != device:
         raise ValueError(f"workspace is on {ws.device}, expected cuda:{device}")
-    return ws, n
+    return ws.data_ptr(), n
 
 
 def rotate(x, inv_freq, *, positions=None, pairs=True, inverse=False, out=None, stream=None):
@@ -1140,10 +1144,9 @@ def rotate(x, inv_freq, *, positions=None, pairs=True, inverse=False, out=None, 
     other strides); inv_freq: [dim/2] fp32; positions: [B,T] int32 (None: 0 ..
     T-1).  ``pairs``: (x[2i], x[2i+1]), else (x[i], x[i+dim/2]).  ``out`` may be x
     itself; returns it, or a new contiguous tensor."""
-    moved = _moved(rotate, x, stream, (x, inv_freq), dict(positions=positions, pairs=pairs,
-                                                          inverse=inverse, out=out))
-    if moved:
-        return moved[0]
+    if _away(x, stream):
+        return _moved(rotate, x, stream, x, inv_freq, positions=positions, pairs=pairs,
+                      inverse=inverse, out=out)
     dev, ty = _start(x, "rotate")
     if x.dim() not in (3, 4) or x.numel() == 0:
         raise ValueError(f"x must be [B,T,H,dim] or [B,T,dim] and not empty, got {tuple(x.shape)}")
@@ -1196,10 +1199,9 @@ def latent_append(latent, k_rope, cache, page_table, lengths, *, inv_freq=None, 
     there (None: all).  inv_freq [R/2] fp32 and ``pairs`` as :func:`rotate` (None:
     keys are copied).  No page that is written may belong to two sequences.
     Returns the rotated queries [B,T,H,R] (``q_out``, contiguous), or None."""
-    moved = _moved(latent_append, latent, stream, (latent, k_rope, cache, page_table, lengths),
-                   dict(inv_freq=inv_freq, new=new, q_rope=q_rope, pairs=pairs, q_out=q_out))
-    if moved:
-        return moved[0]
+    if _away(latent, stream):
+        return _moved(latent_append, latent, stream, latent, k_rope, cache, page_table, lengths,
+                      inv_freq=inv_freq, new=new, q_rope=q_rope, pairs=pairs, q_out=q_out)
     dev, ty = _start(latent, "latent_append")
     if latent.dim() != 3:
         raise ValueError(f"latent must be [B,T,C], got {tuple(latent.shape)}")
@@ -1257,11 +1259,9 @@ def latent_step(q, q_rope, cache, page_table, lengths, *, scale, new=None, retur
     bf16), "auto" takes "tc" where it serves the layout.  Returns o [B,T,H,C], the
     weighted latents, 0 for a token that is not there, and with ``return_lse`` the
     log sum of exp of the scores [B,H,T] fp32."""
-    moved = _moved(latent_step, q, stream, (q, q_rope, cache, page_table, lengths),
-                   dict(scale=scale, new=new, return_lse=return_lse, out=out,
-                        workspace=workspace, impl=impl))
-    if moved:
-        return moved[0]
+    if _away(q, stream):
+        return _moved(latent_step, q, stream, q, q_rope, cache, page_table, lengths, scale=scale,
+                      new=new, return_lse=return_lse, out=out, workspace=workspace, impl=impl)
     dev, ty = _start(q, "latent_step")
     if q.dim() != 4:
         raise ValueError(f"q must be [B,T,H,C], got {tuple(q.shape)}")
@@ -1283,7 +1283,7 @@ def latent_step(q, q_rope, cache, page_table, lengths, *, scale, new=None, retur
     st = L.kda_latent_step(
         d, qp, rp, cp, tp, _at(lengths, "lengths", (B,), _i32, dev),
         _at(new, "new", (B,), _i32, dev), scale, _at(o, "out", (B, T, H, C), ty, dev),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        None if lse is None else lse.data_ptr(), ws, n, IMPLS[impl],
         _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_step")
@@ -1338,11 +1338,10 @@ def latent_fwd(q, k, v, *, q_rope=None, k_rope=None, scale=None, segment_ids=Non
     (bf16; the softmax's weights are rounded to bf16), "auto" takes "tc" where it
     serves the layout.  Returns o [B,T,H,V], and with ``save_lse`` also what
     :func:`latent_bwd` reads, the log sum of exp of the scores [B,H,T] fp32."""
-    moved = _moved(latent_fwd, q, stream, (q, k, v),
-                   dict(q_rope=q_rope, k_rope=k_rope, scale=scale, segment_ids=segment_ids,
-                        save_lse=save_lse, out=out, workspace=workspace, impl=impl))
-    if moved:
-        return moved[0]
+    if _away(q, stream):
+        return _moved(latent_fwd, q, stream, q, k, v, q_rope=q_rope, k_rope=k_rope, scale=scale,
+                      segment_ids=segment_ids, save_lse=save_lse, out=out, workspace=workspace,
+                      impl=impl)
     dev, ty, (B, T, H, K, R, V), d, ptrs = _latent_inputs(q, k, v, q_rope, k_rope, "latent_fwd")
     o = q.new_empty((B, T, H, V)) if out is None else out
     lse = torch.empty((B, H, T), dtype=_f32, device=q.device) if save_lse else None
@@ -1352,7 +1351,7 @@ def latent_fwd(q, k, v, *, q_rope=None, k_rope=None, scale=None, segment_ids=Non
     st = L.kda_latent_fwd(
         d, *ptrs, (K + R) ** -0.5 if scale is None else scale,
         _at(segment_ids, "segment_ids", (B, T), _i32, dev), _at(o, "out", (B, T, H, V), ty, dev),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        None if lse is None else lse.data_ptr(), ws, n, IMPLS[impl],
         _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_fwd")
@@ -1365,11 +1364,9 @@ def latent_bwd(q, k, v, o, lse, d_o, *, q_rope=None, k_rope=None, scale=None, se
     ``d_o`` [B,T,H,V] of o: ``(dq, dk, dv, dq_rope, dk_rope)``, contiguous, of the
     inputs' dtype (the last two None without a rope part; dk_rope [B,T,R] is the
     sum over the heads).  Repeated calls agree bit for bit."""
-    moved = _moved(latent_bwd, q, stream, (q, k, v, o, lse, d_o),
-                   dict(q_rope=q_rope, k_rope=k_rope, scale=scale, segment_ids=segment_ids,
-                        workspace=workspace, impl=impl))
-    if moved:
-        return moved[0]
+    if _away(q, stream):
+        return _moved(latent_bwd, q, stream, q, k, v, o, lse, d_o, q_rope=q_rope, k_rope=k_rope,
+                      scale=scale, segment_ids=segment_ids, workspace=workspace, impl=impl)
     dev, ty, (B, T, H, K, R, V), d, ptrs = _latent_inputs(q, k, v, q_rope, k_rope, "latent_bwd")
     dq, dk, dv = (q.new_empty((B, T, H, n)) for n in (K, K, V))
     dqr = dkr = None
@@ -1383,7 +1380,7 @@ def latent_bwd(q, k, v, o, lse, d_o, *, q_rope=None, k_rope=None, scale=None, se
         _at(segment_ids, "segment_ids", (B, T), _i32, dev), _at(o, "o", (B, T, H, V), ty, dev),
         _at(lse, "lse", (B, H, T), _f32, dev), _at(d_o, "d_o", (B, T, H, V), ty, dev),
         dq.data_ptr(), None if dqr is None else dqr.data_ptr(), dk.data_ptr(),
-        None if dkr is None else dkr.data_ptr(), dv.data_ptr(), ws.data_ptr(), n, IMPLS[impl],
+        None if dkr is None else dkr.data_ptr(), dv.data_ptr(), ws, n, IMPLS[impl],
         _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_bwd")

@@ -21,16 +21,35 @@ constexpr int kThreads = 256;
 constexpr int kBlk = 64;          // rows of a tile, either side
 constexpr int kLdP = kBlk + 4;    // of a tile of weights
 
-// Rows t0 .. t0 + 63 of [x | xr] (n and nr values) as fp32, zeros from row `lim` on.
+__device__ __forceinline__ float4 four(const float *x) {
+  return *reinterpret_cast<const float4 *>(x);
+}
+__device__ __forceinline__ float4 four(const __nv_bfloat16 *x) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(x);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Rows t0 .. t0 + 63 of [x | xr] (n and nr values) as fp32, zeros from row `lim` on: 16
+// threads a row, 4 values each where these can be read at once.
 template <typename T>
 __device__ __forceinline__ void load_rows(float *dst, int ld, const T *x, long long st, int n,
-                                          const T *xr, long long str, int nr, int t0, int lim) {
-  const int w = n + nr;
-  for (int i = threadIdx.x; i < kBlk * w; i += kThreads) {
-    const int r = i / w, c = i % w;
-    float v = 0.f;
-    if (t0 + r < lim) v = to_f32(c < n ? x[(t0 + r) * st + c] : xr[(t0 + r) * str + c - n]);
-    dst[r * ld + c] = v;
+                                          const T *xr, long long str, int nr, int t0, int lim,
+                                          int fours) {
+  const int w = n + nr, r0 = threadIdx.x >> 4, c0 = 4 * (threadIdx.x & 15);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 16 * i, t = t0 + r;
+    const T *a = x + t * st, *b = xr + t * str - n;
+    for (int c = c0; c < w; c += 64) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < lim) {
+        const T *y = (c < n ? a : b) + c;
+        v = fours ? four(y) : make_float4(to_f32(y[0]), to_f32(y[1]), to_f32(y[2]), to_f32(y[3]));
+      }
+      *reinterpret_cast<float4 *>(dst + r * ld + c) = v;
+    }
   }
 }
 
@@ -129,7 +148,7 @@ __device__ __forceinline__ Where where(const Prompt &p, bool last_first) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
   float *sq = sm, *sk = sq + kBlk * ldq, *sv = sk + kBlk * ldq, *sp = sv + kBlk * ldv;
@@ -137,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
   const Where at0 = where(p, true);
   const int b = at0.b, h = at0.h, t0 = at0.t0;
   load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
-               p.qr_s.t, p.R, t0, p.T);
+               p.qr_s.t, p.R, t0, p.T, p.fours);
   int lo[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -152,9 +171,8 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
   for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
     __syncthreads();
     load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
-                 p.kr_s.t, p.R, j0, p.T);
-    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0,
-                 p.T);
+                 p.kr_s.t, p.R, j0, p.T, p.fours);
+    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0, p.T, p.fours);
     __syncthreads();
     float s[4][4];
     rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
@@ -232,9 +250,8 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
   const Where at0 = where(p, false);
   const int b = at0.b, h = at0.h, t0 = at0.t0;
   load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
-               p.kr_s.t, p.R, t0, p.T);
-  load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, t0,
-               p.T);
+               p.kr_s.t, p.R, t0, p.T, p.fours);
+  load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, t0, p.T, p.fours);
   int end[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -247,9 +264,9 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
   for (int i0 = t0; i0 < last; i0 += kBlk) {
     __syncthreads();
     load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
-                 p.qr_s.t, p.R, i0, p.T);
+                 p.qr_s.t, p.R, i0, p.T, p.fours);
     load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
-                 (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, i0, p.T);
+                 (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, i0, p.T, 1);
     if (tid < kBlk && i0 + tid < p.T) {
       const size_t r = ((size_t)b * p.H + h) * p.T + i0 + tid;
       s_lse[tid] = p.lse[r] * kLog2e;
@@ -306,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(Prompt p) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
   float *sq = sm, *su = sq + kBlk * ldq, *sk = su + kBlk * ldv, *sv = sk + kBlk * ldq,
@@ -315,9 +332,9 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
   const Where at0 = where(p, true);
   const int b = at0.b, h = at0.h, t0 = at0.t0;
   load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
-               p.qr_s.t, p.R, t0, p.T);
+               p.qr_s.t, p.R, t0, p.T, p.fours);
   load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
-               (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, t0, p.T);
+               (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, t0, p.T, 1);
   int lo[4];
   float lse[4], delta[4];
 #pragma unroll
@@ -335,9 +352,8 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
   for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
     __syncthreads();
     load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
-                 p.kr_s.t, p.R, j0, p.T);
-    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0,
-                 p.T);
+                 p.kr_s.t, p.R, j0, p.T, p.fours);
+    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0, p.T, p.fours);
     __syncthreads();
     float s[4][4], dp[4][4];
     rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
@@ -382,78 +398,83 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
 }
 
 // ---- runs -------------------------------------------------------------------
-// Where each token's run begins and ends, one CTA a row: a running maximum of
-// the starts from the left, a running minimum of the ends from the right, 8
-// tokens a thread at a time.
-constexpr int kRunThreads = 1024, kRunTokens = 8;
+// Where each token's run begins and ends, one CTA a row.  A warp takes 8 rows of 32
+// tokens; a vote shows where a row's runs begin and end, so the latest beginning and the
+// next end are bit searches.
+constexpr int kRunThreads = 1024, kRunRows = 8, kRunChunk = kRunThreads * kRunRows;
 
-template <bool kMax>
-__device__ __forceinline__ int scan(int x, int *tmp) {   // inclusive, in thread order
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The starts and / or the ends of tokens t0 .. t0 + 8191; carry_start is the start that
+// holds before them, carry_end the end that holds behind them.
+template <bool kStart, bool kEnd>
+__device__ __forceinline__ void run_chunk(const int *ids, int T, int *start, int *end, int t0,
+                                          int &carry_start, int &carry_end) {
+  __shared__ int s_top[kRunThreads / 32], s_low[kRunThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = t0 + warp * 32 * kRunRows;
+  int id[kRunRows];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x = kMax ? max(x, y) : min(x, y);
+  for (int i = 0; i < kRunRows; ++i) {
+    const int t = w0 + 32 * i + lane;
+    id[i] = t < T ? ids[t] : 0;
+  }
+  const int prev = w0 > 0 && w0 <= T ? ids[w0 - 1] : 0;      // around the warp's tokens
+  const int next = w0 + 32 * kRunRows < T ? ids[w0 + 32 * kRunRows] : 0;
+  unsigned begins[kRunRows], ends[kRunRows];
+  int top = 0, low = T;
+#pragma unroll
+  for (int i = 0; i < kRunRows; ++i) {
+    const int t = w0 + 32 * i + lane;
+    int before = __shfl_up_sync(0xffffffffu, id[i], 1);
+    int behind = __shfl_down_sync(0xffffffffu, id[i], 1);
+    const int left = i ? __shfl_sync(0xffffffffu, id[i ? i - 1 : 0], 31) : prev;
+    const int right = i + 1 < kRunRows ? __shfl_sync(0xffffffffu, id[i + 1 < kRunRows ? i + 1 : 0], 0) : next;
+    if (lane == 0) before = left;
+    if (lane == 31) behind = right;
+    begins[i] = __ballot_sync(0xffffffffu, t < T && id[i] != before);
+    ends[i] = __ballot_sync(0xffffffffu, t < T && id[i] != behind);
+    if (begins[i]) top = w0 + 32 * i + 31 - __clz(begins[i]);
+    if (ends[i] && low == T) low = w0 + 32 * i + __ffs(ends[i]);
+  }
+  if (lane == 0) {
+    s_top[warp] = top;
+    s_low[warp] = low;
   }
   __syncthreads();
-  if (lane == 31) tmp[warp] = x;
+  int from = max(carry_start, __reduce_max_sync(0xffffffffu, lane < warp ? s_top[lane] : 0));
+  int to = min(carry_end, __reduce_min_sync(0xffffffffu, lane > warp ? s_low[lane] : T));
+#pragma unroll
+  for (int i = 0; i < kRunRows; ++i) {
+    const int t = w0 + 32 * i + lane;
+    const unsigned m = begins[i] & (0xffffffffu >> (31 - lane));
+    if (kStart && t < T)
+      start[t] = id[i] == 0 ? t + 1 : m ? w0 + 32 * i + 31 - __clz(m) : from;
+    if (begins[i]) from = w0 + 32 * i + 31 - __clz(begins[i]);
+  }
+#pragma unroll
+  for (int i = kRunRows - 1; i >= 0; --i) {
+    const int t = w0 + 32 * i + lane;
+    const unsigned m = ends[i] & (0xffffffffu << lane);
+    if (kEnd && t < T) end[t] = id[i] == 0 ? t : m ? w0 + 32 * i + __ffs(m) : to;
+    if (ends[i]) to = w0 + 32 * i + __ffs(ends[i]);
+  }
+  carry_start = max(carry_start, __reduce_max_sync(0xffffffffu, s_top[lane]));
+  carry_end = min(carry_end, __reduce_min_sync(0xffffffffu, s_low[lane]));
   __syncthreads();
-  for (int w = 0; w < warp; ++w) x = kMax ? max(x, tmp[w]) : min(x, tmp[w]);
-  return x;
 }
 
 __global__ void __launch_bounds__(kRunThreads) runs_kernel(const int *ids, int T, int *start,
                                                            int *end) {
-  __shared__ int tmp[kRunThreads / 32], edge[kRunThreads];
+  start_next();
   const size_t row = (size_t)blockIdx.x * T;
-  ids += row;
-  start += row;
-  end += row;
-  const int per = kRunThreads * kRunTokens, tid = threadIdx.x;
-  int carry = 0;
-  for (int t0 = 0; t0 < T; t0 += per) {
-    const int a = t0 + tid * kRunTokens;
-    int v[kRunTokens], id[kRunTokens];
-    int prev = a > 0 && a <= T ? ids[a - 1] : 0, top = 0;
-#pragma unroll
-    for (int i = 0; i < kRunTokens; ++i) {
-      id[i] = a + i < T ? ids[a + i] : 0;
-      if (a + i < T && id[i] != prev) top = a + i;
-      prev = id[i];
-      v[i] = top;
-    }
-    const int sum = scan<true>(top, tmp);
-    edge[tid] = sum;
-    __syncthreads();
-    const int in = max(carry, tid ? edge[tid - 1] : 0);
-    carry = max(carry, edge[kRunThreads - 1]);
-#pragma unroll
-    for (int i = 0; i < kRunTokens; ++i)
-      if (a + i < T) start[a + i] = id[i] ? max(in, v[i]) : a + i + 1;
-    __syncthreads();
+  int a = 0, z = T;
+  if (T <= kRunChunk) {
+    run_chunk<true, true>(ids + row, T, start + row, end + row, 0, a, z);
+    return;
   }
-  carry = T;
-  for (int t0 = (T - 1) / per * per; t0 >= 0; t0 -= per) {
-    const int z = t0 + (kRunThreads - 1 - tid) * kRunTokens;   // from the right
-    int v[kRunTokens], id[kRunTokens];
-    int next = z + kRunTokens < T ? ids[z + kRunTokens] : 0, low = T;
-#pragma unroll
-    for (int i = kRunTokens - 1; i >= 0; --i) {
-      id[i] = z + i < T ? ids[z + i] : 0;
-      if (z + i < T && (z + i == T - 1 || id[i] != next)) low = z + i + 1;
-      next = id[i];
-      v[i] = low;
-    }
-    const int sum = scan<false>(low, tmp);
-    edge[tid] = sum;
-    __syncthreads();
-    const int in = min(carry, tid ? edge[tid - 1] : T);
-    carry = min(carry, edge[kRunThreads - 1]);
-#pragma unroll
-    for (int i = 0; i < kRunTokens; ++i)
-      if (z + i < T) end[z + i] = id[i] ? min(in, v[i]) : z + i;
-    __syncthreads();
-  }
+  for (int t0 = 0; t0 < T; t0 += kRunChunk)
+    run_chunk<true, false>(ids + row, T, start + row, end + row, t0, a, z);
+  a = 0, z = T;
+  for (int t0 = (T - 1) / kRunChunk * kRunChunk; t0 >= 0; t0 -= kRunChunk)
+    run_chunk<false, true>(ids + row, T, start + row, end + row, t0, a, z);
 }
 
 // ---- around the backward ----------------------------------------------------
@@ -573,15 +594,24 @@ Prompt make(const kda_latent_shape *s, const void *q, const void *q_rope, const 
   memset(&p, 0, sizeof(p));
   p.B = s->B; p.T = s->T; p.H = s->H; p.K = s->K; p.R = s->R; p.V = s->V;
   p.q = q; p.qr = q_rope; p.k = k; p.kr = k_rope; p.v = v;
-  p.q_s = {s->q_stride_b, s->q_stride_t, s->q_stride_h};
-  p.k_s = {s->k_stride_b, s->k_stride_t, s->k_stride_h};
-  p.v_s = {s->v_stride_b, s->v_stride_t, s->v_stride_h};
+  auto of = [&](long long b, long long t, long long h) {
+    return strides_of(s->B, s->T, s->H, b, t, h);
+  };
+  p.q_s = of(s->q_stride_b, s->q_stride_t, s->q_stride_h);
+  p.k_s = of(s->k_stride_b, s->k_stride_t, s->k_stride_h);
+  p.v_s = of(s->v_stride_b, s->v_stride_t, s->v_stride_h);
   if (s->R) {
-    p.qr_s = {s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h};
-    p.kr_s = {s->k_rope_stride_b, s->k_rope_stride_t, 0};
+    p.qr_s = of(s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h);
+    p.kr_s = of(s->k_rope_stride_b, s->k_rope_stride_t, 0);
   }
   p.scale = scale;
   p.status = &static_cast<WsHeader *>(workspace)->status;
+  const uintptr_t bytes = s->dtype == KDA_DTYPE_BF16 ? 8 : 16;
+  p.fours = 1;
+  for (const void *x : {q, q_rope, k, k_rope, v})
+    if (reinterpret_cast<uintptr_t>(x) % bytes) p.fours = 0;
+  for (const Strides &x : {p.q_s, p.qr_s, p.k_s, p.kr_s, p.v_s})
+    if ((x.b | x.t | x.h) & 3) p.fours = 0;
   return p;
 }
 

@@ -20,6 +20,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct Strides {
   long long b, t, h;
 };
+// The stride of a dimension of 1 is not the caller's to say.
+inline Strides strides_of(int B, int T, int H, long long b, long long t, long long h) {
+  return {B > 1 ? b : 0, T > 1 ? t : 0, H > 1 ? h : 0};
+}
 
 // ---- the expanded form ------------------------------------------------------
 struct Prompt {
@@ -27,6 +31,7 @@ struct Prompt {
   const void *q, *qr, *k, *kr, *v;
   Strides q_s, qr_s, k_s, kr_s, v_s;     // (kr_s.h is 0)
   float scale;
+  int fours;                             // 4 values of a row can be read at once
   // of each token: the first token of its run, and one past the run's last.
   // Padding has start = t + 1, end = t.  NULL: one run a row.  Both rise along
   // a row.

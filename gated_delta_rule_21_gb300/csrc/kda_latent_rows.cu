@@ -5,9 +5,10 @@
 // heads, so a CTA takes a few tokens, makes their cos and sin once in shared
 // memory and then goes over the heads with 16-byte accesses.
 //
-// The angle t * f is reduced in integers: f / 2 pi modulo 1 as a fraction of
-// 2^64, times t modulo 2^64, is the turn exactly but for the 53 bits of
-// f / 2 pi; what is left goes to sincospi in fp32.
+// The angle t * f is reduced in integers: f / 2 pi modulo 1 in units of 2^-64, times t
+// modulo 2^64, is the fraction of a turn (off by t units at most); what is left goes
+// to sincospi in fp32.  (The card's 64-bit floating point is too slow for this: a
+// prompt's angles took 5 of 18 us in it.)
 #include <string.h>
 
 #include "kda_latent.cuh"
@@ -18,7 +19,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;   // of a vector (dim <= 256)
-constexpr double kInv2Pi = 0.15915494309189533577;
 
 struct RotateParams {
   int B, T, H, dim;
@@ -38,13 +38,28 @@ struct RotateParams {
   long long page_stride, token_stride;
 };
 
-__device__ __forceinline__ float2 turn(float f, int t, bool inverse) {
+// The fraction of a turn that f is worth, in 2^-64: f / 2 pi modulo 1.  f is m 2^(e - 150)
+// with 24 bits of m; 1 / 2 pi stands in 126 bits, and the bits of the product from
+// 2^-64 up to 2^-1 are cut out.
+__device__ __forceinline__ unsigned long long fraction(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const int e = (int)(u >> 23 & 255u);
+  const unsigned long long m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+  // floor(2^128 / 2 pi)
+  constexpr unsigned long long hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+  const unsigned long long p0 = m * lo, p1 = __umul64hi(m, lo), q0 = m * hi, q1 = __umul64hi(m, hi);
+  const unsigned long long w0 = p0, w1 = p1 + q0, w2 = q1 + (w1 < p1 ? 1ull : 0ull);
+  const int s = 214 - (e ? e : 1);          // the bit of the product that is worth 2^-64
+  if (s < 0 || s >= 192) return 0;
+  const int k = s & 63;
+  const unsigned long long a = s < 64 ? w0 : s < 128 ? w1 : w2;
+  const unsigned long long b = s < 64 ? w1 : s < 128 ? w2 : 0ull;
+  const unsigned long long r = k ? a >> k | b << (64 - k) : a;
+  return u >> 31 ? 0ull - r : r;
+}
+
+__device__ __forceinline__ float2 turn(unsigned long long unit, float f, int t, bool inverse) {
   if (!finite(f)) return make_float2(f - f, f - f);
-  const double r = (double)f * kInv2Pi;
-  const double frac = r - floor(r);                        // [0, 1)
-  const unsigned long long unit =                          // of 2^64, in two halves
-      ((unsigned long long)(frac * 4294967296.0) << 32) |
-      (unsigned long long)((frac * 4294967296.0 - floor(frac * 4294967296.0)) * 4294967296.0);
   const long long part = (long long)(unit * (unsigned long long)(long long)t);
   float s, c;
   sincospif((float)part * 0x1p-63f, &s, &c);               // half turns in [-1, 1]
@@ -57,111 +72,142 @@ struct alignas(kWide ? sizeof(T) * N : sizeof(T)) Vec {
   T v[N];
 };
 
-// P pairs from pair i of a vector, rotated (cs NULL: copied).
-template <typename T, int P>
-__device__ __forceinline__ void rotate_pairs(const T *x, T *y, int i, int dim, int pairs,
-                                             const float2 *cs) {
-  float a[P], b[P];
-  using Pairs = Vec<T, 2 * P, (P > 1)>;
-  using Half = Vec<T, P, (P > 1)>;
-  if (pairs) {
-    const Pairs v = *reinterpret_cast<const Pairs *>(x + 2 * i);
-    Pairs w;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      a[j] = to_f32(v.v[2 * j]);
-      b[j] = to_f32(v.v[2 * j + 1]);
-      const float2 z = cs ? cs[i + j] : make_float2(1.f, 0.f);
-      w.v[2 * j] = cs ? from_f32<T>(a[j] * z.x - b[j] * z.y) : v.v[2 * j];
-      w.v[2 * j + 1] = cs ? from_f32<T>(b[j] * z.x + a[j] * z.y) : v.v[2 * j + 1];
+// P pairs of a vector: 2 P values side by side, or P of each half.
+template <typename T, int P, bool kPairs>
+struct Some {
+  using Piece = Vec<T, kPairs ? 2 * P : P, (P > 1)>;
+  Piece u, v;
+  __device__ __forceinline__ void load(const T *x, int i, int half) {
+    if (kPairs) {
+      u = *reinterpret_cast<const Piece *>(x + 2 * i);
+    } else {
+      u = *reinterpret_cast<const Piece *>(x + i);
+      v = *reinterpret_cast<const Piece *>(x + i + half);
     }
-    *reinterpret_cast<Pairs *>(y + 2 * i) = w;
-  } else {
-    const Half u = *reinterpret_cast<const Half *>(x + i);
-    const Half v = *reinterpret_cast<const Half *>(x + i + dim / 2);
-    Half lo, hi;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      a[j] = to_f32(u.v[j]);
-      b[j] = to_f32(v.v[j]);
-      const float2 z = cs ? cs[i + j] : make_float2(1.f, 0.f);
-      lo.v[j] = cs ? from_f32<T>(a[j] * z.x - b[j] * z.y) : u.v[j];
-      hi.v[j] = cs ? from_f32<T>(b[j] * z.x + a[j] * z.y) : v.v[j];
-    }
-    *reinterpret_cast<Half *>(y + i) = lo;
-    *reinterpret_cast<Half *>(y + i + dim / 2) = hi;
   }
-}
+  __device__ __forceinline__ void turn(const float2 *cs) {
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      T &x = kPairs ? u.v[2 * j] : u.v[j], &y = kPairs ? u.v[2 * j + 1] : v.v[j];
+      const float a = to_f32(x), b = to_f32(y);
+      x = from_f32<T>(a * cs[j].x - b * cs[j].y);
+      y = from_f32<T>(b * cs[j].x + a * cs[j].y);
+    }
+  }
+  __device__ __forceinline__ void store(T *y, int i, int half) const {
+    if (kPairs) {
+      *reinterpret_cast<Piece *>(y + 2 * i) = u;
+    } else {
+      *reinterpret_cast<Piece *>(y + i) = u;
+      *reinterpret_cast<Piece *>(y + i + half) = v;
+    }
+  }
+};
 
-// P: pairs a thread takes at once (1: any alignment).  kAppend: the tokens'
-// keys and latents go to the cache as well.
-template <typename T, int P, bool kAppend>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(RotateParams p) {
+struct Token {
+  long long x, y, kr, lat;   // element offsets of its rows
+  long long place;           // in the cache; -1: nowhere
+  int at;                    // position; append: -1: not there
+};
+
+// P: pairs a thread takes at once (1: any alignment).  kAppend: the tokens' keys and
+// latents go to the cache as well.  A thread keeps its pairs and goes over the
+// (token, head) rows, four on their way at a time.
+template <typename T, int P, bool kPairs, bool kAppend>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
   extern __shared__ float2 cs[];               // [tokens][dim / 2]
-  __shared__ int pos[kThreads];
-  __shared__ long long place[kThreads];        // of a token in the cache, -1: nowhere
+  __shared__ Token tok[kThreads];
   const int tid = threadIdx.x, half = p.dim / 2;
   const long long all = (long long)p.B * p.T, first = (long long)blockIdx.x * p.tokens;
   const int n = (int)(all - first < p.tokens ? all - first : p.tokens);
   if (tid < n) {
     const int b = (int)((first + tid) / p.T), t = (int)((first + tid) % p.T);
-    int at = t;
+    Token k;
+    k.x = b * p.x_s.b + t * p.x_s.t;
+    k.y = b * p.y_s.b + t * p.y_s.t;
+    k.at = t;
     if (kAppend) {
+      k.kr = b * p.kr_s.b + t * p.kr_s.t;
+      k.lat = b * p.lat_s.b + t * p.lat_s.t;
+      k.place = k.at = -1;
       const int f = p.fresh ? p.fresh[b] : p.T;
       const int fresh = f < 0 ? 0 : f > p.T ? p.T : f;
       const long long q = (long long)p.lengths[b] - fresh + t;
-      long long where = -1;
-      at = -1;
       if (t < fresh && q >= 0) {
-        at = (int)q;
+        k.at = (int)q;
         if (q / p.page < p.max_pages) {
           const int pg = p.table[(size_t)b * p.max_pages + q / p.page];
           if (pg >= 0 && pg < p.n_pages)
-            where = pg * p.page_stride + (q % p.page) * p.token_stride;
+            k.place = pg * p.page_stride + (q % p.page) * p.token_stride;
         }
       }
-      place[tid] = where;
     } else if (p.positions) {
-      at = p.positions[first + tid];
+      k.at = p.positions[first + tid];
     }
-    pos[tid] = at;
+    tok[tid] = k;
   }
   __syncthreads();
-  if (p.freq)
-    for (int i = tid; i < n * half; i += kThreads)
-      cs[i] = turn(p.freq[i % half], pos[i / half], p.inverse != 0);
-  __syncthreads();
+  if (p.freq) {
+    for (int i = tid; i < n * half; i += kThreads) {
+      const float f = p.freq[i % half];
+      cs[i] = turn(fraction(f), f, tok[i / half].at, p.inverse != 0);
+    }
+    __syncthreads();
+  }
+  using Part = Some<T, P, kPairs>;
+  const int steps = half / P;
   if (p.x) {
-    const int steps = half / P, row = p.H * steps;
-    for (long long i = tid; i < (long long)n * row; i += kThreads) {
-      const int k = (int)(i / row), r = (int)(i % row), h = r / steps, j = (r % steps) * P;
-      const int b = (int)((first + k) / p.T), t = (int)((first + k) % p.T);
-      const bool turned = p.freq && (!kAppend || pos[k] >= 0);
-      rotate_pairs<T, P>(static_cast<const T *>(p.x) + b * p.x_s.b + t * p.x_s.t + h * p.x_s.h,
-                         static_cast<T *>(p.y) + b * p.y_s.b + t * p.y_s.t + h * p.y_s.h, j,
-                         p.dim, p.pairs, turned ? cs + k * half : nullptr);
+    const int lanes = steps < kThreads ? steps : kThreads, row0 = tid / lanes,
+              step = kThreads / lanes, j = (tid % lanes) * P;
+    constexpr int U = 4;
+    int k[U], h[U];
+    int ck = row0 / p.H, ch = row0 % p.H;
+    const int dk = step / p.H, dh = step % p.H;
+    const T *x = static_cast<const T *>(p.x);
+    T *y = static_cast<T *>(p.y);
+    if (row0 < step) {
+      while (ck < n) {
+        Part part[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          k[u] = ck;
+          h[u] = ch;
+          if (ck < n) part[u].load(x + tok[ck].x + ch * p.x_s.h, j, half);
+          ck += dk;
+          ch += dh;
+          if (ch >= p.H) ch -= p.H, ++ck;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (k[u] >= n) break;
+          const Token &t = tok[k[u]];
+          if (!kAppend || t.at >= 0) part[u].turn(cs + k[u] * half + j);
+          part[u].store(y + t.y + h[u] * p.y_s.h, j, half);
+        }
+      }
     }
   }
   if (kAppend) {
-    const int steps = half / P;
     for (int i = tid; i < n * steps; i += kThreads) {
       const int k = i / steps, j = (i % steps) * P;
-      if (place[k] < 0) continue;
-      const int b = (int)((first + k) / p.T), t = (int)((first + k) % p.T);
-      rotate_pairs<T, P>(static_cast<const T *>(p.kr) + b * p.kr_s.b + t * p.kr_s.t,
-                         static_cast<T *>(p.cache) + place[k] + p.C, j, p.dim, p.pairs,
-                         p.freq ? cs + k * half : nullptr);
+      if (tok[k].place < 0) continue;
+      Part part;
+      part.load(static_cast<const T *>(p.kr) + tok[k].kr, j, half);
+      if (p.freq) part.turn(cs + k * half + j);
+      part.store(static_cast<T *>(p.cache) + tok[k].place + p.C, j, half);
     }
     constexpr int W = P == 1 ? 1 : 16 / (int)sizeof(T);
+    using Piece = Vec<T, W, (P > 1)>;
     const int words = p.C / W;
-    for (int i = tid; i < n * words; i += kThreads) {
-      const int k = i / words, j = (i % words) * W;
-      if (place[k] < 0) continue;
-      const int b = (int)((first + k) / p.T), t = (int)((first + k) % p.T);
-      using Piece = Vec<T, W, (P > 1)>;
-      *reinterpret_cast<Piece *>(static_cast<T *>(p.cache) + place[k] + j) =
-          *reinterpret_cast<const Piece *>(static_cast<const T *>(p.latent) + b * p.lat_s.b +
-                                           t * p.lat_s.t + j);
+    const int lanes = words < kThreads ? words : kThreads, rows = kThreads / lanes;
+    if (tid < rows * lanes) {
+      for (int k = tid / lanes; k < n; k += rows) {
+        if (tok[k].place < 0) continue;
+        const T *x = static_cast<const T *>(p.latent) + tok[k].lat;
+        T *y = static_cast<T *>(p.cache) + tok[k].place;
+        for (int i = tid % lanes; i < words; i += lanes)
+          *reinterpret_cast<Piece *>(y + i * W) = *reinterpret_cast<const Piece *>(x + i * W);
+      }
     }
   }
 }
@@ -183,9 +229,11 @@ cudaError_t launch(RotateParams p, bool wide, cudaStream_t cs) {
   const long long grid = (all + tokens - 1) / tokens;
   const size_t smem = sizeof(float2) * (size_t)tokens * half;
   constexpr int P = 8 / (int)sizeof(T);        // pairs in 16 bytes
-  if (wide && p.pairs) rotate_kernel<T, P, kAppend><<<(unsigned)grid, kThreads, smem, cs>>>(p);
-  else if (wide) rotate_kernel<T, 2 * P, kAppend><<<(unsigned)grid, kThreads, smem, cs>>>(p);
-  else rotate_kernel<T, 1, kAppend><<<(unsigned)grid, kThreads, smem, cs>>>(p);
+  const unsigned g = (unsigned)grid;
+  if (wide && p.pairs) rotate_kernel<T, P, true, kAppend><<<g, kThreads, smem, cs>>>(p);
+  else if (wide) rotate_kernel<T, 2 * P, false, kAppend><<<g, kThreads, smem, cs>>>(p);
+  else if (p.pairs) rotate_kernel<T, 1, true, kAppend><<<g, kThreads, smem, cs>>>(p);
+  else rotate_kernel<T, 1, false, kAppend><<<g, kThreads, smem, cs>>>(p);
   return cudaGetLastError();
 }
 
@@ -220,8 +268,8 @@ kda_status kda_rotate(const kda_rotate_desc *d, const void *x, const int32_t *po
   memset(&p, 0, sizeof(p));
   p.B = d->B; p.T = d->T; p.H = d->H; p.dim = d->dim;
   p.pairs = d->pairs; p.inverse = d->inverse;
-  p.x_s = {d->x_stride_b, d->x_stride_t, d->x_stride_h};
-  p.y_s = {d->y_stride_b, d->y_stride_t, d->y_stride_h};
+  p.x_s = strides_of(d->B, d->T, d->H, d->x_stride_b, d->x_stride_t, d->x_stride_h);
+  p.y_s = strides_of(d->B, d->T, d->H, d->y_stride_b, d->y_stride_t, d->y_stride_h);
   p.x = x; p.positions = positions; p.freq = inv_freq; p.y = y;
   const bool wide = wide_ok(x, p.x_s, es) && wide_ok(y, p.y_s, es) &&
                     d->dim % ((d->pairs ? 16 : 32) / es) == 0;
@@ -255,16 +303,17 @@ kda_status kda_latent_append(const kda_latent_cache *s, const void *latent, cons
   RotateParams p;
   memset(&p, 0, sizeof(p));
   p.B = s->B; p.T = s->T; p.H = s->H; p.dim = s->R; p.pairs = pairs;
-  p.x_s = {s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h};
+  p.x_s = strides_of(s->B, s->T, s->H, s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h);
   p.y_s = {(long long)s->T * s->H * s->R, (long long)s->H * s->R, s->R};
   p.x = q_rope; p.freq = inv_freq; p.y = q_out;
   p.latent = latent; p.kr = k_rope; p.cache = cache;
-  p.lat_s = {s->latent_stride_b, s->latent_stride_t, 0};
-  p.kr_s = {s->k_rope_stride_b, s->k_rope_stride_t, 0};
+  p.lat_s = strides_of(s->B, s->T, 1, s->latent_stride_b, s->latent_stride_t, 0);
+  p.kr_s = strides_of(s->B, s->T, 1, s->k_rope_stride_b, s->k_rope_stride_t, 0);
   p.table = page_table; p.lengths = lengths; p.fresh = new_tokens;
   p.C = s->C; p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page = s->page_size;
-  p.page_stride = s->page_stride; p.token_stride = s->token_stride;
-  const Strides cache_s = {s->page_stride, s->token_stride, s->C};
+  p.page_stride = s->n_pages > 1 ? s->page_stride : 0;
+  p.token_stride = s->page_size > 1 ? s->token_stride : 0;
+  const Strides cache_s = {p.page_stride, p.token_stride, s->C};
   const bool wide = (!q_rope || (wide_ok(q_rope, p.x_s, es) && wide_ok(q_out, p.y_s, es))) &&
                     (!k_rope || wide_ok(k_rope, p.kr_s, es)) && wide_ok(latent, p.lat_s, es) &&
                     wide_ok(cache, cache_s, es) && s->R % ((pairs ? 16 : 32) / es) == 0;

@@ -374,10 +374,13 @@ kda_status kda_latent_step(const kda_latent_cache *s, const void *q, const void 
   p.B = s->B; p.T = s->T; p.H = s->H; p.C = s->C; p.R = s->R;
   p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page = s->page_size;
   p.row_tiles = (int)(((long long)s->T * s->H + kRows - 1) / kRows);
-  p.page_stride = s->page_stride; p.token_stride = s->token_stride;
+  p.page_stride = s->n_pages > 1 ? s->page_stride : 0;
+  p.token_stride = s->page_size > 1 ? s->token_stride : 0;
   p.q = q; p.qr = q_rope; p.cache = cache;
-  p.q_s = {s->q_stride_b, s->q_stride_t, s->q_stride_h};
-  if (q_rope) p.qr_s = {s->q_rope_stride_b, s->q_rope_stride_t, s->q_rope_stride_h};
+  p.q_s = strides_of(s->B, s->T, s->H, s->q_stride_b, s->q_stride_t, s->q_stride_h);
+  if (q_rope)
+    p.qr_s = strides_of(s->B, s->T, s->H, s->q_rope_stride_b, s->q_rope_stride_t,
+                        s->q_rope_stride_h);
   p.table = page_table; p.lengths = lengths; p.fresh = new_tokens;
   p.scale = scale;
   p.o = o; p.lse = lse;

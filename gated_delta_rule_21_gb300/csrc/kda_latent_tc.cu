@@ -32,29 +32,88 @@ struct Maps {
 };
 
 // The launch's 384 threads have 168 registers each (504 of three warpgroups); the two
-// that work on rows take 216, the third keeps 56: 488.
+// that work on rows take 216, the third keeps 72: 504.
 __device__ __forceinline__ void few_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 }
 __device__ __forceinline__ void many_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
 }
 
+// Key tiles [lo, hi) that a query tile sees.
+struct Range {
+  int lo, hi;
+};
+// Two query tiles of one head, and the key tiles that either sees.
+struct Item {
+  int b, h, pair;              // pair < 0: no more
+  Range r[2];
+  int all_lo[2];               // every row of a tile sees the keys from here on
+  int jl, jh;
+  __device__ __forceinline__ bool has(int x) const { return r[x].lo < r[x].hi; }
+  __device__ __forceinline__ bool active(int x, int j) const {
+    return j >= (x ? r[1].lo : r[0].lo) && j < (x ? r[1].hi : r[0].hi);
+  }
+};
+
 struct FwdControl {
-  uint64_t q_full[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
-  uint64_t s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t q_full[2], q_empty[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots],
+      v_empty[kVSlots];
+  uint64_t s_full[2], p_ready[2], o_done[2], o_free[2], drain;
+  uint64_t claim, item_full, item_empty;
+  uint4 claimed;
+  Item item;
   uint32_t tmem;
   int fail;
 };
 
-// Key tiles [lo, hi) that query tile t (of 128 rows) sees.
-struct Range {
-  int lo, hi;
-};
 __device__ __forceinline__ Range keys_of(const Prompt &p, int b, int t) {
   if (t * kRowsQ >= p.T) return {0, 0};
   const int lo = run_start(p, b, t * kRowsQ) / kRowsQ;
   return {lo, lo > t ? lo : t + 1};
+}
+__device__ __forceinline__ Item make_item(const Prompt &p, unsigned index, int pairs) {
+  // a head's keys stay in L2 while its queries are worked on, the longest first
+  const int bh = (int)(index / (unsigned)pairs);
+  Item m;
+  m.pair = pairs - 1 - (int)(index % (unsigned)pairs);
+  m.b = bh / p.H;
+  m.h = bh % p.H;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int t = 2 * m.pair + x;
+    m.r[x] = keys_of(p, m.b, t);
+    m.all_lo[x] = t * kRowsQ < p.T ? run_start(p, m.b, min(p.T, (t + 1) * kRowsQ) - 1) : 0;
+  }
+  const bool a = m.has(0), z = m.has(1);
+  m.jl = a && z ? min(m.r[0].lo, m.r[1].lo) : a ? m.r[0].lo : z ? m.r[1].lo : 0;
+  m.jh = a && z ? max(m.r[0].hi, m.r[1].hi) : a ? m.r[0].hi : z ? m.r[1].hi : 0;
+  return m;
+}
+
+// Asks for a CTA of this launch that has not begun; the answer comes to `dst` (16 bytes).
+__device__ __forceinline__ void claim_next(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// Whether there was one, and its index.
+__device__ __forceinline__ bool claimed(uint32_t src, unsigned &index) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(src)
+      : "memory");
+  index = x;
+  return ok != 0;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -65,150 +124,191 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   const uint32_t s0 = tc::smem_u32(smem);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int pairs = (p.T + 2 * kRowsQ - 1) / (2 * kRowsQ);
-  // a head's keys stay in L2 while its queries are worked on, the longest first
-  const int bh = (int)(blockIdx.x / (unsigned)pairs),
-            pair = pairs - 1 - (int)(blockIdx.x % (unsigned)pairs);
-  const int b = bh / p.H, h = bh % p.H;
   const int nk = (p.K + kChunkCols - 1) / kChunkCols, nc = nk + (p.R > 0 ? 1 : 0);
   const int nv = (p.V + kChunkCols - 1) / kChunkCols;
-  const Range ra = keys_of(p, b, 2 * pair), rb = keys_of(p, b, 2 * pair + 1);
-  const bool has_a = ra.lo < ra.hi, has_b = rb.lo < rb.hi;
-  const int jl = has_a && has_b ? min(ra.lo, rb.lo) : has_a ? ra.lo : has_b ? rb.lo : 0;
-  const int jh = has_a && has_b ? max(ra.hi, rb.hi) : has_a ? ra.hi : has_b ? rb.hi : 0;
-  auto active = [&](int x, int j) {
-    return x ? j >= rb.lo && j < rb.hi : j >= ra.lo && j < ra.hi;
-  };
   auto bar = [](uint64_t &x) { return tc::smem_u32(&x); };
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(c.q_full[i]), 1);
+      tc::mbar_init(bar(c.q_empty[i]), 1);
       tc::mbar_init(bar(c.v_full[i]), 1);
       tc::mbar_init(bar(c.v_empty[i]), 1);
       tc::mbar_init(bar(c.s_full[i]), 1);
       tc::mbar_init(bar(c.p_ready[i]), 128);
       tc::mbar_init(bar(c.o_done[i]), 1);
+      tc::mbar_init(bar(c.o_free[i]), 128);
     }
     for (int i = 0; i < kKSlots; ++i) {
       tc::mbar_init(bar(c.k_full[i]), 1);
       tc::mbar_init(bar(c.k_empty[i]), 1);
     }
     tc::mbar_init(bar(c.drain), 1);
+    tc::mbar_init(bar(c.claim), 1);
+    tc::mbar_init(bar(c.item_full), 1);
+    tc::mbar_init(bar(c.item_empty), 256 + 2);
     c.fail = 0;
     tc::fence_mbar_init();
   }
   if (warp == 9) tc::tmem_alloc(tc::smem_u32(&c.tmem), 512);
+  after_previous();        // the table of runs
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = c.tmem;
   volatile int *fail = &c.fail;
+  // the next item, by every thread that works on them
+  auto next_item = [&](Item &m, uint32_t round) {
+    const bool ok = wait_or_fail(bar(c.item_full), round & 1, fail);
+    m = c.item;
+    if (!ok) m.pair = -1;
+    tc::mbar_arrive(bar(c.item_empty));
+    return m.pair >= 0;
+  };
 
   if (warp >= 8) {
     few_registers();
-    if (warp == 8) {
+    if (warp == 10) {
+      // ---- items: this CTA's own, then those of CTAs that have not begun ----
+      if (lane == 0) {
+        bool ok = true;
+        unsigned index = blockIdx.x;
+        for (uint32_t round = 0; ok; ++round) {
+          if (round > 0) {
+            // (asked for once everyone has begun the item before)
+            if (!wait_or_fail(bar(c.item_empty), (round - 1) & 1, fail)) break;
+            tc::mbar_expect_tx(bar(c.claim), 16);
+            claim_next(tc::smem_u32(&c.claimed), bar(c.claim));
+            if (!wait_or_fail(bar(c.claim), (round - 1) & 1, fail)) break;
+            ok = claimed(tc::smem_u32(&c.claimed), index);
+            tc::fence_proxy_async();
+          }
+          if (ok) c.item = make_item(p, index, pairs);
+          else c.item.pair = -1;
+          tc::mbar_arrive(bar(c.item_full));
+        }
+      }
+      __syncwarp();
+    } else if (warp == 8) {
       // ---- copies ----
       if (lane == 0) {
-        int kn = 0, vn = 0;
+        uint32_t kn = 0, vn = 0, qn[2] = {0, 0};
         bool ok = true;
+        Item m{};
         auto load_q = [&](int x) {
-          const int t = (2 * pair + x) * kRowsQ;
-          if (t >= p.T) return;
-          tc::mbar_expect_tx(bar(c.q_full[x]), (uint32_t)nc * kChunkB);
+          ok = wait_or_fail(bar(c.q_empty[x]), (qn[x] + 1) & 1, fail);
+          if (!ok) return;
+          const int t = (2 * m.pair + x) * kRowsQ;
+          const uint32_t full = bar(c.q_full[x]);
+          tc::mbar_expect_tx(full, (uint32_t)nc * kChunkB);
           for (int i = 0; i < nk; ++i)
-            tma_load_4d(s0 + (uint32_t)(3 * x + i) * kChunkB, &maps.q, i * kChunkCols, h, t, b,
-                        bar(c.q_full[x]));
+            tma_load_4d(s0 + (uint32_t)(3 * x + i) * kChunkB, &maps.q, i * kChunkCols, m.h, t, m.b,
+                        full);
           if (nc > nk)
-            tma_load_4d(s0 + (uint32_t)(3 * x + nk) * kChunkB, &maps.qr, 0, h, t, b,
-                        bar(c.q_full[x]));
+            tma_load_4d(s0 + (uint32_t)(3 * x + nk) * kChunkB, &maps.qr, 0, m.h, t, m.b, full);
+          ++qn[x];
         };
         auto load_k = [&](int j) {
-          for (int i = 0; ok && i < nc; ++i, ++kn) {
-            const int s = kn % kKSlots;
-            ok = wait_or_fail(bar(c.k_empty[s]), (uint32_t)(kn / kKSlots + 1) & 1, fail);
+          for (int i = 0; i < nc; ++i, ++kn) {
+            const uint32_t s = kn % kKSlots;
+            ok = wait_or_fail(bar(c.k_empty[s]), (kn / kKSlots + 1) & 1, fail);
             if (!ok) return;
-            tc::mbar_expect_tx(bar(c.k_full[s]), kChunkB);
-            const uint32_t d = s0 + kOffK + (uint32_t)s * kChunkB;
-            if (i < nk)
-              tma_load_4d(d, &maps.k, i * kChunkCols, h, j * kRowsQ, b, bar(c.k_full[s]));
-            else
-              tma_load_4d(d, &maps.kr, 0, 0, j * kRowsQ, b, bar(c.k_full[s]));
+            const uint32_t full = bar(c.k_full[s]), d = s0 + kOffK + s * kChunkB;
+            tc::mbar_expect_tx(full, kChunkB);
+            if (i < nk) tma_load_4d(d, &maps.k, i * kChunkCols, m.h, j * kRowsQ, m.b, full);
+            else tma_load_4d(d, &maps.kr, 0, 0, j * kRowsQ, m.b, full);
           }
         };
-        if (jl < jh) {
-          if (has_a) load_q(0);
-          load_k(jl);
-          if (has_b) load_q(1);
-          for (int j = jl; ok && j < jh; ++j, ++vn) {
-            const int s = vn % kVSlots;
-            ok = wait_or_fail(bar(c.v_empty[s]), (uint32_t)(vn / kVSlots + 1) & 1, fail);
+        for (uint32_t round = 0; ok && next_item(m, round); ++round) {
+          if (m.jl >= m.jh) continue;
+          if (m.has(0)) load_q(0);
+          if (ok) load_k(m.jl);
+          if (ok && m.has(1)) load_q(1);
+          for (int j = m.jl; ok && j < m.jh; ++j) {
+            const uint32_t s = vn % kVSlots;
+            ok = wait_or_fail(bar(c.v_empty[s]), (vn / kVSlots + 1) & 1, fail);
             if (!ok) break;
-            tc::mbar_expect_tx(bar(c.v_full[s]), (uint32_t)nv * kChunkB);
+            const uint32_t full = bar(c.v_full[s]);
+            tc::mbar_expect_tx(full, (uint32_t)nv * kChunkB);
             for (int i = 0; i < nv; ++i)
-              tma_load_4d(s0 + kOffV + (uint32_t)(2 * s + i) * kChunkB, &maps.v, i * kChunkCols, h,
-                          j * kRowsQ, b, bar(c.v_full[s]));
-            if (j + 1 < jh) load_k(j + 1);
+              tma_load_4d(s0 + kOffV + (2 * s + (uint32_t)i) * kChunkB, &maps.v, i * kChunkCols, m.h,
+                          j * kRowsQ, m.b, full);
+            ++vn;
+            if (j + 1 < m.jh) load_k(j + 1);
           }
         }
         if (*fail) {   // what is on its way comes in before the CTA ends
-          if (has_a) tc::mbar_wait(bar(c.q_full[0]), 0);
-          if (has_b) tc::mbar_wait(bar(c.q_full[1]), 0);
-          for (int k = max(0, kn - kKSlots); k < kn; ++k)
-            tc::mbar_wait(bar(c.k_full[k % kKSlots]), (uint32_t)(k / kKSlots) & 1);
-          for (int k = max(0, vn - kVSlots); k < vn; ++k)
-            tc::mbar_wait(bar(c.v_full[k % kVSlots]), (uint32_t)(k / kVSlots) & 1);
+          for (int x = 0; x < 2; ++x)
+            if (qn[x]) tc::mbar_wait(bar(c.q_full[x]), (qn[x] - 1) & 1);
+          for (uint32_t k = kn > kKSlots ? kn - kKSlots : 0; k < kn; ++k)
+            tc::mbar_wait(bar(c.k_full[k % kKSlots]), (k / kKSlots) & 1);
+          for (uint32_t k = vn > kVSlots ? vn - kVSlots : 0; k < vn; ++k)
+            tc::mbar_wait(bar(c.v_full[k % kVSlots]), (k / kVSlots) & 1);
         }
       }
       __syncwarp();
     } else if (warp == 9) {
       // ---- products: one thread ----
-      if (jl < jh && elect_one()) {
+      if (elect_one()) {
         constexpr uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0);
         const uint32_t id_o = tc::idesc_bf16(128, nv * kChunkCols, 0, 1);
         bool ok = true;
-        int count[2] = {0, 0};
-        for (int j = jl - 1; ok && j < jh; ++j) {
-          const int kbase = (j + 1 - jl) * nc, vn = j - jl;
-          for (int x = 0; ok && x < 2; ++x) {
-            if (j >= jl && active(x, j)) {
-              ok = wait_or_fail(bar(c.p_ready[x]), (uint32_t)(count[x] - 1) & 1, fail) &&
-                   wait_or_fail(bar(c.v_full[vn % kVSlots]), (uint32_t)(vn / kVSlots) & 1, fail);
-              if (!ok) break;
-              tc::tc_fence_after();
-              const uint64_t dv =
-                  swizzled_desc(s0 + kOffV + (uint32_t)(2 * (vn % kVSlots)) * kChunkB, kChunkB);
-              const uint32_t old = count[x] > 1 ? 1u : 0u;
+        // of all items: products S, and items, of a tile; key chunks and value tiles
+        uint32_t sn[2] = {0, 0}, qn[2] = {0, 0}, kn = 0, vn = 0;
+        Item m{};
+        for (uint32_t round = 0; ok && next_item(m, round); ++round) {
+          for (int j = m.jl - 1; ok && j < m.jh; ++j) {
+            const bool now = j >= m.jl;
+            for (int x = 0; ok && x < 2; ++x) {
+              const int lo = x ? m.r[1].lo : m.r[0].lo, hi = x ? m.r[1].hi : m.r[0].hi;
+              const bool on = now && j >= lo && j < hi;
+              if (on) {
+                // the rows of the item before have been read
+                if (j == lo) ok = wait_or_fail(bar(c.o_free[x]), qn[x] & 1, fail);
+                ok = ok && wait_or_fail(bar(c.p_ready[x]), (sn[x] - 1) & 1, fail) &&
+                     wait_or_fail(bar(c.v_full[vn % kVSlots]), (vn / kVSlots) & 1, fail);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint64_t dv =
+                    swizzled_desc(s0 + kOffV + 2 * (vn % kVSlots) * kChunkB, kChunkB);
+                const uint32_t old = j > lo ? 1u : 0u;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e, dv + kStepRows * e, id_o,
-                            e > 0 ? 1u : old);
+                for (int e = 0; e < 8; ++e)
+                  mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * e, dv + kStepRows * e,
+                              id_o, e > 0 ? 1u : old);
+              }
+              if (j + 1 >= lo && j + 1 < hi) {
+                if (j + 1 == lo) {
+                  ok = wait_or_fail(bar(c.q_full[x]), qn[x] & 1, fail);
+                  if (!ok) break;
+                  ++qn[x];
+                }
+                const bool last = x == 1 || !m.active(1, j + 1);
+                for (int i = 0; i < nc; ++i) {
+                  const uint32_t k = kn + (uint32_t)i, s = k % kKSlots;
+                  ok = wait_or_fail(bar(c.k_full[s]), (k / kKSlots) & 1, fail);
+                  if (!ok) break;
+                  const uint64_t da = swizzled_desc(s0 + (uint32_t)(3 * x + i) * kChunkB, 16),
+                                 dk = swizzled_desc(s0 + kOffK + s * kChunkB, 16);
+                  const uint32_t old = i > 0 ? 1u : 0u;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    tc::mma_bf16(tmem + 128 * x, da + kStepK * e, dk + kStepK * e, id_s,
+                                 e > 0 ? 1u : old);
+                  if (last) tc::mma_commit(bar(c.k_empty[s]));
+                }
+                if (!ok) break;
+                tc::mma_commit(bar(c.s_full[x]));
+                ++sn[x];
+                if (j + 2 == hi) tc::mma_commit(bar(c.q_empty[x]));
+                if (last) kn += (uint32_t)nc;
+              }
+              if (on && j + 1 == hi) tc::mma_commit(bar(c.o_done[x]));
             }
-            if (j + 1 < jh && active(x, j + 1)) {
-              if (count[x] == 0) {
-                ok = wait_or_fail(bar(c.q_full[x]), 0, fail);
-                if (!ok) break;
-              }
-              const bool last = x == 1 || !active(1, j + 1);
-              for (int i = 0; i < nc; ++i) {
-                const int s = (kbase + i) % kKSlots;
-                ok = wait_or_fail(bar(c.k_full[s]), (uint32_t)((kbase + i) / kKSlots) & 1, fail);
-                if (!ok) break;
-                const uint64_t da = swizzled_desc(s0 + (uint32_t)(3 * x + i) * kChunkB, 16),
-                               dk = swizzled_desc(s0 + kOffK + (uint32_t)s * kChunkB, 16);
-                const uint32_t old = i > 0 ? 1u : 0u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  tc::mma_bf16(tmem + 128 * x, da + kStepK * e, dk + kStepK * e, id_s,
-                               e > 0 ? 1u : old);
-                if (last) tc::mma_commit(bar(c.k_empty[s]));
-              }
-              if (!ok) break;
-              tc::mma_commit(bar(c.s_full[x]));
-              ++count[x];
-            } else if (j >= jl && active(x, j)) {
-              tc::mma_commit(bar(c.o_done[x]));      // its last
+            if (ok && now) {
+              tc::mma_commit(bar(c.v_empty[vn % kVSlots]));
+              ++vn;
             }
           }
-          if (ok && j >= jl) tc::mma_commit(bar(c.v_empty[vn % kVSlots]));
         }
         if (*fail) {
           tc::mma_commit(bar(c.drain));
@@ -220,125 +320,134 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   } else {
     many_registers();
     // ---- softmax: a row a thread ----
-    const int x = warp >> 2, tile = 2 * pair + x;
-    const int row = tile * kRowsQ + (tid & 127);
-    const Range r = x ? rb : ra;
+    const int x = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t t_s = tmem + 128 * x + lanes, t_o = tmem + 256 + 128 * x + lanes;
-    const float sign = p.scale < 0.f ? -1.f : 1.f, scale = fabsf(p.scale) * kLog2e;
+    const float scale = p.scale * kLog2e;      // not negative
     const u64 scale2 = pk2(scale, scale);
-    const int lo = row < p.T ? run_start(p, b, row) : 0x7fffffff;
-    // the tiles that all rows see whole
-    const int all_lo = tile * kRowsQ < p.T ? run_start(p, b, min(p.T, (tile + 1) * kRowsQ) - 1) : 0;
-    float m = -INFINITY, l = 0.f;
-    for (int j = r.lo; j < r.hi; ++j) {
-      wait_or_fail(bar(c.s_full[x]), (uint32_t)(j - r.lo) & 1, fail);
-      __syncwarp();
-      tc::tc_fence_after();
-      uint32_t u[4][32];
+    uint32_t sn = 0, items = 0;
+    Item m0{};
+    for (uint32_t round = 0; __all_sync(0xffffffffu, next_item(m0, round)); ++round) {
+      const int b = m0.b, h = m0.h, tile = 2 * m0.pair + x, row = tile * kRowsQ + (tid & 127);
+      const Range r = x ? m0.r[1] : m0.r[0];
+      const int all_lo = x ? m0.all_lo[1] : m0.all_lo[0];
+      const int lo = row < p.T ? run_start(p, b, row) : 0x7fffffff;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int j = r.lo; j < r.hi; ++j, ++sn) {
+        wait_or_fail(bar(c.s_full[x]), sn & 1, fail);
+        __syncwarp();
+        tc::tc_fence_after();
+        uint32_t u[4][32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32_nw(t_s + 32 * i, u[i]);
-      tc::tmem_wait_ld();
+        for (int i = 0; i < 4; ++i) tmem_ld32_nw(t_s + 32 * i, u[i]);
+        tc::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) reg_fence32(u[i]);
-      if (sign < 0.f) {
+        for (int i = 0; i < 4; ++i) reg_fence32(u[i]);
+        if (j == tile || j * kRowsQ < all_lo) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) u[i >> 5][i & 31] ^= 0x80000000u;
-      }
-      if (j == tile || j * kRowsQ < all_lo) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          const int k = j * kRowsQ + i;
-          if (k < lo || k > row) u[i >> 5][i & 31] = 0xff800000u;   // -inf
-        }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 128; ++i) top = fmaxf(top, __uint_as_float(u[i >> 5][i & 31]));
-      top *= scale;
-      if (scale == 0.f) top = 0.f;
-      const bool over = top > m + kSlack;
-      if (__any_sync(0xffffffffu, over)) {
-        const float now = over ? top : m;
-        const float f = over ? exp2f(m - now) : 1.f;
-        m = now;
-        l *= f;
-        if (j > r.lo) {      // PV of the keys before is done: S of these came after it
-          for (int q = 0; q < 2 * nv; ++q) {
-            uint32_t o[32];
-            tmem_ld32_wait(t_o + 32 * q, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(t_o + 32 * q, o);
+          for (int i = 0; i < 128; ++i) {
+            const int k = j * kRowsQ + i;
+            if (k < lo || k > row) u[i >> 5][i & 31] = 0xff800000u;   // -inf
           }
         }
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      const u64 nb = pk2(-base, -base);
-      u64 sum = 0;
+        float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 128; ++i) top = fmaxf(top, __uint_as_float(u[i >> 5][i & 31]));
+        top *= scale;
+        if (scale == 0.f) top = 0.f;
+        const bool over = top > m + kSlack;
+        if (__any_sync(0xffffffffu, over)) {
+          const float now = over ? top : m;
+          const float f = over ? exp2f(m - now) : 1.f;
+          m = now;
+          l *= f;
+          if (j > r.lo) {      // PV of the keys before is done: S of these came after it
+#pragma unroll 1
+            for (int q = 0; q < 2 * nv; ++q) {
+              uint32_t o[32];
+              tmem_ld32_wait(t_o + 32 * q, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(t_o + 32 * q, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const u64 nb = pk2(-base, -base);
+        u64 sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, d;
+            upk2(fma2(pk2(__uint_as_float(u[i][2 * e]), __uint_as_float(u[i][2 * e + 1])), scale2,
+                      nb),
+                 a, d);
+            a = tc::ex2(a);
+            d = tc::ex2(d);
+            sum = add2(sum, pk2(a, d));
+            w[e] = tc::pack_bf16(a, d);
+          }
+          tmem_st16(t_s + 16 * i, w);
+        }
+        float a, d;
+        upk2(sum, a, d);
+        l += a + d;
+        tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(bar(c.p_ready[x]));
+      }
+      // ---- the rows ----
+      const bool any = r.lo < r.hi;
+      if (any) {
+        wait_or_fail(bar(c.o_done[x]), items & 1, fail);
+        __syncwarp();
+        tc::tc_fence_after();
+        ++items;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool bad = false;
+      __nv_bfloat16 *o =
+          static_cast<__nv_bfloat16 *>(p.o) + (((size_t)b * p.T + row) * p.H + h) * p.V;
+#pragma unroll 1
+      for (int q = 0; q < p.V / 32; ++q) {
+        uint32_t y[32];
+        if (any) {
+          tmem_ld32_wait(t_o + 32 * q, y);
+          if (q + 1 == p.V / 32) {     // the next item's products may write there
+            tc::tc_fence_before();
+            tc::mbar_arrive(bar(c.o_free[x]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = 0;
+        }
         uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float a, d;
-          upk2(fma2(pk2(__uint_as_float(u[i][2 * e]), __uint_as_float(u[i][2 * e + 1])), scale2, nb),
-               a, d);
-          a = tc::ex2(a);
-          d = tc::ex2(d);
-          sum = add2(sum, pk2(a, d));
-          w[e] = tc::pack_bf16(a, d);
+        for (int i = 0; i < 16; ++i) {
+          const float a = l == 0.f ? 0.f : __uint_as_float(y[2 * i]) * inv;
+          const float d = l == 0.f ? 0.f : __uint_as_float(y[2 * i + 1]) * inv;
+          bad |= !finite(a) || !finite(d);
+          w[i] = tc::pack_bf16(a, d);
         }
-        tmem_st16(t_s + 16 * i, w);
-      }
-      float a, d;
-      upk2(sum, a, d);
-      l += a + d;
-      tmem_wait_st();
-      tc::tc_fence_before();
-      tc::mbar_arrive(bar(c.p_ready[x]));
-    }
-    // ---- the rows ----
-    const bool any = r.lo < r.hi;
-    if (any) {
-      wait_or_fail(bar(c.o_done[x]), 0, fail);
-      __syncwarp();
-      tc::tc_fence_after();
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    bool bad = false;
-    __nv_bfloat16 *o =
-        static_cast<__nv_bfloat16 *>(p.o) + (((size_t)b * p.T + row) * p.H + h) * p.V;
-    for (int q = 0; q < p.V / 32; ++q) {
-      uint32_t y[32];
-      if (any) {
-        tmem_ld32_wait(t_o + 32 * q, y);
-      } else {
+        if (row < p.T) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = 0;
-      }
-      uint32_t w[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float a = l == 0.f ? 0.f : __uint_as_float(y[2 * i]) * inv;
-        const float d = l == 0.f ? 0.f : __uint_as_float(y[2 * i + 1]) * inv;
-        bad |= !finite(a) || !finite(d);
-        w[i] = tc::pack_bf16(a, d);
-      }
-      if (row < p.T) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4 *>(o + 32 * q)[i] =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(o + 32 * q)[i] =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        __syncwarp();
       }
       __syncwarp();
+      if (p.lse && row < p.T)
+        p.lse[((size_t)b * p.H + h) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      unsigned which = __ballot_sync(0xffffffffu, bad && row < p.T);
+      __syncwarp();
+      for (; which; which &= which - 1)
+        forward_row<__nv_bfloat16>(p, b, h, row - lane + __ffs(which) - 1, lane);
     }
-    if (p.lse && row < p.T)
-      p.lse[((size_t)b * p.H + h) * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    unsigned which = __ballot_sync(0xffffffffu, bad && row < p.T);
-    __syncwarp();
-    for (; which; which &= which - 1)
-      forward_row<__nv_bfloat16>(p, b, h, row - lane + __ffs(which) - 1, lane);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -365,7 +474,8 @@ bool prompt_map(CUtensorMap *m, const void *x, const Strides &s, const Prompt &p
 }
 
 bool prompt_tc_ok(const Prompt &p) {
-  return tensor_ok(p.q, p.q_s, p, true) && tensor_ok(p.k, p.k_s, p, true) &&
+  // (the largest product is the largest score only where the scale is not negative)
+  return p.scale >= 0.f && tensor_ok(p.q, p.q_s, p, true) && tensor_ok(p.k, p.k_s, p, true) &&
          tensor_ok(p.v, p.v_s, p, true) &&
          (p.R == 0 || (tensor_ok(p.qr, p.qr_s, p, true) && tensor_ok(p.kr, p.kr_s, p, false)));
 }
@@ -384,7 +494,10 @@ cudaError_t launch_prompt_tc(const Prompt &p, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem);
   if (e != cudaSuccess) return e;
   const unsigned pairs = (unsigned)((p.T + 2 * kRowsQ - 1) / (2 * kRowsQ));
-  prompt_fwd_tc_kernel<<<pairs * (unsigned)(p.B * p.H), kThreads, kFwdSmem, s>>>(m, p);
+  const unsigned grid = pairs * (unsigned)(p.B * p.H);
+  if (p.start)             // it gets ready while the table of runs is made
+    return launch_next(prompt_fwd_tc_kernel, dim3(grid), kThreads, kFwdSmem, s, m, p);
+  prompt_fwd_tc_kernel<<<grid, kThreads, kFwdSmem, s>>>(m, p);
   return cudaGetLastError();
 }
 

@@ -684,6 +684,7 @@ KDA_API kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, con
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  * pairs != 0: (x[2i], x[2i+1]), else (x[i], x[i + dim/2]).  The angle is reduced
  * exactly, so far positions lose nothing; cos, sin and the products are fp32.
+ * (Here and below, the stride of a dimension of 1 is not read.)
  *   x             device [B,T,H,dim] of d->dtype, the last dimension contiguous.
  *   positions     device int32 [B,T] or NULL (t = 0 .. T-1).
  *   inv_freq      device float32 [dim/2].
