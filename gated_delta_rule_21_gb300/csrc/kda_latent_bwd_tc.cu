@@ -255,7 +255,9 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       tc::tmem_wait_ld();
       reg_fence32(s);
       reg_fence32(d);
-      const bool whole = y0 >= all_from && y0 + 32 <= all_to;
+      const uint32_t on = column_bits(from, to, y0);
+      const bool whole = (y0 >= all_from && y0 + 32 <= all_to) ||
+                         __all_sync(0xffffffffu, on == 0xffffffffu);
       uint32_t pw[16], dw[16];
       const u64 sc = pk2(scale, scale), nl = pk2(-lse, -lse), nd = pk2(-delta, -delta);
 #pragma unroll
@@ -271,8 +273,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
                        kKeys ? pk2(de[e].x, de[e].y) : nd)),
              g0, g1);
         if (!whole) {
-          const int y = y0 + 2 * e;
-          const bool on0 = y >= from && y < to, on1 = y + 1 >= from && y + 1 < to;
+          const bool on0 = on >> (2 * e) & 1u, on1 = on >> (2 * e + 1) & 1u;
           w0 = on0 ? w0 : 0.f;
           g0 = on0 ? g0 : 0.f;
           w1 = on1 ? w1 : 0.f;

@@ -345,10 +345,15 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) reg_fence32(u[i]);
         if (j == tile || j * kRowsQ < all_lo) {
+          // a warp's rows see most groups of 32 keys whole or not at all
 #pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const int k = j * kRowsQ + i;
-            if (k < lo || k > row) u[i >> 5][i & 31] = 0xff800000u;   // -inf
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t on = column_bits(lo, row + 1, j * kRowsQ + 32 * i);
+            if (!__all_sync(0xffffffffu, on == 0xffffffffu)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(on >> e & 1u)) u[i][e] = 0xff800000u;   // -inf
+            }
           }
         }
         float top = -INFINITY;

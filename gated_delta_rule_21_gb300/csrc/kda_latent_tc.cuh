@@ -109,6 +109,13 @@ struct Slot {
   }
 };
 
+// Columns [from, to) of 32 that begin at `at`, as bits.
+__device__ __forceinline__ uint32_t column_bits(int from, int to, int at) {
+  const int a = min(max(from - at, 0), 32), z = min(max(to - at, 0), 32);
+  const uint32_t below = z >= 32 ? 0xffffffffu : (1u << z) - 1u;
+  return a >= 32 ? 0u : below & (0xffffffffu << a);
+}
+
 // D (+)= A B over one K = 16 step, A in tensor memory (bf16, two a column).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                             uint32_t idesc, uint32_t accum) {
