@@ -2,12 +2,12 @@
 // runs, the small kernels around the backward, and the fp32 kernels on the
 // CUDA cores, which serve every type and layout.
 //
-// CUDA cores: a CTA of 256 threads holds 64 queries (forward, gradient of the
+// CUDA cores: a CTA of 512 threads holds 64 queries (forward, gradient of the
 // queries) or 64 keys (gradients of keys and values) of one head in shared
 // memory as fp32 and walks the other side in tiles of 64.  A thread makes a
-// 4 x 4 piece of the tile of scores with packed multiply-adds (two terms of the
-// sum at once) and 4 rows of the outputs.  What bounds it: shared memory, 3 of
-// 4 cycles of the multiply-adds.
+// 2 x 4 piece of the tile of scores with packed multiply-adds (two terms of the
+// sum at once) and 2 rows of the outputs.  What bounds it: the way of the longest
+// row, tile after tile.  TODO-TIMES
 #include <string.h>
 
 #include "kda_f32x2.cuh"
@@ -17,8 +17,9 @@ namespace kda {
 namespace latent {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kBlk = 64;          // rows of a tile, either side
+constexpr int kRt = 2;            // rows of a thread
 constexpr int kLdP = kBlk + 4;    // of a tile of weights
 
 __device__ __forceinline__ float4 four(const float *x) {
@@ -39,8 +40,8 @@ __device__ __forceinline__ void load_rows(float *dst, int ld, const T *x, long l
                                           int fours) {
   const int w = n + nr, r0 = threadIdx.x >> 4, c0 = 4 * (threadIdx.x & 15);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 16 * i, t = t0 + r;
+  for (int i = 0; i < kRt; ++i) {
+    const int r = r0 + kThreads / 16 * i, t = t0 + r;
     const T *a = x + t * st, *b = xr + t * str - n;
     for (int c = c0; c < w; c += 64) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -53,25 +54,25 @@ __device__ __forceinline__ void load_rows(float *dst, int ld, const T *x, long l
   }
 }
 
-// s[i][j] = sum_c a[4 ty + i][c] b[tx + 16 j][c] over n (a multiple of 4) values.
+// s[i][j] = sum_c a[2 ty + i][c] b[tx + 16 j][c] over n (a multiple of 4) values.
 __device__ __forceinline__ void rows_by_rows(const float *a, int lda, const float *b, int ldb,
-                                             int n, int ty, int tx, float (&s)[4][4]) {
-  u64 acc[4][4];
+                                             int n, int ty, int tx, float (&s)[kRt][4]) {
+  u64 acc[kRt][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kRt; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0;
-  a += 4 * ty * lda;
+  a += kRt * ty * lda;
   b += tx * ldb;
 #pragma unroll 2
   for (int c = 0; c < n; c += 4) {
-    ulonglong2 x[4], y[4];
+    ulonglong2 x[kRt], y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2 *>(a + i * lda + c);
+    for (int i = 0; i < kRt; ++i) x[i] = *reinterpret_cast<const ulonglong2 *>(a + i * lda + c);
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2 *>(b + 16 * j * ldb + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kRt; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         acc[i][j] = fma2(x[i].x, y[j].x, acc[i][j]);
@@ -79,7 +80,7 @@ __device__ __forceinline__ void rows_by_rows(const float *a, int lda, const floa
       }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kRt; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float lo, hi;
@@ -88,17 +89,17 @@ __device__ __forceinline__ void rows_by_rows(const float *a, int lda, const floa
     }
 }
 
-// acc[i][q] += sum_k w[4 ty + i][k] y[k][4 tx + 64 q ..] over the tile's 64 k.
+// acc[i][q] += sum_k w[2 ty + i][k] y[k][4 tx + 64 q ..] over the tile's 64 k.
 template <int N>
 __device__ __forceinline__ void weights_by_rows(const float *w, const float *y, int ld, int n,
-                                                int ty, int tx, u64 (&acc)[4][N][2]) {
-  w += 4 * ty * kLdP;
+                                                int ty, int tx, u64 (&acc)[kRt][N][2]) {
+  w += kRt * ty * kLdP;
   y += 4 * tx;
 #pragma unroll 1
   for (int k = 0; k < kBlk; k += 4) {
-    float4 c[4];
+    float4 c[kRt];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const float4 *>(w + i * kLdP + k);
+    for (int i = 0; i < kRt; ++i) c[i] = *reinterpret_cast<const float4 *>(w + i * kLdP + k);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -106,7 +107,7 @@ __device__ __forceinline__ void weights_by_rows(const float *w, const float *y, 
         if (4 * tx + 64 * q >= n) continue;
         const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(y + (k + kk) * ld + 64 * q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kRt; ++i) {
           const float f = kk == 0 ? c[i].x : kk == 1 ? c[i].y : kk == 2 ? c[i].z : c[i].w;
           const u64 ff = pk2(f, f);
           acc[i][q][0] = fma2(ff, v.x, acc[i][q][0]);
@@ -117,9 +118,9 @@ __device__ __forceinline__ void weights_by_rows(const float *w, const float *y, 
 }
 
 template <int N>
-__device__ __forceinline__ void clear(u64 (&acc)[4][N][2]) {
+__device__ __forceinline__ void clear(u64 (&acc)[kRt][N][2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kRt; ++i)
 #pragma unroll
     for (int q = 0; q < N; ++q) acc[i][q][0] = acc[i][q][1] = 0;
 }
@@ -148,7 +149,7 @@ __device__ __forceinline__ Where where(const Prompt &p, bool last_first) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
   float *sq = sm, *sk = sq + kBlk * ldq, *sv = sk + kBlk * ldq, *sp = sv + kBlk * ldv;
@@ -157,15 +158,15 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
   const int b = at0.b, h = at0.h, t0 = at0.t0;
   load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
                p.qr_s.t, p.R, t0, p.T, p.fours);
-  int lo[4];
+  int lo[kRt];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    lo[i] = t0 + 4 * ty + i < p.T ? run_start(p, b, t0 + 4 * ty + i) : 0x7fffffff;
-  float m[4], l[4];
-  u64 acc[4][2][2];
+  for (int i = 0; i < kRt; ++i)
+    lo[i] = t0 + kRt * ty + i < p.T ? run_start(p, b, t0 + kRt * ty + i) : 0x7fffffff;
+  float m[kRt], l[kRt];
+  u64 acc[kRt][2][2];
   clear(acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  for (int i = 0; i < kRt; ++i) m[i] = -INFINITY, l[i] = 0.f;
   const float scale = p.scale * kLog2e;
   const int last = min(p.T, t0 + kBlk);
   for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
@@ -174,11 +175,11 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
                  p.kr_s.t, p.R, j0, p.T, p.fours);
     load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0, p.T, p.fours);
     __syncthreads();
-    float s[4][4];
+    float s[kRt][4];
     rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + 4 * ty + i;
+    for (int i = 0; i < kRt; ++i) {
+      const int t = t0 + kRt * ty + i;
       float top = m[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
       for (int j = 0; j < 4; ++j) {
         const float w = exp2f(s[i][j] - base);
         sum += w;
-        sp[(4 * ty + i) * kLdP + tx + 16 * j] = w;
+        sp[(kRt * ty + i) * kLdP + tx + 16 * j] = w;
       }
       l[i] = l[i] * f + row_sum(sum);
       m[i] = top;
@@ -209,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
     __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * ty + i;
+  for (int i = 0; i < kRt; ++i) {
+    const int t = t0 + kRt * ty + i;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     bool bad = false;
     if (t < p.T) {
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(Prompt p) {
     }
     const unsigned which = __ballot_sync(0xffffffffu, bad);
     __syncwarp();
-    if (which & 0xffffu) forward_row<T>(p, b, h, t0 + 8 * (tid >> 5) + i, tid & 31);
-    if (which & 0xffff0000u) forward_row<T>(p, b, h, t0 + 8 * (tid >> 5) + 4 + i, tid & 31);
+    if (which & 0xffffu) forward_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + i, tid & 31);
+    if (which & 0xffff0000u) forward_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + kRt + i, tid & 31);
   }
 }
 
@@ -252,12 +253,12 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
   load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
                p.kr_s.t, p.R, t0, p.T, p.fours);
   load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, t0, p.T, p.fours);
-  int end[4];
+  int end[kRt];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    end[i] = t0 + 4 * ty + i < p.T ? run_end(p, b, t0 + 4 * ty + i) : 0;
+  for (int i = 0; i < kRt; ++i)
+    end[i] = t0 + kRt * ty + i < p.T ? run_end(p, b, t0 + kRt * ty + i) : 0;
   const int last = run_end(p, b, min(p.T, t0 + kBlk) - 1);
-  u64 ak[4][3][2], av[4][2][2];
+  u64 ak[kRt][3][2], av[kRt][2][2];
   clear(ak);
   clear(av);
   const float scale = p.scale * kLog2e;
@@ -273,18 +274,18 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
       s_delta[tid] = p.delta[r];
     }
     __syncthreads();
-    float s[4][4], dp[4][4];
+    float s[kRt][4], dp[kRt][4];
     rows_by_rows(sk, ldq, sq, ldq, D, ty, tx, s);
     rows_by_rows(sv, ldv, su, ldv, p.V, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kRt; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = tx + 16 * j, t = i0 + c;
-        const bool on = t >= t0 + 4 * ty + i && t < end[i];
+        const bool on = t >= t0 + kRt * ty + i && t < end[i];
         const float w = on ? exp2f(s[i][j] * scale - s_lse[c]) : 0.f;
-        sp[(4 * ty + i) * kLdP + c] = w;
-        sd[(4 * ty + i) * kLdP + c] = on ? w * (dp[i][j] - s_delta[c]) : 0.f;
+        sp[(kRt * ty + i) * kLdP + c] = w;
+        sd[(kRt * ty + i) * kLdP + c] = on ? w * (dp[i][j] - s_delta[c]) : 0.f;
       }
     __syncwarp();
     weights_by_rows<2>(sp, su, ldv, p.V, ty, tx, av);
@@ -292,8 +293,8 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
     __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * ty + i;
+  for (int i = 0; i < kRt; ++i) {
+    const int t = t0 + kRt * ty + i;
     const size_t row = ((size_t)b * p.T + t) * p.H + h;
     bool bad = false;
     if (t < p.T) {
@@ -317,13 +318,13 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
     }
     const unsigned which = __ballot_sync(0xffffffffu, bad);
     __syncwarp();
-    if (which & 0xffffu) key_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + i, tid & 31);
-    if (which & 0xffff0000u) key_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + 4 + i, tid & 31);
+    if (which & 0xffffu) key_grad_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + i, tid & 31);
+    if (which & 0xffff0000u) key_grad_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + kRt + i, tid & 31);
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
   float *sq = sm, *su = sq + kBlk * ldq, *sk = su + kBlk * ldv, *sv = sk + kBlk * ldq,
@@ -335,17 +336,17 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(Prompt p) {
                p.qr_s.t, p.R, t0, p.T, p.fours);
   load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
                (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, t0, p.T, 1);
-  int lo[4];
-  float lse[4], delta[4];
+  int lo[kRt];
+  float lse[kRt], delta[kRt];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * ty + i;
+  for (int i = 0; i < kRt; ++i) {
+    const int t = t0 + kRt * ty + i;
     lo[i] = t < p.T ? run_start(p, b, t) : 0x7fffffff;
     const size_t r = ((size_t)b * p.H + h) * p.T + min(t, p.T - 1);
     lse[i] = p.lse[r] * kLog2e;
     delta[i] = p.delta[r];
   }
-  u64 acc[4][3][2];
+  u64 acc[kRt][3][2];
   clear(acc);
   const float scale = p.scale * kLog2e;
   const int last = min(p.T, t0 + kBlk);
@@ -355,16 +356,16 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(Prompt p) {
                  p.kr_s.t, p.R, j0, p.T, p.fours);
     load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0, p.T, p.fours);
     __syncthreads();
-    float s[4][4], dp[4][4];
+    float s[kRt][4], dp[kRt][4];
     rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
     rows_by_rows(su, ldv, sv, ldv, p.V, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kRt; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = j0 + tx + 16 * j;
-        const bool on = k >= lo[i] && k <= t0 + 4 * ty + i;
-        sd[(4 * ty + i) * kLdP + tx + 16 * j] =
+        const bool on = k >= lo[i] && k <= t0 + kRt * ty + i;
+        sd[(kRt * ty + i) * kLdP + tx + 16 * j] =
             on ? exp2f(s[i][j] * scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
       }
     __syncwarp();
@@ -372,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(Prompt p) {
     __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * ty + i;
+  for (int i = 0; i < kRt; ++i) {
+    const int t = t0 + kRt * ty + i;
     const size_t row = ((size_t)b * p.T + t) * p.H + h;
     bool bad = false;
     if (t < p.T) {
@@ -392,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(Prompt p) {
     }
     const unsigned which = __ballot_sync(0xffffffffu, bad);
     __syncwarp();
-    if (which & 0xffffu) query_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + i, tid & 31);
-    if (which & 0xffff0000u) query_grad_row<T>(p, b, h, t0 + 8 * (tid >> 5) + 4 + i, tid & 31);
+    if (which & 0xffffu) query_grad_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + i, tid & 31);
+    if (which & 0xffff0000u) query_grad_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + kRt + i, tid & 31);
   }
 }
 
@@ -478,11 +479,13 @@ __global__ void __launch_bounds__(kRunThreads) runs_kernel(const int *ids, int T
 }
 
 // ---- around the backward ----------------------------------------------------
+constexpr int kSmall = 256;       // threads
+
 // delta[b][h][t] = d_o . o, 8 lanes a row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) delta_kernel(Prompt p) {
+__global__ void __launch_bounds__(kSmall) delta_kernel(Prompt p) {
   const long long rows = (long long)p.B * p.T * p.H;
-  const long long r = (long long)blockIdx.x * (kThreads / 8) + threadIdx.x / 8;
+  const long long r = (long long)blockIdx.x * (kSmall / 8) + threadIdx.x / 8;
   float s = 0.f;
   if (r < rows) {
     const T *o = static_cast<const T *>(p.o) + r * p.V,
@@ -510,9 +513,9 @@ __global__ void __launch_bounds__(kThreads) delta_kernel(Prompt p) {
 
 // dk_rope = the sum of the heads' parts, in the order of the heads.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_sum_kernel(Prompt p) {
+__global__ void __launch_bounds__(kSmall) rope_sum_kernel(Prompt p) {
   const int quads = p.R / 4;
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long i = (long long)blockIdx.x * kSmall + threadIdx.x;
   if (i >= (long long)p.B * p.T * quads) return;
   const float4 *x = reinterpret_cast<const float4 *>(p.dkr_part) + i / quads * p.H * quads +
                     i % quads;
@@ -549,7 +552,7 @@ cudaError_t forward_simt(const Prompt &p, cudaStream_t cs) {
 template <typename T>
 cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
   const long long rows = (long long)p.B * p.T * p.H;
-  delta_kernel<T><<<(unsigned)((rows + kThreads / 8 - 1) / (kThreads / 8)), kThreads, 0, cs>>>(p);
+  delta_kernel<T><<<(unsigned)((rows + kSmall / 8 - 1) / (kSmall / 8)), kSmall, 0, cs>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (tc) {
@@ -562,7 +565,7 @@ cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
   }
   if (e != cudaSuccess || p.R == 0) return e;
   const long long quads = (long long)p.B * p.T * (p.R / 4);
-  rope_sum_kernel<T><<<(unsigned)((quads + kThreads - 1) / kThreads), kThreads, 0, cs>>>(p);
+  rope_sum_kernel<T><<<(unsigned)((quads + kSmall - 1) / kSmall), kSmall, 0, cs>>>(p);
   return cudaGetLastError();
 }
 
