@@ -32,26 +32,92 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16 *x) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Rows t0 .. t0 + 63 of [x | xr] (n and nr values) as fp32, zeros from row `lim` on: 16
-// threads a row, 4 values each where these can be read at once.
+// Rows of one head, [x | xr] of n and nr values; fours: 4 values can be read at once.
 template <typename T>
-__device__ __forceinline__ void load_rows(float *dst, int ld, const T *x, long long st, int n,
-                                          const T *xr, long long str, int nr, int t0, int lim,
-                                          int fours) {
-  const int w = n + nr, r0 = threadIdx.x >> 4, c0 = 4 * (threadIdx.x & 15);
+struct Side {
+  const T *x, *xr;
+  long long st, str;
+  int n, nr, fours;
+  // Rows t0 .. t0 + 63 as fp32, zeros from row `lim` on, 16 threads a row.  fp32 values
+  // come by asynchronous copies.
+  __device__ __forceinline__ void load(float *dst, int ld, int t0, int lim) const {
+    const int w = n + nr, r0 = threadIdx.x >> 4, c0 = 4 * (threadIdx.x & 15);
 #pragma unroll
-  for (int i = 0; i < kRt; ++i) {
-    const int r = r0 + kThreads / 16 * i, t = t0 + r;
-    const T *a = x + t * st, *b = xr + t * str - n;
-    for (int c = c0; c < w; c += 64) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < lim) {
+    for (int i = 0; i < kRt; ++i) {
+      const int r = r0 + kThreads / 16 * i, t = t0 + r;
+      const T *a = x + t * st, *b = xr + t * str - n;
+      for (int c = c0; c < w; c += 64) {
         const T *y = (c < n ? a : b) + c;
-        v = fours ? four(y) : make_float4(to_f32(y[0]), to_f32(y[1]), to_f32(y[2]), to_f32(y[3]));
+        float *d = dst + r * ld + c;
+        if (sizeof(T) == 4 && fours) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           (uint32_t)__cvta_generic_to_shared(d)),
+                       "l"(t < lim ? y : x), "r"(t < lim ? 16 : 0)
+                       : "memory");
+        } else {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (t < lim)
+            v = fours ? four(y)
+                      : make_float4(to_f32(y[0]), to_f32(y[1]), to_f32(y[2]), to_f32(y[3]));
+          *reinterpret_cast<float4 *>(d) = v;
+        }
       }
-      *reinterpret_cast<float4 *>(dst + r * ld + c) = v;
     }
   }
+};
+template <typename T>
+__device__ __forceinline__ Side<T> keys_side(const Prompt &p, int b, int h) {
+  return {at<T>(p.k, p.k_s, b, 0, h), at<T>(p.kr, p.kr_s, b, 0, 0), p.k_s.t, p.kr_s.t, p.K, p.R,
+          p.fours};
+}
+template <typename T>
+__device__ __forceinline__ Side<T> queries_side(const Prompt &p, int b, int h) {
+  return {at<T>(p.q, p.q_s, b, 0, h), at<T>(p.qr, p.qr_s, b, 0, h), p.q_s.t, p.qr_s.t, p.K, p.R,
+          p.fours};
+}
+template <typename T>
+__device__ __forceinline__ Side<T> values_side(const Prompt &p, int b, int h) {
+  return {at<T>(p.v, p.v_s, b, 0, h), nullptr, p.v_s.t, 0, p.V, 0, p.fours};
+}
+template <typename T>
+__device__ __forceinline__ Side<T> up_side(const Prompt &p, int b, int h) {
+  return {static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V, nullptr,
+          (long long)p.H * p.V, 0, p.V, 0, 1};
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last `kBut` groups are in.
+template <int kBut>
+__device__ __forceinline__ void copies_in() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kBut) : "memory");
+}
+
+// The other side's tiles from t0 up to `last`: while work(t, stage) goes over one, the next
+// one is on its way where the shared memory has two stages.
+template <typename L, typename W>
+__device__ __forceinline__ void walk(int t0, int last, int stages, L load, W work) {
+  int st = 0;
+  if (t0 < last) load(t0, 0);
+  copies_sent();
+  for (; t0 < last; t0 += kBlk) {
+    const bool more = t0 + kBlk < last;
+    if (stages == 2) {
+      if (more) load(t0 + kBlk, st ^ 1);
+      copies_sent();
+      copies_in<1>();
+    } else {
+      copies_in<0>();
+    }
+    __syncthreads();
+    work(t0, st);
+    __syncthreads();
+    if (stages == 2) {
+      st ^= 1;
+    } else if (more) {
+      load(t0 + kBlk, 0);
+      copies_sent();
+    }
+  }
+  copies_in<0>();
 }
 
 // s[i][j] = sum_c a[2 ty + i][c] b[tx + 16 j][c] over n (a multiple of 4) values.
@@ -89,13 +155,16 @@ __device__ __forceinline__ void rows_by_rows(const float *a, int lda, const floa
     }
 }
 
-// acc[i][q] += sum_k w[2 ty + i][k] y[k][4 tx + 64 q ..] over the tile's 64 k.
-template <int N>
-__device__ __forceinline__ void weights_by_rows(const float *w, const float *y, int ld, int n,
-                                                int ty, int tx, u64 (&acc)[kRt][N][2]) {
+// acc[i][q] += sum_k w[2 ty + i][k] y[k][4 tx + 64 q ..] over the tile's 64 k, for q < N.
+template <int N, int M>
+__device__ __forceinline__ void weights_by_some(const float *w, const float *y, int ld, int n,
+                                                int ty, int tx, u64 (&acc)[kRt][M][2]) {
   w += kRt * ty * kLdP;
-  y += 4 * tx;
-#pragma unroll 1
+  const float *at[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) at[q] = y + 4 * tx + 64 * q;
+  if (4 * tx + 64 * (N - 1) >= n) at[N - 1] = y;     // (its sums are not used)
+#pragma unroll 2
   for (int k = 0; k < kBlk; k += 4) {
     float4 c[kRt];
 #pragma unroll
@@ -104,8 +173,7 @@ __device__ __forceinline__ void weights_by_rows(const float *w, const float *y, 
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int q = 0; q < N; ++q) {
-        if (4 * tx + 64 * q >= n) continue;
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(y + (k + kk) * ld + 64 * q);
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(at[q] + (k + kk) * ld);
 #pragma unroll
         for (int i = 0; i < kRt; ++i) {
           const float f = kk == 0 ? c[i].x : kk == 1 ? c[i].y : kk == 2 ? c[i].z : c[i].w;
@@ -115,6 +183,13 @@ __device__ __forceinline__ void weights_by_rows(const float *w, const float *y, 
         }
       }
   }
+}
+template <int M>
+__device__ __forceinline__ void weights_by_rows(const float *w, const float *y, int ld, int n,
+                                                int ty, int tx, u64 (&acc)[kRt][M][2]) {
+  if (n <= 64) weights_by_some<1>(w, y, ld, n, ty, tx, acc);
+  else if (n <= 128) weights_by_some<2>(w, y, ld, n, ty, tx, acc);
+  else if (M > 2) weights_by_some<M>(w, y, ld, n, ty, tx, acc);
 }
 
 template <int N>
@@ -149,15 +224,16 @@ __device__ __forceinline__ Where where(const Prompt &p, bool last_first) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(const Prompt p, int stages) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
-  float *sq = sm, *sk = sq + kBlk * ldq, *sv = sk + kBlk * ldq, *sp = sv + kBlk * ldv;
+  float *sq = sm, *sp = sq + kBlk * ldq, *ring = sp + kBlk * kLdP;
+  const int stage = kBlk * (ldq + ldv);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Where at0 = where(p, true);
   const int b = at0.b, h = at0.h, t0 = at0.t0;
-  load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
-               p.qr_s.t, p.R, t0, p.T, p.fours);
+  const Side<T> keys = keys_side<T>(p, b, h), values = values_side<T>(p, b, h);
+  queries_side<T>(p, b, h).load(sq, ldq, t0, p.T);
   int lo[kRt];
 #pragma unroll
   for (int i = 0; i < kRt; ++i)
@@ -169,12 +245,12 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
   for (int i = 0; i < kRt; ++i) m[i] = -INFINITY, l[i] = 0.f;
   const float scale = p.scale * kLog2e;
   const int last = min(p.T, t0 + kBlk);
-  for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
-    __syncthreads();
-    load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
-                 p.kr_s.t, p.R, j0, p.T, p.fours);
-    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0, p.T, p.fours);
-    __syncthreads();
+  auto load = [&](int j0, int st) {
+    keys.load(ring + st * stage, ldq, j0, p.T);
+    values.load(ring + st * stage + kBlk * ldq, ldv, j0, p.T);
+  };
+  walk(run_start(p, b, t0) / kBlk * kBlk, last, stages, load, [&](int j0, int st) {
+    const float *sk = ring + st * stage, *sv = sk + kBlk * ldq;
     float s[kRt][4];
     rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
 #pragma unroll
@@ -206,9 +282,8 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
       }
     }
     __syncwarp();   // the rows of a warp are its own
-    weights_by_rows<2>(sp, sv, ldv, p.V, ty, tx, acc);
-    __syncwarp();
-  }
+    weights_by_rows(sp, sv, ldv, p.V, ty, tx, acc);
+  });
 #pragma unroll
   for (int i = 0; i < kRt; ++i) {
     const int t = t0 + kRt * ty + i;
@@ -241,18 +316,19 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(Prompt p) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(const Prompt p, int stages) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
-  float *sk = sm, *sv = sk + kBlk * ldq, *sq = sv + kBlk * ldv, *su = sq + kBlk * ldq,
-        *sp = su + kBlk * ldv, *sd = sp + kBlk * kLdP;
-  __shared__ float s_lse[kBlk], s_delta[kBlk];
+  float *sk = sm, *sv = sk + kBlk * ldq, *sp = sv + kBlk * ldv, *sd = sp + kBlk * kLdP,
+        *ring = sd + kBlk * kLdP;
+  const int stage = kBlk * (ldq + ldv);
+  __shared__ float s_lse[2][kBlk], s_delta[2][kBlk];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Where at0 = where(p, false);
   const int b = at0.b, h = at0.h, t0 = at0.t0;
-  load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
-               p.kr_s.t, p.R, t0, p.T, p.fours);
-  load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, t0, p.T, p.fours);
+  const Side<T> queries = queries_side<T>(p, b, h), up = up_side<T>(p, b, h);
+  keys_side<T>(p, b, h).load(sk, ldq, t0, p.T);
+  values_side<T>(p, b, h).load(sv, ldv, t0, p.T);
   int end[kRt];
 #pragma unroll
   for (int i = 0; i < kRt; ++i)
@@ -262,18 +338,17 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
   clear(ak);
   clear(av);
   const float scale = p.scale * kLog2e;
-  for (int i0 = t0; i0 < last; i0 += kBlk) {
-    __syncthreads();
-    load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
-                 p.qr_s.t, p.R, i0, p.T, p.fours);
-    load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
-                 (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, i0, p.T, 1);
+  auto load = [&](int i0, int st) {
+    queries.load(ring + st * stage, ldq, i0, p.T);
+    up.load(ring + st * stage + kBlk * ldq, ldv, i0, p.T);
     if (tid < kBlk && i0 + tid < p.T) {
       const size_t r = ((size_t)b * p.H + h) * p.T + i0 + tid;
-      s_lse[tid] = p.lse[r] * kLog2e;
-      s_delta[tid] = p.delta[r];
+      s_lse[st][tid] = p.lse[r] * kLog2e;
+      s_delta[st][tid] = p.delta[r];
     }
-    __syncthreads();
+  };
+  walk(t0, last, stages, load, [&](int i0, int st) {
+    const float *sq = ring + st * stage, *su = sq + kBlk * ldq;
     float s[kRt][4], dp[kRt][4];
     rows_by_rows(sk, ldq, sq, ldq, D, ty, tx, s);
     rows_by_rows(sv, ldv, su, ldv, p.V, ty, tx, dp);
@@ -283,15 +358,14 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
       for (int j = 0; j < 4; ++j) {
         const int c = tx + 16 * j, t = i0 + c;
         const bool on = t >= t0 + kRt * ty + i && t < end[i];
-        const float w = on ? exp2f(s[i][j] * scale - s_lse[c]) : 0.f;
+        const float w = on ? exp2f(s[i][j] * scale - s_lse[st][c]) : 0.f;
         sp[(kRt * ty + i) * kLdP + c] = w;
-        sd[(kRt * ty + i) * kLdP + c] = on ? w * (dp[i][j] - s_delta[c]) : 0.f;
+        sd[(kRt * ty + i) * kLdP + c] = on ? w * (dp[i][j] - s_delta[st][c]) : 0.f;
       }
     __syncwarp();
-    weights_by_rows<2>(sp, su, ldv, p.V, ty, tx, av);
-    weights_by_rows<3>(sd, sq, ldq, D, ty, tx, ak);
-    __syncwarp();
-  }
+    weights_by_rows(sp, su, ldv, p.V, ty, tx, av);
+    weights_by_rows(sd, sq, ldq, D, ty, tx, ak);
+  });
 #pragma unroll
   for (int i = 0; i < kRt; ++i) {
     const int t = t0 + kRt * ty + i;
@@ -324,18 +398,17 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(Prompt p) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
+__global__ void __launch_bounds__(kThreads) prompt_dq_kernel(const Prompt p, int stages) {
   extern __shared__ __align__(16) float sm[];
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
-  float *sq = sm, *su = sq + kBlk * ldq, *sk = su + kBlk * ldv, *sv = sk + kBlk * ldq,
-        *sd = sv + kBlk * ldv;
+  float *sq = sm, *su = sq + kBlk * ldq, *sd = su + kBlk * ldv, *ring = sd + kBlk * kLdP;
+  const int stage = kBlk * (ldq + ldv);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Where at0 = where(p, true);
   const int b = at0.b, h = at0.h, t0 = at0.t0;
-  load_rows<T>(sq, ldq, at<T>(p.q, p.q_s, b, 0, h), p.q_s.t, p.K, at<T>(p.qr, p.qr_s, b, 0, h),
-               p.qr_s.t, p.R, t0, p.T, p.fours);
-  load_rows<T>(su, ldv, static_cast<const T *>(p.d_o) + ((size_t)b * p.T * p.H + h) * p.V,
-               (long long)p.H * p.V, p.V, (const T *)nullptr, 0, 0, t0, p.T, 1);
+  const Side<T> keys = keys_side<T>(p, b, h), values = values_side<T>(p, b, h);
+  queries_side<T>(p, b, h).load(sq, ldq, t0, p.T);
+  up_side<T>(p, b, h).load(su, ldv, t0, p.T);
   int lo[kRt];
   float lse[kRt], delta[kRt];
 #pragma unroll
@@ -350,12 +423,12 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
   clear(acc);
   const float scale = p.scale * kLog2e;
   const int last = min(p.T, t0 + kBlk);
-  for (int j0 = run_start(p, b, t0) / kBlk * kBlk; j0 < last; j0 += kBlk) {
-    __syncthreads();
-    load_rows<T>(sk, ldq, at<T>(p.k, p.k_s, b, 0, h), p.k_s.t, p.K, at<T>(p.kr, p.kr_s, b, 0, 0),
-                 p.kr_s.t, p.R, j0, p.T, p.fours);
-    load_rows<T>(sv, ldv, at<T>(p.v, p.v_s, b, 0, h), p.v_s.t, p.V, (const T *)nullptr, 0, 0, j0, p.T, p.fours);
-    __syncthreads();
+  auto load = [&](int j0, int st) {
+    keys.load(ring + st * stage, ldq, j0, p.T);
+    values.load(ring + st * stage + kBlk * ldq, ldv, j0, p.T);
+  };
+  walk(run_start(p, b, t0) / kBlk * kBlk, last, stages, load, [&](int j0, int st) {
+    const float *sk = ring + st * stage, *sv = sk + kBlk * ldq;
     float s[kRt][4], dp[kRt][4];
     rows_by_rows(sq, ldq, sk, ldq, D, ty, tx, s);
     rows_by_rows(su, ldv, sv, ldv, p.V, ty, tx, dp);
@@ -369,9 +442,8 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_kernel(Prompt p) {
             on ? exp2f(s[i][j] * scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
       }
     __syncwarp();
-    weights_by_rows<3>(sd, sk, ldq, D, ty, tx, acc);
-    __syncwarp();
-  }
+    weights_by_rows(sd, sk, ldq, D, ty, tx, acc);
+  });
 #pragma unroll
   for (int i = 0; i < kRt; ++i) {
     const int t = t0 + kRt * ty + i;
@@ -532,21 +604,27 @@ __global__ void __launch_bounds__(kSmall) rope_sum_kernel(Prompt p) {
   d[3] = from_f32<T>(s.w);
 }
 
+constexpr size_t kMaxSmem = 226 * 1024;
+
+// `held`: rows of a tile's width that stay, beside one or two stages of the other side.
 template <typename K>
-cudaError_t launch_tiles(K kern, const Prompt &p, size_t floats, cudaStream_t cs) {
-  const size_t smem = floats * sizeof(float);
+cudaError_t launch_tiles(K kern, const Prompt &p, size_t held, cudaStream_t cs) {
+  const size_t stage = sizeof(float) * kBlk * (size_t)(p.K + p.R + 4 + p.V + 4);
+  held *= sizeof(float);
+  const int stages = held + 2 * stage <= kMaxSmem ? 2 : 1;
+  const size_t smem = held + stages * stage;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)((p.T + kBlk - 1) / kBlk);
-  kern<<<tiles * p.B * p.H, kThreads, smem, cs>>>(p);
+  kern<<<tiles * p.B * p.H, kThreads, smem, cs>>>(p, stages);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t forward_simt(const Prompt &p, cudaStream_t cs) {
-  const size_t q = (size_t)kBlk * (p.K + p.R + 4), v = (size_t)kBlk * (p.V + 4);
-  return launch_tiles(prompt_fwd_kernel<T>, p, 2 * q + v + kBlk * kLdP, cs);
+  const size_t q = (size_t)kBlk * (p.K + p.R + 4);
+  return launch_tiles(prompt_fwd_kernel<T>, p, q + kBlk * kLdP, cs);
 }
 
 template <typename T>
@@ -560,8 +638,8 @@ cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
   } else {
     const size_t q = (size_t)kBlk * (p.K + p.R + 4), v = (size_t)kBlk * (p.V + 4),
                  w = (size_t)kBlk * kLdP;
-    e = launch_tiles(prompt_dkv_kernel<T>, p, 2 * q + 2 * v + 2 * w, cs);
-    if (e == cudaSuccess) e = launch_tiles(prompt_dq_kernel<T>, p, 2 * q + 2 * v + w, cs);
+    e = launch_tiles(prompt_dkv_kernel<T>, p, q + v + 2 * w, cs);
+    if (e == cudaSuccess) e = launch_tiles(prompt_dq_kernel<T>, p, q + v + w, cs);
   }
   if (e != cudaSuccess || p.R == 0) return e;
   const long long quads = (long long)p.B * p.T * (p.R / 4);
