@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(const Prompt p, in
 template <typename T>
 __global__ void __launch_bounds__(kThreads) prompt_dkv_kernel(const Prompt p, int stages) {
   extern __shared__ __align__(16) float sm[];
+  start_next();
   const int D = p.K + p.R, ldq = D + 4, ldv = p.V + 4;
   float *sk = sm, *sv = sk + kBlk * ldq, *sp = sv + kBlk * ldv, *sd = sp + kBlk * kLdP,
         *ring = sd + kBlk * kLdP;
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_kernel(const Prompt p, int
     if (which & 0xffffu) query_grad_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + i, tid & 31);
     if (which & 0xffff0000u) query_grad_row<T>(p, b, h, t0 + 2 * kRt * (tid >> 5) + kRt + i, tid & 31);
   }
+  if (blockIdx.x == 0) after_previous();
 }
 
 // ---- runs -------------------------------------------------------------------
@@ -608,7 +610,7 @@ constexpr size_t kMaxSmem = 226 * 1024;
 
 // `held`: rows of a tile's width that stay, beside one or two stages of the other side.
 template <typename K>
-cudaError_t launch_tiles(K kern, const Prompt &p, size_t held, cudaStream_t cs) {
+cudaError_t launch_tiles(K kern, const Prompt &p, size_t held, cudaStream_t cs, bool beside = false) {
   const size_t stage = sizeof(float) * kBlk * (size_t)(p.K + p.R + 4 + p.V + 4);
   held *= sizeof(float);
   const int stages = held + 2 * stage <= kMaxSmem ? 2 : 1;
@@ -617,6 +619,7 @@ cudaError_t launch_tiles(K kern, const Prompt &p, size_t held, cudaStream_t cs) 
                                        (int)smem);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)((p.T + kBlk - 1) / kBlk);
+  if (beside) return launch_next(kern, dim3(tiles * p.B * p.H), kThreads, smem, cs, p, stages);
   kern<<<tiles * p.B * p.H, kThreads, smem, cs>>>(p, stages);
   return cudaGetLastError();
 }
@@ -627,6 +630,9 @@ cudaError_t forward_simt(const Prompt &p, cudaStream_t cs) {
   return launch_tiles(prompt_fwd_kernel<T>, p, q + kBlk * kLdP, cs);
 }
 
+// The gradients of the queries need nothing of those of the keys and values: their
+// kernel begins once all CTAs of the other one have begun, on the SMs that these leave.
+// One of its CTAs ends after the other kernel has, so what follows waits for both.
 template <typename T>
 cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
   const long long rows = (long long)p.B * p.T * p.H;
@@ -639,7 +645,7 @@ cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
     const size_t q = (size_t)kBlk * (p.K + p.R + 4), v = (size_t)kBlk * (p.V + 4),
                  w = (size_t)kBlk * kLdP;
     e = launch_tiles(prompt_dkv_kernel<T>, p, q + v + 2 * w, cs);
-    if (e == cudaSuccess) e = launch_tiles(prompt_dq_kernel<T>, p, q + v + w, cs);
+    if (e == cudaSuccess) e = launch_tiles(prompt_dq_kernel<T>, p, q + v + w, cs, true);
   }
   if (e != cudaSuccess || p.R == 0) return e;
   const long long quads = (long long)p.B * p.T * (p.R / 4);

@@ -81,6 +81,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  if (kKeys) start_next();
   const uint32_t tmem = c.tmem;
   volatile int *fail = &c.fail;
 
@@ -349,6 +350,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   tc::tc_fence_after();
   if (tid == 0 && c.fail) set_status(p.status, KDA_DEVICE_TIMEOUT);
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
+  if (!kKeys && blockIdx.x == 0) after_previous();
 }
 
 template <bool kKeys>
@@ -357,7 +359,9 @@ cudaError_t launch(const Maps &m, const Prompt &p, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)((p.T + kOuter - 1) / kOuter);
-  prompt_bwd_tc_kernel<kKeys><<<tiles * (unsigned)(p.B * p.H), kThreads, kSmem, s>>>(m, p);
+  const unsigned grid = tiles * (unsigned)(p.B * p.H);
+  if (!kKeys) return launch_next(prompt_bwd_tc_kernel<kKeys>, dim3(grid), kThreads, kSmem, s, m, p);
+  prompt_bwd_tc_kernel<kKeys><<<grid, kThreads, kSmem, s>>>(m, p);
   return cudaGetLastError();
 }
 
