@@ -21,7 +21,9 @@ constexpr int kTokens = 32;          // tokens in shared memory at once
 constexpr int kLdW = kTokens + 4;
 
 // CUDA cores, fp32.  The 32 rows of queries and 32 tokens lie in shared memory;
-// a warp makes the scores of its 4 rows and their sums over the latents.
+// a warp makes the scores of its 4 rows and their sums over the latents.  The tokens are
+// cut in tiles of 32 (three texts of up to 997 tokens, 24 rows of 160 values: 21 us with
+// the join, with tiles of 128 44); what bounds it is the latency of a tile's steps.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
   extern __shared__ __align__(16) float sm[];
@@ -300,14 +302,15 @@ cudaError_t launch_simt(const Step &p, cudaStream_t cs) {
   return cudaGetLastError();
 }
 
-// Rows with many parts (fewer than 38 sequences and row tiles, so 4 parts or more each
-// where the texts are long) share them among 4 groups: two texts of 131072 tokens,
-// TODO.  More rows take a row each.
+// A row has about 152 / (sequences x row tiles) parts.  From 16 of these on four groups of
+// threads share them (one text of 32768 tokens 20 us, with a group a row 31; four of
+// 16384 22 and 26), with fewer a row has one group (16 texts of 2000 tokens 19 us, with
+// four groups 24; 120 of 4096 126 and 160).
 template <typename T>
 cudaError_t launch_join(const Step &p, cudaStream_t cs) {
   const int cols = p.C / 4;
   const long long rows = (long long)p.B * p.T * p.H;
-  if ((long long)p.B * p.row_tiles * 4 <= kParts)
+  if ((long long)p.B * p.row_tiles * 16 <= kParts)
     return launch_next(join_kernel<T, 4>, dim3((unsigned)rows), (unsigned)(cols * 4), 0, cs, p, 1);
   const int block_rows = 256 / cols;
   return launch_next(join_kernel<T, 1>, dim3((unsigned)((rows + block_rows - 1) / block_rows)), 256u,
@@ -394,6 +397,8 @@ kda_status kda_latent_step(const kda_latent_cache *s, const void *q, const void 
   if (impl == KDA_IMPL_TC && !can) return KDA_ERR_UNSUPPORTED;
   const bool tc = can && impl != KDA_IMPL_SIMT;
   p.tile = tc ? 128 : kTokens;
+  // (120 texts of up to 8192 tokens: 158 us with 0, 147 with 1, 134 with 2, 128 with 3, 131
+  // with 5; two of 131072 81 to 83)
   p.extra = 3;
   cudaError_t e = tc ? launch_step_tc(p, cs)
                   : bf16 ? launch_simt<__nv_bfloat16>(p, cs)
