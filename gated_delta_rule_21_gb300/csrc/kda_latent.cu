@@ -636,10 +636,13 @@ cudaError_t forward_simt(const Prompt &p, cudaStream_t cs) {
 // One of its CTAs ends after the other kernel has, so what follows waits for both.
 template <typename T>
 cudaError_t backward(const Prompt &p, bool tc, cudaStream_t cs) {
-  const long long rows = (long long)p.B * p.T * p.H;
-  delta_kernel<T><<<(unsigned)((rows + kSmall / 8 - 1) / (kSmall / 8)), kSmall, 0, cs>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!tc || p.T > kExactKeys) {     // (the tensor cores' path makes the rest by itself)
+    const long long rows = (long long)p.B * p.T * p.H;
+    delta_kernel<T><<<(unsigned)((rows + kSmall / 8 - 1) / (kSmall / 8)), kSmall, 0, cs>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (tc) {
     e = launch_prompt_bwd_tc(p, cs);
   } else {

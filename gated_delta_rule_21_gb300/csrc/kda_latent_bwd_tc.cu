@@ -3,7 +3,7 @@
 //
 // With D_i = d_o_i . o_i, p_ij = exp(s_ij - lse_i) and ds_ij = p_ij (d_o_i . v_j - D_i):
 //     dv_j = sum_i p_ij d_o_i,   dk_j = scale sum_i ds_ij q_i,   dq_i = scale sum_j ds_ij k_j
-// Two kernels of one shape, which make s and ds twice so that every sum stays in
+// Two kernels of one shape (and a third for D of queries with few keys), which make s and ds twice so that every sum stays in
 // one CTA's tensor memory: no atomics, no sums in global memory but the heads' parts of
 // dk_rope.  A CTA holds 128 rows of one side of one head (keys and values, or queries
 // and d_o) and walks the other side in tiles of 64:
@@ -42,10 +42,18 @@ struct Control {
   float stat[8][2][32];
 };
 
-// kKeys: the rows are keys (dk, dv), else queries (dq).
-template <bool kKeys>
+// What a launch makes.  kDelta: D of queries that see at most kExact tiles of keys, as
+// sum_j p_ij (d_o_i . v_j) / sum_j p_ij.  D from the stored o has o's rounding, whose part of
+// ds = p (dp - D) is the larger the fewer keys a query sees (dq and dk of rows of 40
+// tokens 2.9e-3 off in the 2-norm, with this 2.3e-3, 1.7e-3 of it their own rounding; of
+// 1000 tokens 2.6e-3 and 2.3e-3).
+enum What { kKeysOf, kQueriesOf, kDelta };
+constexpr int kExact = kExactKeys / kInner;
+
+template <What kWhat>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
+  constexpr bool kKeys = kWhat == kKeysOf;
   extern __shared__ __align__(1024) unsigned char raw[];
   unsigned char *smem = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
   Control &c = *reinterpret_cast<Control *>(smem + kOffC);
@@ -63,6 +71,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   const int first = kKeys ? t0 / kInner : run_start(p, b, t0) / kInner;
   const int stop = kKeys ? (run_end(p, b, t_last) + kInner - 1) / kInner : t_last / kInner + 1;
   const int n = stop > first ? stop - first : 0;
+  if (kWhat == kDelta && n > kExact) return;
   auto bar = [](uint64_t &x) { return tc::smem_u32(&x); };
   if (tid == 0) {
     tc::mbar_init(bar(c.x_full), 1);
@@ -175,20 +184,22 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           dp(i + 1);
           tc::mma_commit(bar(c.s_full));
         }
-        // steps of 16 rows of Y: the two halves of 32 stand 32 columns apart
-        const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
-        const uint32_t w = tmem + kInner * (i & 1), old = i > 0 ? 1u : 0u;
-        const uint64_t dy = swizzled_desc(y, kYChunkB);
-        if (kKeys) {
+        if (kWhat != kDelta) {
+          // steps of 16 rows of Y: the two halves of 32 stand 32 columns apart
+          const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
+          const uint32_t w = tmem + kInner * (i & 1), old = i > 0 ? 1u : 0u;
+          const uint64_t dy = swizzled_desc(y, kYChunkB);
+          if (kKeys) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma_bf16_ts(tmem + kTX2, w + 32 * (e >> 1) + 8 * (e & 1),
+                          dy + 3 * kYChunkB / 16 + kStepRows * e, id_x2, e > 0 ? 1u : old);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mma_bf16_ts(tmem + kTX2, w + 32 * (e >> 1) + 8 * (e & 1),
-                        dy + 3 * kYChunkB / 16 + kStepRows * e, id_x2, e > 0 ? 1u : old);
+            mma_bf16_ts(tmem + kTX1, w + 16 + 32 * (e >> 1) + 8 * (e & 1), dy + kStepRows * e, id_x1,
+                        e > 0 ? 1u : old);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_bf16_ts(tmem + kTX1, w + 16 + 32 * (e >> 1) + 8 * (e & 1), dy + kStepRows * e, id_x1,
-                      e > 0 ? 1u : old);
         tc::mma_commit(bar(c.y_empty[i % kStages]));
       }
       if (ok) tc::mma_commit(bar(c.done));
@@ -223,8 +234,9 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       if (n > 0) fetch(0);
     } else if (row < p.T) {
       lse = p.lse[head + row] * kLog2e;
-      delta = p.delta[head + row];
+      if (kWhat == kQueriesOf) delta = p.delta[head + row];
     }
+    u64 sum_w = 0, sum_g = 0;           // of p and p dp
     for (int i = 0; i < n; ++i) {
       const int y0 = (first + i) * kInner + 32 * half;
       float2 st[16], de[16];
@@ -280,69 +292,90 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           w1 = on1 ? w1 : 0.f;
           g1 = on1 ? g1 : 0.f;
         }
+        if (kWhat == kDelta) {
+          sum_w = add2(sum_w, pk2(w0, w1));
+          sum_g = add2(sum_g, pk2(g0, g1));
+        }
         pw[e] = tc::pack_bf16(w0, w1);
         dw[e] = tc::pack_bf16(g0, g1);
       }
-      if (kKeys) tmem_st16(t_s, pw);
-      tmem_st16(t_s + 16, dw);
-      tmem_wait_st();
+      if (kWhat != kDelta) {
+        if (kKeys) tmem_st16(t_s, pw);
+        tmem_st16(t_s + 16, dw);
+        tmem_wait_st();
+      }
       tc::tc_fence_before();
       tc::mbar_arrive(bar(c.ds_ready));
     }
-    // ---- the sums, 32 columns at a time, the halves in turn ----
-    if (n > 0) {
-      wait_or_fail(bar(c.done), 0, fail);
-      __syncwarp();
-      tc::tc_fence_after();
-    }
-    bool bad = false;
-    const size_t at_row = ((size_t)b * p.T + row) * p.H + h;
-    for (int q = half; q < 2 * nc + (kKeys ? 2 * nv : 0); q += 2) {
-      const bool is_x2 = q >= 2 * nc, is_rope = !is_x2 && q >= 2 * nk;
-      const int col = 32 * (is_x2 ? q - 2 * nc : is_rope ? q - 2 * nk : q);
-      const int width = is_x2 ? p.V : is_rope ? p.R : p.K;
-      uint32_t x[32];
+    if (kWhat == kDelta) {
+      if (n > 0) wait_or_fail(bar(c.done), 0, fail);
+      float a, d;
+      upk2(sum_w, a, d);
+      c.stat[warp][0][lane] = a + d;
+      upk2(sum_g, a, d);
+      c.stat[warp][1][lane] = a + d;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (half == 0 && row < p.T) {
+        const float w = c.stat[warp][0][lane] + c.stat[warp + 4][0][lane];
+        const float g = c.stat[warp][1][lane] + c.stat[warp + 4][1][lane];
+        if (w != 0.f) const_cast<float *>(p.delta)[head + row] = g / w;
+      }
+    } else {
+      // ---- the sums, 32 columns at a time, the halves in turn ----
       if (n > 0) {
-        tmem_ld32_wait(tmem + lanes + (is_x2 ? kTX2 + 32 * (q - 2 * nc) : kTX1 + 32 * q), x);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0;
+        wait_or_fail(bar(c.done), 0, fail);
+        __syncwarp();
+        tc::tc_fence_after();
       }
-      if (col < width && row < p.T) {
-        const float f = is_x2 ? 1.f : p.scale;
-        float y[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          y[i] = __uint_as_float(x[i]) * f;
-          bad |= !finite(y[i]);
-        }
-        if (kKeys && is_rope) {
-          float4 *o = reinterpret_cast<float4 *>(p.dkr_part + at_row * p.R + col);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      bool bad = false;
+      const size_t at_row = ((size_t)b * p.T + row) * p.H + h;
+      for (int q = half; q < 2 * nc + (kKeys ? 2 * nv : 0); q += 2) {
+        const bool is_x2 = q >= 2 * nc, is_rope = !is_x2 && q >= 2 * nk;
+        const int col = 32 * (is_x2 ? q - 2 * nc : is_rope ? q - 2 * nk : q);
+        const int width = is_x2 ? p.V : is_rope ? p.R : p.K;
+        uint32_t x[32];
+        if (n > 0) {
+          tmem_ld32_wait(tmem + lanes + (is_x2 ? kTX2 + 32 * (q - 2 * nc) : kTX1 + 32 * q), x);
         } else {
-          void *base = is_x2 ? p.dv : kKeys ? p.dk : is_rope ? p.dqr : p.dq;
-          uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at_row * width + col);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = make_uint4(tc::pack_bf16(y[8 * i], y[8 * i + 1]),
-                              tc::pack_bf16(y[8 * i + 2], y[8 * i + 3]),
-                              tc::pack_bf16(y[8 * i + 4], y[8 * i + 5]),
-                              tc::pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+          for (int i = 0; i < 32; ++i) x[i] = 0;
         }
+        if (col < width && row < p.T) {
+          const float f = is_x2 ? 1.f : p.scale;
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            y[i] = __uint_as_float(x[i]) * f;
+            bad |= !finite(y[i]);
+          }
+          if (kKeys && is_rope) {
+            float4 *o = reinterpret_cast<float4 *>(p.dkr_part + at_row * p.R + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else {
+            void *base = is_x2 ? p.dv : kKeys ? p.dk : is_rope ? p.dqr : p.dq;
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(base) + at_row * width + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[i] = make_uint4(tc::pack_bf16(y[8 * i], y[8 * i + 1]),
+                                tc::pack_bf16(y[8 * i + 2], y[8 * i + 3]),
+                                tc::pack_bf16(y[8 * i + 4], y[8 * i + 5]),
+                                tc::pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    const unsigned which = __ballot_sync(0xffffffffu, bad);
-    if (lane == 0) c.bad[warp] = which;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    // rows that were not finite, again: 16 of each 32 by either half
-    unsigned again = (c.bad[warp & 3] | c.bad[(warp & 3) + 4]) & (half ? 0xffff0000u : 0xffffu);
-    for (; again; again &= again - 1) {
-      const int r = row - lane + __ffs(again) - 1;
-      if (kKeys) key_grad_row<__nv_bfloat16>(p, b, h, r, lane);
-      else query_grad_row<__nv_bfloat16>(p, b, h, r, lane);
+      const unsigned which = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) c.bad[warp] = which;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // rows that were not finite, again: 16 of each 32 by either half
+      unsigned again = (c.bad[warp & 3] | c.bad[(warp & 3) + 4]) & (half ? 0xffff0000u : 0xffffu);
+      for (; again; again &= again - 1) {
+        const int r = row - lane + __ffs(again) - 1;
+        if (kKeys) key_grad_row<__nv_bfloat16>(p, b, h, r, lane);
+        else query_grad_row<__nv_bfloat16>(p, b, h, r, lane);
+      }
     }
   }
   tc::tc_fence_before();
@@ -350,18 +383,19 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   tc::tc_fence_after();
   if (tid == 0 && c.fail) set_status(p.status, KDA_DEVICE_TIMEOUT);
   if (warp == 9) tc::tmem_dealloc(tmem, 512);
-  if (!kKeys && blockIdx.x == 0) after_previous();
+  if (kWhat == kQueriesOf && blockIdx.x == 0) after_previous();
 }
 
-template <bool kKeys>
+template <What kWhat>
 cudaError_t launch(const Maps &m, const Prompt &p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(prompt_bwd_tc_kernel<kKeys>,
+  cudaError_t e = cudaFuncSetAttribute(prompt_bwd_tc_kernel<kWhat>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)((p.T + kOuter - 1) / kOuter);
   const unsigned grid = tiles * (unsigned)(p.B * p.H);
-  if (!kKeys) return launch_next(prompt_bwd_tc_kernel<kKeys>, dim3(grid), kThreads, kSmem, s, m, p);
-  prompt_bwd_tc_kernel<kKeys><<<grid, kThreads, kSmem, s>>>(m, p);
+  if (kWhat == kQueriesOf)
+    return launch_next(prompt_bwd_tc_kernel<kWhat>, dim3(grid), kThreads, kSmem, s, m, p);
+  prompt_bwd_tc_kernel<kWhat><<<grid, kThreads, kSmem, s>>>(m, p);
   return cudaGetLastError();
 }
 
@@ -386,8 +420,9 @@ cudaError_t launch_prompt_bwd_tc(const Prompt &p, cudaStream_t s) {
               !prompt_map(&queries.x1r, p.qr, p.qr_s, p, p.H, p.R, kOuter) ||
               !prompt_map(&queries.y1r, p.kr, p.kr_s, p, 1, p.R, kInner)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = launch<true>(keys, p, s);
-  return e != cudaSuccess ? e : launch<false>(queries, p, s);
+  cudaError_t e = launch<kDelta>(queries, p, s);
+  if (e == cudaSuccess) e = launch<kKeysOf>(keys, p, s);
+  return e != cudaSuccess ? e : launch<kQueriesOf>(queries, p, s);
 }
 
 }  // namespace latent
