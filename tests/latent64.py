@@ -69,7 +69,7 @@ def prompt(x, scale, seg=None, impl="simt", dtype=torch.float32, d_o=None):
         e = w * ds.abs() + p * (off + 1e-6 * (up.abs() @ v.abs().transpose(-1, -2)))
         et = e.transpose(-1, -2)
         dq, dk = scale * ds @ k, scale * ds.transpose(-1, -2) @ q
-        eq, ek = scale * e @ k.abs(), scale * et @ q.abs()
+        eq, ek = abs(scale) * e @ k.abs(), abs(scale) * et @ q.abs()
         for n, a, b in (("dq", dq, eq), ("dk", dk, ek)):
             got[n] = (a[..., :K], half * a[..., :K].abs() + b[..., :K])
         if q.shape[-1] > K:

@@ -43,6 +43,8 @@ def expect(q, q_rope, cache, table, lengths, new, scale, impl, dtype):
         if n == 0:
             continue
         tokens, there = gathered(cache, table, b, int(lengths[b]))
+        if len(tokens) == 0:
+            continue
         seen = (int(lengths[b]) - n + 1 + torch.arange(T)).clamp(max=tokens.shape[0])
         seen[n:] = 0
         got = latent64.step(q[b].double(), None if q_rope is None else q_rope[b].double(), tokens,
