@@ -27,7 +27,7 @@ constexpr uint32_t kXChunkB = kOuter * kRowBytes, kYChunkB = kInner * kRowBytes;
 constexpr uint32_t kStageB = 5 * kYChunkB;
 constexpr uint32_t kOffY = 5 * kXChunkB, kOffC = kOffY + kStages * kStageB;
 constexpr uint32_t kSmem = kOffC + 4096 + 1024;
-constexpr int kThreads = 320;                  // 8 warps of rows, copies, products
+constexpr int kThreads = 384;                  // 8 warps of rows; copies, products and two idle warps
 constexpr uint32_t kTdP = 128, kTX1 = 192, kTX2 = 384;   // columns
 
 struct Maps {
@@ -94,7 +94,9 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   const uint32_t tmem = c.tmem;
   volatile int *fail = &c.fail;
 
-  if (warp == 8) {
+  if (warp >= 8) {
+    few_registers();
+    if (warp == 8) {
     // ---- copies: one thread ----
     if (lane == 0 && n > 0) {
       // (keys' rope part is shared by the heads)
@@ -132,7 +134,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+    } else if (warp == 9) {
     // ---- products: one thread ----
     if (n > 0 && elect_one()) {
       const uint32_t id_s = tc::idesc_bf16(kOuter, kInner, 0, 0),
@@ -209,7 +211,9 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       }
     }
     __syncwarp();
+    }
   } else {
+    many_registers();
     // ---- rows: two threads a row, 32 columns each ----
     const int half = warp >> 2, row = t0 + (tid & 127);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -246,15 +250,6 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         c.stat[warp][1][lane] = -next_delta;
         __syncwarp();
         if (i + 1 < n) fetch(i + 1);
-      }
-      wait_or_fail(bar(c.s_full), (uint32_t)i & 1, fail);
-      __syncwarp();
-      tc::tc_fence_after();
-      uint32_t s[32], d[32];
-      const uint32_t t_s = tmem + kInner * (i & 1) + 32 * half + lanes;
-      tmem_ld32_nw(t_s, s);
-      tmem_ld32_nw(tmem + kTdP + 32 * half + lanes, d);
-      if (kKeys) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 a = reinterpret_cast<const float4 *>(c.stat[warp][0])[e];
@@ -265,6 +260,13 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           de[2 * e + 1] = make_float2(g.z, g.w);
         }
       }
+      wait_or_fail(bar(c.s_full), (uint32_t)i & 1, fail);
+      __syncwarp();
+      tc::tc_fence_after();
+      uint32_t s[32], d[32];
+      const uint32_t t_s = tmem + kInner * (i & 1) + 32 * half + lanes;
+      tmem_ld32_nw(t_s, s);
+      tmem_ld32_nw(tmem + kTdP + 32 * half + lanes, d);
       tc::tmem_wait_ld();
       reg_fence32(s);
       reg_fence32(d);

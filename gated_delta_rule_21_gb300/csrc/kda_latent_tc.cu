@@ -31,15 +31,6 @@ struct Maps {
   CUtensorMap q, qr, k, kr, v;
 };
 
-// The launch's 384 threads have 168 registers each (504 of three warpgroups); the two
-// that work on rows take 216, the third keeps 72: 504.
-__device__ __forceinline__ void few_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-}
-__device__ __forceinline__ void many_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-}
-
 // Key tiles [lo, hi) that a query tile sees.
 struct Range {
   int lo, hi;

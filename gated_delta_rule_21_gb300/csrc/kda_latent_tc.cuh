@@ -109,6 +109,15 @@ struct Slot {
   }
 };
 
+// The launch's 384 threads have 168 registers each (504 of three warpgroups); the two
+// that work on rows take 216, the third keeps 72: 504.
+__device__ __forceinline__ void few_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+}
+__device__ __forceinline__ void many_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+}
+
 // Columns [from, to) of 32 that begin at `at`, as bits.
 __device__ __forceinline__ uint32_t column_bits(int from, int to, int at) {
   const int a = min(max(from - at, 0), 32), z = min(max(to - at, 0), 32);
