@@ -747,8 +747,8 @@ KDA_API kda_status kda_latent_append(const kda_latent_cache *s, const void *late
  * The absorbed form over the cache, which holds the new tokens already.
  *   q             device [B,T,H,C], q_rope [B,T,H,R] (NULL when R = 0), the last
  *                 dimension contiguous.  Rows of a projection's output serve.
- *   o             device [B,T,H,C] contiguous, of s->dtype; 0 for a token that
- *                 is not there or sees nothing.
+ *   o             device [B,T,H,C] contiguous, of s->dtype, 16-byte aligned; 0 for a
+ *                 token that is not there or sees nothing.  It must not alias an input.
  *   lse           device float32 [B,H,T] or NULL: log sum_j exp(s_ij), -inf for
  *                 those tokens.
  *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores, every type and layout.
@@ -779,13 +779,15 @@ KDA_API kda_status kda_latent_step(const kda_latent_cache *s, const void *q, con
  *                 the others at the shape's strides: slices of projections serve.
  *   segment_ids   as kda_chunk_fwd: a token sees those of its own run up to
  *                 itself; padding (id 0) sees nothing, its o is 0.
- *   o             device [B,T,H,V] contiguous, of s->dtype.
+ *   o             device [B,T,H,V] contiguous, of s->dtype, 16-byte aligned.  It must
+ *                 not alias an input.
  *   lse           device float32 [B,H,T] or NULL: log sum_j exp(s_ij) (-inf for
  *                 padding), which the backward reads.
  *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores, every type and layout.
  *                 KDA_IMPL_TC: the tensor cores (bf16; p and the gradient of s are
  *                 rounded to bf16, sums and statistics fp32); pointers 16-byte
- *                 aligned and strides multiples of 8 (KDA_ERR_ALIGNMENT).
+ *                 aligned, strides positive multiples of 8 (KDA_ERR_ALIGNMENT), a scale
+ *                 that is not negative (KDA_ERR_UNSUPPORTED).
  *                 KDA_IMPL_AUTO: TC where that holds, else SIMT.
  *   workspace     device, kda_latent_workspace_size bytes, 256-byte aligned,
  *                 its first 256 bytes zero-filled before its first use.  Calls
@@ -813,7 +815,8 @@ KDA_API kda_status kda_latent_fwd(const kda_latent_shape *s, const void *q, cons
  * The gradients, from the inputs, the forward's o and lse, and the gradient of o.
  *   o, d_o        device [B,T,H,V] contiguous, of s->dtype.
  *   dq, dk, dv, dq_rope, dk_rope   device, contiguous, of s->dtype, the shapes of
- *                 q, k, v, q_rope, k_rope; dk_rope is the sum over the heads.
+ *                 q, k, v, q_rope, k_rope; dk_rope is the sum over the heads.  All seven
+ *                 are 16-byte aligned; none of the outputs aliases an input.
  * Padding tokens get zeros.  No atomics: repeated calls agree bit for bit.
  * workspace as above, of kda_latent_workspace_size(s, 1) bytes.
  */

@@ -91,8 +91,8 @@ COMMON = [
     (dict(kr=None), 1), (dict(R=0), 1), (dict(scale=float("nan")), 1), (dict(impl=3), 1),
     (dict(B=0), 1), (dict(T=0), 1), (dict(H=0), 1), (dict(dtype=2), 1), (dict(K=96), 2),
     (dict(V=256), 2), (dict(R=16), 2), (dict(B=1 << 10, T=1 << 14, H=1), 2),
-    (dict(impl=2, dtype=0), 2), (dict(q=FAKE + 1), 3), (dict(o=FAKE + 8), 3),
-    (dict(lse=FAKE + 2), 3), (dict(impl=2, q=FAKE + 2), 3), (dict(impl=2, qt=515), 3),
+    (dict(impl=2, dtype=0), 2), (dict(impl=2, scale=-0.1), 2), (dict(q=FAKE + 1), 3),
+    (dict(o=FAKE + 8), 3), (dict(lse=FAKE + 2), 3), (dict(impl=2, q=FAKE + 2), 3), (dict(impl=2, qt=515), 3),
     (dict(seg=FAKE + 2), 3), (dict(ws=FAKE + 64), 3), (dict(ws=None), 4), (dict(nbytes=255), 4)]
 
 
