@@ -65,7 +65,8 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   Control &c = *reinterpret_cast<Control *>(smem + kOffC);
   const uint32_t s0 = tc::smem_u32(smem);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-  const int tiles = (p.T + kOuter - 1) / kOuter;
+  int tiles = (p.T + kOuter - 1) / kOuter;
+  if (kWhat == kDelta && !p.start) tiles = min(tiles, kExactKeys / kOuter);
   // one head after another, its longest rows first
   const int bh = (int)(blockIdx.x / (unsigned)tiles), order = (int)(blockIdx.x % (unsigned)tiles);
   const int t0 = (kKeys ? order : tiles - 1 - order) * kOuter;
@@ -399,7 +400,8 @@ cudaError_t launch(const Maps &m, const Prompt &p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(prompt_bwd_tc_kernel<kWhat>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned tiles = (unsigned)((p.T + kOuter - 1) / kOuter);
+  unsigned tiles = (unsigned)((p.T + kOuter - 1) / kOuter);
+  if (kWhat == kDelta && !p.start && tiles > kExactKeys / kOuter) tiles = kExactKeys / kOuter;
   const unsigned grid = tiles * (unsigned)(p.B * p.H);
   if (kWhat == kQueriesOf)
     return launch_next(prompt_bwd_tc_kernel<kWhat>, dim3(grid), kThreads, kSmem, s, m, p);
