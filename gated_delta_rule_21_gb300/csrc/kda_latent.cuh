@@ -81,7 +81,8 @@ __device__ __forceinline__ float score(const Prompt &p, int b, int h, int i, int
 
 // The tiles multiply masked weights of 0 with what stands there, and 0 times
 // infinity is NaN.  A row whose sum came out not finite is made again by these,
-// key by key over what it sees; a row that is not finite by itself stays so.
+// key by key over what it sees; a row that is not finite by itself stays so (and is done
+// with at its first weight that is NaN).
 // One warp a row; V, K <= 128, R <= 64.
 template <typename T>
 __device__ __noinline__ void forward_row(const Prompt &p, int b, int h, int i, int lane) {
@@ -96,6 +97,7 @@ __device__ __noinline__ void forward_row(const Prompt &p, int b, int h, int i, i
     for (int e = 0; e < 4; ++e)
       if (lane + 32 * e < p.V) acc[e] = acc[e] * c + w * to_f32(v[lane + 32 * e]);
     m = mn;
+    if (l != l) break;      // so is everything from here on
   }
   T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + i) * p.H + h) * p.V;
 #pragma unroll
@@ -127,6 +129,7 @@ __device__ __noinline__ void query_grad_row(const Prompt &p, int b, int h, int i
       const int c = lane + 32 * e;
       if (c < p.K + p.R) acc[e] += ds * to_f32(c < p.K ? k[c] : kr[c - p.K]);
     }
+    if (ds != ds) break;
   }
   const size_t row = ((size_t)b * p.T + i) * p.H + h;
   T *dq = static_cast<T *>(p.dq) + row * p.K, *dqr = static_cast<T *>(p.dqr) + row * p.R;
@@ -155,6 +158,7 @@ __device__ __noinline__ void key_grad_row(const Prompt &p, int b, int h, int j, 
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (lane + 32 * e < p.V) av[e] += w * to_f32(up[lane + 32 * e]);
+    if (w != w) break;
   }
   const size_t row = ((size_t)b * p.T + j) * p.H + h;
   T *dk = static_cast<T *>(p.dk) + row * p.K, *dv = static_cast<T *>(p.dv) + row * p.V;
@@ -367,6 +371,7 @@ __device__ __noinline__ void step_row(const Step &p, int b, int r, int n, int la
     for (int e = 0; e < 16; ++e)
       if (lane + 32 * e < p.C) acc[e] = acc[e] * f + w * to_f32(c[lane + 32 * e]);
     m = mn;
+    if (l != l) break;
   }
   T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.C;
 #pragma unroll

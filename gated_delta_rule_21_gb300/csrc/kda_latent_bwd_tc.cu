@@ -17,7 +17,7 @@
 // Shared memory (200 KB): 5 chunks of 16 KB of X, 3 stages of 5 chunks of 8 KB of Y.
 // Tensor memory: S twice and dP of 64 columns, dX1 192, dX2 128.
 //
-// A row of 8192 tokens, 32 heads of 128 + 64: keys and values 910 us, queries 890, D 43 (with
+// A row of 8192 tokens, 32 heads of 128 + 64: keys and values 910 us, queries 886, D 34 (with
 // fewer registers, and what a column needs read after the wait, 1050 and 905).  What bounds
 // them: the products (44 cycles an instruction of N 64: 1400 of 1800 cycles a tile) and the
 // tiles of the other side, which come from L2 at 6 to 7 TB/s.
@@ -99,7 +99,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   tc::tc_fence_after();
   if (kKeys) start_next();
   const uint32_t tmem = c.tmem;
-  volatile int *fail = &c.fail;
+  const Waits wait(&c.fail, p.T);
 
   if (warp >= 8) {
     few_registers();
@@ -121,7 +121,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % kStages, y0 = (first + i) * kInner;
-        ok = wait_or_fail(bar(c.y_empty[s]), (uint32_t)(i / kStages + 1) & 1, fail);
+        ok = wait(bar(c.y_empty[s]), (uint32_t)(i / kStages + 1) & 1);
         if (!ok) break;
         const uint32_t d = s0 + kOffY + (uint32_t)s * kStageB;
         tc::mbar_expect_tx(bar(c.y_full[s]), (uint32_t)(nc + nv) * kYChunkB);
@@ -134,7 +134,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           tma_load_4d(d + (uint32_t)(3 + e) * kYChunkB, &maps.y2, e * kChunkCols, h, y0, b,
                       bar(c.y_full[s]));
       }
-      if (*fail) {   // what is on its way comes in before the CTA ends
+      if (c.fail) {   // what is on its way comes in before the CTA ends
         tc::mbar_wait(bar(c.x_full), 0);
         for (int k = max(0, i - kStages); k < i; ++k)
           tc::mbar_wait(bar(c.y_full[k % kStages]), (uint32_t)(k / kStages) & 1);
@@ -172,9 +172,9 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         }
       };
       auto loaded = [&](int i) {
-        return wait_or_fail(bar(c.y_full[i % kStages]), (uint32_t)(i / kStages) & 1, fail);
+        return wait(bar(c.y_full[i % kStages]), (uint32_t)(i / kStages) & 1);
       };
-      bool ok = wait_or_fail(bar(c.x_full), 0, fail) && loaded(0);
+      bool ok = wait(bar(c.x_full), 0) && loaded(0);
       if (ok) {
         scores(0);
         dp(0);
@@ -186,7 +186,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           if (!ok) break;
           scores(i + 1);
         }
-        ok = wait_or_fail(bar(c.ds_ready), (uint32_t)i & 1, fail);
+        ok = wait(bar(c.ds_ready), (uint32_t)i & 1);
         if (!ok) break;
         tc::tc_fence_after();
         if (i + 1 < n) {
@@ -212,7 +212,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         tc::mma_commit(bar(c.y_empty[i % kStages]));
       }
       if (ok) tc::mma_commit(bar(c.done));
-      if (*fail) {
+      if (c.fail) {
         tc::mma_commit(bar(c.drain));
         tc::mbar_wait(bar(c.drain), 0);
       }
@@ -267,7 +267,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           de[2 * e + 1] = make_float2(g.z, g.w);
         }
       }
-      wait_or_fail(bar(c.s_full), (uint32_t)i & 1, fail);
+      wait(bar(c.s_full), (uint32_t)i & 1);
       __syncwarp();
       tc::tc_fence_after();
       uint32_t s[32], d[32];
@@ -317,7 +317,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       tc::mbar_arrive(bar(c.ds_ready));
     }
     if (kWhat == kDelta) {
-      if (n > 0) wait_or_fail(bar(c.done), 0, fail);
+      if (n > 0) wait(bar(c.done), 0);
       float a, d;
       upk2(sum_w, a, d);
       c.stat[warp][0][lane] = a + d;
@@ -332,7 +332,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
     } else {
       // ---- the sums, 32 columns at a time, the halves in turn ----
       if (n > 0) {
-        wait_or_fail(bar(c.done), 0, fail);
+        wait(bar(c.done), 0);
         __syncwarp();
         tc::tc_fence_after();
       }

@@ -119,7 +119,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
   start_next();
   const uint32_t tmem = c.tmem, t_o = tmem + 2 * kRows;
   const bool rope = p.R > 0;
-  volatile int *fail = &c.fail;
+  const Waits wait(&c.fail, (long long)p.max_pages * p.page);
   Segment g{};
 
   if (warp == 8) {
@@ -147,7 +147,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         const int in_page = t0 & (p.page - 1);
         // the first pair, the rope chunk, the other pairs
         for (int k = 0; k < ring.npair; ++k) {
-          ok = __all_sync(0xffffffffu, wait_or_fail(bar(c.empty[pr.at]), pr.lap ^ 1u, fail));
+          ok = __all_sync(0xffffffffu, wait(bar(c.empty[pr.at]), pr.lap ^ 1u));
           if (!ok) break;
           const uint32_t full = bar(c.full[pr.at]);
           if (lane == 0) tc::mbar_expect_tx(full, 2 * bytes);
@@ -169,7 +169,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
             for (int x = 0; x < p.C + p.R; x += kChunkCols)
               tma_prefetch_3d(&map, x, (t0 + kTile) & (p.page - 1), next);
           if (!rope) continue;
-          ok = __all_sync(0xffffffffu, wait_or_fail(bar(c.rempty[rr.at]), rr.lap ^ 1u, fail));
+          ok = __all_sync(0xffffffffu, wait(bar(c.rempty[rr.at]), rr.lap ^ 1u));
           if (!ok) break;
           const uint32_t rfull = bar(c.rfull[rr.at]);
           if (lane == 0) tc::mbar_expect_tx(rfull, bytes);
@@ -182,7 +182,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         }
       }
     }
-    if (*fail) {   // what is on its way comes in before the CTA ends
+    if (c.fail) {   // what is on its way comes in before the CTA ends
       auto drain = [](uint64_t *full, Slot s, int slots, int n) {
         for (; n > 0; --n) {               // the last n, from the latest back
           if (--s.at < 0) {
@@ -212,7 +212,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
       uint32_t nt = 0, ns = 0;
       bool ok = true;
       while (ok && cur.next(p, g)) {
-        ok = wait_or_fail(bar(c.q_ready), ns & 1, fail);
+        ok = wait(bar(c.q_ready), ns & 1);
         ++ns;
         tc::tc_fence_after();
         // S of the next tile begins (its first pair and its rope chunk) while the
@@ -220,13 +220,13 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         Slot in = pr;
         auto begin = [&](uint32_t t) {
           const uint32_t t_s = tmem + (t & 1) * kRows;
-          if (!wait_or_fail(bar(c.full[in.at]), in.lap, fail)) return false;
+          if (!wait(bar(c.full[in.at]), in.lap)) return false;
           const uint32_t a = s_ring + (uint32_t)in.at * kPairB;
           chunk(t_s, a, dq0, 0u);
           chunk(t_s, a + kChunkB, dq0 + kQChunkB / 16, 1u);
           in.next(ring.pairs);
           if (!rope) return true;
-          if (!wait_or_fail(bar(c.rfull[rr.at]), rr.lap, fail)) return false;
+          if (!wait(bar(c.rfull[rr.at]), rr.lap)) return false;
           chunk(t_s, s_rope + (uint32_t)rr.at * kChunkB,
                 dq0 + (uint64_t)(2 * ring.npair) * (kQChunkB / 16), 1u);
           tc::mma_commit(bar(c.rempty[rr.at]));
@@ -237,7 +237,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         for (int i = 0; ok && i < g.n; ++i, ++nt) {
           const uint32_t t_s = tmem + (nt & 1) * kRows;
           for (int k = 1; k < ring.npair; ++k) {
-            ok = wait_or_fail(bar(c.full[in.at]), in.lap, fail);
+            ok = wait(bar(c.full[in.at]), in.lap);
             if (!ok) break;
             const uint32_t a = s_ring + (uint32_t)in.at * kPairB;
             const uint64_t dq = dq0 + (uint64_t)(2 * k) * (kQChunkB / 16);
@@ -248,7 +248,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           if (!ok) break;
           tc::mma_commit(bar(c.s_full[nt & 1]));
           if (i + 1 < g.n) ok = begin(nt + 1);
-          ok = ok && wait_or_fail(bar(c.p_ready), nt & 1, fail);
+          ok = ok && wait(bar(c.p_ready), nt & 1);
           if (!ok) break;
           tc::tc_fence_after();
           const uint32_t old = i > 0 ? 1u : 0u;
@@ -264,7 +264,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           tc::mma_commit(bar(c.o_done));
         }
       }
-      if (*fail) {
+      if (c.fail) {
         tc::mma_commit(bar(c.drain));
         tc::mbar_wait(bar(c.drain), 0);
       }
@@ -332,7 +332,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         int pg = -1;
         if (k < g.s.held) pg = p.table[(size_t)g.b * p.max_pages + (k >> log_page)];
         const bool there = pg >= 0 && pg < p.n_pages;
-        wait_or_fail(bar(c.s_full[nt & 1]), (nt >> 1) & 1, fail);
+        wait(bar(c.s_full[nt & 1]), (nt >> 1) & 1);
         __syncwarp();
         tc::tc_fence_after();
         float v[kMine], w[kMine];
@@ -353,7 +353,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
                                 fmaxf(c.top[2][mc], c.top[3][mc]));
         const bool over = top > mine + kSlack;
         // O^T of the tile before has read P, and its sums stand still
-        if (i > 0) wait_or_fail(bar(c.o_done), (nt - 1) & 1, fail);
+        if (i > 0) wait(bar(c.o_done), (nt - 1) & 1);
         __syncwarp();
         if (__any_sync(0xffffffffu, over)) {
           const float now = fmaxf(mine, top);
@@ -399,7 +399,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           const uint4 zero = make_uint4(0, 0, 0, 0);
           Slot in = pr;
           for (int m = 0; m < ring.npair; ++m) {
-            wait_or_fail(bar(c.full[in.at]), in.lap, fail);
+            wait(bar(c.full[in.at]), in.lap);
             unsigned char *d = smem + (uint32_t)in.at * kPairB + (uint32_t)half * kChunkB +
                                (uint32_t)token * kRowBytes;
             for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(d + 16 * e) = zero;
@@ -429,7 +429,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
         }
         c.val[mc] = g.whole ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
       }
-      wait_or_fail(bar(c.o_done), (nt - 1) & 1, fail);
+      wait(bar(c.o_done), (nt - 1) & 1);
       half_barrier(half);
       tc::tc_fence_after();
       unsigned bad = 0;

@@ -152,10 +152,10 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = c.tmem;
-  volatile int *fail = &c.fail;
+  const Waits wait(&c.fail, p.T);
   // the next item, by every thread that works on them
   auto next_item = [&](Item &m, uint32_t round) {
-    const bool ok = wait_or_fail(bar(c.item_full), round & 1, fail);
+    const bool ok = wait(bar(c.item_full), round & 1);
     m = c.item;
     if (!ok) m.pair = -1;
     tc::mbar_arrive(bar(c.item_empty));
@@ -172,10 +172,10 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         for (uint32_t round = 0; ok; ++round) {
           if (round > 0) {
             // (asked for once everyone has begun the item before)
-            if (!wait_or_fail(bar(c.item_empty), (round - 1) & 1, fail)) break;
+            if (!wait(bar(c.item_empty), (round - 1) & 1)) break;
             tc::mbar_expect_tx(bar(c.claim), 16);
             claim_next(tc::smem_u32(&c.claimed), bar(c.claim));
-            if (!wait_or_fail(bar(c.claim), (round - 1) & 1, fail)) break;
+            if (!wait(bar(c.claim), (round - 1) & 1)) break;
             ok = claimed(tc::smem_u32(&c.claimed), index);
             tc::fence_proxy_async();
           }
@@ -192,7 +192,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         bool ok = true;
         Item m{};
         auto load_q = [&](int x) {
-          ok = wait_or_fail(bar(c.q_empty[x]), (qn[x] + 1) & 1, fail);
+          ok = wait(bar(c.q_empty[x]), (qn[x] + 1) & 1);
           if (!ok) return;
           const int t = (2 * m.pair + x) * kRowsQ;
           const uint32_t full = bar(c.q_full[x]);
@@ -207,7 +207,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         auto load_k = [&](int j) {
           for (int i = 0; i < nc; ++i, ++kn) {
             const uint32_t s = kn % kKSlots;
-            ok = wait_or_fail(bar(c.k_empty[s]), (kn / kKSlots + 1) & 1, fail);
+            ok = wait(bar(c.k_empty[s]), (kn / kKSlots + 1) & 1);
             if (!ok) return;
             const uint32_t full = bar(c.k_full[s]), d = s0 + kOffK + s * kChunkB;
             tc::mbar_expect_tx(full, kChunkB);
@@ -222,7 +222,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
           if (ok && m.has(1)) load_q(1);
           for (int j = m.jl; ok && j < m.jh; ++j) {
             const uint32_t s = vn % kVSlots;
-            ok = wait_or_fail(bar(c.v_empty[s]), (vn / kVSlots + 1) & 1, fail);
+            ok = wait(bar(c.v_empty[s]), (vn / kVSlots + 1) & 1);
             if (!ok) break;
             const uint32_t full = bar(c.v_full[s]);
             tc::mbar_expect_tx(full, (uint32_t)nv * kChunkB);
@@ -233,7 +233,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
             if (j + 1 < m.jh) load_k(j + 1);
           }
         }
-        if (*fail) {   // what is on its way comes in before the CTA ends
+        if (c.fail) {   // what is on its way comes in before the CTA ends
           for (int x = 0; x < 2; ++x)
             if (qn[x]) tc::mbar_wait(bar(c.q_full[x]), (qn[x] - 1) & 1);
           for (uint32_t k = kn > kKSlots ? kn - kKSlots : 0; k < kn; ++k)
@@ -260,9 +260,9 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
               const bool on = now && j >= lo && j < hi;
               if (on) {
                 // the rows of the item before have been read
-                if (j == lo) ok = wait_or_fail(bar(c.o_free[x]), qn[x] & 1, fail);
-                ok = ok && wait_or_fail(bar(c.p_ready[x]), (sn[x] - 1) & 1, fail) &&
-                     wait_or_fail(bar(c.v_full[vn % kVSlots]), (vn / kVSlots) & 1, fail);
+                if (j == lo) ok = wait(bar(c.o_free[x]), qn[x] & 1);
+                ok = ok && wait(bar(c.p_ready[x]), (sn[x] - 1) & 1) &&
+                     wait(bar(c.v_full[vn % kVSlots]), (vn / kVSlots) & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
                 const uint64_t dv =
@@ -275,14 +275,14 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
               }
               if (j + 1 >= lo && j + 1 < hi) {
                 if (j + 1 == lo) {
-                  ok = wait_or_fail(bar(c.q_full[x]), qn[x] & 1, fail);
+                  ok = wait(bar(c.q_full[x]), qn[x] & 1);
                   if (!ok) break;
                   ++qn[x];
                 }
                 const bool last = x == 1 || !m.active(1, j + 1);
                 for (int i = 0; i < nc; ++i) {
                   const uint32_t k = kn + (uint32_t)i, s = k % kKSlots;
-                  ok = wait_or_fail(bar(c.k_full[s]), (k / kKSlots) & 1, fail);
+                  ok = wait(bar(c.k_full[s]), (k / kKSlots) & 1);
                   if (!ok) break;
                   const uint64_t da = swizzled_desc(s0 + (uint32_t)(3 * x + i) * kChunkB, 16),
                                  dk = swizzled_desc(s0 + kOffK + s * kChunkB, 16);
@@ -307,7 +307,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
             }
           }
         }
-        if (*fail) {
+        if (c.fail) {
           tc::mma_commit(bar(c.drain));
           tc::mbar_wait(bar(c.drain), 0);
         }
@@ -332,7 +332,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int j = r.lo; j < r.hi; ++j, ++sn) {
-        wait_or_fail(bar(c.s_full[x]), sn & 1, fail);
+        wait(bar(c.s_full[x]), sn & 1);
         __syncwarp();
         tc::tc_fence_after();
         uint32_t u[4][32];
@@ -404,7 +404,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       // ---- the rows ----
       const bool any = r.lo < r.hi;
       if (any) {
-        wait_or_fail(bar(c.o_done[x]), items & 1, fail);
+        wait(bar(c.o_done[x]), items & 1);
         __syncwarp();
         tc::tc_fence_after();
         ++items;

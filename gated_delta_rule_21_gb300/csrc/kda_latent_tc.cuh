@@ -65,22 +65,28 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// A wait that the other threads of the CTA can end: it gives up after tc::kWaitLimit
-// clocks, or once one of them has; whoever gives up first says so in *fail.  Threads
-// that share barriers of their own go on all the same, without waiting, so that all of
-// them come to the end.
-__device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, volatile int *fail) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!tc::mbar_try_wait(bar, parity)) {
-    if (*fail) return false;
-    if (clock64() - t0 > tc::kWaitLimit) {
-      *fail = 1;
-      return false;
+// A wait that the other threads of the CTA can end: it gives up after `clocks`, or once
+// one of them has; whoever gives up first says so in *fail.  Threads that share barriers
+// of their own go on all the same, without waiting, so that all of them come to the end.
+struct Waits {
+  volatile int *fail;
+  long long clocks;
+  // About a second, and what the rows of a tile take where they are made again key by key.
+  __device__ __forceinline__ Waits(int *f, long long keys)
+      : fail(f), clocks(tc::kWaitLimit + (min(keys, 1ll << 20) << 16)) {}
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!tc::mbar_try_wait(bar, parity)) {
+      if (*fail) return false;
+      if (clock64() - t0 > clocks) {
+        *fail = 1;
+        return false;
+      }
     }
+    return true;
   }
-  return true;
-}
+};
 
 // One thread of a warp that is whole.  (The compiler then knows that the branch holds
 // one thread; behind `lane == 0` it readies each product's uniform registers for many.)

@@ -192,6 +192,27 @@ def test_a_long_row_of_many_heads():
             latent64.check(have, pair, f"{n} of head {h}")
 
 
+@pytest.mark.parametrize("impl,dtype", [("simt", F32), ("tc", BF)])
+def test_every_row_made_again(impl, dtype):
+    """An infinite value at the first token: every row comes out not finite and is made
+    again key by key, no wait of the others runs out, and the other columns are right."""
+    import gated_delta_rule_21_gb300 as kda
+    gen = torch.Generator().manual_seed(11)
+    B, T, H, K, R, V = 1, 3000, 2, 64, 32, 64
+    x, _ = inputs(B, T, H, K, R, V, dtype, gen, strided=False)
+    clean = run(x, None, impl)
+    x["v"][0, 0, :, 7] = float("inf")
+    ws = kda.alloc_latent_workspace(B, T, H, R)
+    got = run(x, None, impl, workspace=ws)
+    assert kda.read_device_status(ws) == 0
+    assert not torch.isfinite(got["o"][..., 7]).any()
+    rest = [c for c in range(V) if c != 7]
+    a, b = got["o"][..., rest].double(), clean["o"][..., rest].double()
+    # weights rounded to bf16 or not, and the output's own rounding
+    assert float((a - b).abs().max()) <= (3e-2 if dtype == BF else 1e-4) * float(b.abs().max())
+    assert float((got["lse"] - clean["lse"]).abs().max()) <= 1e-3
+
+
 def test_calls_at_once():
     """Two streams, each with its own workspace, while a third appends."""
     import gated_delta_rule_21_gb300 as kda
