@@ -15,12 +15,15 @@
 // first when they are done: the products then hide behind the exponentials.
 //
 // Shared memory (200 KB): 5 chunks of 16 KB of X, 3 stages of 5 chunks of 8 KB of Y.
-// Tensor memory: S twice and dP of 64 columns, dX1 192, dX2 128.
+// Tensor memory: S twice and dP of 64 columns, dX1 192, dX2 128; for the queries, without
+// dX2, X1 instead, whose chunks make room for a fourth stage.
 //
-// A row of 8192 tokens, 32 heads of 128 + 64: keys and values 910 us, queries 886, D 34 (with
-// fewer registers, and what a column needs read after the wait, 1050 and 905).  What bounds
-// them: the products (44 cycles an instruction of N 64: 1400 of 1800 cycles a tile) and the
-// tiles of the other side, which come from L2 at 6 to 7 TB/s.
+// A row of 8192 tokens, 32 heads of 128 + 64: keys and values 910 to 925 us (with fewer
+// registers, and what a column needs read after the wait, 1050), queries 778 (with X1 in
+// shared memory and three stages 886), D 29.  What bounds them: the products (an instruction
+// of N 64 takes 44 cycles with both operands in shared memory, 29 with one: 1400 of 1800
+// cycles a tile for the keys) and the tiles of the other side, which come from L2 at 6 to
+// 7 TB/s.
 #include "kda_f32x2.cuh"
 #include "kda_latent_tc.cuh"
 
@@ -28,24 +31,25 @@ namespace kda {
 namespace latent {
 namespace {
 
-constexpr int kOuter = 128, kInner = 64, kStages = 3;
+constexpr int kOuter = 128, kInner = 64;
+constexpr int kMaxStages = 4;
 constexpr uint32_t kXChunkB = kOuter * kRowBytes, kYChunkB = kInner * kRowBytes;
 constexpr uint32_t kStageB = 5 * kYChunkB;
-constexpr uint32_t kOffY = 5 * kXChunkB, kOffC = kOffY + kStages * kStageB;
+constexpr uint32_t kOffY = 5 * kXChunkB, kOffC = kOffY + 3 * kStageB;
 constexpr uint32_t kSmem = kOffC + 4096 + 1024;
 constexpr int kThreads = 384;                  // 8 warps of rows; copies, products, two idle ones
-constexpr uint32_t kTdP = 128, kTX1 = 192, kTX2 = 384;   // columns
+constexpr uint32_t kTdP = 128, kTX1 = 192, kTX2 = 384;   // columns; X1 itself where dX2 is not made
 
 struct Maps {
   CUtensorMap x1, x1r, x2, y1, y1r, y2;
 };
 
 struct Control {
-  uint64_t x_full, y_full[kStages], y_empty[kStages], s_full, ds_ready, done, drain;
+  uint64_t x_full, x_moved, y_full[kMaxStages], y_empty[kMaxStages], s_full, ds_ready, done, drain;
   uint32_t tmem;
   int fail;
   unsigned bad[8];
-  float stat[8][2][32];
+  alignas(16) float stat[8][2][32];      // read four at a time
 };
 
 // What a launch makes.  kDelta: D of queries that see at most kExact tiles of keys, as
@@ -60,6 +64,7 @@ template <What kWhat>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   constexpr bool kKeys = kWhat == kKeysOf;
+  constexpr int kStages = kKeys ? 3 : 4;
   extern __shared__ __align__(1024) unsigned char raw[];
   unsigned char *smem = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
   Control &c = *reinterpret_cast<Control *>(smem + kOffC);
@@ -82,6 +87,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   auto bar = [](uint64_t &x) { return tc::smem_u32(&x); };
   if (tid == 0) {
     tc::mbar_init(bar(c.x_full), 1);
+    tc::mbar_init(bar(c.x_moved), 256);
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar(c.y_full[i]), 1);
       tc::mbar_init(bar(c.y_empty[i]), 1);
@@ -100,6 +106,8 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   if (kKeys) start_next();
   const uint32_t tmem = c.tmem;
   const Waits wait(&c.fail, p.T);
+  // the fourth stage lies where X1 was
+  auto stage_at = [&](int s) { return s < 3 ? s0 + kOffY + (uint32_t)s * kStageB : s0; };
 
   if (warp >= 8) {
     few_registers();
@@ -122,8 +130,9 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       for (; i < n; ++i) {
         const int s = i % kStages, y0 = (first + i) * kInner;
         ok = wait(bar(c.y_empty[s]), (uint32_t)(i / kStages + 1) & 1);
+        if (ok && i == 3 && !kKeys) ok = wait(bar(c.x_moved), 0);
         if (!ok) break;
-        const uint32_t d = s0 + kOffY + (uint32_t)s * kStageB;
+        const uint32_t d = stage_at(s);
         tc::mbar_expect_tx(bar(c.y_full[s]), (uint32_t)(nc + nv) * kYChunkB);
         for (int e = 0; e < nk; ++e)
           tma_load_4d(d + (uint32_t)e * kYChunkB, &maps.y1, e * kChunkCols, h, y0, b,
@@ -148,19 +157,24 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
                      id_x1 = tc::idesc_bf16(kOuter, nc * kChunkCols, 0, 1),
                      id_x2 = tc::idesc_bf16(kOuter, nv * kChunkCols, 0, 1);
       auto scores = [&](int i) {        // S of tile i
-        const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
+        const uint32_t y = stage_at(i % kStages);
         const uint64_t dx = swizzled_desc(s0, 16), dy = swizzled_desc(y, 16);
         for (int e = 0; e < nc; ++e) {
           const uint64_t x = dx + kXChunkB / 16 * e, z = dy + kYChunkB / 16 * e;
           const uint32_t old = e > 0 ? 1u : 0u;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16(tmem + kInner * (i & 1), x + kStepK * k, z + kStepK * k, id_s,
-                         k > 0 ? 1u : old);
+          for (int k = 0; k < 4; ++k) {
+            if (kKeys)
+              tc::mma_bf16(tmem + kInner * (i & 1), x + kStepK * k, z + kStepK * k, id_s,
+                           k > 0 ? 1u : old);
+            else
+              mma_bf16_ts(tmem + kInner * (i & 1), tmem + kTX2 + 32 * e + 8 * k, z + kStepK * k, id_s,
+                          k > 0 ? 1u : old);
+          }
         }
       };
       auto dp = [&](int i) {
-        const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
+        const uint32_t y = stage_at(i % kStages);
         const uint64_t dx = swizzled_desc(s0 + 3 * kXChunkB, 16),
                        dy = swizzled_desc(y + 3 * kYChunkB, 16);
         for (int e = 0; e < nv; ++e) {
@@ -174,7 +188,8 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       auto loaded = [&](int i) {
         return wait(bar(c.y_full[i % kStages]), (uint32_t)(i / kStages) & 1);
       };
-      bool ok = wait(bar(c.x_full), 0) && loaded(0);
+      bool ok = wait(bar(c.x_full), 0) && (kKeys || wait(bar(c.x_moved), 0)) && loaded(0);
+      if (!kKeys) tc::tc_fence_after();
       if (ok) {
         scores(0);
         dp(0);
@@ -195,7 +210,7 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         }
         if (kWhat != kDelta) {
           // steps of 16 rows of Y: the two halves of 32 stand 32 columns apart
-          const uint32_t y = s0 + kOffY + (uint32_t)(i % kStages) * kStageB;
+          const uint32_t y = stage_at(i % kStages);
           const uint32_t w = tmem + kInner * (i & 1), old = i > 0 ? 1u : 0u;
           const uint64_t dy = swizzled_desc(y, kYChunkB);
           if (kKeys) {
@@ -235,6 +250,28 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
     // columns that every row sees
     const int all_from = kKeys ? t_last : run_start(p, b, t_last);
     const int all_to = t_last - t0 + 1 < kOuter ? 0 : kKeys ? run_end(p, b, t0) : t0 + 1;
+    if (!kKeys && n > 0) {
+      // X1 to tensor memory: its products then read one operand from shared memory, and
+      // its place takes another stage
+      wait(bar(c.x_full), 0);
+      __syncwarp();
+      for (int g = half; g < 2 * nc; g += 2) {      // 32 channels
+        uint32_t x[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(
+              smem + (uint32_t)(g >> 1) * kXChunkB + piece_off(tid & 127, 4 * (g & 1) + e));
+          x[4 * e] = v.x;
+          x[4 * e + 1] = v.y;
+          x[4 * e + 2] = v.z;
+          x[4 * e + 3] = v.w;
+        }
+        tmem_st16(tmem + kTX2 + 16 * g + lanes, x);
+      }
+      tmem_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(bar(c.x_moved));
+    }
     float lse = 0.f, delta = 0.f, next_lse = 0.f, next_delta = 0.f;
     auto fetch = [&](int i) {
       const int y = (first + i) * kInner + 32 * half + lane;
