@@ -33,7 +33,7 @@ constexpr int kMine = kRows / 2;         // rows of a softmax thread
 constexpr uint32_t kChunkB = kTile * kRowBytes;        // 16 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kRing = 11;                // chunks in shared memory
-constexpr int kMaxPairs = 5, kMaxRopes = 5;
+constexpr int kMaxPairs = 5, kMaxRopes = 3;
 constexpr uint32_t kQChunkB = kRows * kRowBytes;       // 4 KB
 constexpr uint32_t kQB = 9 * kQChunkB;
 constexpr uint32_t kPB = kTile * kRows * 2;            // 8 KB
@@ -516,8 +516,8 @@ cudaError_t launch_step_tc(const Step &p, cudaStream_t s) {
   Ring r;
   r.npair = p.C / 128;
   // as many tiles ahead as fit: half of the next one beside 512 latents
-  r.pairs = p.C == 512 ? 5 : p.C == 256 ? 4 : 3;
-  r.ropes = p.C == 512 ? 1 : p.C == 256 ? 2 : 3;
+  r.pairs = p.C == 512 ? 5 : 4;
+  r.ropes = p.C == 512 ? 1 : 3;
   r.box = p.page < kTile ? p.page : kTile;
   CUtensorMap map;
   const uint64_t dims[3] = {(uint64_t)(p.C + p.R), (uint64_t)p.page, (uint64_t)p.n_pages};
