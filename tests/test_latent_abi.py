@@ -131,6 +131,33 @@ def test_workspace_sizes(L):
     assert ctypes.sizeof(kda.kda_rotate_desc) == 80
 
 
+def test_a_call_goes_to_its_tensors_device(monkeypatch):
+    """Whichever device is current; with a stream, to the stream."""
+    import contextlib
+
+    class Far:
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    seen = []
+
+    @contextlib.contextmanager
+    def entered(where):
+        seen.append(where)
+        yield
+
+    monkeypatch.setattr(kda, "_device_now", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", entered)
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    assert kda._away(Far(), None) and not kda._away(torch.zeros(2), None)
+    assert kda._moved(lambda a, b: (a, b), Far(), None, 5, b=6) == (5, 6) and seen == [1]
+    assert kda._moved(lambda a: a, Far(), "its stream", 7) == 7 and seen == [1, "its stream"]
+    monkeypatch.setattr(kda, "_device_now", lambda: 1)
+    assert not kda._away(Far(), None)
+
+
 def test_python_checks_come_before_the_library():
     x = torch.zeros(1, 4, 2, 32)
     with pytest.raises(ValueError, match="CUDA"):
