@@ -380,7 +380,8 @@ __device__ __noinline__ void step_row(const Step &p, int b, int r, int n, int la
   if (p.lse && lane == 0) p.lse[((size_t)b * p.H + h) * p.T + t] = m + logf(l);
 }
 
-// Rows of up to so many keys have their D = d_o . o made again from the products.
+// Rows that see up to so many keys have their D = d_o . o made from the products (tensor
+// cores).
 constexpr int kExactKeys = 1024;
 
 // ---- launchers --------------------------------------------------------------

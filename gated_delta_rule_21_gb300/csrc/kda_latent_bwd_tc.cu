@@ -52,13 +52,17 @@ struct Control {
   alignas(16) float stat[8][2][32];      // read four at a time
 };
 
-// What a launch makes.  kDelta: D of queries that see at most kExact tiles of keys, as
+// What a launch makes.  kDelta: D of queries that see at most kExactKeys keys, as
 // sum_j p_ij (d_o_i . v_j) / sum_j p_ij.  D from the stored o has o's rounding, whose part of
 // ds = p (dp - D) is the larger the fewer keys a query sees (dq and dk of rows of 40
 // tokens 2.9e-3 off in the 2-norm, with this 2.3e-3, 1.7e-3 of it their own rounding; of
-// 1000 tokens 2.6e-3 and 2.3e-3).
+// 1000 tokens 2.6e-3 and 2.3e-3).  Whether a query is one of them hangs on it alone: a CTA
+// walks the keys from the first one that such a query of its rows sees, at most
+// kExactKeys + 127 of them, and leaves D of the other rows as it is.
 enum What { kKeysOf, kQueriesOf, kDelta };
-constexpr int kExact = kExactKeys / kInner;
+__device__ __forceinline__ bool few_keys(int start, int row) {
+  return start <= row && row - start < kExactKeys;
+}
 
 template <What kWhat>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -80,10 +84,21 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
   const int nv = (p.V + kChunkCols - 1) / kChunkCols;
   const int t_last = min(p.T, t0 + kOuter) - 1;
   // tiles of the other side
-  const int first = kKeys ? t0 / kInner : run_start(p, b, t0) / kInner;
+  int first_key = kKeys ? t0 : run_start(p, b, t0);
+  if (kWhat == kDelta) {       // (every warp looks at all rows; starts rise along them)
+    first_key = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < kOuter / 32; ++i) {
+      const int row = t0 + 32 * i + lane;
+      const int start = row < p.T ? run_start(p, b, row) : 0x7fffffff;
+      if (few_keys(start, row)) first_key = min(first_key, start);
+    }
+    first_key = __reduce_min_sync(0xffffffffu, first_key);
+    if (first_key == 0x7fffffff) return;
+  }
+  const int first = first_key / kInner;
   const int stop = kKeys ? (run_end(p, b, t_last) + kInner - 1) / kInner : t_last / kInner + 1;
   const int n = stop > first ? stop - first : 0;
-  if (kWhat == kDelta && n > kExact) return;
   auto bar = [](uint64_t &x) { return tc::smem_u32(&x); };
   if (tid == 0) {
     tc::mbar_init(bar(c.x_full), 1);
@@ -361,10 +376,10 @@ prompt_bwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
       upk2(sum_g, a, d);
       c.stat[warp][1][lane] = a + d;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (half == 0 && row < p.T) {
+      if (half == 0 && row < p.T && few_keys(from, row)) {
         const float w = c.stat[warp][0][lane] + c.stat[warp + 4][0][lane];
         const float g = c.stat[warp][1][lane] + c.stat[warp + 4][1][lane];
-        if (w != 0.f) const_cast<float *>(p.delta)[head + row] = g / w;
+        const_cast<float *>(p.delta)[head + row] = w == 0.f ? 0.f : g / w;
       }
     } else {
       // ---- the sums, 32 columns at a time, the halves in turn ----
