@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(const Prompt p, in
 #pragma unroll
   for (int i = 0; i < kRt; ++i) {
     const int t = t0 + kRt * ty + i;
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i], none = no_weights(lo[i] <= t);
     bool bad = false;
     if (t < p.T) {
       T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.V;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) prompt_fwd_kernel(const Prompt p, in
         upk2(acc[i][q][1], x[2], x[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = l[i] == 0.f ? 0.f : x[e] * inv;
+          const float y = l[i] == 0.f ? none : x[e] * inv;
           bad |= !finite(y);
           o[4 * tx + 64 * q + e] = from_f32<T>(y);
         }

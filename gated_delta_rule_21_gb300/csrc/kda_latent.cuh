@@ -79,6 +79,10 @@ __device__ __forceinline__ float score(const Prompt &p, int b, int h, int i, int
   return warp_sum(s) * p.scale;
 }
 
+// o of a row whose weights sum up to 0: 0 where it sees nothing; where all that it sees has
+// a score of minus infinity, which softmax gives no weights, NaN.
+__device__ __forceinline__ float no_weights(bool sees) { return sees ? NAN : 0.f; }
+
 // The tiles multiply masked weights of 0 with what stands there, and 0 times
 // infinity is NaN.  A row whose sum came out not finite is made again by these,
 // key by key over what it sees; a row that is not finite by itself stays so (and is done
@@ -87,7 +91,8 @@ __device__ __forceinline__ float score(const Prompt &p, int b, int h, int i, int
 template <typename T>
 __device__ __noinline__ void forward_row(const Prompt &p, int b, int h, int i, int lane) {
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j = run_start(p, b, i); j <= i; ++j) {
+  const int start = run_start(p, b, i);
+  for (int j = start; j <= i; ++j) {
     const float s = score<T>(p, b, h, i, j, lane);
     const float mn = s > m ? s : m;
     const float c = m == mn ? 1.f : expf(m - mn), w = s == -INFINITY ? 0.f : expf(s - mn);
@@ -102,7 +107,8 @@ __device__ __noinline__ void forward_row(const Prompt &p, int b, int h, int i, i
   T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + i) * p.H + h) * p.V;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < p.V) o[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : acc[e] / l);
+    if (lane + 32 * e < p.V)
+      o[lane + 32 * e] = from_f32<T>(l == 0.f ? no_weights(start <= i) : acc[e] / l);
   if (p.lse && lane == 0) p.lse[((size_t)b * p.H + h) * p.T + i] = m + logf(l);
 }
 
@@ -194,7 +200,8 @@ struct Step {
   void *o;
   float *lse;
   int2 *plan;                    // [B][row_tiles]: the first and last part of a row tile, the
-                                 // first one as its slot; {-1, -1}: it was written whole
+                                 // first one as its slot; {-1, rows}: it was written whole,
+                                 // these of its rows (as bits) without weights
   float *parts;                  // [2 * kParts][kRows][C]: sums, not yet divided
   float *stats;                  // [2 * kParts][kRows][2]: maximum (of scale log2e s) and sum
   uint32_t *status;
@@ -340,11 +347,27 @@ struct Cursor {
   // What the kernel that joins the parts has to know (one thread).
   __device__ __forceinline__ static void note(const Step &p, const Segment &g) {
     int2 *d = p.plan + (size_t)g.b * p.row_tiles + g.rt;
-    if (g.whole) *d = make_int2(-1, -1);
+    if (g.whole) *d = make_int2(-1, 0);
     else if (g.j0 == 0) d->x = g.slot;
     else if (g.j0 + g.n == tiles_of(p, g.s)) d->y = blockIdx.x;
   }
+  // Of 16 rows (behind note): what they see is left to that kernel to look up.
+  __device__ __forceinline__ static void note_none(const Step &p, const Segment &g, int half,
+                                                   unsigned rows) {
+    int2 *d = p.plan + (size_t)g.b * p.row_tiles + g.rt;
+    reinterpret_cast<unsigned short *>(&d->y)[half] = (unsigned short)rows;
+  }
 };
+
+// Whether any of the first n tokens of sequence b has a page.  One warp.
+inline __device__ __noinline__ bool any_there(const Step &p, int b, int n, int lane) {
+  const int pages = n / p.page + (n % p.page != 0);
+  for (int i = 0; i < pages; i += 32) {
+    const int pg = i + lane < pages ? p.table[(size_t)b * p.max_pages + i + lane] : -1;
+    if (__any_sync(0xffffffffu, pg >= 0 && pg < p.n_pages)) return true;
+  }
+  return false;
+}
 
 // The absorbed form's counterpart of forward_row: row r of sequence b, which sees n
 // tokens.  One warp.
@@ -356,9 +379,11 @@ __device__ __noinline__ void step_row(const Step &p, int b, int r, int n, int la
   float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  bool any = false;
   for (int j = 0; j < n; ++j) {
     const int pg = p.table[(size_t)b * p.max_pages + j / p.page];
     if (pg < 0 || pg >= p.n_pages) continue;
+    any = true;
     const T *c = static_cast<const T *>(p.cache) + pg * p.page_stride +
                  (long long)(j % p.page) * p.token_stride;
     float s = dot(q, c, p.C, lane);
@@ -376,7 +401,8 @@ __device__ __noinline__ void step_row(const Step &p, int b, int r, int n, int la
   T *o = static_cast<T *>(p.o) + (((size_t)b * p.T + t) * p.H + h) * p.C;
 #pragma unroll
   for (int e = 0; e < 16; ++e)
-    if (lane + 32 * e < p.C) o[lane + 32 * e] = from_f32<T>(l == 0.f ? 0.f : acc[e] / l);
+    if (lane + 32 * e < p.C)
+      o[lane + 32 * e] = from_f32<T>(l == 0.f ? no_weights(any) : acc[e] / l);
   if (p.lse && lane == 0) p.lse[((size_t)b * p.H + h) * p.T + t] = m + logf(l);
 }
 

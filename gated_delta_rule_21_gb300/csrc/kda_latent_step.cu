@@ -167,6 +167,11 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
       const float li = __shfl_sync(0xffffffffu, l[i & 1], (i >> 1) * 16);
       if (r >= rows) continue;
       bool bad = false;
+      float none = 0.f;
+      if (whole && li == 0.f) {
+        const int n = seen(p, s, r);
+        none = no_weights(n > 0 && any_there(p, g.b, n, lane));
+      }
       const int t = r / p.H, h = r % p.H;
       T *o = static_cast<T *>(p.o) + (((size_t)g.b * p.T + t) * p.H + h) * p.C;
       float *part = p.parts + ((size_t)slot * kRows + rr) * p.C;
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) step_simt_kernel(Step p) {
         for (int e = 0; e < 4; ++e) {
           const int c = 128 * q + 4 * lane + e;
           if (whole) {
-            const float z = li == 0.f ? 0.f : v[e] / li;
+            const float z = li == 0.f ? none : v[e] / li;
             bad |= !finite(z);
             o[c] = from_f32<T>(z);
           } else {
@@ -233,7 +238,15 @@ __global__ void __launch_bounds__(512) join_kernel(Step p, int block_rows) {
     }
     return;
   }
-  if (range.x < 0) return;
+  auto none = [&] {        // a row without weights: four channels a thread
+    const int n = seen(p, s, r);
+    if (n > 0 && any_there(p, b, n, lane))
+      for (int e = 0; e < 4; ++e) o[4 * col + e] = from_f32<T>(no_weights(true));
+  };
+  if (range.x < 0) {
+    if (group == 0 && range.y >> r % kRows & 1) none();
+    return;
+  }
   const int first = range.x, g0 = first >> 1, g1 = range.y;
   auto slot = [&](int g) { return (size_t)(g == g0 ? first : 2 * g) * kRows + r % kRows; };
   const float2 *stats = reinterpret_cast<const float2 *>(p.stats);
@@ -279,6 +292,7 @@ __global__ void __launch_bounds__(512) join_kernel(Step p, int block_rows) {
     w.x[e] = from_f32<T>(z);
   }
   *reinterpret_cast<Four *>(o + 4 * col) = w;
+  if (l == 0.f) none();    // (all threads of the row or none)
   if (col == 0 && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   if (p.T == 1) return;   // every row sees what the others see
   // a row with a value that is not finite, again; its warps write the same values

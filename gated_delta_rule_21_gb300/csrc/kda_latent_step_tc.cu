@@ -428,6 +428,8 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
               total == 0.f ? -INFINITY : (mine + log2f(total)) * kLn2;
         }
         c.val[mc] = g.whole ? (total == 0.f ? 0.f : 1.f / total) : 1.f;
+        const unsigned none = __ballot_sync(0xffffu, total == 0.f);
+        if (g.whole && lane == 0) Cursor::note_none(p, g, half, none);
       }
       wait(bar(c.o_done), (nt - 1) & 1);
       half_barrier(half);

@@ -416,7 +416,7 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         tc::tc_fence_after();
         ++items;
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l, none = no_weights(lo <= row);
       bool bad = false;
       __nv_bfloat16 *o =
           static_cast<__nv_bfloat16 *>(p.o) + (((size_t)b * p.T + row) * p.H + h) * p.V;
@@ -436,8 +436,8 @@ prompt_fwd_tc_kernel(const __grid_constant__ Maps maps, const Prompt p) {
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float a = l == 0.f ? 0.f : __uint_as_float(y[2 * i]) * inv;
-          const float d = l == 0.f ? 0.f : __uint_as_float(y[2 * i + 1]) * inv;
+          const float a = l == 0.f ? none : __uint_as_float(y[2 * i]) * inv;
+          const float d = l == 0.f ? none : __uint_as_float(y[2 * i + 1]) * inv;
           bad |= !finite(a) || !finite(d);
           w[i] = tc::pack_bf16(a, d);
         }

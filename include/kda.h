@@ -762,7 +762,7 @@ KDA_API kda_status kda_latent_append(const kda_latent_cache *s, const void *late
  *                 (the device status word).  Calls on different streams need
  *                 their own.
  * C is 128, 256 or 512, R 0, 32 or 64.  Values that are not finite reach the tokens
- * that see them alone.  The work is cut evenly over the SMs by the lengths on the
+ * that see them alone; a row whose every score is minus infinity has o NaN, lse -inf.  The work is cut evenly over the SMs by the lengths on the
  * device, so a captured call serves whatever lengths it finds.  Asynchronous.
  */
 KDA_API size_t kda_latent_step_workspace_size(const kda_latent_cache *s);
@@ -793,7 +793,8 @@ KDA_API kda_status kda_latent_step(const kda_latent_cache *s, const void *q, con
  *                 its first 256 bytes zero-filled before its first use.  Calls
  *                 on different streams need their own.
  * K and V are 32, 64 or 128, R 0, 32 or 64; B*T*H*(K+R) < 2^31.  Values that are not
- * finite reach the tokens that see them alone.  Asynchronous on `stream`.
+ * finite reach the tokens that see them alone; a query whose every score is minus
+ * infinity has o NaN, lse -inf.  Asynchronous on `stream`.
  */
 typedef struct kda_latent_shape {
   int B, T, H, K, R, V;
