@@ -1079,7 +1079,8 @@ def block_norm_bwd(y, w_post, stats, d_out, *, d_x=None, residual=None, gate=Non
 # ---------------------------------------------------------------------------
 # attention over one shared latent vector a token
 #
-# A call goes to the device of its tensors, whichever is current.
+# A call goes to the device of its tensors, whichever is current; a stream has to be
+# one of that device.
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1114,6 +1115,8 @@ _device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
 
 def _away(x, stream):
     """Whether a call has to be made under another stream or device."""
+    if stream is not None and x.is_cuda and stream.device.index != x.get_device():
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{x.get_device()}")
     return stream is not None and _elsewhere(stream) or \
         x.is_cuda and x.get_device() != _device_now()
 
