@@ -1146,7 +1146,8 @@ def rotate(x, inv_freq, *, positions=None, pairs=True, inverse=False, out=None, 
     x: [B,T,H,dim] or [B,T,dim] (bf16 or fp32, the last dimension contiguous, any
     other strides); inv_freq: [dim/2] fp32; positions: [B,T] int32 (None: 0 ..
     T-1).  ``pairs``: (x[2i], x[2i+1]), else (x[i], x[i+dim/2]).  ``out`` may be x
-    itself; returns it, or a new contiguous tensor."""
+    itself, and is not to overlap it otherwise nor its own rows; returns it, or a new
+    contiguous tensor."""
     if _away(x, stream):
         return _moved(rotate, x, stream, x, inv_freq, positions=positions, pairs=pairs,
                       inverse=inverse, out=out)

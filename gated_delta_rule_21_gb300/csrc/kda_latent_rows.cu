@@ -244,6 +244,9 @@ bool wide_ok(const void *p, const Strides &s, int esize) {
          (s.h * esize) % 16 == 0;
 }
 
+// Whether rows of n values lie over each other for a stride of their own.
+bool over(long long stride, int count, int n) { return count > 1 && stride < n && stride > -n; }
+
 bool dtype_ok(kda_dtype d) { return d == KDA_DTYPE_F32 || d == KDA_DTYPE_BF16; }
 
 }  // namespace
@@ -262,6 +265,9 @@ kda_status kda_rotate(const kda_rotate_desc *d, const void *x, const int32_t *po
   if (!x || !inv_freq || !y) return KDA_ERR_INVALID_ARG;
   if (d->dim % 2 || d->dim > 2 * kMaxPairs) return KDA_ERR_UNSUPPORTED;
   if ((long long)d->B * d->T >= (1ll << 31) || d->H >= (1 << 20)) return KDA_ERR_UNSUPPORTED;
+  if (over(d->y_stride_b, d->B, d->dim) || over(d->y_stride_t, d->T, d->dim) ||
+      over(d->y_stride_h, d->H, d->dim))
+    return KDA_ERR_INVALID_ARG;
   const int es = d->dtype == KDA_DTYPE_BF16 ? 2 : 4;
   if (!multiple(x, es) || !multiple(y, es) || !multiple(inv_freq, 4) || !multiple(positions, 4))
     return KDA_ERR_ALIGNMENT;
@@ -295,6 +301,9 @@ kda_status kda_latent_append(const kda_latent_cache *s, const void *latent, cons
   if (inv_freq && s->R == 0) return KDA_ERR_INVALID_ARG;
   if (s->C > 4096 || s->R % 2 || s->R > 2 * kMaxPairs) return KDA_ERR_UNSUPPORTED;
   if ((long long)s->B * s->T >= (1ll << 31) || s->H >= (1 << 20)) return KDA_ERR_UNSUPPORTED;
+  if (over(s->page_stride, s->n_pages, s->C + s->R) ||
+      over(s->token_stride, s->page_size, s->C + s->R))
+    return KDA_ERR_INVALID_ARG;
   const int es = s->dtype == KDA_DTYPE_BF16 ? 2 : 4;
   for (const void *ptr : {latent, k_rope, q_rope, (const void *)cache, (const void *)q_out})
     if (!multiple(ptr, es)) return KDA_ERR_ALIGNMENT;

@@ -688,7 +688,9 @@ KDA_API kda_status kda_block_norm_bwd(const kda_norm_desc *d, const void *y, con
  *   x             device [B,T,H,dim] of d->dtype, the last dimension contiguous.
  *   positions     device int32 [B,T] or NULL (t = 0 .. T-1).
  *   inv_freq      device float32 [dim/2].
- *   y             device [B,T,H,dim] at its own strides; may be x at x's strides.
+ *   y             device [B,T,H,dim] at its own strides; may be x at x's strides, and
+ *                 else must not overlap it.  No two of its rows may overlap (a stride
+ *                 of less than dim is KDA_ERR_INVALID_ARG).
  * dim is even, 2 to 256 (KDA_ERR_UNSUPPORTED above).  Asynchronous on `stream`.
  */
 typedef struct kda_rotate_desc {
@@ -735,7 +737,8 @@ typedef struct kda_latent_cache {
  *                 are not there as they came).
  *   inv_freq      device float32 [R/2] or NULL: nothing is rotated (then no q_rope).
  *   cache         written at the new tokens' places alone.  The places of one call
- *                 must differ (no page that is written is shared).
+ *                 must differ (no page that is written is shared) and not overlap (a
+ *                 stride of less than C + R is KDA_ERR_INVALID_ARG).
  * C is 1 to 4096, R even and at most 256.  Asynchronous on `stream`.
  */
 KDA_API kda_status kda_latent_append(const kda_latent_cache *s, const void *latent,
