@@ -1261,8 +1261,10 @@ def latent_step(q, q_rope, cache, page_table, lengths, *, scale, new=None, retur
     expanded form, (K+R)**-0.5).  ``impl``: "simt" computes in fp32 on the CUDA
     cores, "tc" on the tensor cores (bf16; the softmax's weights are rounded to
     bf16), "auto" takes "tc" where it serves the layout.  Returns o [B,T,H,C], the
-    weighted latents, 0 for a token that is not there, and with ``return_lse`` the
-    log sum of exp of the scores [B,H,T] fp32."""
+    weighted latents, 0 for a token that is not there or sees nothing, and with
+    ``return_lse`` the log sum of exp of the scores [B,H,T] fp32.  A new token that has
+    no place in the cache (behind the table's room, or on a page outside it) is seen by
+    nobody; its query sees the earlier ones that have one."""
     if _away(q, stream):
         return _moved(latent_step, q, stream, q, q_rope, cache, page_table, lengths, scale=scale,
                       new=new, return_lse=return_lse, out=out, workspace=workspace, impl=impl)

@@ -711,12 +711,16 @@ KDA_API kda_status kda_rotate(const kda_rotate_desc *d, const void *x, const int
  *                 tokens of a sequence.  A page outside [0, n_pages) holds no
  *                 tokens: nothing is written to it, nothing read from it.
  *   lengths       device int32 [B]: tokens of each sequence, the new ones of
- *                 this call among them (what the table has no room for is not
- *                 there).
+ *                 this call among them.
  *   new_tokens    device int32 [B] or NULL (T for all): how many of the T tokens
  *                 of each row are there (0 .. T; the first ones).  Token t of row
  *                 b stands at position lengths[b] - new_tokens[b] + t; one
  *                 before position 0 is not there.
+ * A new token that is there but has no place (behind the max_pages * page_size tokens
+ * that the table has room for, or on a page outside the cache) is not stored, and
+ * nobody sees it, itself included.  Its query is one like the others: it is rotated and
+ * sees those tokens of its sequence up to its own position that have a place.  A program
+ * that must not go on without a place compares the lengths with the pages it gave.
  */
 typedef struct kda_latent_cache {
   int B, T, H;                        /* of the new tokens */
@@ -751,7 +755,8 @@ KDA_API kda_status kda_latent_append(const kda_latent_cache *s, const void *late
  *   q             device [B,T,H,C], q_rope [B,T,H,R] (NULL when R = 0), the last
  *                 dimension contiguous.  Rows of a projection's output serve.
  *   o             device [B,T,H,C] contiguous, of s->dtype, 16-byte aligned; 0 for a
- *                 token that is not there or sees nothing.  It must not alias an input.
+ *                 token that is not there and for one that sees nothing.  It must not
+ *                 alias an input.
  *   lse           device float32 [B,H,T] or NULL: log sum_j exp(s_ij), -inf for
  *                 those tokens.
  *   impl          KDA_IMPL_SIMT: fp32 on the CUDA cores, every type and layout.
