@@ -1366,8 +1366,9 @@ def latent_fwd(q, k, v, *, q_rope=None, k_rope=None, scale=None, segment_ids=Non
 
 def latent_bwd(q, k, v, o, lse, d_o, *, q_rope=None, k_rope=None, scale=None, segment_ids=None,
                workspace=None, impl="auto", stream=None):
-    """Gradients of latent_fwd from its inputs, its o and lse, and the gradient
-    ``d_o`` [B,T,H,V] of o: ``(dq, dk, dv, dq_rope, dk_rope)``, contiguous, of the
+    """Gradients of latent_fwd from its inputs, its o and lse for these very inputs
+    (not joined from calls on parts of the keys), and the gradient ``d_o`` [B,T,H,V] of
+    o: ``(dq, dk, dv, dq_rope, dk_rope)``, contiguous, of the
     inputs' dtype (the last two None without a rope part; dk_rope [B,T,R] is the
     sum over the heads).  Repeated calls agree bit for bit."""
     if _away(q, stream):

@@ -822,6 +822,10 @@ KDA_API kda_status kda_latent_fwd(const kda_latent_shape *s, const void *q, cons
                                   kda_stream_t stream);
 /*
  * The gradients, from the inputs, the forward's o and lse, and the gradient of o.
+ * o and lse are those that kda_latent_fwd gave for these very inputs, not ones that were
+ * joined from calls on parts of the keys: D_i = d_o_i . o_i is made from the keys and values
+ * of this call for queries that see at most 1024 of them, on the tensor cores, and for all
+ * others taken from o, with its rounding.
  *   o, d_o        device [B,T,H,V] contiguous, of s->dtype.
  *   dq, dk, dv, dq_rope, dk_rope   device, contiguous, of s->dtype, the shapes of
  *                 q, k, v, q_rope, k_rope; dk_rope is the sum over the heads.  All seven
