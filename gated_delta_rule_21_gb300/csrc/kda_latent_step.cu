@@ -411,8 +411,9 @@ kda_status kda_latent_step(const kda_latent_cache *s, const void *q, const void 
   if (impl == KDA_IMPL_TC && !can) return KDA_ERR_UNSUPPORTED;
   const bool tc = can && impl != KDA_IMPL_SIMT;
   p.tile = tc ? 128 : kTokens;
-  // (120 texts of up to 8192 tokens: 158 us with 0, 147 with 1, 134 with 2, 128 with 3, 131
-  // with 5; two of 131072 81 to 83)
+  // (With 1, 3 and 5: 120 texts of up to 8192 tokens 131, 127.5, 132 us; 64 of them 80, 77, 77;
+  // 300 of up to 2000 110, 104, 109; 16 of up to 32768 67, 69, 68; 16 of 2000 19.6, 19.3, 22.6;
+  // 120 of 500 33, 31, 30; 8 of 5000 with 64 heads 31, 29, 29)
   p.extra = 3;
   cudaError_t e = tc ? launch_step_tc(p, cs)
                   : bf16 ? launch_simt<__nv_bfloat16>(p, cs)

@@ -136,7 +136,6 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
     };
     int next = -1;
     while (ok && cur.next(p, g)) {
-      const bool ahead = p.row_tiles > 1 && g.n >= 20;
       for (int i = 0; ok && i < g.n; ++i) {
         const int t0 = (g.j0 + i) * kTile + lane * ring.box;
         if (i == 0) next = page_of(t0);
@@ -160,14 +159,11 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           pr.next(ring.pairs);
           np = min(np + 1, ring.pairs);
           if (k > 0) continue;
-          // The next tile comes into L2 while the slots that it will take are in use, where
-          // row tiles share a long part (two texts of 131072 tokens, 64 heads: 85 us, without
-          // 92; 32 texts of 4096, 13 tiles a part, 87 and 82; one row tile, 120 texts 128
-          // and 121).
+          // (The next tile's pages are looked up before its slots are free.  To fetch the tile
+          // into L2 as well costs 2 to 21 % where texts have lengths of their own (64 heads, 32 of up
+          // to 16384 tokens 111 us, without 103; two of up to 262144 123 and 102) and gains 3 to 7
+          // % where the row tiles of equal texts walk them in step (two of 131072: 84 and 87).)
           next = i + 1 < g.n ? page_of(t0 + kTile) : -1;
-          if (ahead && next >= 0)
-            for (int x = 0; x < p.C + p.R; x += kChunkCols)
-              tma_prefetch_3d(&map, x, (t0 + kTile) & (p.page - 1), next);
           if (!rope) continue;
           ok = __all_sync(0xffffffffu, wait(bar(c.rempty[rr.at]), rr.lap ^ 1u));
           if (!ok) break;
