@@ -249,7 +249,7 @@ __device__ __forceinline__ long long units_of(const Step &p, const Seq &s) {
 // The first unit of this CTA: sequence, and units into it.  All threads call; `tmp`
 // has 36 words.
 struct Work {
-  long long unit, end;
+  long long unit, end, total;    // (total: of all CTAs)
   int b;
   long long off;
 };
@@ -265,7 +265,7 @@ __device__ __forceinline__ Work find_work(const Step &p, long long *tmp) {
     total = 0;
     for (int w = 0; w < (n >> 5); ++w) total += tmp[w];
   }
-  Work x = {0, 0, 0, 0};
+  Work x = {0, 0, 0, 0, 0};
   long long base = 0;
   for (int b0 = 0; b0 < p.B; b0 += n) {
     if (b0 || p.B > n) __syncthreads();
@@ -297,6 +297,7 @@ __device__ __forceinline__ Work find_work(const Step &p, long long *tmp) {
     base = all;
   }
   __syncthreads();
+  x.total = total;
   if (x.unit < x.end) {
     x.b = (int)tmp[33];
     x.off = tmp[34];

@@ -83,6 +83,16 @@ __device__ __forceinline__ void half_barrier(int half) {
   asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory");
 }
 
+// Whether the next tile is fetched into L2 while the slots that it will take are in use: where
+// the row tiles of a text walk it in step, that is, each takes a whole number of parts and two
+// CTAs are at the same tile at the same time.  In step: 64 heads, two texts of 131072 tokens
+// 83 us, without 88; 19 of 13440 83 and 90; 128 heads, two of 65280 83 and 85.5.  Out of step
+// it would cost 2 to 20 %: 64 heads, 32 texts of up to 16384 tokens 111 us, without 103; 12 of 21504
+// 114.5 and 109; and so it would where one text has two row tiles (262272 tokens: 96 and 89).
+__device__ __forceinline__ bool in_step(const Step &p, const Segment &g, long long total) {
+  return p.B * p.row_tiles > 2 && (tiles_of(p, g.s) + p.extra) * parts_used(total) % total == 0;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring ring) {
   extern __shared__ __align__(1024) unsigned char raw[];
@@ -136,6 +146,7 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
     };
     int next = -1;
     while (ok && cur.next(p, g)) {
+      bool ahead = false;
       for (int i = 0; ok && i < g.n; ++i) {
         const int t0 = (g.j0 + i) * kTile + lane * ring.box;
         if (i == 0) next = page_of(t0);
@@ -159,11 +170,11 @@ step_tc_kernel(const __grid_constant__ CUtensorMap map, const Step p, const Ring
           pr.next(ring.pairs);
           np = min(np + 1, ring.pairs);
           if (k > 0) continue;
-          // (The next tile's pages are looked up before its slots are free.  To fetch the tile
-          // into L2 as well costs 2 to 21 % where texts have lengths of their own (64 heads, 32 of up
-          // to 16384 tokens 111 us, without 103; two of up to 262144 123 and 102) and gains 3 to 7
-          // % where the row tiles of equal texts walk them in step (two of 131072: 84 and 87).)
           next = i + 1 < g.n ? page_of(t0 + kTile) : -1;
+          if (i == 0 && p.row_tiles > 1) ahead = in_step(p, g, cur.x.total);
+          if (ahead && next >= 0)
+            for (int x = 0; x < p.C + p.R; x += kChunkCols)
+              tma_prefetch_3d(&map, x, (t0 + kTile) & (p.page - 1), next);
           if (!rope) continue;
           ok = __all_sync(0xffffffffu, wait(bar(c.rempty[rr.at]), rr.lap ^ 1u));
           if (!ok) break;
