@@ -1260,7 +1260,9 @@ def latent_step(q, q_rope, cache, page_table, lengths, *, scale, new=None, retur
     and ``new`` as :func:`latent_append`.  ``scale`` is that of the scores (of the
     expanded form, (K+R)**-0.5).  ``impl``: "simt" computes in fp32 on the CUDA
     cores, "tc" on the tensor cores (bf16; the softmax's weights are rounded to
-    bf16), "auto" takes "tc" where it serves the layout.  Returns o [B,T,H,C], the
+    bf16), "auto" takes "tc" where it serves the cache: 16-byte aligned tokens, pages of
+    a power of two of at least 8.  (Elsewhere bf16 takes 10 to 55 times as long.)
+    Returns o [B,T,H,C], the
     weighted latents, 0 for a token that is not there or sees nothing, and with
     ``return_lse`` the log sum of exp of the scores [B,H,T] fp32.  A new token that has
     no place in the cache (behind the table's room, or on a page outside it) is seen by
@@ -1342,7 +1344,8 @@ def latent_fwd(q, k, v, *, q_rope=None, k_rope=None, scale=None, segment_ids=Non
     (a token sees its own run up to itself).  ``scale`` None means (K+R)**-0.5.
     ``impl``: "simt" computes in fp32 on the CUDA cores, "tc" on the tensor cores
     (bf16; the softmax's weights are rounded to bf16), "auto" takes "tc" where it
-    serves the layout.  Returns o [B,T,H,V], and with ``save_lse`` also what
+    serves the call: rows that are 16-byte aligned, no dimension broadcast, a scale that
+    is not negative.  (Elsewhere bf16 takes 10 to 55 times as long.)  Returns o [B,T,H,V], and with ``save_lse`` also what
     :func:`latent_bwd` reads, the log sum of exp of the scores [B,H,T] fp32."""
     if _away(q, stream):
         return _moved(latent_fwd, q, stream, q, k, v, q_rope=q_rope, k_rope=k_rope, scale=scale,

@@ -1,8 +1,8 @@
 // kda_latent_step.cu -- the absorbed latent attention over the paged cache:
 // entry point, the kernel on the CUDA cores and the one that joins the parts.
 //
-// The tokens of all sequences are cut into tiles of 128, and the tiles evenly
-// into one part for each SM, so a part may hold the end of one sequence, whole
+// The tokens of all sequences are cut into tiles of 128 (on the CUDA cores of 32), and the tiles
+// evenly into one part for each SM, so a part may hold the end of one sequence, whole
 // ones and the beginning of another.  Whole sequences are written at once;
 // of the others each part leaves its sums with the softmax's maximum and sum, and
 // a second kernel joins them.  The cut goes by the lengths on the device: a call

@@ -17,9 +17,10 @@
 // warp 9 the products.
 //
 // What bounds it: memory, where a row tile reads its own texts (120 texts of up to 8192
-// tokens, 551 MB: 116 us with the join, 4.7 TB/s), and the chain of a tile where row tiles share
-// them (two texts of 131072, 64 heads: 81 us, 2.8 us a tile: S 2000 cycles, softmax 1100, O
-// 1500).  One text of 1000 tokens: 14 us with the join.
+// tokens, 576 MB: 128 us with the join in a graph, 4.5 TB/s; with cold caches this kernel 117,
+// the join 19), and the chain of a tile where row tiles share them (two texts of 131072, 64
+// heads: 84 us, 2.8 us a tile: S 2000 cycles, softmax 1100, O 1500).  One text of 1000 tokens: 14
+// us with the join.
 #include "kda_latent_tc.cuh"
 
 namespace kda {
